@@ -12,6 +12,11 @@ Entry points mirror the C ABI declared in include/fusedlin.h:
     input_bias_gemm(A, bias_in, W, bias, residual, out, act)             (A + bias_in) W^T epilogue
     rms_norm(x, gamma, out, eps)                                          standalone RMSNorm
     swiglu_ffn(x, gamma, Wg, Wu, Wd, bias_down, out, eps, workspace)
+    w4_quantize(W, group)                                                 16-bit weight -> 4-bit codes, group scales
+    w4_gemm(x, q, scales, zeros, gamma, bias, residual, out, eps, act)    dense layer on a 4-bit weight
+    w4_swiglu_ffn(x, gamma, Wg, Wu, Wd, bias_down, out, eps, workspace)   the SwiGLU block on 4-bit weights
+    rope(q, k, positions, inv_freq, sections)                             rotary positions, one to four axes
+    kv_write / kv_read                                                    paged 8-bit key/value cache
 """
 from __future__ import annotations
 
@@ -28,7 +33,7 @@ NORMS = {"rms": 0, "layer": 1}
 ACTS = {"none": 0, "gelu": 1, "silu": 2, "relu": 3}
 DTYPE_CODES = {"f16": 0, "bf16": 1}
 STATUS_NAMES = {0: "FL_OK", 1: "FL_ERR_INVALID_ARG", 2: "FL_ERR_UNSUPPORTED", 3: "FL_ERR_ALIGNMENT",
-                4: "FL_ERR_WORKSPACE", 5: "FL_ERR_CUDA", 6: "FL_ERR_TIMEOUT"}
+                4: "FL_ERR_WORKSPACE", 5: "FL_ERR_CUDA", 6: "FL_ERR_TIMEOUT", 7: "FL_ERR_RANGE"}
 OPTIONS = {"tile_n": 0, "variant": 1, "timeout_ms": 2, "split_k": 3, "pdl": 4, "weight_preload": 5,
            "launch_cache": 6}
 
@@ -40,8 +45,36 @@ class LayerDesc(ctypes.Structure):
                                              "bias_o", "h", "gamma_ffn", "Wg", "Wu", "Wd", "out")]
 
 
+class W4Weight(ctypes.Structure):
+    """fl_w4_weight: the device pointers of one 4-bit weight."""
+    _fields_ = [("q", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p),
+                ("group", ctypes.c_int)]
+
+
+class RopeDesc(ctypes.Structure):
+    """fl_rope_desc."""
+    _fields_ = ([(n, ctypes.c_int) for n in ("dtype", "rows", "heads_q", "heads_k", "head_dim", "rotary_dim", "n_axes",
+                                             "interleaved", "inverse")]
+                + [("axis_of", ctypes.c_char_p), ("positions", ctypes.c_void_p), ("positions_stride", ctypes.c_longlong),
+                   ("inv_freq", ctypes.c_void_p)]
+                + [(n, ctypes.c_void_p) for n in ("q", "k", "q_out", "k_out")]
+                + [(n, ctypes.c_longlong) for n in ("q_row", "q_head", "k_row", "k_head", "q_out_row", "q_out_head",
+                                                    "k_out_row", "k_out_head")])
+
+
+class KvDesc(ctypes.Structure):
+    """fl_kv_desc."""
+    _fields_ = ([(n, ctypes.c_int) for n in ("dtype", "format", "rows", "heads", "head_dim", "page_size", "n_pages",
+                                             "n_seqs", "table_pages")]
+                + [("table_stride", ctypes.c_longlong)]
+                + [(n, ctypes.c_void_p) for n in ("page_table", "cu_rows", "start", "k", "v")]
+                + [(n, ctypes.c_longlong) for n in ("k_row", "k_head", "v_row", "v_head")]
+                + [(n, ctypes.c_void_p) for n in ("k_cache", "v_cache", "k_scale", "v_scale")])
+
+
 # C ABI: name -> (restype, argtypes)
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_w4 = ctypes.POINTER(W4Weight)
 SIGNATURES = {
     "fl_gemm_epilogue": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp]),
     "fl_norm_gemm": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _f, _i, _i, _i, _vp]),
@@ -51,6 +84,14 @@ SIGNATURES = {
     "fl_norm_gemm_multi": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _i, _i, _f, _i, _i, _vp]),
     "fl_input_bias_gemm": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp]),
     "fl_rms_norm": (_i, [_vp, _vp, _vp, _i, _i, _f, _i, _vp]),
+    "fl_w4_quantize": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _vp]),
+    "fl_w4_gemm_workspace_size": (_sz, [_i, _i, _i]),
+    "fl_w4_gemm": (_i, [_vp, _vp, _w4, _vp, _vp, _vp, _i, _i, _i, _f, _i, _vp, _sz, _i, _vp]),
+    "fl_w4_swiglu_ffn_workspace_size": (_sz, [_i, _i, _i]),
+    "fl_w4_swiglu_ffn": (_i, [_vp, _vp, _w4, _w4, _w4, _vp, _vp, _i, _i, _i, _f, _vp, _sz, _i, _vp]),
+    "fl_rope": (_i, [ctypes.POINTER(RopeDesc), _vp]),
+    "fl_kv_write": (_i, [ctypes.POINTER(KvDesc), _vp]),
+    "fl_kv_read": (_i, [ctypes.POINTER(KvDesc), _vp]),
     "fl_layer_create": (_i, [ctypes.POINTER(LayerDesc), ctypes.POINTER(_vp)]),
     "fl_layer_issue": (_i, [_vp, _i, _vp]),
     "fl_layer_destroy": (None, [_vp]),
@@ -346,6 +387,310 @@ def swiglu_ffn_noalloc(x, gamma, Wg, Wu, Wd, bias_down=None, out=None, eps=1e-6,
     return out
 
 
+# ---------------------------------------------------------------------------
+# serving operators: 4-bit weights, rotary positions, the quantised cache
+# ---------------------------------------------------------------------------
+def _check_call(**tensors):
+    """Every tensor given is on the current CUDA device (the one whose stream the call is issued on)."""
+    import torch
+    here = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.device.index != here:
+            raise ValueError(f"{name} is on device {t.device.index}, the current device is {here}")
+
+
+def _check_shape(name, t, shape):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _check_kind(name, t, dtype, contiguous=True):
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous (row-major)")
+
+
+def _made(stream, *tensors):
+    """Tensors a call made for itself and used on `stream`: not reused for another stream's work before it is done."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def w4_quantize(W, group=128, q=None, scales=None, stream=None):
+    """Symmetric round-to-nearest 4-bit quantisation of W [N, K]: returns (q, scales), codes [N, K / 2] uint8 (two
+    along K to a byte, the even k in the low half, 8 standing for zero) and one scale of W's dtype per `group` k."""
+    import torch
+    N, K = W.shape
+    if group not in (32, 64, 128) or K % group:
+        raise ValueError(f"group must be 32, 64 or 128 and divide K (group {group}, K {K})")
+    made = []
+    if q is None:
+        q = torch.empty((N, K // 2), dtype=torch.uint8, device=W.device)
+        made.append(q)
+    if scales is None:
+        scales = torch.empty((N, K // group), dtype=W.dtype, device=W.device)
+        made.append(scales)
+    _check_call(W=W, q=q, scales=scales)
+    _check_tensors(W.dtype, W=W, scales=scales)
+    _check_kind("q", q, torch.uint8)
+    _check_shape("q", q, (N, K // 2))
+    _check_shape("scales", scales, (N, K // group))
+    _check(lib().fl_w4_quantize(_ptr(W), _ptr(q), _ptr(scales), N, K, group, _dtype_code(W), _stream(stream)))
+    _made(stream, *made)
+    return q, scales
+
+
+def _w4_weight(name, dtype, K, q, scales, zeros=None):
+    """The C description of a 4-bit weight, and its row count."""
+    import torch
+    if q.dim() != 2 or q.shape[1] * 2 != K:
+        raise ValueError(f"{name}: q has shape {tuple(q.shape)}, expected [N, {K // 2}]")
+    N = q.shape[0]
+    if scales.dim() != 2 or scales.shape[0] != N or scales.shape[1] < 1 or K % scales.shape[1]:
+        raise ValueError(f"{name}: scales has shape {tuple(scales.shape)}, expected [{N}, K / group]")
+    _check_call(**{f"{name}: q": q, f"{name}: scales": scales, f"{name}: zeros": zeros})
+    _check_kind(f"{name}: q", q, torch.uint8)
+    _check_kind(f"{name}: scales", scales, dtype)
+    _check_kind(f"{name}: zeros", zeros, torch.uint8)
+    _check_shape(f"{name}: zeros", zeros, scales.shape)
+    return W4Weight(q=q.data_ptr(), scales=scales.data_ptr(), zeros=None if zeros is None else zeros.data_ptr(),
+                    group=K // scales.shape[1]), N
+
+
+def _workspace(workspace, need, device):
+    """(workspace or one made here, its bytes, whether it was made)."""
+    import torch
+    if workspace is not None:
+        _check_call(workspace=workspace)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        return workspace, workspace.numel() * workspace.element_size(), False
+    if need == 0:
+        return None, 0, False
+    return torch.empty(need, dtype=torch.uint8, device=device), need, True
+
+
+def w4_gemm_workspace_size(M: int, K: int, norm: bool) -> int:
+    return int(lib().fl_w4_gemm_workspace_size(M, K, int(norm)))
+
+
+def w4_gemm(x, q, scales, zeros=None, gamma=None, bias=None, residual=None, out=None, eps=1e-6, act="none",
+            workspace=None, stream=None):
+    """out[M,N] = act(norm(x) W^T + bias) (+ residual) with W[n, k] = scales[n, k / group] * (code[n, k] -
+    zeros[n, k / group]); norm is RMSNorm with `gamma`, or none. q, scales: as w4_quantize returns them; zeros
+    [N, K / group] uint8 (8 everywhere if None). The workspace (w4_gemm_workspace_size bytes) must not be
+    shared by calls or captured graphs that may overlap on the GPU."""
+    import torch
+    M, K = x.shape
+    W, N = _w4_weight("W", x.dtype, K, q, scales, zeros)
+    made = []
+    if out is None:
+        out = torch.empty((M, N), dtype=x.dtype, device=x.device)
+        made.append(out)
+    _check_call(x=x, gamma=gamma, bias=bias, residual=residual, out=out)
+    _check_tensors(x.dtype, x=x, gamma=gamma, bias=bias, residual=residual, out=out)
+    _check_shape("gamma", gamma, (K,))
+    _check_shape("bias", bias, (N,))
+    _check_shape("residual", residual, (M, N))
+    _check_shape("out", out, (M, N))
+    ws, size, own = _workspace(workspace, w4_gemm_workspace_size(M, K, gamma is not None), x.device)
+    if own:
+        made.append(ws)
+    _check(lib().fl_w4_gemm(_ptr(x), _ptr(gamma), ctypes.byref(W), _ptr(bias), _ptr(residual), _ptr(out), M, N, K,
+                            float(eps), ACTS[act], _ptr(ws), size, _dtype_code(x), _stream(stream)))
+    _made(stream, *made)
+    return out
+
+
+def w4_swiglu_ffn_workspace_size(M: int, D: int, F: int) -> int:
+    return int(lib().fl_w4_swiglu_ffn_workspace_size(M, D, F))
+
+
+def w4_swiglu_ffn(x, gamma, Wg, Wu, Wd, bias_down=None, out=None, eps=1e-6, workspace=None, stream=None):
+    """swiglu_ffn on 4-bit weights, each a tuple (q, scales) or (q, scales, zeros)."""
+    import torch
+    M, D = x.shape
+    F = Wg[0].shape[0]
+    g, _ = _w4_weight("Wg", x.dtype, D, *Wg)
+    u, n = _w4_weight("Wu", x.dtype, D, *Wu)
+    d, m = _w4_weight("Wd", x.dtype, F, *Wd)
+    if n != F or m != D:
+        raise ValueError(f"Wu has {n} rows, expected {F}; Wd has {m}, expected {D}")
+    made = []
+    if out is None:
+        out = torch.empty_like(x)
+        made.append(out)
+    _check_call(x=x, gamma=gamma, bias_down=bias_down, out=out)
+    _check_tensors(x.dtype, x=x, gamma=gamma, bias_down=bias_down, out=out)
+    _check_shape("gamma", gamma, (D,))
+    _check_shape("bias_down", bias_down, (D,))
+    _check_shape("out", out, (M, D))
+    ws, size, own = _workspace(workspace, w4_swiglu_ffn_workspace_size(M, D, F), x.device)
+    if own:
+        made.append(ws)
+    _check(lib().fl_w4_swiglu_ffn(_ptr(x), _ptr(gamma), ctypes.byref(g), ctypes.byref(u), ctypes.byref(d),
+                                  _ptr(bias_down), _ptr(out), M, D, F, float(eps), _ptr(ws), size, _dtype_code(x),
+                                  _stream(stream)))
+    _made(stream, *made)
+    return out
+
+
+def _heads(name, t, dtype, rows=None):
+    """Checks a [rows, heads, head_dim] view: dtype, contiguous channels."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [rows, heads, head_dim]")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: the channels of a head must be contiguous")
+    if rows is not None and t.shape[0] != rows:
+        raise ValueError(f"{name} has {t.shape[0]} rows, expected {rows}")
+
+
+def _strides(t):
+    """Row and head stride of a [rows, heads, head_dim] view; of an axis of one, the one it would have if dense."""
+    head = t.stride(1) if t.shape[1] > 1 else t.shape[2]
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * head, head
+
+
+def rope(q, k, positions, inv_freq, sections=None, interleaved=False, inverse=False, out_q=None, out_k=None,
+         stream=None):
+    """Rotary positions of q [rows, heads_q, D] and k [rows, heads_k, D] (k may be None): returns (out_q, out_k).
+
+    The pairs (i, i + R/2) of the first R = 2 * len(inv_freq) channels, or (2i, 2i + 1) if interleaved, are turned
+    by positions * inv_freq[i]; the other channels are copied. positions: int32 [rows], or [axes, rows] with
+    `sections` saying how many consecutive pairs follow each axis. inverse turns back: the gradient with respect to
+    the input. q, k and the outputs may be strided views with contiguous channels (column ranges of a stacked
+    projection's output); an output may be its input itself."""
+    import torch
+    dt = q.dtype
+    _heads("q", q, dt)
+    rows, heads_q, D = q.shape
+    pos = positions if positions.dim() == 2 else positions.reshape(1, -1)
+    axes = pos.shape[0]
+    _check_shape("positions", pos, (axes, rows))
+    _check_kind("positions", pos, torch.int32, contiguous=False)
+    if rows > 1 and pos.stride(1) != 1:
+        raise ValueError("positions must be contiguous along the rows")
+    _check_kind("inv_freq", inv_freq, torch.float32)
+    if inv_freq.dim() != 1:
+        raise ValueError(f"inv_freq has shape {tuple(inv_freq.shape)}, expected [R / 2]")
+    pairs = inv_freq.shape[0]
+    if sections is None:
+        if axes != 1:
+            raise ValueError(f"positions has {axes} axes: sections must say which pairs follow which")
+        sections = (pairs,)
+    if len(sections) != axes or sum(sections) != pairs or min(sections) < 0:
+        raise ValueError(f"sections {tuple(sections)} must give the {pairs} pairs to the {axes} axes")
+    if axes > 4:
+        raise ValueError(f"1..4 axes, got {axes}")
+    made = []
+    if out_q is None:
+        out_q = torch.empty((rows, heads_q, D), dtype=dt, device=q.device)
+        made.append(out_q)
+    if k is None and out_k is not None:
+        raise ValueError("out_k without k")
+    if k is not None and out_k is None:
+        out_k = torch.empty(tuple(k.shape), dtype=dt, device=k.device)
+        made.append(out_k)
+    _check_call(q=q, k=k, positions=pos, inv_freq=inv_freq, out_q=out_q, out_k=out_k)
+    _heads("out_q", out_q, dt)
+    _check_shape("out_q", out_q, q.shape)
+    if k is not None:
+        _heads("k", k, dt, rows)
+        _heads("out_k", out_k, dt)
+        _check_shape("k", k, (rows, k.shape[1], D))
+        _check_shape("out_k", out_k, k.shape)
+    desc = RopeDesc(dtype=_dtype_code(q), rows=rows, heads_q=heads_q, heads_k=0 if k is None else k.shape[1],
+                    head_dim=D, rotary_dim=2 * pairs, n_axes=axes, interleaved=int(bool(interleaved)),
+                    inverse=int(bool(inverse)), axis_of=b"".join(bytes([a]) * n for a, n in enumerate(sections)),
+                    positions=pos.data_ptr(), positions_stride=pos.stride(0) if axes > 1 else rows,
+                    inv_freq=inv_freq.data_ptr(), q=q.data_ptr(), q_out=out_q.data_ptr())
+    desc.q_row, desc.q_head = _strides(q)
+    desc.q_out_row, desc.q_out_head = _strides(out_q)
+    if k is not None:
+        desc.k, desc.k_out = k.data_ptr(), out_k.data_ptr()
+        desc.k_row, desc.k_head = _strides(k)
+        desc.k_out_row, desc.k_out_head = _strides(out_k)
+    _check(lib().fl_rope(ctypes.byref(desc), _stream(stream)))
+    _made(stream, *made)
+    return out_q, out_k
+
+
+def _kv_desc(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_rows, start):
+    import torch
+    formats = {torch.int8: 0, torch.float8_e4m3fn: 1}
+    if k_cache.dtype not in formats:
+        raise TypeError(f"k_cache has dtype {k_cache.dtype}, expected int8 or float8_e4m3fn")
+    if k_cache.dim() != 4:
+        raise ValueError(f"k_cache has shape {tuple(k_cache.shape)}, expected [pages, page_size, heads, head_dim]")
+    pages, size, heads, dim = k_cache.shape
+    _check_call(k=k, v=v, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, page_table=page_table,
+                cu_rows=cu_rows, start=start)
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _check_kind(name, t, k_cache.dtype)
+        _check_shape(name, t, k_cache.shape)
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _check_kind(name, t, torch.float32)
+        _check_shape(name, t, (pages, size, heads))
+    rows = k.shape[0]
+    for name, t in (("k", k), ("v", v)):
+        _heads(name, t, k.dtype, rows)
+        _check_shape(name, t, (rows, heads, dim))
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected [sequences, pages]")
+    seqs, per = page_table.shape
+    _check_kind("page_table", page_table, torch.int32, contiguous=False)
+    if per > 1 and page_table.stride(1) != 1:
+        raise ValueError("page_table must be contiguous along a sequence's pages")
+    _check_kind("cu_rows", cu_rows, torch.int32)
+    _check_shape("cu_rows", cu_rows, (seqs + 1,))
+    _check_kind("start", start, torch.int32)
+    _check_shape("start", start, (seqs,))
+    opt = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    (k_row, k_head), (v_row, v_head) = _strides(k), _strides(v)
+    return KvDesc(dtype=_dtype_code(k), format=formats[k_cache.dtype], rows=rows, heads=heads, head_dim=dim,
+                  page_size=size, n_pages=pages, n_seqs=seqs, table_pages=per,
+                  table_stride=page_table.stride(0) if seqs > 1 else per, page_table=page_table.data_ptr(),
+                  cu_rows=opt(cu_rows), start=opt(start), k=k.data_ptr(), v=v.data_ptr(), k_row=k_row,
+                  k_head=k_head, v_row=v_row, v_head=v_head, k_cache=k_cache.data_ptr(),
+                  v_cache=v_cache.data_ptr(), k_scale=k_scale.data_ptr(), v_scale=v_scale.data_ptr())
+
+
+def kv_write(k, v, k_cache, v_cache, k_scale, v_scale, page_table, start, cu_rows=None, stream=None):
+    """Quantises rows of k and v [rows, heads, head_dim] into the paged cache.
+
+    k_cache, v_cache: int8 or float8_e4m3fn [pages, page_size, heads, head_dim]; k_scale, v_scale: fp32
+    [pages, page_size, heads]. Row i of sequence b (cu_rows[b] <= i < cu_rows[b + 1]; without cu_rows, row b) is
+    position start[b] + i - cu_rows[b] of it, in page page_table[b][position / page_size]. Rows behind the
+    last sequence are left out; one whose position has no page is skipped and device_status() raises FL_ERR_RANGE.
+    No two rows of a call may have the same place in the cache."""
+    if start is None:
+        raise ValueError("start must be given")
+    desc = _kv_desc(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_rows, start)
+    _check(lib().fl_kv_write(ctypes.byref(desc), _stream(stream)))
+
+
+def kv_read(k_cache, v_cache, k_scale, v_scale, page_table, cu_rows, start=None, out_k=None, out_v=None, stream=None):
+    """Reads rows of the cache back (scale * code) into out_k, out_v [rows, heads, head_dim]: row i of the outputs is
+    the position start[b] + i - cu_rows[b] (start: 0 if None) of the sequence b that cu_rows gives it to; with
+    cu_rows None it is position start[i] of sequence i. Rows that belong to no sequence are left as they were.
+    Returns (out_k, out_v)."""
+    if out_k is None or out_v is None:
+        raise ValueError("out_k and out_v must be given: the row count is not known on the host")
+    desc = _kv_desc(out_k, out_v, k_cache, v_cache, k_scale, v_scale, page_table, cu_rows, start)
+    _check(lib().fl_kv_read(ctypes.byref(desc), _stream(stream)))
+    return out_k, out_v
+
+
 def launch_cache_stats():
     """(hits, misses) of the host-side launch cache since the library was loaded."""
     h, m = ctypes.c_longlong(), ctypes.c_longlong()
@@ -365,7 +710,8 @@ def kernel_launches() -> int:
 
 
 def device_status(stream=None) -> None:
-    """Synchronise the stream and raise FusedLinError(FL_ERR_TIMEOUT) if a kernel's wait ran out."""
+    """Synchronise the stream and raise FusedLinError: FL_ERR_TIMEOUT if a kernel's wait ran out, FL_ERR_RANGE if a
+    row of the paged cache had no page."""
     _check(lib().fl_device_status(_stream(stream)))
 
 

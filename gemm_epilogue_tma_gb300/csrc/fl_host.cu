@@ -16,6 +16,7 @@
 #include <mutex>
 
 #include "../../include/fusedlin.h"
+#include "fl_host.h"
 #include "fl_internal.h"
 
 using fl::GemmParams;
@@ -24,6 +25,11 @@ using fl::GemmParamsMulti;
 // Device status words: a kernel records a bounded-wait expiry in the word of
 // the stream it was launched (or captured) on.
 __device__ int g_fl_status[fl::kStatusSlots];
+// Range words, one per stream like the status words: a kernel that reads
+// indexes from device memory (page tables, row offsets) skips an entry outside
+// its table and records it here. They are words of their own because a kernel
+// that finds its status word set gives up its slow waits.
+__device__ int g_fl_range[fl::kStatusSlots];
 
 namespace {
 
@@ -68,6 +74,7 @@ struct DeviceInfo {
     int sms = 0;
     int major = 0, minor = 0;
     int* status = nullptr;  // device address of g_fl_status[0]
+    int* range = nullptr;   // device address of g_fl_range[0]
     // stream handle of each status word (word 0: the legacy default stream
     // and overflow), filled in first-use order under slot_mu
     std::mutex slot_mu;
@@ -97,6 +104,8 @@ fl_status device_info(DeviceInfo** out) {
             d.major = prop.major;
             d.minor = prop.minor;
             e = cudaGetSymbolAddress(reinterpret_cast<void**>(&d.status), g_fl_status);
+            if (e != cudaSuccess) return fail(FL_ERR_CUDA, "cudaGetSymbolAddress: %s", cudaGetErrorString(e));
+            e = cudaGetSymbolAddress(reinterpret_cast<void**>(&d.range), g_fl_range);
             if (e != cudaSuccess) return fail(FL_ERR_CUDA, "cudaGetSymbolAddress: %s", cudaGetErrorString(e));
             cudaMemPoolProps props = {};
             props.allocType = cudaMemAllocationTypePinned;
@@ -911,6 +920,48 @@ bool valid_dtype(int dt) { return dt == FL_F16 || dt == FL_BF16; }
 
 int fl::set_last_error(int status, const char* message) { return fail((fl_status)status, "%s", message); }
 
+// ---------------------------------------------------------------------------
+// services for the entry points of other translation units (fl_host.h)
+// ---------------------------------------------------------------------------
+namespace fl {
+namespace host {
+
+fl_status fail(fl_status s, const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(tls_err, sizeof(tls_err), fmt, ap);
+    va_end(ap);
+    return s;
+}
+
+fl_status ok() { return ::ok(); }
+
+fl_status launch_context(cudaStream_t stream, LaunchContext* ctx) {
+    DeviceInfo* di = nullptr;
+    const fl_status st = device_info(&di);
+    if (st != FL_OK) return st;
+    const int slot = status_slot(di, stream);
+    ctx->sms = di->sms;
+    ctx->status = di->status + slot;
+    ctx->range = di->range + slot;
+    ctx->pdl = g_opt_pdl.load();
+    ctx->timeout_ns = (unsigned long long)g_opt_timeout_ms.load() * 1000000ull;
+    return FL_OK;
+}
+
+fl_status launched(cudaError_t e, const char* what) {
+    if (e != cudaSuccess) return ::fail(FL_ERR_CUDA, "%s launch failed: %s", what, cudaGetErrorString(e));
+    count_launch();
+    return ::ok();
+}
+
+fl_status check_ptr(const char* name, const void* p, bool required) { return ::check_ptr(name, p, required); }
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) { return ::overlap(a, na, b, nb); }
+
+}  // namespace host
+}  // namespace fl
+
 // ===========================================================================
 // C ABI
 // ===========================================================================
@@ -1174,8 +1225,15 @@ fl_status fl_device_status(void* stream) {
     int v = 0;
     e = cudaMemcpyFromSymbol(&v, g_fl_status, sizeof(int), off);
     if (e != cudaSuccess) return fail(FL_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
-    if (v == 0) return ok();
     const int zero = 0;
+    if (v == 0) {
+        e = cudaMemcpyFromSymbol(&v, g_fl_range, sizeof(int), off);
+        if (e != cudaSuccess) return fail(FL_ERR_CUDA, "range word read: %s", cudaGetErrorString(e));
+        if (v == 0) return ok();
+        e = cudaMemcpyToSymbol(g_fl_range, &zero, sizeof(int), off);
+        if (e != cudaSuccess) return fail(FL_ERR_CUDA, "range word clear: %s", cudaGetErrorString(e));
+        return fail(FL_ERR_RANGE, "a row of the paged cache has no page or lies outside its table (row %d)", v - 1);
+    }
     e = cudaMemcpyToSymbol(g_fl_status, &zero, sizeof(int), off);
     if (e != cudaSuccess) return fail(FL_ERR_CUDA, "status clear: %s", cudaGetErrorString(e));
     return fail(FL_ERR_TIMEOUT, "a device-side wait ran past its limit (code %d, wait site %d)", v & 0xff, v >> 8);

@@ -1,0 +1,68 @@
+// Host services of fl_host.cu for the entry points that live in other
+// translation units: errors, the current device, argument checks.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "../../include/fusedlin.h"
+
+namespace fl {
+namespace host {
+
+// Records the message for fl_last_error() and returns the status.
+fl_status fail(fl_status s, const char* fmt, ...);
+fl_status ok();
+
+// What a launch on `stream` needs of the current device: its SM count, the
+// stream's status word (bounded waits) and range word (indexes a kernel found
+// outside their tables), and the launch options.
+struct LaunchContext {
+    int sms;
+    int* status;
+    int* range;
+    int pdl;
+    unsigned long long timeout_ns;
+};
+fl_status launch_context(cudaStream_t stream, LaunchContext* ctx);
+
+// Counts a launch and turns the launch call's result into a status.
+fl_status launched(cudaError_t e, const char* what);
+
+// Null and 16-byte alignment check of one pointer.
+fl_status check_ptr(const char* name, const void* p, bool required);
+bool overlap(const void* a, size_t na, const void* b, size_t nb);
+// Whether two strided matrices of `elem`-byte elements whose spans overlap share
+// no element because their rows interleave: the same row stride, and b's
+// columns beside a's within it.
+inline bool apart(const void* a, long long a_row, long long a_width, const void* b, long long b_row, long long b_width,
+                  int elem) {
+    if (a_row != b_row || a_row <= 0 || a_width > a_row || b_width > b_row) return false;
+    const long long bytes = (long long)(reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a));
+    if (bytes % elem != 0) return false;
+    const long long d = ((bytes / elem) % a_row + a_row) % a_row;
+    return d >= a_width && a_row - d >= b_width;
+}
+inline bool valid_dtype(int dt) { return dt == FL_F16 || dt == FL_BF16; }
+
+// cudaLaunchKernelEx with the programmatic-dependency attribute of the library's launches.
+template <typename Kern, typename... Args>
+cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, int pdl, cudaStream_t stream, const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute a[1];
+    a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a[0].val.programmaticStreamSerializationAllowed = pdl;
+    cfg.attrs = a;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+}  // namespace host
+}  // namespace fl

@@ -1,0 +1,234 @@
+// Rotary positions of q and k with one to four position axes (fl_rope).
+//
+//   (a, b) -> (a cos t - b sin t, b cos t + a sin t),
+//   t = positions[axis_of[i]][row] * inv_freq[i]
+//
+// Bound by HBM: every channel is read and written once. The angle depends on
+// the row and the pair only, so a CTA computes the sines of its rows once into
+// shared memory and applies them to every head of q and k.
+//
+// The angle is taken in turns, in fixed point: f = frac(inv_freq / 2 pi) as a
+// 64-bit fraction (from the 53 bits of one double product), and position * f
+// modulo 2^64 is the fraction of a turn, exact in the position: for the
+// largest int32 position the error is below 2^-24 turns, where the fp32
+// product position * inv_freq would be off by whole turns. The top 32 bits go
+// to sincospif.
+#include "fl_common.cuh"
+#include "fl_host.h"
+
+namespace fl {
+
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeRows = 4;  // rows of one CTA at most
+constexpr int kRopePairs = FL_ROPE_MAX_DIM / 2;
+
+struct RopeParams {
+    const uint16_t* x[2];  // q, k
+    uint16_t* y[2];
+    long long x_row[2], x_head[2], y_row[2], y_head[2];
+    const int* positions;
+    const float* inv_freq;
+    long long positions_stride;
+    int rows, heads[2], head_dim, pairs, rows_per_cta;
+    int interleaved, inverse;
+    int copy;  // channels behind the rotated ones are copied (out of place)
+    unsigned char axis_of[kRopePairs];
+};
+
+// frac(f / 2 pi) in units of 2^-64 turns
+__device__ __forceinline__ unsigned long long turns_per_position(float f) {
+    const double t = (double)f * 0.15915494309189533577;  // 1 / (2 pi)
+    return (unsigned long long)((t - floor(t)) * 18446744073709551616.0);
+}
+
+template <int DT>
+__device__ __forceinline__ void rotate2(uint32_t a, uint32_t b, float2 cs0, float2 cs1, uint32_t& oa, uint32_t& ob) {
+    using Ops = DTypeOps<DT>;
+    const float2 x = Ops::unpack(a), y = Ops::unpack(b);
+    oa = Ops::pack(fmaf(x.x, cs0.x, -y.x * cs0.y), fmaf(x.y, cs1.x, -y.y * cs1.y));
+    ob = Ops::pack(fmaf(y.x, cs0.x, x.x * cs0.y), fmaf(y.y, cs1.x, x.y * cs1.y));
+}
+
+// VEC: 8 (16-byte vectors, everything aligned to them) or 1.
+template <int DT, int VEC>
+__global__ void __launch_bounds__(kRopeThreads) fl_rope_kernel(const __grid_constant__ RopeParams p) {
+    using Ops = DTypeOps<DT>;
+    __shared__ float2 cs[kRopeRows][kRopePairs];  // cos, sin
+    const int r0 = blockIdx.x * p.rows_per_cta, nr = min(p.rows_per_cta, p.rows - r0);
+    griddep_wait();
+    griddep_launch_dependents();
+    for (int i = threadIdx.x; i < p.pairs; i += kRopeThreads) {
+        const unsigned long long f = turns_per_position(__ldg(p.inv_freq + i));
+        const int* pos = p.positions + p.axis_of[i] * p.positions_stride + r0;
+        for (int r = 0; r < nr; ++r) {
+            const unsigned long long t = (unsigned long long)(long long)__ldg(pos + r) * f;
+            float s, c;
+            sincospif((float)(int)(t >> 32) * 0x1p-31f, &s, &c);
+            cs[r][i] = make_float2(c, p.inverse ? -s : s);
+        }
+    }
+    __syncthreads();
+    // one task: VEC pairs of one head's row, or VEC channels behind them
+    const int rot = p.pairs / VEC, per = rot + (p.copy ? (p.head_dim - 2 * p.pairs) / VEC : 0);
+    const int heads = p.heads[0] + p.heads[1], tasks = nr * heads * per;
+    for (int t = threadIdx.x; t < tasks; t += kRopeThreads) {
+        const int u = t % per, h2 = t / per % heads, r = t / per / heads;
+        const int w = h2 >= p.heads[0], h = w ? h2 - p.heads[0] : h2;
+        const uint16_t* x = p.x[w] + (r0 + r) * p.x_row[w] + h * p.x_head[w];
+        uint16_t* y = p.y[w] + (r0 + r) * p.y_row[w] + h * p.y_head[w];
+        if (u >= rot) {
+            const int c = 2 * p.pairs + (u - rot) * VEC;
+            if constexpr (VEC == 8)
+                *reinterpret_cast<uint4*>(y + c) = *reinterpret_cast<const uint4*>(x + c);
+            else
+                y[c] = x[c];
+            continue;
+        }
+        const int i = u * VEC;
+        const int ia = p.interleaved ? 2 * i : i, ib = p.interleaved ? 2 * i + VEC : i + p.pairs;
+        if constexpr (VEC == 8) {
+            const uint4 a = *reinterpret_cast<const uint4*>(x + ia), b = *reinterpret_cast<const uint4*>(x + ib);
+            uint4 oa, ob;
+            if (p.interleaved) {
+                // (a, b) are the halves of one word
+                const uint32_t in[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                uint32_t o[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float2 v = Ops::unpack(in[e]), k = cs[r][i + e];
+                    o[e] = Ops::pack(fmaf(v.x, k.x, -v.y * k.y), fmaf(v.y, k.x, v.x * k.y));
+                }
+                oa = make_uint4(o[0], o[1], o[2], o[3]);
+                ob = make_uint4(o[4], o[5], o[6], o[7]);
+            } else {
+                const float4* k = reinterpret_cast<const float4*>(&cs[r][i]);
+                const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+                uint32_t ao[4], bo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float4 k2 = k[e];
+                    rotate2<DT>(aw[e], bw[e], make_float2(k2.x, k2.y), make_float2(k2.z, k2.w), ao[e], bo[e]);
+                }
+                oa = make_uint4(ao[0], ao[1], ao[2], ao[3]);
+                ob = make_uint4(bo[0], bo[1], bo[2], bo[3]);
+            }
+            *reinterpret_cast<uint4*>(y + ia) = oa;
+            *reinterpret_cast<uint4*>(y + ib) = ob;
+        } else {
+            const float a = Ops::unpack(x[ia]).x, b = Ops::unpack(x[ib]).x;
+            const float2 k = cs[r][i];
+            const uint32_t o = Ops::pack(fmaf(a, k.x, -b * k.y), fmaf(b, k.x, a * k.y));
+            y[ia] = (uint16_t)(o & 0xffffu);
+            y[ib] = (uint16_t)(o >> 16);
+        }
+    }
+}
+
+struct View {
+    const void* p;
+    long long row, head;
+    int heads;
+};
+
+size_t span(const View& v, int rows, int dim) {
+    return ((size_t)(rows - 1) * v.row + (size_t)(v.heads - 1) * v.head + dim) * 2;
+}
+
+}  // namespace
+
+}  // namespace fl
+
+extern "C" fl_status fl_rope(const fl_rope_desc* d, void* stream) {
+    using namespace fl;
+    using host::fail;
+    if (d == nullptr) return fail(FL_ERR_INVALID_ARG, "fl_rope: null description");
+    if (!host::valid_dtype(d->dtype)) return fail(FL_ERR_INVALID_ARG, "fl_rope: bad dtype %d", (int)d->dtype);
+    if (d->rows < 0 || d->heads_q < 1 || d->heads_k < 0 || d->head_dim < 1)
+        return fail(FL_ERR_INVALID_ARG, "fl_rope: sizes must be positive (rows may be 0)");
+    if (d->heads_q > 65535 || d->heads_k > 65535) return fail(FL_ERR_UNSUPPORTED, "fl_rope: more than 65535 heads");
+    if (d->head_dim > FL_ROPE_MAX_DIM)
+        return fail(FL_ERR_UNSUPPORTED, "fl_rope: head_dim above %d (%d)", FL_ROPE_MAX_DIM, d->head_dim);
+    if (d->rotary_dim < 2 || d->rotary_dim % 2 != 0 || d->rotary_dim > d->head_dim)
+        return fail(FL_ERR_INVALID_ARG, "fl_rope: rotary_dim must be even, 2 .. head_dim (%d of %d)", d->rotary_dim,
+                    d->head_dim);
+    if (d->n_axes < 1 || d->n_axes > 4) return fail(FL_ERR_INVALID_ARG, "fl_rope: n_axes must be 1 .. 4 (%d)", d->n_axes);
+    const int pairs = d->rotary_dim / 2;
+    for (int i = 0; d->axis_of != nullptr && i < pairs; ++i)
+        if (d->axis_of[i] >= d->n_axes)
+            return fail(FL_ERR_INVALID_ARG, "fl_rope: pair %d takes axis %d of %d", i, (int)d->axis_of[i], d->n_axes);
+    if (d->rows == 0) return host::ok();
+    const bool has_k = d->heads_k > 0;
+    if (d->positions == nullptr || d->inv_freq == nullptr || d->q == nullptr || d->q_out == nullptr ||
+        (has_k && (d->k == nullptr || d->k_out == nullptr)))
+        return fail(FL_ERR_INVALID_ARG, "fl_rope: a required pointer is null");
+    if ((reinterpret_cast<uintptr_t>(d->positions) | reinterpret_cast<uintptr_t>(d->inv_freq)) & 3u)
+        return fail(FL_ERR_ALIGNMENT, "fl_rope: positions and inv_freq must be 4-byte aligned");
+    if (d->n_axes > 1 && d->positions_stride < d->rows)
+        return fail(FL_ERR_INVALID_ARG, "fl_rope: positions_stride below rows");
+    const View in[2] = {{d->q, d->q_row, d->q_head, d->heads_q}, {d->k, d->k_row, d->k_head, d->heads_k}};
+    const View out[2] = {{d->q_out, d->q_out_row, d->q_out_head, d->heads_q},
+                         {d->k_out, d->k_out_row, d->k_out_head, d->heads_k}};
+    const int n = has_k ? 2 : 1;
+    bool vec = pairs % 8 == 0 && d->head_dim % 8 == 0, in_place = true;
+    for (int i = 0; i < n; ++i) {
+        for (const View& v : {in[i], out[i]}) {
+            const uintptr_t a = reinterpret_cast<uintptr_t>(v.p);
+            if (a & 1u) return fail(FL_ERR_ALIGNMENT, "fl_rope: tensors must be 2-byte aligned");
+            if (v.row < 0 || v.head < 0) return fail(FL_ERR_INVALID_ARG, "fl_rope: negative stride");
+            vec = vec && (a & 15u) == 0 && v.row % 8 == 0 && v.head % 8 == 0;
+        }
+        // no two elements of an output share a place
+        const View& o = out[i];
+        const long long by_row = (o.heads - 1) * o.head + d->head_dim, by_head = (d->rows - 1) * o.row + d->head_dim;
+        if ((o.heads > 1 && o.head < d->head_dim) || (d->rows > 1 && o.row < d->head_dim) ||
+            (d->rows > 1 && o.heads > 1 && o.row < by_row && o.head < by_head))
+            return fail(FL_ERR_INVALID_ARG, "fl_rope: an output's strides make its rows overlap");
+        const bool same = o.p == in[i].p && o.row == in[i].row && o.head == in[i].head;
+        in_place = in_place && same;
+        // against every input, and the other output
+        for (int j = 0; j < 2 * n; ++j) {
+            const View& v = j < n ? in[j] : out[j - n];
+            if ((j == i && same) || j - n == i) continue;
+            const long long wo = by_row, wv = (v.heads - 1) * v.head + d->head_dim;
+            if (host::overlap(o.p, span(o, d->rows, d->head_dim), v.p, span(v, d->rows, d->head_dim)) &&
+                !host::apart(o.p, o.row, wo, v.p, v.row, wv, 2))
+                return fail(FL_ERR_INVALID_ARG, "fl_rope: an output overlaps another tensor of the call");
+        }
+        const size_t pos = ((size_t)(d->n_axes - 1) * d->positions_stride + d->rows) * 4;
+        if (host::overlap(o.p, span(o, d->rows, d->head_dim), d->positions, pos) ||
+            host::overlap(o.p, span(o, d->rows, d->head_dim), d->inv_freq, (size_t)pairs * 4))
+            return fail(FL_ERR_INVALID_ARG, "fl_rope: an output overlaps another tensor of the call");
+    }
+    host::LaunchContext ctx;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const fl_status st = host::launch_context(s, &ctx);
+    if (st != FL_OK) return st;
+    RopeParams p = {};
+    for (int i = 0; i < n; ++i) {
+        p.x[i] = static_cast<const uint16_t*>(in[i].p);
+        p.y[i] = static_cast<uint16_t*>(const_cast<void*>(out[i].p));
+        p.x_row[i] = in[i].row, p.x_head[i] = in[i].head;
+        p.y_row[i] = out[i].row, p.y_head[i] = out[i].head;
+        p.heads[i] = in[i].heads;
+    }
+    p.positions = d->positions, p.positions_stride = d->positions_stride, p.inv_freq = d->inv_freq;
+    p.rows = d->rows, p.head_dim = d->head_dim, p.pairs = pairs;
+    p.interleaved = d->interleaved != 0, p.inverse = d->inverse != 0;
+    p.copy = !in_place && d->rotary_dim < d->head_dim;
+    for (int i = 0; i < pairs; ++i) p.axis_of[i] = d->axis_of != nullptr ? d->axis_of[i] : 0;
+    // one row per CTA until that fills the SMs several times over
+    p.rows_per_cta = 1;
+    while (p.rows_per_cta < kRopeRows && (d->rows + p.rows_per_cta - 1) / p.rows_per_cta > 8 * ctx.sms)
+        p.rows_per_cta *= 2;
+    const dim3 grid((unsigned)((d->rows + p.rows_per_cta - 1) / p.rows_per_cta));
+    cudaError_t e;
+    if (d->dtype == FL_F16)
+        e = vec ? host::launch(fl_rope_kernel<DT_F16, 8>, grid, kRopeThreads, 0, ctx.pdl, s, p)
+                : host::launch(fl_rope_kernel<DT_F16, 1>, grid, kRopeThreads, 0, ctx.pdl, s, p);
+    else
+        e = vec ? host::launch(fl_rope_kernel<DT_BF16, 8>, grid, kRopeThreads, 0, ctx.pdl, s, p)
+                : host::launch(fl_rope_kernel<DT_BF16, 1>, grid, kRopeThreads, 0, ctx.pdl, s, p);
+    return host::launched(e, "rotary kernel");
+}

@@ -1,0 +1,346 @@
+// Dense layers on 4-bit weights (fl_w4_gemm, fl_w4_swiglu_ffn) and their
+// quantiser (fl_w4_quantize).
+//
+//   out[m, n] = act(r[m] * sum_k x'[m, k] w[n, k] + bias[n]) (+ residual[m, n])
+//   w[n, k]   = scale[n, k / G] * (code[n, k] - zero[n, k / G])
+//
+// with x' = x * gamma rounded to the dtype and r the RMSNorm row scale where
+// there is a prologue (else x and 1).
+#include "fl_common.cuh"
+#include "fl_host.h"
+#include "fl_quant.cuh"
+#include "fl_w4.h"
+
+namespace fl {
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// quantiser
+// ---------------------------------------------------------------------------
+constexpr int kQuantThreads = 256;
+constexpr int kQuantVecs = 4;  // 16-byte vectors per lane in flight
+
+// clamp(round(w / s), -7, 7) with inv = 1 / s rounded. w * inv is within two
+// units in the last place of the quotient, and a quotient of two 16-bit values
+// that is not a tie is further than that from one (both have at most 11
+// significant bits): only next to a tie is the quotient itself computed. An
+// inv that overflowed (a subnormal scale) takes that way too.
+__device__ __forceinline__ float code4(float w, float s, float inv) {
+    const float y = w * inv;
+    float r = rintf(y);
+    if (!(fabsf(y - r) <= 0.4999f)) r = rintf(__fdiv_rn(w, s));
+    return fminf(fmaxf(r, -7.f), 7.f);
+}
+
+// Groups are consecutive in W [N, K] taken as one array, so are their codes
+// and scales: lane i of a warp takes the i-th 16-byte vector, G / 8
+// neighbouring lanes share a group. Bound by HBM (2.5 bytes per weight and a
+// little).
+template <int DT>
+__global__ void __launch_bounds__(kQuantThreads)
+    fl_w4_quantize_kernel(const uint16_t* __restrict__ W, uint32_t* __restrict__ q, uint16_t* __restrict__ scales,
+                          long long vecs, int lanes) {
+    using Ops = DTypeOps<DT>;
+    griddep_wait();
+    griddep_launch_dependents();
+    const long long v0 = (long long)blockIdx.x * (kQuantThreads * kQuantVecs) + threadIdx.x;
+    uint4 v[kQuantVecs];
+#pragma unroll
+    for (int u = 0; u < kQuantVecs; ++u) {
+        const long long i = v0 + u * kQuantThreads;
+        v[u] = i < vecs ? ldg_v4(W + i * 8) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int u = 0; u < kQuantVecs; ++u) {
+        const long long i = v0 + u * kQuantThreads;
+        uint32_t m = absmax8<DT>(v[u]);
+        for (int o = lanes / 2; o > 0; o >>= 1) m = absmax2<DT>(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (i >= vecs) continue;
+        const bool fine = (m & 0xffffu) < Bits16<DT>::kInf;
+        // the quotient by 7 is never next to a border of the 16-bit format
+        // without being on its near side, so rounding it twice is rounding once
+        uint32_t sb = Ops::pack(Ops::unpack(m).x / 7.0f, 0.f) & 0xffffu;
+        if (sb == 0u) sb = 1u;  // smallest positive value
+        const float s = Ops::unpack(sb).x, inv = 1.0f / s;
+        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+        uint32_t out = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = Ops::unpack(w[e]);
+            const int a = 8 + (int)code4(f.x, s, inv), b = 8 + (int)code4(f.y, s, inv);
+            out |= (uint32_t)(a | (b << 4)) << (8 * e);
+        }
+        q[i] = fine ? out : 0x88888888u;
+        if ((i & (lanes - 1)) == 0) scales[i / lanes] = fine ? (uint16_t)sb : (uint16_t)0x7fffu;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the products
+// ---------------------------------------------------------------------------
+constexpr int kSimpleRows = 4;
+
+// One warp: kSimpleRows rows of x against one row of the weight (or of the
+// gate and the up weight).
+template <int DT, bool DUAL>
+__global__ void __launch_bounds__(256) fl_w4_gemm_kernel(const __grid_constant__ W4Params p) {
+    using Ops = DTypeOps<DT>;
+    constexpr int NW = DUAL ? 2 : 1;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31, K = p.K, G = p.group;
+    const long long t = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int n = (int)(t % p.N);
+    const long long m0 = t / p.N * kSimpleRows;
+    if (m0 >= p.M) return;
+    float acc[NW][kSimpleRows] = {}, sq[kSimpleRows] = {};
+    for (int k = lane * 8; k < K; k += 256) {
+        float w[NW][8];
+#pragma unroll
+        for (int j = 0; j < NW; ++j) {
+            const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(p.q[j] + ((size_t)n * K + k) / 2));
+            const size_t g = (size_t)n * (K / G) + k / G;
+            const float s = Ops::unpack(__ldg(p.scales[j] + g)).x;
+            const float z = p.zeros[j] != nullptr ? (float)__ldg(p.zeros[j] + g) : 8.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[j][e] = s * ((float)((c >> (4 * e)) & 15u) - z);
+        }
+#pragma unroll
+        for (int r = 0; r < kSimpleRows; ++r) {
+            if (m0 + r >= p.M) continue;
+            uint4 v = ldg_v4(p.x + (m0 + r) * K + k);
+            const uint32_t xs[4] = {v.x, v.y, v.z, v.w};
+            uint4 g = make_uint4(0, 0, 0, 0);
+            if (p.gamma != nullptr) g = ldg_v4(p.gamma + k);
+            const uint32_t gs[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float2 f = Ops::unpack(xs[e]);
+                if (p.gamma != nullptr) {
+                    sq[r] = fmaf(f.x, f.x, fmaf(f.y, f.y, sq[r]));
+                    f = Ops::unpack(Ops::mul2(xs[e], gs[e]));
+                }
+#pragma unroll
+                for (int j = 0; j < NW; ++j) acc[j][r] = fmaf(f.x, w[j][2 * e], fmaf(f.y, w[j][2 * e + 1], acc[j][r]));
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < kSimpleRows; ++r) {
+        const long long m = m0 + r;
+        for (int o = 16; o > 0; o >>= 1) {
+            sq[r] += __shfl_xor_sync(0xffffffffu, sq[r], o);
+            for (int j = 0; j < NW; ++j) acc[j][r] += __shfl_xor_sync(0xffffffffu, acc[j][r], o);
+        }
+        if (lane != 0 || m >= p.M) continue;
+        const float rs = p.gamma != nullptr ? rsqrtf(sq[r] / (float)K + p.eps) : 1.f;
+        float y = acc[0][r] * rs;
+        if constexpr (DUAL) {
+            y = act_apply(ACT_SILU, y) * (acc[1][r] * rs);
+        } else {
+            if (p.bias != nullptr) y += Ops::unpack(p.bias[n]).x;
+            y = act_apply(p.act, y);
+            if (p.residual != nullptr) y += Ops::unpack(p.residual[m * p.N + n]).x;
+        }
+        p.out[m * p.N + n] = (uint16_t)(Ops::pack(y, 0.f) & 0xffffu);
+    }
+}
+
+fl_status check_weight(const char* name, const fl_w4_weight* w, long long N, long long K) {
+    using host::fail;
+    if (w == nullptr) return fail(FL_ERR_INVALID_ARG, "%s must not be null", name);
+    if (w->group != 32 && w->group != 64 && w->group != 128)
+        return fail(FL_ERR_INVALID_ARG, "%s: group must be 32, 64 or 128 (%d)", name, w->group);
+    if (N < 1 || K < 1) return fail(FL_ERR_INVALID_ARG, "%s: sizes must be positive (N=%lld K=%lld)", name, N, K);
+    if (N % 8 != 0 || K % w->group != 0)
+        return fail(FL_ERR_ALIGNMENT, "%s: N must be a multiple of 8 and K of the group (N=%lld K=%lld group %d)", name,
+                    N, K, w->group);
+    fl_status st;
+    if ((st = host::check_ptr(name, w->q, true)) != FL_OK) return st;
+    if ((st = host::check_ptr(name, w->scales, true)) != FL_OK) return st;
+    return host::check_ptr(name, w->zeros, false);
+}
+
+// Every tensor of one call: outputs overlap no input and no other output.
+struct Ranges {
+    struct R {
+        const void* p;
+        size_t n;
+    } in[16];
+    int n = 0;
+    void add(const void* p, size_t bytes) { in[n++] = R{p, bytes}; }
+    void add(const fl_w4_weight* w, size_t N, size_t K) {
+        add(w->q, N * K / 2);
+        add(w->scales, N * (K / w->group) * 2);
+        add(w->zeros, N * (K / w->group));
+    }
+    bool hit(const void* p, size_t bytes) const {
+        for (int i = 0; i < n; ++i)
+            if (host::overlap(p, bytes, in[i].p, in[i].n)) return true;
+        return false;
+    }
+};
+
+void set_weight(W4Params& p, int j, const fl_w4_weight* w) {
+    p.q[j] = static_cast<const uint8_t*>(w->q);
+    p.scales[j] = static_cast<const uint16_t*>(w->scales);
+    p.zeros[j] = static_cast<const uint8_t*>(w->zeros);
+    p.group = w->group;
+}
+
+// One product whose arguments have been checked.
+fl_status run(int dt, bool dual, const W4Params& p, const host::LaunchContext& ctx, cudaStream_t stream) {
+    const long long warps = (p.M + kSimpleRows - 1) / kSimpleRows * (long long)p.N;
+    const dim3 grid((unsigned)((warps + 7) / 8));
+    cudaError_t e;
+    if (dt == FL_F16)
+        e = dual ? host::launch(fl_w4_gemm_kernel<DT_F16, true>, grid, 256, 0, ctx.pdl, stream, p)
+                 : host::launch(fl_w4_gemm_kernel<DT_F16, false>, grid, 256, 0, ctx.pdl, stream, p);
+    else
+        e = dual ? host::launch(fl_w4_gemm_kernel<DT_BF16, true>, grid, 256, 0, ctx.pdl, stream, p)
+                 : host::launch(fl_w4_gemm_kernel<DT_BF16, false>, grid, 256, 0, ctx.pdl, stream, p);
+    return host::launched(e, "4-bit product kernel");
+}
+
+fl_status check_workspace(const void* workspace, size_t bytes, size_t need) {
+    if (need == 0) return FL_OK;
+    if (workspace == nullptr) return host::fail(FL_ERR_WORKSPACE, "workspace must not be null");
+    if (reinterpret_cast<uintptr_t>(workspace) & 15u)
+        return host::fail(FL_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+    if (bytes < need) return host::fail(FL_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", bytes, need);
+    return FL_OK;
+}
+
+}  // namespace
+
+}  // namespace fl
+
+extern "C" {
+
+fl_status fl_w4_quantize(const void* W, void* q, void* scales, int N, int K, int group, fl_dtype dtype,
+                         void* stream) {
+    using namespace fl;
+    if (!host::valid_dtype(dtype)) return host::fail(FL_ERR_INVALID_ARG, "bad dtype %d", (int)dtype);
+    const fl_w4_weight w = {q, scales, nullptr, group};
+    fl_status st;
+    if ((st = check_weight("fl_w4_quantize", &w, N, K)) != FL_OK) return st;
+    if ((st = host::check_ptr("W", W, true)) != FL_OK) return st;
+    const size_t n = (size_t)N * K;
+    if (host::overlap(q, n / 2, W, n * 2) || host::overlap(scales, n / group * 2, W, n * 2) ||
+        host::overlap(q, n / 2, scales, n / group * 2))
+        return host::fail(FL_ERR_INVALID_ARG, "q or scales overlaps another tensor of the call");
+    const long long vecs = (long long)(n / 8), per = kQuantThreads * kQuantVecs;
+    if ((vecs + per - 1) / per > 0x7fffffffll) return host::fail(FL_ERR_UNSUPPORTED, "fl_w4_quantize: too many weights");
+    host::LaunchContext ctx;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if ((st = host::launch_context(s, &ctx)) != FL_OK) return st;
+    const dim3 grid((unsigned)((vecs + per - 1) / per));
+    auto kern = dtype == FL_F16 ? fl_w4_quantize_kernel<DT_F16> : fl_w4_quantize_kernel<DT_BF16>;
+    return host::launched(host::launch(kern, grid, kQuantThreads, 0, ctx.pdl, s, static_cast<const uint16_t*>(W),
+                                       static_cast<uint32_t*>(q), static_cast<uint16_t*>(scales), vecs, group / 8),
+                          "4-bit quantiser");
+}
+
+size_t fl_w4_gemm_workspace_size(int M, int K, int norm) {
+    (void)M, (void)K, (void)norm;
+    return 0;
+}
+
+fl_status fl_w4_gemm(const void* x, const void* gamma, const fl_w4_weight* W, const void* bias, const void* residual,
+                     void* out, int M, int N, int K, float eps, fl_act act, void* workspace, size_t workspace_bytes,
+                     fl_dtype dtype, void* stream) {
+    using namespace fl;
+    if (!host::valid_dtype(dtype)) return host::fail(FL_ERR_INVALID_ARG, "bad dtype %d", (int)dtype);
+    if ((int)act < 0 || (int)act > FL_ACT_RELU) return host::fail(FL_ERR_INVALID_ARG, "bad activation %d", (int)act);
+    if (!(eps >= 0.0f) || eps > 1e30f) return host::fail(FL_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if (M < 1) return host::fail(FL_ERR_INVALID_ARG, "fl_w4_gemm: sizes must be positive (M=%d)", M);
+    fl_status st;
+    if ((st = check_weight("fl_w4_gemm: W", W, N, K)) != FL_OK) return st;
+    if ((st = host::check_ptr("x", x, true)) != FL_OK) return st;
+    if ((st = host::check_ptr("out", out, true)) != FL_OK) return st;
+    if ((st = host::check_ptr("gamma", gamma, false)) != FL_OK) return st;
+    if ((st = host::check_ptr("bias", bias, false)) != FL_OK) return st;
+    if ((st = host::check_ptr("residual", residual, false)) != FL_OK) return st;
+    const size_t need = fl_w4_gemm_workspace_size(M, K, gamma != nullptr), ob = (size_t)M * N * 2;
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != FL_OK) return st;
+    Ranges r;
+    r.add(x, (size_t)M * K * 2);
+    r.add(W, N, K);
+    r.add(gamma, (size_t)K * 2);
+    r.add(bias, (size_t)N * 2);
+    if (r.hit(out, ob)) return host::fail(FL_ERR_INVALID_ARG, "out overlaps an input");
+    if (residual != nullptr && residual != out && host::overlap(out, ob, residual, ob))
+        return host::fail(FL_ERR_INVALID_ARG, "out may alias residual only exactly");
+    if (need > 0 && (r.hit(workspace, need) || host::overlap(workspace, need, out, ob) ||
+                     host::overlap(workspace, need, residual, ob)))
+        return host::fail(FL_ERR_INVALID_ARG, "workspace overlaps another tensor of the call");
+    host::LaunchContext ctx;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if ((st = host::launch_context(s, &ctx)) != FL_OK) return st;
+    W4Params p = {};
+    p.x = static_cast<const uint16_t*>(x), p.gamma = static_cast<const uint16_t*>(gamma);
+    set_weight(p, 0, W);
+    p.bias = static_cast<const uint16_t*>(bias), p.residual = static_cast<const uint16_t*>(residual);
+    p.out = static_cast<uint16_t*>(out);
+    p.M = M, p.N = N, p.K = K, p.eps = eps, p.act = act;
+    return run(dtype, false, p, ctx, s);
+}
+
+size_t fl_w4_swiglu_ffn_workspace_size(int M, int D, int F) {
+    (void)D;
+    if (M < 1 || F < 1) return 0;
+    return (size_t)M * F * 2;
+}
+
+fl_status fl_w4_swiglu_ffn(const void* x, const void* gamma, const fl_w4_weight* Wg, const fl_w4_weight* Wu,
+                           const fl_w4_weight* Wd, const void* bias_down, void* out, int M, int D, int F, float eps,
+                           void* workspace, size_t workspace_bytes, fl_dtype dtype, void* stream) {
+    using namespace fl;
+    if (!host::valid_dtype(dtype)) return host::fail(FL_ERR_INVALID_ARG, "bad dtype %d", (int)dtype);
+    if (!(eps >= 0.0f) || eps > 1e30f) return host::fail(FL_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if (M < 1) return host::fail(FL_ERR_INVALID_ARG, "fl_w4_swiglu_ffn: sizes must be positive (M=%d)", M);
+    fl_status st;
+    if ((st = check_weight("fl_w4_swiglu_ffn: Wg", Wg, F, D)) != FL_OK) return st;
+    if ((st = check_weight("fl_w4_swiglu_ffn: Wu", Wu, F, D)) != FL_OK) return st;
+    if ((st = check_weight("fl_w4_swiglu_ffn: Wd", Wd, D, F)) != FL_OK) return st;
+    if (Wg->group != Wu->group || (Wg->zeros == nullptr) != (Wu->zeros == nullptr))
+        return host::fail(FL_ERR_INVALID_ARG, "fl_w4_swiglu_ffn: Wg and Wu must have the same group, and zero points both or neither");
+    if ((st = host::check_ptr("x", x, true)) != FL_OK) return st;
+    if ((st = host::check_ptr("gamma", gamma, true)) != FL_OK) return st;
+    if ((st = host::check_ptr("out", out, true)) != FL_OK) return st;
+    if ((st = host::check_ptr("bias_down", bias_down, false)) != FL_OK) return st;
+    const size_t need = fl_w4_swiglu_ffn_workspace_size(M, D, F), ob = (size_t)M * D * 2;
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != FL_OK) return st;
+    Ranges r;
+    r.add(x, ob);
+    r.add(gamma, (size_t)D * 2);
+    r.add(bias_down, (size_t)D * 2);
+    r.add(Wg, F, D);
+    r.add(Wu, F, D);
+    r.add(Wd, D, F);
+    if (r.hit(out, ob)) return host::fail(FL_ERR_INVALID_ARG, "out overlaps an input");
+    if (r.hit(workspace, need)) return host::fail(FL_ERR_INVALID_ARG, "workspace overlaps an input");
+    if (host::overlap(workspace, need, out, ob)) return host::fail(FL_ERR_INVALID_ARG, "workspace overlaps out");
+    host::LaunchContext ctx;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if ((st = host::launch_context(s, &ctx)) != FL_OK) return st;
+    // h = silu(RMSNorm(x) Wg^T) * (RMSNorm(x) Wu^T)
+    W4Params p = {};
+    p.x = static_cast<const uint16_t*>(x), p.gamma = static_cast<const uint16_t*>(gamma);
+    set_weight(p, 0, Wg);
+    set_weight(p, 1, Wu);
+    p.out = static_cast<uint16_t*>(workspace);
+    p.M = M, p.N = F, p.K = D, p.eps = eps;
+    if ((st = run(dtype, true, p, ctx, s)) != FL_OK) return st;
+    // out = h Wd^T (+ bias_down) + x
+    W4Params d = {};
+    d.x = static_cast<const uint16_t*>(workspace);
+    set_weight(d, 0, Wd);
+    d.bias = static_cast<const uint16_t*>(bias_down), d.residual = static_cast<const uint16_t*>(x);
+    d.out = static_cast<uint16_t*>(out);
+    d.M = M, d.N = D, d.K = F;
+    return run(dtype, false, d, ctx, s);
+}
+
+}  // extern "C"

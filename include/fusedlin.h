@@ -66,9 +66,10 @@ typedef enum {
     FL_ERR_INVALID_ARG = 1, /* null pointer, bad size, bad enum, forbidden aliasing */
     FL_ERR_UNSUPPORTED = 2, /* no sm_103a device, or a size beyond what the kernels handle */
     FL_ERR_ALIGNMENT = 3,   /* pointer not 16-byte aligned, or K/N/D/F not a multiple of 8 */
-    FL_ERR_WORKSPACE = 4,   /* FFN workspace missing or smaller than fl_swiglu_ffn_workspace_size */
+    FL_ERR_WORKSPACE = 4,   /* workspace missing or smaller than the call's *_workspace_size */
     FL_ERR_CUDA = 5,        /* a CUDA runtime or driver call failed (message in fl_last_error) */
-    FL_ERR_TIMEOUT = 6      /* a device-side wait ran past its limit (from fl_device_status) */
+    FL_ERR_TIMEOUT = 6,     /* a device-side wait ran past its limit (from fl_device_status) */
+    FL_ERR_RANGE = 7        /* a row of the paged cache had no page, and was skipped (from fl_device_status) */
 } fl_status;
 
 typedef enum { FL_F16 = 0, FL_BF16 = 1 } fl_dtype;
@@ -312,8 +313,10 @@ const char* fl_last_error(void);
 /*
  * Synchronises `stream`, then reads and clears the status word of `stream`,
  * which this library's kernels launched on that stream set when a bounded
- * wait runs out. Returns FL_OK, FL_ERR_TIMEOUT, or FL_ERR_CUDA if the
- * synchronisation itself failed.
+ * wait runs out, and its range word, which a kernel sets that skipped a row
+ * of the paged cache. Returns FL_OK, FL_ERR_TIMEOUT, FL_ERR_RANGE (a timeout
+ * first, the range word then stays set for the next call), or FL_ERR_CUDA if
+ * the synchronisation itself failed.
  * Each device keeps 64 status words: word 0 for the legacy default stream
  * (NULL), then one per stream handle in the order the library first sees
  * them; the 64th distinct handle and later ones share word 0. A kernel
@@ -411,6 +414,159 @@ fl_status fl_kernel_launches(long long* count);
  * with fl_device_status(stream) to read (and clear) the status.
  */
 fl_status fl_debug_wait_timeout(int limit_us, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Dense layers on 4-bit weights
+ * ------------------------------------------------------------------------
+ * A weight [N, K] is held as 4-bit codes, two to a byte along K (the even k in
+ * the low half), with one scale per `group` consecutive k of a row:
+ *   w[n, k] = scales[n, k / group] * (code[n, k] - zero[n, k / group])
+ *   q:      [N, K / 2] bytes
+ *   scales: [N, K / group] of the call's dtype
+ *   zeros:  [N, K / group] bytes (0 .. 15), or NULL: 8 everywhere
+ * group is 32, 64 or 128, K a multiple of group, N a multiple of 8. q is
+ * 16-byte aligned; scales and zeros are 16-byte aligned too.
+ */
+typedef struct {
+    const void* q;
+    const void* scales;
+    const void* zeros; /* or NULL */
+    int group;
+} fl_w4_weight;
+
+/*
+ * Symmetric round-to-nearest quantisation of W [N, K] (fp16 / bf16) into q and
+ * scales as above (zero point 8, codes 1 .. 15). Per group, with amax the
+ * largest |w|:
+ *   scale = amax / 7 rounded to the dtype, at least its smallest positive value
+ *   code  = 8 + clamp(round(w / scale), -7, 7), ties to even
+ * The codes are those of the exact quotient by the stored scale. A group that
+ * holds a NaN or an infinity gets a NaN scale and codes of 8.
+ */
+fl_status fl_w4_quantize(const void* W, void* q, void* scales, int N, int K, int group, fl_dtype dtype,
+                         void* stream);
+
+/*
+ * out[M,N] = act(norm(x)[M,K] W^T + bias) (+ residual) on a 4-bit weight.
+ *   gamma: [K], the RMSNorm prologue of fl_norm_gemm; NULL: x as it is.
+ *   bias [N] and residual [M,N] may be NULL; residual may be the same pointer
+ *   as out. Epilogue order as in fl_gemm_epilogue.
+ * workspace: fl_w4_gemm_workspace_size(M, K, gamma != NULL) bytes (0 for some
+ * sizes, and then NULL is accepted), 16-byte aligned, the call's own until its
+ * kernels are done: calls (and captured graphs) that may overlap on the GPU
+ * need one each.
+ */
+size_t fl_w4_gemm_workspace_size(int M, int K, int norm);
+fl_status fl_w4_gemm(const void* x, const void* gamma, const fl_w4_weight* W, const void* bias,
+                     const void* residual, void* out, int M, int N, int K, float eps, fl_act act,
+                     void* workspace, size_t workspace_bytes, fl_dtype dtype, void* stream);
+
+/*
+ * fl_swiglu_ffn on 4-bit weights: Wg, Wu are [F, D], Wd is [D, F]. D and F are
+ * multiples of the weights' groups (and of 8); Wg and Wu have the same group,
+ * and zero points both or neither. h is kept in the dtype, as there.
+ * workspace: fl_w4_swiglu_ffn_workspace_size(M, D, F) bytes, as above.
+ */
+size_t fl_w4_swiglu_ffn_workspace_size(int M, int D, int F);
+fl_status fl_w4_swiglu_ffn(const void* x, const void* gamma, const fl_w4_weight* Wg, const fl_w4_weight* Wu,
+                           const fl_w4_weight* Wd, const void* bias_down, void* out, int M, int D, int F,
+                           float eps, void* workspace, size_t workspace_bytes, fl_dtype dtype, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions
+ * ------------------------------------------------------------------------
+ * Rotates the first rotary_dim channels of every head of q and k by
+ * angle(row, i) = positions[axis_of[i]][row] * inv_freq[i], i < rotary_dim / 2:
+ *   (a, b) -> (a cos - b sin, b cos + a sin)
+ * where (a, b) are channels (i, i + rotary_dim / 2), or (2i, 2i + 1) with
+ * interleaved; the other channels are copied. inverse rotates by -angle: the
+ * gradient of the rotation with respect to its input. The angle is reduced
+ * exactly (the position times the frequency in turns, in 64-bit fixed point),
+ * so far positions lose nothing; positions are any int32.
+ *   q: [rows, heads_q, head_dim] at the row and head strides given (elements;
+ *   channels are contiguous), k likewise (k NULL or heads_k 0: q alone).
+ *   q_out, k_out: where to, with strides of their own; may be the inputs
+ *   themselves (same pointer and strides). No other overlap is allowed.
+ *   positions: device, [n_axes][rows] int32, axis a at positions + a *
+ *   positions_stride. inv_freq: device, [rotary_dim / 2] fp32, finite.
+ *   axis_of: HOST, rotary_dim / 2 bytes below n_axes, read during the call;
+ *   NULL: axis 0 for all.
+ * Pointers are 2-byte aligned (inv_freq and positions 4); rows whose base and
+ * strides are multiples of 16 bytes take the vector form. head_dim <= 512,
+ * rotary_dim even, 2 .. head_dim; n_axes 1 .. 4. rows 0 does nothing.
+ */
+#define FL_ROPE_MAX_DIM 512
+typedef struct {
+    fl_dtype dtype;
+    int rows, heads_q, heads_k, head_dim, rotary_dim, n_axes, interleaved, inverse;
+    const unsigned char* axis_of;
+    const int* positions;
+    long long positions_stride;
+    const float* inv_freq;
+    const void* q;
+    const void* k;
+    void* q_out;
+    void* k_out;
+    long long q_row, q_head, k_row, k_head, q_out_row, q_out_head, k_out_row, k_out_head;
+} fl_rope_desc;
+fl_status fl_rope(const fl_rope_desc* desc, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Paged 8-bit key/value cache
+ * ------------------------------------------------------------------------
+ * k_cache, v_cache: [n_pages, page_size, heads, head_dim] codes, one byte each;
+ * k_scale, v_scale: [n_pages, page_size, heads] fp32, one per row and head.
+ * A head's row x is held as codes with the value scale * code:
+ *   scale = max(amax / top, 2^-126), amax the largest |x|; top 127 or 448
+ *   FL_KV_INT8: code = round(x / scale), ties to even (two's complement)
+ *   FL_KV_E4M3: code = x / scale rounded to the nearest 8-bit float with 4
+ *               exponent and 3 mantissa bits (finite variant), ties to even
+ * The codes are those of the exact quotient by the stored scale. A head's row
+ * that holds a NaN or an infinity gets a NaN scale and codes of 0, and so reads
+ * back as NaN.
+ *
+ * Rows of k and v belong to sequences: row i to the sequence b with
+ * cu_rows[b] <= i < cu_rows[b + 1], at its position p = start[b] + i -
+ * cu_rows[b], which is held at row p % page_size of page
+ * page_table[b][p / page_size].
+ *   cu_rows: device, [n_seqs + 1] int32, not decreasing; NULL: row b is the
+ *   one row of sequence b (a decode step).
+ *   start:   device, [n_seqs] int32; NULL: 0.
+ *   page_table: device, [n_seqs][table_pages] int32, sequence b at
+ *   page_table + b * table_stride.
+ * Rows in front of cu_rows[0] and from cu_rows[n_seqs] on (from n_seqs on
+ * without cu_rows) belong to no sequence: they are neither written nor
+ * read. A row whose position is negative or past its table, or whose page is
+ * not in 0 .. n_pages - 1, is skipped, and fl_device_status() on the stream
+ * reports FL_ERR_RANGE.
+ *
+ * fl_kv_write quantises rows of k and v into the cache. No place of the cache
+ * may be reached by two rows of one call: which of them it then holds, and
+ * whether codes and scale belong together, is not defined.
+ * fl_kv_read writes scale * code, rounded to the dtype, to rows of k and v.
+ *   k, v: [rows, heads, head_dim] at the row and head strides given (elements,
+ *   multiples of 8; channels are contiguous), 16-byte aligned.
+ * head_dim is a multiple of 8, 8 .. 256. rows 0 does nothing.
+ */
+typedef enum { FL_KV_INT8 = 0, FL_KV_E4M3 = 1 } fl_kv_format;
+typedef struct {
+    fl_dtype dtype;
+    fl_kv_format format;
+    int rows, heads, head_dim, page_size, n_pages, n_seqs, table_pages;
+    long long table_stride;
+    const int* page_table;
+    const int* cu_rows;
+    const int* start;
+    void* k; /* read by fl_kv_write, written by fl_kv_read */
+    void* v;
+    long long k_row, k_head, v_row, v_head;
+    void* k_cache;
+    void* v_cache;
+    float* k_scale;
+    float* v_scale;
+} fl_kv_desc;
+fl_status fl_kv_write(const fl_kv_desc* desc, void* stream);
+fl_status fl_kv_read(const fl_kv_desc* desc, void* stream);
 
 /* Library version string. */
 const char* fl_version(void);

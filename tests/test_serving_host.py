@@ -1,0 +1,325 @@
+"""The serving operators without a GPU: refusals of the C ABI, pins of their oracle, and the kernels' index and
+rounding steps restated on the CPU."""
+import ctypes
+from fractions import Fraction
+
+import numpy as np
+import pytest
+import torch
+
+import gemm_epilogue_tma_gb300 as fl
+import oracle
+from gemm_epilogue_tma_gb300 import _build
+
+OK, INVALID, UNSUPPORTED, ALIGN, WORKSPACE, CUDA, TIMEOUT, RANGE = range(8)
+BASE = 0x7F0000000000
+PASSES = (UNSUPPORTED,)  # validation passed: the device query fails on this machine
+
+
+@pytest.fixture(scope="module")
+def L():
+    _build.build()
+    return fl.lib()
+
+
+no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="fake addresses must not reach a device")
+
+
+def addr(i, off=0):
+    return BASE + i * (1 << 36) + off
+
+
+# ---------------------------------------------------------------------------
+# refusals
+# ---------------------------------------------------------------------------
+def weight(i=10, **kw):
+    return fl.W4Weight(**{**dict(q=addr(i), scales=addr(i + 1), zeros=None, group=64), **kw})
+
+
+@no_gpu
+def test_w4_quantize_refusals(L):
+    def call(W=addr(0), q=addr(1), s=addr(2), N=64, K=256, group=64, dt=0):
+        return L.fl_w4_quantize(W, q, s, N, K, group, dt, None)
+    assert call() in PASSES
+    assert call(W=None) == INVALID and call(q=None) == INVALID and call(s=None) == INVALID
+    assert call(group=16) == INVALID and call(group=0) == INVALID and call(group=256) == INVALID
+    assert call(N=0) == INVALID and call(K=0) == INVALID and call(K=-64) == INVALID
+    assert call(K=96) == ALIGN and call(N=12) == ALIGN
+    assert call(q=addr(1, 4)) == ALIGN and call(W=addr(0, 2)) == ALIGN
+    assert call(dt=2) == INVALID
+    assert call(q=addr(0, 64)) == INVALID and call(s=addr(1, 16)) == INVALID
+
+
+@no_gpu
+def test_w4_gemm_refusals(L):
+    def call(x=addr(0), gamma=addr(1), W=None, bias=addr(2), res=addr(3), out=addr(4), M=5, N=64, K=256, eps=1e-6,
+             act=0, ws=addr(5), size=1 << 30, dt=0, no_weight=False):
+        w = None if no_weight else ctypes.byref(W or weight())
+        return L.fl_w4_gemm(x, gamma, w, bias, res, out, M, N, K, eps, act, ws, size, dt, None)
+    assert call() in PASSES
+    assert call(gamma=None, bias=None, res=None) in PASSES
+    assert call(res=addr(4)) in PASSES
+    assert call(no_weight=True) == INVALID
+    assert call(x=None) == INVALID and call(out=None) == INVALID
+    assert call(W=weight(q=None)) == INVALID and call(W=weight(scales=None)) == INVALID
+    assert call(W=weight(group=48)) == INVALID and call(W=weight(group=128), K=192) == ALIGN
+    assert call(W=weight(q=addr(10, 8))) == ALIGN and call(W=weight(zeros=addr(12, 2))) == ALIGN
+    assert call(M=0) == INVALID and call(N=0) == INVALID and call(N=60) == ALIGN
+    assert call(act=4) == INVALID and call(dt=7) == INVALID
+    assert call(eps=-1.0) == INVALID and call(eps=float("nan")) == INVALID and call(eps=float("inf")) == INVALID
+    assert call(out=addr(0, 16)) == INVALID and call(out=addr(10, 16)) == INVALID and call(out=addr(11)) == INVALID
+    assert call(res=addr(4, 16)) == INVALID
+    for rows in (1, 9, 300):
+        need = fl.w4_gemm_workspace_size(rows, 256, True)
+        if need:
+            assert call(M=rows, ws=None) == WORKSPACE and call(M=rows, size=need - 1) == WORKSPACE
+            assert call(M=rows, ws=addr(5, 8)) == ALIGN
+            assert call(M=rows, ws=addr(0)) == INVALID and call(M=rows, ws=addr(4)) == INVALID
+            assert call(M=rows, ws=addr(3)) == INVALID
+
+
+@no_gpu
+def test_w4_swiglu_refusals(L):
+    def call(x=addr(0), gamma=addr(1), g=None, u=None, d=None, bias=addr(2), out=addr(4), M=5, D=128, F=256, ws=addr(5),
+             size=1 << 30):
+        g, u, d = g or weight(20), u or weight(22), d or weight(24)
+        return L.fl_w4_swiglu_ffn(x, gamma, ctypes.byref(g), ctypes.byref(u), ctypes.byref(d), bias, out, M, D, F, 1e-6,
+                                  ws, size, 1, None)
+    assert call() in PASSES
+    assert call(bias=None) in PASSES
+    assert call(gamma=None) == INVALID and call(x=None) == INVALID
+    assert call(u=weight(22, group=128)) == INVALID          # another group than Wg's
+    assert call(u=weight(22, zeros=addr(26))) == INVALID     # zero points on one of the pair
+    assert call(g=weight(20, zeros=addr(27)), u=weight(22, zeros=addr(26))) in PASSES
+    assert call(d=weight(24, group=128), F=192) == ALIGN
+    assert call(ws=None) == WORKSPACE and call(size=5 * 256 * 2 - 1) == WORKSPACE
+    assert call(ws=addr(20, 64)) == INVALID and call(ws=addr(4)) == INVALID and call(ws=addr(0)) == INVALID
+    assert call(out=addr(0)) == INVALID and call(out=addr(23)) == INVALID
+
+
+def rope_desc(**kw):
+    d = dict(dtype=1, rows=10, heads_q=4, heads_k=2, head_dim=64, rotary_dim=64, n_axes=1, interleaved=0, inverse=0,
+             axis_of=None, positions=addr(0), positions_stride=10, inv_freq=addr(1), q=addr(2), k=addr(3),
+             q_out=addr(4), k_out=addr(5), q_row=256, q_head=64, k_row=128, k_head=64, q_out_row=256, q_out_head=64,
+             k_out_row=128, k_out_head=64)
+    return fl.RopeDesc(**{**d, **kw})
+
+
+@no_gpu
+def test_rope_refusals(L):
+    def call(**kw):
+        return L.fl_rope(ctypes.byref(rope_desc(**kw)), None)
+    assert L.fl_rope(None, None) == INVALID
+    assert call() in PASSES
+    assert call(rows=0, q=None) == OK
+    assert call(heads_k=0, k=None, k_out=None) in PASSES
+    assert call(q_out=addr(2), k_out=addr(3)) in PASSES                       # in place
+    assert call(q_out=addr(2), q_out_row=512) == INVALID                      # in place needs the same strides
+    assert call(q_out=addr(2, 128)) == INVALID and call(q_out=addr(3)) == INVALID and call(k_out=addr(4)) == INVALID
+    # q and k as column ranges of one matrix, in place and to another such matrix
+    both = dict(q_row=384, k_row=384, q=addr(2), k=addr(2, 512), q_out_row=384, k_out_row=384)
+    assert call(**both, q_out=addr(2), k_out=addr(2, 512)) in PASSES
+    assert call(**both, q_out=addr(4), k_out=addr(4, 512)) in PASSES
+    assert call(**both, q_out=addr(4), k_out=addr(4, 510)) == INVALID
+    assert call(**both, q_out=addr(2, 512), k_out=addr(2)) == INVALID
+    assert call(rotary_dim=63) == INVALID and call(rotary_dim=66) == INVALID and call(rotary_dim=0) == INVALID
+    assert call(head_dim=520, rotary_dim=64) == UNSUPPORTED
+    assert call(n_axes=0) == INVALID and call(n_axes=5) == INVALID
+    assert call(n_axes=2, axis_of=bytes([0, 1] * 16)) in PASSES
+    assert call(n_axes=2, axis_of=bytes([0, 2] * 16)) == INVALID
+    assert call(n_axes=2, axis_of=bytes(32), positions_stride=9) == INVALID
+    assert call(dtype=3) == INVALID and call(rows=-1) == INVALID and call(heads_q=0) == INVALID
+    assert call(positions=None) == INVALID and call(k=None) == INVALID
+    assert call(q=addr(2, 1)) == ALIGN and call(positions=addr(0, 2)) == ALIGN
+    assert call(q=addr(2, 2)) in PASSES                                       # the scalar form
+    assert call(q_out_row=32) == INVALID and call(q_out_head=32) == INVALID and call(q_row=-256) == INVALID
+    assert call(q_row=0, q_head=0) in PASSES                                  # a broadcast input
+    assert call(q_out=addr(0)) == INVALID and call(k_out=addr(1)) == INVALID
+
+
+def kv_desc(**kw):
+    d = dict(dtype=1, format=0, rows=20, heads=2, head_dim=64, page_size=16, n_pages=8, n_seqs=3, table_pages=4,
+             table_stride=4, page_table=addr(0), cu_rows=addr(1), start=addr(2), k=addr(3), v=addr(4), k_row=128,
+             k_head=64, v_row=128, v_head=64, k_cache=addr(5), v_cache=addr(6), k_scale=addr(7), v_scale=addr(8))
+    return fl.KvDesc(**{**d, **kw})
+
+
+@no_gpu
+@pytest.mark.parametrize("name", ["fl_kv_write", "fl_kv_read"])
+def test_kv_refusals(L, name):
+    fn, write = getattr(L, name), name == "fl_kv_write"
+
+    def call(**kw):
+        return fn(ctypes.byref(kv_desc(**kw)), None)
+    assert fn(None, None) == INVALID
+    assert call() in PASSES
+    assert call(cu_rows=None, start=None) in PASSES
+    assert call(rows=0) == OK
+    for n in ("rows", "heads", "head_dim", "page_size", "n_pages", "n_seqs", "table_pages"):
+        assert call(**{n: -1}) == INVALID
+    assert call(head_dim=60) == ALIGN and call(head_dim=264) == UNSUPPORTED
+    assert call(format=2) == INVALID and call(dtype=2) == INVALID
+    for n in ("k", "v", "k_cache", "v_cache", "k_scale", "v_scale", "page_table"):
+        assert call(**{n: None}) == INVALID
+    assert call(k=addr(3, 8)) == ALIGN and call(k_row=132) == ALIGN and call(page_table=addr(0, 2)) == ALIGN
+    assert call(table_stride=3) == INVALID
+    # k and v as column ranges of one matrix
+    both = dict(k_row=384, v_row=384, k=addr(3), v=addr(3, 256))
+    assert call(**both) in PASSES
+    assert call(**{**both, "v": addr(3, 240)}) == (UNSUPPORTED if write else INVALID)
+    assert call(v=addr(3)) == (UNSUPPORTED if write else INVALID)
+    assert call(k_row=0) == (UNSUPPORTED if write else INVALID)               # a broadcast input
+    assert call(k_head=32) == (UNSUPPORTED if write else INVALID)
+    assert call(k_row=64, k_head=64) == (UNSUPPORTED if write else INVALID)
+    # heads-first outputs: [heads, rows, dim]
+    assert call(k_row=64, k_head=20 * 64, v_row=64, v_head=20 * 64) in PASSES
+    assert call(k_cache=addr(6)) == (INVALID if write else UNSUPPORTED)
+    assert call(k_cache=addr(3)) == INVALID and call(k_scale=addr(4)) == INVALID
+    assert call(rows=1 << 30, k_row=8, v_row=8, heads=1, head_dim=8) == UNSUPPORTED
+    assert "rows" in fl.last_error()
+
+
+def test_struct_layouts_match_the_header(L):
+    # sizes of the C structs on LP64: ints, then 8-byte pointers and strides
+    assert ctypes.sizeof(fl.W4Weight) == 32
+    assert ctypes.sizeof(fl.RopeDesc) == 9 * 4 + 4 + 4 * 8 + 4 * 8 + 8 * 8
+    assert ctypes.sizeof(fl.KvDesc) == 9 * 4 + 4 + 8 + 5 * 8 + 4 * 8 + 4 * 8
+
+
+# ---------------------------------------------------------------------------
+# oracle pins
+# ---------------------------------------------------------------------------
+def round16(dt):
+    t = {"f16": torch.float16, "bf16": torch.bfloat16}[dt]
+    return lambda v: torch.from_numpy(np.asarray(v, dtype=np.float32)).to(t).double().numpy()
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_w4_codes_are_the_exact_nearest(dt):
+    rng = np.random.default_rng(5)
+    W = round16(dt)(rng.standard_normal((4, 64)))
+    W[0, :8] = [7, 3.5, 2.5, 1.5, -2.5, 0.5, -0.5, 0]        # exact ties with a scale of 1
+    W[0, 8:32] = 0
+    code, scale = oracle.w4_quantize(W, 32, round16(dt), 2.0 ** -24)
+    assert scale[0, 0] == 1.0 and list(code[0, :8] - 8) == [7, 4, 2, 2, -2, 0, 0, 0]
+    for n in range(4):
+        for k in range(64):
+            quo = Fraction(W[n, k]) / Fraction(scale[n, k // 32])
+            assert abs(quo - (int(code[n, k]) - 8)) <= Fraction(1, 2) or abs(quo) > 7
+    back = oracle.w4_weight(oracle.w4_pack(code), scale)
+    assert np.abs(back - W).max() <= 0.51 * scale.max()
+    z = rng.integers(0, 16, scale.shape)
+    assert np.array_equal(oracle.w4_weight(oracle.w4_pack(code), scale, z)[1, :32], (code[1, :32] - z[1, 0]) * scale[1, 0])
+
+
+def test_e4m3_rounding_matches_the_format():
+    every = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).float().double().numpy()
+    every = np.unique(every[np.isfinite(every)])
+    assert every[-1] == 448 and np.array_equal(oracle.e4m3_round(every), every)
+    rng = np.random.default_rng(1)
+    x = np.concatenate([rng.uniform(-448, 448, 500), rng.standard_normal(500) * 0.02])
+    near = every[np.abs(every[None] - x[:, None]).argmin(1)]
+    assert np.array_equal(oracle.e4m3_round(x), near)
+    mid = (every[:-1] + every[1:]) / 2
+    t = torch.from_numpy(mid.astype(np.float32)).to(torch.float8_e4m3fn).float().double().numpy()
+    assert np.array_equal(oracle.e4m3_round(mid), t)  # ties to even
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_oracle_is_a_rotation(interleaved):
+    rng = np.random.default_rng(2)
+    x = rng.standard_normal((3, 2, 10))
+    f = np.array([1.0, 0.3, 0.01], dtype=np.float32)
+    pos = np.array([[0, 5, -7], [1, 2, 3]])
+    axis = [0, 1, 0]
+    y = oracle.rope(x, pos, f, axis, interleaved)
+    assert np.array_equal(y[..., 6:], x[..., 6:])
+    assert np.allclose((y ** 2).sum(-1), (x ** 2).sum(-1))
+    assert np.allclose(oracle.rope(y, pos, f, axis, interleaved, inverse=True), x)
+    lo, hi = (2, 3) if interleaved else (1, 4)
+    z = (x[2, 1, lo] + 1j * x[2, 1, hi]) * np.exp(1j * 3 * float(f[1]))
+    assert np.allclose([y[2, 1, lo], y[2, 1, hi]], [z.real, z.imag])
+
+
+# ---------------------------------------------------------------------------
+# the kernels' steps, restated
+# ---------------------------------------------------------------------------
+def test_fixed_point_turns_hold_for_every_position():
+    """position * frac(f / 2 pi) modulo one turn in 64-bit fixed point, against exact arithmetic: at most 2^-24 turns
+    off (half a unit of float64 in f / 2 pi, times 2^31, is 2^-25 for f <= 2 pi)."""
+    rng = np.random.default_rng(3)
+    inv2pi = Fraction(0.15915494309189533577)
+    exact_inv2pi = Fraction("0.159154943091895335768883763372514362034459645740456448747667344058896797634226535")
+    for f in [1.0, 0.5, 1e-4, 0.731, 6.0, 2e-7] + list(rng.uniform(0, 1, 20)):
+        f = float(np.float32(f))
+        t = float(f) * float(inv2pi)
+        F = min(int((t - np.floor(t)) * 18446744073709551616.0), 2 ** 64 - 1)
+        for p in [0, 1, -1, 2 ** 31 - 1, -2 ** 31, 1048575] + list(rng.integers(-2 ** 31, 2 ** 31, 20)):
+            got = Fraction((int(p) * F) % 2 ** 64, 2 ** 64)
+            want = (int(p) * Fraction(f) * exact_inv2pi) % 1
+            off = abs(got - want)
+            assert min(off, 1 - off) <= Fraction(1, 2 ** 24), (f, p)
+
+
+def find_slot(i, n_seqs, cu):
+    """The kernel's 32-ary search, lane by lane: the number of entries of cu[1:] that are <= i. Every index it reads
+    is checked."""
+    lo, n, rounds = 0, n_seqs, 0
+    while n > 0:
+        step = (n + 31) // 32
+        c = 0
+        for lane in range(32):
+            at = min(lo + (lane + 1) * step, lo + n)
+            assert 0 <= at <= n_seqs
+            le = cu[at] <= i
+            c += bool(le and lo + (lane + 1) * step <= lo + n + step - 1)
+        done = min(c * step, n)
+        lo += done
+        n = 0 if done == n else min(step - 1, n - done)
+        rounds += 1
+        assert rounds < 8
+    return lo
+
+
+@pytest.mark.parametrize("n_seqs", [1, 2, 31, 32, 33, 64, 100, 1024, 1025, 5000])
+def test_sequence_search(n_seqs):
+    rng = np.random.default_rng(n_seqs)
+    for kind in range(3):
+        n = rng.integers(0, 4, n_seqs) if kind else np.ones(n_seqs, dtype=int)
+        cu = np.concatenate([[rng.integers(0, 3) if kind == 2 else 0], n]).cumsum()
+        for i in rng.integers(0, cu[-1] + 3, 12):
+            want = int(np.searchsorted(cu[1:], i, side="right"))
+            assert find_slot(i, n_seqs, cu) == want
+    # offsets out of order: some index in range, and an end
+    junk = rng.integers(-5, 50, n_seqs + 1)
+    for i in (0, 10, 60):
+        assert 0 <= find_slot(i, n_seqs, junk) <= n_seqs
+
+
+def test_codes_next_to_a_border():
+    """The kernel's fp32 steps against the exact quotient, on rows whose values lie on and next to borders."""
+    f32 = np.float32
+
+    def fma(a, b, c):  # one rounding; exact in Fraction
+        return f32(float(Fraction(float(a)) * Fraction(float(b)) + Fraction(float(c))))
+
+    def nearest_even(fr):
+        lo = fr.numerator // fr.denominator
+        d = fr - lo
+        return lo + 1 if d > Fraction(1, 2) or (d == Fraction(1, 2) and lo % 2) else lo
+
+    rng = np.random.default_rng(9)
+    for _ in range(300):
+        amax = f32(round16("bf16")(abs(rng.standard_normal()) + 0.01))
+        s = f32(amax / f32(127.0))
+        inv = f32(f32(1.0) / s)
+        for c in rng.integers(-127, 127, 6):
+            for x in {float(round16("bf16")((c + 0.5) * float(s))), float(amax) / 2, float(amax)}:
+                x = f32(x)
+                y = f32(x * inv)
+                r = np.rint(y)
+                if abs(f32(y - r)) > f32(0.4999):
+                    lo = np.floor(y)
+                    d = fma(-(lo + f32(0.5)), s, x)
+                    r = lo + 1 if d > 0 else lo if d < 0 else f32(2) * np.rint(f32(0.5) * (lo + f32(0.5)))
+                assert int(r) == nearest_even(Fraction(float(x)) / Fraction(float(s)))
