@@ -179,17 +179,20 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// Row-major [outer, inner] fp16/bf16 matrix, box {box_inner, box_outer},
-// 128-byte swizzle (or none), zero fill out of range.
+// Row-major [outer, inner] matrix (fp16/bf16, or bytes with elem_bytes 1), box
+// {box_inner, box_outer}, 128-byte swizzle (or none), zero fill out of range.
 fl_status encode_2d(CUtensorMap* m, int dt, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_inner,
-                    uint32_t box_outer, bool swizzle = true) {
+                    uint32_t box_outer, bool swizzle = true, int elem_bytes = 2) {
     EncodeTiledFn fn = encode_fn();
     if (fn == nullptr) return fail(FL_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
     cuuint64_t dims[2] = {inner, outer};
-    cuuint64_t strides[1] = {inner * 2};
+    cuuint64_t strides[1] = {inner * elem_bytes};
     cuuint32_t box[2] = {box_inner, box_outer};
     cuuint32_t estr[2] = {1, 1};
-    CUresult r = fn(m, dt == FL_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+    const CUtensorMapDataType type = elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : dt == FL_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    CUresult r = fn(m, type, 2,
                     const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                     swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -958,6 +961,11 @@ fl_status launched(cudaError_t e, const char* what) {
 fl_status check_ptr(const char* name, const void* p, bool required) { return ::check_ptr(name, p, required); }
 
 bool overlap(const void* a, size_t na, const void* b, size_t nb) { return ::overlap(a, na, b, nb); }
+
+fl_status encode_matrix(CUtensorMap* m, int dt, int elem_bytes, const void* ptr, uint64_t inner, uint64_t outer,
+                        uint32_t box_inner, uint32_t box_outer) {
+    return encode_2d(m, dt, ptr, inner, outer, box_inner, box_outer, true, elem_bytes);
+}
 
 }  // namespace host
 }  // namespace fl

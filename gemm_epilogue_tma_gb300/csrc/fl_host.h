@@ -48,6 +48,12 @@ inline bool apart(const void* a, long long a_row, long long a_width, const void*
 }
 inline bool valid_dtype(int dt) { return dt == FL_F16 || dt == FL_BF16; }
 
+// Tensor map of a row-major [outer, inner] matrix of 16-bit elements (fp16 or
+// bf16 by dt) or of bytes, box {box_inner, box_outer}, 128-byte swizzle, zero
+// fill out of range.
+fl_status encode_matrix(CUtensorMap* m, int dt, int elem_bytes, const void* ptr, uint64_t inner, uint64_t outer,
+                        uint32_t box_inner, uint32_t box_outer);
+
 // cudaLaunchKernelEx with the programmatic-dependency attribute of the library's launches.
 template <typename Kern, typename... Args>
 cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, int pdl, cudaStream_t stream, const Args&... args) {

@@ -8,6 +8,7 @@
 // there is a prologue (else x and 1).
 #include "fl_common.cuh"
 #include "fl_host.h"
+#include "fl_internal.h"
 #include "fl_quant.cuh"
 #include "fl_w4.h"
 
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(256) fl_w4_gemm_kernel(const __grid_constant__
             const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(p.q[j] + ((size_t)n * K + k) / 2));
             const size_t g = (size_t)n * (K / G) + k / G;
             const float s = Ops::unpack(__ldg(p.scales[j] + g)).x;
-            const float z = p.zeros[j] != nullptr ? (float)__ldg(p.zeros[j] + g) : 8.f;
+            const float z = p.zeros[j] != nullptr ? (float)(__ldg(p.zeros[j] + g) & 15) : 8.f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[j][e] = s * ((float)((c >> (4 * e)) & 15u) - z);
         }
@@ -189,8 +190,24 @@ void set_weight(W4Params& p, int j, const fl_w4_weight* w) {
     p.group = w->group;
 }
 
-// One product whose arguments have been checked.
-fl_status run(int dt, bool dual, const W4Params& p, const host::LaunchContext& ctx, cudaStream_t stream) {
+// Few rows: the weight-streaming kernel, which applies the norm itself.
+constexpr int kFewRows = 8;
+constexpr int kMaxRows = 65535 * 128;  // token tiles of one grid
+bool few_rows(int M) { return M <= kFewRows; }
+
+// One product whose arguments have been checked. `normed`: where the rows go
+// that the tile kernel reads, x * gamma / rms rounded to the dtype.
+fl_status run(int dt, bool dual, const W4Params& p, void* normed, const host::LaunchContext& ctx, cudaStream_t stream) {
+    if (!few_rows(p.M)) {
+        W4Params t = p;
+        if (p.gamma != nullptr) {
+            const fl_status st = host::launched(
+                launch_rms_norm(dt, p.x, p.gamma, normed, p.M, p.K, p.eps, ctx.pdl, ctx.sms, stream), "RMSNorm kernel");
+            if (st != FL_OK) return st;
+            t.x = static_cast<const uint16_t*>(normed);
+        }
+        return w4_tile(dt, dual, t, ctx, stream);
+    }
     const long long warps = (p.M + kSimpleRows - 1) / kSimpleRows * (long long)p.N;
     const dim3 grid((unsigned)((warps + 7) / 8));
     cudaError_t e;
@@ -243,8 +260,7 @@ fl_status fl_w4_quantize(const void* W, void* q, void* scales, int N, int K, int
 }
 
 size_t fl_w4_gemm_workspace_size(int M, int K, int norm) {
-    (void)M, (void)K, (void)norm;
-    return 0;
+    return norm && M > 0 && K > 0 && !fl::few_rows(M) ? (size_t)M * K * 2 : 0;
 }
 
 fl_status fl_w4_gemm(const void* x, const void* gamma, const fl_w4_weight* W, const void* bias, const void* residual,
@@ -255,6 +271,7 @@ fl_status fl_w4_gemm(const void* x, const void* gamma, const fl_w4_weight* W, co
     if ((int)act < 0 || (int)act > FL_ACT_RELU) return host::fail(FL_ERR_INVALID_ARG, "bad activation %d", (int)act);
     if (!(eps >= 0.0f) || eps > 1e30f) return host::fail(FL_ERR_INVALID_ARG, "eps must be finite and >= 0");
     if (M < 1) return host::fail(FL_ERR_INVALID_ARG, "fl_w4_gemm: sizes must be positive (M=%d)", M);
+    if (M > kMaxRows) return host::fail(FL_ERR_UNSUPPORTED, "fl_w4_gemm: more than %d rows", kMaxRows);
     fl_status st;
     if ((st = check_weight("fl_w4_gemm: W", W, N, K)) != FL_OK) return st;
     if ((st = host::check_ptr("x", x, true)) != FL_OK) return st;
@@ -284,13 +301,12 @@ fl_status fl_w4_gemm(const void* x, const void* gamma, const fl_w4_weight* W, co
     p.bias = static_cast<const uint16_t*>(bias), p.residual = static_cast<const uint16_t*>(residual);
     p.out = static_cast<uint16_t*>(out);
     p.M = M, p.N = N, p.K = K, p.eps = eps, p.act = act;
-    return run(dtype, false, p, ctx, s);
+    return run(dtype, false, p, workspace, ctx, s);
 }
 
 size_t fl_w4_swiglu_ffn_workspace_size(int M, int D, int F) {
-    (void)D;
-    if (M < 1 || F < 1) return 0;
-    return (size_t)M * F * 2;
+    if (M < 1 || F < 1 || D < 1) return 0;
+    return (size_t)M * F * 2 + fl_w4_gemm_workspace_size(M, D, 1);
 }
 
 fl_status fl_w4_swiglu_ffn(const void* x, const void* gamma, const fl_w4_weight* Wg, const fl_w4_weight* Wu,
@@ -300,6 +316,7 @@ fl_status fl_w4_swiglu_ffn(const void* x, const void* gamma, const fl_w4_weight*
     if (!host::valid_dtype(dtype)) return host::fail(FL_ERR_INVALID_ARG, "bad dtype %d", (int)dtype);
     if (!(eps >= 0.0f) || eps > 1e30f) return host::fail(FL_ERR_INVALID_ARG, "eps must be finite and >= 0");
     if (M < 1) return host::fail(FL_ERR_INVALID_ARG, "fl_w4_swiglu_ffn: sizes must be positive (M=%d)", M);
+    if (M > kMaxRows) return host::fail(FL_ERR_UNSUPPORTED, "fl_w4_swiglu_ffn: more than %d rows", kMaxRows);
     fl_status st;
     if ((st = check_weight("fl_w4_swiglu_ffn: Wg", Wg, F, D)) != FL_OK) return st;
     if ((st = check_weight("fl_w4_swiglu_ffn: Wu", Wu, F, D)) != FL_OK) return st;
@@ -325,6 +342,7 @@ fl_status fl_w4_swiglu_ffn(const void* x, const void* gamma, const fl_w4_weight*
     host::LaunchContext ctx;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if ((st = host::launch_context(s, &ctx)) != FL_OK) return st;
+    // (h in front, then the tile kernel's normalised rows)
     // h = silu(RMSNorm(x) Wg^T) * (RMSNorm(x) Wu^T)
     W4Params p = {};
     p.x = static_cast<const uint16_t*>(x), p.gamma = static_cast<const uint16_t*>(gamma);
@@ -332,7 +350,7 @@ fl_status fl_w4_swiglu_ffn(const void* x, const void* gamma, const fl_w4_weight*
     set_weight(p, 1, Wu);
     p.out = static_cast<uint16_t*>(workspace);
     p.M = M, p.N = F, p.K = D, p.eps = eps;
-    if ((st = run(dtype, true, p, ctx, s)) != FL_OK) return st;
+    if ((st = run(dtype, true, p, static_cast<uint8_t*>(workspace) + (size_t)M * F * 2, ctx, s)) != FL_OK) return st;
     // out = h Wd^T (+ bias_down) + x
     W4Params d = {};
     d.x = static_cast<const uint16_t*>(workspace);
@@ -340,7 +358,7 @@ fl_status fl_w4_swiglu_ffn(const void* x, const void* gamma, const fl_w4_weight*
     d.bias = static_cast<const uint16_t*>(bias_down), d.residual = static_cast<const uint16_t*>(x);
     d.out = static_cast<uint16_t*>(out);
     d.M = M, d.N = D, d.K = F;
-    return run(dtype, false, d, ctx, s);
+    return run(dtype, false, d, nullptr, ctx, s);
 }
 
 }  // extern "C"

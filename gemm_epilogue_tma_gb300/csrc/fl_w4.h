@@ -1,7 +1,11 @@
 // Declarations shared by the 4-bit product kernels.
 #pragma once
 
+#include <cuda_runtime.h>
+
 #include <cstdint>
+
+#include "fl_host.h"
 
 namespace fl {
 
@@ -18,5 +22,8 @@ struct W4Params {
     int M, N, K, group, act;
     float eps;
 };
+
+// Tile kernel (fl_w4_tile.cu): no prologue, any number of rows.
+fl_status w4_tile(int dt, bool dual, const W4Params& p, const host::LaunchContext& ctx, cudaStream_t stream);
 
 }  // namespace fl

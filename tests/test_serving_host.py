@@ -92,7 +92,7 @@ def test_w4_swiglu_refusals(L):
     assert call(u=weight(22, zeros=addr(26))) == INVALID     # zero points on one of the pair
     assert call(g=weight(20, zeros=addr(27)), u=weight(22, zeros=addr(26))) in PASSES
     assert call(d=weight(24, group=128), F=192) == ALIGN
-    assert call(ws=None) == WORKSPACE and call(size=5 * 256 * 2 - 1) == WORKSPACE
+    assert call(ws=None) == WORKSPACE and call(size=fl.w4_swiglu_ffn_workspace_size(5, 128, 256) - 1) == WORKSPACE
     assert call(ws=addr(20, 64)) == INVALID and call(ws=addr(4)) == INVALID and call(ws=addr(0)) == INVALID
     assert call(out=addr(0)) == INVALID and call(out=addr(23)) == INVALID
 
