@@ -154,10 +154,12 @@ def _ptr(t):
 
 
 def _stream(stream):
-    import torch
+    """The raw handle of `stream`, or of the current stream of the current device. (Read directly: building the
+    Stream object that torch.cuda.current_stream() returns takes as long as a launch.)"""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        from torch import _C
+        return _C._cuda_getCurrentRawStream(_C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _dtype_code(t) -> int:
@@ -390,10 +392,21 @@ def swiglu_ffn_noalloc(x, gamma, Wg, Wu, Wd, bias_down=None, out=None, eps=1e-6,
 # ---------------------------------------------------------------------------
 # serving operators: 4-bit weights, rotary positions, the quantised cache
 # ---------------------------------------------------------------------------
+# A decode step issues these calls back to back, so their host side is kept near
+# the launch's own time: one quick test per tensor, and the checks that say what
+# is wrong only where it fails.
+def _fits(t, dtype, here):
+    return t is None or (t.dtype is dtype and t.get_device() == here and t.is_contiguous())
+
+
+def _here():
+    from torch import _C
+    return _C._cuda_getDevice()
+
+
 def _check_call(**tensors):
     """Every tensor given is on the current CUDA device (the one whose stream the call is issued on)."""
-    import torch
-    here = torch.cuda.current_device()
+    here = _here()
     for name, t in tensors.items():
         if t is None:
             continue
@@ -404,7 +417,7 @@ def _check_call(**tensors):
 
 
 def _check_shape(name, t, shape):
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if t is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
@@ -417,11 +430,19 @@ def _check_kind(name, t, dtype, contiguous=True):
         raise ValueError(f"{name} must be contiguous (row-major)")
 
 
+def _explain(dtype, **tensors):
+    """Raises what is wrong with the tensors (of `dtype`, contiguous, on the current device)."""
+    _check_call(**tensors)
+    for name, t in tensors.items():
+        _check_kind(name, t, dtype)
+
+
 def _made(stream, *tensors):
     """Tensors a call made for itself and used on `stream`: not reused for another stream's work before it is done."""
     if stream is not None:
         for t in tensors:
-            t.record_stream(stream)
+            if t is not None:
+                t.record_stream(stream)
 
 
 def w4_quantize(W, group=128, q=None, scales=None, stream=None):
@@ -431,24 +452,24 @@ def w4_quantize(W, group=128, q=None, scales=None, stream=None):
     N, K = W.shape
     if group not in (32, 64, 128) or K % group:
         raise ValueError(f"group must be 32, 64 or 128 and divide K (group {group}, K {K})")
-    made = []
-    if q is None:
+    new_q, new_s = q is None, scales is None
+    if new_q:
         q = torch.empty((N, K // 2), dtype=torch.uint8, device=W.device)
-        made.append(q)
-    if scales is None:
+    if new_s:
         scales = torch.empty((N, K // group), dtype=W.dtype, device=W.device)
-        made.append(scales)
-    _check_call(W=W, q=q, scales=scales)
-    _check_tensors(W.dtype, W=W, scales=scales)
-    _check_kind("q", q, torch.uint8)
+    here = _here()
+    if not (_fits(W, W.dtype, here) and _fits(scales, W.dtype, here) and _fits(q, torch.uint8, here)):
+        _explain(W.dtype, W=W, scales=scales)
+        _explain(torch.uint8, q=q)
     _check_shape("q", q, (N, K // 2))
     _check_shape("scales", scales, (N, K // group))
-    _check(lib().fl_w4_quantize(_ptr(W), _ptr(q), _ptr(scales), N, K, group, _dtype_code(W), _stream(stream)))
-    _made(stream, *made)
+    _check(lib().fl_w4_quantize(W.data_ptr(), q.data_ptr(), scales.data_ptr(), N, K, group, _dtype_code(W),
+                                _stream(stream)))
+    _made(stream, q if new_q else None, scales if new_s else None)
     return q, scales
 
 
-def _w4_weight(name, dtype, K, q, scales, zeros=None):
+def _w4_weight(name, dtype, K, here, q, scales, zeros=None):
     """The C description of a 4-bit weight, and its row count."""
     import torch
     if q.dim() != 2 or q.shape[1] * 2 != K:
@@ -456,26 +477,31 @@ def _w4_weight(name, dtype, K, q, scales, zeros=None):
     N = q.shape[0]
     if scales.dim() != 2 or scales.shape[0] != N or scales.shape[1] < 1 or K % scales.shape[1]:
         raise ValueError(f"{name}: scales has shape {tuple(scales.shape)}, expected [{N}, K / group]")
-    _check_call(**{f"{name}: q": q, f"{name}: scales": scales, f"{name}: zeros": zeros})
-    _check_kind(f"{name}: q", q, torch.uint8)
-    _check_kind(f"{name}: scales", scales, dtype)
-    _check_kind(f"{name}: zeros", zeros, torch.uint8)
-    _check_shape(f"{name}: zeros", zeros, scales.shape)
-    return W4Weight(q=q.data_ptr(), scales=scales.data_ptr(), zeros=None if zeros is None else zeros.data_ptr(),
-                    group=K // scales.shape[1]), N
+    if not (_fits(q, torch.uint8, here) and _fits(scales, dtype, here) and _fits(zeros, torch.uint8, here)):
+        _explain(torch.uint8, **{f"{name}: q": q, f"{name}: zeros": zeros})
+        _explain(dtype, **{f"{name}: scales": scales})
+    if zeros is not None:
+        _check_shape(f"{name}: zeros", zeros, scales.shape)
+    return W4Weight(q.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(),
+                    K // scales.shape[1]), N
 
 
-def _workspace(workspace, need, device):
-    """(workspace or one made here, its bytes, whether it was made)."""
+def _workspace(workspace, need, like):
+    """(address or None, bytes, the tensor if it was made here)."""
     import torch
     if workspace is not None:
         _check_call(workspace=workspace)
         if not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous CUDA tensor")
-        return workspace, workspace.numel() * workspace.element_size(), False
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), None
     if need == 0:
-        return None, 0, False
-    return torch.empty(need, dtype=torch.uint8, device=device), need, True
+        return None, 0, None
+    made = torch.empty(need, dtype=torch.uint8, device=like.device)
+    return made.data_ptr(), need, made
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def w4_gemm_workspace_size(M: int, K: int, norm: bool) -> int:
@@ -490,23 +516,24 @@ def w4_gemm(x, q, scales, zeros=None, gamma=None, bias=None, residual=None, out=
     shared by calls or captured graphs that may overlap on the GPU."""
     import torch
     M, K = x.shape
-    W, N = _w4_weight("W", x.dtype, K, q, scales, zeros)
-    made = []
-    if out is None:
-        out = torch.empty((M, N), dtype=x.dtype, device=x.device)
-        made.append(out)
-    _check_call(x=x, gamma=gamma, bias=bias, residual=residual, out=out)
-    _check_tensors(x.dtype, x=x, gamma=gamma, bias=bias, residual=residual, out=out)
+    dt, here = x.dtype, _here()
+    W, N = _w4_weight("W", dt, K, here, q, scales, zeros)
+    new = out is None
+    if new:
+        out = torch.empty((M, N), dtype=dt, device=x.device)
+    if not (_fits(x, dt, here) and _fits(gamma, dt, here) and _fits(bias, dt, here) and _fits(residual, dt, here)
+            and _fits(out, dt, here)):
+        _explain(dt, x=x, gamma=gamma, bias=bias, residual=residual, out=out)
     _check_shape("gamma", gamma, (K,))
     _check_shape("bias", bias, (N,))
     _check_shape("residual", residual, (M, N))
     _check_shape("out", out, (M, N))
-    ws, size, own = _workspace(workspace, w4_gemm_workspace_size(M, K, gamma is not None), x.device)
-    if own:
-        made.append(ws)
-    _check(lib().fl_w4_gemm(_ptr(x), _ptr(gamma), ctypes.byref(W), _ptr(bias), _ptr(residual), _ptr(out), M, N, K,
-                            float(eps), ACTS[act], _ptr(ws), size, _dtype_code(x), _stream(stream)))
-    _made(stream, *made)
+    L = lib()
+    ws, size, own = _workspace(workspace, L.fl_w4_gemm_workspace_size(M, K, gamma is not None), x)
+    _check(L.fl_w4_gemm(x.data_ptr(), _addr(gamma), ctypes.byref(W), _addr(bias), _addr(residual), out.data_ptr(), M, N,
+                        K, eps, ACTS[act], ws, size, _dtype_code(x), _stream(stream)))
+    if stream is not None:
+        _made(stream, own, out if new else None)
     return out
 
 
@@ -518,47 +545,60 @@ def w4_swiglu_ffn(x, gamma, Wg, Wu, Wd, bias_down=None, out=None, eps=1e-6, work
     """swiglu_ffn on 4-bit weights, each a tuple (q, scales) or (q, scales, zeros)."""
     import torch
     M, D = x.shape
+    dt, here = x.dtype, _here()
     F = Wg[0].shape[0]
-    g, _ = _w4_weight("Wg", x.dtype, D, *Wg)
-    u, n = _w4_weight("Wu", x.dtype, D, *Wu)
-    d, m = _w4_weight("Wd", x.dtype, F, *Wd)
+    g, _ = _w4_weight("Wg", dt, D, here, *Wg)
+    u, n = _w4_weight("Wu", dt, D, here, *Wu)
+    d, m = _w4_weight("Wd", dt, F, here, *Wd)
     if n != F or m != D:
         raise ValueError(f"Wu has {n} rows, expected {F}; Wd has {m}, expected {D}")
-    made = []
-    if out is None:
-        out = torch.empty_like(x)
-        made.append(out)
-    _check_call(x=x, gamma=gamma, bias_down=bias_down, out=out)
-    _check_tensors(x.dtype, x=x, gamma=gamma, bias_down=bias_down, out=out)
+    new = out is None
+    if new:
+        out = torch.empty((M, D), dtype=dt, device=x.device)
+    if not (_fits(x, dt, here) and _fits(gamma, dt, here) and _fits(bias_down, dt, here) and _fits(out, dt, here)):
+        _explain(dt, x=x, gamma=gamma, bias_down=bias_down, out=out)
     _check_shape("gamma", gamma, (D,))
     _check_shape("bias_down", bias_down, (D,))
     _check_shape("out", out, (M, D))
-    ws, size, own = _workspace(workspace, w4_swiglu_ffn_workspace_size(M, D, F), x.device)
-    if own:
-        made.append(ws)
-    _check(lib().fl_w4_swiglu_ffn(_ptr(x), _ptr(gamma), ctypes.byref(g), ctypes.byref(u), ctypes.byref(d),
-                                  _ptr(bias_down), _ptr(out), M, D, F, float(eps), _ptr(ws), size, _dtype_code(x),
-                                  _stream(stream)))
-    _made(stream, *made)
+    L = lib()
+    ws, size, own = _workspace(workspace, L.fl_w4_swiglu_ffn_workspace_size(M, D, F), x)
+    _check(L.fl_w4_swiglu_ffn(x.data_ptr(), gamma.data_ptr(), ctypes.byref(g), ctypes.byref(u), ctypes.byref(d),
+                              _addr(bias_down), out.data_ptr(), M, D, F, eps, ws, size, _dtype_code(x),
+                              _stream(stream)))
+    if stream is not None:
+        _made(stream, own, out if new else None)
     return out
 
 
-def _heads(name, t, dtype, rows=None):
-    """Checks a [rows, heads, head_dim] view: dtype, contiguous channels."""
+def _heads(name, t, dtype, here):
+    """Checks a [rows, heads, head_dim] view: dtype, device, contiguous channels. Returns its shape and its row and
+    head strides; of an axis of one, the stride it would have if dense."""
     if t.dim() != 3:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [rows, heads, head_dim]")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    if t.dtype is not dtype or t.get_device() != here:
+        _check_call(**{name: t})
+        _check_kind(name, t, dtype, contiguous=False)
+    shape = t.shape
+    rows, heads, dim = shape
+    row, head, unit = t.stride()
+    if unit != 1 and dim > 1:
         raise ValueError(f"{name}: the channels of a head must be contiguous")
-    if rows is not None and t.shape[0] != rows:
-        raise ValueError(f"{name} has {t.shape[0]} rows, expected {rows}")
+    if heads == 1:
+        head = dim
+    return shape, (row if rows != 1 else heads * head), head
 
 
-def _strides(t):
-    """Row and head stride of a [rows, heads, head_dim] view; of an axis of one, the one it would have if dense."""
-    head = t.stride(1) if t.shape[1] > 1 else t.shape[2]
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * head, head
+def _rope_axes(pairs, axes, sections):
+    """The axis of each pair, as the bytes fl_rope takes (None: axis 0 for all)."""
+    if axes > 4:
+        raise ValueError(f"1..4 axes, got {axes}")
+    if sections is None:
+        if axes != 1:
+            raise ValueError(f"positions has {axes} axes: sections must say which pairs follow which")
+        return None
+    if len(sections) != axes or sum(sections) != pairs or min(sections) < 0:
+        raise ValueError(f"sections {tuple(sections)} must give the {pairs} pairs to the {axes} axes")
+    return b"".join([bytes((a,)) * n for a, n in enumerate(sections)]) if axes > 1 else None
 
 
 def rope(q, k, positions, inv_freq, sections=None, interleaved=False, inverse=False, out_q=None, out_k=None,
@@ -571,98 +611,96 @@ def rope(q, k, positions, inv_freq, sections=None, interleaved=False, inverse=Fa
     the input. q, k and the outputs may be strided views with contiguous channels (column ranges of a stacked
     projection's output); an output may be its input itself."""
     import torch
-    dt = q.dtype
-    _heads("q", q, dt)
-    rows, heads_q, D = q.shape
-    pos = positions if positions.dim() == 2 else positions.reshape(1, -1)
-    axes = pos.shape[0]
-    _check_shape("positions", pos, (axes, rows))
-    _check_kind("positions", pos, torch.int32, contiguous=False)
-    if rows > 1 and pos.stride(1) != 1:
+    dt, here = q.dtype, _here()
+    shape, q_row, q_head = _heads("q", q, dt, here)
+    rows, heads_q, D = shape
+    if positions.dim() == 2:
+        axes, stride = positions.shape[0], positions.stride(0)
+    else:
+        axes, stride = 1, rows
+    if not (positions.dtype is torch.int32 and positions.get_device() == here and positions.shape[-1] == rows
+            and positions.dim() <= 2 and (rows <= 1 or positions.stride(-1) == 1)):
+        _check_call(positions=positions)
+        _check_kind("positions", positions, torch.int32, contiguous=False)
+        _check_shape("positions", positions, (axes, rows) if positions.dim() == 2 else (rows,))
         raise ValueError("positions must be contiguous along the rows")
-    _check_kind("inv_freq", inv_freq, torch.float32)
-    if inv_freq.dim() != 1:
+    if not _fits(inv_freq, torch.float32, here) or inv_freq.dim() != 1:
+        _explain(torch.float32, inv_freq=inv_freq)
         raise ValueError(f"inv_freq has shape {tuple(inv_freq.shape)}, expected [R / 2]")
     pairs = inv_freq.shape[0]
-    if sections is None:
-        if axes != 1:
-            raise ValueError(f"positions has {axes} axes: sections must say which pairs follow which")
-        sections = (pairs,)
-    if len(sections) != axes or sum(sections) != pairs or min(sections) < 0:
-        raise ValueError(f"sections {tuple(sections)} must give the {pairs} pairs to the {axes} axes")
-    if axes > 4:
-        raise ValueError(f"1..4 axes, got {axes}")
-    made = []
-    if out_q is None:
-        out_q = torch.empty((rows, heads_q, D), dtype=dt, device=q.device)
-        made.append(out_q)
-    if k is None and out_k is not None:
-        raise ValueError("out_k without k")
-    if k is not None and out_k is None:
-        out_k = torch.empty(tuple(k.shape), dtype=dt, device=k.device)
-        made.append(out_k)
-    _check_call(q=q, k=k, positions=pos, inv_freq=inv_freq, out_q=out_q, out_k=out_k)
-    _heads("out_q", out_q, dt)
-    _check_shape("out_q", out_q, q.shape)
-    if k is not None:
-        _heads("k", k, dt, rows)
-        _heads("out_k", out_k, dt)
-        _check_shape("k", k, (rows, k.shape[1], D))
-        _check_shape("out_k", out_k, k.shape)
-    desc = RopeDesc(dtype=_dtype_code(q), rows=rows, heads_q=heads_q, heads_k=0 if k is None else k.shape[1],
-                    head_dim=D, rotary_dim=2 * pairs, n_axes=axes, interleaved=int(bool(interleaved)),
-                    inverse=int(bool(inverse)), axis_of=b"".join(bytes([a]) * n for a, n in enumerate(sections)),
-                    positions=pos.data_ptr(), positions_stride=pos.stride(0) if axes > 1 else rows,
-                    inv_freq=inv_freq.data_ptr(), q=q.data_ptr(), q_out=out_q.data_ptr())
-    desc.q_row, desc.q_head = _strides(q)
-    desc.q_out_row, desc.q_out_head = _strides(out_q)
-    if k is not None:
-        desc.k, desc.k_out = k.data_ptr(), out_k.data_ptr()
-        desc.k_row, desc.k_head = _strides(k)
-        desc.k_out_row, desc.k_out_head = _strides(out_k)
+    axis_of = _rope_axes(pairs, axes, sections)
+    new_q, new_k = out_q is None, k is not None and out_k is None
+    if new_q:
+        out_q = torch.empty(shape, dtype=dt, device=q.device)
+        o_row, o_head = heads_q * D, D
+    else:
+        o_shape, o_row, o_head = _heads("out_q", out_q, dt, here)
+        _check_shape("out_q", out_q, shape)
+    heads_k = k_addr = ko_addr = k_row = k_head = ko_row = ko_head = 0
+    if k is None:
+        if out_k is not None:
+            raise ValueError("out_k without k")
+    else:
+        k_shape, k_row, k_head = _heads("k", k, dt, here)
+        heads_k = k_shape[1]
+        _check_shape("k", k, (rows, heads_k, D))
+        if new_k:
+            out_k = torch.empty(k_shape, dtype=dt, device=k.device)
+            ko_row, ko_head = heads_k * D, D
+        else:
+            o_shape, ko_row, ko_head = _heads("out_k", out_k, dt, here)
+            _check_shape("out_k", out_k, k_shape)
+        k_addr, ko_addr = k.data_ptr(), out_k.data_ptr()
+    desc = RopeDesc(_dtype_code(q), rows, heads_q, heads_k, D, 2 * pairs, axes, bool(interleaved), bool(inverse), axis_of,
+                    positions.data_ptr(), stride, inv_freq.data_ptr(), q.data_ptr(), k_addr, out_q.data_ptr(), ko_addr,
+                    q_row, q_head, k_row, k_head, o_row, o_head, ko_row, ko_head)
     _check(lib().fl_rope(ctypes.byref(desc), _stream(stream)))
-    _made(stream, *made)
+    if stream is not None:
+        _made(stream, out_q if new_q else None, out_k if new_k else None)
     return out_q, out_k
 
 
 def _kv_desc(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_rows, start):
     import torch
-    formats = {torch.int8: 0, torch.float8_e4m3fn: 1}
-    if k_cache.dtype not in formats:
-        raise TypeError(f"k_cache has dtype {k_cache.dtype}, expected int8 or float8_e4m3fn")
-    if k_cache.dim() != 4:
-        raise ValueError(f"k_cache has shape {tuple(k_cache.shape)}, expected [pages, page_size, heads, head_dim]")
-    pages, size, heads, dim = k_cache.shape
-    _check_call(k=k, v=v, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, page_table=page_table,
-                cu_rows=cu_rows, start=start)
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _check_kind(name, t, k_cache.dtype)
-        _check_shape(name, t, k_cache.shape)
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _check_kind(name, t, torch.float32)
-        _check_shape(name, t, (pages, size, heads))
-    rows = k.shape[0]
-    for name, t in (("k", k), ("v", v)):
-        _heads(name, t, k.dtype, rows)
-        _check_shape(name, t, (rows, heads, dim))
+    here = _here()
+    kind = k_cache.dtype
+    if kind is not torch.int8 and kind is not torch.float8_e4m3fn:
+        raise TypeError(f"k_cache has dtype {kind}, expected int8 or float8_e4m3fn")
+    shape = k_cache.shape
+    if len(shape) != 4:
+        raise ValueError(f"k_cache has shape {tuple(shape)}, expected [pages, page_size, heads, head_dim]")
+    pages, size, heads, dim = shape
+    f32, i32 = torch.float32, torch.int32
+    if not (_fits(k_cache, kind, here) and _fits(v_cache, kind, here) and _fits(k_scale, f32, here)
+            and _fits(v_scale, f32, here) and _fits(cu_rows, i32, here) and _fits(start, i32, here)):
+        _explain(kind, k_cache=k_cache, v_cache=v_cache)
+        _explain(f32, k_scale=k_scale, v_scale=v_scale)
+        _explain(i32, cu_rows=cu_rows, start=start)
+    if v_cache.shape != shape or k_scale.shape != shape[:3] or v_scale.shape != shape[:3]:
+        _check_shape("v_cache", v_cache, shape)
+        _check_shape("k_scale", k_scale, shape[:3])
+        _check_shape("v_scale", v_scale, shape[:3])
+    dt = k.dtype
+    k_shape, k_row, k_head = _heads("k", k, dt, here)
+    v_shape, v_row, v_head = _heads("v", v, dt, here)
+    rows = k_shape[0]
+    if k_shape != (rows, heads, dim) or v_shape != k_shape:
+        _check_shape("k", k, (rows, heads, dim))
+        _check_shape("v", v, (rows, heads, dim))
     if page_table.dim() != 2:
         raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected [sequences, pages]")
     seqs, per = page_table.shape
-    _check_kind("page_table", page_table, torch.int32, contiguous=False)
-    if per > 1 and page_table.stride(1) != 1:
+    stride, unit = page_table.stride()
+    if page_table.dtype is not i32 or page_table.get_device() != here or (unit != 1 and per > 1):
+        _check_call(page_table=page_table)
+        _check_kind("page_table", page_table, i32, contiguous=False)
         raise ValueError("page_table must be contiguous along a sequence's pages")
-    _check_kind("cu_rows", cu_rows, torch.int32)
     _check_shape("cu_rows", cu_rows, (seqs + 1,))
-    _check_kind("start", start, torch.int32)
     _check_shape("start", start, (seqs,))
-    opt = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    (k_row, k_head), (v_row, v_head) = _strides(k), _strides(v)
-    return KvDesc(dtype=_dtype_code(k), format=formats[k_cache.dtype], rows=rows, heads=heads, head_dim=dim,
-                  page_size=size, n_pages=pages, n_seqs=seqs, table_pages=per,
-                  table_stride=page_table.stride(0) if seqs > 1 else per, page_table=page_table.data_ptr(),
-                  cu_rows=opt(cu_rows), start=opt(start), k=k.data_ptr(), v=v.data_ptr(), k_row=k_row,
-                  k_head=k_head, v_row=v_row, v_head=v_head, k_cache=k_cache.data_ptr(),
-                  v_cache=v_cache.data_ptr(), k_scale=k_scale.data_ptr(), v_scale=v_scale.data_ptr())
+    return KvDesc(_dtype_code(k), 0 if kind is torch.int8 else 1, rows, heads, dim, size, pages, seqs, per,
+                  stride if seqs > 1 else per, page_table.data_ptr(), _addr(cu_rows), _addr(start), k.data_ptr(),
+                  v.data_ptr(), k_row, k_head, v_row, v_head, k_cache.data_ptr(), v_cache.data_ptr(),
+                  k_scale.data_ptr(), v_scale.data_ptr())
 
 
 def kv_write(k, v, k_cache, v_cache, k_scale, v_scale, page_table, start, cu_rows=None, stream=None):
