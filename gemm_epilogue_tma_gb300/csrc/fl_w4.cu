@@ -192,7 +192,7 @@ void set_weight(W4Params& p, int j, const fl_w4_weight* w) {
 
 // Few rows: the weight-streaming kernel, which applies the norm itself.
 constexpr int kFewRows = 8;
-constexpr int kMaxRows = 65535 * 128;  // token tiles of one grid
+constexpr int kMaxRows = 65000 * 256;  // token tiles of one grid
 bool few_rows(int M) { return M <= kFewRows; }
 
 // One product whose arguments have been checked. `normed`: where the rows go

@@ -1,25 +1,27 @@
 // 4-bit products for nine rows and more, on the tensor cores.
 //
-// The weight is the M operand: a tile takes 128 rows of each of two weight
-// blocks (rows n .. n + 255 of one weight, or, for the SwiGLU pair, rows
-// n .. n + 127 of Wg and of Wu) against up to 128 tokens, so that the 4-bit
-// codes are expanded where the MMA reads them: in tensor memory. Each K step
-// of 64 a dequantising thread owns one weight row: it reads 32 bytes of codes
-// from shared memory, forms scale * (code - zero) in the dtype (one rounding)
-// and writes its row of the A operand with tcgen05.st; the tokens are the B
-// operand, staged by TMA. 16-bit weights exist nowhere else.
+// The weight is the M operand: a tile takes 128 weight rows (or, for the
+// SwiGLU pair, 64 rows of Wg and the same rows of Wu) against up to 256 tokens,
+// so that the 4-bit codes are expanded where the MMA reads them: in tensor
+// memory. Each K step of 64 a dequantising thread owns one weight row: it reads
+// 32 bytes of codes from shared memory, forms scale * (code - zero) in the
+// dtype (one rounding) and writes its row of the A operand with tcgen05.st; the
+// tokens are the B operand, staged by TMA. 16-bit weights exist nowhere else.
 //
-// Per K step and SM the two MMAs (128 x BT x 64 each) read 2 * BT * 128 bytes
-// of shared memory and TMA writes BT * 128 bytes and 8 KB of codes. With few
-// tokens the tile is a weight stream: the K range is then split over a cluster
-// of up to 8 CTAs, whose fp32 partials are added through distributed shared
-// memory in rank order.
+// What bounds it: with many tokens the shared-memory traffic of the B operand
+// (per K step 256 * 128 bytes written by TMA and read by the MMA, against 590
+// cycles of MMA); with few the weight stream, for which the K range is split over a
+// cluster of up to 8 CTAs whose fp32 partials are added through distributed
+// shared memory in rank order. A tile of two blocks of 128 rows by 128 tokens
+// moved fewer bytes per MMA but expanded every code for half as many tokens, and the
+// expansion (about 440 instructions a warp and step) set its pace: 237 us at
+// 4096^3.
 //
 // Roles: warp 0 TMA producer (codes in stages of 256 k, tokens in stages of
 // 64 k), warp 1 tensor memory and MMA issue, warps 2 and 3 load the scales and
 // zero points of 1024 k at a time into shared memory (transposed: one row per
-// thread there), warps 4-7 and 8-11 dequantise block 0 and block 1 and, when
-// the MMAs are done, apply the epilogue.
+// thread there), warps 4-19 dequantise, four to a K step, and when the MMAs are
+// done apply the epilogue.
 //
 // Every mbarrier wait is bounded as in the other kernels.
 #include <atomic>
@@ -32,36 +34,38 @@ namespace fl {
 
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kRows = 128;       // weight rows of one block (TMEM lanes)
-constexpr int kTok = 128;        // tokens of a tile at most
+constexpr int kThreads = 640;
+constexpr int kRows = 128;       // weight rows of a tile (TMEM lanes)
+constexpr int kTok = 256;        // tokens of a tile at most
 constexpr int kStep = 64;        // k per B stage and A slot
-constexpr int kWk = 256;         // k per code stage
-constexpr int kSk = 1024;        // k per scale stage
-constexpr int kBStages = 6, kWStages = 2, kSStages = 2, kSlots = 4;
-constexpr int kBBytes = kTok * kStep * 2;           // 16 KB
-constexpr int kWBytes = kRows * kWk / 2;            // 16 KB, one block
+constexpr int kGroups = 4;       // dequantising warpgroups: K step kb goes to kb % 4
+constexpr int kWk = kGroups * kStep;  // k per code stage: one step of each warpgroup
+constexpr int kSIter = 4;        // code stages per scale stage
+constexpr int kSk = kSIter * kWk;
+constexpr int kBStages = 5, kWStages = 2, kSStages = 2, kSlots = kWStages * kGroups;
+constexpr int kBBytes = kTok * kStep * 2;           // 32 KB
+constexpr int kWBytes = kRows * kWk / 2;            // 16 KB
 constexpr int kSPitch = 130;                        // 16-bit scales of one group: 128 rows, padded
 constexpr int kZPitch = 132;                        // zero-point bytes of one group
 constexpr int kSGroups = kSk / 32;
-constexpr int kSBytes = kSGroups * kSPitch * 2;     // scales of one block and stage
+constexpr int kSBytes = kSGroups * kSPitch * 2;
 constexpr int kZBytes = kSGroups * kZPitch;
 
 constexpr int kOffW = kBStages * kBBytes;
-constexpr int kOffS = kOffW + kWStages * 2 * kWBytes;
-constexpr int kOffZ = kOffS + kSStages * 2 * kSBytes;
-constexpr int kOffBar = (kOffZ + kSStages * 2 * kZBytes + 7) / 8 * 8;
+constexpr int kOffS = kOffW + kWStages * kWBytes;
+constexpr int kOffZ = kOffS + kSStages * kSBytes;
+constexpr int kOffBar = (kOffZ + kSStages * kZBytes + 7) / 8 * 8;
 constexpr int kBars = 2 * kBStages + 2 * kWStages + 2 * kSlots + 2 * kSStages + 2;
 constexpr int kOffSlot = kOffBar + kBars * 8;
 constexpr int kSmem = kOffSlot + 16 + 1024;         // + alignment slack
 static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
-static_assert(kRows * 2 * kTok * 4 <= kOffS, "the partial sums fit in the rings");
+static_assert(kRows * kTok * 4 <= kOffS, "the partial sums fit in the rings");
 
-constexpr int kACol = 256;  // first tensor-memory column of the A slots (the accumulators: 0 and 128)
+constexpr int kACol = 256;  // first tensor-memory column of the A slots (the accumulator: 0 .. 255)
 
 struct TileParams {
     CUtensorMap tm_x;     // x [M, K], box {64, BT}
-    CUtensorMap tm_q[2];  // codes [N, K / 2] bytes, box {128, 128}
+    CUtensorMap tm_q[2];  // codes [N, K / 2] bytes, box {128, 128} (pair: {128, 64} each)
     W4Params w;
     int bt, splits, steps_per_split, steps;  // K steps of 64
     int* status;
@@ -129,9 +133,12 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tile = blockIdx.x / p.splits, rank = blockIdx.x % p.splits;
     const int m0 = blockIdx.y * p.bt;
-    // first row of each weight block
-    const int n0 = tile * (DUAL ? kRows : 2 * kRows);
+    const int n0 = tile * (DUAL ? kRows / 2 : kRows);  // first weight row (of each weight of the pair)
     const int k0 = rank * p.steps_per_split, k1 = min(p.steps, k0 + p.steps_per_split), nk = k1 - k0;
+    // weight and row of TMEM lane r: for the pair, each warp's lanes 0-15 are
+    // rows of Wg and 16-31 the same rows of Wu
+    auto weight_of = [&](int r) { return DUAL ? (r >> 4) & 1 : 0; };
+    auto row_of = [&](int r) { return n0 + (DUAL ? (r >> 5) * 16 + (r & 15) : r); };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kBStages; ++s) {
@@ -140,15 +147,15 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
         }
         for (int s = 0; s < kWStages; ++s) {
             mbar_init(wfull(s), 1);
-            mbar_init(wempty(s), 8);
+            mbar_init(wempty(s), 4 * kGroups);
         }
         for (int s = 0; s < kSlots; ++s) {
-            mbar_init(afull(s), 8);
+            mbar_init(afull(s), 4);
             mbar_init(aempty(s), 1);
         }
         for (int s = 0; s < kSStages; ++s) {
             mbar_init(sfull(s), 2);
-            mbar_init(sempty(s), 8);
+            mbar_init(sempty(s), 4 * kGroups);
         }
         mbar_init(dfull, 1);
         mbar_init(drain, 1);
@@ -169,28 +176,27 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kOffSlot);
     // the first codes towards L2 (the point of coherence) while the previous kernel finishes
     if (warp == 0 && lane == 0) {
-        for (int i = 0; i < kWStages && i * (kWk / kStep) < nk; ++i) {
-            tma_prefetch_2d(&p.tm_q[0], k0 * (kStep / 2) + i * (kWk / 2), n0);
-            tma_prefetch_2d(&p.tm_q[DUAL], k0 * (kStep / 2) + i * (kWk / 2), DUAL ? n0 : n0 + kRows);
-        }
+        for (int i = 0; i < kWStages && i * kGroups < nk; ++i)
+            for (int j = 0; j <= (DUAL ? 1 : 0); ++j)
+                tma_prefetch_2d(&p.tm_q[j], k0 * (kStep / 2) + i * (kWk / 2), n0);
     }
     griddep_wait();
     if (threadIdx.x == 0) griddep_launch_dependents();
 
-    bool ready = false;  // epilogue warps: the accumulators are complete
+    bool ready = false;  // epilogue warps: the accumulator is complete
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         if (lane == 0) {
             int bi = 0, wi = 0;  // loads issued
             for (int kb = 0; kb < nk; ++kb) {
-                if (kb % (kWk / kStep) == 0) {
+                if (kb % kGroups == 0) {
                     const int s = wi % kWStages;
                     if (!wait_bar(wempty(s), (uint32_t)((wi / kWStages) & 1) ^ 1u, p.status, p.timeout_ns, 20)) break;
-                    mbar_arrive_expect_tx(wfull(s), 2 * kWBytes);
-                    const uint32_t dst = sbase + kOffW + s * 2 * kWBytes;
+                    mbar_arrive_expect_tx(wfull(s), kWBytes);
+                    const uint32_t dst = sbase + kOffW + s * kWBytes;
                     const int x = (k0 + kb) * (kStep / 2);
                     tma_load_2d(dst, &p.tm_q[0], wfull(s), x, n0);
-                    tma_load_2d(dst + kWBytes, &p.tm_q[DUAL], wfull(s), x, DUAL ? n0 : n0 + kRows);
+                    if (DUAL) tma_load_2d(dst + kWBytes / 2, &p.tm_q[1], wfull(s), x, n0);
                     ++wi;
                 }
                 const int s = bi % kBStages;
@@ -218,11 +224,8 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
                 tc_fence_after();
                 const uint64_t db = sw128_kmajor_desc(sbase + s * kBBytes);
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int kk = 0; kk < kStep / 16; ++kk)
-                        umma_f16_ts(tmem + 128u * j, tmem + kACol + 64u * a + 32u * j + 8u * kk, db + 2 * kk, idesc,
-                                    (kb | kk) != 0);
+                for (int kk = 0; kk < kStep / 16; ++kk)
+                    umma_f16_ts(tmem, tmem + kACol + 32u * a + 8u * kk, db + 2 * kk, idesc, (kb | kk) != 0);
                 umma_commit(bempty(s));
                 umma_commit(aempty(a));
             }
@@ -232,34 +235,33 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
             wait_bar_drain(drain, 0, 20000000ull);
         }
     } else if (warp < 4) {
-        // ------------------------------------------------------------ scales and zero points of block j
-        const int j = warp - 2, row0 = DUAL ? n0 : n0 + kRows * j;
-        const uint16_t* sc = w.scales[DUAL ? j : 0];
-        const uint8_t* zp = w.zeros[DUAL ? j : 0];
+        // ------------------------------------------------------------ scales and zero points, 64 rows each
         const int per_row = w.K / w.group, ng = kSk / w.group;  // groups of a row; of a stage (8, 16 or 32)
         const int sh = 31 - __clz(ng);
-        const int stages = (nk * kStep + kSk - 1) / kSk;
+        const int g_end = min(per_row, (k1 * kStep + w.group - 1) / w.group);
+        const int stages = (nk * kStep + kSk - 1) / kSk, half = kRows / 2 << sh;
         for (int i = 0; i < stages; ++i) {
             const int s = i % kSStages;
             if (!wait_bar(sempty(s), (uint32_t)((i / kSStages) & 1) ^ 1u, p.status, p.timeout_ns, 24)) break;
             const int g0 = (k0 * kStep + i * kSk) / w.group;
-            uint16_t* ds = reinterpret_cast<uint16_t*>(smem + kOffS + (s * 2 + j) * kSBytes);
-            uint8_t* dz = smem + kOffZ + (s * 2 + j) * kZBytes;
-            constexpr int U = 16;
-            for (int b = lane; b < kRows << sh; b += 32 * U) {
+            uint16_t* ds = reinterpret_cast<uint16_t*>(smem + kOffS + s * kSBytes);
+            uint8_t* dz = smem + kOffZ + s * kZBytes;
+            constexpr int U = 16;  // loads in flight per lane
+            for (int b = (warp - 2) * half + lane; b < (warp - 1) * half; b += 32 * U) {
                 uint16_t v[U];
                 uint8_t z[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int e = b + 32 * u, r = e >> sh, g = g0 + (e & (ng - 1));
-                    const bool in = r < kRows && row0 + r < w.N && g < per_row;
-                    v[u] = in ? __ldg(sc + (size_t)(row0 + r) * per_row + g) : (uint16_t)0;
-                    z[u] = in && zp != nullptr ? (uint8_t)(__ldg(zp + (size_t)(row0 + r) * per_row + g) & 15) : (uint8_t)8;
+                    const int e = b + 32 * u, r = e >> sh, g = g0 + (e & (ng - 1)), n = row_of(r);
+                    const bool in = e < (warp - 1) * half && n < w.N && g < g_end;
+                    const int j = weight_of(r);
+                    v[u] = in ? __ldg(w.scales[j] + (size_t)n * per_row + g) : (uint16_t)0;
+                    z[u] = in && w.zeros[j] != nullptr ? (uint8_t)(__ldg(w.zeros[j] + (size_t)n * per_row + g) & 15) : (uint8_t)8;
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const int e = b + 32 * u, r = e >> sh, g = e & (ng - 1);
-                    if (r < kRows) {
+                    if (e < (warp - 1) * half) {
                         ds[g * kSPitch + r] = v[u];
                         dz[g * kZPitch + r] = z[u];
                     }
@@ -269,27 +271,28 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
             if (lane == 0) mbar_arrive(sfull(s));
         }
     } else {
-        // ------------------------------------------------------------ dequantise block j, one row per thread
-        const int j = (warp - 4) >> 2, row = (threadIdx.x - 128) & 127;
+        // ------------------------------------------------------------ dequantise, one row per thread
+        const int grp = (warp - 4) >> 2, r = (threadIdx.x - 128) & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const int gsh = 31 - __clz(w.group);
+        // this row's codes of the warpgroup's K step in a code stage
+        const int srow = DUAL ? weight_of(r) * (kRows / 2) + (r >> 5) * 16 + (r & 15) : r;
+        const uint32_t src0 = sbase + kOffW + srow * 128 + (((2 * grp) ^ (srow & 7)) << 4);
+        const uint32_t src1 = sbase + kOffW + srow * 128 + (((2 * grp + 1) ^ (srow & 7)) << 4);
         bool ok = true;
-        for (int kb = 0; kb < nk; ++kb) {
-            const int wi = kb / (kWk / kStep), ws = wi % kWStages, q = kb % (kWk / kStep);
-            const int si = kb / (kSk / kStep), ss = si % kSStages;
-            if (q == 0) ok = wait_bar(wfull(ws), (uint32_t)((wi / kWStages) & 1), p.status, p.timeout_ns, 25);
-            if (ok && kb % (kSk / kStep) == 0)
-                ok = wait_bar(sfull(ss), (uint32_t)((si / kSStages) & 1), p.status, p.timeout_ns, 26);
+        for (int it = 0, kb = grp; kb < nk; ++it, kb += kGroups) {
+            const int ws = it % kWStages, ss = it / kSIter % kSStages;
+            ok = wait_bar(wfull(ws), (uint32_t)((it / kWStages) & 1), p.status, p.timeout_ns, 25);
+            if (ok && it % kSIter == 0)
+                ok = wait_bar(sfull(ss), (uint32_t)((it / (kSIter * kSStages)) & 1), p.status, p.timeout_ns, 26);
             if (!ok) break;
-            const uint32_t src = sbase + kOffW + (ws * 2 + j) * kWBytes + row * 128;
-            const uint4 c0 = ld_shared_v4(src + (((2 * q) ^ (row & 7)) << 4));
-            const uint4 c1 = ld_shared_v4(src + (((2 * q + 1) ^ (row & 7)) << 4));
-            const uint16_t* ds = reinterpret_cast<const uint16_t*>(smem + kOffS + (ss * 2 + j) * kSBytes);
-            const uint8_t* dz = smem + kOffZ + (ss * 2 + j) * kZBytes;
-            const int kin = (kb % (kSk / kStep)) * kStep;
+            const uint4 c0 = ld_shared_v4(src0 + ws * kWBytes), c1 = ld_shared_v4(src1 + ws * kWBytes);
+            const uint16_t* ds = reinterpret_cast<const uint16_t*>(smem + kOffS + ss * kSBytes);
+            const uint8_t* dz = smem + kOffZ + ss * kZBytes;
+            const int kin = (it % kSIter) * kWk + grp * kStep;
             const int ga = kin >> gsh, gb = (kin + 32) >> gsh;
-            const uint32_t sa = (uint32_t)ds[ga * kSPitch + row] * 0x10001u, sb = (uint32_t)ds[gb * kSPitch + row] * 0x10001u;
-            const uint32_t za = zero_const<DT>(dz[ga * kZPitch + row]), zb = zero_const<DT>(dz[gb * kZPitch + row]);
+            const uint32_t sa = (uint32_t)ds[ga * kSPitch + r] * 0x10001u, sb = (uint32_t)ds[gb * kSPitch + r] * 0x10001u;
+            const uint32_t za = zero_const<DT>(dz[ga * kZPitch + r]), zb = zero_const<DT>(dz[gb * kZPitch + r]);
             uint32_t o[32];
             dequant8<DT>(c0.x, sa, za, o);
             dequant8<DT>(c0.y, sa, za, o + 4);
@@ -301,15 +304,14 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
             dequant8<DT>(c1.w, sb, zb, o + 28);
             __syncwarp();
             if (lane == 0) {
-                // the last reads of a stage of codes and of scales
-                if (q == kWk / kStep - 1 || kb == nk - 1) mbar_arrive(wempty(ws));
-                if (kb % (kSk / kStep) == kSk / kStep - 1 || kb == nk - 1) mbar_arrive(sempty(ss));
+                mbar_arrive(wempty(ws));
+                if (it % kSIter == kSIter - 1) mbar_arrive(sempty(ss));
             }
-            const int a = kb % kSlots;
-            ok = wait_bar(aempty(a), (uint32_t)((kb / kSlots) & 1) ^ 1u, p.status, p.timeout_ns, 27);
+            const int a = ws * kGroups + grp;
+            ok = wait_bar(aempty(a), (uint32_t)((it / kWStages) & 1) ^ 1u, p.status, p.timeout_ns, 27);
             if (!ok) break;
             tc_fence_after();
-            tmem_st_32x32b_x32(tmem + lanes + kACol + 64u * a + 32u * j, o);
+            tmem_st_32x32b_x32(tmem + lanes + kACol + 32u * a, o);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -320,91 +322,92 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
     }
 
     // ---------------------------------------------------------------- epilogue
-    const int jb = (warp - 4) >> 2;  // weight block of an epilogue warp
-    const int lrow = (threadIdx.x - 128) & 127;
-    const int n = n0 + lrow + (DUAL ? 0 : kRows * jb);
+    const int grp = (warp - 4) >> 2, r = (threadIdx.x - 128) & 127;
     const uint32_t dcol = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    // out[m][n] of two tokens: lanes n and n + 1 exchange, so that the even
-    // lane stores both rows' values of token m, the odd lane those of m + 1
+    const int n = row_of(r), nn = n & ~1;
     const float bias = warp >= 4 && !DUAL && w.bias != nullptr && n < w.N ? Ops::unpack(w.bias[n]).x : 0.f;
-    auto store2 = [&](int m, float v0, float v1) {
-        if constexpr (!DUAL) {
-            v0 = act_apply(w.act, v0 + bias);
-            v1 = act_apply(w.act, v1 + bias);
-        }
-        const float give = (lane & 1) ? v0 : v1, got = __shfl_xor_sync(0xffffffffu, give, 1);
-        float a = (lane & 1) ? got : v0, b = (lane & 1) ? v1 : got;
-        const int mm = m + (lane & 1), nn = n & ~1;
-        if (mm >= w.M || mm >= m0 + p.bt || nn >= w.N) return;
-        const size_t at = (size_t)mm * w.N + nn;
+    // two neighbouring outputs of token m
+    auto store = [&](int m, float a, float b) {
+        if (m >= w.M || m >= m0 + p.bt || nn >= w.N) return;
+        const size_t at = (size_t)m * w.N + nn;
         if (!DUAL && w.residual != nullptr) {
-            const float2 r = Ops::unpack(*reinterpret_cast<const uint32_t*>(w.residual + at));
-            a += r.x;
-            b += r.y;
+            const float2 x = Ops::unpack(*reinterpret_cast<const uint32_t*>(w.residual + at));
+            a += x.x;
+            b += x.y;
         }
         *reinterpret_cast<uint32_t*>(w.out + at) = Ops::pack(a, b);
     };
+    // of two values, the one for the even lane stays there, the other goes over: lane pairs then hold
+    // neighbouring outputs, of the first value's token in the even lane and the second's in the odd one
+    auto pair = [&](float v0, float v1, float& a, float& b) {
+        const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v0 : v1, 1);
+        a = (lane & 1) ? got : v0;
+        b = (lane & 1) ? v1 : got;
+    };
+    // accumulators of tokens m .. m + 3 at this lane's row
+    auto emit4 = [&](int m, float v0, float v1, float v2, float v3) {
+        float a, b;
+        if constexpr (DUAL) {
+            // lanes 16 apart hold the gate and the up value: the gate's lane takes tokens m and m + 2, the up's m + 1 and m + 3
+            const bool up = lane & 16;
+            const float o0 = __shfl_xor_sync(0xffffffffu, up ? v0 : v1, 16), o1 = __shfl_xor_sync(0xffffffffu, up ? v2 : v3, 16);
+            const float h0 = act_apply(ACT_SILU, up ? o0 : v0) * (up ? v1 : o0);
+            const float h1 = act_apply(ACT_SILU, up ? o1 : v2) * (up ? v3 : o1);
+            pair(h0, h1, a, b);
+            store(m + (up ? 1 : 0) + ((lane & 1) ? 2 : 0), a, b);
+        } else {
+            pair(act_apply(w.act, v0 + bias), act_apply(w.act, v1 + bias), a, b);
+            store(m + (lane & 1), a, b);
+            pair(act_apply(w.act, v2 + bias), act_apply(w.act, v3 + bias), a, b);
+            store(m + 2 + (lane & 1), a, b);
+        }
+    };
     if (p.splits == 1) {
-        // (the pair's epilogue is shared by token halves: both blocks' accumulators are at the same lanes)
         if (warp >= 4 && __all_sync(0xffffffffu, ready)) {
-            const int chunks = (p.bt + 31) / 32;
-            for (int c = DUAL ? jb : 0; c < chunks; c += DUAL ? 2 : 1) {
+            for (int c = grp; c < (p.bt + 31) / 32; c += kGroups) {
                 uint32_t g[32];
-                tmem_ld_32x32b_x32(dcol + (DUAL ? 0u : 128u * jb) + 32u * c, g);
-                if constexpr (DUAL) {
-                    uint32_t u[32];
-                    tmem_ld_32x32b_x32(dcol + 128u + 32u * c, u);
-                    tmem_ld_wait();
+                tmem_ld_32x32b_x32(dcol + 32u * c, g);
+                tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        g[e] = __float_as_uint(act_apply(ACT_SILU, __uint_as_float(g[e])) * __uint_as_float(u[e]));
-                } else {
-                    tmem_ld_wait();
-                }
-#pragma unroll
-                for (int e = 0; e < 32; e += 2)
-                    store2(m0 + 32 * c + e, __uint_as_float(g[e]), __uint_as_float(g[e + 1]));
+                for (int e = 0; e < 32; e += 4)
+                    emit4(m0 + 32 * c + e, __uint_as_float(g[e]), __uint_as_float(g[e + 1]), __uint_as_float(g[e + 2]),
+                          __uint_as_float(g[e + 3]));
             }
         }
     } else {
-        // partial sums into this CTA's shared memory: [block][token][row]
+        // partial sums into this CTA's shared memory: [token][row]
         float* part = reinterpret_cast<float*>(smem);
         if (warp >= 4 && __all_sync(0xffffffffu, ready)) {
-            for (int c = 0; c < (p.bt + 31) / 32; ++c) {
+            for (int c = grp; c < (p.bt + 31) / 32; c += kGroups) {
                 uint32_t g[32];
-                tmem_ld_32x32b_x32(dcol + 128u * jb + 32u * c, g);
+                tmem_ld_32x32b_x32(dcol + 32u * c, g);
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
-                    if (32 * c + e < p.bt) part[(jb * p.bt + 32 * c + e) * kRows + lrow] = __uint_as_float(g[e]);
+                    if (32 * c + e < p.bt) part[(32 * c + e) * kRows + r] = __uint_as_float(g[e]);
             }
         }
         __syncwarp();
         cluster_barrier_sync();
         // each rank finishes its range of tokens
         if (warp >= 4) {
-            const int per = ((p.bt + p.splits - 1) / p.splits + 1) & ~1;
+            const int per = ((p.bt + p.splits - 1) / p.splits + 3) & ~3;
             const int t1 = min(p.bt, (rank + 1) * per);
-            auto sum = [&](int j, int t) {
-                const uint32_t a = sbase + (uint32_t)((j * p.bt + t) * kRows + lrow) * 4u;
-                float v[8];
+            for (int t = rank * per + 4 * grp; t < t1; t += 4 * kGroups) {
+                float v[4][8];
 #pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    if (r < p.splits) v[r] = ld_cluster_f32(mapa_cluster(a, (uint32_t)r));
-                float s = v[0];
+                for (int i = 0; i < 8; ++i) {
+                    if (i >= p.splits) break;
+                    const uint32_t a = mapa_cluster(sbase + (uint32_t)(t * kRows + r) * 4u, (uint32_t)i);
 #pragma unroll
-                for (int r = 1; r < 8; ++r)
-                    if (r < p.splits) s += v[r];
-                return s;
-            };
-            for (int t = rank * per + (DUAL ? 2 * jb : 0); t < t1; t += DUAL ? 4 : 2) {
-                const int tb = t + 1 < p.bt ? t + 1 : t;
-                float v0 = sum(DUAL ? 0 : jb, t), v1 = sum(DUAL ? 0 : jb, tb);
-                if constexpr (DUAL) {
-                    v0 = act_apply(ACT_SILU, v0) * sum(1, t);
-                    v1 = act_apply(ACT_SILU, v1) * sum(1, tb);
+                    for (int e = 0; e < 4; ++e) v[e][i] = ld_cluster_f32(a + e * kRows * 4);
                 }
-                store2(m0 + t, v0, v1);
+#pragma unroll
+                for (int i = 1; i < 8; ++i)
+                    if (i < p.splits)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[e][0] += v[e][i];
+                emit4(m0 + t, v[0][0], v[1][0], v[2][0], v[3][0]);
             }
         }
         __syncwarp();
@@ -470,36 +473,46 @@ struct Kern {
 
 fl_status w4_tile(int dt, bool dual, const W4Params& w, const host::LaunchContext& ctx, cudaStream_t stream) {
     TileParams p;
-    const int token_tiles = (w.M + kTok - 1) / kTok;
-    p.bt = ((w.M + token_tiles - 1) / token_tiles + 15) / 16 * 16;
-    const int row_tiles = dual ? (w.N + kRows - 1) / kRows : (w.N + 2 * kRows - 1) / (2 * kRows);
-    const long long tiles = (long long)row_tiles * token_tiles;
     p.steps = (w.K + kStep - 1) / kStep;
-    // K split over a cluster when the tiles leave SMs idle: the least time, in
-    // units of one unsplit tile, of whole waves of resident clusters. Ranges
-    // are whole multiples of 128 k, the largest group.
+    const int rows = dual ? kRows / 2 : kRows, row_tiles = (w.N + rows - 1) / rows;
+    // Tokens of a tile and K split: the least time of whole waves of resident
+    // clusters. A K step costs the MMA and its shared-memory traffic (2.7
+    // cycles a token) or the expansion of its codes (about 300), whichever is
+    // more; a split adds the exchange of the partial sums. Ranges of a split
+    // are multiples of 128 k, the largest group.
     static std::atomic<int> resident[9];
-    int best = 1;
     double least = 0;
-    for (int s = 1; s <= 8; ++s) {
-        const int per = ((p.steps + 1) / 2 + s - 1) / s * 2;
-        if (s > 1 && (per < 4 || (p.steps + per - 1) / per != s)) continue;
-        int n = resident[s].load();
-        if (n == 0) {
-            n = Kern<DT_BF16, false>::resident(s);
-            if (n <= 0) n = -1;
-            resident[s] = n;
+    const int tt0 = (w.M + kTok - 1) / kTok;
+    int token_tiles = 0;
+    for (int tt = tt0; tt <= tt0 + 2 && tt <= w.M; ++tt) {
+        const int bt = ((w.M + tt - 1) / tt + 15) / 16 * 16;
+        for (int s = 1; s <= 8; ++s) {
+            const int per = ((p.steps + 1) / 2 + s - 1) / s * 2;
+            if (s > 1 && (per < 4 || (p.steps + per - 1) / per != s)) continue;
+            int n = resident[s].load();
+            if (n == 0) {
+                n = Kern<DT_BF16, false>::resident(s);
+                if (n <= 0) n = -1;
+                resident[s] = n;
+            }
+            if (n < 0) continue;
+            const long long waves = ((long long)row_tiles * tt + n - 1) / n;
+            const double step = 2.7 * bt > 300.0 ? 2.7 * bt : 300.0;
+            const double cost = (double)waves * (step * per + 4000.0 + (s > 1 ? 1500.0 + 12.0 * bt : 0.0));
+            if (token_tiles == 0 || cost < least) {
+                least = cost;
+                token_tiles = tt;
+                p.bt = bt;
+                p.splits = s;
+                p.steps_per_split = per;
+            }
         }
-        if (n < 0) continue;
-        const double cost = (double)((tiles + n - 1) / n) * (per / (double)p.steps + (s > 1 ? 0.02 : 0.0));
-        if (s == 1 || cost < least) best = s, least = cost;
     }
-    p.splits = best;
-    p.steps_per_split = ((p.steps + 1) / 2 + best - 1) / best * 2;
+    if (token_tiles == 0) return host::fail(FL_ERR_CUDA, "4-bit tile kernel: no resident CTA");
     fl_status st;
     if ((st = host::encode_matrix(&p.tm_x, dt, 2, w.x, w.K, w.M, kStep, p.bt)) != FL_OK) return st;
-    if ((st = host::encode_matrix(&p.tm_q[0], dt, 1, w.q[0], w.K / 2, w.N, kWk / 2, kRows)) != FL_OK) return st;
-    if (dual && (st = host::encode_matrix(&p.tm_q[1], dt, 1, w.q[1], w.K / 2, w.N, kWk / 2, kRows)) != FL_OK) return st;
+    if ((st = host::encode_matrix(&p.tm_q[0], dt, 1, w.q[0], w.K / 2, w.N, kWk / 2, rows)) != FL_OK) return st;
+    if (dual && (st = host::encode_matrix(&p.tm_q[1], dt, 1, w.q[1], w.K / 2, w.N, kWk / 2, rows)) != FL_OK) return st;
     if (!dual) p.tm_q[1] = p.tm_q[0];
     p.w = w;
     p.status = ctx.status;
