@@ -17,11 +17,20 @@
 // expansion (about 440 instructions a warp and step) set its pace: 237 us at
 // 4096^3.
 //
-// Roles: warp 0 TMA producer (codes in stages of 256 k, tokens in stages of
-// 64 k), warp 1 tensor memory and MMA issue, warps 2 and 3 load the scales and
-// zero points of 1024 k at a time into shared memory (transposed: one row per
-// thread there), warps 4-19 dequantise, four to a K step, and when the MMAs are
-// done apply the epilogue.
+// Roles: warp 0 loads the tokens by TMA (stages of 64 k), warp 1 owns tensor
+// memory and issues the MMAs, warps 2 and 3 load the scales and zero points of
+// 1024 k at a time into shared memory (transposed: one row per thread there; the
+// first of them is loaded by the dequantising warps, which have nothing else to
+// do yet), warps 4-19 dequantise, four to a K step, and when the MMAs are done
+// apply the epilogue, warp 20 loads the codes by TMA (stages of 256 k). Codes
+// and tokens have producers of their own, so that the codes, which come from
+// HBM and are needed first, run ahead as far as their ring reaches; the fewer
+// the tokens, the more of shared memory is the codes'. A stage of tokens and the A
+// slot of the same step share one full and one empty barrier (the bytes and
+// the four warps' arrivals on the one, the MMA's commit on the other): the single
+// issuing thread competes with four dequantising warps for its scheduler, and a
+// step with two waits and two commits took it 680 to 850 cycles whatever the
+// tile's width.
 //
 // Every mbarrier wait is bounded as in the other kernels.
 #include <atomic>
@@ -34,7 +43,7 @@ namespace fl {
 
 namespace {
 
-constexpr int kThreads = 640;
+constexpr int kThreads = 672;
 constexpr int kRows = 128;       // weight rows of a tile (TMEM lanes)
 constexpr int kTok = 256;        // tokens of a tile at most
 constexpr int kStep = 64;        // k per B stage and A slot
@@ -42,8 +51,8 @@ constexpr int kGroups = 4;       // dequantising warpgroups: K step kb goes to k
 constexpr int kWk = kGroups * kStep;  // k per code stage: one step of each warpgroup
 constexpr int kSIter = 4;        // code stages per scale stage
 constexpr int kSk = kSIter * kWk;
-constexpr int kBStages = 5, kWStages = 2, kSStages = 2, kSlots = kWStages * kGroups;
-constexpr int kBBytes = kTok * kStep * 2;           // 32 KB
+constexpr int kStages = 2 * kGroups, kWStages = 8, kSStages = 2;  // (at most; stages of tokens: 4 or 8)
+constexpr int kRing = 192 * 1024;                   // both rings
 constexpr int kWBytes = kRows * kWk / 2;            // 16 KB
 constexpr int kSPitch = 130;                        // 16-bit scales of one group: 128 rows, padded
 constexpr int kZPitch = 132;                        // zero-point bytes of one group
@@ -51,15 +60,14 @@ constexpr int kSGroups = kSk / 32;
 constexpr int kSBytes = kSGroups * kSPitch * 2;
 constexpr int kZBytes = kSGroups * kZPitch;
 
-constexpr int kOffW = kBStages * kBBytes;
-constexpr int kOffS = kOffW + kWStages * kWBytes;
+constexpr int kOffS = kRing;
 constexpr int kOffZ = kOffS + kSStages * kSBytes;
 constexpr int kOffBar = (kOffZ + kSStages * kZBytes + 7) / 8 * 8;
-constexpr int kBars = 2 * kBStages + 2 * kWStages + 2 * kSlots + 2 * kSStages + 2;
+constexpr int kBars = 2 * kStages + 2 * kWStages + 2 * kSStages + 2;
 constexpr int kOffSlot = kOffBar + kBars * 8;
 constexpr int kSmem = kOffSlot + 16 + 1024;         // + alignment slack
 static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
-static_assert(kRows * kTok * 4 <= kOffS, "the partial sums fit in the rings");
+static_assert(kRows * kTok * 4 <= kRing, "the partial sums fit in the rings");
 
 constexpr int kACol = 256;  // first tensor-memory column of the A slots (the accumulator: 0 .. 255)
 
@@ -68,6 +76,7 @@ struct TileParams {
     CUtensorMap tm_q[2];  // codes [N, K / 2] bytes, box {128, 128} (pair: {128, 64} each)
     W4Params w;
     int bt, splits, steps_per_split, steps;  // K steps of 64
+    int stages, w_stages, b_bytes;           // rings: stages * b_bytes of tokens, then the code stages
     int* status;
     unsigned long long timeout_ns;
 };
@@ -120,14 +129,12 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
     const W4Params& w = p.w;
 
     const uint32_t bar0 = sbase + kOffBar;
-    auto bfull = [&](int s) { return bar0 + 8u * s; };
-    auto bempty = [&](int s) { return bar0 + 8u * (kBStages + s); };
-    auto wfull = [&](int s) { return bar0 + 8u * (2 * kBStages + s); };
-    auto wempty = [&](int s) { return bar0 + 8u * (2 * kBStages + kWStages + s); };
-    auto afull = [&](int s) { return bar0 + 8u * (2 * kBStages + 2 * kWStages + s); };
-    auto aempty = [&](int s) { return bar0 + 8u * (2 * kBStages + 2 * kWStages + kSlots + s); };
-    auto sfull = [&](int s) { return bar0 + 8u * (2 * kBStages + 2 * kWStages + 2 * kSlots + s); };
-    auto sempty = [&](int s) { return bar0 + 8u * (2 * kBStages + 2 * kWStages + 2 * kSlots + kSStages + s); };
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (kStages + s); };
+    auto wfull = [&](int s) { return bar0 + 8u * (2 * kStages + s); };
+    auto wempty = [&](int s) { return bar0 + 8u * (2 * kStages + kWStages + s); };
+    auto sfull = [&](int s) { return bar0 + 8u * (2 * kStages + 2 * kWStages + s); };
+    auto sempty = [&](int s) { return bar0 + 8u * (2 * kStages + 2 * kWStages + kSStages + s); };
     const uint32_t dfull = bar0 + 8u * (kBars - 2), drain = bar0 + 8u * (kBars - 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -135,23 +142,21 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
     const int m0 = blockIdx.y * p.bt;
     const int n0 = tile * (DUAL ? kRows / 2 : kRows);  // first weight row (of each weight of the pair)
     const int k0 = rank * p.steps_per_split, k1 = min(p.steps, k0 + p.steps_per_split), nk = k1 - k0;
+    const int nb = p.stages, nw = p.w_stages;
+    const uint32_t wring = sbase + (uint32_t)(nb * p.b_bytes);
     // weight and row of TMEM lane r: for the pair, each warp's lanes 0-15 are
     // rows of Wg and 16-31 the same rows of Wu
     auto weight_of = [&](int r) { return DUAL ? (r >> 4) & 1 : 0; };
     auto row_of = [&](int r) { return n0 + (DUAL ? (r >> 5) * 16 + (r & 15) : r); };
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kBStages; ++s) {
-            mbar_init(bfull(s), 1);
-            mbar_init(bempty(s), 1);
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full(s), 1 + 4);
+            mbar_init(empty(s), 1);
         }
         for (int s = 0; s < kWStages; ++s) {
             mbar_init(wfull(s), 1);
             mbar_init(wempty(s), 4 * kGroups);
-        }
-        for (int s = 0; s < kSlots; ++s) {
-            mbar_init(afull(s), 4);
-            mbar_init(aempty(s), 1);
         }
         for (int s = 0; s < kSStages; ++s) {
             mbar_init(sfull(s), 2);
@@ -175,59 +180,101 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kOffSlot);
     // the first codes towards L2 (the point of coherence) while the previous kernel finishes
-    if (warp == 0 && lane == 0) {
-        for (int i = 0; i < kWStages && i * kGroups < nk; ++i)
+    if (warp == 20 && lane == 0) {
+        for (int i = 0; i < nw && i * kGroups < nk; ++i)
             for (int j = 0; j <= (DUAL ? 1 : 0); ++j)
                 tma_prefetch_2d(&p.tm_q[j], k0 * (kStep / 2) + i * (kWk / 2), n0);
     }
     griddep_wait();
     if (threadIdx.x == 0) griddep_launch_dependents();
 
+    // Scales and zero points of scale stage i into shared memory, by `count`
+    // threads: neighbouring threads take neighbouring groups of a row.
+    const int s_count = (nk * kStep + kSk - 1) / kSk;
+    auto load_scales = [&](int i, int tid, int count) {
+        const int per_row = w.K / w.group, ng = kSk / w.group, sh = 31 - __clz(ng);  // groups of a row; of a stage (8, 16, 32)
+        const int g0 = (k0 * kStep + i * kSk) / w.group, g_end = min(per_row, (k1 * kStep + w.group - 1) / w.group);
+        uint16_t* ds = reinterpret_cast<uint16_t*>(smem + kOffS + (i % kSStages) * kSBytes);
+        uint8_t* dz = smem + kOffZ + (i % kSStages) * kZBytes;
+        const bool zeros = w.zeros[0] != nullptr;
+        constexpr int U = 8;  // loads in flight per thread
+        for (int b = tid; b < kRows << sh; b += count * U) {
+            uint16_t v[U];
+            uint8_t z[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int e = b + count * u, r = e >> sh, g = g0 + (e & (ng - 1)), n = row_of(r);
+                const bool in = r < kRows && n < w.N && g < g_end;
+                const size_t at = in ? (size_t)n * per_row + g : 0;  // (0: a valid address whose value is not used)
+                v[u] = __ldg((weight_of(r) ? w.scales[1] : w.scales[0]) + at);
+                if (zeros) z[u] = __ldg((weight_of(r) ? w.zeros[1] : w.zeros[0]) + at);
+                if (!in) v[u] = 0;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int e = b + count * u, r = e >> sh, g = e & (ng - 1);
+                if (r < kRows) {
+                    ds[g * kSPitch + r] = v[u];
+                    dz[g * kZPitch + r] = zeros ? (uint8_t)(z[u] & 15) : (uint8_t)8;
+                }
+            }
+        }
+    };
+
     bool ready = false;  // epilogue warps: the accumulator is complete
     if (warp == 0) {
-        // ------------------------------------------------------------ producer
+        // ------------------------------------------------------------ tokens
         if (lane == 0) {
-            int bi = 0, wi = 0;  // loads issued
+            int issued = 0, s = 0;
+            uint32_t ph = 0;
             for (int kb = 0; kb < nk; ++kb) {
-                if (kb % kGroups == 0) {
-                    const int s = wi % kWStages;
-                    if (!wait_bar(wempty(s), (uint32_t)((wi / kWStages) & 1) ^ 1u, p.status, p.timeout_ns, 20)) break;
-                    mbar_arrive_expect_tx(wfull(s), kWBytes);
-                    const uint32_t dst = sbase + kOffW + s * kWBytes;
-                    const int x = (k0 + kb) * (kStep / 2);
-                    tma_load_2d(dst, &p.tm_q[0], wfull(s), x, n0);
-                    if (DUAL) tma_load_2d(dst + kWBytes / 2, &p.tm_q[1], wfull(s), x, n0);
-                    ++wi;
-                }
-                const int s = bi % kBStages;
-                if (!wait_bar(bempty(s), (uint32_t)((bi / kBStages) & 1) ^ 1u, p.status, p.timeout_ns, 21)) break;
-                mbar_arrive_expect_tx(bfull(s), (uint32_t)p.bt * (kStep * 2));
-                tma_load_2d(sbase + s * kBBytes, &p.tm_x, bfull(s), (k0 + kb) * kStep, m0);
-                ++bi;
+                if (!wait_bar(empty(s), ph ^ 1u, p.status, p.timeout_ns, 21)) break;
+                mbar_arrive_expect_tx(full(s), (uint32_t)p.b_bytes);
+                tma_load_2d(sbase + s * p.b_bytes, &p.tm_x, full(s), (k0 + kb) * kStep, m0);
+                ++issued;
+                if (++s == nb) s = 0, ph ^= 1u;
             }
             // every load this thread issued lands before the CTA may exit
-            for (int i = 1; i <= kBStages && i <= bi; ++i)
-                wait_bar_drain(bfull((bi - i) % kBStages), (uint32_t)(((bi - i) / kBStages) & 1), 20000000ull);
-            for (int i = 1; i <= kWStages && i <= wi; ++i)
-                wait_bar_drain(wfull((wi - i) % kWStages), (uint32_t)(((wi - i) / kWStages) & 1), 20000000ull);
+            for (int i = 1; i <= nb && i <= issued; ++i)
+                wait_bar_drain(full((issued - i) % nb), (uint32_t)(((issued - i) / nb) & 1), 20000000ull);
+        }
+    } else if (warp == 20) {
+        // ------------------------------------------------------------ codes
+        if (lane == 0) {
+            int issued = 0, s = 0;
+            uint32_t ph = 0;
+            for (int kb = 0; kb < nk; kb += kGroups) {
+                if (!wait_bar(wempty(s), ph ^ 1u, p.status, p.timeout_ns, 20)) break;
+                mbar_arrive_expect_tx(wfull(s), kWBytes);
+                const uint32_t dst = wring + s * kWBytes;
+                const int x = (k0 + kb) * (kStep / 2);
+                tma_load_2d(dst, &p.tm_q[0], wfull(s), x, n0);
+                if (DUAL) tma_load_2d(dst + kWBytes / 2, &p.tm_q[1], wfull(s), x, n0);
+                ++issued;
+                if (++s == nw) s = 0, ph ^= 1u;
+            }
+            for (int i = 1; i <= nw && i <= issued; ++i)
+                wait_bar_drain(wfull((issued - i) % nw), (uint32_t)(((issued - i) / nw) & 1), 20000000ull);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         if (lane == 0) {
             const uint32_t idesc = umma_idesc_f16(Ops::kFormat, 128, (uint32_t)p.bt);
             bool ok = true;
-            for (int kb = 0; kb < nk; ++kb) {
-                const int s = kb % kBStages, a = kb % kSlots;
-                ok = wait_bar(bfull(s), (uint32_t)((kb / kBStages) & 1), p.status, p.timeout_ns, 22) &&
-                     wait_bar(afull(a), (uint32_t)((kb / kSlots) & 1), p.status, p.timeout_ns, 23);
+            uint32_t ph = 0, acc = 0;
+            for (int kb = 0, s = 0; kb < nk; ++kb) {
+                ok = wait_bar(full(s), ph, p.status, p.timeout_ns, 22);
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t db = sw128_kmajor_desc(sbase + s * kBBytes);
+                const uint64_t db = sw128_kmajor_desc(sbase + s * p.b_bytes);
+                const uint32_t ta = tmem + kACol + 32u * s;
 #pragma unroll
-                for (int kk = 0; kk < kStep / 16; ++kk)
-                    umma_f16_ts(tmem, tmem + kACol + 32u * a + 8u * kk, db + 2 * kk, idesc, (kb | kk) != 0);
-                umma_commit(bempty(s));
-                umma_commit(aempty(a));
+                for (int kk = 0; kk < kStep / 16; ++kk) {
+                    umma_f16_ts(tmem, ta + 8u * kk, db + 2 * kk, idesc, acc);
+                    acc = 1;
+                }
+                umma_commit(empty(s));
+                if (++s == nb) s = 0, ph ^= 1u;
             }
             if (ok) umma_commit(dfull);
             // all MMAs issued by this thread complete before tensor memory is released
@@ -235,38 +282,11 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
             wait_bar_drain(drain, 0, 20000000ull);
         }
     } else if (warp < 4) {
-        // ------------------------------------------------------------ scales and zero points, 64 rows each
-        const int per_row = w.K / w.group, ng = kSk / w.group;  // groups of a row; of a stage (8, 16 or 32)
-        const int sh = 31 - __clz(ng);
-        const int g_end = min(per_row, (k1 * kStep + w.group - 1) / w.group);
-        const int stages = (nk * kStep + kSk - 1) / kSk, half = kRows / 2 << sh;
-        for (int i = 0; i < stages; ++i) {
+        // ------------------------------------------------------------ scales and zero points of the later stages
+        for (int i = 1; i < s_count; ++i) {
             const int s = i % kSStages;
             if (!wait_bar(sempty(s), (uint32_t)((i / kSStages) & 1) ^ 1u, p.status, p.timeout_ns, 24)) break;
-            const int g0 = (k0 * kStep + i * kSk) / w.group;
-            uint16_t* ds = reinterpret_cast<uint16_t*>(smem + kOffS + s * kSBytes);
-            uint8_t* dz = smem + kOffZ + s * kZBytes;
-            constexpr int U = 16;  // loads in flight per lane
-            for (int b = (warp - 2) * half + lane; b < (warp - 1) * half; b += 32 * U) {
-                uint16_t v[U];
-                uint8_t z[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int e = b + 32 * u, r = e >> sh, g = g0 + (e & (ng - 1)), n = row_of(r);
-                    const bool in = e < (warp - 1) * half && n < w.N && g < g_end;
-                    const int j = weight_of(r);
-                    v[u] = in ? __ldg(w.scales[j] + (size_t)n * per_row + g) : (uint16_t)0;
-                    z[u] = in && w.zeros[j] != nullptr ? (uint8_t)(__ldg(w.zeros[j] + (size_t)n * per_row + g) & 15) : (uint8_t)8;
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int e = b + 32 * u, r = e >> sh, g = e & (ng - 1);
-                    if (e < (warp - 1) * half) {
-                        ds[g * kSPitch + r] = v[u];
-                        dz[g * kZPitch + r] = z[u];
-                    }
-                }
-            }
+            load_scales(i, threadIdx.x - 64, 64);
             __syncwarp();
             if (lane == 0) mbar_arrive(sfull(s));
         }
@@ -277,14 +297,21 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
         const int gsh = 31 - __clz(w.group);
         // this row's codes of the warpgroup's K step in a code stage
         const int srow = DUAL ? weight_of(r) * (kRows / 2) + (r >> 5) * 16 + (r & 15) : r;
-        const uint32_t src0 = sbase + kOffW + srow * 128 + (((2 * grp) ^ (srow & 7)) << 4);
-        const uint32_t src1 = sbase + kOffW + srow * 128 + (((2 * grp + 1) ^ (srow & 7)) << 4);
+        const uint32_t src0 = wring + srow * 128 + (((2 * grp) ^ (srow & 7)) << 4);
+        const uint32_t src1 = wring + srow * 128 + (((2 * grp + 1) ^ (srow & 7)) << 4);
+        load_scales(0, threadIdx.x - 128, 512);
+        named_bar_sync(1, 512);
         bool ok = true;
+        int ws = 0, a = grp;
+        uint32_t wph = 0, ph = 0;
         for (int it = 0, kb = grp; kb < nk; ++it, kb += kGroups) {
-            const int ws = it % kWStages, ss = it / kSIter % kSStages;
-            ok = wait_bar(wfull(ws), (uint32_t)((it / kWStages) & 1), p.status, p.timeout_ns, 25);
-            if (ok && it % kSIter == 0)
-                ok = wait_bar(sfull(ss), (uint32_t)((it / (kSIter * kSStages)) & 1), p.status, p.timeout_ns, 26);
+            const int ss = it / kSIter % kSStages;
+            ok = wait_bar(wfull(ws), wph, p.status, p.timeout_ns, 25);
+            if (ok && it % kSIter == 0 && it > 0) {
+                // (stage 0's barrier has seen no phase for the first 1024 k)
+                const int i = it / kSIter, phases = i / kSStages - (ss == 0 ? 1 : 0);
+                ok = wait_bar(sfull(ss), (uint32_t)(phases & 1), p.status, p.timeout_ns, 26);
+            }
             if (!ok) break;
             const uint4 c0 = ld_shared_v4(src0 + ws * kWBytes), c1 = ld_shared_v4(src1 + ws * kWBytes);
             const uint16_t* ds = reinterpret_cast<const uint16_t*>(smem + kOffS + ss * kSBytes);
@@ -307,25 +334,27 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
                 mbar_arrive(wempty(ws));
                 if (it % kSIter == kSIter - 1) mbar_arrive(sempty(ss));
             }
-            const int a = ws * kGroups + grp;
-            ok = wait_bar(aempty(a), (uint32_t)((it / kWStages) & 1) ^ 1u, p.status, p.timeout_ns, 27);
+            if (++ws == nw) ws = 0, wph ^= 1u;
+            ok = wait_bar(empty(a), ph ^ 1u, p.status, p.timeout_ns, 27);
             if (!ok) break;
             tc_fence_after();
             tmem_st_32x32b_x32(tmem + lanes + kACol + 32u * a, o);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(afull(a));
+            if (lane == 0) mbar_arrive(full(a));
+            if ((a += kGroups) >= nb) a = grp, ph ^= 1u;
         }
         ready = ok && wait_bar(dfull, 0, p.status, p.timeout_ns, 28);
         tc_fence_after();
     }
 
     // ---------------------------------------------------------------- epilogue
+    const bool epi = warp >= 4 && warp < 20;
     const int grp = (warp - 4) >> 2, r = (threadIdx.x - 128) & 127;
     const uint32_t dcol = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const int n = row_of(r), nn = n & ~1;
-    const float bias = warp >= 4 && !DUAL && w.bias != nullptr && n < w.N ? Ops::unpack(w.bias[n]).x : 0.f;
+    const float bias = epi && !DUAL && w.bias != nullptr && n < w.N ? Ops::unpack(w.bias[n]).x : 0.f;
     // two neighbouring outputs of token m
     auto store = [&](int m, float a, float b) {
         if (m >= w.M || m >= m0 + p.bt || nn >= w.N) return;
@@ -363,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
         }
     };
     if (p.splits == 1) {
-        if (warp >= 4 && __all_sync(0xffffffffu, ready)) {
+        if (epi && __all_sync(0xffffffffu, ready)) {
             for (int c = grp; c < (p.bt + 31) / 32; c += kGroups) {
                 uint32_t g[32];
                 tmem_ld_32x32b_x32(dcol + 32u * c, g);
@@ -377,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
     } else {
         // partial sums into this CTA's shared memory: [token][row]
         float* part = reinterpret_cast<float*>(smem);
-        if (warp >= 4 && __all_sync(0xffffffffu, ready)) {
+        if (epi && __all_sync(0xffffffffu, ready)) {
             for (int c = grp; c < (p.bt + 31) / 32; c += kGroups) {
                 uint32_t g[32];
                 tmem_ld_32x32b_x32(dcol + 32u * c, g);
@@ -390,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
         __syncwarp();
         cluster_barrier_sync();
         // each rank finishes its range of tokens
-        if (warp >= 4) {
+        if (epi) {
             const int per = ((p.bt + p.splits - 1) / p.splits + 3) & ~3;
             const int t1 = min(p.bt, (rank + 1) * per);
             for (int t = rank * per + 4 * grp; t < t1; t += 4 * kGroups) {
@@ -509,6 +538,11 @@ fl_status w4_tile(int dt, bool dual, const W4Params& w, const host::LaunchContex
         }
     }
     if (token_tiles == 0) return host::fail(FL_ERR_CUDA, "4-bit tile kernel: no resident CTA");
+    // rings: eight stages of tokens where they leave half of shared memory to the codes, else four
+    p.b_bytes = p.bt * kStep * 2;
+    p.stages = 2 * kGroups * p.b_bytes <= kRing / 2 ? 2 * kGroups : kGroups;
+    p.w_stages = (kRing - p.stages * p.b_bytes) / kWBytes;
+    if (p.w_stages > kWStages) p.w_stages = kWStages;
     fl_status st;
     if ((st = host::encode_matrix(&p.tm_x, dt, 2, w.x, w.K, w.M, kStep, p.bt)) != FL_OK) return st;
     if ((st = host::encode_matrix(&p.tm_q[0], dt, 1, w.q[0], w.K / 2, w.N, kWk / 2, rows)) != FL_OK) return st;
