@@ -77,77 +77,6 @@ __global__ void __launch_bounds__(kQuantThreads)
     }
 }
 
-// ---------------------------------------------------------------------------
-// the products
-// ---------------------------------------------------------------------------
-constexpr int kSimpleRows = 4;
-
-// One warp: kSimpleRows rows of x against one row of the weight (or of the
-// gate and the up weight).
-template <int DT, bool DUAL>
-__global__ void __launch_bounds__(256) fl_w4_gemm_kernel(const __grid_constant__ W4Params p) {
-    using Ops = DTypeOps<DT>;
-    constexpr int NW = DUAL ? 2 : 1;
-    griddep_wait();
-    griddep_launch_dependents();
-    const int lane = threadIdx.x & 31, K = p.K, G = p.group;
-    const long long t = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int n = (int)(t % p.N);
-    const long long m0 = t / p.N * kSimpleRows;
-    if (m0 >= p.M) return;
-    float acc[NW][kSimpleRows] = {}, sq[kSimpleRows] = {};
-    for (int k = lane * 8; k < K; k += 256) {
-        float w[NW][8];
-#pragma unroll
-        for (int j = 0; j < NW; ++j) {
-            const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(p.q[j] + ((size_t)n * K + k) / 2));
-            const size_t g = (size_t)n * (K / G) + k / G;
-            const float s = Ops::unpack(__ldg(p.scales[j] + g)).x;
-            const float z = p.zeros[j] != nullptr ? (float)(__ldg(p.zeros[j] + g) & 15) : 8.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[j][e] = s * ((float)((c >> (4 * e)) & 15u) - z);
-        }
-#pragma unroll
-        for (int r = 0; r < kSimpleRows; ++r) {
-            if (m0 + r >= p.M) continue;
-            uint4 v = ldg_v4(p.x + (m0 + r) * K + k);
-            const uint32_t xs[4] = {v.x, v.y, v.z, v.w};
-            uint4 g = make_uint4(0, 0, 0, 0);
-            if (p.gamma != nullptr) g = ldg_v4(p.gamma + k);
-            const uint32_t gs[4] = {g.x, g.y, g.z, g.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float2 f = Ops::unpack(xs[e]);
-                if (p.gamma != nullptr) {
-                    sq[r] = fmaf(f.x, f.x, fmaf(f.y, f.y, sq[r]));
-                    f = Ops::unpack(Ops::mul2(xs[e], gs[e]));
-                }
-#pragma unroll
-                for (int j = 0; j < NW; ++j) acc[j][r] = fmaf(f.x, w[j][2 * e], fmaf(f.y, w[j][2 * e + 1], acc[j][r]));
-            }
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < kSimpleRows; ++r) {
-        const long long m = m0 + r;
-        for (int o = 16; o > 0; o >>= 1) {
-            sq[r] += __shfl_xor_sync(0xffffffffu, sq[r], o);
-            for (int j = 0; j < NW; ++j) acc[j][r] += __shfl_xor_sync(0xffffffffu, acc[j][r], o);
-        }
-        if (lane != 0 || m >= p.M) continue;
-        const float rs = p.gamma != nullptr ? rsqrtf(sq[r] / (float)K + p.eps) : 1.f;
-        float y = acc[0][r] * rs;
-        if constexpr (DUAL) {
-            y = act_apply(ACT_SILU, y) * (acc[1][r] * rs);
-        } else {
-            if (p.bias != nullptr) y += Ops::unpack(p.bias[n]).x;
-            y = act_apply(p.act, y);
-            if (p.residual != nullptr) y += Ops::unpack(p.residual[m * p.N + n]).x;
-        }
-        p.out[m * p.N + n] = (uint16_t)(Ops::pack(y, 0.f) & 0xffffu);
-    }
-}
-
 fl_status check_weight(const char* name, const fl_w4_weight* w, long long N, long long K) {
     using host::fail;
     if (w == nullptr) return fail(FL_ERR_INVALID_ARG, "%s must not be null", name);
@@ -190,15 +119,12 @@ void set_weight(W4Params& p, int j, const fl_w4_weight* w) {
     p.group = w->group;
 }
 
-// Few rows: the weight-streaming kernel, which applies the norm itself.
-constexpr int kFewRows = 8;
 constexpr int kMaxRows = 65000 * 256;  // token tiles of one grid
-bool few_rows(int M) { return M <= kFewRows; }
 
 // One product whose arguments have been checked. `normed`: where the rows go
 // that the tile kernel reads, x * gamma / rms rounded to the dtype.
 fl_status run(int dt, bool dual, const W4Params& p, void* normed, const host::LaunchContext& ctx, cudaStream_t stream) {
-    if (!few_rows(p.M)) {
+    if (!w4_few_rows(p.M, p.K)) {
         W4Params t = p;
         if (p.gamma != nullptr) {
             const fl_status st = host::launched(
@@ -208,16 +134,7 @@ fl_status run(int dt, bool dual, const W4Params& p, void* normed, const host::La
         }
         return w4_tile(dt, dual, t, ctx, stream);
     }
-    const long long warps = (p.M + kSimpleRows - 1) / kSimpleRows * (long long)p.N;
-    const dim3 grid((unsigned)((warps + 7) / 8));
-    cudaError_t e;
-    if (dt == FL_F16)
-        e = dual ? host::launch(fl_w4_gemm_kernel<DT_F16, true>, grid, 256, 0, ctx.pdl, stream, p)
-                 : host::launch(fl_w4_gemm_kernel<DT_F16, false>, grid, 256, 0, ctx.pdl, stream, p);
-    else
-        e = dual ? host::launch(fl_w4_gemm_kernel<DT_BF16, true>, grid, 256, 0, ctx.pdl, stream, p)
-                 : host::launch(fl_w4_gemm_kernel<DT_BF16, false>, grid, 256, 0, ctx.pdl, stream, p);
-    return host::launched(e, "4-bit product kernel");
+    return w4_rows(dt, dual, p, ctx, stream);
 }
 
 fl_status check_workspace(const void* workspace, size_t bytes, size_t need) {
@@ -260,7 +177,7 @@ fl_status fl_w4_quantize(const void* W, void* q, void* scales, int N, int K, int
 }
 
 size_t fl_w4_gemm_workspace_size(int M, int K, int norm) {
-    return norm && M > 0 && K > 0 && !fl::few_rows(M) ? (size_t)M * K * 2 : 0;
+    return norm && M > 0 && K > 0 && !fl::w4_few_rows(M, K) ? (size_t)M * K * 2 : 0;
 }
 
 fl_status fl_w4_gemm(const void* x, const void* gamma, const fl_w4_weight* W, const void* bias, const void* residual,

@@ -23,6 +23,10 @@ struct W4Params {
     float eps;
 };
 
+// Decode kernel (fl_w4_rows.cu): up to 8 rows that fit in shared memory, with the RMSNorm prologue.
+bool w4_few_rows(int M, int K);
+fl_status w4_rows(int dt, bool dual, const W4Params& p, const host::LaunchContext& ctx, cudaStream_t stream);
+
 // Tile kernel (fl_w4_tile.cu): no prologue, any number of rows.
 fl_status w4_tile(int dt, bool dual, const W4Params& p, const host::LaunchContext& ctx, cudaStream_t stream);
 

@@ -1,0 +1,372 @@
+// 4-bit products for one to eight rows: the weight as a stream.
+//
+// The step is bound by reading the codes once (0.5 bytes a weight and 2 per
+// group), and next to that by turning them into operands. The weight is the A
+// operand of warp-level m16n8k16 MMAs, 16 weight rows (or, for the SwiGLU pair,
+// 8 rows of Wg over the same 8 of Wu) against up to 8 activation rows as B, so one set of
+// expanded codes serves every row and no MMA is padded along the weight.
+//
+// A lane of a quad loads words of 8 consecutive codes straight into registers:
+// for a group of 32 V codes (V = 1, 2, 4), V words at k = t * 8 V of the group
+// (t: lane of the quad), so every MMA's 16 k lie in one group, the codes are
+// exact integers in the operand (code - zero), and the group's scale multiplies
+// the fp32 sums of the group: no rounding of the weight at all. In a word, code i
+// is paired with code i + 4 (a mask and an OR put both into the mantissas of
+// 128 or 1024, one subtraction leaves the integers); the activation rows are
+// stored in shared memory in the same order, one 16-byte vector per word.
+//
+// Loads run in blocks of 16 (V = 1: 8) words of each of the lane's two weight rows,
+// double-buffered across units (16 or 8 + 8 weight rows); a CTA's 8 warps take
+// 8 slices of K and add their sums through shared memory in warp order.
+#include "fl_common.cuh"
+#include "fl_host.h"
+#include "fl_w4.h"
+
+namespace fl {
+
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+// words of one weight row in a register block (groups of 32 also hold four times the scales)
+__host__ __device__ constexpr int block_words(int V) { return V == 1 ? 8 : 16; }
+constexpr int kSmemMax = 200 * 1024;
+
+// Row stride of the activation rows in 16-byte vectors: 4 mod 8, so that the
+// 8 lanes of a quarter warp (two rows, four vectors each) hit different banks.
+__host__ __device__ __forceinline__ int row_vecs(int K) { return (K / 8 + 7) / 8 * 8 + 4; }
+__host__ __device__ __forceinline__ int smem_bytes(int M, int K) { return M * row_vecs(K) * 16; }
+
+template <int DT>
+struct Mma;
+template <>
+struct Mma<DT_F16> {
+    static constexpr uint32_t kMagic = 0x64006400u;  // 1024
+    static __device__ __forceinline__ void run(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+    static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
+        uint32_t d;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
+};
+template <>
+struct Mma<DT_BF16> {
+    static constexpr uint32_t kMagic = 0x43004300u;  // 128
+    static __device__ __forceinline__ void run(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+    static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
+        uint32_t d;
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
+};
+
+// Codes of one weight row, V words, not kept in L1.
+template <int V>
+__device__ __forceinline__ void load_words(uint32_t (&w)[V], const uint8_t* p) {
+    if constexpr (V == 4)
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+            : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
+    else if constexpr (V == 2)
+        asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+    else
+        asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+}
+
+// One register block of the stream: U groups of the lane's two weight rows, and
+// the scales and zero points of groups t, t + 4, .. of them (lane t of the quad).
+template <int V>
+struct Block {
+    static constexpr int U = block_words(V) / V, S = U / 4;
+    uint32_t w[2][U][V];
+    uint16_t s[2][S];
+    uint8_t z[2][S];
+};
+
+// The weight rows of a lane in unit u, first and second half of the MMA's 16.
+struct Rows {
+    const uint8_t* q[2];
+    const uint16_t* s[2];
+    const uint8_t* z[2];
+};
+
+template <bool DUAL>
+__device__ __forceinline__ Rows rows_of(const W4Params& p, int u, int g, int groups) {
+    Rows r;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int j = DUAL ? h : 0;
+        // (rows past N, in the last unit when N is 8 mod 16, repeat row N - 1)
+        const size_t n = DUAL ? (size_t)u * 8 + g : (size_t)min(u * 16 + h * 8 + g, p.N - 1);
+        r.q[h] = p.q[j] + n * (p.K / 2);
+        r.s[h] = p.scales[j] + n * groups;
+        r.z[h] = p.zeros[j] == nullptr ? nullptr : p.zeros[j] + n * groups;
+    }
+    return r;
+}
+
+// Issues the loads of groups c0 .. c0 + U - 1 (below c1).
+template <int V>
+__device__ __forceinline__ void load_block(Block<V>& B, const Rows& r, int c0, int c1, int t) {
+#pragma unroll
+    for (int i = 0; i < Block<V>::U; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (c0 + i < c1) {
+                load_words<V>(B.w[h][i], r.q[h] + ((size_t)(c0 + i) * 4 + t) * (4 * V));
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) B.w[h][i][j] = 0u;
+            }
+        }
+#pragma unroll
+    for (int i = 0; i < Block<V>::S; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = c0 + 4 * i + t;
+            B.s[h][i] = c < c1 ? __ldg(r.s[h] + c) : (uint16_t)0;
+            B.z[h][i] = c < c1 && r.z[h] != nullptr ? __ldg(r.z[h] + c) : (uint8_t)8;
+        }
+}
+
+// acc += the block's groups times the activation rows (xrow: this lane's row of
+// them, offset to the quad's lane, or null).
+template <int DT, int V>
+__device__ __forceinline__ void mma_block(const Block<V>& B, const uint4* xrow, int c0, int c1, int t, float (&acc)[4]) {
+    using O = Mma<DT>;
+#pragma unroll
+    for (int i = 0; i < Block<V>::U; ++i) {
+        if (c0 + i >= c1) break;  // (warp-uniform)
+        // the group's scale and zero point of both rows, from lane i % 4 of the quad
+        const uint32_t mine = (uint32_t)B.s[0][i / 4] | ((uint32_t)B.s[1][i / 4] << 16);
+        const uint32_t both = __shfl_sync(0xffffffffu, mine, i & 3, 4);
+        const uint32_t zm = (uint32_t)B.z[0][i / 4] | ((uint32_t)B.z[1][i / 4] << 8);
+        const uint32_t zb = __shfl_sync(0xffffffffu, zm, i & 3, 4);
+        const uint32_t z0 = O::kMagic + (zb & 15u) * 0x10001u, z1 = O::kMagic + ((zb >> 8) & 15u) * 0x10001u;
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const uint4 x = xrow != nullptr ? xrow[((c0 + i) * V + j) * 4] : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t w0 = B.w[0][i][j], w1 = B.w[1][i][j];
+            uint32_t e[2][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                e[0][k] = O::sub(((w0 >> (4 * k)) & 0x000f000fu) | O::kMagic, z0);
+                e[1][k] = O::sub(((w1 >> (4 * k)) & 0x000f000fu) | O::kMagic, z1);
+            }
+            const uint32_t a0[4] = {e[0][0], e[1][0], e[0][1], e[1][1]}, a1[4] = {e[0][2], e[1][2], e[0][3], e[1][3]};
+            O::run(c, a0, x.x, x.y);
+            O::run(c, a1, x.z, x.w);
+        }
+        const float2 s = DTypeOps<DT>::unpack(both);
+        acc[0] = fmaf(s.x, c[0], acc[0]);
+        acc[1] = fmaf(s.x, c[1], acc[1]);
+        acc[2] = fmaf(s.y, c[2], acc[2]);
+        acc[3] = fmaf(s.y, c[3], acc[3]);
+    }
+}
+
+// A 16-byte vector of 8 activations as (0, 4), (1, 5), (2, 6), (3, 7).
+__device__ __forceinline__ uint4 pair_up(const uint4& v) {
+    return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                      __byte_perm(v.y, v.w, 0x7632));
+}
+
+// The activation rows in shared memory: x, or x * gamma rounded once with the
+// RMS row scale in rscale. Vector v of a row (8 k) goes to the place where the
+// quad reads it: group v / 4V, word v % V of lane v / V % 4. R: a bound on M.
+template <int DT, bool NORM, int R, int V, typename Pre>
+__device__ void build_rows(const W4Params& p, uint4* xs, float* rscale, Pre pre) {
+    using Ops = DTypeOps<DT>;
+    const int M = p.M, vecs = p.K / 8, ld = row_vecs(p.K);
+    __shared__ float part[kWarps][R];
+    float sq[R];
+#pragma unroll
+    for (int m = 0; m < R; ++m) sq[m] = 0.f;
+    bool first = true;
+    constexpr int C = R <= 4 ? 2 : 1;  // vectors of a row in flight per thread
+    for (int c0 = threadIdx.x; c0 < vecs || first; c0 += C * kThreads) {
+        uint4 v[C][R], gv[C];
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            const int c = c0 + j * kThreads;
+            if (c < vecs) {
+                if (NORM) gv[j] = ldg_v4(p.gamma + (size_t)c * 8);
+#pragma unroll
+                for (int m = 0; m < R; ++m)
+                    if (m < M) v[j][m] = ldg_v4(p.x + (size_t)m * p.K + (size_t)c * 8);
+            }
+        }
+        if (first) pre();
+        first = false;
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            const int c = c0 + j * kThreads;
+            if (c >= vecs) continue;
+            const int to = c / (4 * V) * (4 * V) + c % V * 4 + c / V % 4;
+#pragma unroll
+            for (int m = 0; m < R; ++m) {
+                if (m >= M) continue;
+                uint4 o = v[j][m];
+                if (NORM) {
+                    const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = Ops::unpack(w[e]);
+                        sq[m] = fmaf(f.x, f.x, fmaf(f.y, f.y, sq[m]));
+                    }
+                    o = make_uint4(Ops::mul2(o.x, gv[j].x), Ops::mul2(o.y, gv[j].y), Ops::mul2(o.z, gv[j].z),
+                                   Ops::mul2(o.w, gv[j].w));
+                }
+                xs[m * ld + to] = pair_up(o);
+            }
+        }
+    }
+    if (NORM) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+        for (int m = 0; m < R; ++m) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sq[m] += __shfl_xor_sync(0xffffffffu, sq[m], o);
+            if (lane == 0) part[warp][m] = sq[m];
+        }
+        __syncthreads();
+        if (threadIdx.x < R) {
+            float a = 0.f;
+            for (int w = 0; w < kWarps; ++w) a += part[w][threadIdx.x];
+            rscale[threadIdx.x] = rsqrtf(a / (float)p.K + p.eps);
+        }
+    }
+    __syncthreads();
+}
+
+template <int DT, bool DUAL, int V>
+__global__ void __launch_bounds__(kThreads, 2) fl_w4_rows_kernel(const __grid_constant__ W4Params p) {
+    using Ops = DTypeOps<DT>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint4* xs = reinterpret_cast<uint4*>(smem);
+    __shared__ float rscale[8];
+    __shared__ float4 red[2][kWarps][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int groups = p.K / (32 * V), units = DUAL ? p.N / 8 : (p.N + 15) / 16;
+    const int per = (groups + kWarps - 1) / kWarps, s0 = min(groups, warp * per), s1 = min(groups, s0 + per);
+    constexpr int U = Block<V>::U;
+    const int blocks = (per + U - 1) / U;  // (the same for every warp: the block loop holds barriers)
+    Rows rows = rows_of<DUAL>(p, blockIdx.x, g, groups);
+    // L2 prefetch of the rows of x (each line by one CTA of the grid) and of this
+    // warp's first codes: L2 is the point of coherence, so a prefetch before the
+    // dependency wait cannot bring in stale data
+    {
+        const int xl = (p.M * p.K * 2 + 127) / 128;
+        for (int i = (int)(threadIdx.x * gridDim.x + blockIdx.x); i < xl; i += kThreads * gridDim.x)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(p.x) + (size_t)i * 128));
+        // 128-byte lines of the slice: 256 codes each
+        for (int c = s0 * 16 * V + t * 128; c < s1 * 16 * V && c < s0 * 16 * V + 512; c += 512) {
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(rows.q[0] + c));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(rows.q[1] + c));
+        }
+    }
+    griddep_wait();
+    Block<V> A, B;
+    auto pre = [&] { load_block<V>(A, rows, s0, s1, t); };
+    if (p.gamma != nullptr) {
+        if (p.M <= 2) build_rows<DT, true, 2, V>(p, xs, rscale, pre);
+        else if (p.M <= 4) build_rows<DT, true, 4, V>(p, xs, rscale, pre);
+        else build_rows<DT, true, 8, V>(p, xs, rscale, pre);
+    } else {
+        if (threadIdx.x < 8) rscale[threadIdx.x] = 1.f;
+        if (p.M <= 4) build_rows<DT, false, 4, V>(p, xs, rscale, pre);
+        else build_rows<DT, false, 8, V>(p, xs, rscale, pre);
+    }
+    griddep_launch_dependents();
+    const uint4* xrow = g < p.M ? xs + g * row_vecs(p.K) + t : nullptr;
+
+    int q = 0, buf = 0;
+    for (int u = blockIdx.x; u < units; u += gridDim.x, buf ^= 1) {
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int b = 0; b < blocks; ++b, ++q) {
+            const bool last = b == blocks - 1, more = !last || u + (int)gridDim.x < units;
+            const int nb = last ? 0 : b + 1;
+            if (last && more) rows = rows_of<DUAL>(p, u + gridDim.x, g, groups);
+            if ((q & 1) == 0) {
+                if (more) load_block<V>(B, rows, s0 + nb * U, s1, t);
+                mma_block<DT, V>(A, xrow, s0 + b * U, s1, t, acc);
+            } else {
+                if (more) load_block<V>(A, rows, s0 + nb * U, s1, t);
+                mma_block<DT, V>(B, xrow, s0 + b * U, s1, t, acc);
+            }
+        }
+        red[buf][warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        __syncthreads();
+        // lane (g, t) of the sums: weight rows g and g + 8 (gate and up), activation rows 2 t and 2 t + 1
+        if (warp == 0) {
+            float4 v = red[buf][0][lane];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) {
+                const float4 o = red[buf][w][lane];
+                v.x += o.x;
+                v.y += o.y;
+                v.z += o.z;
+                v.w += o.w;
+            }
+            const float sum[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int m = 2 * t + e;
+                if (m >= p.M) continue;
+                const float rs = rscale[m];
+                if constexpr (DUAL) {
+                    const float h = act_apply(ACT_SILU, sum[e] * rs) * (sum[2 + e] * rs);
+                    p.out[(size_t)m * p.N + u * 8 + g] = (uint16_t)(Ops::pack(h, 0.f) & 0xffffu);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int n = u * 16 + h * 8 + g;
+                        if (n >= p.N) continue;
+                        float y = sum[2 * h + e] * rs;
+                        if (p.bias != nullptr) y += Ops::unpack(p.bias[n]).x;
+                        y = act_apply(p.act, y);
+                        if (p.residual != nullptr) y += Ops::unpack(p.residual[(size_t)m * p.N + n]).x;
+                        p.out[(size_t)m * p.N + n] = (uint16_t)(Ops::pack(y, 0.f) & 0xffffu);
+                    }
+                }
+            }
+        }
+        // (red is double-buffered: the next unit writes the other half, and the
+        // one after that only follows the next __syncthreads)
+    }
+}
+
+template <int DT, bool DUAL, int V>
+cudaError_t launch_rows(const W4Params& p, const host::LaunchContext& ctx, cudaStream_t stream) {
+    auto kern = fl_w4_rows_kernel<DT, DUAL, V>;
+    static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    if (attr != cudaSuccess) return attr;
+    const int smem = smem_bytes(p.M, p.K), units = DUAL ? p.N / 8 : (p.N + 15) / 16;
+    const int most = ctx.sms * (smem <= 104 * 1024 ? 2 : 1);  // resident CTAs
+    return host::launch(kern, dim3((unsigned)(units < most ? units : most)), kThreads, (size_t)smem, ctx.pdl, stream, p);
+}
+
+}  // namespace
+
+bool w4_few_rows(int M, int K) { return M <= 8 && smem_bytes(M, K) <= kSmemMax; }
+
+fl_status w4_rows(int dt, bool dual, const W4Params& p, const host::LaunchContext& ctx, cudaStream_t stream) {
+    cudaError_t e = cudaErrorInvalidValue;
+#define FL_CASE(DT, DUAL, V) \
+    if (dt == DT && dual == DUAL && p.group == 32 * V) e = launch_rows<DT, DUAL, V>(p, ctx, stream);
+    FL_CASE(0, false, 1) FL_CASE(0, false, 2) FL_CASE(0, false, 4) FL_CASE(0, true, 1) FL_CASE(0, true, 2) FL_CASE(0, true, 4)
+    FL_CASE(1, false, 1) FL_CASE(1, false, 2) FL_CASE(1, false, 4) FL_CASE(1, true, 1) FL_CASE(1, true, 2) FL_CASE(1, true, 4)
+#undef FL_CASE
+    return host::launched(e, "4-bit decode kernel");
+}
+
+}  // namespace fl
