@@ -30,4 +30,13 @@ fl_status w4_rows(int dt, bool dual, const W4Params& p, const host::LaunchContex
 // Tile kernel (fl_w4_tile.cu): no prologue, any number of rows.
 fl_status w4_tile(int dt, bool dual, const W4Params& p, const host::LaunchContext& ctx, cudaStream_t stream);
 
+#ifdef __CUDACC__
+// (a & mask) | bits as one instruction (the compiler makes two of it when both are immediates)
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t bits) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(mask), "r"(bits));
+    return d;
+}
+#endif
+
 }  // namespace fl

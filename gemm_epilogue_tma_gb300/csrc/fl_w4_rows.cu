@@ -47,6 +47,13 @@ struct Mma<DT_F16> {
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     }
+    // c = a b
+    static __device__ __forceinline__ void first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %10, %10, %10};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+    }
     static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
         uint32_t d;
         asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -61,6 +68,13 @@ struct Mma<DT_BF16> {
             "{%0, %1, %2, %3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+    // c = a b
+    static __device__ __forceinline__ void first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %10, %10, %10};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
     }
     static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
         uint32_t d;
@@ -114,7 +128,7 @@ __device__ __forceinline__ Rows rows_of(const W4Params& p, int u, int g, int gro
 }
 
 // Issues the loads of groups c0 .. c0 + U - 1 (below c1).
-template <int V>
+template <int V, bool Z>
 __device__ __forceinline__ void load_block(Block<V>& B, const Rows& r, int c0, int c1, int t) {
 #pragma unroll
     for (int i = 0; i < Block<V>::U; ++i)
@@ -133,13 +147,13 @@ __device__ __forceinline__ void load_block(Block<V>& B, const Rows& r, int c0, i
         for (int h = 0; h < 2; ++h) {
             const int c = c0 + 4 * i + t;
             B.s[h][i] = c < c1 ? __ldg(r.s[h] + c) : (uint16_t)0;
-            B.z[h][i] = c < c1 && r.z[h] != nullptr ? __ldg(r.z[h] + c) : (uint8_t)8;
+            if (Z) B.z[h][i] = c < c1 ? __ldg(r.z[h] + c) : (uint8_t)0;
         }
 }
 
 // acc += the block's groups times the activation rows (xrow: this lane's row of
-// them, offset to the quad's lane, or null).
-template <int DT, int V>
+// them, offset to the quad's lane).
+template <int DT, int V, bool Z>
 __device__ __forceinline__ void mma_block(const Block<V>& B, const uint4* xrow, int c0, int c1, int t, float (&acc)[4]) {
     using O = Mma<DT>;
 #pragma unroll
@@ -148,22 +162,26 @@ __device__ __forceinline__ void mma_block(const Block<V>& B, const uint4* xrow, 
         // the group's scale and zero point of both rows, from lane i % 4 of the quad
         const uint32_t mine = (uint32_t)B.s[0][i / 4] | ((uint32_t)B.s[1][i / 4] << 16);
         const uint32_t both = __shfl_sync(0xffffffffu, mine, i & 3, 4);
-        const uint32_t zm = (uint32_t)B.z[0][i / 4] | ((uint32_t)B.z[1][i / 4] << 8);
-        const uint32_t zb = __shfl_sync(0xffffffffu, zm, i & 3, 4);
-        const uint32_t z0 = O::kMagic + (zb & 15u) * 0x10001u, z1 = O::kMagic + ((zb >> 8) & 15u) * 0x10001u;
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t z0 = O::kMagic + 0x00080008u, z1 = z0;
+        if (Z) {
+            const uint32_t zm = (uint32_t)B.z[0][i / 4] | ((uint32_t)B.z[1][i / 4] << 8);
+            const uint32_t zb = __shfl_sync(0xffffffffu, zm, i & 3, 4);
+            z0 = O::kMagic + (zb & 15u) * 0x10001u, z1 = O::kMagic + ((zb >> 8) & 15u) * 0x10001u;
+        }
+        float c[4];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const uint4 x = xrow != nullptr ? xrow[((c0 + i) * V + j) * 4] : make_uint4(0u, 0u, 0u, 0u);
+            const uint4 x = xrow[((c0 + i) * V + j) * 4];
             const uint32_t w0 = B.w[0][i][j], w1 = B.w[1][i][j];
             uint32_t e[2][4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                e[0][k] = O::sub(((w0 >> (4 * k)) & 0x000f000fu) | O::kMagic, z0);
-                e[1][k] = O::sub(((w1 >> (4 * k)) & 0x000f000fu) | O::kMagic, z1);
+                e[0][k] = O::sub(and_or(w0 >> (4 * k), 0x000f000fu, O::kMagic), z0);
+                e[1][k] = O::sub(and_or(w1 >> (4 * k), 0x000f000fu, O::kMagic), z1);
             }
             const uint32_t a0[4] = {e[0][0], e[1][0], e[0][1], e[1][1]}, a1[4] = {e[0][2], e[1][2], e[0][3], e[1][3]};
-            O::run(c, a0, x.x, x.y);
+            if (j == 0) O::first(c, a0, x.x, x.y);
+            else O::run(c, a0, x.x, x.y);
             O::run(c, a1, x.z, x.w);
         }
         const float2 s = DTypeOps<DT>::unpack(both);
@@ -248,7 +266,7 @@ __device__ void build_rows(const W4Params& p, uint4* xs, float* rscale, Pre pre)
     __syncthreads();
 }
 
-template <int DT, bool DUAL, int V>
+template <int DT, bool DUAL, int V, bool Z>
 __global__ void __launch_bounds__(kThreads, 2) fl_w4_rows_kernel(const __grid_constant__ W4Params p) {
     using Ops = DTypeOps<DT>;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -276,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 2) fl_w4_rows_kernel(const __grid_co
     }
     griddep_wait();
     Block<V> A, B;
-    auto pre = [&] { load_block<V>(A, rows, s0, s1, t); };
+    auto pre = [&] { load_block<V, Z>(A, rows, s0, s1, t); };
     if (p.gamma != nullptr) {
         if (p.M <= 2) build_rows<DT, true, 2, V>(p, xs, rscale, pre);
         else if (p.M <= 4) build_rows<DT, true, 4, V>(p, xs, rscale, pre);
@@ -287,7 +305,8 @@ __global__ void __launch_bounds__(kThreads, 2) fl_w4_rows_kernel(const __grid_co
         else build_rows<DT, false, 8, V>(p, xs, rscale, pre);
     }
     griddep_launch_dependents();
-    const uint4* xrow = g < p.M ? xs + g * row_vecs(p.K) + t : nullptr;
+    // (a column of the MMA past the last row is not used: any row will do)
+    const uint4* xrow = xs + (g < p.M ? g : 0) * row_vecs(p.K) + t;
 
     int q = 0, buf = 0;
     for (int u = blockIdx.x; u < units; u += gridDim.x, buf ^= 1) {
@@ -297,47 +316,37 @@ __global__ void __launch_bounds__(kThreads, 2) fl_w4_rows_kernel(const __grid_co
             const int nb = last ? 0 : b + 1;
             if (last && more) rows = rows_of<DUAL>(p, u + gridDim.x, g, groups);
             if ((q & 1) == 0) {
-                if (more) load_block<V>(B, rows, s0 + nb * U, s1, t);
-                mma_block<DT, V>(A, xrow, s0 + b * U, s1, t, acc);
+                if (more) load_block<V, Z>(B, rows, s0 + nb * U, s1, t);
+                mma_block<DT, V, Z>(A, xrow, s0 + b * U, s1, t, acc);
             } else {
-                if (more) load_block<V>(A, rows, s0 + nb * U, s1, t);
-                mma_block<DT, V>(B, xrow, s0 + b * U, s1, t, acc);
+                if (more) load_block<V, Z>(A, rows, s0 + nb * U, s1, t);
+                mma_block<DT, V, Z>(B, xrow, s0 + b * U, s1, t, acc);
             }
         }
         red[buf][warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
         __syncthreads();
-        // lane (g, t) of the sums: weight rows g and g + 8 (gate and up), activation rows 2 t and 2 t + 1
-        if (warp == 0) {
-            float4 v = red[buf][0][lane];
+        // One thread per output: lane (g, t) of the sums holds weight rows g and
+        // g + 8 (gate and up) and activation rows 2 t and 2 t + 1.
+        if (threadIdx.x < (DUAL ? 8 : 16) * p.M) {
+            const int m = threadIdx.x / (DUAL ? 8 : 16), r = threadIdx.x % (DUAL ? 8 : 16);
+            const float* src = &red[buf][0][(r & 7) * 4 + (m >> 1)].x + (m & 1) + (r >> 3) * 2;
+            const float rs = rscale[m];
+            float y = src[0], up = DUAL ? src[2] : 0.f;
 #pragma unroll
             for (int w = 1; w < kWarps; ++w) {
-                const float4 o = red[buf][w][lane];
-                v.x += o.x;
-                v.y += o.y;
-                v.z += o.z;
-                v.w += o.w;
+                y += src[w * 128];
+                if (DUAL) up += src[w * 128 + 2];
             }
-            const float sum[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int m = 2 * t + e;
-                if (m >= p.M) continue;
-                const float rs = rscale[m];
-                if constexpr (DUAL) {
-                    const float h = act_apply(ACT_SILU, sum[e] * rs) * (sum[2 + e] * rs);
-                    p.out[(size_t)m * p.N + u * 8 + g] = (uint16_t)(Ops::pack(h, 0.f) & 0xffffu);
-                } else {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int n = u * 16 + h * 8 + g;
-                        if (n >= p.N) continue;
-                        float y = sum[2 * h + e] * rs;
-                        if (p.bias != nullptr) y += Ops::unpack(p.bias[n]).x;
-                        y = act_apply(p.act, y);
-                        if (p.residual != nullptr) y += Ops::unpack(p.residual[(size_t)m * p.N + n]).x;
-                        p.out[(size_t)m * p.N + n] = (uint16_t)(Ops::pack(y, 0.f) & 0xffffu);
-                    }
-                }
+            const int n = DUAL ? u * 8 + r : u * 16 + r;
+            const size_t at = (size_t)m * p.N + n;
+            if constexpr (DUAL) {
+                p.out[at] = (uint16_t)(Ops::pack(act_apply(ACT_SILU, y * rs) * (up * rs), 0.f) & 0xffffu);
+            } else if (n < p.N) {
+                y *= rs;
+                if (p.bias != nullptr) y += Ops::unpack(p.bias[n]).x;
+                y = act_apply(p.act, y);
+                if (p.residual != nullptr) y += Ops::unpack(p.residual[at]).x;
+                p.out[at] = (uint16_t)(Ops::pack(y, 0.f) & 0xffffu);
             }
         }
         // (red is double-buffered: the next unit writes the other half, and the
@@ -345,9 +354,9 @@ __global__ void __launch_bounds__(kThreads, 2) fl_w4_rows_kernel(const __grid_co
     }
 }
 
-template <int DT, bool DUAL, int V>
+template <int DT, bool DUAL, int V, bool Z>
 cudaError_t launch_rows(const W4Params& p, const host::LaunchContext& ctx, cudaStream_t stream) {
-    auto kern = fl_w4_rows_kernel<DT, DUAL, V>;
+    auto kern = fl_w4_rows_kernel<DT, DUAL, V, Z>;
     static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (attr != cudaSuccess) return attr;
     const int smem = smem_bytes(p.M, p.K), units = DUAL ? p.N / 8 : (p.N + 15) / 16;
@@ -361,8 +370,10 @@ bool w4_few_rows(int M, int K) { return M <= 8 && smem_bytes(M, K) <= kSmemMax; 
 
 fl_status w4_rows(int dt, bool dual, const W4Params& p, const host::LaunchContext& ctx, cudaStream_t stream) {
     cudaError_t e = cudaErrorInvalidValue;
-#define FL_CASE(DT, DUAL, V) \
-    if (dt == DT && dual == DUAL && p.group == 32 * V) e = launch_rows<DT, DUAL, V>(p, ctx, stream);
+#define FL_CASE(DT, DUAL, V)                                             \
+    if (dt == DT && dual == DUAL && p.group == 32 * V)                   \
+        e = p.zeros[0] != nullptr ? launch_rows<DT, DUAL, V, true>(p, ctx, stream) \
+                                  : launch_rows<DT, DUAL, V, false>(p, ctx, stream);
     FL_CASE(0, false, 1) FL_CASE(0, false, 2) FL_CASE(0, false, 4) FL_CASE(0, true, 1) FL_CASE(0, true, 2) FL_CASE(0, true, 4)
     FL_CASE(1, false, 1) FL_CASE(1, false, 2) FL_CASE(1, false, 4) FL_CASE(1, true, 1) FL_CASE(1, true, 2) FL_CASE(1, true, 4)
 #undef FL_CASE

@@ -104,7 +104,7 @@ __device__ __forceinline__ void dequant8(uint32_t w, uint32_t s2, uint32_t zc, u
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t pair = __byte_perm(w, v, (uint32_t)(i * 0x1111 + 0x4400));  // bytes w.i, w.i, v.i, v.i
-        out[i] = DTypeOps<DT>::mul2(hfma2<DT>((pair & 0x0078000fu) | kMagic, kUnit, zc), s2);
+        out[i] = DTypeOps<DT>::mul2(hfma2<DT>(and_or(pair, 0x0078000fu, kMagic), kUnit, zc), s2);
     }
 }
 
