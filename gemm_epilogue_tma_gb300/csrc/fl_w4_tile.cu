@@ -120,6 +120,35 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     return v;
 }
 
+// One K step, by a whole converged warp: four MMAs (A in tensor memory, 8
+// columns each; B 32 bytes further along its swizzled rows) and the commit that
+// frees the step's stage, issued by one elected lane. Operands computed by the
+// converged warp stay in uniform registers, where the instructions take them
+// from; under a divergent `lane == 0` each MMA waits for its operands to be moved there.
+__device__ __forceinline__ void mma_step(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 r, a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+        "elect.sync r|p, 0xffffffff;\n\t"
+        "setp.ne.b32 q, %4, 0;\n\t"
+        "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
+        "add.u64 b1, %2, 2;\n\tadd.u64 b2, %2, 4;\n\tadd.u64 b3, %2, 6;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, q;\n\t"
+        "setp.eq.u32 q, 0, 0;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, q;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, q;\n\t"
+        "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void commit_elected(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b32 r;\n\telect.sync r|p, 0xffffffff;\n\t"
+        "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
+}
+
 template <int DT, bool DUAL>
 __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_constant__ TileParams p) {
     using Ops = DTypeOps<DT>;
@@ -257,30 +286,21 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
                 wait_bar_drain(wfull((issued - i) % nw), (uint32_t)(((issued - i) / nw) & 1), 20000000ull);
         }
     } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            const uint32_t idesc = umma_idesc_f16(Ops::kFormat, 128, (uint32_t)p.bt);
-            bool ok = true;
-            uint32_t ph = 0, acc = 0;
-            for (int kb = 0, s = 0; kb < nk; ++kb) {
-                ok = wait_bar(full(s), ph, p.status, p.timeout_ns, 22);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t db = sw128_kmajor_desc(sbase + s * p.b_bytes);
-                const uint32_t ta = tmem + kACol + 32u * s;
-#pragma unroll
-                for (int kk = 0; kk < kStep / 16; ++kk) {
-                    umma_f16_ts(tmem, ta + 8u * kk, db + 2 * kk, idesc, acc);
-                    acc = 1;
-                }
-                umma_commit(empty(s));
-                if (++s == nb) s = 0, ph ^= 1u;
-            }
-            if (ok) umma_commit(dfull);
-            // all MMAs issued by this thread complete before tensor memory is released
-            umma_commit(drain);
-            wait_bar_drain(drain, 0, 20000000ull);
+        // ------------------------------------------------------------ MMA issuer (the whole warp, converged)
+        const uint32_t idesc = umma_idesc_f16(Ops::kFormat, 128, (uint32_t)p.bt);
+        bool ok = true;
+        uint32_t ph = 0;
+        for (int kb = 0, s = 0; kb < nk; ++kb) {
+            ok = __all_sync(0xffffffffu, wait_bar(full(s), ph, p.status, p.timeout_ns, 22));
+            if (!ok) break;
+            tc_fence_after();
+            mma_step(tmem, tmem + kACol + 32u * s, sw128_kmajor_desc(sbase + s * p.b_bytes), idesc, kb, empty(s));
+            if (++s == nb) s = 0, ph ^= 1u;
         }
+        if (ok) commit_elected(dfull);
+        // all MMAs issued by this warp complete before tensor memory is released
+        commit_elected(drain);
+        wait_bar_drain(drain, 0, 20000000ull);
     } else if (warp < 4) {
         // ------------------------------------------------------------ scales and zero points of the later stages
         for (int i = 1; i < s_count; ++i) {
