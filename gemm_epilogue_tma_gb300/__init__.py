@@ -392,116 +392,40 @@ def swiglu_ffn_noalloc(x, gamma, Wg, Wu, Wd, bias_down=None, out=None, eps=1e-6,
 # ---------------------------------------------------------------------------
 # serving operators: 4-bit weights, rotary positions, the quantised cache
 # ---------------------------------------------------------------------------
-# A decode step issues these calls back to back, so their host side is kept near
-# the launch's own time: one quick test per tensor, and the checks that say what
-# is wrong only where it fails.
-def _fits(t, dtype, here):
-    return t is None or (t.dtype is dtype and t.get_device() == here and t.is_contiguous())
+_ops = None
 
 
-def _here():
-    from torch import _C
-    return _C._cuda_getDevice()
+def ops():
+    """The extension module that passes torch tensors to the operators below (raises if it has not been built)."""
+    global _ops
+    if _ops is None:
+        import torch  # noqa: F401  (its libraries are loaded first)
+        lib()
+        try:
+            from . import _torch_binding
+        except ImportError as e:
+            raise ImportError(f"gemm_epilogue_tma_gb300/_torch_binding.so cannot be loaded ({e}): build it with "
+                              "`python -m gemm_epilogue_tma_gb300._build`") from e
+        _torch_binding.set_error(FusedLinError)
+        _ops = _torch_binding
+    return _ops
 
 
-def _check_call(**tensors):
-    """Every tensor given is on the current CUDA device (the one whose stream the call is issued on)."""
-    here = _here()
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if t.device.index != here:
-            raise ValueError(f"{name} is on device {t.device.index}, the current device is {here}")
-
-
-def _check_shape(name, t, shape):
-    if t is not None and t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-
-
-def _check_kind(name, t, dtype, contiguous=True):
-    if t is None:
-        return
-    if t.dtype != dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous (row-major)")
-
-
-def _explain(dtype, **tensors):
-    """Raises what is wrong with the tensors (of `dtype`, contiguous, on the current device)."""
-    _check_call(**tensors)
-    for name, t in tensors.items():
-        _check_kind(name, t, dtype)
-
-
-def _made(stream, *tensors):
-    """Tensors a call made for itself and used on `stream`: not reused for another stream's work before it is done."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _on(stream, *made):
+    """Tensors that a call made for itself and used on `stream` are not reused by another stream before it is done."""
+    for t in made:
+        if t is not None:
+            t.record_stream(stream)
 
 
 def w4_quantize(W, group=128, q=None, scales=None, stream=None):
     """Symmetric round-to-nearest 4-bit quantisation of W [N, K]: returns (q, scales), codes [N, K / 2] uint8 (two
     along K to a byte, the even k in the low half, 8 standing for zero) and one scale of W's dtype per `group` k."""
-    import torch
-    N, K = W.shape
-    if group not in (32, 64, 128) or K % group:
-        raise ValueError(f"group must be 32, 64 or 128 and divide K (group {group}, K {K})")
-    new_q, new_s = q is None, scales is None
-    if new_q:
-        q = torch.empty((N, K // 2), dtype=torch.uint8, device=W.device)
-    if new_s:
-        scales = torch.empty((N, K // group), dtype=W.dtype, device=W.device)
-    here = _here()
-    if not (_fits(W, W.dtype, here) and _fits(scales, W.dtype, here) and _fits(q, torch.uint8, here)):
-        _explain(W.dtype, W=W, scales=scales)
-        _explain(torch.uint8, q=q)
-    _check_shape("q", q, (N, K // 2))
-    _check_shape("scales", scales, (N, K // group))
-    _check(lib().fl_w4_quantize(W.data_ptr(), q.data_ptr(), scales.data_ptr(), N, K, group, _dtype_code(W),
-                                _stream(stream)))
-    _made(stream, q if new_q else None, scales if new_s else None)
-    return q, scales
-
-
-def _w4_weight(name, dtype, K, here, q, scales, zeros=None):
-    """The C description of a 4-bit weight, and its row count."""
-    import torch
-    if q.dim() != 2 or q.shape[1] * 2 != K:
-        raise ValueError(f"{name}: q has shape {tuple(q.shape)}, expected [N, {K // 2}]")
-    N = q.shape[0]
-    if scales.dim() != 2 or scales.shape[0] != N or scales.shape[1] < 1 or K % scales.shape[1]:
-        raise ValueError(f"{name}: scales has shape {tuple(scales.shape)}, expected [{N}, K / group]")
-    if not (_fits(q, torch.uint8, here) and _fits(scales, dtype, here) and _fits(zeros, torch.uint8, here)):
-        _explain(torch.uint8, **{f"{name}: q": q, f"{name}: zeros": zeros})
-        _explain(dtype, **{f"{name}: scales": scales})
-    if zeros is not None:
-        _check_shape(f"{name}: zeros", zeros, scales.shape)
-    return W4Weight(q.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(),
-                    K // scales.shape[1]), N
-
-
-def _workspace(workspace, need, like):
-    """(address or None, bytes, the tensor if it was made here)."""
-    import torch
-    if workspace is not None:
-        _check_call(workspace=workspace)
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous CUDA tensor")
-        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), None
-    if need == 0:
-        return None, 0, None
-    made = torch.empty(need, dtype=torch.uint8, device=like.device)
-    return made.data_ptr(), need, made
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
+    if stream is None:
+        return (_ops or ops()).w4_quantize(W, group, q, scales, None)
+    r = ops().w4_quantize(W, group, q, scales, stream.cuda_stream)
+    _on(stream, None if q is not None else r[0], None if scales is not None else r[1])
+    return r
 
 
 def w4_gemm_workspace_size(M: int, K: int, norm: bool) -> int:
@@ -514,27 +438,11 @@ def w4_gemm(x, q, scales, zeros=None, gamma=None, bias=None, residual=None, out=
     zeros[n, k / group]); norm is RMSNorm with `gamma`, or none. q, scales: as w4_quantize returns them; zeros
     [N, K / group] uint8 (8 everywhere if None). The workspace (w4_gemm_workspace_size bytes) must not be
     shared by calls or captured graphs that may overlap on the GPU."""
-    import torch
-    M, K = x.shape
-    dt, here = x.dtype, _here()
-    W, N = _w4_weight("W", dt, K, here, q, scales, zeros)
-    new = out is None
-    if new:
-        out = torch.empty((M, N), dtype=dt, device=x.device)
-    if not (_fits(x, dt, here) and _fits(gamma, dt, here) and _fits(bias, dt, here) and _fits(residual, dt, here)
-            and _fits(out, dt, here)):
-        _explain(dt, x=x, gamma=gamma, bias=bias, residual=residual, out=out)
-    _check_shape("gamma", gamma, (K,))
-    _check_shape("bias", bias, (N,))
-    _check_shape("residual", residual, (M, N))
-    _check_shape("out", out, (M, N))
-    L = lib()
-    ws, size, own = _workspace(workspace, L.fl_w4_gemm_workspace_size(M, K, gamma is not None), x)
-    _check(L.fl_w4_gemm(x.data_ptr(), _addr(gamma), ctypes.byref(W), _addr(bias), _addr(residual), out.data_ptr(), M, N,
-                        K, eps, ACTS[act], ws, size, _dtype_code(x), _stream(stream)))
-    if stream is not None:
-        _made(stream, own, out if new else None)
-    return out
+    if stream is None:
+        return (_ops or ops()).w4_gemm(x, q, scales, zeros, gamma, bias, residual, out, eps, ACTS[act], workspace, None)[0]
+    r, ws = ops().w4_gemm(x, q, scales, zeros, gamma, bias, residual, out, eps, ACTS[act], workspace, stream.cuda_stream)
+    _on(stream, ws, None if out is not None else r)
+    return r
 
 
 def w4_swiglu_ffn_workspace_size(M: int, D: int, F: int) -> int:
@@ -543,62 +451,11 @@ def w4_swiglu_ffn_workspace_size(M: int, D: int, F: int) -> int:
 
 def w4_swiglu_ffn(x, gamma, Wg, Wu, Wd, bias_down=None, out=None, eps=1e-6, workspace=None, stream=None):
     """swiglu_ffn on 4-bit weights, each a tuple (q, scales) or (q, scales, zeros)."""
-    import torch
-    M, D = x.shape
-    dt, here = x.dtype, _here()
-    F = Wg[0].shape[0]
-    g, _ = _w4_weight("Wg", dt, D, here, *Wg)
-    u, n = _w4_weight("Wu", dt, D, here, *Wu)
-    d, m = _w4_weight("Wd", dt, F, here, *Wd)
-    if n != F or m != D:
-        raise ValueError(f"Wu has {n} rows, expected {F}; Wd has {m}, expected {D}")
-    new = out is None
-    if new:
-        out = torch.empty((M, D), dtype=dt, device=x.device)
-    if not (_fits(x, dt, here) and _fits(gamma, dt, here) and _fits(bias_down, dt, here) and _fits(out, dt, here)):
-        _explain(dt, x=x, gamma=gamma, bias_down=bias_down, out=out)
-    _check_shape("gamma", gamma, (D,))
-    _check_shape("bias_down", bias_down, (D,))
-    _check_shape("out", out, (M, D))
-    L = lib()
-    ws, size, own = _workspace(workspace, L.fl_w4_swiglu_ffn_workspace_size(M, D, F), x)
-    _check(L.fl_w4_swiglu_ffn(x.data_ptr(), gamma.data_ptr(), ctypes.byref(g), ctypes.byref(u), ctypes.byref(d),
-                              _addr(bias_down), out.data_ptr(), M, D, F, eps, ws, size, _dtype_code(x),
-                              _stream(stream)))
-    if stream is not None:
-        _made(stream, own, out if new else None)
-    return out
-
-
-def _heads(name, t, dtype, here):
-    """Checks a [rows, heads, head_dim] view: dtype, device, contiguous channels. Returns its shape and its row and
-    head strides; of an axis of one, the stride it would have if dense."""
-    if t.dim() != 3:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [rows, heads, head_dim]")
-    if t.dtype is not dtype or t.get_device() != here:
-        _check_call(**{name: t})
-        _check_kind(name, t, dtype, contiguous=False)
-    shape = t.shape
-    rows, heads, dim = shape
-    row, head, unit = t.stride()
-    if unit != 1 and dim > 1:
-        raise ValueError(f"{name}: the channels of a head must be contiguous")
-    if heads == 1:
-        head = dim
-    return shape, (row if rows != 1 else heads * head), head
-
-
-def _rope_axes(pairs, axes, sections):
-    """The axis of each pair, as the bytes fl_rope takes (None: axis 0 for all)."""
-    if axes > 4:
-        raise ValueError(f"1..4 axes, got {axes}")
-    if sections is None:
-        if axes != 1:
-            raise ValueError(f"positions has {axes} axes: sections must say which pairs follow which")
-        return None
-    if len(sections) != axes or sum(sections) != pairs or min(sections) < 0:
-        raise ValueError(f"sections {tuple(sections)} must give the {pairs} pairs to the {axes} axes")
-    return b"".join([bytes((a,)) * n for a, n in enumerate(sections)]) if axes > 1 else None
+    if stream is None:
+        return (_ops or ops()).w4_swiglu_ffn(x, gamma, Wg, Wu, Wd, bias_down, out, eps, workspace, None)[0]
+    r, ws = ops().w4_swiglu_ffn(x, gamma, Wg, Wu, Wd, bias_down, out, eps, workspace, stream.cuda_stream)
+    _on(stream, ws, None if out is not None else r)
+    return r
 
 
 def rope(q, k, positions, inv_freq, sections=None, interleaved=False, inverse=False, out_q=None, out_k=None,
@@ -610,97 +467,11 @@ def rope(q, k, positions, inv_freq, sections=None, interleaved=False, inverse=Fa
     `sections` saying how many consecutive pairs follow each axis. inverse turns back: the gradient with respect to
     the input. q, k and the outputs may be strided views with contiguous channels (column ranges of a stacked
     projection's output); an output may be its input itself."""
-    import torch
-    dt, here = q.dtype, _here()
-    shape, q_row, q_head = _heads("q", q, dt, here)
-    rows, heads_q, D = shape
-    if positions.dim() == 2:
-        axes, stride = positions.shape[0], positions.stride(0)
-    else:
-        axes, stride = 1, rows
-    if not (positions.dtype is torch.int32 and positions.get_device() == here and positions.shape[-1] == rows
-            and positions.dim() <= 2 and (rows <= 1 or positions.stride(-1) == 1)):
-        _check_call(positions=positions)
-        _check_kind("positions", positions, torch.int32, contiguous=False)
-        _check_shape("positions", positions, (axes, rows) if positions.dim() == 2 else (rows,))
-        raise ValueError("positions must be contiguous along the rows")
-    if not _fits(inv_freq, torch.float32, here) or inv_freq.dim() != 1:
-        _explain(torch.float32, inv_freq=inv_freq)
-        raise ValueError(f"inv_freq has shape {tuple(inv_freq.shape)}, expected [R / 2]")
-    pairs = inv_freq.shape[0]
-    axis_of = _rope_axes(pairs, axes, sections)
-    new_q, new_k = out_q is None, k is not None and out_k is None
-    if new_q:
-        out_q = torch.empty(shape, dtype=dt, device=q.device)
-        o_row, o_head = heads_q * D, D
-    else:
-        o_shape, o_row, o_head = _heads("out_q", out_q, dt, here)
-        _check_shape("out_q", out_q, shape)
-    heads_k = k_addr = ko_addr = k_row = k_head = ko_row = ko_head = 0
-    if k is None:
-        if out_k is not None:
-            raise ValueError("out_k without k")
-    else:
-        k_shape, k_row, k_head = _heads("k", k, dt, here)
-        heads_k = k_shape[1]
-        _check_shape("k", k, (rows, heads_k, D))
-        if new_k:
-            out_k = torch.empty(k_shape, dtype=dt, device=k.device)
-            ko_row, ko_head = heads_k * D, D
-        else:
-            o_shape, ko_row, ko_head = _heads("out_k", out_k, dt, here)
-            _check_shape("out_k", out_k, k_shape)
-        k_addr, ko_addr = k.data_ptr(), out_k.data_ptr()
-    desc = RopeDesc(_dtype_code(q), rows, heads_q, heads_k, D, 2 * pairs, axes, bool(interleaved), bool(inverse), axis_of,
-                    positions.data_ptr(), stride, inv_freq.data_ptr(), q.data_ptr(), k_addr, out_q.data_ptr(), ko_addr,
-                    q_row, q_head, k_row, k_head, o_row, o_head, ko_row, ko_head)
-    _check(lib().fl_rope(ctypes.byref(desc), _stream(stream)))
-    if stream is not None:
-        _made(stream, out_q if new_q else None, out_k if new_k else None)
-    return out_q, out_k
-
-
-def _kv_desc(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_rows, start):
-    import torch
-    here = _here()
-    kind = k_cache.dtype
-    if kind is not torch.int8 and kind is not torch.float8_e4m3fn:
-        raise TypeError(f"k_cache has dtype {kind}, expected int8 or float8_e4m3fn")
-    shape = k_cache.shape
-    if len(shape) != 4:
-        raise ValueError(f"k_cache has shape {tuple(shape)}, expected [pages, page_size, heads, head_dim]")
-    pages, size, heads, dim = shape
-    f32, i32 = torch.float32, torch.int32
-    if not (_fits(k_cache, kind, here) and _fits(v_cache, kind, here) and _fits(k_scale, f32, here)
-            and _fits(v_scale, f32, here) and _fits(cu_rows, i32, here) and _fits(start, i32, here)):
-        _explain(kind, k_cache=k_cache, v_cache=v_cache)
-        _explain(f32, k_scale=k_scale, v_scale=v_scale)
-        _explain(i32, cu_rows=cu_rows, start=start)
-    if v_cache.shape != shape or k_scale.shape != shape[:3] or v_scale.shape != shape[:3]:
-        _check_shape("v_cache", v_cache, shape)
-        _check_shape("k_scale", k_scale, shape[:3])
-        _check_shape("v_scale", v_scale, shape[:3])
-    dt = k.dtype
-    k_shape, k_row, k_head = _heads("k", k, dt, here)
-    v_shape, v_row, v_head = _heads("v", v, dt, here)
-    rows = k_shape[0]
-    if k_shape != (rows, heads, dim) or v_shape != k_shape:
-        _check_shape("k", k, (rows, heads, dim))
-        _check_shape("v", v, (rows, heads, dim))
-    if page_table.dim() != 2:
-        raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected [sequences, pages]")
-    seqs, per = page_table.shape
-    stride, unit = page_table.stride()
-    if page_table.dtype is not i32 or page_table.get_device() != here or (unit != 1 and per > 1):
-        _check_call(page_table=page_table)
-        _check_kind("page_table", page_table, i32, contiguous=False)
-        raise ValueError("page_table must be contiguous along a sequence's pages")
-    _check_shape("cu_rows", cu_rows, (seqs + 1,))
-    _check_shape("start", start, (seqs,))
-    return KvDesc(_dtype_code(k), 0 if kind is torch.int8 else 1, rows, heads, dim, size, pages, seqs, per,
-                  stride if seqs > 1 else per, page_table.data_ptr(), _addr(cu_rows), _addr(start), k.data_ptr(),
-                  v.data_ptr(), k_row, k_head, v_row, v_head, k_cache.data_ptr(), v_cache.data_ptr(),
-                  k_scale.data_ptr(), v_scale.data_ptr())
+    if stream is None:
+        return (_ops or ops()).rope(q, k, positions, inv_freq, sections, interleaved, inverse, out_q, out_k, None)
+    r = ops().rope(q, k, positions, inv_freq, sections, interleaved, inverse, out_q, out_k, stream.cuda_stream)
+    _on(stream, None if out_q is not None else r[0], None if out_k is not None else r[1])
+    return r
 
 
 def kv_write(k, v, k_cache, v_cache, k_scale, v_scale, page_table, start, cu_rows=None, stream=None):
@@ -713,8 +484,8 @@ def kv_write(k, v, k_cache, v_cache, k_scale, v_scale, page_table, start, cu_row
     No two rows of a call may have the same place in the cache."""
     if start is None:
         raise ValueError("start must be given")
-    desc = _kv_desc(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_rows, start)
-    _check(lib().fl_kv_write(ctypes.byref(desc), _stream(stream)))
+    (_ops or ops()).kv_write(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_rows, start,
+                             None if stream is None else stream.cuda_stream)
 
 
 def kv_read(k_cache, v_cache, k_scale, v_scale, page_table, cu_rows, start=None, out_k=None, out_v=None, stream=None):
@@ -724,8 +495,8 @@ def kv_read(k_cache, v_cache, k_scale, v_scale, page_table, cu_rows, start=None,
     Returns (out_k, out_v)."""
     if out_k is None or out_v is None:
         raise ValueError("out_k and out_v must be given: the row count is not known on the host")
-    desc = _kv_desc(out_k, out_v, k_cache, v_cache, k_scale, v_scale, page_table, cu_rows, start)
-    _check(lib().fl_kv_read(ctypes.byref(desc), _stream(stream)))
+    (_ops or ops()).kv_read(out_k, out_v, k_cache, v_cache, k_scale, v_scale, page_table, cu_rows, start,
+                            None if stream is None else stream.cuda_stream)
     return out_k, out_v
 
 

@@ -3,7 +3,9 @@
 Each translation unit under csrc/ compiles to an object in parallel; the
 objects link into gemm_epilogue_tma_gb300/libfusedlin.so (CUDA runtime linked
 statically, the driver reached through the runtime's entry-point query, so
-the library loads on a machine without a GPU).
+the library loads on a machine without a GPU). binding/fl_torch.cpp, the
+extension module that passes torch tensors to the serving operators, compiles
+beside them with the host compiler into _torch_binding.so.
 
     python -m gemm_epilogue_tma_gb300._build [--force] [--verbose-ptxas]
 """
@@ -23,6 +25,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfusedlin.so")
+BINDING_SRC = os.path.join(PKG, "binding", "fl_torch.cpp")
+BINDING = os.path.join(PKG, "_torch_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -67,6 +71,39 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
+def _run(what: str, cmd) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_binding() -> str:
+    obj = os.path.join(BUILD, "fl_torch.o")
+    if not _stale(obj, [BINDING_SRC] + _headers()):
+        return obj
+    import sysconfig
+
+    import torch
+    root = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    _run("the binding's compilation",
+         [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", root,
+          "-I", os.path.join(root, "torch", "csrc", "api", "include"), "-I", os.path.join(cuda, "include"),
+          "-I", sysconfig.get_paths()["include"], "-c", BINDING_SRC, "-o", obj])
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    tmp = BINDING + ".tmp"
+    _run("the binding's link",
+         [shutil.which("g++") or "g++", "-shared", "-o", tmp, obj, "-L", PKG, "-lfusedlin", "-Wl,-rpath,$ORIGIN",
+          "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch", "-ltorch_cuda",
+          "-ltorch_cpu", "-lc10_cuda", "-lc10"])
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = None) -> str:
     """Compile csrc/*.cu and link libfusedlin.so; returns the library path."""
     os.makedirs(BUILD, exist_ok=True)
@@ -74,17 +111,16 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
     if force:
         for o in glob.glob(os.path.join(BUILD, "*.o")):
             os.remove(o)
-    if not force and not _stale(LIB, srcs + _headers()):
+    if not force and not _stale(LIB, srcs + _headers()) and not _stale(BINDING, [BINDING_SRC, LIB]):
         return LIB
-    jobs = jobs or min(len(srcs), os.cpu_count() or 4)
+    jobs = jobs or min(len(srcs) + 1, os.cpu_count() or 4)
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
-    tmp = LIB + ".tmp"
-    cmd = [nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
+        tmp = LIB + ".tmp"
+        _run("link", [nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *objs])
+        os.replace(tmp, LIB)
+        _link_binding(binding.result())
     return LIB
 
 
