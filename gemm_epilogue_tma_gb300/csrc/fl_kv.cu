@@ -1,19 +1,20 @@
 // Paged 8-bit key/value cache: k and v rows quantised as they are written, and
 // read back (fl_kv_write, fl_kv_read).
 //
-//   scale = max(amax / top, 2^-126), code = x / scale rounded to the format
+//   scale = max(amax * (1 / top), 2^-126), code = x / scale rounded to the format
 //   x'    = scale * code
 //
 // with amax over the head_dim channels of one head's row and top = 127 (int8)
 // or 448 (e4m3). Both kernels are bound by HBM: 3 bytes per channel (2 of the
 // 16-bit side, 1 of the cache) and 4 per head's row.
 //
-// A head's row is handled by the smallest power-of-two group of lanes that
-// holds it in 16-byte vectors (16 lanes at head_dim 128), so amax is a
-// butterfly over the group. One warp takes a row of k or of v (or kVecs
-// vectors per lane of it) at a time; its 16-bit vectors are requested before
-// the row's sequence and page are looked up, so a decode step pays for the
-// look-up's dependent loads and the data once, side by side.
+// A lane takes 16 channels (8 where head_dim is not a multiple of 16), a head's
+// row the smallest power-of-two group of lanes that holds it (8 lanes at
+// head_dim 128), so amax is a butterfly over the group. One warp takes a row of
+// both k and v, four passes of 32 lanes in flight, so that the look-up of the row's sequence
+// and page, a chain of dependent loads, is made once for them; with few rows (a
+// decode step) the passes are spread over more warps. The writing kernel
+// requests its 16-bit vectors before the look-up.
 #include <cuda_fp8.h>
 
 #include "fl_common.cuh"
@@ -25,7 +26,7 @@ namespace fl {
 namespace {
 
 constexpr int kKvThreads = 128;
-constexpr int kVecs = 4;  // 16-byte vectors per lane in flight
+constexpr int kPasses = 4;  // passes of one warp task in flight
 
 struct KvParams {
     const uint16_t* src[2];  // write: k, v
@@ -38,8 +39,11 @@ struct KvParams {
     const int* start;
     long long table_stride;
     int rows, heads, head_dim, page_size, n_pages, n_seqs, table_pages;
-    int lanes;   // lanes of one head's row (power of two)
-    int chunks;  // warp tasks of one row of k (or v)
+    int lanes_log;  // lanes of one head's row: a power of two
+    int half;       // passes of one row of k (or v)
+    int per_task;   // passes of one warp task
+    int tasks_row;  // warp tasks of one row
+    uint32_t tasks;
     int* range;
 };
 
@@ -81,50 +85,93 @@ __device__ __forceinline__ long long find_slot(const KvParams& p, int i, int lan
     return (long long)page * p.page_size + (at - j * (uint32_t)p.page_size);
 }
 
-// int8 code of x: round(x / s) with inv = 1 / s rounded. x * inv is within two
-// units in the last place of the quotient, so only a quotient next to a border
-// between two codes can round to the wrong side: there the sign of
-// x - (border) * s, one FMA, decides, and 0 is a tie, which goes to even.
-__device__ __forceinline__ int code_int8(float x, float s, float inv) {
-    const float y = x * inv;
-    float r = rintf(y);
-    if (fabsf(y - r) > 0.4999f) {
-        const float lo = floorf(y), d = fmaf(-(lo + 0.5f), s, x);
-        r = d > 0.f ? lo + 1.f : d < 0.f ? lo : 2.f * rintf(0.5f * (lo + 0.5f));
-    }
-    return (int)fminf(fmaxf(r, -127.f), 127.f);
+// The quotient x / s of a value next to a border between two codes, to the
+// bit: x * inv, one Newton step, then the sign of the residual, one FMA.
+__device__ __forceinline__ float quotient(float x, float s, float inv, float& residual) {
+    float y = x * inv;
+    y = fmaf(fmaf(-y, s, x), inv, y);
+    residual = fmaf(-y, s, x);
+    return y;
+}
+
+// int8 code next to a border: which side of lo + 1/2 the quotient lies is the
+// sign of x - (lo + 1/2) s, and 0 is a tie, which goes to even.
+__device__ __noinline__ int int8_exact(float x, float s, float inv) {
+    const float lo = floorf(x * inv), d = fmaf(-(lo + 0.5f), s, x);
+    return (int)(d > 0.f ? lo + 1.f : d < 0.f ? lo : 2.f * rintf(0.5f * (lo + 0.5f)));
 }
 
 // x / s with its last bit set when the quotient is not exact (rounding to
-// odd), so that the conversion to e4m3, which keeps 4 of the 24 bits, rounds
-// the exact quotient: x * inv, one Newton step, then the residual's sign.
-__device__ __forceinline__ float odd_quotient(float x, float s, float inv) {
-    float y = x * inv;
-    y = fmaf(fmaf(-y, s, x), inv, y);
-    const float e = fmaf(-y, s, x);
+// odd): the conversion to e4m3, which keeps 4 of the 24 bits, then rounds the
+// exact quotient.
+__device__ __noinline__ float odd_quotient(float x, float s, float inv) {
+    float e;
+    const float y = quotient(x, s, inv, e);
     uint32_t u = __float_as_uint(y);
     if (e != 0.f && (u & 1u) == 0u && (u << 1) != 0u) u += ((__float_as_uint(e) ^ u) >> 31) ? 0xffffffffu : 1u;
     return __uint_as_float(u);
 }
 
+// Codes of 8 values. x * inv is within two units in the last place of the
+// quotient, so a code can only differ from the exact quotient's where x * inv
+// is within a few of a border between two codes: those values (one in about
+// 10^4) are computed again, exactly.
+//   int8: x * inv + 1.5 * 2^23 rounds to an integer, ties to even, in the low
+//   bits of the sum.
+//   e4m3: a border has 0x80000 in the 20 bits below the three that are kept;
+//   below 2^-6, where fewer are kept, every value is computed again.
 template <int DT, int FMT>
-__device__ __forceinline__ uint2 encode8(const uint4& v, float s) {
+__device__ __forceinline__ uint2 encode8(const uint4& v, float s, float inv) {
     using Ops = DTypeOps<DT>;
-    const float inv = 1.0f / s;
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t o[4];
+    float x[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const float2 f = Ops::unpack(w[e]);
-        if constexpr (FMT == FL_KV_INT8) {
-            const int a = code_int8(f.x, s, inv), b = code_int8(f.y, s, inv);
-            o[e] = (a & 0xff) | ((b & 0xff) << 8);
-        } else {
-            o[e] = __nv_cvt_float2_to_fp8x2(make_float2(odd_quotient(f.x, s, inv), odd_quotient(f.y, s, inv)),
-                                            __NV_SATFINITE, __NV_E4M3);
+        x[2 * e] = f.x;
+        x[2 * e + 1] = f.y;
+    }
+    uint32_t o[2];
+    if constexpr (FMT == FL_KV_INT8) {
+        constexpr float kShift = 12582912.0f;  // 1.5 * 2^23
+        uint32_t r[8];
+        float far = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float y = x[e] * inv, t = y + kShift;
+            far = fmaxf(far, fabsf(y - (t - kShift)));
+            r[e] = __float_as_uint(t);
+        }
+        if (far > 0.4999f) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float y = x[e] * inv;
+                if (fabsf(y - rintf(y)) > 0.4999f) r[e] = (uint32_t)int8_exact(x[e], s, inv);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            o[e] = __byte_perm(__byte_perm(r[4 * e], r[4 * e + 1], 0x0040), __byte_perm(r[4 * e + 2], r[4 * e + 3], 0x0040), 0x5410);
+    } else {
+        float y[8];
+        bool near = false;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            y[e] = x[e] * inv;
+            near |= ((__float_as_uint(y[e]) + (0x80000u + 8u)) & 0xfffffu) <= 16u || fabsf(y[e]) < 0x1p-6f;
+        }
+        if (near) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = odd_quotient(x[e], s, inv);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * e], y[4 * e + 1]), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * e + 2], y[4 * e + 3]), __NV_SATFINITE, __NV_E4M3);
+            o[e] = lo | (hi << 16);
         }
     }
-    return make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+    return make_uint2(o[0], o[1]);
 }
 
 template <int DT, int FMT>
@@ -133,12 +180,15 @@ __device__ __forceinline__ uint4 decode8(uint2 c, float s) {
     uint32_t o[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const uint32_t w = ((e < 2 ? c.x : c.y) >> (16 * (e & 1))) & 0xffffu;
+        const uint32_t w = e < 2 ? c.x : c.y;
         float2 f;
         if constexpr (FMT == FL_KV_INT8) {
-            f = make_float2((float)(int8_t)(w & 0xff), (float)(int8_t)(w >> 8));
+            // the byte plus 128 in the mantissa of 2^23
+            const uint32_t b = w ^ 0x80808080u;
+            f.x = __uint_as_float(__byte_perm(b, 0x4b000000u, 0x7440 + 2 * (e & 1))) - 8388736.0f;
+            f.y = __uint_as_float(__byte_perm(b, 0x4b000000u, 0x7441 + 2 * (e & 1))) - 8388736.0f;
         } else {
-            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w, __NV_E4M3);
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * (e & 1))), __NV_E4M3);
             f = __half22float2(*reinterpret_cast<const __half2*>(&h));
         }
         o[e] = Ops::pack(f.x * s, f.y * s);
@@ -146,90 +196,118 @@ __device__ __forceinline__ uint4 decode8(uint2 c, float s) {
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// One warp task: row i of k (which = 0) or v, head rows [h0, h0 + units).
+// A warp task: the passes [p0, p1) of row i; pass p is the p % half-th group of
+// head rows of k (p < half) or v.
 struct Task {
-    int i, which, h0, units;
+    int i, p0, p1;
 };
 __device__ __forceinline__ Task task_of(const KvParams& p, uint32_t t) {
-    const int per = 32 / p.lanes * kVecs;
-    Task k;
-    const uint32_t rest = t / (uint32_t)p.chunks;
-    k.which = (int)(rest & 1u);
-    k.i = (int)(rest >> 1);
-    k.h0 = (int)(t - rest * (uint32_t)p.chunks) * per;
-    k.units = min(per, p.heads - k.h0);
-    return k;
+    const uint32_t row = t / (uint32_t)p.tasks_row;
+    const int p0 = (int)(t - row * (uint32_t)p.tasks_row) * p.per_task;
+    return Task{(int)row, p0, min(p0 + p.per_task, 2 * p.half)};
+}
+// (which, head row) of this lane in pass q
+struct Unit {
+    int which, h;
+    bool in;
+};
+__device__ __forceinline__ Unit unit_of(const KvParams& p, int q, int end, int grp, bool in) {
+    Unit u;
+    u.which = q >= p.half;
+    u.h = ((q - (u.which ? p.half : 0)) << (5 - p.lanes_log)) + grp;
+    u.in = in && q < end && u.h < p.heads;
+    return u;
 }
 
-template <int DT, int FMT>
+// W: 16-byte vectors of 16-bit values per lane (1 or 2).
+template <int DT, int FMT, int W>
 __global__ void __launch_bounds__(kKvThreads) fl_kv_write_kernel(const __grid_constant__ KvParams p) {
     griddep_wait();
     griddep_launch_dependents();
-    const int lane = threadIdx.x & 31, sub = lane & (p.lanes - 1), grp = lane / p.lanes, groups = 32 / p.lanes;
-    const uint32_t tasks = 2u * p.rows * p.chunks, stride = gridDim.x * (kKvThreads / 32);
-    for (uint32_t t = blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5); t < tasks; t += stride) {
-        const Task k = task_of(p, t);
-        const bool in = sub * 8 < p.head_dim;
-        const uint16_t* src = p.src[k.which] + k.i * p.row[k.which] + sub * 8;
-        uint4 v[kVecs];
+    const int lane = threadIdx.x & 31, sub = lane & ((1 << p.lanes_log) - 1), grp = lane >> p.lanes_log;
+    const bool in = sub * (8 * W) < p.head_dim;
+    const uint32_t t = blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5);
+    if (t >= p.tasks) return;
+    const Task k = task_of(p, t);
+    long long slot = 0;
+    for (int q0 = k.p0; q0 < k.p1; q0 += kPasses) {
+        uint4 v[kPasses][W];
 #pragma unroll
-        for (int u = 0; u < kVecs; ++u) {
-            const int h = u * groups + grp;
-            v[u] = in && h < k.units ? ldg_v4(src + (k.h0 + h) * p.head[k.which]) : make_uint4(0u, 0u, 0u, 0u);
+        for (int j = 0; j < kPasses; ++j) {
+            const Unit u = unit_of(p, q0 + j, k.p1, grp, in);
+            const uint16_t* src = p.src[u.which] + k.i * p.row[u.which] + u.h * p.head[u.which] + sub * (8 * W);
+#pragma unroll
+            for (int e = 0; e < W; ++e) v[j][e] = u.in ? ldg_v4(src + 8 * e) : make_uint4(0u, 0u, 0u, 0u);
         }
-        const long long slot = find_slot(p, k.i, lane);
-        if (slot < 0) {
-            if (slot == -2 && lane == 0) atomicCAS(p.range, 0, k.i + 1);
-            continue;
+        if (q0 == k.p0) {
+            slot = find_slot(p, k.i, lane);
+            if (slot < 0) {
+                if (slot == -2 && lane == 0) atomicCAS(p.range, 0, k.i + 1);
+                return;
+            }
         }
 #pragma unroll
-        for (int u = 0; u < kVecs; ++u) {
-            const int h = u * groups + grp;
-            uint32_t m = absmax8<DT>(v[u]);
-            for (int o = p.lanes / 2; o > 0; o >>= 1) m = absmax2<DT>(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (h >= k.units) continue;
+        for (int j = 0; j < kPasses; ++j) {
+            const Unit u = unit_of(p, q0 + j, k.p1, grp, in);
+            uint32_t m = absmax8<DT>(v[j][0]);
+            if (W == 2) m = absmax2<DT>(m, absmax8<DT>(v[j][W - 1]));
+            for (int o = 1 << p.lanes_log >> 1; o > 0; o >>= 1) m = absmax2<DT>(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (!u.in) continue;
             const bool fine = (m & 0xffffu) < Bits16<DT>::kInf;
-            const float top = FMT == FL_KV_INT8 ? 127.0f : 448.0f;
-            const float s = fmaxf(DTypeOps<DT>::unpack(m).x / top, 0x1p-126f);
-            const long long at = slot * p.heads + k.h0 + h;
-            if (sub == 0) p.scale[k.which][at] = fine ? s : __int_as_float(0x7fffffff);
-            if (in)
-                *reinterpret_cast<uint2*>(p.cache[k.which] + at * p.head_dim + sub * 8) =
-                    fine ? encode8<DT, FMT>(v[u], s) : make_uint2(0u, 0u);
+            const float s = fmaxf(DTypeOps<DT>::unpack(m).x * (1.0f / (FMT == FL_KV_INT8 ? 127.0f : 448.0f)), 0x1p-126f);
+            const float inv = __frcp_rn(s);
+            const long long at = slot * p.heads + u.h;
+            if (sub == 0) p.scale[u.which][at] = fine ? s : __int_as_float(0x7fffffff);
+            uint2 c[W];
+#pragma unroll
+            for (int e = 0; e < W; ++e) c[e] = fine ? encode8<DT, FMT>(v[j][e], s, inv) : make_uint2(0u, 0u);
+            uint8_t* dst = p.cache[u.which] + at * p.head_dim + sub * (8 * W);
+            if constexpr (W == 2)
+                *reinterpret_cast<uint4*>(dst) = make_uint4(c[0].x, c[0].y, c[1].x, c[1].y);
+            else
+                *reinterpret_cast<uint2*>(dst) = c[0];
         }
     }
 }
 
-template <int DT, int FMT>
+template <int DT, int FMT, int W>
 __global__ void __launch_bounds__(kKvThreads) fl_kv_read_kernel(const __grid_constant__ KvParams p) {
     griddep_wait();
     griddep_launch_dependents();
-    const int lane = threadIdx.x & 31, sub = lane & (p.lanes - 1), grp = lane / p.lanes, groups = 32 / p.lanes;
-    const uint32_t tasks = 2u * p.rows * p.chunks, stride = gridDim.x * (kKvThreads / 32);
-    for (uint32_t t = blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5); t < tasks; t += stride) {
-        const Task k = task_of(p, t);
-        const long long slot = find_slot(p, k.i, lane);
-        if (slot < 0) {
-            if (slot == -2 && lane == 0) atomicCAS(p.range, 0, k.i + 1);
-            continue;
-        }
-        const bool in = sub * 8 < p.head_dim;
-        uint2 c[kVecs];
-        float s[kVecs];
+    const int lane = threadIdx.x & 31, sub = lane & ((1 << p.lanes_log) - 1), grp = lane >> p.lanes_log;
+    const bool in = sub * (8 * W) < p.head_dim;
+    const uint32_t t = blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5);
+    if (t >= p.tasks) return;
+    const Task k = task_of(p, t);
+    const long long slot = find_slot(p, k.i, lane);
+    if (slot < 0) {
+        if (slot == -2 && lane == 0) atomicCAS(p.range, 0, k.i + 1);
+        return;
+    }
+    for (int q0 = k.p0; q0 < k.p1; q0 += kPasses) {
+        uint2 c[kPasses][W];
+        float s[kPasses];
 #pragma unroll
-        for (int u = 0; u < kVecs; ++u) {
-            const int h = u * groups + grp;
-            if (!in || h >= k.units) continue;
-            const long long at = slot * p.heads + k.h0 + h;
-            c[u] = __ldg(reinterpret_cast<const uint2*>(p.cache[k.which] + at * p.head_dim + sub * 8));
-            s[u] = __ldg(p.scale[k.which] + at);
+        for (int j = 0; j < kPasses; ++j) {
+            const Unit u = unit_of(p, q0 + j, k.p1, grp, in);
+            const long long at = u.in ? slot * p.heads + u.h : 0;
+            const uint8_t* src = p.cache[u.which] + at * p.head_dim + (u.in ? sub * (8 * W) : 0);
+            if constexpr (W == 2) {
+                const uint4 x = ldg_v4(src);
+                c[j][0] = make_uint2(x.x, x.y);
+                c[j][W - 1] = make_uint2(x.z, x.w);
+            } else {
+                c[j][0] = __ldg(reinterpret_cast<const uint2*>(src));
+            }
+            s[j] = __ldg(p.scale[u.which] + at);
         }
-        uint16_t* dst = p.dst[k.which] + k.i * p.row[k.which] + sub * 8;
 #pragma unroll
-        for (int u = 0; u < kVecs; ++u) {
-            const int h = u * groups + grp;
-            if (!in || h >= k.units) continue;
-            *reinterpret_cast<uint4*>(dst + (k.h0 + h) * p.head[k.which]) = decode8<DT, FMT>(c[u], s[u]);
+        for (int j = 0; j < kPasses; ++j) {
+            const Unit u = unit_of(p, q0 + j, k.p1, grp, in);
+            if (!u.in) continue;
+            uint16_t* dst = p.dst[u.which] + k.i * p.row[u.which] + u.h * p.head[u.which] + sub * (8 * W);
+#pragma unroll
+            for (int e = 0; e < W; ++e) *reinterpret_cast<uint4*>(dst + 8 * e) = decode8<DT, FMT>(c[j][e], s[j]);
         }
     }
 }
@@ -310,10 +388,11 @@ fl_status run(const char* what, const fl_kv_desc* d, bool write, cudaStream_t st
             if (host::overlap(all[i].p, all[i].n, all[j].p, all[j].n))
                 return host::fail(FL_ERR_INVALID_ARG, "%s: an output overlaps another tensor of the call", what);
         }
-    int lanes = 1;
-    while (lanes * 8 < d->head_dim) lanes *= 2;
-    const int per = 32 / lanes * kVecs, chunks = (d->heads + per - 1) / per;
-    if (2ll * d->rows * chunks >= (1ll << 31)) return host::fail(FL_ERR_UNSUPPORTED, "%s: too many rows", what);
+    const int W = d->head_dim % 16 == 0 ? 2 : 1;
+    int lanes_log = 0;
+    while ((8 * W << lanes_log) < d->head_dim) ++lanes_log;
+    const int groups = 32 >> lanes_log, half = (d->heads + groups - 1) / groups;
+    if (2ll * d->rows * half >= (1ll << 31)) return host::fail(FL_ERR_UNSUPPORTED, "%s: too many rows", what);
     host::LaunchContext ctx;
     if ((st = host::launch_context(stream, &ctx)) != FL_OK) return st;
     KvParams p = {};
@@ -326,21 +405,22 @@ fl_status run(const char* what, const fl_kv_desc* d, bool write, cudaStream_t st
     p.table_stride = d->table_stride;
     p.rows = d->rows, p.heads = d->heads, p.head_dim = d->head_dim, p.page_size = d->page_size;
     p.n_pages = d->n_pages, p.n_seqs = d->n_seqs, p.table_pages = d->table_pages;
-    p.lanes = lanes, p.chunks = chunks;
+    p.lanes_log = lanes_log, p.half = half;
+    // a whole row to a warp once that gives every scheduler several warps
+    p.per_task = 2 * half;
+    while (p.per_task > 1 && (long long)d->rows * ((2 * half + p.per_task - 1) / p.per_task) < 16ll * ctx.sms)
+        p.per_task = (p.per_task + 1) / 2;
+    p.tasks_row = (2 * half + p.per_task - 1) / p.per_task;
+    p.tasks = (uint32_t)d->rows * (uint32_t)p.tasks_row;
     p.range = ctx.range;
-    const long long ctas = (2ll * d->rows * p.chunks + kKvThreads / 32 - 1) / (kKvThreads / 32);
-    const long long most = 16ll * ctx.sms;
-    const dim3 grid((unsigned)(ctas < most ? ctas : most));
-    cudaError_t e;
-#define FL_CASE(DT, FMT)                                                                                   \
-    if (d->dtype == DT && d->format == FMT)                                                                \
-        e = write ? host::launch(fl_kv_write_kernel<DT, FMT>, grid, kKvThreads, 0, ctx.pdl, stream, p)      \
-                  : host::launch(fl_kv_read_kernel<DT, FMT>, grid, kKvThreads, 0, ctx.pdl, stream, p)
-    e = cudaErrorInvalidValue;
-    FL_CASE(0, 0);
-    FL_CASE(0, 1);
-    FL_CASE(1, 0);
-    FL_CASE(1, 1);
+    const dim3 grid((p.tasks + kKvThreads / 32 - 1) / (kKvThreads / 32));
+    cudaError_t e = cudaErrorInvalidValue;
+#define FL_CASE(DT, FMT, WW)                                                                               \
+    if (d->dtype == DT && d->format == FMT && W == WW)                                                     \
+    e = write ? host::launch(fl_kv_write_kernel<DT, FMT, WW>, grid, kKvThreads, 0, ctx.pdl, stream, p)     \
+              : host::launch(fl_kv_read_kernel<DT, FMT, WW>, grid, kKvThreads, 0, ctx.pdl, stream, p);
+    FL_CASE(0, 0, 1) FL_CASE(0, 0, 2) FL_CASE(0, 1, 1) FL_CASE(0, 1, 2)
+    FL_CASE(1, 0, 1) FL_CASE(1, 0, 2) FL_CASE(1, 1, 1) FL_CASE(1, 1, 2)
 #undef FL_CASE
     return host::launched(e, what);
 }

@@ -5,14 +5,16 @@
 //
 // Bound by HBM: every channel is read and written once. The angle depends on
 // the row and the pair only, so a CTA computes the sines of its rows once into
-// shared memory and applies them to every head of q and k.
+// shared memory and applies them to every head of q and k; a thread has four
+// tasks (8 pairs of a head each, two 16-byte vectors) in flight, the first of
+// them requested before the sines are computed.
 //
 // The angle is taken in turns, in fixed point: f = frac(inv_freq / 2 pi) as a
-// 64-bit fraction (from the 53 bits of one double product), and position * f
-// modulo 2^64 is the fraction of a turn, exact in the position: for the
-// largest int32 position the error is below 2^-24 turns, where the fp32
-// product position * inv_freq would be off by whole turns. The top 32 bits go
-// to sincospif.
+// 64-bit fraction, from the 24-bit significand of inv_freq times 64 bits of
+// 1 / 2 pi, and position * f modulo 2^64 is the fraction of a turn, exact in
+// the position: for the largest int32 position and a frequency up to 256 the
+// error is below 2^-24 turns, where the fp32 product position * inv_freq would
+// be off by whole turns. The top 32 bits go to sincospif.
 #include "fl_common.cuh"
 #include "fl_host.h"
 
@@ -23,6 +25,7 @@ namespace {
 constexpr int kRopeThreads = 256;
 constexpr int kRopeRows = 4;  // rows of one CTA at most
 constexpr int kRopePairs = FL_ROPE_MAX_DIM / 2;
+constexpr int kMaxHeads = 4096;
 
 struct RopeParams {
     const uint16_t* x[2];  // q, k
@@ -32,15 +35,34 @@ struct RopeParams {
     const float* inv_freq;
     long long positions_stride;
     int rows, heads[2], head_dim, pairs, rows_per_cta;
+    uint32_t per, per_inv;      // tasks of a head's row, and 2^32 / it rounded up
+    uint32_t all, all_inv;      // heads of q and k, likewise
+    uint32_t pairs_inv;
     int interleaved, inverse;
     int copy;  // channels behind the rotated ones are copied (out of place)
     unsigned char axis_of[kRopePairs];
 };
 
-// frac(f / 2 pi) in units of 2^-64 turns
+// n / d with inv = ceil(2^32 / d): exact while n * d < 2^32 (here n is at most 4 rows * kMaxHeads * d, d at most 512).
+__device__ __forceinline__ uint32_t quick_div(uint32_t n, uint32_t d, uint32_t inv) { return d == 1 ? n : __umulhi(n, inv); }
+
+// frac(f / 2 pi) in units of 2^-64 turns: f = m 2^e with a 24-bit integer m, and
+// 1 / 2 pi = kInv 2^-66 (64 bits of it), so the fraction is m kInv 2^(e - 2)
+// modulo 2^64.
 __device__ __forceinline__ unsigned long long turns_per_position(float f) {
-    const double t = (double)f * 0.15915494309189533577;  // 1 / (2 pi)
-    return (unsigned long long)((t - floor(t)) * 18446744073709551616.0);
+    constexpr unsigned long long kInv = 0xa2f9836e4e441529ull;  // 2^66 / (2 pi), rounded down
+    const uint32_t u = __float_as_uint(f), x = (u >> 23) & 255u;
+    const unsigned long long m = (u & 0x7fffffu) | (x != 0u ? 0x800000u : 0u);
+    const int e = (int)(x != 0u ? x : 1u) - 150 - 2;  // power of the last place of m * kInv, in units of 2^-64
+    const unsigned long long lo = m * kInv, hi = __umul64hi(m, kInv);
+    unsigned long long t;
+    if (e >= 0)
+        t = e < 64 ? lo << e : 0ull;
+    else if (e > -64)
+        t = (lo >> -e) | (hi << (64 + e));
+    else
+        t = e > -128 ? hi >> (-e - 64) : 0ull;
+    return u >> 31 ? 0ull - t : t;
 }
 
 template <int DT>
@@ -55,73 +77,106 @@ __device__ __forceinline__ void rotate2(uint32_t a, uint32_t b, float2 cs0, floa
 template <int DT, int VEC>
 __global__ void __launch_bounds__(kRopeThreads) fl_rope_kernel(const __grid_constant__ RopeParams p) {
     using Ops = DTypeOps<DT>;
-    __shared__ float2 cs[kRopeRows][kRopePairs];  // cos, sin
+    __shared__ __align__(16) float2 cs[kRopeRows][kRopePairs];  // cos, sin
     const int r0 = blockIdx.x * p.rows_per_cta, nr = min(p.rows_per_cta, p.rows - r0);
+    const uint32_t rot = (uint32_t)p.pairs / VEC, tasks = (uint32_t)nr * p.all * p.per;
+    constexpr int U = VEC == 8 ? 4 : 1;  // tasks in flight per thread
+    // one task: VEC pairs of one head's row, or VEC channels behind them
+    struct Task {
+        const uint16_t* x;
+        uint16_t* y;
+        int r, i, ia, ib;  // ib < 0: channels that are copied
+    };
+    auto task = [&](uint32_t t) {
+        const uint32_t hr = quick_div(t, p.per, p.per_inv), u = t - hr * p.per;
+        const uint32_t r = quick_div(hr, p.all, p.all_inv);
+        const int h2 = (int)(hr - r * p.all), w = h2 >= p.heads[0], h = w ? h2 - p.heads[0] : h2;
+        Task k;
+        k.x = p.x[w] + (r0 + (long long)r) * p.x_row[w] + h * p.x_head[w];
+        k.y = p.y[w] + (r0 + (long long)r) * p.y_row[w] + h * p.y_head[w];
+        k.r = (int)r;
+        k.i = (int)u * VEC;
+        if (u < rot) {
+            k.ia = p.interleaved ? 2 * k.i : k.i;
+            k.ib = p.interleaved ? 2 * k.i + VEC : k.i + p.pairs;
+        } else {
+            k.ia = 2 * p.pairs + (int)(u - rot) * VEC;
+            k.ib = -1;
+        }
+        return k;
+    };
     griddep_wait();
     griddep_launch_dependents();
-    for (int i = threadIdx.x; i < p.pairs; i += kRopeThreads) {
-        const unsigned long long f = turns_per_position(__ldg(p.inv_freq + i));
-        const int* pos = p.positions + p.axis_of[i] * p.positions_stride + r0;
-        for (int r = 0; r < nr; ++r) {
-            const unsigned long long t = (unsigned long long)(long long)__ldg(pos + r) * f;
-            float s, c;
-            sincospif((float)(int)(t >> 32) * 0x1p-31f, &s, &c);
-            cs[r][i] = make_float2(c, p.inverse ? -s : s);
+    uint4 a[U], b[U];
+    uint16_t sa = 0, sb = 0;
+    auto load = [&](uint32_t t0) {
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const uint32_t t = t0 + j * kRopeThreads;
+            if (t >= tasks) continue;
+            const Task k = task(t);
+            if constexpr (VEC == 8) {
+                a[j] = *reinterpret_cast<const uint4*>(k.x + k.ia);
+                if (k.ib >= 0) b[j] = *reinterpret_cast<const uint4*>(k.x + k.ib);
+            } else {
+                sa = k.x[k.ia];
+                if (k.ib >= 0) sb = k.x[k.ib];
+            }
         }
+    };
+    load(threadIdx.x);
+    for (uint32_t e = threadIdx.x; e < (uint32_t)(nr * p.pairs); e += kRopeThreads) {
+        const uint32_t r = quick_div(e, (uint32_t)p.pairs, p.pairs_inv), i = e - r * (uint32_t)p.pairs;
+        const int pos = __ldg(p.positions + p.axis_of[i] * p.positions_stride + r0 + r);
+        const unsigned long long t = (unsigned long long)(long long)pos * turns_per_position(__ldg(p.inv_freq + i));
+        float s, c;
+        sincospif((float)(int)(t >> 32) * 0x1p-31f, &s, &c);
+        cs[r][i] = make_float2(c, p.inverse ? -s : s);
     }
     __syncthreads();
-    // one task: VEC pairs of one head's row, or VEC channels behind them
-    const int rot = p.pairs / VEC, per = rot + (p.copy ? (p.head_dim - 2 * p.pairs) / VEC : 0);
-    const int heads = p.heads[0] + p.heads[1], tasks = nr * heads * per;
-    for (int t = threadIdx.x; t < tasks; t += kRopeThreads) {
-        const int u = t % per, h2 = t / per % heads, r = t / per / heads;
-        const int w = h2 >= p.heads[0], h = w ? h2 - p.heads[0] : h2;
-        const uint16_t* x = p.x[w] + (r0 + r) * p.x_row[w] + h * p.x_head[w];
-        uint16_t* y = p.y[w] + (r0 + r) * p.y_row[w] + h * p.y_head[w];
-        if (u >= rot) {
-            const int c = 2 * p.pairs + (u - rot) * VEC;
-            if constexpr (VEC == 8)
-                *reinterpret_cast<uint4*>(y + c) = *reinterpret_cast<const uint4*>(x + c);
-            else
-                y[c] = x[c];
-            continue;
-        }
-        const int i = u * VEC;
-        const int ia = p.interleaved ? 2 * i : i, ib = p.interleaved ? 2 * i + VEC : i + p.pairs;
-        if constexpr (VEC == 8) {
-            const uint4 a = *reinterpret_cast<const uint4*>(x + ia), b = *reinterpret_cast<const uint4*>(x + ib);
-            uint4 oa, ob;
-            if (p.interleaved) {
-                // (a, b) are the halves of one word
-                const uint32_t in[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                uint32_t o[8];
+    for (uint32_t t0 = threadIdx.x; t0 < tasks; t0 += U * kRopeThreads) {
+        if (t0 != threadIdx.x) load(t0);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float2 v = Ops::unpack(in[e]), k = cs[r][i + e];
-                    o[e] = Ops::pack(fmaf(v.x, k.x, -v.y * k.y), fmaf(v.y, k.x, v.x * k.y));
+        for (int j = 0; j < U; ++j) {
+            const uint32_t t = t0 + j * kRopeThreads;
+            if (t >= tasks) continue;
+            const Task k = task(t);
+            if constexpr (VEC == 8) {
+                uint4 oa = a[j], ob = b[j];
+                if (k.ib >= 0 && p.interleaved) {
+                    // (a, b) are the halves of one word
+                    const uint32_t in[8] = {a[j].x, a[j].y, a[j].z, a[j].w, b[j].x, b[j].y, b[j].z, b[j].w};
+                    uint32_t o[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float2 v = Ops::unpack(in[e]), f = cs[k.r][k.i + e];
+                        o[e] = Ops::pack(fmaf(v.x, f.x, -v.y * f.y), fmaf(v.y, f.x, v.x * f.y));
+                    }
+                    oa = make_uint4(o[0], o[1], o[2], o[3]);
+                    ob = make_uint4(o[4], o[5], o[6], o[7]);
+                } else if (k.ib >= 0) {
+                    const float4* f = reinterpret_cast<const float4*>(&cs[k.r][k.i]);
+                    const uint32_t aw[4] = {a[j].x, a[j].y, a[j].z, a[j].w}, bw[4] = {b[j].x, b[j].y, b[j].z, b[j].w};
+                    uint32_t ao[4], bo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float4 f2 = f[e];
+                        rotate2<DT>(aw[e], bw[e], make_float2(f2.x, f2.y), make_float2(f2.z, f2.w), ao[e], bo[e]);
+                    }
+                    oa = make_uint4(ao[0], ao[1], ao[2], ao[3]);
+                    ob = make_uint4(bo[0], bo[1], bo[2], bo[3]);
                 }
-                oa = make_uint4(o[0], o[1], o[2], o[3]);
-                ob = make_uint4(o[4], o[5], o[6], o[7]);
+                *reinterpret_cast<uint4*>(k.y + k.ia) = oa;
+                if (k.ib >= 0) *reinterpret_cast<uint4*>(k.y + k.ib) = ob;
+            } else if (k.ib < 0) {
+                k.y[k.ia] = sa;
             } else {
-                const float4* k = reinterpret_cast<const float4*>(&cs[r][i]);
-                const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
-                uint32_t ao[4], bo[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float4 k2 = k[e];
-                    rotate2<DT>(aw[e], bw[e], make_float2(k2.x, k2.y), make_float2(k2.z, k2.w), ao[e], bo[e]);
-                }
-                oa = make_uint4(ao[0], ao[1], ao[2], ao[3]);
-                ob = make_uint4(bo[0], bo[1], bo[2], bo[3]);
+                const float x = Ops::unpack(sa).x, y = Ops::unpack(sb).x;
+                const float2 f = cs[k.r][k.i];
+                const uint32_t o = Ops::pack(fmaf(x, f.x, -y * f.y), fmaf(y, f.x, x * f.y));
+                k.y[k.ia] = (uint16_t)(o & 0xffffu);
+                k.y[k.ib] = (uint16_t)(o >> 16);
             }
-            *reinterpret_cast<uint4*>(y + ia) = oa;
-            *reinterpret_cast<uint4*>(y + ib) = ob;
-        } else {
-            const float a = Ops::unpack(x[ia]).x, b = Ops::unpack(x[ib]).x;
-            const float2 k = cs[r][i];
-            const uint32_t o = Ops::pack(fmaf(a, k.x, -b * k.y), fmaf(b, k.x, a * k.y));
-            y[ia] = (uint16_t)(o & 0xffffu);
-            y[ib] = (uint16_t)(o >> 16);
         }
     }
 }
@@ -147,7 +202,8 @@ extern "C" fl_status fl_rope(const fl_rope_desc* d, void* stream) {
     if (!host::valid_dtype(d->dtype)) return fail(FL_ERR_INVALID_ARG, "fl_rope: bad dtype %d", (int)d->dtype);
     if (d->rows < 0 || d->heads_q < 1 || d->heads_k < 0 || d->head_dim < 1)
         return fail(FL_ERR_INVALID_ARG, "fl_rope: sizes must be positive (rows may be 0)");
-    if (d->heads_q > 65535 || d->heads_k > 65535) return fail(FL_ERR_UNSUPPORTED, "fl_rope: more than 65535 heads");
+    if (d->heads_q + (long long)d->heads_k > kMaxHeads)
+        return fail(FL_ERR_UNSUPPORTED, "fl_rope: more than %d heads of q and k", kMaxHeads);
     if (d->head_dim > FL_ROPE_MAX_DIM)
         return fail(FL_ERR_UNSUPPORTED, "fl_rope: head_dim above %d (%d)", FL_ROPE_MAX_DIM, d->head_dim);
     if (d->rotary_dim < 2 || d->rotary_dim % 2 != 0 || d->rotary_dim > d->head_dim)
@@ -218,6 +274,10 @@ extern "C" fl_status fl_rope(const fl_rope_desc* d, void* stream) {
     p.interleaved = d->interleaved != 0, p.inverse = d->inverse != 0;
     p.copy = !in_place && d->rotary_dim < d->head_dim;
     for (int i = 0; i < pairs; ++i) p.axis_of[i] = d->axis_of != nullptr ? d->axis_of[i] : 0;
+    p.per = (uint32_t)(vec ? pairs / 8 : pairs) + (p.copy ? (uint32_t)(d->head_dim - d->rotary_dim) / (vec ? 8 : 1) : 0u);
+    p.all = (uint32_t)(d->heads_q + (has_k ? d->heads_k : 0));
+    auto inverse = [](uint32_t n) { return (uint32_t)(((1ull << 32) + n - 1) / n); };
+    p.per_inv = inverse(p.per), p.all_inv = inverse(p.all), p.pairs_inv = inverse((uint32_t)pairs);
     // one row per CTA until that fills the SMs several times over
     p.rows_per_cta = 1;
     while (p.rows_per_cta < kRopeRows && (d->rows + p.rows_per_cta - 1) / p.rows_per_cta > 8 * ctx.sms)

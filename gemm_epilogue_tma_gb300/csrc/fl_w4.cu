@@ -22,26 +22,52 @@ namespace {
 constexpr int kQuantThreads = 256;
 constexpr int kQuantVecs = 4;  // 16-byte vectors per lane in flight
 
-// clamp(round(w / s), -7, 7) with inv = 1 / s rounded. w * inv is within two
-// units in the last place of the quotient, and a quotient of two 16-bit values
-// that is not a tie is further than that from one (both have at most 11
-// significant bits): only next to a tie is the quotient itself computed. An
-// inv that overflowed (a subnormal scale) takes that way too.
-__device__ __forceinline__ float code4(float w, float s, float inv) {
-    const float y = w * inv;
-    float r = rintf(y);
-    if (!(fabsf(y - r) <= 0.4999f)) r = rintf(__fdiv_rn(w, s));
-    return fminf(fmaxf(r, -7.f), 7.f);
+// Codes of 8 weights of a group, two to a byte. w * inv is within two units in
+// the last place of the quotient, and a quotient of two 16-bit values that is
+// not a tie is further than that from one (both have at most 11 significant
+// bits): only next to a tie, or where the clamp or an overflowed inv (a
+// subnormal scale) may matter, is the quotient itself computed.
+// w * inv + 1.5 * 2^23 + 8 rounds to 8 + an integer, ties to even, in the low
+// bits of the sum r_i = B + code_i, and sum_i r_i 16^i = 0x11111111 B + the
+// packed word, modulo 2^32.
+template <int DT>
+__device__ __forceinline__ uint32_t codes8(const uint4& v, float s, float inv, bool clamped) {
+    using Ops = DTypeOps<DT>;
+    constexpr float kShift = 12582912.0f + 8.0f;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 f = Ops::unpack(w[e]);
+        x[2 * e] = f.x;
+        x[2 * e + 1] = f.y;
+    }
+    float far = 0.f;
+    uint32_t out = 0;
+#pragma unroll
+    for (int e = 7; e >= 0; --e) {
+        const float y = x[e] * inv, t = y + kShift;
+        far = fmaxf(far, fabsf(y - (t - kShift)));
+        out = out * 16u + __float_as_uint(t);
+    }
+    out -= 0x4b400000u * 0x11111111u;
+    if (clamped || far > 0.4999f) {
+        out = 0;
+#pragma unroll
+        for (int e = 7; e >= 0; --e)
+            out = out * 16u + (uint32_t)(8 + (int)fminf(fmaxf(rintf(__fdiv_rn(x[e], s)), -7.f), 7.f));
+    }
+    return out;
 }
 
 // Groups are consecutive in W [N, K] taken as one array, so are their codes
 // and scales: lane i of a warp takes the i-th 16-byte vector, G / 8
 // neighbouring lanes share a group. Bound by HBM (2.5 bytes per weight and a
-// little).
+// little): kQuantVecs vectors are in flight per lane.
 template <int DT>
 __global__ void __launch_bounds__(kQuantThreads)
     fl_w4_quantize_kernel(const uint16_t* __restrict__ W, uint32_t* __restrict__ q, uint16_t* __restrict__ scales,
-                          long long vecs, int lanes) {
+                          long long vecs, int lanes_log) {
     using Ops = DTypeOps<DT>;
     griddep_wait();
     griddep_launch_dependents();
@@ -56,24 +82,19 @@ __global__ void __launch_bounds__(kQuantThreads)
     for (int u = 0; u < kQuantVecs; ++u) {
         const long long i = v0 + u * kQuantThreads;
         uint32_t m = absmax8<DT>(v[u]);
-        for (int o = lanes / 2; o > 0; o >>= 1) m = absmax2<DT>(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int o = 1 << lanes_log >> 1; o > 0; o >>= 1) m = absmax2<DT>(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (i >= vecs) continue;
         const bool fine = (m & 0xffffu) < Bits16<DT>::kInf;
-        // the quotient by 7 is never next to a border of the 16-bit format
-        // without being on its near side, so rounding it twice is rounding once
-        uint32_t sb = Ops::pack(Ops::unpack(m).x / 7.0f, 0.f) & 0xffffu;
+        // (amax / 7 is never within 2^-13 of a border of the 16-bit format
+        // without lying on it, so the fp32 product with 1 / 7, 2^-23 off at
+        // most, rounds to the same 16 bits)
+        const float amax = Ops::unpack(m).x;
+        uint32_t sb = Ops::pack(amax * (1.0f / 7.0f), 0.f) & 0xffffu;
         if (sb == 0u) sb = 1u;  // smallest positive value
-        const float s = Ops::unpack(sb).x, inv = 1.0f / s;
-        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-        uint32_t out = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 f = Ops::unpack(w[e]);
-            const int a = 8 + (int)code4(f.x, s, inv), b = 8 + (int)code4(f.y, s, inv);
-            out |= (uint32_t)(a | (b << 4)) << (8 * e);
-        }
+        const float s = Ops::unpack(sb).x, inv = __frcp_rn(s);
+        const uint32_t out = codes8<DT>(v[u], s, inv, !(amax * inv < 7.4f));
         q[i] = fine ? out : 0x88888888u;
-        if ((i & (lanes - 1)) == 0) scales[i / lanes] = fine ? (uint16_t)sb : (uint16_t)0x7fffu;
+        if ((i & ((1 << lanes_log) - 1)) == 0) scales[i >> lanes_log] = fine ? (uint16_t)sb : (uint16_t)0x7fffu;
     }
 }
 
@@ -172,7 +193,7 @@ fl_status fl_w4_quantize(const void* W, void* q, void* scales, int N, int K, int
     const dim3 grid((unsigned)((vecs + per - 1) / per));
     auto kern = dtype == FL_F16 ? fl_w4_quantize_kernel<DT_F16> : fl_w4_quantize_kernel<DT_BF16>;
     return host::launched(host::launch(kern, grid, kQuantThreads, 0, ctx.pdl, s, static_cast<const uint16_t*>(W),
-                                       static_cast<uint32_t*>(q), static_cast<uint16_t*>(scales), vecs, group / 8),
+                                       static_cast<uint32_t*>(q), static_cast<uint16_t*>(scales), vecs, group == 32 ? 2 : group == 64 ? 3 : 4),
                           "4-bit quantiser");
 }
 

@@ -493,7 +493,8 @@ fl_status fl_w4_swiglu_ffn(const void* x, const void* gamma, const fl_w4_weight*
  *   NULL: axis 0 for all.
  * Pointers are 2-byte aligned (inv_freq and positions 4); rows whose base and
  * strides are multiples of 16 bytes take the vector form. head_dim <= 512,
- * rotary_dim even, 2 .. head_dim; n_axes 1 .. 4. rows 0 does nothing.
+ * rotary_dim even, 2 .. head_dim; n_axes 1 .. 4; at most 4096 heads of q and k
+ * together. rows 0 does nothing.
  */
 #define FL_ROPE_MAX_DIM 512
 typedef struct {
@@ -517,7 +518,8 @@ fl_status fl_rope(const fl_rope_desc* desc, void* stream);
  * k_cache, v_cache: [n_pages, page_size, heads, head_dim] codes, one byte each;
  * k_scale, v_scale: [n_pages, page_size, heads] fp32, one per row and head.
  * A head's row x is held as codes with the value scale * code:
- *   scale = max(amax / top, 2^-126), amax the largest |x|; top 127 or 448
+ *   scale = max(amax * (1 / top), 2^-126), amax the largest |x|, top 127 or
+ *           448, 1 / top rounded to fp32 and the product too
  *   FL_KV_INT8: code = round(x / scale), ties to even (two's complement)
  *   FL_KV_E4M3: code = x / scale rounded to the nearest 8-bit float with 4
  *               exponent and 3 mantissa bits (finite variant), ties to even

@@ -80,7 +80,8 @@ def kv_quantize(x, fmt):
     x = np.asarray(x, dtype=np.float64)
     fine = np.isfinite(x).all(-1)
     x = np.where(fine[..., None], x, 0.0)
-    scale = np.maximum((np.abs(x).max(-1) / KV_TOP[fmt]).astype(np.float32), np.float32(KV_TINY)).astype(np.float64)
+    inv = np.float32(1.0) / np.float32(KV_TOP[fmt])
+    scale = np.maximum(np.abs(x).max(-1).astype(np.float32) * inv, np.float32(KV_TINY)).astype(np.float64)
     y = x / scale[..., None]
     code = np.clip(np.rint(y), -127, 127) if fmt == "int8" else e4m3_round(y)
     return code, np.where(fine, scale, np.nan)

@@ -124,6 +124,7 @@ def test_rope_refusals(L):
     assert call(**both, q_out=addr(2, 512), k_out=addr(2)) == INVALID
     assert call(rotary_dim=63) == INVALID and call(rotary_dim=66) == INVALID and call(rotary_dim=0) == INVALID
     assert call(head_dim=520, rotary_dim=64) == UNSUPPORTED
+    assert call(heads_q=4096) == UNSUPPORTED and "heads" in fl.last_error()
     assert call(n_axes=0) == INVALID and call(n_axes=5) == INVALID
     assert call(n_axes=2, axis_of=bytes([0, 1] * 16)) in PASSES
     assert call(n_axes=2, axis_of=bytes([0, 2] * 16)) == INVALID
@@ -244,19 +245,34 @@ def test_rope_oracle_is_a_rotation(interleaved):
 # ---------------------------------------------------------------------------
 # the kernels' steps, restated
 # ---------------------------------------------------------------------------
+def turns_per_position(f):
+    """The kernel's steps: the 24-bit significand times 64 bits of 1 / 2 pi, shifted, modulo 2^64."""
+    u = int(np.float32(f).view(np.uint32))
+    x = (u >> 23) & 255
+    m = (u & 0x7fffff) | (0x800000 if x else 0)
+    e = (x if x else 1) - 150 - 2
+    lo, hi, mod = m * 0xa2f9836e4e441529 % 2 ** 64, m * 0xa2f9836e4e441529 >> 64, 2 ** 64
+    if e >= 0:
+        t = (lo << e) % mod if e < 64 else 0
+    elif e > -64:
+        t = (lo >> -e) | ((hi << (64 + e)) % mod)
+    else:
+        t = hi >> (-e - 64) if e > -128 else 0
+    return (mod - t) % mod if u >> 31 else t
+
+
 def test_fixed_point_turns_hold_for_every_position():
-    """position * frac(f / 2 pi) modulo one turn in 64-bit fixed point, against exact arithmetic: at most 2^-24 turns
-    off (half a unit of float64 in f / 2 pi, times 2^31, is 2^-25 for f <= 2 pi)."""
+    """position * frac(f / 2 pi) modulo one turn in 64-bit fixed point, against exact arithmetic: the fraction is off by
+    one unit of 2^-64 for its shift and f * 2^-64 for the bits of 1 / 2 pi, so 2^31 positions are off by 2^-24 turns at
+    most up to f = 256."""
     rng = np.random.default_rng(3)
-    inv2pi = Fraction(0.15915494309189533577)
-    exact_inv2pi = Fraction("0.159154943091895335768883763372514362034459645740456448747667344058896797634226535")
-    for f in [1.0, 0.5, 1e-4, 0.731, 6.0, 2e-7] + list(rng.uniform(0, 1, 20)):
+    inv2pi = Fraction("0.159154943091895335768883763372514362034459645740456448747667344058896797634226535")
+    for f in [1.0, 0.5, 1e-4, 0.731, 6.0, 2e-7, 1e-12, 1e-40, -0.25, 255.0, 6.2831855] + list(rng.uniform(0, 1, 20)):
         f = float(np.float32(f))
-        t = float(f) * float(inv2pi)
-        F = min(int((t - np.floor(t)) * 18446744073709551616.0), 2 ** 64 - 1)
+        F = turns_per_position(f)
         for p in [0, 1, -1, 2 ** 31 - 1, -2 ** 31, 1048575] + list(rng.integers(-2 ** 31, 2 ** 31, 20)):
             got = Fraction((int(p) * F) % 2 ** 64, 2 ** 64)
-            want = (int(p) * Fraction(f) * exact_inv2pi) % 1
+            want = (int(p) * Fraction(f) * inv2pi) % 1
             off = abs(got - want)
             assert min(off, 1 - off) <= Fraction(1, 2 ** 24), (f, p)
 
@@ -311,7 +327,7 @@ def test_codes_next_to_a_border():
     rng = np.random.default_rng(9)
     for _ in range(300):
         amax = f32(round16("bf16")(abs(rng.standard_normal()) + 0.01))
-        s = f32(amax / f32(127.0))
+        s = f32(amax * f32(f32(1.0) / f32(127.0)))
         inv = f32(f32(1.0) / s)
         for c in rng.integers(-127, 127, 6):
             for x in {float(round16("bf16")((c + 0.5) * float(s))), float(amax) / 2, float(amax)}:
