@@ -49,19 +49,21 @@ struct KvParams {
 
 // Place of row i in the cache (page * page_size + row in the page), -1 if it
 // belongs to no sequence, -2 if its position has no page. Whole warp; every
-// lane gets the answer. The sequence is found 32 offsets at a time: first the
-// block of a 32-ary split that holds it, then inside.
+// lane gets the answer. Among up to 128 sequences the one that holds the row is
+// found in one step, in which each lane also loads what the answer will need of its
+// sequences, so the look-up is two dependent loads, this one and the page;
+// more sequences are narrowed down first, 32 offsets at a time.
 __device__ __forceinline__ long long find_slot(const KvParams& p, int i, int lane) {
-    int b;
-    long long pos;
+    int b, first = 0, from = 0;
     if (p.cu_rows == nullptr) {
         if (i >= p.n_seqs) return -1;
-        b = i;
-        pos = 0;
+        b = first = i;
+        if (p.start != nullptr) from = __ldg(p.start + b);
     } else {
         // the number of entries of cu_rows[1 ..] that are <= i
+        constexpr int J = 4;       // sequences per lane in the last step
         int lo = 0, n = p.n_seqs;  // the answer is in [lo, lo + n]
-        while (n > 0) {
+        while (n > 32 * J) {
             const int step = (n + 31) / 32;
             const int at = min(lo + (lane + 1) * step, lo + n);  // candidates lo + step, lo + 2 step, .., lo + n
             const bool le = __ldg(p.cu_rows + at) <= i;
@@ -71,13 +73,36 @@ __device__ __forceinline__ long long find_slot(const KvParams& p, int i, int lan
             lo += done;
             n = done == n ? 0 : min(step - 1, n - done);
         }
-        if (lo >= p.n_seqs) return -1;
-        b = lo;
-        const int first = __ldg(p.cu_rows + b);
+        int end[J], begin[J], s[J];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int mine = min(lo + 32 * j + lane, p.n_seqs - 1);
+            if (j == 0 || 32 * j < n) {
+                end[j] = __ldg(p.cu_rows + mine + 1);
+                begin[j] = __ldg(p.cu_rows + mine);
+                s[j] = p.start != nullptr ? __ldg(p.start + mine) : 0;
+            }
+        }
+        int c = 0;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            if (j == 0 || 32 * j < n) c += __popc(__ballot_sync(0xffffffffu, 32 * j + lane < n && end[j] <= i));
+        b = lo + c;
+        if (b >= p.n_seqs) return -1;
+        int fb = begin[0], fs = s[0];
+#pragma unroll
+        for (int j = 1; j < J; ++j)
+            if (c >= 32 * j && 32 * j < n) fb = begin[j], fs = s[j];
+        if (c < 32 * ((max(n, 1) + 31) / 32)) {
+            first = __shfl_sync(0xffffffffu, fb, c & 31);
+            from = __shfl_sync(0xffffffffu, fs, c & 31);
+        } else {
+            first = __ldg(p.cu_rows + b);
+            if (p.start != nullptr) from = __ldg(p.start + b);
+        }
         if (i < first) return -1;
-        pos = i - first;
     }
-    if (p.start != nullptr) pos += __ldg(p.start + b);
+    const long long pos = (long long)(i - first) + from;
     if (pos < 0 || pos >= (long long)p.table_pages * p.page_size) return -2;
     const uint32_t at = (uint32_t)pos, j = at / (uint32_t)p.page_size;  // (two int32 added: below 2^32)
     const int page = __ldg(p.page_table + b * p.table_stride + j);
@@ -85,93 +110,77 @@ __device__ __forceinline__ long long find_slot(const KvParams& p, int i, int lan
     return (long long)page * p.page_size + (at - j * (uint32_t)p.page_size);
 }
 
-// The quotient x / s of a value next to a border between two codes, to the
-// bit: x * inv, one Newton step, then the sign of the residual, one FMA.
-__device__ __forceinline__ float quotient(float x, float s, float inv, float& residual) {
-    float y = x * inv;
-    y = fmaf(fmaf(-y, s, x), inv, y);
-    residual = fmaf(-y, s, x);
-    return y;
+// Tiny rows scaled by 2^64, which leaves the quotient as it is, so that no
+// residual below underflows.
+__device__ __forceinline__ void lift(float& x, float& s, float& inv) {
+    if (s < 0x1p-40f) {
+        x *= 0x1p64f;
+        s *= 0x1p64f;
+        inv *= 0x1p-64f;
+    }
 }
 
 // int8 code next to a border: which side of lo + 1/2 the quotient lies is the
-// sign of x - (lo + 1/2) s, and 0 is a tie, which goes to even.
-__device__ __noinline__ int int8_exact(float x, float s, float inv) {
-    const float lo = floorf(x * inv), d = fmaf(-(lo + 0.5f), s, x);
+// sign of x - (lo + 1/2) s, one FMA, and 0 is a tie, which goes to even.
+__device__ __forceinline__ int int8_exact(float x, float s, float inv) {
+    lift(x, s, inv);
+    const float y = x * inv, lo = floorf(y);
+    if (fabsf(y - rintf(y)) < 0.499f) return (int)rintf(y);
+    const float d = fmaf(-(lo + 0.5f), s, x);
     return (int)(d > 0.f ? lo + 1.f : d < 0.f ? lo : 2.f * rintf(0.5f * (lo + 0.5f)));
 }
 
 // x / s with its last bit set when the quotient is not exact (rounding to
 // odd): the conversion to e4m3, which keeps 4 of the 24 bits, then rounds the
-// exact quotient.
-__device__ __noinline__ float odd_quotient(float x, float s, float inv) {
-    float e;
-    const float y = quotient(x, s, inv, e);
+// exact quotient. x * inv, one Newton step, then the sign of the residual.
+__device__ __forceinline__ float odd_quotient(float x, float s, float inv) {
+    lift(x, s, inv);
+    float y = x * inv;
+    y = fmaf(fmaf(-y, s, x), inv, y);
+    const float e = fmaf(-y, s, x);
     uint32_t u = __float_as_uint(y);
     if (e != 0.f && (u & 1u) == 0u && (u << 1) != 0u) u += ((__float_as_uint(e) ^ u) >> 31) ? 0xffffffffu : 1u;
     return __uint_as_float(u);
 }
 
-// Codes of 8 values. x * inv is within two units in the last place of the
-// quotient, so a code can only differ from the exact quotient's where x * inv
-// is within a few of a border between two codes: those values (one in about
-// 10^4) are computed again, exactly.
-//   int8: x * inv + 1.5 * 2^23 rounds to an integer, ties to even, in the low
-//   bits of the sum.
-//   e4m3: a border has 0x80000 in the 20 bits below the three that are kept;
-//   below 2^-6, where fewer are kept, every value is computed again.
+// Codes of 8 values. The quotient lies between x * dn and x * up (1 / s, within
+// 2^-23 of it, times 1 -+ 2^-21); rounding is monotonic, so where both round to
+// the same code it is the exact quotient's. The others are computed exactly: few,
+// but not as few as the width of the interval says, since 16-bit values are apt to lie on
+// a border (x = amax / 2 for int8), so only the pair that needs it is.
+//   int8: fma(x, up, 1.5 * 2^23) has the integer in its low bits.
 template <int DT, int FMT>
-__device__ __forceinline__ uint2 encode8(const uint4& v, float s, float inv) {
+__device__ __forceinline__ uint2 encode8(const uint4& v, float s, float up, float dn) {
     using Ops = DTypeOps<DT>;
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    float x[8];
+    uint32_t c[4], d[4];  // two codes each, from above and from below
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const float2 f = Ops::unpack(w[e]);
-        x[2 * e] = f.x;
-        x[2 * e + 1] = f.y;
-    }
-    uint32_t o[2];
-    if constexpr (FMT == FL_KV_INT8) {
-        constexpr float kShift = 12582912.0f;  // 1.5 * 2^23
-        uint32_t r[8];
-        float far = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float y = x[e] * inv, t = y + kShift;
-            far = fmaxf(far, fabsf(y - (t - kShift)));
-            r[e] = __float_as_uint(t);
-        }
-        if (far > 0.4999f) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float y = x[e] * inv;
-                if (fabsf(y - rintf(y)) > 0.4999f) r[e] = (uint32_t)int8_exact(x[e], s, inv);
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            o[e] = __byte_perm(__byte_perm(r[4 * e], r[4 * e + 1], 0x0040), __byte_perm(r[4 * e + 2], r[4 * e + 3], 0x0040), 0x5410);
-    } else {
-        float y[8];
-        bool near = false;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            y[e] = x[e] * inv;
-            near |= ((__float_as_uint(y[e]) + (0x80000u + 8u)) & 0xfffffu) <= 16u || fabsf(y[e]) < 0x1p-6f;
-        }
-        if (near) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = odd_quotient(x[e], s, inv);
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * e], y[4 * e + 1]), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * e + 2], y[4 * e + 3]), __NV_SATFINITE, __NV_E4M3);
-            o[e] = lo | (hi << 16);
+        if constexpr (FMT == FL_KV_INT8) {
+            constexpr float kShift = 12582912.0f;  // 1.5 * 2^23
+            c[e] = __byte_perm(__float_as_uint(fmaf(f.x, up, kShift)), __float_as_uint(fmaf(f.y, up, kShift)), 0x0040);
+            d[e] = __byte_perm(__float_as_uint(fmaf(f.x, dn, kShift)), __float_as_uint(fmaf(f.y, dn, kShift)), 0x0040);
+        } else {
+            c[e] = __nv_cvt_float2_to_fp8x2(make_float2(f.x * up, f.y * up), __NV_SATFINITE, __NV_E4M3);
+            d[e] = __nv_cvt_float2_to_fp8x2(make_float2(f.x * dn, f.y * dn), __NV_SATFINITE, __NV_E4M3);
         }
     }
-    return make_uint2(o[0], o[1]);
+    uint2 o = make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
+    if (o.x != __byte_perm(d[0], d[1], 0x5410) || o.y != __byte_perm(d[2], d[3], 0x5410)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (((c[e] ^ d[e]) & 0xffffu) == 0u) continue;
+            const float2 f = Ops::unpack(w[e]);
+            if constexpr (FMT == FL_KV_INT8)
+                c[e] = __byte_perm((uint32_t)int8_exact(f.x, s, up), (uint32_t)int8_exact(f.y, s, up), 0x0040);
+            else
+                c[e] = __nv_cvt_float2_to_fp8x2(make_float2(odd_quotient(f.x, s, up), odd_quotient(f.y, s, up)),
+                                                __NV_SATFINITE, __NV_E4M3);
+        }
+        o = make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
+    }
+    return o;
 }
 
 template <int DT, int FMT>
@@ -206,38 +215,45 @@ __device__ __forceinline__ Task task_of(const KvParams& p, uint32_t t) {
     const int p0 = (int)(t - row * (uint32_t)p.tasks_row) * p.per_task;
     return Task{(int)row, p0, min(p0 + p.per_task, 2 * p.half)};
 }
-// (which, head row) of this lane in pass q
-struct Unit {
-    int which, h;
+// Where this lane's values of a pass are: pass q takes the head rows (q mod half)
+// * groups + grp of k (q < half) or v.
+template <int W, typename T>
+struct Lane {
+    T* x[2];            // its first pass's 16-bit values of k and v
+    long long step[2];  // elements from one pass to the next
+    int grp, sub, groups;
     bool in;
+    __device__ __forceinline__ Lane(const KvParams& p, T* const (&base)[2], int row, int lane) {
+        sub = lane & ((1 << p.lanes_log) - 1), grp = lane >> p.lanes_log, groups = 32 >> p.lanes_log;
+        in = sub * (8 * W) < p.head_dim;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            x[w] = base[w] + row * p.row[w] + grp * p.head[w] + sub * (8 * W);
+            step[w] = groups * p.head[w];
+        }
+    }
 };
-__device__ __forceinline__ Unit unit_of(const KvParams& p, int q, int end, int grp, bool in) {
-    Unit u;
-    u.which = q >= p.half;
-    u.h = ((q - (u.which ? p.half : 0)) << (5 - p.lanes_log)) + grp;
-    u.in = in && q < end && u.h < p.heads;
-    return u;
-}
 
 // W: 16-byte vectors of 16-bit values per lane (1 or 2).
 template <int DT, int FMT, int W>
 __global__ void __launch_bounds__(kKvThreads) fl_kv_write_kernel(const __grid_constant__ KvParams p) {
     griddep_wait();
     griddep_launch_dependents();
-    const int lane = threadIdx.x & 31, sub = lane & ((1 << p.lanes_log) - 1), grp = lane >> p.lanes_log;
-    const bool in = sub * (8 * W) < p.head_dim;
     const uint32_t t = blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5);
     if (t >= p.tasks) return;
+    const int lane = threadIdx.x & 31;
     const Task k = task_of(p, t);
+    const Lane<W, const uint16_t> l(p, p.src, k.i, lane);
     long long slot = 0;
     for (int q0 = k.p0; q0 < k.p1; q0 += kPasses) {
         uint4 v[kPasses][W];
 #pragma unroll
         for (int j = 0; j < kPasses; ++j) {
-            const Unit u = unit_of(p, q0 + j, k.p1, grp, in);
-            const uint16_t* src = p.src[u.which] + k.i * p.row[u.which] + u.h * p.head[u.which] + sub * (8 * W);
+            const int q = q0 + j, w = q >= p.half, c = w ? q - p.half : q;
+            const bool in = l.in && q < k.p1 && c * l.groups + l.grp < p.heads;
+            const uint16_t* src = (w ? l.x[1] : l.x[0]) + c * (w ? l.step[1] : l.step[0]);
 #pragma unroll
-            for (int e = 0; e < W; ++e) v[j][e] = u.in ? ldg_v4(src + 8 * e) : make_uint4(0u, 0u, 0u, 0u);
+            for (int e = 0; e < W; ++e) v[j][e] = in ? ldg_v4(src + 8 * e) : make_uint4(0u, 0u, 0u, 0u);
         }
         if (q0 == k.p0) {
             slot = find_slot(p, k.i, lane);
@@ -248,20 +264,21 @@ __global__ void __launch_bounds__(kKvThreads) fl_kv_write_kernel(const __grid_co
         }
 #pragma unroll
         for (int j = 0; j < kPasses; ++j) {
-            const Unit u = unit_of(p, q0 + j, k.p1, grp, in);
             uint32_t m = absmax8<DT>(v[j][0]);
             if (W == 2) m = absmax2<DT>(m, absmax8<DT>(v[j][W - 1]));
             for (int o = 1 << p.lanes_log >> 1; o > 0; o >>= 1) m = absmax2<DT>(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (!u.in) continue;
-            const bool fine = (m & 0xffffu) < Bits16<DT>::kInf;
+            const int q = q0 + j, w = q >= p.half, h = (w ? q - p.half : q) * l.groups + l.grp;
+            if (!l.in || q >= k.p1 || h >= p.heads) continue;
+            m = absmax_halves<DT>(m);
+            const bool fine = m < Bits16<DT>::kInf;
             const float s = fmaxf(DTypeOps<DT>::unpack(m).x * (1.0f / (FMT == FL_KV_INT8 ? 127.0f : 448.0f)), 0x1p-126f);
-            const float inv = __frcp_rn(s);
-            const long long at = slot * p.heads + u.h;
-            if (sub == 0) p.scale[u.which][at] = fine ? s : __int_as_float(0x7fffffff);
+            const float inv = rcp_approx(s), up = inv * (1.0f + 0x1p-21f), dn = inv * (1.0f - 0x1p-21f);
+            const long long at = slot * p.heads + h;
+            if (l.sub == 0) p.scale[w][at] = fine ? s : __int_as_float(0x7fffffff);
             uint2 c[W];
 #pragma unroll
-            for (int e = 0; e < W; ++e) c[e] = fine ? encode8<DT, FMT>(v[j][e], s, inv) : make_uint2(0u, 0u);
-            uint8_t* dst = p.cache[u.which] + at * p.head_dim + sub * (8 * W);
+            for (int e = 0; e < W; ++e) c[e] = fine ? encode8<DT, FMT>(v[j][e], s, up, dn) : make_uint2(0u, 0u);
+            uint8_t* dst = p.cache[w] + at * p.head_dim + l.sub * (8 * W);
             if constexpr (W == 2)
                 *reinterpret_cast<uint4*>(dst) = make_uint4(c[0].x, c[0].y, c[1].x, c[1].y);
             else
@@ -274,24 +291,26 @@ template <int DT, int FMT, int W>
 __global__ void __launch_bounds__(kKvThreads) fl_kv_read_kernel(const __grid_constant__ KvParams p) {
     griddep_wait();
     griddep_launch_dependents();
-    const int lane = threadIdx.x & 31, sub = lane & ((1 << p.lanes_log) - 1), grp = lane >> p.lanes_log;
-    const bool in = sub * (8 * W) < p.head_dim;
     const uint32_t t = blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5);
     if (t >= p.tasks) return;
+    const int lane = threadIdx.x & 31;
     const Task k = task_of(p, t);
     const long long slot = find_slot(p, k.i, lane);
     if (slot < 0) {
         if (slot == -2 && lane == 0) atomicCAS(p.range, 0, k.i + 1);
         return;
     }
+    const Lane<W, uint16_t> l(p, p.dst, k.i, lane);
     for (int q0 = k.p0; q0 < k.p1; q0 += kPasses) {
         uint2 c[kPasses][W];
         float s[kPasses];
 #pragma unroll
         for (int j = 0; j < kPasses; ++j) {
-            const Unit u = unit_of(p, q0 + j, k.p1, grp, in);
-            const long long at = u.in ? slot * p.heads + u.h : 0;
-            const uint8_t* src = p.cache[u.which] + at * p.head_dim + (u.in ? sub * (8 * W) : 0);
+            // (a lane with nothing to read in this pass reads the place's first head row, so that all loads go out together)
+            const int q = min(q0 + j, k.p1 - 1), w = q >= p.half, h = (w ? q - p.half : q) * l.groups + l.grp;
+            const bool in = l.in && h < p.heads;
+            const long long at = slot * p.heads + (in ? h : 0);
+            const uint8_t* src = p.cache[w] + at * p.head_dim + (in ? l.sub * (8 * W) : 0);
             if constexpr (W == 2) {
                 const uint4 x = ldg_v4(src);
                 c[j][0] = make_uint2(x.x, x.y);
@@ -299,13 +318,13 @@ __global__ void __launch_bounds__(kKvThreads) fl_kv_read_kernel(const __grid_con
             } else {
                 c[j][0] = __ldg(reinterpret_cast<const uint2*>(src));
             }
-            s[j] = __ldg(p.scale[u.which] + at);
+            s[j] = __ldg(p.scale[w] + at);
         }
 #pragma unroll
         for (int j = 0; j < kPasses; ++j) {
-            const Unit u = unit_of(p, q0 + j, k.p1, grp, in);
-            if (!u.in) continue;
-            uint16_t* dst = p.dst[u.which] + k.i * p.row[u.which] + u.h * p.head[u.which] + sub * (8 * W);
+            const int q = q0 + j, w = q >= p.half, i = w ? q - p.half : q;
+            if (!l.in || q >= k.p1 || i * l.groups + l.grp >= p.heads) continue;
+            uint16_t* dst = (w ? l.x[1] : l.x[0]) + i * (w ? l.step[1] : l.step[0]);
 #pragma unroll
             for (int e = 0; e < W; ++e) *reinterpret_cast<uint4*>(dst + 8 * e) = decode8<DT, FMT>(c[j][e], s[j]);
         }

@@ -12,22 +12,34 @@ struct Bits16 {
     static constexpr uint32_t kInf = DT == DT_F16 ? 0x7c00u : 0x7f80u;
 };
 
-// Largest of the packed pairs' magnitudes, NaN if one is a NaN.
+// Larger of the packed pairs' magnitudes, NaN if one is a NaN. (The sign of the
+// result means nothing: mask it when done.)
 template <int DT>
 __device__ __forceinline__ uint32_t absmax2(uint32_t a, uint32_t b) {
     uint32_t r;
     if constexpr (DT == DT_F16)
-        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7fff7fffu), "r"(b & 0x7fff7fffu));
+        asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     else
-        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7fff7fffu), "r"(b & 0x7fff7fffu));
+        asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
-// Largest magnitude of 8 values, in both halves of the result.
 template <int DT>
 __device__ __forceinline__ uint32_t absmax8(const uint4& v) {
-    const uint32_t m = absmax2<DT>(absmax2<DT>(v.x, v.y), absmax2<DT>(v.z, v.w));
-    return absmax2<DT>(m, __funnelshift_l(m, m, 16));
+    return absmax2<DT>(absmax2<DT>(v.x, v.y), absmax2<DT>(v.z, v.w));
+}
+
+// Magnitude of the larger half, as 16 bits.
+template <int DT>
+__device__ __forceinline__ uint32_t absmax_halves(uint32_t m) {
+    return absmax2<DT>(m, __funnelshift_l(m, m, 16)) & 0x7fffu;
+}
+
+// 1 / x within one unit in the last place; infinite for the smallest subnormals.
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 }  // namespace fl

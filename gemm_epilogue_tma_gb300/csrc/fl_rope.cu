@@ -77,7 +77,10 @@ __device__ __forceinline__ void rotate2(uint32_t a, uint32_t b, float2 cs0, floa
 template <int DT, int VEC>
 __global__ void __launch_bounds__(kRopeThreads) fl_rope_kernel(const __grid_constant__ RopeParams p) {
     using Ops = DTypeOps<DT>;
-    __shared__ __align__(16) float2 cs[kRopeRows][kRopePairs];  // cos, sin
+    // (cos, sin) of the rows' pairs. In the vector form a thread reads 8
+    // neighbouring pairs as four float4, and its neighbours the next 8: the
+    // first float4 of every 8 lie side by side, then the second ones, ..
+    __shared__ __align__(16) float2 cs[kRopeRows][kRopePairs];
     const int r0 = blockIdx.x * p.rows_per_cta, nr = min(p.rows_per_cta, p.rows - r0);
     const uint32_t rot = (uint32_t)p.pairs / VEC, tasks = (uint32_t)nr * p.all * p.per;
     constexpr int U = VEC == 8 ? 4 : 1;  // tasks in flight per thread
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__(kRopeThreads) fl_rope_kernel(const __grid_cons
         const unsigned long long t = (unsigned long long)(long long)pos * turns_per_position(__ldg(p.inv_freq + i));
         float s, c;
         sincospif((float)(int)(t >> 32) * 0x1p-31f, &s, &c);
-        cs[r][i] = make_float2(c, p.inverse ? -s : s);
+        cs[r][VEC == 8 ? ((i % 8 / 2) * rot + i / 8) * 2 + i % 2 : i] = make_float2(c, p.inverse ? -s : s);
     }
     __syncthreads();
     for (uint32_t t0 = threadIdx.x; t0 < tasks; t0 += U * kRopeThreads) {
@@ -143,28 +146,25 @@ __global__ void __launch_bounds__(kRopeThreads) fl_rope_kernel(const __grid_cons
             const Task k = task(t);
             if constexpr (VEC == 8) {
                 uint4 oa = a[j], ob = b[j];
-                if (k.ib >= 0 && p.interleaved) {
-                    // (a, b) are the halves of one word
-                    const uint32_t in[8] = {a[j].x, a[j].y, a[j].z, a[j].w, b[j].x, b[j].y, b[j].z, b[j].w};
+                if (k.ib >= 0) {
+                    const float4* f = reinterpret_cast<const float4*>(&cs[k.r][0]) + k.i / 8;
+                    const uint32_t aw[4] = {a[j].x, a[j].y, a[j].z, a[j].w}, bw[4] = {b[j].x, b[j].y, b[j].z, b[j].w};
                     uint32_t o[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float2 v = Ops::unpack(in[e]), f = cs[k.r][k.i + e];
-                        o[e] = Ops::pack(fmaf(v.x, f.x, -v.y * f.y), fmaf(v.y, f.x, v.x * f.y));
+                    for (int e = 0; e < 4; ++e) {
+                        const float4 f2 = f[e * rot];
+                        if (p.interleaved) {
+                            // a pair is the two halves of one word
+                            const float2 v = Ops::unpack(e < 2 ? aw[2 * e] : bw[2 * e - 4]);
+                            const float2 u = Ops::unpack(e < 2 ? aw[2 * e + 1] : bw[2 * e - 3]);
+                            o[2 * e] = Ops::pack(fmaf(v.x, f2.x, -v.y * f2.y), fmaf(v.y, f2.x, v.x * f2.y));
+                            o[2 * e + 1] = Ops::pack(fmaf(u.x, f2.z, -u.y * f2.w), fmaf(u.y, f2.z, u.x * f2.w));
+                        } else {
+                            rotate2<DT>(aw[e], bw[e], make_float2(f2.x, f2.y), make_float2(f2.z, f2.w), o[e], o[4 + e]);
+                        }
                     }
                     oa = make_uint4(o[0], o[1], o[2], o[3]);
                     ob = make_uint4(o[4], o[5], o[6], o[7]);
-                } else if (k.ib >= 0) {
-                    const float4* f = reinterpret_cast<const float4*>(&cs[k.r][k.i]);
-                    const uint32_t aw[4] = {a[j].x, a[j].y, a[j].z, a[j].w}, bw[4] = {b[j].x, b[j].y, b[j].z, b[j].w};
-                    uint32_t ao[4], bo[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float4 f2 = f[e];
-                        rotate2<DT>(aw[e], bw[e], make_float2(f2.x, f2.y), make_float2(f2.z, f2.w), ao[e], bo[e]);
-                    }
-                    oa = make_uint4(ao[0], ao[1], ao[2], ao[3]);
-                    ob = make_uint4(bo[0], bo[1], bo[2], bo[3]);
                 }
                 *reinterpret_cast<uint4*>(k.y + k.ia) = oa;
                 if (k.ib >= 0) *reinterpret_cast<uint4*>(k.y + k.ib) = ob;

@@ -20,81 +20,100 @@ namespace {
 // quantiser
 // ---------------------------------------------------------------------------
 constexpr int kQuantThreads = 256;
-constexpr int kQuantVecs = 4;  // 16-byte vectors per lane in flight
+constexpr int kQuantUnits = 2;  // units of 16 weights per lane in flight
 
-// Codes of 8 weights of a group, two to a byte. w * inv is within two units in
-// the last place of the quotient, and a quotient of two 16-bit values that is
-// not a tie is further than that from one (both have at most 11 significant
-// bits): only next to a tie, or where the clamp or an overflowed inv (a
-// subnormal scale) may matter, is the quotient itself computed.
-// w * inv + 1.5 * 2^23 + 8 rounds to 8 + an integer, ties to even, in the low
-// bits of the sum r_i = B + code_i, and sum_i r_i 16^i = 0x11111111 B + the
-// packed word, modulo 2^32.
+// A code next to a tie: which side of lo + 1/2 the quotient lies is the sign of
+// w - (lo + 1/2) s, one FMA (exact: both have at most 11 significant bits), and
+// 0 is the tie, which goes to even. Returned as 8 + the integer.
+__device__ __forceinline__ uint32_t code_exact(float w, float s, float inv) {
+    const float lo = floorf(w * inv), d = fmaf(-(lo + 0.5f), s, w);
+    if (fabsf(w * inv - (lo + 0.5f)) > 0.001f) return (uint32_t)(8 + (int)rintf(w * inv));
+    return (uint32_t)(8 + (int)(d > 0.f ? lo + 1.f : d < 0.f ? lo : 2.f * rintf(0.5f * (lo + 0.5f))));
+}
+
+// Codes of 8 weights of a group, two to a byte. The quotient lies between
+// w * dn and w * up (1 / s, within 2^-24 of it, times 1 -+ 2^-21), and rounding
+// is monotonic: where both round to the same code it is the exact quotient's;
+// the others (16-bit weights over 16-bit scales are ties now and then: one in some
+// hundred) are decided exactly. Where the clamp or an overflowed 1 / s (a
+// subnormal scale) may matter, the quotients are divided out: of two 16-bit
+// values it is a tie or at least 2^-13 away from one, so fp32 division decides it.
+// fma(w, up, 1.5 * 2^23 + 8) has 8 + the integer in its low bits, r_i = B +
+// code_i, and sum_i r_i 16^i = 0x11111111 B + the packed word, modulo 2^32.
 template <int DT>
-__device__ __forceinline__ uint32_t codes8(const uint4& v, float s, float inv, bool clamped) {
+__device__ __forceinline__ uint32_t codes8(const uint4& v, float s, float up, float dn, bool clamped) {
     using Ops = DTypeOps<DT>;
     constexpr float kShift = 12582912.0f + 8.0f;
+    constexpr uint32_t kBase = 0x4b400000u;
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    float x[8];
+    uint32_t c[4], d[4];  // 272 B + two codes, from above and from below
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const float2 f = Ops::unpack(w[e]);
-        x[2 * e] = f.x;
-        x[2 * e + 1] = f.y;
+        c[e] = __float_as_uint(fmaf(f.y, up, kShift)) * 16u + __float_as_uint(fmaf(f.x, up, kShift));
+        d[e] = __float_as_uint(fmaf(f.y, dn, kShift)) * 16u + __float_as_uint(fmaf(f.x, dn, kShift));
     }
-    float far = 0.f;
-    uint32_t out = 0;
+    if (((c[0] ^ d[0]) | (c[1] ^ d[1]) | (c[2] ^ d[2]) | (c[3] ^ d[3])) != 0u) {
 #pragma unroll
-    for (int e = 7; e >= 0; --e) {
-        const float y = x[e] * inv, t = y + kShift;
-        far = fmaxf(far, fabsf(y - (t - kShift)));
-        out = out * 16u + __float_as_uint(t);
+        for (int e = 0; e < 4; ++e) {
+            if (c[e] == d[e]) continue;
+            const float2 f = Ops::unpack(w[e]);
+            c[e] = (kBase + code_exact(f.y, s, up)) * 16u + (kBase + code_exact(f.x, s, up));
+        }
     }
-    out -= 0x4b400000u * 0x11111111u;
-    if (clamped || far > 0.4999f) {
+    uint32_t out = ((c[3] * 256u + c[2]) * 256u + c[1]) * 256u + c[0] - kBase * 0x11111111u;
+    if (clamped) {
         out = 0;
 #pragma unroll
-        for (int e = 7; e >= 0; --e)
-            out = out * 16u + (uint32_t)(8 + (int)fminf(fmaxf(rintf(__fdiv_rn(x[e], s)), -7.f), 7.f));
+        for (int e = 3; e >= 0; --e) {
+            const float2 f = Ops::unpack(w[e]);
+            out = out * 16u + (uint32_t)(8 + (int)fminf(fmaxf(rintf(__fdiv_rn(f.y, s)), -7.f), 7.f));
+            out = out * 16u + (uint32_t)(8 + (int)fminf(fmaxf(rintf(__fdiv_rn(f.x, s)), -7.f), 7.f));
+        }
     }
     return out;
 }
 
 // Groups are consecutive in W [N, K] taken as one array, so are their codes
-// and scales: lane i of a warp takes the i-th 16-byte vector, G / 8
-// neighbouring lanes share a group. Bound by HBM (2.5 bytes per weight and a
-// little): kQuantVecs vectors are in flight per lane.
+// and scales: lane i of a warp takes the i-th unit of 16 weights, G / 16
+// neighbouring lanes share a group. HBM moves 2.5 bytes per weight and a
+// little, which leaves about 9 instructions a weight: the group's maximum, scale and
+// reciprocal cost as much as the codes, so a lane takes two vectors for them.
 template <int DT>
 __global__ void __launch_bounds__(kQuantThreads)
     fl_w4_quantize_kernel(const uint16_t* __restrict__ W, uint32_t* __restrict__ q, uint16_t* __restrict__ scales,
-                          long long vecs, int lanes_log) {
+                          long long units, int lanes_log) {
     using Ops = DTypeOps<DT>;
     griddep_wait();
     griddep_launch_dependents();
-    const long long v0 = (long long)blockIdx.x * (kQuantThreads * kQuantVecs) + threadIdx.x;
-    uint4 v[kQuantVecs];
+    const long long i0 = (long long)blockIdx.x * (kQuantThreads * kQuantUnits) + threadIdx.x;
+    const uint4* src = reinterpret_cast<const uint4*>(W) + i0 * 2;
+    uint4 v[kQuantUnits][2];
 #pragma unroll
-    for (int u = 0; u < kQuantVecs; ++u) {
-        const long long i = v0 + u * kQuantThreads;
-        v[u] = i < vecs ? ldg_v4(W + i * 8) : make_uint4(0u, 0u, 0u, 0u);
-    }
+    for (int u = 0; u < kQuantUnits; ++u)
 #pragma unroll
-    for (int u = 0; u < kQuantVecs; ++u) {
-        const long long i = v0 + u * kQuantThreads;
-        uint32_t m = absmax8<DT>(v[u]);
+        for (int e = 0; e < 2; ++e)
+            v[u][e] = i0 + u * kQuantThreads < units ? __ldg(src + u * (2 * kQuantThreads) + e) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int u = 0; u < kQuantUnits; ++u) {
+        uint32_t m = absmax2<DT>(absmax8<DT>(v[u][0]), absmax8<DT>(v[u][1]));
         for (int o = 1 << lanes_log >> 1; o > 0; o >>= 1) m = absmax2<DT>(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (i >= vecs) continue;
-        const bool fine = (m & 0xffffu) < Bits16<DT>::kInf;
+        if (i0 + u * kQuantThreads >= units) continue;
+        m = absmax_halves<DT>(m);
+        const bool fine = m < Bits16<DT>::kInf;
         // (amax / 7 is never within 2^-13 of a border of the 16-bit format
         // without lying on it, so the fp32 product with 1 / 7, 2^-23 off at
         // most, rounds to the same 16 bits)
         const float amax = Ops::unpack(m).x;
         uint32_t sb = Ops::pack(amax * (1.0f / 7.0f), 0.f) & 0xffffu;
         if (sb == 0u) sb = 1u;  // smallest positive value
-        const float s = Ops::unpack(sb).x, inv = __frcp_rn(s);
-        const uint32_t out = codes8<DT>(v[u], s, inv, !(amax * inv < 7.4f));
-        q[i] = fine ? out : 0x88888888u;
-        if ((i & ((1 << lanes_log) - 1)) == 0) scales[i >> lanes_log] = fine ? (uint16_t)sb : (uint16_t)0x7fffu;
+        const float s = Ops::unpack(sb).x, inv = rcp_approx(s), up = inv * (1.0f + 0x1p-21f), dn = inv * (1.0f - 0x1p-21f);
+        const bool clamped = !(amax * inv < 7.4f);
+        uint2 out = make_uint2(0x88888888u, 0x88888888u);
+        if (fine) out = make_uint2(codes8<DT>(v[u][0], s, up, dn, clamped), codes8<DT>(v[u][1], s, up, dn, clamped));
+        reinterpret_cast<uint2*>(q)[i0 + u * kQuantThreads] = out;
+        if ((threadIdx.x & ((1 << lanes_log) - 1)) == 0)
+            scales[(i0 + u * kQuantThreads) >> lanes_log] = fine ? (uint16_t)sb : (uint16_t)0x7fffu;
     }
 }
 
@@ -185,15 +204,15 @@ fl_status fl_w4_quantize(const void* W, void* q, void* scales, int N, int K, int
     if (host::overlap(q, n / 2, W, n * 2) || host::overlap(scales, n / group * 2, W, n * 2) ||
         host::overlap(q, n / 2, scales, n / group * 2))
         return host::fail(FL_ERR_INVALID_ARG, "q or scales overlaps another tensor of the call");
-    const long long vecs = (long long)(n / 8), per = kQuantThreads * kQuantVecs;
-    if ((vecs + per - 1) / per > 0x7fffffffll) return host::fail(FL_ERR_UNSUPPORTED, "fl_w4_quantize: too many weights");
+    const long long units = (long long)(n / 16), per = kQuantThreads * kQuantUnits;
+    if ((units + per - 1) / per > 0x7fffffffll) return host::fail(FL_ERR_UNSUPPORTED, "fl_w4_quantize: too many weights");
     host::LaunchContext ctx;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if ((st = host::launch_context(s, &ctx)) != FL_OK) return st;
-    const dim3 grid((unsigned)((vecs + per - 1) / per));
+    const dim3 grid((unsigned)((units + per - 1) / per));
     auto kern = dtype == FL_F16 ? fl_w4_quantize_kernel<DT_F16> : fl_w4_quantize_kernel<DT_BF16>;
     return host::launched(host::launch(kern, grid, kQuantThreads, 0, ctx.pdl, s, static_cast<const uint16_t*>(W),
-                                       static_cast<uint32_t*>(q), static_cast<uint16_t*>(scales), vecs, group == 32 ? 2 : group == 64 ? 3 : 4),
+                                       static_cast<uint32_t*>(q), static_cast<uint16_t*>(scales), units, group == 32 ? 1 : group == 64 ? 2 : 3),
                           "4-bit quantiser");
 }
 

@@ -331,7 +331,8 @@ def check_write(x, codes, scales, places, fmt, old_codes, old_scales):
 KV = [  # seqs, rows of each, start, H, D, page, dtype
     ([1], [0], 1, 8, 1, "f16"), ([1], [5], 2, 64, 16, "bf16"), ([37], [0], 8, 128, 16, "bf16"),
     ([5, 0, 1, 19], [3, 7, 16, 0], 3, 80, 16, "f16"), ([1] * 40, list(range(40)), 5, 128, 32, "f16"),
-    ([64, 1, 130], [0, 63, 64], 2, 256, 64, "bf16"), ([9, 4], [100, 0], 40, 24, 8, "bf16"), ([33, 2], [1, 1], 4, 40, 7, "f16")]
+    ([64, 1, 130], [0, 63, 64], 2, 256, 64, "bf16"), ([9, 4], [100, 0], 40, 24, 8, "bf16"), ([33, 2], [1, 1], 4, 40, 7, "f16"), ([1, 2] * 50, [4] * 100, 1, 16, 8, "bf16"),
+      ([1, 0, 3] * 110, [1] * 330, 1, 8, 4, "f16")]
 
 
 def kv_set_up(lens, start, page, rng, spare=2):

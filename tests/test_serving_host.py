@@ -278,10 +278,10 @@ def test_fixed_point_turns_hold_for_every_position():
 
 
 def find_slot(i, n_seqs, cu):
-    """The kernel's 32-ary search, lane by lane: the number of entries of cu[1:] that are <= i. Every index it reads
-    is checked."""
+    """The kernel's search, lane by lane: the number of entries of cu[1:] that are <= i, and the begin offset of that
+    sequence as the kernel gets it. Every index it reads is checked."""
     lo, n, rounds = 0, n_seqs, 0
-    while n > 0:
+    while n > 128:
         step = (n + 31) // 32
         c = 0
         for lane in range(32):
@@ -294,10 +294,25 @@ def find_slot(i, n_seqs, cu):
         n = 0 if done == n else min(step - 1, n - done)
         rounds += 1
         assert rounds < 8
-    return lo
+    c, begin = 0, {}
+    for j in range(4):
+        if j and 32 * j >= n:
+            continue
+        for lane in range(32):
+            mine = min(lo + 32 * j + lane, n_seqs - 1)
+            assert 0 <= mine < n_seqs
+            begin[j, lane] = cu[mine]
+            c += bool(32 * j + lane < n and cu[mine + 1] <= i)
+    b = lo + c
+    if b >= n_seqs:
+        return b, None
+    if c < 32 * ((max(n, 1) + 31) // 32):
+        j = max([0] + [j for j in (1, 2, 3) if c >= 32 * j and 32 * j < n])
+        return b, begin[j, c & 31]
+    return b, cu[b]
 
 
-@pytest.mark.parametrize("n_seqs", [1, 2, 31, 32, 33, 64, 100, 1024, 1025, 5000])
+@pytest.mark.parametrize("n_seqs", [1, 2, 31, 32, 33, 64, 100, 127, 128, 129, 200, 1024, 1025, 5000])
 def test_sequence_search(n_seqs):
     rng = np.random.default_rng(n_seqs)
     for kind in range(3):
@@ -305,15 +320,17 @@ def test_sequence_search(n_seqs):
         cu = np.concatenate([[rng.integers(0, 3) if kind == 2 else 0], n]).cumsum()
         for i in rng.integers(0, cu[-1] + 3, 12):
             want = int(np.searchsorted(cu[1:], i, side="right"))
-            assert find_slot(i, n_seqs, cu) == want
+            b, first = find_slot(i, n_seqs, cu)
+            assert b == want and (b == n_seqs or first == cu[b])
     # offsets out of order: some index in range, and an end
     junk = rng.integers(-5, 50, n_seqs + 1)
     for i in (0, 10, 60):
-        assert 0 <= find_slot(i, n_seqs, junk) <= n_seqs
+        assert 0 <= find_slot(i, n_seqs, junk)[0] <= n_seqs
 
 
 def test_codes_next_to_a_border():
-    """The kernel's fp32 steps against the exact quotient, on rows whose values lie on and next to borders."""
+    """The kernel's fp32 steps against the exact quotient, on rows whose values lie on and next to borders: the two
+    roundings from either side, and the exact step where they differ."""
     f32 = np.float32
 
     def fma(a, b, c):  # one rounding; exact in Fraction
@@ -325,17 +342,24 @@ def test_codes_next_to_a_border():
         return lo + 1 if d > Fraction(1, 2) or (d == Fraction(1, 2) and lo % 2) else lo
 
     rng = np.random.default_rng(9)
+    shift = f32(12582912.0)
+    exact = 0
     for _ in range(300):
         amax = f32(round16("bf16")(abs(rng.standard_normal()) + 0.01))
         s = f32(amax * f32(f32(1.0) / f32(127.0)))
         inv = f32(f32(1.0) / s)
+        up, dn = f32(inv * f32(1 + 2.0 ** -21)), f32(inv * f32(1 - 2.0 ** -21))
         for c in rng.integers(-127, 127, 6):
-            for x in {float(round16("bf16")((c + 0.5) * float(s))), float(amax) / 2, float(amax)}:
-                x = f32(x)
-                y = f32(x * inv)
-                r = np.rint(y)
-                if abs(f32(y - r)) > f32(0.4999):
+            for x in {float(round16("bf16")((c + 0.5) * float(s))), float(amax) / 2, float(amax), float(c) * 0.01}:
+                x = f32(x if abs(x) <= amax else amax)
+                r, q = fma(x, up, shift) - shift, fma(x, dn, shift) - shift
+                if r != q:
+                    exact += 1
+                    y = f32(x * up)
                     lo = np.floor(y)
-                    d = fma(-(lo + f32(0.5)), s, x)
-                    r = lo + 1 if d > 0 else lo if d < 0 else f32(2) * np.rint(f32(0.5) * (lo + f32(0.5)))
+                    r = np.rint(y)
+                    if abs(f32(y - np.rint(y))) >= f32(0.499):
+                        d = fma(-(lo + f32(0.5)), s, x)
+                        r = lo + 1 if d > 0 else lo if d < 0 else f32(2) * np.rint(f32(0.5) * (lo + f32(0.5)))
                 assert int(r) == nearest_even(Fraction(float(x)) / Fraction(float(s)))
+    assert exact > 20
