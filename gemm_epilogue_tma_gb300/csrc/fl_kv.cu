@@ -26,7 +26,8 @@ namespace fl {
 namespace {
 
 constexpr int kKvThreads = 128;
-constexpr int kPasses = 4;  // passes of one warp task in flight
+constexpr int kPasses = 4;       // passes of one reading warp task in flight
+constexpr int kWritePasses = 2;  // and of a writing one, which also needs registers for its arithmetic (4: 10.8 against 9.4 us, 4099 rows)
 
 struct KvParams {
     const uint16_t* src[2];  // write: k, v
@@ -110,77 +111,69 @@ __device__ __forceinline__ long long find_slot(const KvParams& p, int i, int lan
     return (long long)page * p.page_size + (at - j * (uint32_t)p.page_size);
 }
 
-// Tiny rows scaled by 2^64, which leaves the quotient as it is, so that no
-// residual below underflows.
-__device__ __forceinline__ void lift(float& x, float& s, float& inv) {
-    if (s < 0x1p-40f) {
-        x *= 0x1p64f;
-        s *= 0x1p64f;
-        inv *= 0x1p-64f;
+// What encoding a head's row needs of its scale s.
+struct Quant {
+    float up, dn;      // 1 / s, within 2^-23 of it, times 1 +- 2^-21
+    float lift, half;  // s * lift / 2; lift is 2^64 for a tiny s, so that no residual underflows
+    __device__ __forceinline__ explicit Quant(float s) {
+        const float inv = rcp_approx(s);
+        up = inv * (1.0f + 0x1p-21f), dn = inv * (1.0f - 0x1p-21f);
+        lift = s < 0x1p-40f ? 0x1p64f : 1.0f;
+        half = 0.5f * (s * lift);
     }
+};
+
+// Whether x / s rounds to `up` rather than to `dn`, the values of the two
+// neighbouring codes it lies between (or of one code twice): the sign of
+// x - (up + dn) / 2 * s, one FMA, says on which side of the border it is; on the
+// border itself the even code is taken.
+__device__ __forceinline__ bool takes_up(float x, float up, float dn, bool up_even, const Quant& q) {
+    const float d = fmaf(-(up + dn), q.half, x * q.lift);
+    return d == 0.f ? up_even : (d > 0.f) == (x > 0.f);
 }
 
-// int8 code next to a border: which side of lo + 1/2 the quotient lies is the
-// sign of x - (lo + 1/2) s, one FMA, and 0 is a tie, which goes to even.
-__device__ __forceinline__ int int8_exact(float x, float s, float inv) {
-    lift(x, s, inv);
-    const float y = x * inv, lo = floorf(y);
-    if (fabsf(y - rintf(y)) < 0.499f) return (int)rintf(y);
-    const float d = fmaf(-(lo + 0.5f), s, x);
-    return (int)(d > 0.f ? lo + 1.f : d < 0.f ? lo : 2.f * rintf(0.5f * (lo + 0.5f)));
-}
-
-// x / s with its last bit set when the quotient is not exact (rounding to
-// odd): the conversion to e4m3, which keeps 4 of the 24 bits, then rounds the
-// exact quotient. x * inv, one Newton step, then the sign of the residual.
-__device__ __forceinline__ float odd_quotient(float x, float s, float inv) {
-    lift(x, s, inv);
-    float y = x * inv;
-    y = fmaf(fmaf(-y, s, x), inv, y);
-    const float e = fmaf(-y, s, x);
-    uint32_t u = __float_as_uint(y);
-    if (e != 0.f && (u & 1u) == 0u && (u << 1) != 0u) u += ((__float_as_uint(e) ^ u) >> 31) ? 0xffffffffu : 1u;
-    return __uint_as_float(u);
-}
-
-// Codes of 8 values. The quotient lies between x * dn and x * up (1 / s, within
-// 2^-23 of it, times 1 -+ 2^-21); rounding is monotonic, so where both round to
-// the same code it is the exact quotient's. The others are computed exactly: few,
-// but not as few as the width of the interval says, since 16-bit values are apt to lie on
-// a border (x = amax / 2 for int8), so only the pair that needs it is.
+// Codes of 8 values. The quotient lies between x * dn and x * up, and rounding
+// is monotonic, so where both round to the same code it is the exact
+// quotient's. The others are decided exactly: far more than the width of the
+// interval says (1 % of bf16 values), since 16-bit values are apt to lie on or
+// next to a border (x = amax / 2 for int8).
 //   int8: fma(x, up, 1.5 * 2^23) has the integer in its low bits.
 template <int DT, int FMT>
-__device__ __forceinline__ uint2 encode8(const uint4& v, float s, float up, float dn) {
+__device__ __forceinline__ uint2 encode8(const uint4& v, const Quant& q) {
     using Ops = DTypeOps<DT>;
+    constexpr float kShift = 12582912.0f;  // 1.5 * 2^23
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t c[4], d[4];  // two codes each, from above and from below
+    uint32_t c[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const float2 f = Ops::unpack(w[e]);
         if constexpr (FMT == FL_KV_INT8) {
-            constexpr float kShift = 12582912.0f;  // 1.5 * 2^23
-            c[e] = __byte_perm(__float_as_uint(fmaf(f.x, up, kShift)), __float_as_uint(fmaf(f.y, up, kShift)), 0x0040);
-            d[e] = __byte_perm(__float_as_uint(fmaf(f.x, dn, kShift)), __float_as_uint(fmaf(f.y, dn, kShift)), 0x0040);
+            float a = fmaf(f.x, q.up, kShift), b = fmaf(f.y, q.up, kShift);
+            const float a1 = fmaf(f.x, q.dn, kShift), b1 = fmaf(f.y, q.dn, kShift);
+            if (a != a1 || b != b1) {
+                if (!takes_up(f.x, a - kShift, a1 - kShift, (__float_as_uint(a) & 1u) == 0u, q)) a = a1;
+                if (!takes_up(f.y, b - kShift, b1 - kShift, (__float_as_uint(b) & 1u) == 0u, q)) b = b1;
+            }
+            c[e] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040);
         } else {
-            c[e] = __nv_cvt_float2_to_fp8x2(make_float2(f.x * up, f.y * up), __NV_SATFINITE, __NV_E4M3);
-            d[e] = __nv_cvt_float2_to_fp8x2(make_float2(f.x * dn, f.y * dn), __NV_SATFINITE, __NV_E4M3);
+            auto code = [](float a, float b) {
+                return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+            };
+            auto value = [](uint32_t k) {
+                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)k, __NV_E4M3);
+                return __half22float2(*reinterpret_cast<const __half2*>(&h));
+            };
+            uint32_t k = code(f.x * q.up, f.y * q.up);
+            const uint32_t k1 = code(f.x * q.dn, f.y * q.dn);
+            if (k != k1) {
+                const float2 a = value(k), a1 = value(k1);
+                const bool x = takes_up(f.x, a.x, a1.x, (k & 1u) == 0u, q), y = takes_up(f.y, a.y, a1.y, (k & 0x100u) == 0u, q);
+                k = ((x ? k : k1) & 0xffu) | ((y ? k : k1) & 0xff00u);
+            }
+            c[e] = k;
         }
     }
-    uint2 o = make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
-    if (o.x != __byte_perm(d[0], d[1], 0x5410) || o.y != __byte_perm(d[2], d[3], 0x5410)) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (((c[e] ^ d[e]) & 0xffffu) == 0u) continue;
-            const float2 f = Ops::unpack(w[e]);
-            if constexpr (FMT == FL_KV_INT8)
-                c[e] = __byte_perm((uint32_t)int8_exact(f.x, s, up), (uint32_t)int8_exact(f.y, s, up), 0x0040);
-            else
-                c[e] = __nv_cvt_float2_to_fp8x2(make_float2(odd_quotient(f.x, s, up), odd_quotient(f.y, s, up)),
-                                                __NV_SATFINITE, __NV_E4M3);
-        }
-        o = make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
-    }
-    return o;
+    return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
 }
 
 template <int DT, int FMT>
@@ -245,10 +238,10 @@ __global__ void __launch_bounds__(kKvThreads) fl_kv_write_kernel(const __grid_co
     const Task k = task_of(p, t);
     const Lane<W, const uint16_t> l(p, p.src, k.i, lane);
     long long slot = 0;
-    for (int q0 = k.p0; q0 < k.p1; q0 += kPasses) {
-        uint4 v[kPasses][W];
+    for (int q0 = k.p0; q0 < k.p1; q0 += kWritePasses) {
+        uint4 v[kWritePasses][W];
 #pragma unroll
-        for (int j = 0; j < kPasses; ++j) {
+        for (int j = 0; j < kWritePasses; ++j) {
             const int q = q0 + j, w = q >= p.half, c = w ? q - p.half : q;
             const bool in = l.in && q < k.p1 && c * l.groups + l.grp < p.heads;
             const uint16_t* src = (w ? l.x[1] : l.x[0]) + c * (w ? l.step[1] : l.step[0]);
@@ -263,7 +256,7 @@ __global__ void __launch_bounds__(kKvThreads) fl_kv_write_kernel(const __grid_co
             }
         }
 #pragma unroll
-        for (int j = 0; j < kPasses; ++j) {
+        for (int j = 0; j < kWritePasses; ++j) {
             uint32_t m = absmax8<DT>(v[j][0]);
             if (W == 2) m = absmax2<DT>(m, absmax8<DT>(v[j][W - 1]));
             for (int o = 1 << p.lanes_log >> 1; o > 0; o >>= 1) m = absmax2<DT>(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -272,12 +265,12 @@ __global__ void __launch_bounds__(kKvThreads) fl_kv_write_kernel(const __grid_co
             m = absmax_halves<DT>(m);
             const bool fine = m < Bits16<DT>::kInf;
             const float s = fmaxf(DTypeOps<DT>::unpack(m).x * (1.0f / (FMT == FL_KV_INT8 ? 127.0f : 448.0f)), 0x1p-126f);
-            const float inv = rcp_approx(s), up = inv * (1.0f + 0x1p-21f), dn = inv * (1.0f - 0x1p-21f);
+            const Quant quant(s);
             const long long at = slot * p.heads + h;
             if (l.sub == 0) p.scale[w][at] = fine ? s : __int_as_float(0x7fffffff);
             uint2 c[W];
 #pragma unroll
-            for (int e = 0; e < W; ++e) c[e] = fine ? encode8<DT, FMT>(v[j][e], s, up, dn) : make_uint2(0u, 0u);
+            for (int e = 0; e < W; ++e) c[e] = fine ? encode8<DT, FMT>(v[j][e], quant) : make_uint2(0u, 0u);
             uint8_t* dst = p.cache[w] + at * p.head_dim + l.sub * (8 * W);
             if constexpr (W == 2)
                 *reinterpret_cast<uint4*>(dst) = make_uint4(c[0].x, c[0].y, c[1].x, c[1].y);

@@ -355,11 +355,8 @@ def test_codes_next_to_a_border():
                 r, q = fma(x, up, shift) - shift, fma(x, dn, shift) - shift
                 if r != q:
                     exact += 1
-                    y = f32(x * up)
-                    lo = np.floor(y)
-                    r = np.rint(y)
-                    if abs(f32(y - np.rint(y))) >= f32(0.499):
-                        d = fma(-(lo + f32(0.5)), s, x)
-                        r = lo + 1 if d > 0 else lo if d < 0 else f32(2) * np.rint(f32(0.5) * (lo + f32(0.5)))
+                    d = fma(-(r + q), f32(0.5) * s, x)
+                    takes_up = int(r) % 2 == 0 if d == 0 else (d > 0) == (x > 0)
+                    r = r if takes_up else q
                 assert int(r) == nearest_even(Fraction(float(x)) / Fraction(float(s)))
     assert exact > 20
