@@ -161,20 +161,9 @@ void set_weight(W4Params& p, int j, const fl_w4_weight* w) {
 
 constexpr int kMaxRows = 65000 * 256;  // token tiles of one grid
 
-// One product whose arguments have been checked. `normed`: where the rows go
-// that the tile kernel reads, x * gamma / rms rounded to the dtype.
-fl_status run(int dt, bool dual, const W4Params& p, void* normed, const host::LaunchContext& ctx, cudaStream_t stream) {
-    if (!w4_few_rows(p.M, p.K)) {
-        W4Params t = p;
-        if (p.gamma != nullptr) {
-            const fl_status st = host::launched(
-                launch_rms_norm(dt, p.x, p.gamma, normed, p.M, p.K, p.eps, ctx.pdl, ctx.sms, stream), "RMSNorm kernel");
-            if (st != FL_OK) return st;
-            t.x = static_cast<const uint16_t*>(normed);
-        }
-        return w4_tile(dt, dual, t, ctx, stream);
-    }
-    return w4_rows(dt, dual, p, ctx, stream);
+// One product whose arguments have been checked.
+fl_status run(int dt, bool dual, const W4Params& p, void* workspace, const host::LaunchContext& ctx, cudaStream_t stream) {
+    return w4_few_rows(p.M, p.K) ? w4_rows(dt, dual, p, ctx, stream) : w4_tile(dt, dual, p, workspace, ctx, stream);
 }
 
 fl_status check_workspace(const void* workspace, size_t bytes, size_t need) {
@@ -217,7 +206,7 @@ fl_status fl_w4_quantize(const void* W, void* q, void* scales, int N, int K, int
 }
 
 size_t fl_w4_gemm_workspace_size(int M, int K, int norm) {
-    return norm && M > 0 && K > 0 && !fl::w4_few_rows(M, K) ? (size_t)M * K * 2 : 0;
+    return M > 0 && K > 0 && !fl::w4_few_rows(M, K) ? fl::w4_tile_workspace(M, norm != 0) : 0;
 }
 
 fl_status fl_w4_gemm(const void* x, const void* gamma, const fl_w4_weight* W, const void* bias, const void* residual,
@@ -299,7 +288,7 @@ fl_status fl_w4_swiglu_ffn(const void* x, const void* gamma, const fl_w4_weight*
     host::LaunchContext ctx;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if ((st = host::launch_context(s, &ctx)) != FL_OK) return st;
-    // (h in front, then the tile kernel's normalised rows)
+    // (h in front, then the row scales of the tile kernel)
     // h = silu(RMSNorm(x) Wg^T) * (RMSNorm(x) Wu^T)
     W4Params p = {};
     p.x = static_cast<const uint16_t*>(x), p.gamma = static_cast<const uint16_t*>(gamma);

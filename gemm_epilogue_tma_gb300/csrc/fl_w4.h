@@ -27,8 +27,9 @@ struct W4Params {
 bool w4_few_rows(int M, int K);
 fl_status w4_rows(int dt, bool dual, const W4Params& p, const host::LaunchContext& ctx, cudaStream_t stream);
 
-// Tile kernel (fl_w4_tile.cu): no prologue, any number of rows.
-fl_status w4_tile(int dt, bool dual, const W4Params& p, const host::LaunchContext& ctx, cudaStream_t stream);
+// Tile kernel (fl_w4_tile.cu): any number of rows; the RMSNorm prologue keeps the rows' scales in the workspace.
+size_t w4_tile_workspace(int M, bool norm);
+fl_status w4_tile(int dt, bool dual, const W4Params& p, void* workspace, const host::LaunchContext& ctx, cudaStream_t stream);
 
 #ifdef __CUDACC__
 // (a & mask) | bits as one instruction (the compiler makes two of it when both are immediates)

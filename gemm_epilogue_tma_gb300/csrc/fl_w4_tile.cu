@@ -4,9 +4,16 @@
 // SwiGLU pair, 64 rows of Wg and the same rows of Wu) against up to 256 tokens,
 // so that the 4-bit codes are expanded where the MMA reads them: in tensor
 // memory. Each K step of 64 a dequantising thread owns one weight row: it reads
-// 32 bytes of codes from shared memory, forms scale * (code - zero) in the
-// dtype (one rounding) and writes its row of the A operand with tcgen05.st; the
-// tokens are the B operand, staged by TMA. 16-bit weights exist nowhere else.
+// 32 bytes of codes from shared memory, forms the weight in the dtype and writes
+// its row of the A operand with tcgen05.st; the tokens are the B operand, staged
+// by TMA. 16-bit weights exist nowhere else.
+//
+// Roundings: the weight is rounded once, scale * (code - zero), or with the
+// RMSNorm prologue scale * gamma * (code - zero), so that the tokens are
+// multiplied as they are (rounding x * gamma as well would be a third rounding
+// beside the weight's and the output's, and was 1.6 times the error of a plain
+// fp32 product rounded once). The row scale 1 / rms, from a kernel of its own
+// that reads x once, is applied to the fp32 sums.
 //
 // What bounds it: with many tokens the shared-memory traffic of the B operand
 // (per K step 256 * 128 bytes written by TMA and read by the MMA, against 590
@@ -14,26 +21,29 @@
 // cluster of up to 8 CTAs whose fp32 partials are added through distributed
 // shared memory in rank order. A tile of two blocks of 128 rows by 128 tokens
 // moved fewer bytes per MMA but expanded every code for half as many tokens, and the
-// expansion (about 440 instructions a warp and step) set its pace: 237 us at
+// expansion (about 200 instructions a warp and step) set its pace: 237 us at
 // 4096^3.
 //
-// Roles: warp 0 loads the tokens by TMA (stages of 64 k), warp 1 owns tensor
-// memory and issues the MMAs, warps 2 and 3 load the scales and zero points of
-// 1024 k at a time into shared memory (transposed: one row per thread there; the
-// first of them is loaded by the dequantising warps, which have nothing else to
-// do yet), warps 4-19 dequantise, four to a K step, and when the MMAs are done
-// apply the epilogue, warp 20 loads the codes by TMA (stages of 256 k). Codes
-// and tokens have producers of their own, so that the codes, which come from
-// HBM and are needed first, run ahead as far as their ring reaches; the fewer
-// the tokens, the more of shared memory is the codes'. A stage of tokens and the A
-// slot of the same step share one full and one empty barrier (the bytes and
-// the four warps' arrivals on the one, the MMA's commit on the other): the single
-// issuing thread competes with four dequantising warps for its scheduler, and a
-// step with two waits and two commits took it 680 to 850 cycles whatever the
-// tile's width.
+// Roles: warp 0 loads tokens (stages of 64 k) and codes (stages of 256 k) by
+// TMA, warp 1 owns tensor memory and issues the MMAs, warps 2 and 3 load the scales, zero points and
+// gamma of 1024 k at a time into shared memory (transposed: one row per thread
+// there; the first of them is loaded by the dequantising warps, which have
+// nothing else to do yet), warps 4-19 dequantise, four to a K step, and apply the
+// epilogue. (20 warps: a 21st would leave each thread 80 registers instead of
+// 96.) The producer loads codes whenever their ring has room, so that they,
+// which come from HBM and are needed first, run ahead as far as it reaches; the fewer the tokens, the more of shared memory is the codes'. A stage of tokens and the A slot of
+// the same step share one full and one empty barrier (the bytes and the four
+// warps' arrivals on the one, the MMA's commit on the other): the issuing warp
+// competes with four dequantising warps for its scheduler, and a step with two waits and two
+// commits took it 680 to 850 cycles whatever the tile's width.
+//
+// Without a split the CTAs are persistent: every ring runs on into the next
+// tile, and the dequantising warps expand the next tile's first steps before they apply
+// the epilogue, which holds the MMAs up only while the accumulator is read.
 //
 // Every mbarrier wait is bounded as in the other kernels.
 #include <atomic>
+#include <type_traits>
 
 #include "fl_common.cuh"
 #include "fl_host.h"
@@ -43,7 +53,7 @@ namespace fl {
 
 namespace {
 
-constexpr int kThreads = 672;
+constexpr int kThreads = 640;
 constexpr int kRows = 128;       // weight rows of a tile (TMEM lanes)
 constexpr int kTok = 256;        // tokens of a tile at most
 constexpr int kStep = 64;        // k per B stage and A slot
@@ -51,7 +61,7 @@ constexpr int kGroups = 4;       // dequantising warpgroups: K step kb goes to k
 constexpr int kWk = kGroups * kStep;  // k per code stage: one step of each warpgroup
 constexpr int kSIter = 4;        // code stages per scale stage
 constexpr int kSk = kSIter * kWk;
-constexpr int kStages = 2 * kGroups, kWStages = 8, kSStages = 2;  // (at most; stages of tokens: 4 or 8)
+constexpr int kStages = 2 * kGroups, kWStages = 8, kSStages = 2;  // (at most; stages of tokens: 4 to 8)
 constexpr int kRing = 192 * 1024;                   // both rings
 constexpr int kWBytes = kRows * kWk / 2;            // 16 KB
 constexpr int kSPitch = 130;                        // 16-bit scales of one group: 128 rows, padded
@@ -59,11 +69,13 @@ constexpr int kZPitch = 132;                        // zero-point bytes of one g
 constexpr int kSGroups = kSk / 32;
 constexpr int kSBytes = kSGroups * kSPitch * 2;
 constexpr int kZBytes = kSGroups * kZPitch;
+constexpr int kGBytes = kSk * 2;                    // gamma
 
 constexpr int kOffS = kRing;
 constexpr int kOffZ = kOffS + kSStages * kSBytes;
-constexpr int kOffBar = (kOffZ + kSStages * kZBytes + 7) / 8 * 8;
-constexpr int kBars = 2 * kStages + 2 * kWStages + 2 * kSStages + 2;
+constexpr int kOffG = (kOffZ + kSStages * kZBytes + 15) / 16 * 16;
+constexpr int kOffBar = kOffG + kSStages * kGBytes;
+constexpr int kBars = 2 * kStages + 2 * kWStages + 2 * kSStages + 3;
 constexpr int kOffSlot = kOffBar + kBars * 8;
 constexpr int kSmem = kOffSlot + 16 + 1024;         // + alignment slack
 static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
@@ -75,7 +87,9 @@ struct TileParams {
     CUtensorMap tm_x;     // x [M, K], box {64, BT}
     CUtensorMap tm_q[2];  // codes [N, K / 2] bytes, box {128, 128} (pair: {128, 64} each)
     W4Params w;
+    const float* row_scale;  // [M] 1 / rms of the rows of x (with gamma)
     int bt, splits, steps_per_split, steps;  // K steps of 64
+    int row_tiles, tiles;
     int stages, w_stages, b_bytes;           // rings: stages * b_bytes of tokens, then the code stages
     int* status;
     unsigned long long timeout_ns;
@@ -91,20 +105,51 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
     return d;
 }
 
-// Eight codes of a word, in order, as four pairs scale * (code - zero). The
-// code goes into the mantissa of a power of two B (128 bf16, 1024 fp16): the
-// even one as B + c, the odd one, taken from the word shifted by one, as
-// B + 8 c, and one FMA with (1, 1/8) and (-(B + z), -(B/8 + z)) leaves c - z,
-// exactly. The product with the scale is the one rounding.
+// a * b in fp32, of the halves of two 16-bit pairs (exact: at most 5 and 11 significant bits)
 template <int DT>
-__device__ __forceinline__ void dequant8(uint32_t w, uint32_t s2, uint32_t zc, uint32_t* out) {
+__device__ __forceinline__ float2 widening_mul(uint32_t a, uint32_t b) {
+    float2 r;
+    if constexpr (DT == DT_F16)
+        asm("{\n\t.reg .b16 al, ah, bl, bh;\n\tmov.b32 {al, ah}, %2;\n\tmov.b32 {bl, bh}, %3;\n\t"
+            "fma.rn.f32.f16 %0, al, bl, 0f80000000;\n\tfma.rn.f32.f16 %1, ah, bh, 0f80000000;\n\t}"
+            : "=f"(r.x), "=f"(r.y) : "r"(a), "r"(b));
+    else
+        asm("{\n\t.reg .b16 al, ah, bl, bh;\n\tmov.b32 {al, ah}, %2;\n\tmov.b32 {bl, bh}, %3;\n\t"
+            "fma.rn.f32.bf16 %0, al, bl, 0f80000000;\n\tfma.rn.f32.bf16 %1, ah, bh, 0f80000000;\n\t}"
+            : "=f"(r.x), "=f"(r.y) : "r"(a), "r"(b));
+    return r;
+}
+
+// Two fp32 products in one instruction.
+__device__ __forceinline__ float2 mul2_f32(float2 a, float b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %4};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b));
+    return d;
+}
+
+// Eight codes of a word, in order, as four pairs of weights. The code goes into
+// the mantissa of a power of two B (128 bf16, 1024 fp16): the even one as B + c,
+// the odd one, taken from the word shifted by one, as B + 8 c, and one FMA with
+// (1, 1/8) and (-(B + z), -(B/8 + z)) leaves c - z, exactly. The product with
+// the scale (s: its 16 bits twice) is the one rounding; with NORM gamma
+// (g: of the 8 k) is multiplied in first, in fp32 and exactly (s: its fp32 bits).
+template <int DT, bool NORM>
+__device__ __forceinline__ void dequant8(uint32_t w, uint32_t s, uint32_t zc, const uint4& g, uint32_t* out) {
     constexpr uint32_t kMagic = DT == DT_F16 ? 0x64006400u : 0x43004300u;
     constexpr uint32_t kUnit = DT == DT_F16 ? 0x30003c00u : 0x3e003f80u;  // (1, 1/8)
-    const uint32_t v = w >> 1;
+    const uint32_t v = w >> 1, gw[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t pair = __byte_perm(w, v, (uint32_t)(i * 0x1111 + 0x4400));  // bytes w.i, w.i, v.i, v.i
-        out[i] = DTypeOps<DT>::mul2(hfma2<DT>(and_or(pair, 0x0078000fu, kMagic), kUnit, zc), s2);
+        const uint32_t code = hfma2<DT>(and_or(pair, 0x0078000fu, kMagic), kUnit, zc);
+        if constexpr (NORM) {
+            const float2 f = mul2_f32(widening_mul<DT>(code, gw[i]), __uint_as_float(s));
+            out[i] = DTypeOps<DT>::pack(f.x, f.y);
+        } else {
+            out[i] = DTypeOps<DT>::mul2(code, s);
+        }
     }
 }
 
@@ -149,7 +194,40 @@ __device__ __forceinline__ void commit_elected(uint32_t bar) {
         : "memory");
 }
 
-template <int DT, bool DUAL>
+// 1 / rms of the rows of x [M, K]: one warp per row, eight vectors in flight per lane.
+template <int DT>
+__global__ void __launch_bounds__(256) fl_w4_row_scale_kernel(const uint16_t* __restrict__ x, float* __restrict__ scale,
+                                                              int M, int K, float eps) {
+    using Ops = DTypeOps<DT>;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const long long m = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (m >= M) return;
+    const uint16_t* row = x + m * K;
+    float s0 = 0.f, s1 = 0.f;
+    for (int k0 = lane * 8; k0 < K; k0 += 256 * 8) {
+        uint4 v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = k0 + u * 256 < K ? ldg_v4(row + k0 + u * 256) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 f = Ops::unpack(w[e]);
+                s0 = fmaf(f.x, f.x, s0);
+                s1 = fmaf(f.y, f.y, s1);
+            }
+        }
+    }
+    float s = s0 + s1;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) scale[m] = rsqrtf(s / (float)K + eps);
+}
+
+template <int DT, bool DUAL, bool NORM>
 __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_constant__ TileParams p) {
     using Ops = DTypeOps<DT>;
     extern __shared__ uint8_t smem_raw[];
@@ -164,19 +242,22 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
     auto wempty = [&](int s) { return bar0 + 8u * (2 * kStages + kWStages + s); };
     auto sfull = [&](int s) { return bar0 + 8u * (2 * kStages + 2 * kWStages + s); };
     auto sempty = [&](int s) { return bar0 + 8u * (2 * kStages + 2 * kWStages + kSStages + s); };
-    const uint32_t dfull = bar0 + 8u * (kBars - 2), drain = bar0 + 8u * (kBars - 1);
+    const uint32_t dfull = bar0 + 8u * (kBars - 3), dempty = bar0 + 8u * (kBars - 2), drain = bar0 + 8u * (kBars - 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tile = blockIdx.x / p.splits, rank = blockIdx.x % p.splits;
-    const int m0 = blockIdx.y * p.bt;
-    const int n0 = tile * (DUAL ? kRows / 2 : kRows);  // first weight row (of each weight of the pair)
+    const int first_tile = blockIdx.x / p.splits, tile_step = gridDim.x / p.splits, rank = blockIdx.x % p.splits;
     const int k0 = rank * p.steps_per_split, k1 = min(p.steps, k0 + p.steps_per_split), nk = k1 - k0;
+    const int its = (nk + kGroups - 1) / kGroups;        // code stages of a tile
+    const int s_count = (its + kSIter - 1) / kSIter;     // scale stages of a tile
     const int nb = p.stages, nw = p.w_stages;
     const uint32_t wring = sbase + (uint32_t)(nb * p.b_bytes);
+    // weight rows run fastest: the CTAs at work share a few tiles of tokens
+    auto row0_of = [&](int tile) { return tile % p.row_tiles * (DUAL ? kRows / 2 : kRows); };
+    auto token0_of = [&](int tile) { return tile / p.row_tiles * p.bt; };
     // weight and row of TMEM lane r: for the pair, each warp's lanes 0-15 are
     // rows of Wg and 16-31 the same rows of Wu
     auto weight_of = [&](int r) { return DUAL ? (r >> 4) & 1 : 0; };
-    auto row_of = [&](int r) { return n0 + (DUAL ? (r >> 5) * 16 + (r & 15) : r); };
+    auto row_in_tile = [&](int r) { return DUAL ? (r >> 5) * 16 + (r & 15) : r; };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -192,6 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
             mbar_init(sempty(s), 4 * kGroups);
         }
         mbar_init(dfull, 1);
+        mbar_init(dempty, 4 * kGroups);
         mbar_init(drain, 1);
         fence_mbar_init();
     }
@@ -209,30 +291,39 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kOffSlot);
     // the first codes towards L2 (the point of coherence) while the previous kernel finishes
-    if (warp == 20 && lane == 0) {
-        for (int i = 0; i < nw && i * kGroups < nk; ++i)
+    if (warp == 0 && lane == 0) {
+        for (int i = 0; i < nw && i < its; ++i)
             for (int j = 0; j <= (DUAL ? 1 : 0); ++j)
-                tma_prefetch_2d(&p.tm_q[j], k0 * (kStep / 2) + i * (kWk / 2), n0);
+                tma_prefetch_2d(&p.tm_q[j], k0 * (kStep / 2) + i * (kWk / 2), row0_of(first_tile));
     }
     griddep_wait();
     if (threadIdx.x == 0) griddep_launch_dependents();
 
-    // Scales and zero points of scale stage i into shared memory, by `count`
-    // threads: neighbouring threads take neighbouring groups of a row.
-    const int s_count = (nk * kStep + kSk - 1) / kSk;
-    auto load_scales = [&](int i, int tid, int count) {
+    // Scales, zero points and gamma of scale stage i of a tile into stage slot s
+    // of shared memory, by `count` threads: neighbouring threads take
+    // neighbouring groups of a row.
+    auto load_scales = [&](int tile, int i, int s, int tid, int count) {
         const int per_row = w.K / w.group, ng = kSk / w.group, sh = 31 - __clz(ng);  // groups of a row; of a stage (8, 16, 32)
         const int g0 = (k0 * kStep + i * kSk) / w.group, g_end = min(per_row, (k1 * kStep + w.group - 1) / w.group);
-        uint16_t* ds = reinterpret_cast<uint16_t*>(smem + kOffS + (i % kSStages) * kSBytes);
-        uint8_t* dz = smem + kOffZ + (i % kSStages) * kZBytes;
+        const int n0 = row0_of(tile);
+        uint16_t* ds = reinterpret_cast<uint16_t*>(smem + kOffS + s * kSBytes);
+        uint8_t* dz = smem + kOffZ + s * kZBytes;
         const bool zeros = w.zeros[0] != nullptr;
+        if (NORM) {
+            // (past K zeros: the tokens are zero there too)
+            uint4* dg = reinterpret_cast<uint4*>(smem + kOffG + s * kGBytes);
+            for (int e = tid; e < kSk / 8; e += count) {
+                const int k = k0 * kStep + i * kSk + e * 8;
+                dg[e] = k < w.K ? ldg_v4(w.gamma + k) : make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
         constexpr int U = 8;  // loads in flight per thread
         for (int b = tid; b < kRows << sh; b += count * U) {
             uint16_t v[U];
             uint8_t z[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int e = b + count * u, r = e >> sh, g = g0 + (e & (ng - 1)), n = row_of(r);
+                const int e = b + count * u, r = e >> sh, g = g0 + (e & (ng - 1)), n = n0 + row_in_tile(r);
                 const bool in = r < kRows && n < w.N && g < g_end;
                 const size_t at = in ? (size_t)n * per_row + g : 0;  // (0: a valid address whose value is not used)
                 v[u] = __ldg((weight_of(r) ? w.scales[1] : w.scales[0]) + at);
@@ -250,213 +341,272 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
         }
     };
 
-    bool ready = false;  // epilogue warps: the accumulator is complete
+    // ---------------------------------------------------------------- epilogue of the dequantising warps
+    const int grp = (warp - 4) >> 2, r = (threadIdx.x - 128) & 127;
+    const uint32_t dcol = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    // Outputs of tokens [t0, t0 + 4 T) of a tile, from this lane's accumulators of
+    // them (t0 and m0 multiples of 4). Lane pairs exchange, so that each stores two
+    // neighbouring outputs of a token at once.
+    auto emit = [&](auto T, int n0, int m0, int t0, const float* v) {
+        const int n = n0 + row_in_tile(r), nn = n & ~1;
+        const bool odd = lane & 1, up = lane & 16;
+        // this lane's first token: for the pair, gate lanes take tokens 0 and 2 of four, up lanes 1 and 3
+        const int mine = m0 + t0 + (DUAL ? (up ? 1 : 0) + (odd ? 2 : 0) : (odd ? 1 : 0));
+        const int end = nn < w.N ? min(w.M, m0 + p.bt) : 0;  // tokens below it are stored
+        uint16_t* out = w.out + (size_t)mine * w.N + nn;
+        const uint16_t* res = !DUAL && w.residual != nullptr ? w.residual + (size_t)mine * w.N + nn : nullptr;
+        const float bias = !DUAL && w.bias != nullptr && n < w.N ? Ops::unpack(w.bias[n]).x : 0.f;
+        // of two values, the one for the even lane stays there, the other goes over
+        auto exchange = [&](float v0, float v1) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+            return make_float2(odd ? got : v0, odd ? v1 : got);
+        };
+        auto store = [&](float2 y, int t, size_t at) {
+            if (mine + t >= end) return;
+            if (res != nullptr) {
+                const float2 x = Ops::unpack(*reinterpret_cast<const uint32_t*>(res + at));
+                y.x += x.x;
+                y.y += x.y;
+            }
+            *reinterpret_cast<uint32_t*>(out + at) = Ops::pack(y.x, y.y);
+        };
+        auto all = [&](auto act) {
+            size_t at = 0;
+#pragma unroll
+            for (int e = 0; e < 4 * decltype(T)::value; e += 4, at += 4 * (size_t)w.N) {
+                float a[4] = {v[e], v[e + 1], v[e + 2], v[e + 3]};
+                if (NORM) {
+                    const float4 rs = __ldg(reinterpret_cast<const float4*>(p.row_scale + m0 + t0 + e));
+                    a[0] *= rs.x;
+                    a[1] *= rs.y;
+                    a[2] *= rs.z;
+                    a[3] *= rs.w;
+                }
+                if constexpr (DUAL) {
+                    // lanes 16 apart hold the gate and the up value of a row
+                    const float o0 = __shfl_xor_sync(0xffffffffu, up ? a[0] : a[1], 16);
+                    const float o1 = __shfl_xor_sync(0xffffffffu, up ? a[2] : a[3], 16);
+                    store(exchange(act_apply(ACT_SILU, up ? o0 : a[0]) * (up ? a[1] : o0),
+                                   act_apply(ACT_SILU, up ? o1 : a[2]) * (up ? a[3] : o1)),
+                          e, at);
+                } else {
+                    store(exchange(act(a[0] + bias), act(a[1] + bias)), e, at);
+                    store(exchange(act(a[2] + bias), act(a[3] + bias)), e + 2, at + 2 * (size_t)w.N);
+                }
+            }
+        };
+        // (the activation is chosen once, not per value)
+        if (DUAL || w.act == ACT_NONE) all([](float y) { return y; });
+        else all([&](float y) { return act_apply(w.act, y); });
+    };
+    // Epilogue of the i-th tile of this CTA. false: the MMAs did not finish.
+    auto epilogue = [&](int tile, int i) {
+        if (!__all_sync(0xffffffffu, wait_bar(dfull, (uint32_t)(i & 1), p.status, p.timeout_ns, 28))) return false;
+        tc_fence_after();
+        const int n0 = row0_of(tile), m0 = token0_of(tile), chunks = (p.bt + 31) / 32;
+        auto release = [&] {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(dempty);
+        };
+        if (grp >= chunks) release();
+        for (int c = grp; c < chunks; c += kGroups) {
+            float v[32];
+            tmem_ld_32x32b_x32(dcol + 32u * c, reinterpret_cast<uint32_t(&)[32]>(v));
+            tmem_ld_wait();
+            if (p.splits == 1) {
+                if (c + kGroups >= chunks) release();
+                emit(std::integral_constant<int, 8>(), n0, m0, 32 * c, v);
+            } else {
+                // partial sums into this CTA's shared memory: [token][row]
+                float* part = reinterpret_cast<float*>(smem);
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (32 * c + e < p.bt) part[(32 * c + e) * kRows + r] = v[e];
+            }
+        }
+        return true;
+    };
+
     if (warp == 0) {
-        // ------------------------------------------------------------ tokens
+        // ------------------------------------------------------------ producer of tokens and codes
         if (lane == 0) {
-            int issued = 0, s = 0;
+            // Codes: the next stage's tile, index in it, ring slot and phase. They
+            // are loaded as soon as their ring has room, looked for once per step of
+            // tokens, and waited for only where that step needs them (so tokens never
+            // run ahead of codes, and the wait cannot be for itself).
+            int c_tile = first_tile, c_at = 0, c_s = 0, c_issued = 0, c_row = row0_of(first_tile);
+            uint32_t c_ph = 0;
+            auto load_codes = [&] {
+                mbar_arrive_expect_tx(wfull(c_s), kWBytes);
+                const uint32_t dst = wring + c_s * kWBytes;
+                const int x = (k0 + c_at * kGroups) * (kStep / 2);
+                tma_load_2d(dst, &p.tm_q[0], wfull(c_s), x, c_row);
+                if (DUAL) tma_load_2d(dst + kWBytes / 2, &p.tm_q[1], wfull(c_s), x, c_row);
+                ++c_issued;
+                if (++c_s == nw) c_s = 0, c_ph ^= 1u;
+                if (++c_at == its) c_at = 0, c_tile += tile_step, c_row = row0_of(c_tile);
+            };
+            int issued = 0, s = 0, stages = 0;  // token loads, their slot, code stages before this tile
             uint32_t ph = 0;
-            for (int kb = 0; kb < nk; ++kb) {
-                if (!wait_bar(empty(s), ph ^ 1u, p.status, p.timeout_ns, 21)) break;
-                mbar_arrive_expect_tx(full(s), (uint32_t)p.b_bytes);
-                tma_load_2d(sbase + s * p.b_bytes, &p.tm_x, full(s), (k0 + kb) * kStep, m0);
-                ++issued;
-                if (++s == nb) s = 0, ph ^= 1u;
+            bool ok = true;
+            for (int tile = first_tile; ok && tile < p.tiles; tile += tile_step, stages += its) {
+                const int t0 = token0_of(tile);
+                for (int kb = 0; kb < nk; ++kb) {
+                    if (c_issued <= stages + kb / kGroups) {
+                        if (!(ok = wait_bar(wempty(c_s), c_ph ^ 1u, p.status, p.timeout_ns, 20))) break;
+                        load_codes();
+                    } else if (c_tile < p.tiles && mbar_try_wait_cluster(wempty(c_s), c_ph ^ 1u)) {
+                        load_codes();
+                    }
+                    if (!(ok = wait_bar(empty(s), ph ^ 1u, p.status, p.timeout_ns, 21))) break;
+                    mbar_arrive_expect_tx(full(s), (uint32_t)p.b_bytes);
+                    tma_load_2d(sbase + s * p.b_bytes, &p.tm_x, full(s), (k0 + kb) * kStep, t0);
+                    ++issued;
+                    if (++s == nb) s = 0, ph ^= 1u;
+                }
             }
             // every load this thread issued lands before the CTA may exit
             for (int i = 1; i <= nb && i <= issued; ++i)
                 wait_bar_drain(full((issued - i) % nb), (uint32_t)(((issued - i) / nb) & 1), 20000000ull);
-        }
-    } else if (warp == 20) {
-        // ------------------------------------------------------------ codes
-        if (lane == 0) {
-            int issued = 0, s = 0;
-            uint32_t ph = 0;
-            for (int kb = 0; kb < nk; kb += kGroups) {
-                if (!wait_bar(wempty(s), ph ^ 1u, p.status, p.timeout_ns, 20)) break;
-                mbar_arrive_expect_tx(wfull(s), kWBytes);
-                const uint32_t dst = wring + s * kWBytes;
-                const int x = (k0 + kb) * (kStep / 2);
-                tma_load_2d(dst, &p.tm_q[0], wfull(s), x, n0);
-                if (DUAL) tma_load_2d(dst + kWBytes / 2, &p.tm_q[1], wfull(s), x, n0);
-                ++issued;
-                if (++s == nw) s = 0, ph ^= 1u;
-            }
-            for (int i = 1; i <= nw && i <= issued; ++i)
-                wait_bar_drain(wfull((issued - i) % nw), (uint32_t)(((issued - i) / nw) & 1), 20000000ull);
+            for (int i = 1; i <= nw && i <= c_issued; ++i)
+                wait_bar_drain(wfull((c_issued - i) % nw), (uint32_t)(((c_issued - i) / nw) & 1), 20000000ull);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer (the whole warp, converged)
         const uint32_t idesc = umma_idesc_f16(Ops::kFormat, 128, (uint32_t)p.bt);
         bool ok = true;
         uint32_t ph = 0;
-        for (int kb = 0, s = 0; kb < nk; ++kb) {
-            ok = __all_sync(0xffffffffu, wait_bar(full(s), ph, p.status, p.timeout_ns, 22));
-            if (!ok) break;
-            tc_fence_after();
-            mma_step(tmem, tmem + kACol + 32u * s, sw128_kmajor_desc(sbase + s * p.b_bytes), idesc, kb, empty(s));
-            if (++s == nb) s = 0, ph ^= 1u;
+        int s = 0, i = 0;
+        for (int tile = first_tile; ok && tile < p.tiles; tile += tile_step, ++i) {
+            // the previous tile's accumulator has been read
+            if (i > 0) ok = __all_sync(0xffffffffu, wait_bar(dempty, (uint32_t)((i - 1) & 1), p.status, p.timeout_ns, 29));
+            for (int kb = 0; ok && kb < nk; ++kb) {
+                ok = __all_sync(0xffffffffu, wait_bar(full(s), ph, p.status, p.timeout_ns, 22));
+                if (!ok) break;
+                tc_fence_after();
+                mma_step(tmem, tmem + kACol + 32u * s, sw128_kmajor_desc(sbase + s * p.b_bytes), idesc, kb, empty(s));
+                if (++s == nb) s = 0, ph ^= 1u;
+            }
+            if (ok) commit_elected(dfull);
         }
-        if (ok) commit_elected(dfull);
         // all MMAs issued by this warp complete before tensor memory is released
         commit_elected(drain);
         wait_bar_drain(drain, 0, 20000000ull);
     } else if (warp < 4) {
-        // ------------------------------------------------------------ scales and zero points of the later stages
-        for (int i = 1; i < s_count; ++i) {
-            const int s = i % kSStages;
-            if (!wait_bar(sempty(s), (uint32_t)((i / kSStages) & 1) ^ 1u, p.status, p.timeout_ns, 24)) break;
-            load_scales(i, threadIdx.x - 64, 64);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(sfull(s));
-        }
+        // ------------------------------------------------------------ scales and zero points of the stages after the first
+        int g = 0;  // scale stages so far
+        bool ok = true;
+        for (int tile = first_tile; ok && tile < p.tiles; tile += tile_step)
+            for (int i = 0; i < s_count; ++i, ++g) {
+                if (g == 0) continue;
+                const int s = g % kSStages;
+                if (!(ok = __all_sync(0xffffffffu, wait_bar(sempty(s), (uint32_t)((g / kSStages) & 1) ^ 1u, p.status, p.timeout_ns, 24))))
+                    break;
+                load_scales(tile, i, s, threadIdx.x - 64, 64);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sfull(s));
+            }
     } else {
         // ------------------------------------------------------------ dequantise, one row per thread
-        const int grp = (warp - 4) >> 2, r = (threadIdx.x - 128) & 127;
-        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const int gsh = 31 - __clz(w.group);
         // this row's codes of the warpgroup's K step in a code stage
-        const int srow = DUAL ? weight_of(r) * (kRows / 2) + (r >> 5) * 16 + (r & 15) : r;
+        const int srow = weight_of(r) * (kRows / 2) + row_in_tile(r);
         const uint32_t src0 = wring + srow * 128 + (((2 * grp) ^ (srow & 7)) << 4);
         const uint32_t src1 = wring + srow * 128 + (((2 * grp + 1) ^ (srow & 7)) << 4);
-        load_scales(0, threadIdx.x - 128, 512);
+        load_scales(first_tile, 0, 0, threadIdx.x - 128, 512);
         named_bar_sync(1, 512);
         bool ok = true;
-        int ws = 0, a = grp;
-        uint32_t wph = 0, ph = 0;
-        for (int it = 0, kb = grp; kb < nk; ++it, kb += kGroups) {
-            const int ss = it / kSIter % kSStages;
-            ok = wait_bar(wfull(ws), wph, p.status, p.timeout_ns, 25);
-            if (ok && it % kSIter == 0 && it > 0) {
-                // (stage 0's barrier has seen no phase for the first 1024 k)
-                const int i = it / kSIter, phases = i / kSStages - (ss == 0 ? 1 : 0);
-                ok = wait_bar(sfull(ss), (uint32_t)(phases & 1), p.status, p.timeout_ns, 26);
+        int ws = 0, g = 0, done = 0, last = -1;  // scale stages and tiles so far
+        int base = 0;                            // A slot of the tile's first step, and its phase
+        uint32_t wph = 0, base_ph = 0;
+        for (int tile = first_tile; ok && tile < p.tiles; tile += tile_step) {
+            int a = base + grp;
+            uint32_t aph = base_ph;
+            if (a >= nb) a -= nb, aph ^= 1u;
+            for (int it = 0; ok && it < its; ++it) {
+                const int ss = g % kSStages, kb = it * kGroups + grp;
+                ok = wait_bar(wfull(ws), wph, p.status, p.timeout_ns, 25);
+                if (ok && it % kSIter == 0 && g > 0) {
+                    // (the barrier of slot 0 saw no phase for the very first stage)
+                    const int phases = g / kSStages - (ss == 0 ? 1 : 0);
+                    ok = wait_bar(sfull(ss), (uint32_t)(phases & 1), p.status, p.timeout_ns, 26);
+                }
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                uint32_t o[32];
+                if (kb < nk) {
+                    const uint4 c0 = ld_shared_v4(src0 + ws * kWBytes), c1 = ld_shared_v4(src1 + ws * kWBytes);
+                    const uint16_t* ds = reinterpret_cast<const uint16_t*>(smem + kOffS + ss * kSBytes);
+                    const uint8_t* dz = smem + kOffZ + ss * kZBytes;
+                    const int kin = (it % kSIter) * kWk + grp * kStep;
+                    const int ga = kin >> gsh, gb = (kin + 32) >> gsh;
+                    uint32_t sa = ds[ga * kSPitch + r], sb = ds[gb * kSPitch + r];
+                    sa = NORM ? __float_as_uint(Ops::unpack(sa).x) : sa * 0x10001u;
+                    sb = NORM ? __float_as_uint(Ops::unpack(sb).x) : sb * 0x10001u;
+                    const uint32_t za = zero_const<DT>(dz[ga * kZPitch + r]), zb = zero_const<DT>(dz[gb * kZPitch + r]);
+                    const uint32_t sg = sbase + kOffG + ss * kGBytes + kin * 2;
+                    const uint32_t cw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint4 gv = NORM ? ld_shared_v4(sg + 16 * e) : make_uint4(0u, 0u, 0u, 0u);
+                        dequant8<DT, NORM>(cw[e], e < 4 ? sa : sb, e < 4 ? za : zb, gv, o + 4 * e);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(wempty(ws));
+                if (++ws == nw) ws = 0, wph ^= 1u;
+                if (it % kSIter == kSIter - 1 || it == its - 1) {
+                    if (lane == 0) mbar_arrive(sempty(ss));
+                    ++g;
+                }
+                if (kb < nk) {
+                    ok = __all_sync(0xffffffffu, wait_bar(empty(a), aph ^ 1u, p.status, p.timeout_ns, 27));
+                    if (!ok) break;
+                    tc_fence_after();
+                    tmem_st_32x32b_x32(dcol + kACol + 32u * a, o);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full(a));
+                    if ((a += kGroups) >= nb) a -= nb, aph ^= 1u;
+                }
+                // the tile before this one: its last MMAs ran while this tile's first steps were expanded
+                if (it == 0 && last >= 0) {
+                    ok = epilogue(last, done++);
+                    last = -1;
+                }
             }
-            if (!ok) break;
-            const uint4 c0 = ld_shared_v4(src0 + ws * kWBytes), c1 = ld_shared_v4(src1 + ws * kWBytes);
-            const uint16_t* ds = reinterpret_cast<const uint16_t*>(smem + kOffS + ss * kSBytes);
-            const uint8_t* dz = smem + kOffZ + ss * kZBytes;
-            const int kin = (it % kSIter) * kWk + grp * kStep;
-            const int ga = kin >> gsh, gb = (kin + 32) >> gsh;
-            const uint32_t sa = (uint32_t)ds[ga * kSPitch + r] * 0x10001u, sb = (uint32_t)ds[gb * kSPitch + r] * 0x10001u;
-            const uint32_t za = zero_const<DT>(dz[ga * kZPitch + r]), zb = zero_const<DT>(dz[gb * kZPitch + r]);
-            uint32_t o[32];
-            dequant8<DT>(c0.x, sa, za, o);
-            dequant8<DT>(c0.y, sa, za, o + 4);
-            dequant8<DT>(c0.z, sa, za, o + 8);
-            dequant8<DT>(c0.w, sa, za, o + 12);
-            dequant8<DT>(c1.x, sb, zb, o + 16);
-            dequant8<DT>(c1.y, sb, zb, o + 20);
-            dequant8<DT>(c1.z, sb, zb, o + 24);
-            dequant8<DT>(c1.w, sb, zb, o + 28);
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(wempty(ws));
-                if (it % kSIter == kSIter - 1) mbar_arrive(sempty(ss));
-            }
-            if (++ws == nw) ws = 0, wph ^= 1u;
-            ok = wait_bar(empty(a), ph ^ 1u, p.status, p.timeout_ns, 27);
-            if (!ok) break;
-            tc_fence_after();
-            tmem_st_32x32b_x32(tmem + lanes + kACol + 32u * a, o);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(full(a));
-            if ((a += kGroups) >= nb) a = grp, ph ^= 1u;
+            last = tile;
+            base += nk;
+            base_ph ^= (uint32_t)(base / nb) & 1u;
+            base %= nb;
         }
-        ready = ok && wait_bar(dfull, 0, p.status, p.timeout_ns, 28);
-        tc_fence_after();
+        if (ok && last >= 0) epilogue(last, done);
     }
 
-    // ---------------------------------------------------------------- epilogue
-    const bool epi = warp >= 4 && warp < 20;
-    const int grp = (warp - 4) >> 2, r = (threadIdx.x - 128) & 127;
-    const uint32_t dcol = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const int n = row_of(r), nn = n & ~1;
-    const float bias = epi && !DUAL && w.bias != nullptr && n < w.N ? Ops::unpack(w.bias[n]).x : 0.f;
-    // two neighbouring outputs of token m
-    auto store = [&](int m, float a, float b) {
-        if (m >= w.M || m >= m0 + p.bt || nn >= w.N) return;
-        const size_t at = (size_t)m * w.N + nn;
-        if (!DUAL && w.residual != nullptr) {
-            const float2 x = Ops::unpack(*reinterpret_cast<const uint32_t*>(w.residual + at));
-            a += x.x;
-            b += x.y;
-        }
-        *reinterpret_cast<uint32_t*>(w.out + at) = Ops::pack(a, b);
-    };
-    // of two values, the one for the even lane stays there, the other goes over: lane pairs then hold
-    // neighbouring outputs, of the first value's token in the even lane and the second's in the odd one
-    auto pair = [&](float v0, float v1, float& a, float& b) {
-        const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v0 : v1, 1);
-        a = (lane & 1) ? got : v0;
-        b = (lane & 1) ? v1 : got;
-    };
-    // accumulators of tokens m .. m + 3 at this lane's row
-    auto emit4 = [&](int m, float v0, float v1, float v2, float v3) {
-        float a, b;
-        if constexpr (DUAL) {
-            // lanes 16 apart hold the gate and the up value: the gate's lane takes tokens m and m + 2, the up's m + 1 and m + 3
-            const bool up = lane & 16;
-            const float o0 = __shfl_xor_sync(0xffffffffu, up ? v0 : v1, 16), o1 = __shfl_xor_sync(0xffffffffu, up ? v2 : v3, 16);
-            const float h0 = act_apply(ACT_SILU, up ? o0 : v0) * (up ? v1 : o0);
-            const float h1 = act_apply(ACT_SILU, up ? o1 : v2) * (up ? v3 : o1);
-            pair(h0, h1, a, b);
-            store(m + (up ? 1 : 0) + ((lane & 1) ? 2 : 0), a, b);
-        } else {
-            pair(act_apply(w.act, v0 + bias), act_apply(w.act, v1 + bias), a, b);
-            store(m + (lane & 1), a, b);
-            pair(act_apply(w.act, v2 + bias), act_apply(w.act, v3 + bias), a, b);
-            store(m + 2 + (lane & 1), a, b);
-        }
-    };
-    if (p.splits == 1) {
-        if (epi && __all_sync(0xffffffffu, ready)) {
-            for (int c = grp; c < (p.bt + 31) / 32; c += kGroups) {
-                uint32_t g[32];
-                tmem_ld_32x32b_x32(dcol + 32u * c, g);
-                tmem_ld_wait();
-#pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                    emit4(m0 + 32 * c + e, __uint_as_float(g[e]), __uint_as_float(g[e + 1]), __uint_as_float(g[e + 2]),
-                          __uint_as_float(g[e + 3]));
-            }
-        }
-    } else {
-        // partial sums into this CTA's shared memory: [token][row]
-        float* part = reinterpret_cast<float*>(smem);
-        if (epi && __all_sync(0xffffffffu, ready)) {
-            for (int c = grp; c < (p.bt + 31) / 32; c += kGroups) {
-                uint32_t g[32];
-                tmem_ld_32x32b_x32(dcol + 32u * c, g);
-                tmem_ld_wait();
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    if (32 * c + e < p.bt) part[(32 * c + e) * kRows + r] = __uint_as_float(g[e]);
-            }
-        }
+    if (p.splits > 1) {
         __syncwarp();
         cluster_barrier_sync();
-        // each rank finishes its range of tokens
-        if (epi) {
+        // each rank finishes its range of tokens of the cluster's one tile
+        if (warp >= 4) {
+            const int n0 = row0_of(first_tile), m0 = token0_of(first_tile);
             const int per = ((p.bt + p.splits - 1) / p.splits + 3) & ~3;
             const int t1 = min(p.bt, (rank + 1) * per);
             for (int t = rank * per + 4 * grp; t < t1; t += 4 * kGroups) {
-                float v[4][8];
+                float v[8][4];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     if (i >= p.splits) break;
                     const uint32_t a = mapa_cluster(sbase + (uint32_t)(t * kRows + r) * 4u, (uint32_t)i);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e][i] = ld_cluster_f32(a + e * kRows * 4);
+                    for (int e = 0; e < 4; ++e) v[i][e] = ld_cluster_f32(a + e * kRows * 4);
                 }
 #pragma unroll
                 for (int i = 1; i < 8; ++i)
                     if (i < p.splits)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) v[e][0] += v[e][i];
-                emit4(m0 + t, v[0][0], v[1][0], v[2][0], v[3][0]);
+                        for (int e = 0; e < 4; ++e) v[0][e] += v[i][e];
+                emit(std::integral_constant<int, 1>(), n0, m0, t, v[0]);
             }
         }
         __syncwarp();
@@ -471,11 +621,11 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
     }
 }
 
-template <int DT, bool DUAL>
+template <int DT, bool DUAL, bool NORM>
 struct Kern {
     static cudaError_t configure() {
         static const cudaError_t e = [] {
-            auto k = fl_w4_tile_kernel<DT, DUAL>;
+            auto k = fl_w4_tile_kernel<DT, DUAL, NORM>;
             cudaError_t r = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
             return r;
         }();
@@ -501,7 +651,7 @@ struct Kern {
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute a[2];
         config(cfg, a, grid, p.splits, pdl, s);
-        return cudaLaunchKernelEx(&cfg, fl_w4_tile_kernel<DT, DUAL>, p);
+        return cudaLaunchKernelEx(&cfg, fl_w4_tile_kernel<DT, DUAL, NORM>, p);
     }
     // clusters of `splits` CTAs that are resident at once
     static int resident(int splits) {
@@ -510,7 +660,7 @@ struct Kern {
         cudaLaunchAttribute a[2];
         config(cfg, a, dim3((unsigned)splits), splits, 0, nullptr);
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, fl_w4_tile_kernel<DT, DUAL>, &cfg) != cudaSuccess) {
+        if (cudaOccupancyMaxActiveClusters(&n, fl_w4_tile_kernel<DT, DUAL, NORM>, &cfg) != cudaSuccess) {
             cudaGetLastError();
             return 0;
         }
@@ -520,34 +670,49 @@ struct Kern {
 
 }  // namespace
 
-fl_status w4_tile(int dt, bool dual, const W4Params& w, const host::LaunchContext& ctx, cudaStream_t stream) {
+size_t w4_tile_workspace(int M, bool norm) { return norm ? ((size_t)M + kTok + 32) * sizeof(float) : 0; }
+
+fl_status w4_tile(int dt, bool dual, const W4Params& w, void* workspace, const host::LaunchContext& ctx, cudaStream_t stream) {
     TileParams p;
+    const bool norm = w.gamma != nullptr;
+    p.row_scale = nullptr;
+    if (norm) {
+        float* scale = static_cast<float*>(workspace);
+        p.row_scale = scale;
+        const dim3 grid((unsigned)((w.M + 7) / 8));
+        auto kern = dt == FL_F16 ? fl_w4_row_scale_kernel<DT_F16> : fl_w4_row_scale_kernel<DT_BF16>;
+        const fl_status st = host::launched(host::launch(kern, grid, 256, 0, ctx.pdl, stream, w.x, scale, w.M, w.K, w.eps),
+                                            "row scale kernel");
+        if (st != FL_OK) return st;
+    }
     p.steps = (w.K + kStep - 1) / kStep;
     const int rows = dual ? kRows / 2 : kRows, row_tiles = (w.N + rows - 1) / rows;
-    // Tokens of a tile and K split: the least time of whole waves of resident
-    // clusters. A K step costs the MMA and its shared-memory traffic (2.7
-    // cycles a token) or the expansion of its codes (about 300), whichever is
-    // more; a split adds the exchange of the partial sums. Ranges of a split
-    // are multiples of 128 k, the largest group.
+    // Tokens of a tile and K split: the least time of whole rounds of resident
+    // CTAs or clusters. A K step costs the MMA and its shared-memory traffic
+    // (2.7 cycles a token) or the expansion of its codes (about 300), whichever
+    // is more; a round its epilogue, a split the exchange of the partial sums.
+    // Ranges of a split are multiples of 128 k, the largest group.
     static std::atomic<int> resident[9];
     double least = 0;
     const int tt0 = (w.M + kTok - 1) / kTok;
     int token_tiles = 0;
-    for (int tt = tt0; tt <= tt0 + 2 && tt <= w.M; ++tt) {
+    for (int tt = tt0; tt <= 3 * tt0 && tt <= tt0 + 64; ++tt) {
         const int bt = ((w.M + tt - 1) / tt + 15) / 16 * 16;
+        if (tt > tt0 && bt < 64) break;
         for (int s = 1; s <= 8; ++s) {
             const int per = ((p.steps + 1) / 2 + s - 1) / s * 2;
             if (s > 1 && (per < 4 || (p.steps + per - 1) / per != s)) continue;
             int n = resident[s].load();
             if (n == 0) {
-                n = Kern<DT_BF16, false>::resident(s);
+                n = Kern<DT_BF16, false, false>::resident(s);
                 if (n <= 0) n = -1;
                 resident[s] = n;
             }
             if (n < 0) continue;
-            const long long waves = ((long long)row_tiles * tt + n - 1) / n;
+            const double rounds = (double)(((long long)row_tiles * tt + n - 1) / n);
             const double step = 2.7 * bt > 300.0 ? 2.7 * bt : 300.0;
-            const double cost = (double)waves * (step * per + 4000.0 + (s > 1 ? 1500.0 + 12.0 * bt : 0.0));
+            const double cost = s == 1 ? 8000.0 + rounds * (step * per + 1500.0)
+                                       : rounds * (step * per + 9500.0 + 12.0 * bt);
             if (token_tiles == 0 || cost < least) {
                 least = cost;
                 token_tiles = tt;
@@ -558,9 +723,14 @@ fl_status w4_tile(int dt, bool dual, const W4Params& w, const host::LaunchContex
         }
     }
     if (token_tiles == 0) return host::fail(FL_ERR_CUDA, "4-bit tile kernel: no resident CTA");
-    // rings: eight stages of tokens where they leave half of shared memory to the codes, else four
+    const long long tiles = (long long)row_tiles * token_tiles;
+    if (tiles * p.splits > 0x7fffffffll) return host::fail(FL_ERR_UNSUPPORTED, "4-bit tile kernel: too many tiles");
+    p.row_tiles = row_tiles;
+    p.tiles = (int)tiles;
+    // rings: as many stages of tokens as leave the codes two stages, eight at most; the rest to the codes
     p.b_bytes = p.bt * kStep * 2;
-    p.stages = 2 * kGroups * p.b_bytes <= kRing / 2 ? 2 * kGroups : kGroups;
+    p.stages = (kRing - 2 * kWBytes) / p.b_bytes;
+    if (p.stages > kStages) p.stages = kStages;
     p.w_stages = (kRing - p.stages * p.b_bytes) / kWBytes;
     if (p.w_stages > kWStages) p.w_stages = kWStages;
     fl_status st;
@@ -571,12 +741,19 @@ fl_status w4_tile(int dt, bool dual, const W4Params& w, const host::LaunchContex
     p.w = w;
     p.status = ctx.status;
     p.timeout_ns = ctx.timeout_ns;
-    const dim3 grid((unsigned)(row_tiles * p.splits), (unsigned)token_tiles);
+    const int persistent = resident[1].load() > 0 ? resident[1].load() : ctx.sms;
+    const dim3 grid((unsigned)(p.splits > 1 ? p.tiles * p.splits : p.tiles < persistent ? p.tiles : persistent));
     cudaError_t e;
+    if (dual && !norm) return host::fail(FL_ERR_UNSUPPORTED, "4-bit tile kernel: the pair needs gamma");
+#define FL_LAUNCH(DT)                                                                                      \
+    e = dual ? Kern<DT, true, true>::launch(p, grid, ctx.pdl, stream)                                      \
+             : norm ? Kern<DT, false, true>::launch(p, grid, ctx.pdl, stream)                              \
+                    : Kern<DT, false, false>::launch(p, grid, ctx.pdl, stream)
     if (dt == FL_F16)
-        e = dual ? Kern<DT_F16, true>::launch(p, grid, ctx.pdl, stream) : Kern<DT_F16, false>::launch(p, grid, ctx.pdl, stream);
+        FL_LAUNCH(DT_F16);
     else
-        e = dual ? Kern<DT_BF16, true>::launch(p, grid, ctx.pdl, stream) : Kern<DT_BF16, false>::launch(p, grid, ctx.pdl, stream);
+        FL_LAUNCH(DT_BF16);
+#undef FL_LAUNCH
     return host::launched(e, "4-bit tile kernel");
 }
 
