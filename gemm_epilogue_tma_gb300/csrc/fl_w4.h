@@ -20,10 +20,11 @@ struct W4Params {
     const uint16_t* residual;  // [M, N] or null
     uint16_t* out;             // [M, N]
     int M, N, K, group, act;
+    int slab;                  // decode kernel: rows of one half of the grid
     float eps;
 };
 
-// Decode kernel (fl_w4_rows.cu): up to 8 rows that fit in shared memory, with the RMSNorm prologue.
+// Decode kernel (fl_w4_rows.cu): up to 16 rows that fit in shared memory, with the RMSNorm prologue.
 bool w4_few_rows(int M, int K);
 fl_status w4_rows(int dt, bool dual, const W4Params& p, const host::LaunchContext& ctx, cudaStream_t stream);
 

@@ -1,4 +1,4 @@
-// 4-bit products for one to eight rows: the weight as a stream.
+// 4-bit products for one to sixteen rows: the weight as a stream.
 //
 // The step is bound by reading the codes once (0.5 bytes a weight and 2 per
 // group), and next to that by turning them into operands. The weight is the A
@@ -18,6 +18,11 @@
 // Loads run in blocks of 16 (V = 1: 8) words of each of the lane's two weight rows,
 // double-buffered across units (16 or 8 + 8 weight rows); a CTA's 8 warps take
 // 8 slices of K and add their sums through shared memory in warp order.
+//
+// Nine to sixteen rows are two slabs of at most eight, one to each half of the
+// grid: both halves walk the weight at the same pace, so the second reading of it
+// comes from L2. (The tensor-core tile kernel, which expands each code once for all
+// rows, takes 81 us for the 4096 x 11008 FFN at 16 rows.)
 #include "fl_common.cuh"
 #include "fl_host.h"
 #include "fl_w4.h"
@@ -202,9 +207,9 @@ __device__ __forceinline__ uint4 pair_up(const uint4& v) {
 // RMS row scale in rscale. Vector v of a row (8 k) goes to the place where the
 // quad reads it: group v / 4V, word v % V of lane v / V % 4. R: a bound on M.
 template <int DT, bool NORM, int R, int V, typename Pre>
-__device__ void build_rows(const W4Params& p, uint4* xs, float* rscale, Pre pre) {
+__device__ void build_rows(const W4Params& p, const uint16_t* x, int M, uint4* xs, float* rscale, Pre pre) {
     using Ops = DTypeOps<DT>;
-    const int M = p.M, vecs = p.K / 8, ld = row_vecs(p.K);
+    const int vecs = p.K / 8, ld = row_vecs(p.K);
     __shared__ float part[kWarps][R];
     float sq[R];
 #pragma unroll
@@ -220,7 +225,7 @@ __device__ void build_rows(const W4Params& p, uint4* xs, float* rscale, Pre pre)
                 if (NORM) gv[j] = ldg_v4(p.gamma + (size_t)c * 8);
 #pragma unroll
                 for (int m = 0; m < R; ++m)
-                    if (m < M) v[j][m] = ldg_v4(p.x + (size_t)m * p.K + (size_t)c * 8);
+                    if (m < M) v[j][m] = ldg_v4(x + (size_t)m * p.K + (size_t)c * 8);
             }
         }
         if (first) pre();
@@ -274,6 +279,9 @@ __global__ void __launch_bounds__(kThreads, 2) fl_w4_rows_kernel(const __grid_co
     __shared__ float rscale[8];
     __shared__ float4 red[2][kWarps][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    // this half's rows
+    const int m0 = blockIdx.y * p.slab, M = min(p.slab, p.M - m0);
+    const uint16_t* x = p.x + (size_t)m0 * p.K;
     const int groups = p.K / (32 * V), units = DUAL ? p.N / 8 : (p.N + 15) / 16;
     const int per = (groups + kWarps - 1) / kWarps, s0 = min(groups, warp * per), s1 = min(groups, s0 + per);
     constexpr int U = Block<V>::U;
@@ -283,9 +291,9 @@ __global__ void __launch_bounds__(kThreads, 2) fl_w4_rows_kernel(const __grid_co
     // warp's first codes: L2 is the point of coherence, so a prefetch before the
     // dependency wait cannot bring in stale data
     {
-        const int xl = (p.M * p.K * 2 + 127) / 128;
+        const int xl = (M * p.K * 2 + 127) / 128;
         for (int i = (int)(threadIdx.x * gridDim.x + blockIdx.x); i < xl; i += kThreads * gridDim.x)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(p.x) + (size_t)i * 128));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char*>(x) + (size_t)i * 128));
         // 128-byte lines of the slice: 256 codes each
         for (int c = s0 * 16 * V + t * 128; c < s1 * 16 * V && c < s0 * 16 * V + 512; c += 512) {
             asm volatile("prefetch.global.L2 [%0];" ::"l"(rows.q[0] + c));
@@ -296,17 +304,17 @@ __global__ void __launch_bounds__(kThreads, 2) fl_w4_rows_kernel(const __grid_co
     Block<V> A, B;
     auto pre = [&] { load_block<V, Z>(A, rows, s0, s1, t); };
     if (p.gamma != nullptr) {
-        if (p.M <= 2) build_rows<DT, true, 2, V>(p, xs, rscale, pre);
-        else if (p.M <= 4) build_rows<DT, true, 4, V>(p, xs, rscale, pre);
-        else build_rows<DT, true, 8, V>(p, xs, rscale, pre);
+        if (M <= 2) build_rows<DT, true, 2, V>(p, x, M, xs, rscale, pre);
+        else if (M <= 4) build_rows<DT, true, 4, V>(p, x, M, xs, rscale, pre);
+        else build_rows<DT, true, 8, V>(p, x, M, xs, rscale, pre);
     } else {
         if (threadIdx.x < 8) rscale[threadIdx.x] = 1.f;
-        if (p.M <= 4) build_rows<DT, false, 4, V>(p, xs, rscale, pre);
-        else build_rows<DT, false, 8, V>(p, xs, rscale, pre);
+        if (M <= 4) build_rows<DT, false, 4, V>(p, x, M, xs, rscale, pre);
+        else build_rows<DT, false, 8, V>(p, x, M, xs, rscale, pre);
     }
     griddep_launch_dependents();
     // (a column of the MMA past the last row is not used: any row will do)
-    const uint4* xrow = xs + (g < p.M ? g : 0) * row_vecs(p.K) + t;
+    const uint4* xrow = xs + (g < M ? g : 0) * row_vecs(p.K) + t;
 
     int q = 0, buf = 0;
     for (int u = blockIdx.x; u < units; u += gridDim.x, buf ^= 1) {
@@ -327,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 2) fl_w4_rows_kernel(const __grid_co
         __syncthreads();
         // One thread per output: lane (g, t) of the sums holds weight rows g and
         // g + 8 (gate and up) and activation rows 2 t and 2 t + 1.
-        if (threadIdx.x < (DUAL ? 8 : 16) * p.M) {
+        if (threadIdx.x < (DUAL ? 8 : 16) * M) {
             const int m = threadIdx.x / (DUAL ? 8 : 16), r = threadIdx.x % (DUAL ? 8 : 16);
             const float* src = &red[buf][0][(r & 7) * 4 + (m >> 1)].x + (m & 1) + (r >> 3) * 2;
             const float rs = rscale[m];
@@ -338,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 2) fl_w4_rows_kernel(const __grid_co
                 if (DUAL) up += src[w * 128 + 2];
             }
             const int n = DUAL ? u * 8 + r : u * 16 + r;
-            const size_t at = (size_t)m * p.N + n;
+            const size_t at = (size_t)(m0 + m) * p.N + n;
             if constexpr (DUAL) {
                 p.out[at] = (uint16_t)(Ops::pack(act_apply(ACT_SILU, y * rs) * (up * rs), 0.f) & 0xffffu);
             } else if (n < p.N) {
@@ -354,21 +362,27 @@ __global__ void __launch_bounds__(kThreads, 2) fl_w4_rows_kernel(const __grid_co
     }
 }
 
+int slabs_of(int M) { return (M + 7) / 8; }
+int slab_rows(int M) { return (M + slabs_of(M) - 1) / slabs_of(M); }
+
 template <int DT, bool DUAL, int V, bool Z>
 cudaError_t launch_rows(const W4Params& p, const host::LaunchContext& ctx, cudaStream_t stream) {
     auto kern = fl_w4_rows_kernel<DT, DUAL, V, Z>;
     static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (attr != cudaSuccess) return attr;
-    const int smem = smem_bytes(p.M, p.K), units = DUAL ? p.N / 8 : (p.N + 15) / 16;
-    const int most = ctx.sms * (smem <= 104 * 1024 ? 2 : 1);  // resident CTAs
-    return host::launch(kern, dim3((unsigned)(units < most ? units : most)), kThreads, (size_t)smem, ctx.pdl, stream, p);
+    const int slabs = slabs_of(p.M), smem = smem_bytes(p.slab, p.K), units = DUAL ? p.N / 8 : (p.N + 15) / 16;
+    const int most = ctx.sms * (smem <= 104 * 1024 ? 2 : 1) / slabs;  // resident CTAs of a slab
+    return host::launch(kern, dim3((unsigned)(units < most ? units : most), (unsigned)slabs), kThreads, (size_t)smem, ctx.pdl,
+                        stream, p);
 }
 
 }  // namespace
 
-bool w4_few_rows(int M, int K) { return M <= 8 && smem_bytes(M, K) <= kSmemMax; }
+bool w4_few_rows(int M, int K) { return M <= 16 && smem_bytes(slab_rows(M), K) <= kSmemMax; }
 
-fl_status w4_rows(int dt, bool dual, const W4Params& p, const host::LaunchContext& ctx, cudaStream_t stream) {
+fl_status w4_rows(int dt, bool dual, const W4Params& params, const host::LaunchContext& ctx, cudaStream_t stream) {
+    W4Params p = params;
+    p.slab = slab_rows(p.M);
     cudaError_t e = cudaErrorInvalidValue;
 #define FL_CASE(DT, DUAL, V)                                             \
     if (dt == DT && dual == DUAL && p.group == 32 * V)                   \

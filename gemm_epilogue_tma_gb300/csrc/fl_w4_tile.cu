@@ -169,21 +169,24 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
 // columns each; B 32 bytes further along its swizzled rows) and the commit that
 // frees the step's stage, issued by one elected lane. Operands computed by the
 // converged warp stay in uniform registers, where the instructions take them
-// from; under a divergent `lane == 0` each MMA waits for its operands to be moved there.
-__device__ __forceinline__ void mma_step(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t bar) {
+// from; under a divergent `lane == 0` each MMA waits for its operands to be moved
+// there (487 cycles a step at least, measured alone, against 200).
+__device__ __forceinline__ void mma_step(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, uint32_t acc,
+                                         uint32_t bar) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b32 r, a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 r, a1, a2, a3, l1, l2, l3;\n\t.reg .b64 b0, b1, b2, b3;\n\t"
         "elect.sync r|p, 0xffffffff;\n\t"
-        "setp.ne.b32 q, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
         "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
-        "add.u64 b1, %2, 2;\n\tadd.u64 b2, %2, 4;\n\tadd.u64 b3, %2, 6;\n\t"
-        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, q;\n\t"
+        "add.u32 l1, %2, 2;\n\tadd.u32 l2, %2, 4;\n\tadd.u32 l3, %2, 6;\n\t"
+        "mov.b64 b0, {%2, %3};\n\tmov.b64 b1, {l1, %3};\n\tmov.b64 b2, {l2, %3};\n\tmov.b64 b3, {l3, %3};\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b0, %4, q;\n\t"
         "setp.eq.u32 q, 0, 0;\n\t"
-        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n\t"
-        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, q;\n\t"
-        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, q;\n\t"
-        "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(bar)
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %4, q;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %4, q;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %4, q;\n\t"
+        "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n\t}" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc), "r"(bar)
         : "memory");
 }
 
@@ -474,19 +477,28 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer (the whole warp, converged)
+        // The next step's barrier is tested while this step's MMAs are issued, and
+        // tensor memory's base is taken as what it is when all 512 columns are
+        // allocated: 0, so that no operand comes from a register of the warp.
         const uint32_t idesc = umma_idesc_f16(Ops::kFormat, 128, (uint32_t)p.bt);
+        const uint64_t desc = sw128_kmajor_desc(sbase);
+        const uint32_t lo0 = (uint32_t)desc, hi = (uint32_t)(desc >> 32), lo_step = (uint32_t)p.b_bytes >> 4;
         bool ok = true;
-        uint32_t ph = 0;
-        int s = 0, i = 0;
-        for (int tile = first_tile; ok && tile < p.tiles; tile += tile_step, ++i) {
+        uint32_t ph = 0, lo = lo0, slot = 0, ready = 0;
+        for (int tile = first_tile, i = 0; ok && tile < p.tiles; tile += tile_step, ++i) {
             // the previous tile's accumulator has been read
             if (i > 0) ok = __all_sync(0xffffffffu, wait_bar(dempty, (uint32_t)((i - 1) & 1), p.status, p.timeout_ns, 29));
             for (int kb = 0; ok && kb < nk; ++kb) {
-                ok = __all_sync(0xffffffffu, wait_bar(full(s), ph, p.status, p.timeout_ns, 22));
-                if (!ok) break;
+                if (!__all_sync(0xffffffffu, ready) &&
+                    !(ok = __all_sync(0xffffffffu, wait_bar(full(slot), ph, p.status, p.timeout_ns, 22))))
+                    break;
                 tc_fence_after();
-                mma_step(tmem, tmem + kACol + 32u * s, sw128_kmajor_desc(sbase + s * p.b_bytes), idesc, kb, empty(s));
-                if (++s == nb) s = 0, ph ^= 1u;
+                const uint32_t now = slot, now_lo = lo;
+                ++slot;
+                lo += lo_step;
+                if (slot == (uint32_t)nb) slot = 0, lo = lo0, ph ^= 1u;
+                ready = mbar_try_wait_cluster(full(slot), ph);
+                mma_step(0u, kACol + 32u * now, now_lo, hi, idesc, (uint32_t)kb, empty(now));
             }
             if (ok) commit_elected(dfull);
         }
@@ -688,10 +700,11 @@ fl_status w4_tile(int dt, bool dual, const W4Params& w, void* workspace, const h
     p.steps = (w.K + kStep - 1) / kStep;
     const int rows = dual ? kRows / 2 : kRows, row_tiles = (w.N + rows - 1) / rows;
     // Tokens of a tile and K split: the least time of whole rounds of resident
-    // CTAs or clusters. A K step costs the MMA and its shared-memory traffic
-    // (2.7 cycles a token) or the expansion of its codes (about 300), whichever
-    // is more; a round its epilogue, a split the exchange of the partial sums.
-    // Ranges of a split are multiples of 128 k, the largest group.
+    // CTAs or clusters, in cycles as measured. A K step costs the MMA (2.2 a
+    // token) or, below some 260 tokens, what its warps need to expand the codes and
+    // to issue it (570; 690 with gamma, which is multiplied in in fp32); a round
+    // its epilogue, a split the exchange of the partial sums. Ranges of a split
+    // are multiples of 128 k, the largest group.
     static std::atomic<int> resident[9];
     double least = 0;
     const int tt0 = (w.M + kTok - 1) / kTok;
@@ -710,9 +723,9 @@ fl_status w4_tile(int dt, bool dual, const W4Params& w, void* workspace, const h
             }
             if (n < 0) continue;
             const double rounds = (double)(((long long)row_tiles * tt + n - 1) / n);
-            const double step = 2.7 * bt > 300.0 ? 2.7 * bt : 300.0;
-            const double cost = s == 1 ? 8000.0 + rounds * (step * per + 1500.0)
-                                       : rounds * (step * per + 9500.0 + 12.0 * bt);
+            const double least_step = norm ? 690.0 : 570.0, step = 2.2 * bt > least_step ? 2.2 * bt : least_step;
+            const double cost = s == 1 ? 5000.0 + rounds * (step * per + 6000.0)
+                                       : rounds * (step * per + 11000.0 + 12.0 * bt);
             if (token_tiles == 0 || cost < least) {
                 least = cost;
                 token_tiles = tt;
