@@ -84,7 +84,7 @@ struct DeviceInfo {
     // the library's own, so the process's default pool keeps its settings
     cudaMemPool_t pool = nullptr;
 };
-constexpr int kMaxDevices = 64;
+constexpr int kMaxDevices = 64;  // (allow_smem keeps one bit for each)
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_dev_mu;
 
@@ -944,6 +944,7 @@ fl_status launch_context(cudaStream_t stream, LaunchContext* ctx) {
     const fl_status st = device_info(&di);
     if (st != FL_OK) return st;
     const int slot = status_slot(di, stream);
+    ctx->device = (int)(di - g_dev);
     ctx->sms = di->sms;
     ctx->status = di->status + slot;
     ctx->range = di->range + slot;

@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -21,6 +22,7 @@ fl_status ok();
 // stream's status word (bounded waits) and range word (indexes a kernel found
 // outside their tables), and the launch options.
 struct LaunchContext {
+    int device;
     int sms;
     int* status;
     int* range;
@@ -54,6 +56,16 @@ inline bool valid_dtype(int dt) { return dt == FL_F16 || dt == FL_BF16; }
 fl_status encode_matrix(CUtensorMap* m, int dt, int elem_bytes, const void* ptr, uint64_t inner, uint64_t outer,
                         uint32_t box_inner, uint32_t box_outer);
 
+// Lets `kern` use `bytes` of dynamic shared memory on `device`; asked of the
+// runtime once per device (`done`: its bit is set).
+template <typename Kern>
+cudaError_t allow_smem(Kern kern, int bytes, int device, std::atomic<unsigned long long>& done) {
+    if (done.load(std::memory_order_relaxed) >> device & 1) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(1ull << device, std::memory_order_relaxed);
+    return e;
+}
+
 // cudaLaunchKernelEx with the programmatic-dependency attribute of the library's launches.
 template <typename Kern, typename... Args>
 cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, int pdl, cudaStream_t stream, const Args&... args) {
@@ -71,4 +83,9 @@ cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, int pdl, cuda
 }
 
 }  // namespace host
+
+// The argument checks of fl_rope and fl_kv_write alone (fl_layer_attach_cache).
+fl_status check_rope(const fl_rope_desc* desc);
+fl_status check_kv_write(const fl_kv_desc* desc);
+
 }  // namespace fl

@@ -163,7 +163,7 @@ constexpr int kMaxRows = 65000 * 256;  // token tiles of one grid
 
 // One product whose arguments have been checked.
 fl_status run(int dt, bool dual, const W4Params& p, void* workspace, const host::LaunchContext& ctx, cudaStream_t stream) {
-    return w4_few_rows(p.M, p.K) ? w4_rows(dt, dual, p, ctx, stream) : w4_tile(dt, dual, p, workspace, ctx, stream);
+    return w4_few_rows(p.M, p.N, p.K, dual) ? w4_rows(dt, dual, p, ctx, stream) : w4_tile(dt, dual, p, workspace, ctx, stream);
 }
 
 fl_status check_workspace(const void* workspace, size_t bytes, size_t need) {
@@ -206,7 +206,7 @@ fl_status fl_w4_quantize(const void* W, void* q, void* scales, int N, int K, int
 }
 
 size_t fl_w4_gemm_workspace_size(int M, int K, int norm) {
-    return M > 0 && K > 0 && !fl::w4_few_rows(M, K) ? fl::w4_tile_workspace(M, norm != 0) : 0;
+    return M > 0 && K > 0 && !fl::w4_always_few(M, K) ? fl::w4_tile_workspace(M, norm != 0) : 0;
 }
 
 fl_status fl_w4_gemm(const void* x, const void* gamma, const fl_w4_weight* W, const void* bias, const void* residual,

@@ -20,12 +20,13 @@ struct W4Params {
     const uint16_t* residual;  // [M, N] or null
     uint16_t* out;             // [M, N]
     int M, N, K, group, act;
-    int slab;                  // decode kernel: rows of one half of the grid
+    int slab;                  // decode kernel: rows of one slab of the grid
     float eps;
 };
 
-// Decode kernel (fl_w4_rows.cu): up to 16 rows that fit in shared memory, with the RMSNorm prologue.
-bool w4_few_rows(int M, int K);
+// Decode kernel (fl_w4_rows.cu): few rows that fit in shared memory, with the RMSNorm prologue.
+bool w4_few_rows(int M, int N, int K, bool dual);
+bool w4_always_few(int M, int K);  // whatever N is
 fl_status w4_rows(int dt, bool dual, const W4Params& p, const host::LaunchContext& ctx, cudaStream_t stream);
 
 // Tile kernel (fl_w4_tile.cu): any number of rows; the RMSNorm prologue keeps the rows' scales in the workspace.

@@ -1,4 +1,4 @@
-// 4-bit products for one to sixteen rows: the weight as a stream.
+// 4-bit products for few rows (a decode step): the weight as a stream.
 //
 // The step is bound by reading the codes once (0.5 bytes a weight and 2 per
 // group), and next to that by turning them into operands. The weight is the A
@@ -19,10 +19,10 @@
 // double-buffered across units (16 or 8 + 8 weight rows); a CTA's 8 warps take
 // 8 slices of K and add their sums through shared memory in warp order.
 //
-// Nine to sixteen rows are two slabs of at most eight, one to each half of the
-// grid: both halves walk the weight at the same pace, so the second reading of it
-// comes from L2. (The tensor-core tile kernel, which expands each code once for all
-// rows, takes 81 us for the 4096 x 11008 FFN at 16 rows.)
+// More than eight rows are slabs of at most eight, side by side in the grid:
+// they walk the weight at the same pace, so that it is read from HBM once and
+// by the other slabs from L2. w4_few_rows says up to where that beats the
+// tensor-core tile kernel, which expands each code once for all rows.
 #include "fl_common.cuh"
 #include "fl_host.h"
 #include "fl_w4.h"
@@ -35,6 +35,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 // words of one weight row in a register block (groups of 32 also hold four times the scales)
 __host__ __device__ constexpr int block_words(int V) { return V == 1 ? 8 : 16; }
 constexpr int kSmemMax = 200 * 1024;
+constexpr int kSmemPair = 104 * 1024;  // two CTAs to an SM
 
 // Row stride of the activation rows in 16-byte vectors: 4 mod 8, so that the
 // 8 lanes of a quarter warp (two rows, four vectors each) hit different banks.
@@ -279,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 2) fl_w4_rows_kernel(const __grid_co
     __shared__ float rscale[8];
     __shared__ float4 red[2][kWarps][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    // this half's rows
+    // this slab's rows
     const int m0 = blockIdx.y * p.slab, M = min(p.slab, p.M - m0);
     const uint16_t* x = p.x + (size_t)m0 * p.K;
     const int groups = p.K / (32 * V), units = DUAL ? p.N / 8 : (p.N + 15) / 16;
@@ -368,17 +369,30 @@ int slab_rows(int M) { return (M + slabs_of(M) - 1) / slabs_of(M); }
 template <int DT, bool DUAL, int V, bool Z>
 cudaError_t launch_rows(const W4Params& p, const host::LaunchContext& ctx, cudaStream_t stream) {
     auto kern = fl_w4_rows_kernel<DT, DUAL, V, Z>;
-    static const cudaError_t attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t attr = host::allow_smem(kern, kSmemMax, ctx.device, done);
     if (attr != cudaSuccess) return attr;
     const int slabs = slabs_of(p.M), smem = smem_bytes(p.slab, p.K), units = DUAL ? p.N / 8 : (p.N + 15) / 16;
-    const int most = ctx.sms * (smem <= 104 * 1024 ? 2 : 1) / slabs;  // resident CTAs of a slab
+    int most = ctx.sms * (smem <= kSmemPair ? 2 : 1) / slabs;  // resident CTAs of a slab
+    if (most < 1) most = 1;
     return host::launch(kern, dim3((unsigned)(units < most ? units : most), (unsigned)slabs), kThreads, (size_t)smem, ctx.pdl,
                         stream, p);
 }
 
+// The choice between this kernel and the tile kernel, by rows and weights,
+// measured side by side (us, this kernel / the tile kernel):
+//   4096 x 4096: 32 rows 12.6 / 16.5, 64 rows 18.6 / 17.3
+//   FFN 4096 x 11008: 16 rows 44 / 80, 32 rows 71 / 81, 64 rows 130 / 83
+//   2048 x 2048: 64 rows 8.2 / 10.9; 4096 x 1024: 64 rows 9.2 / 9.4, 96 rows 12.8 / 9.9
+//   1024 x 1024: 128 rows 6.2 / 9.1
+int rows_limit(long long weights) { return weights <= (1ll << 20) ? 128 : weights <= (4ll << 20) ? 64 : 32; }
+
 }  // namespace
 
-bool w4_few_rows(int M, int K) { return M <= 16 && smem_bytes(slab_rows(M), K) <= kSmemMax; }
+bool w4_few_rows(int M, int N, int K, bool dual) {
+    return M <= rows_limit((long long)N * K * (dual ? 2 : 1)) && smem_bytes(slab_rows(M), K) <= kSmemMax;
+}
+bool w4_always_few(int M, int K) { return M <= 32 && smem_bytes(slab_rows(M), K) <= kSmemMax; }
 
 fl_status w4_rows(int dt, bool dual, const W4Params& params, const host::LaunchContext& ctx, cudaStream_t stream) {
     W4Params p = params;

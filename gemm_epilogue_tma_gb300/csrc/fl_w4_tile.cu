@@ -87,13 +87,19 @@ struct TileParams {
     CUtensorMap tm_x;     // x [M, K], box {64, BT}
     CUtensorMap tm_q[2];  // codes [N, K / 2] bytes, box {128, 128} (pair: {128, 64} each)
     W4Params w;
-    const float* row_scale;  // [M] 1 / rms of the rows of x (with gamma)
+    const float* row_scale;  // [M] 1 / rms of the rows of x, over kLift (with gamma)
     int bt, splits, steps_per_split, steps;  // K steps of 64
     int row_tiles, tiles;
     int stages, w_stages, b_bytes;           // rings: stages * b_bytes of tokens, then the code stages
     int* status;
     unsigned long long timeout_ns;
 };
+
+// scale * gamma * (code - zero) is formed times this, a power of two that puts
+// weights of usual sizes in the middle of fp16's range, and the row scale times
+// its inverse.
+template <int DT>
+constexpr float kLift = DT == DT_F16 ? 64.f : 1.f;
 
 template <int DT>
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
@@ -197,7 +203,7 @@ __device__ __forceinline__ void commit_elected(uint32_t bar) {
         : "memory");
 }
 
-// 1 / rms of the rows of x [M, K]: one warp per row, eight vectors in flight per lane.
+// 1 / rms (over kLift) of the rows of x [M, K]: one warp per row, eight vectors in flight per lane.
 template <int DT>
 __global__ void __launch_bounds__(256) fl_w4_row_scale_kernel(const uint16_t* __restrict__ x, float* __restrict__ scale,
                                                               int M, int K, float eps) {
@@ -227,7 +233,7 @@ __global__ void __launch_bounds__(256) fl_w4_row_scale_kernel(const uint16_t* __
     float s = s0 + s1;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) scale[m] = rsqrtf(s / (float)K + eps);
+    if (lane == 0) scale[m] = rsqrtf(s / (float)K + eps) * (1.f / kLift<DT>);
 }
 
 template <int DT, bool DUAL, bool NORM>
@@ -553,8 +559,8 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
                     const int kin = (it % kSIter) * kWk + grp * kStep;
                     const int ga = kin >> gsh, gb = (kin + 32) >> gsh;
                     uint32_t sa = ds[ga * kSPitch + r], sb = ds[gb * kSPitch + r];
-                    sa = NORM ? __float_as_uint(Ops::unpack(sa).x) : sa * 0x10001u;
-                    sb = NORM ? __float_as_uint(Ops::unpack(sb).x) : sb * 0x10001u;
+                    sa = NORM ? __float_as_uint(Ops::unpack(sa).x * kLift<DT>) : sa * 0x10001u;
+                    sb = NORM ? __float_as_uint(Ops::unpack(sb).x * kLift<DT>) : sb * 0x10001u;
                     const uint32_t za = zero_const<DT>(dz[ga * kZPitch + r]), zb = zero_const<DT>(dz[gb * kZPitch + r]);
                     const uint32_t sg = sbase + kOffG + ss * kGBytes + kin * 2;
                     const uint32_t cw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
@@ -635,13 +641,9 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
 
 template <int DT, bool DUAL, bool NORM>
 struct Kern {
-    static cudaError_t configure() {
-        static const cudaError_t e = [] {
-            auto k = fl_w4_tile_kernel<DT, DUAL, NORM>;
-            cudaError_t r = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-            return r;
-        }();
-        return e;
+    static cudaError_t configure(int device) {
+        static std::atomic<unsigned long long> done{0};
+        return host::allow_smem(fl_w4_tile_kernel<DT, DUAL, NORM>, kSmem, device, done);
     }
     static void config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* a, dim3 grid, int splits, int pdl, cudaStream_t s) {
         cfg = {};
@@ -657,17 +659,17 @@ struct Kern {
         cfg.attrs = a;
         cfg.numAttrs = 2;
     }
-    static cudaError_t launch(const TileParams& p, dim3 grid, int pdl, cudaStream_t s) {
-        cudaError_t e = configure();
+    static cudaError_t launch(const TileParams& p, dim3 grid, const host::LaunchContext& ctx, cudaStream_t s) {
+        cudaError_t e = configure(ctx.device);
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute a[2];
-        config(cfg, a, grid, p.splits, pdl, s);
+        config(cfg, a, grid, p.splits, ctx.pdl, s);
         return cudaLaunchKernelEx(&cfg, fl_w4_tile_kernel<DT, DUAL, NORM>, p);
     }
     // clusters of `splits` CTAs that are resident at once
-    static int resident(int splits) {
-        if (configure() != cudaSuccess) return 0;
+    static int resident(int splits, int device) {
+        if (configure(device) != cudaSuccess) return 0;
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute a[2];
         config(cfg, a, dim3((unsigned)splits), splits, 0, nullptr);
@@ -712,23 +714,25 @@ fl_status w4_tile(int dt, bool dual, const W4Params& w, void* workspace, const h
     for (int tt = tt0; tt <= 3 * tt0 && tt <= tt0 + 64; ++tt) {
         const int bt = ((w.M + tt - 1) / tt + 15) / 16 * 16;
         if (tt > tt0 && bt < 64) break;
+        // (rounded up to 16 tokens, fewer tiles may do; none starts at or past M)
+        const int count = (w.M + bt - 1) / bt;
         for (int s = 1; s <= 8; ++s) {
             const int per = ((p.steps + 1) / 2 + s - 1) / s * 2;
             if (s > 1 && (per < 4 || (p.steps + per - 1) / per != s)) continue;
             int n = resident[s].load();
             if (n == 0) {
-                n = Kern<DT_BF16, false, false>::resident(s);
+                n = Kern<DT_BF16, false, false>::resident(s, ctx.device);
                 if (n <= 0) n = -1;
                 resident[s] = n;
             }
             if (n < 0) continue;
-            const double rounds = (double)(((long long)row_tiles * tt + n - 1) / n);
+            const double rounds = (double)(((long long)row_tiles * count + n - 1) / n);
             const double least_step = norm ? 690.0 : 570.0, step = 2.2 * bt > least_step ? 2.2 * bt : least_step;
             const double cost = s == 1 ? 5000.0 + rounds * (step * per + 6000.0)
                                        : rounds * (step * per + 11000.0 + 12.0 * bt);
             if (token_tiles == 0 || cost < least) {
                 least = cost;
-                token_tiles = tt;
+                token_tiles = count;
                 p.bt = bt;
                 p.splits = s;
                 p.steps_per_split = per;
@@ -759,9 +763,9 @@ fl_status w4_tile(int dt, bool dual, const W4Params& w, void* workspace, const h
     cudaError_t e;
     if (dual && !norm) return host::fail(FL_ERR_UNSUPPORTED, "4-bit tile kernel: the pair needs gamma");
 #define FL_LAUNCH(DT)                                                                                      \
-    e = dual ? Kern<DT, true, true>::launch(p, grid, ctx.pdl, stream)                                      \
-             : norm ? Kern<DT, false, true>::launch(p, grid, ctx.pdl, stream)                              \
-                    : Kern<DT, false, false>::launch(p, grid, ctx.pdl, stream)
+    e = dual ? Kern<DT, true, true>::launch(p, grid, ctx, stream)                                      \
+             : norm ? Kern<DT, false, true>::launch(p, grid, ctx, stream)                              \
+                    : Kern<DT, false, false>::launch(p, grid, ctx, stream)
     if (dt == FL_F16)
         FL_LAUNCH(DT_F16);
     else
