@@ -72,6 +72,17 @@ class KvDesc(ctypes.Structure):
                 + [(n, ctypes.c_void_p) for n in ("k_cache", "v_cache", "k_scale", "v_scale")])
 
 
+class LayerCacheDesc(ctypes.Structure):
+    """fl_layer_cache_desc."""
+    _fields_ = ([(n, ctypes.c_int) for n in ("head_dim", "rotary_dim", "n_axes", "interleaved")]
+                + [("axis_of", ctypes.c_char_p), ("positions", ctypes.c_void_p), ("positions_stride", ctypes.c_longlong),
+                   ("inv_freq", ctypes.c_void_p)]
+                + [(n, ctypes.c_int) for n in ("format", "page_size", "n_pages", "n_seqs", "table_pages")]
+                + [("table_stride", ctypes.c_longlong)]
+                + [(n, ctypes.c_void_p) for n in ("page_table", "cu_rows", "start", "k_cache", "v_cache", "k_scale",
+                                                  "v_scale")])
+
+
 # C ABI: name -> (restype, argtypes)
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 _w4 = ctypes.POINTER(W4Weight)
@@ -93,6 +104,7 @@ SIGNATURES = {
     "fl_kv_write": (_i, [ctypes.POINTER(KvDesc), _vp]),
     "fl_kv_read": (_i, [ctypes.POINTER(KvDesc), _vp]),
     "fl_layer_create": (_i, [ctypes.POINTER(LayerDesc), ctypes.POINTER(_vp)]),
+    "fl_layer_attach_cache": (_i, [_vp, ctypes.POINTER(LayerCacheDesc)]),
     "fl_layer_issue": (_i, [_vp, _i, _vp]),
     "fl_layer_destroy": (None, [_vp]),
     "fl_capture_begin": (_i, [_vp]),
@@ -298,6 +310,63 @@ class DecoderLayer:
         _check(lib().fl_layer_create(ctypes.byref(desc), ctypes.byref(h)))
         self._h = h
 
+    def attach_cache(self, head_dim, positions=None, inv_freq=None, sections=None, interleaved=False, k_cache=None,
+                     v_cache=None, k_scale=None, v_scale=None, page_table=None, start=None, cu_rows=None) -> None:
+        """Half 0 then also rotates q and k in place (rope's positions, inv_freq, sections, interleaved) and writes k
+        and v into the paged cache (kv_write's tensors; cu_rows None: one row per sequence). Either part may be left
+        out; with neither, a part attached before is taken off. The tensors stay fixed: write new positions, pages and
+        starts into them in place."""
+        import torch
+        T = self.tensors
+        here = T["x"].device
+        if inv_freq is None and k_cache is None:
+            _check(lib().fl_layer_attach_cache(self._h, None))
+            self.attached = ()
+            return
+        d = LayerCacheDesc(head_dim=head_dim)
+        kept = []
+
+        def use(name, t, dtype, shape=None, contiguous=True):
+            if t.device != here or t.dtype != dtype:
+                raise ValueError(f"{name} must be a {dtype} tensor on {here}, got {t.dtype} on {t.device}")
+            if contiguous and not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+            if shape is not None and tuple(t.shape) != tuple(shape):
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+            kept.append(t)
+            return t.data_ptr()
+
+        M = T["x"].shape[0]
+        if inv_freq is not None:
+            pairs, axes = inv_freq.shape[0], positions.shape[0] if positions.dim() == 2 else 1
+            sections = (pairs,) if sections is None and axes == 1 else sections
+            if sections is None or len(sections) != axes or sum(sections) != pairs or min(sections) < 0 or axes > 4:
+                raise ValueError(f"sections must give the {pairs} pairs to the {axes} axes (1..4)")
+            d.rotary_dim, d.n_axes, d.interleaved = 2 * pairs, axes, int(bool(interleaved))
+            d.axis_of = b"".join(bytes((a,)) * n for a, n in enumerate(sections))
+            d.positions = use("positions", positions, torch.int32, (axes, M) if positions.dim() == 2 else (M,))
+            d.positions_stride = M
+            d.inv_freq = use("inv_freq", inv_freq, torch.float32, (pairs,))
+        if k_cache is not None:
+            formats = {torch.int8: 0, torch.float8_e4m3fn: 1}
+            if k_cache.dtype not in formats:
+                raise ValueError(f"k_cache has dtype {k_cache.dtype}, expected int8 or float8_e4m3fn")
+            if start is None or page_table is None:
+                raise ValueError("page_table and start must be given")
+            pages, size = k_cache.shape[:2]
+            seqs, per = page_table.shape
+            shape = (pages, size, T["k"].shape[1] // head_dim, head_dim)
+            d.format, d.page_size, d.n_pages, d.n_seqs, d.table_pages = formats[k_cache.dtype], size, pages, seqs, per
+            d.table_stride = per
+            d.page_table = use("page_table", page_table, torch.int32)
+            d.start = use("start", start, torch.int32, (seqs,))
+            d.cu_rows = None if cu_rows is None else use("cu_rows", cu_rows, torch.int32, (seqs + 1,))
+            d.k_cache, d.v_cache = (use(n, t, k_cache.dtype, shape) for n, t in (("k_cache", k_cache), ("v_cache", v_cache)))
+            d.k_scale, d.v_scale = (use(n, t, torch.float32, shape[:3]) for n, t in (("k_scale", k_scale),
+                                                                                     ("v_scale", v_scale)))
+        _check(lib().fl_layer_attach_cache(self._h, ctypes.byref(d)))
+        self.attached = tuple(kept)  # kept alive as long as the layer uses them
+
     def issue(self, half: int, stream=None) -> None:
         """Issue half 0 or 1 on the stream (capturable)."""
         _check(lib().fl_layer_issue(self._h, int(half), _stream(stream)))
@@ -314,6 +383,9 @@ class DecoderLayer:
             pass
 
 
+_captures = []  # of each Graph.capture at work: the workspaces that calls made for themselves, which replays use
+
+
 class Graph:
     """A CUDA graph of library calls (fl_capture_begin / fl_capture_end / fl_graph_launch)."""
 
@@ -326,13 +398,18 @@ class Graph:
         The stream must not be the legacy default stream (CUDA cannot capture it)."""
         s = _stream(stream)
         _check(lib().fl_capture_begin(s))
+        kept = []
+        _captures.append(kept)
         try:
             fn()
         finally:
+            _captures[:] = [c for c in _captures if c is not kept]
             h = ctypes.c_void_p()
             st = lib().fl_capture_end(s, ctypes.byref(h))
         _check(st)
-        return cls(h)
+        graph = cls(h)
+        graph._kept = kept
+        return graph
 
     def launch(self, stream=None) -> None:
         _check(lib().fl_graph_launch(self._h, _stream(stream)))
@@ -341,6 +418,7 @@ class Graph:
         if getattr(self, "_h", None):
             lib().fl_graph_destroy(self._h)
             self._h = None
+            self._kept = None
 
     def __del__(self):
         try:
@@ -411,21 +489,32 @@ def ops():
     return _ops
 
 
-def _on(stream, *made):
-    """Tensors that a call made for itself and used on `stream` are not reused by another stream before it is done."""
-    for t in made:
-        if t is not None:
-            t.record_stream(stream)
+def _issue(name, args, stream, makes=True):
+    """ops().name(*args) on `stream` (None: the current one). Tensors that the call makes for itself (makes: it may) are
+    `stream`'s, as those of any torch call under torch.cuda.stream(stream)."""
+    f = getattr(_ops or ops(), name)
+    if stream is None:
+        return f(*args, None)
+    if not makes:
+        return f(*args, stream.cuda_stream)
+    import torch
+    with torch.cuda.stream(stream):
+        return f(*args, None)
+
+
+def _issue_ws(name, args, stream, makes):
+    """_issue of a call that returns its output and the workspace it made, or None."""
+    out, ws = _issue(name, args, stream, makes)
+    if ws is not None:
+        for kept in _captures:
+            kept.append(ws)
+    return out
 
 
 def w4_quantize(W, group=128, q=None, scales=None, stream=None):
     """Symmetric round-to-nearest 4-bit quantisation of W [N, K]: returns (q, scales), codes [N, K / 2] uint8 (two
     along K to a byte, the even k in the low half, 8 standing for zero) and one scale of W's dtype per `group` k."""
-    if stream is None:
-        return (_ops or ops()).w4_quantize(W, group, q, scales, None)
-    r = ops().w4_quantize(W, group, q, scales, stream.cuda_stream)
-    _on(stream, None if q is not None else r[0], None if scales is not None else r[1])
-    return r
+    return _issue("w4_quantize", (W, group, q, scales), stream, q is None or scales is None)
 
 
 def w4_gemm_workspace_size(M: int, K: int, norm: bool) -> int:
@@ -438,11 +527,8 @@ def w4_gemm(x, q, scales, zeros=None, gamma=None, bias=None, residual=None, out=
     zeros[n, k / group]); norm is RMSNorm with `gamma`, or none. q, scales: as w4_quantize returns them; zeros
     [N, K / group] uint8 (8 everywhere if None). The workspace (w4_gemm_workspace_size bytes) must not be
     shared by calls or captured graphs that may overlap on the GPU."""
-    if stream is None:
-        return (_ops or ops()).w4_gemm(x, q, scales, zeros, gamma, bias, residual, out, eps, ACTS[act], workspace, None)[0]
-    r, ws = ops().w4_gemm(x, q, scales, zeros, gamma, bias, residual, out, eps, ACTS[act], workspace, stream.cuda_stream)
-    _on(stream, ws, None if out is not None else r)
-    return r
+    return _issue_ws("w4_gemm", (x, q, scales, zeros, gamma, bias, residual, out, eps, ACTS[act], workspace), stream,
+                     out is None or workspace is None)
 
 
 def w4_swiglu_ffn_workspace_size(M: int, D: int, F: int) -> int:
@@ -451,11 +537,8 @@ def w4_swiglu_ffn_workspace_size(M: int, D: int, F: int) -> int:
 
 def w4_swiglu_ffn(x, gamma, Wg, Wu, Wd, bias_down=None, out=None, eps=1e-6, workspace=None, stream=None):
     """swiglu_ffn on 4-bit weights, each a tuple (q, scales) or (q, scales, zeros)."""
-    if stream is None:
-        return (_ops or ops()).w4_swiglu_ffn(x, gamma, Wg, Wu, Wd, bias_down, out, eps, workspace, None)[0]
-    r, ws = ops().w4_swiglu_ffn(x, gamma, Wg, Wu, Wd, bias_down, out, eps, workspace, stream.cuda_stream)
-    _on(stream, ws, None if out is not None else r)
-    return r
+    return _issue_ws("w4_swiglu_ffn", (x, gamma, Wg, Wu, Wd, bias_down, out, eps, workspace), stream,
+                     out is None or workspace is None)
 
 
 def rope(q, k, positions, inv_freq, sections=None, interleaved=False, inverse=False, out_q=None, out_k=None,
@@ -467,11 +550,8 @@ def rope(q, k, positions, inv_freq, sections=None, interleaved=False, inverse=Fa
     `sections` saying how many consecutive pairs follow each axis. inverse turns back: the gradient with respect to
     the input. q, k and the outputs may be strided views with contiguous channels (column ranges of a stacked
     projection's output); an output may be its input itself."""
-    if stream is None:
-        return (_ops or ops()).rope(q, k, positions, inv_freq, sections, interleaved, inverse, out_q, out_k, None)
-    r = ops().rope(q, k, positions, inv_freq, sections, interleaved, inverse, out_q, out_k, stream.cuda_stream)
-    _on(stream, None if out_q is not None else r[0], None if out_k is not None else r[1])
-    return r
+    return _issue("rope", (q, k, positions, inv_freq, sections, interleaved, inverse, out_q, out_k), stream,
+                  out_q is None or (out_k is None and k is not None))
 
 
 def kv_write(k, v, k_cache, v_cache, k_scale, v_scale, page_table, start, cu_rows=None, stream=None):
@@ -484,8 +564,7 @@ def kv_write(k, v, k_cache, v_cache, k_scale, v_scale, page_table, start, cu_row
     No two rows of a call may have the same place in the cache."""
     if start is None:
         raise ValueError("start must be given")
-    (_ops or ops()).kv_write(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_rows, start,
-                             None if stream is None else stream.cuda_stream)
+    _issue("kv_write", (k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_rows, start), stream, False)
 
 
 def kv_read(k_cache, v_cache, k_scale, v_scale, page_table, cu_rows, start=None, out_k=None, out_v=None, stream=None):
@@ -495,8 +574,7 @@ def kv_read(k_cache, v_cache, k_scale, v_scale, page_table, cu_rows, start=None,
     Returns (out_k, out_v)."""
     if out_k is None or out_v is None:
         raise ValueError("out_k and out_v must be given: the row count is not known on the host")
-    (_ops or ops()).kv_read(out_k, out_v, k_cache, v_cache, k_scale, v_scale, page_table, cu_rows, start,
-                            None if stream is None else stream.cuda_stream)
+    _issue("kv_read", (out_k, out_v, k_cache, v_cache, k_scale, v_scale, page_table, cu_rows, start), stream, False)
     return out_k, out_v
 
 

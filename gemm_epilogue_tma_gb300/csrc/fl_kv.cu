@@ -367,7 +367,7 @@ fl_status check_desc(const char* what, const fl_kv_desc* d, bool write) {
     return FL_OK;
 }
 
-fl_status run(const char* what, const fl_kv_desc* d, bool write, cudaStream_t stream) {
+fl_status run(const char* what, const fl_kv_desc* d, bool write, bool check_only, cudaStream_t stream) {
     fl_status st = check_desc(what, d, write);
     if (st != FL_OK) return st;
     if (d->rows == 0) return host::ok();
@@ -405,6 +405,7 @@ fl_status run(const char* what, const fl_kv_desc* d, bool write, cudaStream_t st
     while ((8 * W << lanes_log) < d->head_dim) ++lanes_log;
     const int groups = 32 >> lanes_log, half = (d->heads + groups - 1) / groups;
     if (2ll * d->rows * half >= (1ll << 31)) return host::fail(FL_ERR_UNSUPPORTED, "%s: too many rows", what);
+    if (check_only) return host::ok();
     host::LaunchContext ctx;
     if ((st = host::launch_context(stream, &ctx)) != FL_OK) return st;
     KvParams p = {};
@@ -439,12 +440,14 @@ fl_status run(const char* what, const fl_kv_desc* d, bool write, cudaStream_t st
 
 }  // namespace
 
+fl_status check_kv_write(const fl_kv_desc* desc) { return run("fl_kv_write", desc, true, true, nullptr); }
+
 }  // namespace fl
 
 extern "C" fl_status fl_kv_write(const fl_kv_desc* desc, void* stream) {
-    return fl::run("fl_kv_write", desc, true, static_cast<cudaStream_t>(stream));
+    return fl::run("fl_kv_write", desc, true, false, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" fl_status fl_kv_read(const fl_kv_desc* desc, void* stream) {
-    return fl::run("fl_kv_read", desc, false, static_cast<cudaStream_t>(stream));
+    return fl::run("fl_kv_read", desc, false, false, static_cast<cudaStream_t>(stream));
 }

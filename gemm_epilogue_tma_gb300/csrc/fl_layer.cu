@@ -17,7 +17,9 @@
 //
 // The layer is split where the attention core sits, which this library does
 // not compute:
-//   half 0: q, k, v = RMSNorm(x; gamma_attn) [Wq; Wk; Wv]^T   (one fused launch)
+//   half 0: q, k, v = RMSNorm(x; gamma_attn) [Wq; Wk; Wv]^T   (one fused launch);
+//           with fl_layer_attach_cache, q and k rotated in place and k and v
+//           quantised into the paged cache
 //   -- the caller's attention writes attn [M, D] --
 //   half 1: h   = attn Wo^T (+ bias_o) + x
 //           out = SwiGLU_FFN(h; gamma_ffn, Wg, Wu, Wd) + h      (RMSNorm fused)
@@ -28,6 +30,7 @@
 #include <new>
 
 #include "../../include/fusedlin.h"
+#include "fl_host.h"
 #include "fl_internal.h"
 
 struct fl_layer {
@@ -36,6 +39,10 @@ struct fl_layer {
     void* ffn_workspace = nullptr;  // the FFN's hidden activation [M, F]
     size_t ffn_bytes = 0;
     void* zero_bias = nullptr;      // [D] zeros when the output projection has no bias
+    bool rotates = false, caches = false;  // fl_layer_attach_cache
+    fl_rope_desc rope = {};
+    fl_kv_desc kv = {};
+    unsigned char axis_of[FL_ROPE_MAX_DIM / 2] = {};
 };
 
 namespace {
@@ -62,8 +69,11 @@ fl_status issue_half(const fl_layer* L, int half, cudaStream_t s) {
         const void* W[3] = {d.Wq, d.Wk, d.Wv};
         void* out[3] = {d.q, d.k, d.v};
         const int N[3] = {d.D, d.Dkv, d.Dkv};
-        return fl_norm_gemm_multi(d.x, d.gamma_attn, nullptr, 3, W, nullptr, out, N, nullptr, d.M, d.D, d.eps,
-                                  FL_NORM_RMS, d.dtype, s);
+        fl_status st = fl_norm_gemm_multi(d.x, d.gamma_attn, nullptr, 3, W, nullptr, out, N, nullptr, d.M, d.D, d.eps,
+                                          FL_NORM_RMS, d.dtype, s);
+        if (st == FL_OK && L->rotates) st = fl_rope(&L->rope, s);
+        if (st == FL_OK && L->caches) st = fl_kv_write(&L->kv, s);
+        return st;
     }
     const void* bo = d.bias_o != nullptr ? d.bias_o : L->zero_bias;
     fl_status st = fl_gemm_epilogue(d.attn, d.Wo, bo, d.x, d.h, d.M, d.D, d.D, FL_GEMM_BIAS_RESIDUAL, d.dtype, s);
@@ -132,6 +142,51 @@ extern "C" fl_status fl_layer_create(const fl_layer_desc* desc, fl_layer** layer
         return cuda_err(e, "set-up pass");
     }
     *layer = L;
+    fl::set_last_error(FL_OK, "");
+    return FL_OK;
+}
+
+extern "C" fl_status fl_layer_attach_cache(fl_layer* layer, const fl_layer_cache_desc* desc) {
+    if (layer == nullptr) return err(FL_ERR_INVALID_ARG, "fl_layer_attach_cache: null layer");
+    if (desc == nullptr) {
+        layer->rotates = layer->caches = false;
+        fl::set_last_error(FL_OK, "");
+        return FL_OK;
+    }
+    const fl_layer_cache_desc& c = *desc;
+    const fl_layer_desc& d = layer->d;
+    if (c.head_dim < 1 || d.D % c.head_dim != 0 || d.Dkv % c.head_dim != 0)
+        return err(FL_ERR_INVALID_ARG, "fl_layer_attach_cache: head_dim must divide D and Dkv");
+    if (c.inv_freq == nullptr && c.k_cache == nullptr)
+        return err(FL_ERR_INVALID_ARG, "fl_layer_attach_cache: neither inv_freq nor k_cache");
+    fl_layer next = *layer;  // (a refused description leaves the layer as it was)
+    fl_status st;
+    next.rotates = c.inv_freq != nullptr;
+    if (next.rotates) {
+        fl_rope_desc& r = next.rope;
+        r = {};
+        r.dtype = d.dtype, r.rows = d.M, r.heads_q = d.D / c.head_dim, r.heads_k = d.Dkv / c.head_dim;
+        r.head_dim = c.head_dim, r.rotary_dim = c.rotary_dim, r.n_axes = c.n_axes, r.interleaved = c.interleaved;
+        r.axis_of = c.axis_of, r.positions = c.positions, r.positions_stride = c.positions_stride, r.inv_freq = c.inv_freq;
+        r.q = r.q_out = d.q, r.k = r.k_out = d.k;
+        r.q_row = r.q_out_row = d.D, r.k_row = r.k_out_row = d.Dkv;
+        r.q_head = r.q_out_head = r.k_head = r.k_out_head = c.head_dim;
+        if ((st = fl::check_rope(&r)) != FL_OK) return st;
+        if (c.axis_of != nullptr) memcpy(next.axis_of, c.axis_of, (size_t)c.rotary_dim / 2);
+    }
+    next.caches = c.k_cache != nullptr;
+    if (next.caches) {
+        fl_kv_desc& k = next.kv;
+        k = {};
+        k.dtype = d.dtype, k.format = c.format, k.rows = d.M, k.heads = d.Dkv / c.head_dim, k.head_dim = c.head_dim;
+        k.page_size = c.page_size, k.n_pages = c.n_pages, k.n_seqs = c.n_seqs, k.table_pages = c.table_pages;
+        k.table_stride = c.table_stride, k.page_table = c.page_table, k.cu_rows = c.cu_rows, k.start = c.start;
+        k.k = d.k, k.v = d.v, k.k_row = k.v_row = d.Dkv, k.k_head = k.v_head = c.head_dim;
+        k.k_cache = c.k_cache, k.v_cache = c.v_cache, k.k_scale = c.k_scale, k.v_scale = c.v_scale;
+        if ((st = fl::check_kv_write(&k)) != FL_OK) return st;
+    }
+    *layer = next;
+    if (layer->rotates && c.axis_of != nullptr) layer->rope.axis_of = layer->axis_of;
     fl::set_last_error(FL_OK, "");
     return FL_OK;
 }

@@ -195,8 +195,11 @@ size_t span(const View& v, int rows, int dim) {
 
 }  // namespace fl
 
-extern "C" fl_status fl_rope(const fl_rope_desc* d, void* stream) {
-    using namespace fl;
+namespace fl {
+namespace {
+
+// The checks of fl_rope, and its launch unless `check_only`.
+fl_status rope(const fl_rope_desc* d, bool check_only, cudaStream_t s) {
     using host::fail;
     if (d == nullptr) return fail(FL_ERR_INVALID_ARG, "fl_rope: null description");
     if (!host::valid_dtype(d->dtype)) return fail(FL_ERR_INVALID_ARG, "fl_rope: bad dtype %d", (int)d->dtype);
@@ -257,8 +260,8 @@ extern "C" fl_status fl_rope(const fl_rope_desc* d, void* stream) {
             host::overlap(o.p, span(o, d->rows, d->head_dim), d->inv_freq, (size_t)pairs * 4))
             return fail(FL_ERR_INVALID_ARG, "fl_rope: an output overlaps another tensor of the call");
     }
+    if (check_only) return host::ok();
     host::LaunchContext ctx;
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const fl_status st = host::launch_context(s, &ctx);
     if (st != FL_OK) return st;
     RopeParams p = {};
@@ -291,4 +294,14 @@ extern "C" fl_status fl_rope(const fl_rope_desc* d, void* stream) {
         e = vec ? host::launch(fl_rope_kernel<DT_BF16, 8>, grid, kRopeThreads, 0, ctx.pdl, s, p)
                 : host::launch(fl_rope_kernel<DT_BF16, 1>, grid, kRopeThreads, 0, ctx.pdl, s, p);
     return host::launched(e, "rotary kernel");
+}
+
+}  // namespace
+
+fl_status check_rope(const fl_rope_desc* desc) { return rope(desc, true, nullptr); }
+
+}  // namespace fl
+
+extern "C" fl_status fl_rope(const fl_rope_desc* desc, void* stream) {
+    return fl::rope(desc, false, static_cast<cudaStream_t>(stream));
 }

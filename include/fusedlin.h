@@ -448,7 +448,9 @@ fl_status fl_w4_quantize(const void* W, void* q, void* scales, int N, int K, int
 
 /*
  * out[M,N] = act(norm(x)[M,K] W^T + bias) (+ residual) on a 4-bit weight.
- *   gamma: [K], the RMSNorm prologue of fl_norm_gemm; NULL: x as it is.
+ *   gamma: [K], the RMSNorm prologue of fl_norm_gemm; NULL: x as it is. With
+ *   gamma one product is formed in the dtype, in fp16 within its range: x * gamma
+ *   (few rows) or 64 * w * gamma (many).
  *   bias [N] and residual [M,N] may be NULL; residual may be the same pointer
  *   as out. Epilogue order as in fl_gemm_epilogue.
  * workspace: fl_w4_gemm_workspace_size(M, K, gamma != NULL) bytes (0 for some
@@ -569,6 +571,39 @@ typedef struct {
 } fl_kv_desc;
 fl_status fl_kv_write(const fl_kv_desc* desc, void* stream);
 fl_status fl_kv_read(const fl_kv_desc* desc, void* stream);
+
+/*
+ * Rotary positions and the cache as part of a prepared layer: half 0 of
+ * fl_layer_issue, after q, k and v, then also rotates q and k in place
+ * (fl_rope) and quantises k and v into the layer's cache (fl_kv_write), so
+ * that a decode step is the same two calls. The layer's q is [M, D / head_dim,
+ * head_dim] and its k and v [M, Dkv / head_dim, head_dim]; head_dim divides D
+ * and Dkv. The other fields are those of fl_rope_desc (inv_freq NULL: no
+ * rotation) and fl_kv_desc (k_cache NULL: no cache; cu_rows NULL: one row per
+ * sequence). The device pointers stay fixed and are read at each issue; axis_of
+ * is copied. The description is checked as the two calls check theirs, without a
+ * launch; a second call replaces the first, desc NULL detaches. Not to be called while
+ * another thread issues the layer.
+ */
+typedef struct {
+    int head_dim;
+    int rotary_dim, n_axes, interleaved;
+    const unsigned char* axis_of;
+    const int* positions;
+    long long positions_stride;
+    const float* inv_freq;
+    fl_kv_format format;
+    int page_size, n_pages, n_seqs, table_pages;
+    long long table_stride;
+    const int* page_table;
+    const int* cu_rows;
+    const int* start;
+    void* k_cache;
+    void* v_cache;
+    float* k_scale;
+    float* v_scale;
+} fl_layer_cache_desc;
+fl_status fl_layer_attach_cache(fl_layer* layer, const fl_layer_cache_desc* desc);
 
 /* Library version string. */
 const char* fl_version(void);

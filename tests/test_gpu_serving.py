@@ -110,7 +110,8 @@ def w4_check(got, y, mag, sq, K, dt, act_mag=0.0, what=""):
 
 SHAPES = [(1, 8, 32, 32), (1, 1024, 1024, 128), (2, 264, 320, 64), (3, 40, 4096, 32), (7, 2048, 2048, 128),
           (8, 520, 11008, 128), (9, 136, 256, 64), (16, 1032, 1056, 32), (33, 8, 128, 128), (65, 392, 640, 64),
-          (128, 128, 512, 128), (130, 2048, 4096, 128), (257, 264, 96, 32), (300, 6144, 1024, 64)]
+          (128, 128, 512, 128), (129, 512, 512, 32), (100, 1024, 1024, 64), (60, 2048, 2048, 128), (32, 4104, 1024, 32),
+          (17, 264, 11008, 128), (130, 2048, 4096, 128), (257, 264, 96, 32), (300, 6144, 1024, 64)]
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
@@ -220,6 +221,66 @@ def test_w4_rows_do_not_depend_on_their_number():
         fl.w4_gemm(x[:M].contiguous(), w[0], w[1], gamma=gamma, out=buf[1:M + 1])
         assert (buf[0] == 7).all() and (buf[M + 1] == 7).all()
         w4_check(buf[1:M + 1], y[:M], mag[:M], sq[:M], 384, "bf16", what=f"{M} rows")
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("M", [3, 20, 200])
+def test_w4_gemm_small_gamma(dt, M):
+    """Weights and gammas that are small together lose nothing to the type's smallest values (fp16 x * gamma and
+    64 * w * gamma stay above 2^-14 but for a share too small to see)."""
+    rng = gen(9, M)
+    x = put(rng.standard_normal((M, 512)), dt)
+    q, s, z = w4_tensors(rng, 264, 512, 64, False, dt)
+    s = put(rng.uniform(0.5, 1.5, s.shape) * 1e-3, dt)
+    gamma = put((1 + 0.1 * rng.standard_normal(512)) * 4e-3, dt)
+    w = (q, s, z)
+    y, mag, sq = w4_ref(x, w, gamma, 1e-6)
+    y, mag, sq = y * 4096, mag * 4096, sq * 4096 ** 2   # (outputs of some 1e-4: the last rounding, fp16's too, is absolute)
+    got = f64(fl.w4_gemm(x, q, s, gamma=gamma)) * 4096
+    fl.device_status()
+    err, u = np.abs(got - y), U[dt]
+    last = 4096 * 2.0 ** -25 if dt == "f16" else 0.0
+    # x * gamma below 2^-14 (|x| < 0.015) is rounded by 2^-25 absolutely, 2^-11 of 2^-14
+    lost = 4096 * 2.0 ** -25 * 512 * 8 * 1.5e-3 if dt == "f16" else 0.0
+    assert (err <= u * np.abs(y) + (2.1 * u + 512 * 2.0 ** -22) * mag + last + lost).all()
+    assert np.sqrt((err ** 2).mean()) <= np.sqrt((u * u * (y ** 2 + 2 * sq)).mean()) + last
+
+
+@pytest.mark.parametrize("M", [1, 8, 20, 40, 300])
+def test_w4_gemm_not_finite_weights(M):
+    """A NaN or infinite scale, bias or residual stays in the outputs that it belongs to."""
+    rng = gen(10, M)
+    x = put(rng.standard_normal((M, 512)), "bf16")
+    q, s, z = w4_tensors(rng, 264, 512, 128, True, "bf16")
+    r = put(rng.standard_normal((M, 264)), "bf16")
+    b = put(rng.standard_normal(264), "bf16")
+    gamma = put(1 + 0.1 * rng.standard_normal(512), "bf16")
+    want = fl.w4_gemm(x, q, s, zeros=z, gamma=gamma, bias=b, residual=r)
+    s[5, 1], s[140, 3], b[77], r[M - 1, 200] = float("nan"), float("inf"), float("inf"), float("nan")
+    got = fl.w4_gemm(x, q, s, zeros=z, gamma=gamma, bias=b, residual=r)
+    fl.device_status()
+    bad = torch.zeros((M, 264), dtype=torch.bool, device="cuda")
+    bad[:, 5] = bad[:, 140] = bad[:, 77] = bad[M - 1, 200] = True
+    assert torch.equal(got[~bad], want[~bad]) and not torch.isfinite(got[bad]).any()
+
+
+@pytest.mark.parametrize("M,N,K,group", [(16401, 264, 128, 64), (16400, 8, 64, 32), (4099, 128, 64, 64)])
+def test_w4_gemm_many_rows_and_exact_workspace(M, N, K, group):
+    """Tokens in many tiles, whose last ends anywhere, with no byte of workspace or output more than said."""
+    rng = gen(11, M)
+    x = put(rng.standard_normal((M, K)), "f16")
+    w = w4_tensors(rng, N, K, group, False, "f16")
+    gamma = put(1 + 0.1 * rng.standard_normal(K), "f16")
+    need = fl.w4_gemm_workspace_size(M, K, True)
+    ws = torch.full((need + 512,), 0xa5, dtype=torch.uint8, device="cuda")
+    out = torch.full((M + 2, N), 7.0, dtype=torch.float16, device="cuda")
+    fl.w4_gemm(x, w[0], w[1], gamma=gamma, out=out[1:M + 1], workspace=ws[256:need + 256])
+    fl.device_status()
+    assert (ws[:256] == 0xa5).all() and (ws[need + 256:] == 0xa5).all() and (out[0] == 7).all() and (out[-1] == 7).all()
+    y, mag, sq = w4_ref(x, w, gamma, 1e-6)
+    w4_check(out[1:M + 1], y, mag, sq, K, "f16")
+    with pytest.raises(fl.FusedLinError):
+        fl.w4_gemm(x, w[0], w[1], gamma=gamma, workspace=ws[256:need + 240])
 
 
 # ---------------------------------------------------------------------------
@@ -583,6 +644,68 @@ def test_decode_steps_together():
     graph.close()
 
 
+@pytest.mark.parametrize("dt,fmt", [("f16", "int8"), ("bf16", "e4m3")])
+def test_decoder_layer_with_cache(dt, fmt):
+    """A prepared layer with rotary positions and a cache attached: half 0 gives what the calls one by one give, direct
+    and captured, follows positions and starts rewritten in place, and goes back to the plain half when detached."""
+    rng = gen(42)
+    M, D, Dkv, F, hd, page = 3, 512, 256, 512, 64, 16
+    e = lambda *s: torch.zeros(s, dtype=DT[dt], device="cuda")  # noqa: E731
+    T = {n: put(rng.standard_normal(s) / np.sqrt(s[-1]), dt) for n, s in
+         (("Wq", (D, D)), ("Wk", (Dkv, D)), ("Wv", (Dkv, D)), ("Wo", (D, D)), ("Wg", (F, D)), ("Wu", (F, D)), ("Wd", (D, F)))}
+    T.update(x=put(rng.standard_normal((M, D)), dt), gamma_attn=put(1 + 0.1 * rng.standard_normal(D), dt),
+             gamma_ffn=put(1 + 0.1 * rng.standard_normal(D), dt), q=e(M, D), k=e(M, Dkv), v=e(M, Dkv), attn=e(M, D), h=e(M, D),
+             out=e(M, D))
+    layer = fl.DecoderLayer(**T)
+    layer.issue(0)
+    q, k, v = (T[n].clone() for n in "qkv")
+    f = put((1e4 ** (-np.arange(24) / 24)).astype(np.float32))
+    pos = put(np.array([[5, 90, 17], [1, 2, 3]], dtype=np.int32))
+    table, start = put(np.array([[2, 4], [1, 0], [3, 5]], dtype=np.int32)), put(np.array([5, 30, 17], dtype=np.int32))
+    (kc, vc), (ks, vs) = cache(6, page, Dkv // hd, hd, fmt)
+    (kc2, vc2), (ks2, vs2) = cache(6, page, Dkv // hd, hd, fmt)
+    with pytest.raises(fl.FusedLinError):
+        layer.attach_cache(60, positions=pos, inv_freq=f, sections=(16, 8))
+    with pytest.raises(ValueError):
+        layer.attach_cache(hd, positions=pos, inv_freq=f, sections=(16, 9))
+    with pytest.raises(ValueError):
+        layer.attach_cache(hd, k_cache=kc, v_cache=vc, k_scale=ks, v_scale=vs, page_table=table)
+    layer.issue(0)
+    assert torch.equal(T["q"], q) and torch.equal(T["k"], k)  # refused: as it was
+    layer.attach_cache(hd, positions=pos, inv_freq=f, sections=(16, 8), k_cache=kc, v_cache=vc, k_scale=ks, v_scale=vs,
+                       page_table=table, start=start)
+
+    def expect():
+        rq, rk = fl.rope(q.unflatten(1, (D // hd, hd)), k.unflatten(1, (Dkv // hd, hd)), pos, f, sections=(16, 8))
+        fl.kv_write(rk, v.unflatten(1, (Dkv // hd, hd)), kc2, vc2, ks2, vs2, table, start)
+        return rq.flatten(1), rk.flatten(1)
+
+    def check():
+        rq, rk = expect()
+        assert torch.equal(T["q"], rq) and torch.equal(T["k"], rk) and torch.equal(T["v"], v)
+        for a, b in ((kc, kc2), (vc, vc2)):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        assert torch.equal(ks, ks2) and torch.equal(vs, vs2)
+    layer.issue(0)
+    check()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        graph = fl.Graph.capture(lambda: (layer.issue(0), layer.issue(1)))
+    torch.cuda.current_stream().wait_stream(side)
+    pos += 1
+    start += 1
+    graph.launch()
+    torch.cuda.synchronize()
+    check()
+    graph.close()
+    layer.attach_cache(hd)
+    layer.issue(0)
+    assert torch.equal(T["q"], q) and torch.equal(T["k"], k)
+    fl.device_status()
+    layer.close()
+
+
 def test_calls_on_two_streams_at_once():
     """The same operators issued on two streams with their own buffers give what they give alone."""
     rng = gen(41)
@@ -600,6 +723,103 @@ def test_calls_on_two_streams_at_once():
     for i in range(2):
         assert all(torch.equal(g, want[i]) for g in got[i])
         fl.device_status(streams[i])
+
+
+def serving_calls(rng, M):
+    """Every operator as a function that leaves its result in fixed tensors, those tensors, and the launches it makes."""
+    w = w4_tensors(rng, 512, 512, 64, True, "bf16")
+    wide = [w4_tensors(rng, 768, 512, 64, False, "bf16")[:2] for _ in range(2)] + [w4_tensors(rng, 512, 768, 64, False, "bf16")[:2]]
+    x, gamma = put(rng.standard_normal((M, 512)), "bf16"), put(1 + 0.1 * rng.standard_normal(512), "bf16")
+    e = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    o, y, q, k, ck, cv = e(M, 512), e(M, 512), e(M, 8, 64), e(M, 2, 64), e(M, 2, 64), e(M, 2, 64)
+    codes, scales = torch.zeros((512, 384), dtype=torch.uint8, device="cuda"), e(512, 24)
+    W = put(rng.standard_normal((512, 768)), "bf16")
+    pos, f = put(rng.integers(0, 5000, M).astype(np.int32)), put((1e4 ** (-np.arange(32) / 32)).astype(np.float32))
+    (kc, vc), (ks, vs) = cache((M + 15) // 16, 16, 2, 64, "e4m3")
+    table = put(np.arange((M + 15) // 16, dtype=np.int32)[None])
+    cu, start = put(np.array([0, M], dtype=np.int32)), put(np.zeros(1, dtype=np.int32))
+    heads = x.unflatten(1, (8, 64))
+    few = M <= 32
+    return [(lambda: fl.w4_quantize(W, 32, q=codes, scales=scales), (codes, scales), 1),
+            (lambda: fl.w4_gemm(x, *w[:2], zeros=w[2], gamma=gamma, out=o), (o,), 1 if few else 2),
+            (lambda: fl.w4_swiglu_ffn(x, gamma, *wide, out=y), (y,), 2 if few else 3),
+            (lambda: fl.rope(heads, heads[:, :2], pos, f, out_q=q, out_k=k), (q, k), 1),
+            (lambda: fl.kv_write(heads[:, :2], heads[:, 2:4], kc, vc, ks, vs, table, start, cu_rows=cu), (kc, vc, ks, vs), 1),
+            (lambda: fl.kv_read(kc, vc, ks, vs, table, cu, out_k=ck, out_v=cv), (ck, cv), 1)]
+
+
+def snapshot(tensors):
+    return [t.view(torch.uint8).clone() if t.element_size() == 1 else t.clone() for t in tensors]
+
+
+@pytest.mark.parametrize("M", [2, 300])
+@pytest.mark.parametrize("how", ["direct", "torch graph", "library graph", "no overlap of launches"])
+def test_every_way_of_issuing(M, how):
+    """Each operator's results are the same issued directly, captured and replayed after its tensors were overwritten,
+    and without programmatic launches; each counts its kernels."""
+    for call, made, launches in serving_calls(gen(43, M), M):
+        before = snapshot(made)
+        call()
+        torch.cuda.synchronize()
+        want = snapshot(made)
+        n = fl.kernel_launches()
+        if how == "direct":
+            call()
+            assert fl.kernel_launches() - n == launches
+        elif how == "no overlap of launches":
+            fl.set_option("pdl", 0)
+            try:
+                call()
+                torch.cuda.synchronize()
+            finally:
+                fl.set_option("pdl", 1)
+        elif how == "torch graph":
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                call()
+            for t, b in zip(made, before):
+                t.view(b.dtype).copy_(b)
+            graph.replay()
+        else:
+            side = torch.cuda.Stream()
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                graph = fl.Graph.capture(call)
+            for t, b in zip(made, before):
+                t.view(b.dtype).copy_(b)
+            # (a workspace that the call made belongs to the graph: this must not get it)
+            other = [torch.full((M * 768 * 2 + 4096,), 0xff, dtype=torch.uint8, device="cuda") for _ in range(4)]
+            with torch.cuda.stream(side):
+                other += [torch.full((M * 768 * 2 + 4096,), 0xff, dtype=torch.uint8, device="cuda") for _ in range(4)]
+            torch.cuda.synchronize()
+            graph.launch()
+            torch.cuda.synchronize()
+            assert all((t == 0xff).all() for t in other)
+            graph.close()
+        torch.cuda.synchronize()
+        for t, s in zip(made, want):
+            assert torch.equal(t.view(torch.uint8), s.view(torch.uint8))
+    fl.device_status()
+
+
+def test_tensors_made_on_a_stream():
+    """A call on a stream other than the current one takes its workspace and outputs from that stream's memory, so that
+    they are not blocks which the current stream's kernels still write."""
+    rng = gen(44)
+    w = w4_tensors(rng, 512, 512, 64, True, "bf16")
+    x, gamma = put(rng.standard_normal((300, 512)), "bf16"), put(1 + 0.1 * rng.standard_normal(512), "bf16")
+    want = fl.w4_gemm(x, *w[:2], zeros=w[2], gamma=gamma)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(20):
+        t = torch.empty((300, 512), dtype=torch.bfloat16, device="cuda")
+        for _ in range(50):
+            t.fill_(3.0)
+        del t
+        got = fl.w4_gemm(x, *w[:2], zeros=w[2], gamma=gamma, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    fl.device_status(side)
 
 
 def test_python_refusals():

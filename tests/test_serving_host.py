@@ -185,6 +185,11 @@ def test_struct_layouts_match_the_header(L):
     assert ctypes.sizeof(fl.W4Weight) == 32
     assert ctypes.sizeof(fl.RopeDesc) == 9 * 4 + 4 + 4 * 8 + 4 * 8 + 8 * 8
     assert ctypes.sizeof(fl.KvDesc) == 9 * 4 + 4 + 8 + 5 * 8 + 4 * 8 + 4 * 8
+    assert ctypes.sizeof(fl.LayerCacheDesc) == 4 * 4 + 4 * 8 + 5 * 4 + 4 + 8 + 7 * 8
+
+
+def test_attach_cache_refuses_a_null_layer(L):
+    assert L.fl_layer_attach_cache(None, None) == INVALID
 
 
 # ---------------------------------------------------------------------------
