@@ -89,7 +89,8 @@ struct TileParams {
     W4Params w;
     const float* row_scale;  // [M] 1 / rms of the rows of x, over kLift (with gamma)
     int bt, splits, steps_per_split, steps;  // K steps of 64
-    int row_tiles, tiles;
+    int row_tiles, tile0, tiles;             // tiles tile0 .. tiles - 1
+    int tail;                                // the second launch of a product
     int stages, w_stages, b_bytes;           // rings: stages * b_bytes of tokens, then the code stages
     int* status;
     unsigned long long timeout_ns;
@@ -254,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
     const uint32_t dfull = bar0 + 8u * (kBars - 3), dempty = bar0 + 8u * (kBars - 2), drain = bar0 + 8u * (kBars - 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int first_tile = blockIdx.x / p.splits, tile_step = gridDim.x / p.splits, rank = blockIdx.x % p.splits;
+    const int first_tile = p.tile0 + blockIdx.x / p.splits, tile_step = gridDim.x / p.splits, rank = blockIdx.x % p.splits;
     const int k0 = rank * p.steps_per_split, k1 = min(p.steps, k0 + p.steps_per_split), nk = k1 - k0;
     const int its = (nk + kGroups - 1) / kGroups;        // code stages of a tile
     const int s_count = (its + kSIter - 1) / kSIter;     // scale stages of a tile
@@ -305,7 +306,10 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
             for (int j = 0; j <= (DUAL ? 1 : 0); ++j)
                 tma_prefetch_2d(&p.tm_q[j], k0 * (kStep / 2) + i * (kWk / 2), row0_of(first_tile));
     }
-    griddep_wait();
+    // The tail of a product need not wait for the launch before it, which waited
+    // itself for what both read before it let this one in; it waits before it
+    // ends, so that what follows finds both done.
+    if (!p.tail) griddep_wait();
     if (threadIdx.x == 0) griddep_launch_dependents();
 
     // Scales, zero points and gamma of scale stage i of a tile into stage slot s
@@ -637,6 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    if (p.tail) griddep_wait();
 }
 
 template <int DT, bool DUAL, bool NORM>
@@ -705,45 +710,62 @@ fl_status w4_tile(int dt, bool dual, const W4Params& w, void* workspace, const h
     // CTAs or clusters, in cycles as measured. A K step costs the MMA (2.2 a
     // token) or, below some 260 tokens, what its warps need to expand the codes and
     // to issue it (570; 690 with gamma, which is multiplied in in fp32); a round
-    // its epilogue, a split the exchange of the partial sums. Ranges of a split
-    // are multiples of 128 k, the largest group.
+    // its epilogue, a split the exchange of the partial sums. Tiles left over from
+    // whole rounds may be split in a launch of their own (the tail), which fills
+    // the multiprocessors as they fall idle. Ranges of a split are multiples of
+    // 128 k, the largest group.
     static std::atomic<int> resident[9];
     double least = 0;
     const int tt0 = (w.M + kTok - 1) / kTok;
-    int token_tiles = 0;
+    int token_tiles = 0, tail_splits = 1, per_round = 0;
+    auto split_steps = [&](int s) { return ((p.steps + 1) / 2 + s - 1) / s * 2; };
+    auto can_split = [&](int s) {
+        const int per = split_steps(s);
+        return per >= 4 && (p.steps + per - 1) / per == s;
+    };
+    auto clusters = [&](int s) {  // resident at once (0: none)
+        int n = resident[s].load();
+        if (n == 0) {
+            n = Kern<DT_BF16, false, false>::resident(s, ctx.device);
+            if (n <= 0) n = -1;
+            resident[s] = n;
+        }
+        return n > 0 ? n : 0;
+    };
     for (int tt = tt0; tt <= 3 * tt0 && tt <= tt0 + 64; ++tt) {
         const int bt = ((w.M + tt - 1) / tt + 15) / 16 * 16;
         if (tt > tt0 && bt < 64) break;
         // (rounded up to 16 tokens, fewer tiles may do; none starts at or past M)
         const int count = (w.M + bt - 1) / bt;
-        for (int s = 1; s <= 8; ++s) {
-            const int per = ((p.steps + 1) / 2 + s - 1) / s * 2;
-            if (s > 1 && (per < 4 || (p.steps + per - 1) / per != s)) continue;
-            int n = resident[s].load();
-            if (n == 0) {
-                n = Kern<DT_BF16, false, false>::resident(s, ctx.device);
-                if (n <= 0) n = -1;
-                resident[s] = n;
-            }
-            if (n < 0) continue;
-            const double rounds = (double)(((long long)row_tiles * count + n - 1) / n);
-            const double least_step = norm ? 690.0 : 570.0, step = 2.2 * bt > least_step ? 2.2 * bt : least_step;
-            const double cost = s == 1 ? 5000.0 + rounds * (step * per + 6000.0)
-                                       : rounds * (step * per + 11000.0 + 12.0 * bt);
-            if (token_tiles == 0 || cost < least) {
-                least = cost;
-                token_tiles = count;
-                p.bt = bt;
-                p.splits = s;
-                p.steps_per_split = per;
-            }
+        const long long tiles = (long long)row_tiles * count;
+        const double least_step = norm ? 690.0 : 570.0, step = 2.2 * bt > least_step ? 2.2 * bt : least_step;
+        const double round = step * p.steps + 6000.0;
+        const int n1 = clusters(1);
+        if (n1 == 0) break;
+        auto consider = [&](double cost, int splits, int tail) {
+            if (token_tiles != 0 && cost >= least) return;
+            least = cost;
+            token_tiles = count;
+            p.bt = bt;
+            p.splits = splits;
+            tail_splits = tail;
+        };
+        consider(5000.0 + (double)((tiles + n1 - 1) / n1) * round, 1, 1);
+        for (int s = 2; s <= 8; ++s) {
+            const int n = can_split(s) ? clusters(s) : 0;
+            if (n == 0) continue;
+            const double one = step * split_steps(s) + 11000.0 + 12.0 * bt;
+            consider((double)((tiles + n - 1) / n) * one, s, 1);
+            if (tiles > n1 && tiles % n1 != 0)
+                consider(5000.0 + (double)(tiles / n1) * round + 3000.0 + (double)((tiles % n1 + n - 1) / n) * one, 1, s);
         }
+        per_round = n1;
     }
     if (token_tiles == 0) return host::fail(FL_ERR_CUDA, "4-bit tile kernel: no resident CTA");
     const long long tiles = (long long)row_tiles * token_tiles;
     if (tiles * p.splits > 0x7fffffffll) return host::fail(FL_ERR_UNSUPPORTED, "4-bit tile kernel: too many tiles");
     p.row_tiles = row_tiles;
-    p.tiles = (int)tiles;
+    const int all = (int)tiles, plain = tail_splits > 1 ? all / per_round * per_round : all;
     // rings: as many stages of tokens as leave the codes two stages, eight at most; the rest to the codes
     p.b_bytes = p.bt * kStep * 2;
     p.stages = (kRing - 2 * kWBytes) / p.b_bytes;
@@ -758,20 +780,27 @@ fl_status w4_tile(int dt, bool dual, const W4Params& w, void* workspace, const h
     p.w = w;
     p.status = ctx.status;
     p.timeout_ns = ctx.timeout_ns;
-    const int persistent = resident[1].load() > 0 ? resident[1].load() : ctx.sms;
-    const dim3 grid((unsigned)(p.splits > 1 ? p.tiles * p.splits : p.tiles < persistent ? p.tiles : persistent));
-    cudaError_t e;
     if (dual && !norm) return host::fail(FL_ERR_UNSUPPORTED, "4-bit tile kernel: the pair needs gamma");
-#define FL_LAUNCH(DT)                                                                                      \
-    e = dual ? Kern<DT, true, true>::launch(p, grid, ctx, stream)                                      \
-             : norm ? Kern<DT, false, true>::launch(p, grid, ctx, stream)                              \
+    // tiles [t0, t1) with K split over clusters of `splits`
+    auto launch_tiles = [&](int t0, int t1, int splits) {
+        p.tile0 = t0, p.tiles = t1, p.tail = t0 > 0;
+        p.splits = splits, p.steps_per_split = split_steps(splits);
+        const int n = t1 - t0;
+        const dim3 grid((unsigned)(splits > 1 ? n * splits : n < per_round ? n : per_round));
+        cudaError_t e;
+#define FL_LAUNCH(DT)                                                                                \
+    e = dual ? Kern<DT, true, true>::launch(p, grid, ctx, stream)                                    \
+             : norm ? Kern<DT, false, true>::launch(p, grid, ctx, stream)                            \
                     : Kern<DT, false, false>::launch(p, grid, ctx, stream)
-    if (dt == FL_F16)
-        FL_LAUNCH(DT_F16);
-    else
-        FL_LAUNCH(DT_BF16);
+        if (dt == FL_F16)
+            FL_LAUNCH(DT_F16);
+        else
+            FL_LAUNCH(DT_BF16);
 #undef FL_LAUNCH
-    return host::launched(e, "4-bit tile kernel");
+        return host::launched(e, "4-bit tile kernel");
+    };
+    if ((st = launch_tiles(0, plain, p.splits)) != FL_OK || plain == all) return st;
+    return launch_tiles(plain, all, tail_splits);
 }
 
 }  // namespace fl

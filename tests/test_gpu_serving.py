@@ -111,7 +111,8 @@ def w4_check(got, y, mag, sq, K, dt, act_mag=0.0, what=""):
 SHAPES = [(1, 8, 32, 32), (1, 1024, 1024, 128), (2, 264, 320, 64), (3, 40, 4096, 32), (7, 2048, 2048, 128),
           (8, 520, 11008, 128), (9, 136, 256, 64), (16, 1032, 1056, 32), (33, 8, 128, 128), (65, 392, 640, 64),
           (128, 128, 512, 128), (129, 512, 512, 32), (100, 1024, 1024, 64), (60, 2048, 2048, 128), (32, 4104, 1024, 32),
-          (17, 264, 11008, 128), (130, 2048, 4096, 128), (257, 264, 96, 32), (300, 6144, 1024, 64)]
+          (17, 264, 11008, 128), (130, 2048, 4096, 128), (257, 264, 96, 32), (300, 6144, 1024, 64),
+          (40, 20488, 2048, 128)]
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
@@ -144,7 +145,7 @@ def test_w4_gemm(dt, M, N, K, group):
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
 @pytest.mark.parametrize("M,D,F,group,zeros", [(1, 1024, 2816, 128, False), (3, 256, 384, 32, True), (8, 320, 64, 64, True),
                                                (20, 512, 1408, 64, False), (200, 384, 1024, 128, True),
-                                               (513, 1024, 2816, 128, False)])
+                                               (513, 1024, 2816, 128, False), (40, 2048, 9856, 64, False)])
 def test_w4_swiglu_ffn(dt, M, D, F, group, zeros):
     rng = gen(4, M, D, F)
     x = put(rng.standard_normal((M, D)), dt)
