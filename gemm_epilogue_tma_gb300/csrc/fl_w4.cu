@@ -4,11 +4,13 @@
 //   out[m, n] = act(r[m] * sum_k x'[m, k] w[n, k] + bias[n]) (+ residual[m, n])
 //   w[n, k]   = scale[n, k / G] * (code[n, k] - zero[n, k / G])
 //
-// with x' = x * gamma rounded to the dtype and r the RMSNorm row scale where
-// there is a prologue (else x and 1).
+// with x' = x * gamma and r the RMSNorm row scale where there is a prologue
+// (else x and 1). fl_w4_rows.cu computes few rows, fl_w4_tile.cu many.
+//
+// The quantiser is bound by HBM, 2.5 bytes a weight and 2 per group: 20.6 us at
+// 11008 x 4096, group 128 (5.5 TB/s), where its lanes' arithmetic is next.
 #include "fl_common.cuh"
 #include "fl_host.h"
-#include "fl_internal.h"
 #include "fl_quant.cuh"
 #include "fl_w4.h"
 
@@ -123,6 +125,7 @@ fl_status check_weight(const char* name, const fl_w4_weight* w, long long N, lon
     if (w->group != 32 && w->group != 64 && w->group != 128)
         return fail(FL_ERR_INVALID_ARG, "%s: group must be 32, 64 or 128 (%d)", name, w->group);
     if (N < 1 || K < 1) return fail(FL_ERR_INVALID_ARG, "%s: sizes must be positive (N=%lld K=%lld)", name, N, K);
+    if (N > 0x7fffff00ll) return fail(FL_ERR_UNSUPPORTED, "%s: too many rows (%lld)", name, N);
     if (N % 8 != 0 || K % w->group != 0)
         return fail(FL_ERR_ALIGNMENT, "%s: N must be a multiple of 8 and K of the group (N=%lld K=%lld group %d)", name,
                     N, K, w->group);

@@ -15,6 +15,13 @@
 // 128 or 1024, one subtraction leaves the integers); the activation rows are
 // stored in shared memory in the same order, one 16-byte vector per word.
 //
+// Measured: 1 x 4096 x 4096 4.8 us, 1 x 11008 x 4096 8.4 us (2.8 TB/s), SwiGLU FFN
+// 4096 x 11008 of 3 rows 23.7 us (2.9 TB/s). A CTA's start (rows of x to shared
+// memory, their norm, the first codes: 2.3 us at 1 x 1024 x 1024) is what keeps one
+// product of a decode step from the rate of its stream. Loads land in L1 lines, so
+// shared memory taken for more than the rows costs loads in flight: with the
+// largest carve-out the FFN took 32 us.
+//
 // Loads run in blocks of 16 (V = 1: 8) words of each of the lane's two weight rows,
 // double-buffered across units (16 or 8 + 8 weight rows); a CTA's 8 warps take
 // 8 slices of K and add their sums through shared memory in warp order.
@@ -381,18 +388,23 @@ cudaError_t launch_rows(const W4Params& p, const host::LaunchContext& ctx, cudaS
 
 // The choice between this kernel and the tile kernel, by rows and weights,
 // measured side by side (us, this kernel / the tile kernel):
-//   4096 x 4096: 32 rows 12.6 / 16.5, 64 rows 18.6 / 17.3
-//   FFN 4096 x 11008: 16 rows 44 / 80, 32 rows 71 / 81, 64 rows 130 / 83
-//   2048 x 2048: 64 rows 8.2 / 10.9; 4096 x 1024: 64 rows 9.2 / 9.4, 96 rows 12.8 / 9.9
 //   1024 x 1024: 128 rows 6.2 / 9.1
-int rows_limit(long long weights) { return weights <= (1ll << 20) ? 128 : weights <= (4ll << 20) ? 64 : 32; }
+//   2048 x 2048: 64 rows 8.2 / 10.9; 4096 x 1024: 64 rows 9.2 / 9.4, 96 rows 12.8 / 9.9
+//   4096 x 4096: 24 rows 10.6 / 13.8, 32 rows 12.6 / 13.8, 64 rows 18.6 / 14.6
+//   11008 x 4096: 32 rows 24 / 33; 4096 x 11008: 16 rows 17 / 20, 24 rows 23 / 20, 32 rows 26 / 20
+//   FFN 4096 x 11008: 16 rows 44 / 66, 24 rows 58 / 66, 32 rows 71 / 66, 64 rows 130 / 68
+//   (with its gate and up product here and the other there: 70 with 24 rows, so
+//   that long rows, for which 24 is late, keep to the limit of large weights)
+int rows_limit(long long weights, int K) {
+    return weights <= (1ll << 20) ? 128 : weights <= (4ll << 20) ? 64 : weights <= (64ll << 20) && K <= 8192 ? 32 : 24;
+}
 
 }  // namespace
 
 bool w4_few_rows(int M, int N, int K, bool dual) {
-    return M <= rows_limit((long long)N * K * (dual ? 2 : 1)) && smem_bytes(slab_rows(M), K) <= kSmemMax;
+    return M <= rows_limit((long long)N * K * (dual ? 2 : 1), K) && smem_bytes(slab_rows(M), K) <= kSmemMax;
 }
-bool w4_always_few(int M, int K) { return M <= 32 && smem_bytes(slab_rows(M), K) <= kSmemMax; }
+bool w4_always_few(int M, int K) { return M <= 24 && smem_bytes(slab_rows(M), K) <= kSmemMax; }
 
 fl_status w4_rows(int dt, bool dual, const W4Params& params, const host::LaunchContext& ctx, cudaStream_t stream) {
     W4Params p = params;

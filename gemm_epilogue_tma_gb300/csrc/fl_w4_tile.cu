@@ -1,4 +1,4 @@
-// 4-bit products for nine rows and more, on the tensor cores.
+// 4-bit products for more rows than the decode kernel takes, on the tensor cores.
 //
 // The weight is the M operand: a tile takes 128 weight rows (or, for the
 // SwiGLU pair, 64 rows of Wg and the same rows of Wu) against up to 256 tokens,
@@ -13,33 +13,44 @@
 // multiplied as they are (rounding x * gamma as well would be a third rounding
 // beside the weight's and the output's, and was 1.6 times the error of a plain
 // fp32 product rounded once). The row scale 1 / rms, from a kernel of its own
-// that reads x once, is applied to the fp32 sums.
+// that reads x once (2 us at 333 x 4096), is applied to the fp32 sums.
 //
-// What bounds it: with many tokens the shared-memory traffic of the B operand
-// (per K step 256 * 128 bytes written by TMA and read by the MMA, against 590
-// cycles of MMA); with few the weight stream, for which the K range is split over a
-// cluster of up to 8 CTAs whose fp32 partials are added through distributed
-// shared memory in rank order. A tile of two blocks of 128 rows by 128 tokens
-// moved fewer bytes per MMA but expanded every code for half as many tokens, and the
-// expansion (about 200 instructions a warp and step) set its pace: 237 us at
-// 4096^3.
+// What bounds it, per K step: with 256 tokens the MMA (514 cycles; 512 by the
+// tensor rate), with fewer the expansion of the codes, some 400 instructions a
+// warp, which sets a step's least time whatever the tile's width: 570 cycles, or
+// 690 where gamma is multiplied in. Measured: 4096^3 96 us (1430 TFLOP/s),
+// 2048 rows of the SwiGLU FFN 4096 x 11008 430 us (1290 TFLOP/s), 333 x 6144 x
+// 4096 35 us, 64 x 4096 x 4096 14.6 us. Leaving gamma's arithmetic out
+// altogether would save 2.5 %. A tile of two blocks of 128 rows by 128 tokens
+// moved fewer bytes per MMA but expanded every code for half as many tokens:
+// 237 us at 4096^3.
 //
 // Roles: warp 0 loads tokens (stages of 64 k) and codes (stages of 256 k) by
-// TMA, warp 1 owns tensor memory and issues the MMAs, warps 2 and 3 load the scales, zero points and
-// gamma of 1024 k at a time into shared memory (transposed: one row per thread
-// there; the first of them is loaded by the dequantising warps, which have
-// nothing else to do yet), warps 4-19 dequantise, four to a K step, and apply the
-// epilogue. (20 warps: a 21st would leave each thread 80 registers instead of
-// 96.) The producer loads codes whenever their ring has room, so that they,
-// which come from HBM and are needed first, run ahead as far as it reaches; the fewer the tokens, the more of shared memory is the codes'. A stage of tokens and the A slot of
-// the same step share one full and one empty barrier (the bytes and the four
-// warps' arrivals on the one, the MMA's commit on the other): the issuing warp
-// competes with four dequantising warps for its scheduler, and a step with two waits and two
-// commits took it 680 to 850 cycles whatever the tile's width.
+// TMA, warp 1 owns tensor memory and issues the MMAs, warps 2 and 3 load the
+// scales, zero points and gamma of 1024 k at a time into shared memory
+// (transposed: one row per thread there; the first of them is loaded by the
+// dequantising warps, which have nothing else to do yet), warps 4-19 dequantise,
+// four to a K step, and apply the epilogue. (20 warps: a 21st would leave each
+// thread 80 registers instead of 96; eight dequantising warps, with twice the
+// registers, took 163 us at 4096^3.) The producer loads codes whenever their ring
+// has room, so that they, which come from HBM and are needed first, run ahead as
+// far as it reaches; the fewer the tokens, the more of shared memory is the
+// codes'. A stage of tokens and the A slot of the same step share one full and
+// one empty barrier (the bytes and the four warps' arrivals on the one, the MMA's
+// commit on the other), so that the issuing warp waits once a step. No role
+// divides inside a step: the producer's tile arithmetic alone, done per step, once
+// held a step at 750 cycles.
 //
-// Without a split the CTAs are persistent: every ring runs on into the next
-// tile, and the dequantising warps expand the next tile's first steps before they apply
+// Few tiles: the K range is split over a cluster of up to 8 CTAs whose fp32
+// partials are added through distributed shared memory in rank order. Without
+// a split the CTAs are persistent: every ring runs on into the next tile, and
+// the dequantising warps expand the next tile's first steps before they apply
 // the epilogue, which holds the MMAs up only while the accumulator is read.
+// Tiles left over from whole rounds of CTAs go to a second launch, split over
+// clusters, whose CTAs start as those of the last round end: FFN 4096 x 11008
+// with 64 rows 84 -> 68 us, 333 x 11008 x 4096 68 -> 49 us. (Equal shares of the
+// last tiles' K range to every CTA of one launch, with partials through global
+// memory, cost 6 to 13 us for the exchange: 333 x 11008 x 4096 59 us.)
 //
 // Every mbarrier wait is bounded as in the other kernels.
 #include <atomic>

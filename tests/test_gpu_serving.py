@@ -284,6 +284,46 @@ def test_w4_gemm_many_rows_and_exact_workspace(M, N, K, group):
         fl.w4_gemm(x, w[0], w[1], gamma=gamma, workspace=ws[256:need + 240])
 
 
+def test_w4_tiles_left_over_from_whole_rounds():
+    """Sizes whose last tiles take a launch of their own beside the others: what follows reads a whole result, however
+    the launches are issued."""
+    rng = gen(12)
+    M, D, F = 40, 2048, 9856
+    x = put(rng.standard_normal((M, D)), "bf16")
+    gamma = put(1 + 0.1 * rng.standard_normal(D), "bf16")
+    Wg, Wu = (w4_tensors(rng, F, D, 128, False, "bf16")[:2] for _ in range(2))
+    Wd = w4_tensors(rng, D, F, 128, False, "bf16")[:2]
+    big = w4_tensors(rng, 20488, D, 128, True, "bf16")
+    ws = torch.empty(fl.w4_swiglu_ffn_workspace_size(M, D, F), dtype=torch.uint8, device="cuda")
+    y, z = torch.empty_like(x), torch.empty((M, 20488), dtype=torch.bfloat16, device="cuda")
+
+    def chain():
+        fl.w4_swiglu_ffn(x, gamma, Wg, Wu, Wd, out=y, workspace=ws)
+        fl.w4_gemm(y, big[0], big[1], zeros=big[2], gamma=gamma, out=z)
+        fl.w4_gemm(z[:, :F].contiguous(), Wd[0], Wd[1], residual=y, out=y)
+    fl.set_option("pdl", 0)
+    try:
+        n = fl.kernel_launches()
+        chain()
+        torch.cuda.synchronize()
+        assert fl.kernel_launches() - n > 3 + 2 + 1  # a row-scale kernel and two launches of tiles, twice; the down products
+    finally:
+        fl.set_option("pdl", 1)
+    want = y.clone(), z.clone()
+    for _ in range(20):
+        y.zero_(), z.zero_(), ws.fill_(0xff)
+        chain()
+        assert torch.equal(y, want[0]) and torch.equal(z, want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain()
+    for _ in range(5):
+        y.zero_(), z.zero_(), ws.fill_(0xff)
+        graph.replay()
+        assert torch.equal(y, want[0]) and torch.equal(z, want[1])
+    fl.device_status()
+
+
 # ---------------------------------------------------------------------------
 # rotary positions
 # ---------------------------------------------------------------------------

@@ -65,6 +65,7 @@ def test_w4_gemm_refusals(L):
     assert call(W=weight(group=48)) == INVALID and call(W=weight(group=128), K=192) == ALIGN
     assert call(W=weight(q=addr(10, 8))) == ALIGN and call(W=weight(zeros=addr(12, 2))) == ALIGN
     assert call(M=0) == INVALID and call(N=0) == INVALID and call(N=60) == ALIGN
+    assert call(N=0x7ffffff8) == UNSUPPORTED and "too many rows" in fl.last_error()
     assert call(act=4) == INVALID and call(dt=7) == INVALID
     assert call(eps=-1.0) == INVALID and call(eps=float("nan")) == INVALID and call(eps=float("inf")) == INVALID
     assert call(out=addr(0, 16)) == INVALID and call(out=addr(10, 16)) == INVALID and call(out=addr(11)) == INVALID
@@ -159,6 +160,7 @@ def test_kv_refusals(L, name):
     for n in ("rows", "heads", "head_dim", "page_size", "n_pages", "n_seqs", "table_pages"):
         assert call(**{n: -1}) == INVALID
     assert call(head_dim=60) == ALIGN and call(head_dim=264) == UNSUPPORTED
+    assert call(n_seqs=(1 << 30) + 1) == UNSUPPORTED and "sequences" in fl.last_error()
     assert call(format=2) == INVALID and call(dtype=2) == INVALID
     for n in ("k", "v", "k_cache", "v_cache", "k_scale", "v_scale", "page_table"):
         assert call(**{n: None}) == INVALID
