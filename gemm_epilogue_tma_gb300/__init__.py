@@ -489,12 +489,11 @@ def ops():
     return _ops
 
 
-def _issue(name, args, stream, makes=True):
-    """ops().name(*args) on `stream` (None: the current one). Tensors that the call makes for itself (makes: it may) are
-    `stream`'s, as those of any torch call under torch.cuda.stream(stream)."""
-    f = getattr(_ops or ops(), name)
-    if stream is None:
-        return f(*args, None)
+def _on(stream, name, args, makes=True):
+    """ops().name(*args) on `stream`. Tensors that the call makes for itself (makes: it may) are `stream`'s, as those of
+    any torch call under torch.cuda.stream(stream). (Calls on the current stream take no detour through here: it would
+    add a tenth to the host time of the shortest ones.)"""
+    f = getattr(ops(), name)
     if not makes:
         return f(*args, stream.cuda_stream)
     import torch
@@ -502,19 +501,20 @@ def _issue(name, args, stream, makes=True):
         return f(*args, None)
 
 
-def _issue_ws(name, args, stream, makes):
-    """_issue of a call that returns its output and the workspace it made, or None."""
-    out, ws = _issue(name, args, stream, makes)
-    if ws is not None:
+def _output(r):
+    """The output of a call that returns it with the workspace it made, or None."""
+    if r[1] is not None:
         for kept in _captures:
-            kept.append(ws)
-    return out
+            kept.append(r[1])
+    return r[0]
 
 
 def w4_quantize(W, group=128, q=None, scales=None, stream=None):
     """Symmetric round-to-nearest 4-bit quantisation of W [N, K]: returns (q, scales), codes [N, K / 2] uint8 (two
     along K to a byte, the even k in the low half, 8 standing for zero) and one scale of W's dtype per `group` k."""
-    return _issue("w4_quantize", (W, group, q, scales), stream, q is None or scales is None)
+    if stream is None:
+        return (_ops or ops()).w4_quantize(W, group, q, scales, None)
+    return _on(stream, "w4_quantize", (W, group, q, scales), q is None or scales is None)
 
 
 def w4_gemm_workspace_size(M: int, K: int, norm: bool) -> int:
@@ -527,8 +527,11 @@ def w4_gemm(x, q, scales, zeros=None, gamma=None, bias=None, residual=None, out=
     zeros[n, k / group]); norm is RMSNorm with `gamma`, or none. q, scales: as w4_quantize returns them; zeros
     [N, K / group] uint8 (8 everywhere if None). The workspace (w4_gemm_workspace_size bytes) must not be
     shared by calls or captured graphs that may overlap on the GPU."""
-    return _issue_ws("w4_gemm", (x, q, scales, zeros, gamma, bias, residual, out, eps, ACTS[act], workspace), stream,
-                     out is None or workspace is None)
+    if stream is None:
+        return _output((_ops or ops()).w4_gemm(x, q, scales, zeros, gamma, bias, residual, out, eps, ACTS[act], workspace,
+                                               None))
+    return _output(_on(stream, "w4_gemm", (x, q, scales, zeros, gamma, bias, residual, out, eps, ACTS[act], workspace),
+                       out is None or workspace is None))
 
 
 def w4_swiglu_ffn_workspace_size(M: int, D: int, F: int) -> int:
@@ -537,8 +540,10 @@ def w4_swiglu_ffn_workspace_size(M: int, D: int, F: int) -> int:
 
 def w4_swiglu_ffn(x, gamma, Wg, Wu, Wd, bias_down=None, out=None, eps=1e-6, workspace=None, stream=None):
     """swiglu_ffn on 4-bit weights, each a tuple (q, scales) or (q, scales, zeros)."""
-    return _issue_ws("w4_swiglu_ffn", (x, gamma, Wg, Wu, Wd, bias_down, out, eps, workspace), stream,
-                     out is None or workspace is None)
+    if stream is None:
+        return _output((_ops or ops()).w4_swiglu_ffn(x, gamma, Wg, Wu, Wd, bias_down, out, eps, workspace, None))
+    return _output(_on(stream, "w4_swiglu_ffn", (x, gamma, Wg, Wu, Wd, bias_down, out, eps, workspace),
+                       out is None or workspace is None))
 
 
 def rope(q, k, positions, inv_freq, sections=None, interleaved=False, inverse=False, out_q=None, out_k=None,
@@ -550,8 +555,10 @@ def rope(q, k, positions, inv_freq, sections=None, interleaved=False, inverse=Fa
     `sections` saying how many consecutive pairs follow each axis. inverse turns back: the gradient with respect to
     the input. q, k and the outputs may be strided views with contiguous channels (column ranges of a stacked
     projection's output); an output may be its input itself."""
-    return _issue("rope", (q, k, positions, inv_freq, sections, interleaved, inverse, out_q, out_k), stream,
-                  out_q is None or (out_k is None and k is not None))
+    if stream is None:
+        return (_ops or ops()).rope(q, k, positions, inv_freq, sections, interleaved, inverse, out_q, out_k, None)
+    return _on(stream, "rope", (q, k, positions, inv_freq, sections, interleaved, inverse, out_q, out_k),
+               out_q is None or (out_k is None and k is not None))
 
 
 def kv_write(k, v, k_cache, v_cache, k_scale, v_scale, page_table, start, cu_rows=None, stream=None):
@@ -564,7 +571,8 @@ def kv_write(k, v, k_cache, v_cache, k_scale, v_scale, page_table, start, cu_row
     No two rows of a call may have the same place in the cache."""
     if start is None:
         raise ValueError("start must be given")
-    _issue("kv_write", (k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_rows, start), stream, False)
+    (_ops or ops()).kv_write(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_rows, start,
+                             None if stream is None else stream.cuda_stream)
 
 
 def kv_read(k_cache, v_cache, k_scale, v_scale, page_table, cu_rows, start=None, out_k=None, out_v=None, stream=None):
@@ -574,7 +582,8 @@ def kv_read(k_cache, v_cache, k_scale, v_scale, page_table, cu_rows, start=None,
     Returns (out_k, out_v)."""
     if out_k is None or out_v is None:
         raise ValueError("out_k and out_v must be given: the row count is not known on the host")
-    _issue("kv_read", (out_k, out_v, k_cache, v_cache, k_scale, v_scale, page_table, cu_rows, start), stream, False)
+    (_ops or ops()).kv_read(out_k, out_v, k_cache, v_cache, k_scale, v_scale, page_table, cu_rows, start,
+                            None if stream is None else stream.cuda_stream)
     return out_k, out_v
 
 

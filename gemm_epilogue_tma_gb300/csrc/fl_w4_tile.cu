@@ -248,7 +248,8 @@ __global__ void __launch_bounds__(256) fl_w4_row_scale_kernel(const uint16_t* __
     if (lane == 0) scale[m] = rsqrtf(s / (float)K + eps) * (1.f / kLift<DT>);
 }
 
-template <int DT, bool DUAL, bool NORM>
+// RES: a residual is added.
+template <int DT, bool DUAL, bool NORM, bool RES>
 __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_constant__ TileParams p) {
     using Ops = DTypeOps<DT>;
     extern __shared__ uint8_t smem_raw[];
@@ -378,8 +379,15 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
         const int mine = m0 + t0 + (DUAL ? (up ? 1 : 0) + (odd ? 2 : 0) : (odd ? 1 : 0));
         const int end = nn < w.N ? min(w.M, m0 + p.bt) : 0;  // tokens below it are stored
         uint16_t* out = w.out + (size_t)mine * w.N + nn;
-        const uint16_t* res = !DUAL && w.residual != nullptr ? w.residual + (size_t)mine * w.N + nn : nullptr;
-        const float bias = !DUAL && w.bias != nullptr && n < w.N ? Ops::unpack(w.bias[n]).x : 0.f;
+        // (all of the residual is requested before any of it is used)
+        [[maybe_unused]] uint32_t res[2 * decltype(T)::value];
+        if constexpr (RES) {
+            const uint16_t* src = w.residual + (size_t)mine * w.N + nn;
+#pragma unroll
+            for (int e = 0; e < 2 * decltype(T)::value; ++e)
+                res[e] = mine + 2 * e < end ? *reinterpret_cast<const uint32_t*>(src + 2 * e * (size_t)w.N) : 0u;
+        }
+        [[maybe_unused]] const float bias = !DUAL && w.bias != nullptr && n < w.N ? Ops::unpack(w.bias[n]).x : 0.f;
         // of two values, the one for the even lane stays there, the other goes over
         auto exchange = [&](float v0, float v1) {
             const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
@@ -387,8 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
         };
         auto store = [&](float2 y, int t, size_t at) {
             if (mine + t >= end) return;
-            if (res != nullptr) {
-                const float2 x = Ops::unpack(*reinterpret_cast<const uint32_t*>(res + at));
+            if constexpr (RES) {
+                const float2 x = Ops::unpack(res[t / 2]);
                 y.x += x.x;
                 y.y += x.y;
             }
@@ -566,42 +574,43 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
                     ok = wait_bar(sfull(ss), (uint32_t)(phases & 1), p.status, p.timeout_ns, 26);
                 }
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                uint32_t o[32];
-                if (kb < nk) {
-                    const uint4 c0 = ld_shared_v4(src0 + ws * kWBytes), c1 = ld_shared_v4(src1 + ws * kWBytes);
-                    const uint16_t* ds = reinterpret_cast<const uint16_t*>(smem + kOffS + ss * kSBytes);
-                    const uint8_t* dz = smem + kOffZ + ss * kZBytes;
-                    const int kin = (it % kSIter) * kWk + grp * kStep;
-                    const int ga = kin >> gsh, gb = (kin + 32) >> gsh;
-                    uint32_t sa = ds[ga * kSPitch + r], sb = ds[gb * kSPitch + r];
-                    sa = NORM ? __float_as_uint(Ops::unpack(sa).x * kLift<DT>) : sa * 0x10001u;
-                    sb = NORM ? __float_as_uint(Ops::unpack(sb).x * kLift<DT>) : sb * 0x10001u;
-                    const uint32_t za = zero_const<DT>(dz[ga * kZPitch + r]), zb = zero_const<DT>(dz[gb * kZPitch + r]);
-                    const uint32_t sg = sbase + kOffG + ss * kGBytes + kin * 2;
-                    const uint32_t cw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint4 gv = NORM ? ld_shared_v4(sg + 16 * e) : make_uint4(0u, 0u, 0u, 0u);
-                        dequant8<DT, NORM>(cw[e], e < 4 ? sa : sb, e < 4 ? za : zb, gv, o + 4 * e);
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(wempty(ws));
-                if (++ws == nw) ws = 0, wph ^= 1u;
-                if (it % kSIter == kSIter - 1 || it == its - 1) {
-                    if (lane == 0) mbar_arrive(sempty(ss));
-                    ++g;
-                }
                 if (kb < nk) {
                     ok = __all_sync(0xffffffffu, wait_bar(empty(a), aph ^ 1u, p.status, p.timeout_ns, 27));
                     if (!ok) break;
                     tc_fence_after();
-                    tmem_st_32x32b_x32(dcol + kACol + 32u * a, o);
+                    const uint16_t* ds = reinterpret_cast<const uint16_t*>(smem + kOffS + ss * kSBytes) + r;
+                    const uint8_t* dz = smem + kOffZ + ss * kZBytes + r;
+                    const int kin = (it % kSIter) * kWk + grp * kStep;
+                    const uint32_t sg = sbase + kOffG + ss * kGBytes + kin * 2;
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        const uint4 c = ld_shared_v4((h ? src1 : src0) + ws * kWBytes);
+                        const int g1 = (kin + 32 * h) >> gsh;
+                        uint32_t sc = ds[g1 * kSPitch];
+                        sc = NORM ? __float_as_uint(Ops::unpack(sc).x * kLift<DT>) : sc * 0x10001u;
+                        const uint32_t zc = zero_const<DT>(dz[g1 * kZPitch]);
+                        const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+                        uint32_t o[16];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint4 gv = NORM ? ld_shared_v4(sg + 64 * h + 16 * e) : make_uint4(0u, 0u, 0u, 0u);
+                            dequant8<DT, NORM>(cw[e], sc, zc, gv, o + 4 * e);
+                        }
+                        tmem_st_32x32b_x16(dcol + kACol + 32u * a + 16u * h, o);
+                    }
                     tmem_st_wait();
                     tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(full(a));
-                    if ((a += kGroups) >= nb) a -= nb, aph ^= 1u;
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    if (kb < nk) mbar_arrive(full(a));
+                    mbar_arrive(wempty(ws));
+                }
+                if (kb < nk && (a += kGroups) >= nb) a -= nb, aph ^= 1u;
+                if (++ws == nw) ws = 0, wph ^= 1u;
+                if (it % kSIter == kSIter - 1 || it == its - 1) {
+                    if (lane == 0) mbar_arrive(sempty(ss));
+                    ++g;
                 }
                 // the tile before this one: its last MMAs ran while this tile's first steps were expanded
                 if (it == 0 && last >= 0) {
@@ -655,11 +664,11 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
     if (p.tail) griddep_wait();
 }
 
-template <int DT, bool DUAL, bool NORM>
+template <int DT, bool DUAL, bool NORM, bool RES>
 struct Kern {
     static cudaError_t configure(int device) {
         static std::atomic<unsigned long long> done{0};
-        return host::allow_smem(fl_w4_tile_kernel<DT, DUAL, NORM>, kSmem, device, done);
+        return host::allow_smem(fl_w4_tile_kernel<DT, DUAL, NORM, RES>, kSmem, device, done);
     }
     static void config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* a, dim3 grid, int splits, int pdl, cudaStream_t s) {
         cfg = {};
@@ -681,7 +690,7 @@ struct Kern {
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute a[2];
         config(cfg, a, grid, p.splits, ctx.pdl, s);
-        return cudaLaunchKernelEx(&cfg, fl_w4_tile_kernel<DT, DUAL, NORM>, p);
+        return cudaLaunchKernelEx(&cfg, fl_w4_tile_kernel<DT, DUAL, NORM, RES>, p);
     }
     // clusters of `splits` CTAs that are resident at once
     static int resident(int splits, int device) {
@@ -690,7 +699,7 @@ struct Kern {
         cudaLaunchAttribute a[2];
         config(cfg, a, dim3((unsigned)splits), splits, 0, nullptr);
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, fl_w4_tile_kernel<DT, DUAL, NORM>, &cfg) != cudaSuccess) {
+        if (cudaOccupancyMaxActiveClusters(&n, fl_w4_tile_kernel<DT, DUAL, NORM, RES>, &cfg) != cudaSuccess) {
             cudaGetLastError();
             return 0;
         }
@@ -710,8 +719,12 @@ fl_status w4_tile(int dt, bool dual, const W4Params& w, void* workspace, const h
         float* scale = static_cast<float*>(workspace);
         p.row_scale = scale;
         const dim3 grid((unsigned)((w.M + 7) / 8));
+        // Its CTAs begin only when the kernel before it is done if they have much to read: let in
+        // early they crowd into the few multiprocessors that are idle in its last round
+        // (us of a product, early / not: 64 x 4096^2 13.8 / 14.0, 333 22.0 / 22.0, 2048 67.3 / 61.5).
+        const int early = (long long)w.M * w.K < (1ll << 21) ? ctx.pdl : 0;
         auto kern = dt == FL_F16 ? fl_w4_row_scale_kernel<DT_F16> : fl_w4_row_scale_kernel<DT_BF16>;
-        const fl_status st = host::launched(host::launch(kern, grid, 256, 0, ctx.pdl, stream, w.x, scale, w.M, w.K, w.eps),
+        const fl_status st = host::launched(host::launch(kern, grid, 256, 0, early, stream, w.x, scale, w.M, w.K, w.eps),
                                             "row scale kernel");
         if (st != FL_OK) return st;
     }
@@ -737,7 +750,7 @@ fl_status w4_tile(int dt, bool dual, const W4Params& w, void* workspace, const h
     auto clusters = [&](int s) {  // resident at once (0: none)
         int n = resident[s].load();
         if (n == 0) {
-            n = Kern<DT_BF16, false, false>::resident(s, ctx.device);
+            n = Kern<DT_BF16, false, false, false>::resident(s, ctx.device);
             if (n <= 0) n = -1;
             resident[s] = n;
         }
@@ -797,12 +810,15 @@ fl_status w4_tile(int dt, bool dual, const W4Params& w, void* workspace, const h
         p.tile0 = t0, p.tiles = t1, p.tail = t0 > 0;
         p.splits = splits, p.steps_per_split = split_steps(splits);
         const int n = t1 - t0;
+        const bool res = w.residual != nullptr;
         const dim3 grid((unsigned)(splits > 1 ? n * splits : n < per_round ? n : per_round));
         cudaError_t e;
 #define FL_LAUNCH(DT)                                                                                \
-    e = dual ? Kern<DT, true, true>::launch(p, grid, ctx, stream)                                    \
-             : norm ? Kern<DT, false, true>::launch(p, grid, ctx, stream)                            \
-                    : Kern<DT, false, false>::launch(p, grid, ctx, stream)
+    e = dual ? Kern<DT, true, true, false>::launch(p, grid, ctx, stream)                             \
+        : norm ? (res ? Kern<DT, false, true, true>::launch(p, grid, ctx, stream)                    \
+                      : Kern<DT, false, true, false>::launch(p, grid, ctx, stream))                  \
+               : (res ? Kern<DT, false, false, true>::launch(p, grid, ctx, stream)                   \
+                      : Kern<DT, false, false, false>::launch(p, grid, ctx, stream))
         if (dt == FL_F16)
             FL_LAUNCH(DT_F16);
         else
