@@ -13,17 +13,17 @@
 // multiplied as they are (rounding x * gamma as well would be a third rounding
 // beside the weight's and the output's, and was 1.6 times the error of a plain
 // fp32 product rounded once). The row scale 1 / rms, from a kernel of its own
-// that reads x once (2 us at 333 x 4096), is applied to the fp32 sums.
+// that reads x once (2 us at 333 x 4096, 5 at 2048 x 4096), is applied to the fp32 sums.
 //
 // What bounds it, per K step: with 256 tokens the MMA (514 cycles; 512 by the
-// tensor rate), with fewer the expansion of the codes, some 400 instructions a
-// warp, which sets a step's least time whatever the tile's width: 570 cycles, or
-// 690 where gamma is multiplied in. Measured: 4096^3 96 us (1430 TFLOP/s),
-// 2048 rows of the SwiGLU FFN 4096 x 11008 430 us (1290 TFLOP/s), 333 x 6144 x
-// 4096 35 us, 64 x 4096 x 4096 14.6 us. Leaving gamma's arithmetic out
-// altogether would save 2.5 %. A tile of two blocks of 128 rows by 128 tokens
-// moved fewer bytes per MMA but expanded every code for half as many tokens:
-// 237 us at 4096^3.
+// tensor rate), with fewer the expansion of the codes, which sets a step's
+// least time whatever the tile's width: some 540 cycles, a tenth more where gamma
+// is multiplied in. Measured: 4096^3 86 to 92 us by box (1490 to 1600 TFLOP/s), 2048
+// rows of the SwiGLU FFN 4096 x 11008 366 to 403 us (1375 to 1510 TFLOP/s), 333 x 6144 x 4096 30 us, 64 x 4096 x
+// 4096 14.0 us. The warps fetch instructions as hard as they compute: a step's two halves as
+// one loop of half the code took 6 % off every size, four quarters gave it
+// back. A tile of two blocks of 128 rows by 128 tokens moved fewer bytes per MMA
+// but expanded every code for half as many tokens: 237 us at 4096^3, when this one took 149.
 //
 // Roles: warp 0 loads tokens (stages of 64 k) and codes (stages of 256 k) by
 // TMA, warp 1 owns tensor memory and issues the MMAs, warps 2 and 3 load the
