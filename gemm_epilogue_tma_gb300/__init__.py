@@ -323,6 +323,8 @@ class DecoderLayer:
             _check(lib().fl_layer_attach_cache(self._h, None))
             self.attached = ()
             return
+        if int(head_dim) < 1 or T["q"].shape[1] % head_dim or T["k"].shape[1] % head_dim:
+            raise ValueError(f"head_dim {head_dim} must divide the widths of q and k")
         d = LayerCacheDesc(head_dim=head_dim)
         kept = []
 

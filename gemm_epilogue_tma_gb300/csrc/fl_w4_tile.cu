@@ -10,20 +10,21 @@
 //
 // Roundings: the weight is rounded once, scale * (code - zero), or with the
 // RMSNorm prologue scale * gamma * (code - zero), so that the tokens are
-// multiplied as they are (rounding x * gamma as well would be a third rounding
-// beside the weight's and the output's, and was 1.6 times the error of a plain
-// fp32 product rounded once). The row scale 1 / rms, from a kernel of its own
+// multiplied as they are: with the output's two roundings, the error 1.4 times
+// that of an fp32 product rounded once (rounding x * gamma as well would be a
+// third: 1.6 times). The row scale 1 / rms, from a kernel of its own
 // that reads x once (2 us at 333 x 4096, 5 at 2048 x 4096), is applied to the fp32 sums.
 //
 // What bounds it, per K step: with 256 tokens the MMA (514 cycles; 512 by the
 // tensor rate), with fewer the expansion of the codes, which sets a step's
 // least time whatever the tile's width: some 540 cycles, a tenth more where gamma
-// is multiplied in. Measured: 4096^3 86 to 92 us by box (1490 to 1600 TFLOP/s), 2048
-// rows of the SwiGLU FFN 4096 x 11008 366 to 403 us (1375 to 1510 TFLOP/s), 333 x 6144 x 4096 30 us, 64 x 4096 x
-// 4096 14.0 us. The warps fetch instructions as hard as they compute: a step's two halves as
-// one loop of half the code took 6 % off every size, four quarters gave it
-// back. A tile of two blocks of 128 rows by 128 tokens moved fewer bytes per MMA
-// but expanded every code for half as many tokens: 237 us at 4096^3, when this one took 149.
+// is multiplied in. Measured: 4096^3 86 to 92 us by box (1490 to 1600 TFLOP/s),
+// 2048 rows of the SwiGLU FFN 4096 x 11008 366 to 403 us (1375 to 1510 TFLOP/s),
+// 333 x 6144 x 4096 30 us, 64 x 4096 x 4096 14.0 us. The warps fetch instructions
+// as hard as they compute: a step's two halves as one loop of half the code took
+// 6 % off every size, four quarters gave it back. A tile of two blocks of 128
+// rows by 128 tokens moved fewer bytes per MMA but expanded every code for half
+// as many tokens: 237 us at 4096^3, when this one took 149.
 //
 // Roles: warp 0 loads tokens (stages of 64 k) and codes (stages of 256 k) by
 // TMA, warp 1 owns tensor memory and issues the MMAs, warps 2 and 3 load the
@@ -46,8 +47,8 @@
 // a split the CTAs are persistent: every ring runs on into the next tile, and
 // the dequantising warps expand the next tile's first steps before they apply
 // the epilogue, which holds the MMAs up only while the accumulator is read.
-// Tiles left over from whole rounds of CTAs go to a second launch, split over
-// clusters, whose CTAs start as those of the last round end: FFN 4096 x 11008
+// Tiles left over from whole waves of CTAs go to a second launch, split over
+// clusters, whose CTAs start as those of the last wave end: FFN 4096 x 11008
 // with 64 rows 84 -> 68 us, 333 x 11008 x 4096 68 -> 49 us. (Equal shares of the
 // last tiles' K range to every CTA of one launch, with partials through global
 // memory, cost 6 to 13 us for the exchange: 333 x 11008 x 4096 59 us.)
@@ -720,7 +721,7 @@ fl_status w4_tile(int dt, bool dual, const W4Params& w, void* workspace, const h
         p.row_scale = scale;
         const dim3 grid((unsigned)((w.M + 7) / 8));
         // Its CTAs begin only when the kernel before it is done if they have much to read: let in
-        // early they crowd into the few multiprocessors that are idle in its last round
+        // early they crowd into the few multiprocessors that are idle in its last wave
         // (us of a product, early / not: 64 x 4096^2 13.8 / 14.0, 333 22.0 / 22.0, 2048 67.3 / 61.5).
         const int early = (long long)w.M * w.K < (1ll << 21) ? ctx.pdl : 0;
         auto kern = dt == FL_F16 ? fl_w4_row_scale_kernel<DT_F16> : fl_w4_row_scale_kernel<DT_BF16>;
@@ -730,12 +731,12 @@ fl_status w4_tile(int dt, bool dual, const W4Params& w, void* workspace, const h
     }
     p.steps = (w.K + kStep - 1) / kStep;
     const int rows = dual ? kRows / 2 : kRows, row_tiles = (w.N + rows - 1) / rows;
-    // Tokens of a tile and K split: the least time of whole rounds of resident
+    // Tokens of a tile and K split: the least time of whole waves of resident
     // CTAs or clusters, in cycles as measured. A K step costs the MMA (2.2 a
     // token) or, below some 260 tokens, what its warps need to expand the codes and
-    // to issue it (570; 690 with gamma, which is multiplied in in fp32); a round
+    // to issue it (570; 690 with gamma, which is multiplied in in fp32); a wave
     // its epilogue, a split the exchange of the partial sums. Tiles left over from
-    // whole rounds may be split in a launch of their own (the tail), which fills
+    // whole waves may be split in a launch of their own (the tail), which fills
     // the multiprocessors as they fall idle. Ranges of a split are multiples of
     // 128 k, the largest group.
     static std::atomic<int> resident[9];

@@ -705,8 +705,11 @@ def test_decoder_layer_with_cache(dt, fmt):
     table, start = put(np.array([[2, 4], [1, 0], [3, 5]], dtype=np.int32)), put(np.array([5, 30, 17], dtype=np.int32))
     (kc, vc), (ks, vs) = cache(6, page, Dkv // hd, hd, fmt)
     (kc2, vc2), (ks2, vs2) = cache(6, page, Dkv // hd, hd, fmt)
-    with pytest.raises(fl.FusedLinError):
-        layer.attach_cache(60, positions=pos, inv_freq=f, sections=(16, 8))
+    for head_dim in (60, 0):
+        with pytest.raises(ValueError):
+            layer.attach_cache(head_dim, positions=pos, inv_freq=f, sections=(16, 8))
+    with pytest.raises(fl.FusedLinError):                      # 24 pairs do not fit in 32 channels
+        layer.attach_cache(32, positions=pos, inv_freq=f, sections=(16, 8))
     with pytest.raises(ValueError):
         layer.attach_cache(hd, positions=pos, inv_freq=f, sections=(16, 9))
     with pytest.raises(ValueError):
