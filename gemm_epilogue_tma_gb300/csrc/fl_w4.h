@@ -20,7 +20,8 @@ struct W4Params {
     const uint16_t* residual;  // [M, N] or null
     uint16_t* out;             // [M, N]
     int M, N, K, group, act;
-    int slab;                  // decode kernel: rows of one slab of the grid
+    int slab;                  // decode kernel: rows of one slab of the grid, and whether
+    bool halves;               // x * gamma is carried as two 16-bit numbers
     float eps;
 };
 

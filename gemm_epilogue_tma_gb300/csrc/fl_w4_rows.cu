@@ -26,6 +26,11 @@
 // double-buffered across units (16 or 8 + 8 weight rows); a CTA's 8 warps take
 // 8 slices of K and add their sums through shared memory in warp order.
 //
+// x * gamma is rounded to the dtype, the one rounding before the output's. For up
+// to four rows half of the MMA's columns would be idle, and take what that rounding
+// cuts off: there is no rounding to speak of then (FFN of 3 rows 23.8 -> 24.1 us,
+// 3 x 4096 x 4096 5.3 -> 5.8).
+//
 // More than eight rows are slabs of at most eight, side by side in the grid:
 // they walk the weight at the same pace, so that it is read from HBM once and
 // by the other slabs from L2. w4_few_rows says up to where that beats the
@@ -211,7 +216,16 @@ __device__ __forceinline__ uint4 pair_up(const uint4& v) {
                       __byte_perm(v.y, v.w, 0x7632));
 }
 
-// The activation rows in shared memory: x, or x * gamma rounded once with the
+// x * g - p of packed pairs, p being x * g rounded: the difference fits the dtype to
+// its own precision.
+template <int DT>
+__device__ __forceinline__ uint32_t rest(uint32_t x, uint32_t g, uint32_t p) {
+    const float2 a = DTypeOps<DT>::unpack(x), b = DTypeOps<DT>::unpack(g), c = DTypeOps<DT>::unpack(p);
+    return DTypeOps<DT>::pack(fmaf(a.x, b.x, -c.x), fmaf(a.y, b.y, -c.y));
+}
+
+// The activation rows in shared memory: x, or x * gamma rounded once (and what
+// that leaves in rows of their own behind, p.halves) with the
 // RMS row scale in rscale. Vector v of a row (8 k) goes to the place where the
 // quad reads it: group v / 4V, word v % V of lane v / V % 4. R: a bound on M.
 template <int DT, bool NORM, int R, int V, typename Pre>
@@ -254,8 +268,11 @@ __device__ void build_rows(const W4Params& p, const uint16_t* x, int M, uint4* x
                         const float2 f = Ops::unpack(w[e]);
                         sq[m] = fmaf(f.x, f.x, fmaf(f.y, f.y, sq[m]));
                     }
-                    o = make_uint4(Ops::mul2(o.x, gv[j].x), Ops::mul2(o.y, gv[j].y), Ops::mul2(o.z, gv[j].z),
-                                   Ops::mul2(o.w, gv[j].w));
+                    const uint4 g = gv[j], x1 = o;
+                    o = make_uint4(Ops::mul2(o.x, g.x), Ops::mul2(o.y, g.y), Ops::mul2(o.z, g.z), Ops::mul2(o.w, g.w));
+                    if (R <= 4 && p.halves)
+                        xs[(M + m) * ld + to] = pair_up(make_uint4(rest<DT>(x1.x, g.x, o.x), rest<DT>(x1.y, g.y, o.y),
+                                                                   rest<DT>(x1.z, g.z, o.z), rest<DT>(x1.w, g.w, o.w)));
                 }
                 xs[m * ld + to] = pair_up(o);
             }
@@ -321,8 +338,10 @@ __global__ void __launch_bounds__(kThreads, 2) fl_w4_rows_kernel(const __grid_co
         else build_rows<DT, false, 8, V>(p, x, M, xs, rscale, pre);
     }
     griddep_launch_dependents();
-    // (a column of the MMA past the last row is not used: any row will do)
-    const uint4* xrow = xs + (g < M ? g : 0) * row_vecs(p.K) + t;
+    // columns 0 to 3, and 4 to 7 with p.halves: a row and what its rounding left
+    // (a column past the last row is not used: any row will do)
+    const int row = p.halves && g >= 4 ? (g - 4 < M ? M + g - 4 : 0) : g < M ? g : 0;
+    const uint4* xrow = xs + row * row_vecs(p.K) + t;
 
     int q = 0, buf = 0;
     for (int u = blockIdx.x; u < units; u += gridDim.x, buf ^= 1) {
@@ -353,6 +372,13 @@ __global__ void __launch_bounds__(kThreads, 2) fl_w4_rows_kernel(const __grid_co
                 y += src[w * 128];
                 if (DUAL) up += src[w * 128 + 2];
             }
+            if (p.halves) {  // (columns 4 on: two lanes further)
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    y += src[w * 128 + 8];
+                    if (DUAL) up += src[w * 128 + 10];
+                }
+            }
             const int n = DUAL ? u * 8 + r : u * 16 + r;
             const size_t at = (size_t)(m0 + m) * p.N + n;
             if constexpr (DUAL) {
@@ -379,7 +405,7 @@ cudaError_t launch_rows(const W4Params& p, const host::LaunchContext& ctx, cudaS
     static std::atomic<unsigned long long> done{0};
     const cudaError_t attr = host::allow_smem(kern, kSmemMax, ctx.device, done);
     if (attr != cudaSuccess) return attr;
-    const int slabs = slabs_of(p.M), smem = smem_bytes(p.slab, p.K), units = DUAL ? p.N / 8 : (p.N + 15) / 16;
+    const int slabs = slabs_of(p.M), smem = smem_bytes(p.halves ? 2 * p.slab : p.slab, p.K), units = DUAL ? p.N / 8 : (p.N + 15) / 16;
     int most = ctx.sms * (smem <= kSmemPair ? 2 : 1) / slabs;  // resident CTAs of a slab
     if (most < 1) most = 1;
     return host::launch(kern, dim3((unsigned)(units < most ? units : most), (unsigned)slabs), kThreads, (size_t)smem, ctx.pdl,
@@ -409,6 +435,9 @@ bool w4_always_few(int M, int K) { return M <= 24 && smem_bytes(slab_rows(M), K)
 fl_status w4_rows(int dt, bool dual, const W4Params& params, const host::LaunchContext& ctx, cudaStream_t stream) {
     W4Params p = params;
     p.slab = slab_rows(p.M);
+    // Up to four rows leave half of the MMA's columns idle: there go the parts of
+    // x * gamma that rounding it cuts off, if they fit beside a second CTA.
+    p.halves = p.gamma != nullptr && p.slab <= 4 && smem_bytes(2 * p.slab, p.K) <= kSmemPair;
     cudaError_t e = cudaErrorInvalidValue;
 #define FL_CASE(DT, DUAL, V)                                             \
     if (dt == DT && dual == DUAL && p.group == 32 * V)                   \

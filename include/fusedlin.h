@@ -450,7 +450,7 @@ fl_status fl_w4_quantize(const void* W, void* q, void* scales, int N, int K, int
  * out[M,N] = act(norm(x)[M,K] W^T + bias) (+ residual) on a 4-bit weight.
  *   gamma: [K], the RMSNorm prologue of fl_norm_gemm; NULL: x as it is. With
  *   gamma one product is formed in the dtype, in fp16 within its range: x * gamma
- *   (few rows) or 64 * w * gamma (many).
+ *   (few rows; up to four keep what its rounding cuts off) or 64 * w * gamma (many).
  *   bias [N] and residual [M,N] may be NULL; residual may be the same pointer
  *   as out. Epilogue order as in fl_gemm_epilogue.
  * workspace: fl_w4_gemm_workspace_size(M, K, gamma != NULL) bytes (0 for some

@@ -247,6 +247,25 @@ def test_w4_gemm_small_gamma(dt, M):
     assert np.sqrt((err ** 2).mean()) <= np.sqrt((u * u * (y ** 2 + 2 * sq)).mean()) + last
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("M,N,K,group", [(1, 264, 1024, 32), (2, 136, 4096, 128), (3, 520, 320, 64), (4, 1024, 2048, 128)])
+def test_w4_gemm_up_to_four_rows_round_the_output_alone(dt, M, N, K, group):
+    """x * gamma is carried as two numbers of the dtype, off by u^2 of it (and half of fp16's smallest value), the codes are
+    exact and the sums fp32: next to those the output's rounding is the only one."""
+    rng = gen(13, M, N, K)
+    x = put(rng.standard_normal((M, K)) * np.where(rng.random(K) < 0.01, 20.0, 1.0), dt)
+    w = w4_tensors(rng, N, K, group, True, dt)
+    gamma = put(1 + 0.1 * rng.standard_normal(K), dt)
+    got = fl.w4_gemm(x, w[0], w[1], zeros=w[2], gamma=gamma)
+    fl.device_status()
+    y, mag, _ = w4_ref(x, w, gamma, 1e-6)
+    W = oracle.w4_weight(w[0].cpu().numpy(), f64(w[1]), w[2].cpu().numpy())
+    rms = 1 / np.sqrt((f64(x) ** 2).mean(1, keepdims=True) + 1e-6)
+    small = 2.0 ** -25 * rms * np.abs(W).sum(1) if dt == "f16" else 0.0
+    u = U[dt]
+    assert (np.abs(f64(got) - y) <= u * np.abs(y) + (u * u + K * 2.0 ** -22) * mag + small + 2.0 ** -25).all()
+
+
 @pytest.mark.parametrize("M", [1, 8, 20, 40, 300])
 def test_w4_gemm_not_finite_weights(M):
     """A NaN or infinite scale, bias or residual stays in the outputs that it belongs to."""
