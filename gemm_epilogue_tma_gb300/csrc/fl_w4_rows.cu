@@ -15,8 +15,8 @@
 // 128 or 1024, one subtraction leaves the integers); the activation rows are
 // stored in shared memory in the same order, one 16-byte vector per word.
 //
-// Measured: 1 x 4096 x 4096 4.8 us, 1 x 11008 x 4096 8.4 us (2.8 TB/s), SwiGLU FFN
-// 4096 x 11008 of 3 rows 23.7 us (2.9 TB/s). A CTA's start (rows of x to shared
+// Measured: 1 x 4096 x 4096 4.9 us, 1 x 11008 x 4096 8.6 us (2.7 TB/s), SwiGLU FFN
+// 4096 x 11008 of 3 rows 24.1 us (2.9 TB/s). A CTA's start (rows of x to shared
 // memory, their norm, the first codes: 2.3 us at 1 x 1024 x 1024) is what keeps one
 // product of a decode step from the rate of its stream. Loads land in L1 lines, so
 // shared memory taken for more than the rows costs loads in flight: with the
