@@ -26,7 +26,8 @@
 // double-buffered across units (16 or 8 + 8 weight rows); a CTA's 8 warps take
 // 8 slices of K and add their sums through shared memory in warp order.
 //
-// x * gamma is rounded to the dtype, the one rounding before the output's. For up
+// x * gamma is rounded to the dtype, the one rounding before the output's (in fp16 times
+// a power of two where a row's products leave the type's range: lift_rows). For up
 // to four rows half of the MMA's columns would be idle, and take what that rounding
 // cuts off: there is no rounding to speak of then (FFN of 3 rows 23.8 -> 24.1 us,
 // 3 x 4096 x 4096 5.3 -> 5.8).
@@ -37,6 +38,7 @@
 // tensor-core tile kernel, which expands each code once for all rows.
 #include "fl_common.cuh"
 #include "fl_host.h"
+#include "fl_quant.cuh"
 #include "fl_w4.h"
 
 namespace fl {
@@ -46,6 +48,7 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 // words of one weight row in a register block (groups of 32 also hold four times the scales)
 __host__ __device__ constexpr int block_words(int V) { return V == 1 ? 8 : 16; }
+constexpr uint32_t kLeast16 = 0x2800u;  // 2^-5 in fp16 (lift_rows)
 constexpr int kSmemMax = 200 * 1024;
 constexpr int kSmemPair = 104 * 1024;  // two CTAs to an SM
 
@@ -228,14 +231,17 @@ __device__ __forceinline__ uint32_t rest(uint32_t x, uint32_t g, uint32_t p) {
 // that leaves in rows of their own behind, p.halves) with the
 // RMS row scale in rscale. Vector v of a row (8 k) goes to the place where the
 // quad reads it: group v / 4V, word v % V of lane v / V % 4. R: a bound on M.
+// Returns (fp16) whether a warp saw products outside the type's range: lift_rows then looks at every row.
 template <int DT, bool NORM, int R, int V, typename Pre>
-__device__ void build_rows(const W4Params& p, const uint16_t* x, int M, uint4* xs, float* rscale, Pre pre) {
+__device__ bool build_rows(const W4Params& p, const uint16_t* x, int M, uint4* xs, float* rscale, Pre pre) {
     using Ops = DTypeOps<DT>;
     const int vecs = p.K / 8, ld = row_vecs(p.K);
+    constexpr bool kRange = NORM && DT == DT_F16;
     __shared__ float part[kWarps][R];
     float sq[R];
+    [[maybe_unused]] uint32_t big[R];  // the row's largest |x * gamma|, in pairs
 #pragma unroll
-    for (int m = 0; m < R; ++m) sq[m] = 0.f;
+    for (int m = 0; m < R; ++m) sq[m] = 0.f, big[m] = 0u;
     bool first = true;
     constexpr int C = R <= 4 ? 2 : 1;  // vectors of a row in flight per thread
     for (int c0 = threadIdx.x; c0 < vecs || first; c0 += C * kThreads) {
@@ -270,6 +276,7 @@ __device__ void build_rows(const W4Params& p, const uint16_t* x, int M, uint4* x
                     }
                     const uint4 g = gv[j], x1 = o;
                     o = make_uint4(Ops::mul2(o.x, g.x), Ops::mul2(o.y, g.y), Ops::mul2(o.z, g.z), Ops::mul2(o.w, g.w));
+                    if constexpr (kRange) big[m] = absmax2<DT>(big[m], absmax8<DT>(o));
                     if (R <= 4 && p.halves)
                         xs[(M + m) * ld + to] = pair_up(make_uint4(rest<DT>(x1.x, g.x, o.x), rest<DT>(x1.y, g.y, o.y),
                                                                    rest<DT>(x1.z, g.z, o.z), rest<DT>(x1.w, g.w, o.w)));
@@ -278,15 +285,30 @@ __device__ void build_rows(const W4Params& p, const uint16_t* x, int M, uint4* x
             }
         }
     }
+    int again = 0;
     if (NORM) {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        if constexpr (kRange) {
+            // of each row: whether a product is 2^-5 or more, and whether x is not all zeros; whether a product is infinite
+            uint32_t s = 0u, top = 0u;
+#pragma unroll
+            for (int m = 0; m < R; ++m) {
+                const uint32_t b = absmax_halves<DT>(big[m]);
+                s |= (b >= kLeast16 ? 1u << m : 0u) | (sq[m] > 0.f ? 0x100u << m : 0u);
+                top = max(top, b);
+            }
+            if (top >= Bits16<DT>::kInf) s |= 0x10000u;
+            s = __reduce_or_sync(0xffffffffu, s);
+            again = ((s >> 8) & ~s & 0xffu) != 0u || s >= 0x10000u;
+        }
 #pragma unroll
         for (int m = 0; m < R; ++m) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sq[m] += __shfl_xor_sync(0xffffffffu, sq[m], o);
             if (lane == 0) part[warp][m] = sq[m];
         }
-        __syncthreads();
+        if constexpr (kRange) again = __syncthreads_or(again);
+        else __syncthreads();
         if (threadIdx.x < R) {
             float a = 0.f;
             for (int w = 0; w < kWarps; ++w) a += part[w][threadIdx.x];
@@ -294,6 +316,64 @@ __device__ void build_rows(const W4Params& p, const uint16_t* x, int M, uint4* x
         }
     }
     __syncthreads();
+    return again != 0;
+}
+
+// fp16 rows whose products x * gamma leave the type's range: above 65504, or all
+// below 2^-5, where its smallest values would cost them bits (2^-25 of error next to
+// a largest product of 2^-5 is 2^-20 of it, far below a rounding's 2^-12). The
+// norm makes the answer the same size whatever the row's, so they are formed
+// again times the power of two that puts the largest one into 2^13 .. 2^14, and
+// rscale takes its inverse: exact, and other rows keep their bits. Seldom needed, so
+// x is read again and nothing here is unrolled. Finding such rows costs every fp16
+// call 0.04 to 0.2 us (1 x 4096 x 4096 4.77 -> 4.83, 4 rows 5.79 -> 6.00, 8 rows 6.23 -> 6.26).
+template <int DT, int V>
+__device__ void lift_rows(const W4Params& p, const uint16_t* x, int M, uint4* xs, float* rscale) {
+    using Ops = DTypeOps<DT>;
+    const int vecs = p.K / 8, ld = row_vecs(p.K);
+    __shared__ float most[kWarps];
+#pragma unroll 1
+    for (int m = 0; m < M; ++m) {
+        const uint16_t* row = x + (size_t)m * p.K;
+        float a = 0.f;
+#pragma unroll 1
+        for (int i = threadIdx.x; i < vecs * 4; i += kThreads) {
+            const float2 f = Ops::unpack(__ldg(reinterpret_cast<const uint32_t*>(row) + i));
+            const float2 g = Ops::unpack(__ldg(reinterpret_cast<const uint32_t*>(p.gamma) + i));
+            a = fmaxf(a, fmaxf(fabsf(f.x * g.x), fabsf(f.y * g.y)));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = a;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) a = fmaxf(a, most[w]);
+        // (a product of two fp16 values is 0, or 2^-48 to 2^32, or not finite: then the row is as it is.
+        // From 65520 on it would round to infinity.)
+        const int e = (int)(__float_as_uint(a) >> 23) - 127;
+        if (a > 0.f && e < 128 && (a < 0x1p-5f || a >= 65520.f)) {
+            const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
+#pragma unroll 1
+            for (int c = threadIdx.x; c < vecs; c += kThreads) {
+                const uint4 v = ldg_v4(row + (size_t)c * 8), g = ldg_v4(p.gamma + (size_t)c * 8);
+                const uint32_t vw[4] = {v.x, v.y, v.z, v.w}, gw[4] = {g.x, g.y, g.z, g.w};
+                uint32_t o[4], r[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = Ops::unpack(vw[j]), h = Ops::unpack(gw[j]);
+                    const float2 t = make_float2(f.x * h.x * up, f.y * h.y * up);
+                    o[j] = Ops::pack(t.x, t.y);
+                    const float2 q = Ops::unpack(o[j]);
+                    r[j] = Ops::pack(t.x - q.x, t.y - q.y);
+                }
+                const int to = c / (4 * V) * (4 * V) + c % V * 4 + c / V % 4;
+                xs[m * ld + to] = pair_up(make_uint4(o[0], o[1], o[2], o[3]));
+                if (p.halves) xs[(M + m) * ld + to] = pair_up(make_uint4(r[0], r[1], r[2], r[3]));
+            }
+            if (threadIdx.x == 0) rscale[m] *= __uint_as_float((uint32_t)(127 - 13 + e) << 23);
+        }
+        __syncthreads();  // (`most` is the next row's, and the rows are read next)
+    }
 }
 
 template <int DT, bool DUAL, int V, bool Z>
@@ -329,9 +409,11 @@ __global__ void __launch_bounds__(kThreads, 2) fl_w4_rows_kernel(const __grid_co
     Block<V> A, B;
     auto pre = [&] { load_block<V, Z>(A, rows, s0, s1, t); };
     if (p.gamma != nullptr) {
-        if (M <= 2) build_rows<DT, true, 2, V>(p, x, M, xs, rscale, pre);
-        else if (M <= 4) build_rows<DT, true, 4, V>(p, x, M, xs, rscale, pre);
-        else build_rows<DT, true, 8, V>(p, x, M, xs, rscale, pre);
+        bool again;
+        if (M <= 2) again = build_rows<DT, true, 2, V>(p, x, M, xs, rscale, pre);
+        else if (M <= 4) again = build_rows<DT, true, 4, V>(p, x, M, xs, rscale, pre);
+        else again = build_rows<DT, true, 8, V>(p, x, M, xs, rscale, pre);
+        if (DT == DT_F16 && again) lift_rows<DT, V>(p, x, M, xs, rscale);  // (the same for every thread)
     } else {
         if (threadIdx.x < 8) rscale[threadIdx.x] = 1.f;
         if (M <= 4) build_rows<DT, false, 4, V>(p, x, M, xs, rscale, pre);

@@ -449,8 +449,10 @@ fl_status fl_w4_quantize(const void* W, void* q, void* scales, int N, int K, int
 /*
  * out[M,N] = act(norm(x)[M,K] W^T + bias) (+ residual) on a 4-bit weight.
  *   gamma: [K], the RMSNorm prologue of fl_norm_gemm; NULL: x as it is. With
- *   gamma one product is formed in the dtype, in fp16 within its range: x * gamma
- *   (few rows; up to four keep what its rounding cuts off) or 64 * w * gamma (many).
+ *   gamma one product is formed in the dtype: x * gamma (few rows, of any size: in
+ *   fp16 a row whose products would leave the type's range is carried times a power of
+ *   two; up to four rows keep what the rounding cuts off) or w * gamma (many rows; in
+ *   fp16 64 * w * gamma, which has to stay within the type's range).
  *   bias [N] and residual [M,N] may be NULL; residual may be the same pointer
  *   as out. Epilogue order as in fl_gemm_epilogue.
  * workspace: fl_w4_gemm_workspace_size(M, K, gamma != NULL) bytes (0 for some

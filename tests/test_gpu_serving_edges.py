@@ -1,0 +1,96 @@
+"""Edges of the serving operators on the GPU: ranges, long rows, small activations, what graphs keep (needs an sm_103a GPU).
+
+Bounds are those of tests/test_gpu_serving.py, u the largest relative error of one rounding to the dtype (2^-8 bf16,
+2^-11 fp16 with the type's smallest values next to it), each derived beside its test.
+"""
+import numpy as np
+import pytest
+import torch
+
+import gemm_epilogue_tma_gb300 as fl
+import oracle
+from test_gpu_serving import DT, U, cache, f64, gen, library, put, w4_ref, w4_tensors  # noqa: F401 (library: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------
+# range of x * gamma
+# ---------------------------------------------------------------------------
+def wide_rows(rng, M, K, size):
+    """Rows of about `size`, each with a few channels up to 40 times larger, within fp16."""
+    x = rng.standard_normal((M, K)) * np.where(rng.random((M, K)) < 0.01, 40.0, 1.0) * size
+    return put(np.clip(x, -65504.0, 65504.0), "f16")
+
+
+@pytest.mark.parametrize("size,eps", [(1e4, 1e-6), (6e4, 1e-6), (1e-4, 1e-12), (3e-6, 0.0), (1.0, 1e-6)])
+@pytest.mark.parametrize("M", [1, 2, 4, 8, 24, 300])
+def test_w4_gemm_takes_every_fp16_row(M, size, eps):
+    """The normalised row is of size 1 whatever x is, so the answer is finite and as exact for rows near fp16's largest
+    and smallest values as for rows of size 1, on few rows and on many. Element by element: x * gamma (or the weight
+    with gamma in it), the weight and the output rounded once (2.1 u of the terms, u of the sum), sums fp32 with
+    2^-22 per term at most; no term for values lost to the type's smallest."""
+    rng = gen(50, M, 64 + int(np.log2(size)))
+    K, N, group = 1024, 264, 64
+    x = wide_rows(rng, M, K, size)
+    if M > 1:
+        x[M // 2] = put(rng.standard_normal(K), "f16")           # sizes of rows do not mix
+    gamma = put(3 + rng.uniform(0, 60, K) * (rng.random(K) < 0.1), "f16")
+    w = w4_tensors(rng, N, K, group, True, "f16")
+    got = f64(fl.w4_gemm(x, w[0], w[1], zeros=w[2], gamma=gamma, eps=eps))
+    fl.device_status()
+    y, mag, _ = w4_ref(x, w, gamma, eps)
+    assert np.isfinite(got).all()
+    u = U["f16"]
+    bound = u * np.abs(y) + (2.1 * u + K * 2.0 ** -22) * mag + 2.0 ** -25
+    err = np.abs(got - y)
+    assert (err <= bound).all(), (err / bound).max()
+
+
+@pytest.mark.parametrize("M", [1, 4, 7, 20])
+def test_w4_swiglu_ffn_takes_large_fp16_rows(M):
+    """The block's gate and up products of rows whose x * gamma passes 65504: finite, and the residual's own size."""
+    rng = gen(51, M)
+    D, F = 512, 256
+    x = wide_rows(rng, M, D, 3e3)
+    gamma = put(np.full(D, 30.0), "f16")
+    Wg, Wu, Wd = (w4_tensors(rng, n, k, 64, False, "f16") for n, k in ((F, D), (F, D), (D, F)))
+    got = f64(fl.w4_swiglu_ffn(x, gamma, Wg[:2], Wu[:2], Wd[:2]))
+    fl.device_status()
+    g, gm, _ = w4_ref(x, Wg, gamma, 1e-6)
+    v, vm, _ = w4_ref(x, Wu, gamma, 1e-6)
+    h = oracle.silu(g) * v
+    assert np.abs(h).max() < 6e4                                  # h itself fits
+    W = oracle.w4_weight(Wd[0].cpu().numpy(), f64(Wd[1]))
+    y = h @ W.T + f64(x)
+    # the gate's and the up product's errors through silu (slope below 1.1), h's rounding, the down product's and the output's
+    u = U["f16"]
+    dg, dv = ((1.05 * u + D * 2.0 ** -22) * m for m in (gm, vm))
+    dh = (1.1 * dg + 2.0 ** -9 * np.abs(g)) * (np.abs(v) + dv) + np.abs(oracle.silu(g)) * dv + u * np.abs(h)
+    bound = u * np.abs(y) + dh @ np.abs(W).T + (1.05 * u + F * 2.0 ** -22) * (np.abs(h) @ np.abs(W).T)
+    # (fp16 ends at 65504, and 65520 and more round to infinity: the residual of one element is 65504 itself, and its exact
+    # answer -65645. So an infinity is right where the answer may lie past 65520 within its bound.)
+    with np.errstate(invalid="ignore"):
+        past = np.isinf(got) & (got * y > 0) & (np.abs(y) + bound >= 65520)
+    assert (past | (np.abs(got - y) <= bound)).all()
+
+
+def test_w4_gemm_row_without_a_finite_sum_stays_alone():
+    """An infinite or NaN element makes its own row so, zero rows stay zero, and rows beside them keep their bits."""
+    rng = gen(52)
+    K, N = 512, 136
+    w = w4_tensors(rng, N, K, 128, False, "f16")
+    gamma = put(1 + 0.1 * rng.standard_normal(K), "f16")
+    for M in (4, 8, 20):
+        x = put(rng.standard_normal((M, K)), "f16")
+        x[0] *= 3e4 / 8
+        want = fl.w4_gemm(x, *w[:2], gamma=gamma)
+        assert torch.isfinite(want).all()
+        x2 = x.clone()
+        x2[1, 5], x2[2, 9] = float("inf"), float("nan")
+        x2[3] = 0
+        got = fl.w4_gemm(x2, *w[:2], gamma=gamma)
+        fl.device_status()
+        assert not torch.isfinite(got[1]).any() and torch.isnan(got[2]).all() and (got[3] == 0).all()
+        keep = [m for m in range(M) if m not in (1, 2, 3)]
+        assert torch.equal(got[keep], want[keep])
