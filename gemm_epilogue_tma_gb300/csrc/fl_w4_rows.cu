@@ -464,11 +464,11 @@ __global__ void __launch_bounds__(kThreads, 2) fl_w4_rows_kernel(const __grid_co
             const int n = DUAL ? u * 8 + r : u * 16 + r;
             const size_t at = (size_t)(m0 + m) * p.N + n;
             if constexpr (DUAL) {
-                p.out[at] = (uint16_t)(Ops::pack(act_apply(ACT_SILU, y * rs) * (up * rs), 0.f) & 0xffffu);
+                p.out[at] = (uint16_t)(Ops::pack(w4_act(ACT_SILU, y * rs) * (up * rs), 0.f) & 0xffffu);
             } else if (n < p.N) {
                 y *= rs;
                 if (p.bias != nullptr) y += Ops::unpack(p.bias[n]).x;
-                y = act_apply(p.act, y);
+                y = w4_act(p.act, y);
                 if (p.residual != nullptr) y += Ops::unpack(p.residual[at]).x;
                 p.out[at] = (uint16_t)(Ops::pack(y, 0.f) & 0xffffu);
             }

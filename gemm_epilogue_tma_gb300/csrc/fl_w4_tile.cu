@@ -419,8 +419,8 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
                     // lanes 16 apart hold the gate and the up value of a row
                     const float o0 = __shfl_xor_sync(0xffffffffu, up ? a[0] : a[1], 16);
                     const float o1 = __shfl_xor_sync(0xffffffffu, up ? a[2] : a[3], 16);
-                    store(exchange(act_apply(ACT_SILU, up ? o0 : a[0]) * (up ? a[1] : o0),
-                                   act_apply(ACT_SILU, up ? o1 : a[2]) * (up ? a[3] : o1)),
+                    store(exchange(w4_act(ACT_SILU, up ? o0 : a[0]) * (up ? a[1] : o0),
+                                   w4_act(ACT_SILU, up ? o1 : a[2]) * (up ? a[3] : o1)),
                           e, at);
                 } else {
                     store(exchange(act(a[0] + bias), act(a[1] + bias)), e, at);
@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) fl_w4_tile_kernel(const __grid_co
         };
         // (the activation is chosen once, not per value)
         if (DUAL || w.act == ACT_NONE) all([](float y) { return y; });
-        else all([&](float y) { return act_apply(w.act, y); });
+        else all([&](float y) { return w4_act(w.act, y); });
     };
     // Epilogue of the i-th tile of this CTA. false: the MMAs did not finish.
     auto epilogue = [&](int tile, int i) {

@@ -94,3 +94,67 @@ def test_w4_gemm_row_without_a_finite_sum_stays_alone():
         assert not torch.isfinite(got[1]).any() and torch.isnan(got[2]).all() and (got[3] == 0).all()
         keep = [m for m in range(M) if m not in (1, 2, 3)]
         assert torch.equal(got[keep], want[keep])
+
+
+# ---------------------------------------------------------------------------
+# activations
+# ---------------------------------------------------------------------------
+def exact_act(name, v):
+    """v sigmoid(z), which cancels nowhere."""
+    z = v if name == "silu" else 2 * np.sqrt(2 / np.pi) * (v + 0.044715 * v ** 3)
+    return v / (1 + np.exp(-np.minimum(np.maximum(z, -700), 700)))
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("M", [1, 8, 40, 300])
+def test_w4_gemm_activation_of_negative_values(dt, act, M):
+    """Pre-activations that are exact (x times a code of 1, a bias; all of them multiples of 1/8), mostly -10 .. -2, where
+    the activation is small next to them: the output is its rounding alone. The kernel's sigmoid form is within 2^-16 of
+    the value (an exponential within 2^-18 for arguments down to -20, a sum, a quotient of 2^-22), or 0 where its
+    exponential passes 2^126: below 16 * 2^-126."""
+    rng = gen(53, M)
+    K, N = 128, 512
+    x = np.zeros((M, K))
+    x[:, 0] = np.round(rng.uniform(-2, 2, M) * 8) / 8
+    b = np.round(np.concatenate([rng.uniform(-8, -4, N - 64), rng.uniform(-14, 14, 62), [0, -0.5]]) * 8) / 8
+    code = np.full((N, K), 8)
+    code[:, 0] = 9
+    q, s = put(oracle.w4_pack(code)), put(np.ones((N, 1)), dt)
+    got = f64(fl.w4_gemm(put(x, dt), q, s, bias=put(b, dt), act=act))
+    fl.device_status()
+    y = exact_act(act, x[:, :1] + b)
+    least = 2.0 ** -25 if dt == "f16" else 2.0 ** -122
+    bound = (U[dt] + 2.0 ** -16) * np.abs(y) + least
+    err = np.abs(got - y)
+    assert (err <= bound).all(), (err / bound).max()
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("M", [2, 6, 40, 300])
+def test_w4_swiglu_ffn_activation_of_negative_gates(dt, M):
+    """Gates that are exact (rows of one size, whose norm is 1; one code a row), up 1, the down product an identity: the
+    output is x + silu(gate) with h's rounding and its own."""
+    D, F = 256, 256
+    gate = np.linspace(-12, -1, F)
+    x = np.full((M, D), 2.0 ** -10)
+    x[:, 1::2] *= -1
+    gamma = put(np.ones(D), dt)
+    code = np.full((F, D), 8)
+    code[:, 0] = 9                                                             # x[:, 0] / rms = 1
+    one = put(oracle.w4_pack(code))
+    sg = np.tile(gate[:, None], (1, D // 64))
+    Wg, Wu = (one, put(sg, dt)), (one, put(np.ones((F, D // 64)), dt))
+    code = np.full((D, F), 8)
+    np.fill_diagonal(code, 9)
+    Wd = put(oracle.w4_pack(code)), put(np.ones((D, F // 64)), dt)
+    got = f64(fl.w4_swiglu_ffn(put(x, dt), gamma, Wg, Wu, Wd, eps=0.0))
+    fl.device_status()
+    h = exact_act("silu", f64(Wg[1])[:, 0])[None]
+    y = h + x
+    # (the norm's factor and the sums: 2^-21 of the gate, which changes h by its slope (1 + |gate|) h / gate, and of up)
+    small = 2.0 ** -21 * (2 + np.abs(f64(Wg[1])[:, 0]))[None]
+    u, least = U[dt], 2.0 ** -25 if dt == "f16" else 0.0
+    bound = u * np.abs(y) + (u + 2.0 ** -16 + small) * np.abs(h) * (1 + u) + 2 * least
+    err = np.abs(got - y)
+    assert (err <= bound).all(), (err / bound).max()
