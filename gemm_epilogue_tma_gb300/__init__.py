@@ -174,6 +174,17 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+_captures = []  # of each Graph.capture at work: what the calls made for themselves, which every replay uses
+
+
+def _made(t):
+    """t (a tensor, several, or what holds them), which a call made for itself. A graph under capture keeps it: replays
+    write and read that memory, and torch's allocator, which does not know of the capture, would hand it to others."""
+    for kept in _captures:
+        kept.append(t)
+    return t
+
+
 def _dtype_code(t) -> int:
     import torch
     if t.dtype == torch.float16:
@@ -204,7 +215,7 @@ def gemm_epilogue(A, W, bias=None, residual=None, out=None, pattern="gemm_bias_g
     if W.shape[1] != K:
         raise ValueError(f"W has shape {tuple(W.shape)}, expected [N, {K}]")
     if out is None:
-        out = torch.empty((M, N), dtype=A.dtype, device=A.device)
+        out = _made(torch.empty((M, N), dtype=A.dtype, device=A.device))
     _check_tensors(A.dtype, A=A, W=W, bias=bias, residual=residual, out=out)
     _check(lib().fl_gemm_epilogue(_ptr(A), _ptr(W), _ptr(bias), _ptr(residual), _ptr(out), M, N, K, p,
                                   _dtype_code(A), _stream(stream)))
@@ -219,7 +230,7 @@ def norm_gemm(x, gamma, W, beta=None, bias=None, out=None, eps=1e-6, norm="rms",
     if W.shape[1] != K:
         raise ValueError(f"W has shape {tuple(W.shape)}, expected [N, {K}]")
     if out is None:
-        out = torch.empty((M, N), dtype=x.dtype, device=x.device)
+        out = _made(torch.empty((M, N), dtype=x.dtype, device=x.device))
     _check_tensors(x.dtype, x=x, gamma=gamma, W=W, beta=beta, bias=bias, out=out)
     _check(lib().fl_norm_gemm(_ptr(x), _ptr(gamma), _ptr(beta), _ptr(W), _ptr(bias), _ptr(out), M, N, K,
                               float(eps), NORMS[norm], ACTS[act], _dtype_code(x), _stream(stream)))
@@ -240,7 +251,7 @@ def norm_gemm_multi(x, gamma, Ws, beta=None, biases=None, outs=None, acts=None, 
         if W.shape[1] != K:
             raise ValueError(f"Ws[{i}] has shape {tuple(W.shape)}, expected [N, {K}]")
     if outs is None:
-        outs = [torch.empty((M, W.shape[0]), dtype=x.dtype, device=x.device) for W in Ws]
+        outs = _made([torch.empty((M, W.shape[0]), dtype=x.dtype, device=x.device) for W in Ws])
     biases = list(biases) if biases is not None else [None] * n
     acts = list(acts) if acts is not None else ["none"] * n
     if len(outs) != n or len(biases) != n or len(acts) != n:
@@ -267,7 +278,7 @@ def input_bias_gemm(A, bias_in, W, bias=None, residual=None, out=None, act="none
     if W.shape[1] != K:
         raise ValueError(f"W has shape {tuple(W.shape)}, expected [N, {K}]")
     if out is None:
-        out = torch.empty((M, N), dtype=A.dtype, device=A.device)
+        out = _made(torch.empty((M, N), dtype=A.dtype, device=A.device))
     _check_tensors(A.dtype, A=A, bias_in=bias_in, W=W, bias=bias, residual=residual, out=out)
     _check(lib().fl_input_bias_gemm(_ptr(A), _ptr(bias_in), _ptr(W), _ptr(bias), _ptr(residual), _ptr(out), M, N,
                                     K, ACTS[act], _dtype_code(A), _stream(stream)))
@@ -279,7 +290,7 @@ def rms_norm(x, gamma, out=None, eps=1e-6, stream=None):
     import torch
     M, K = x.shape
     if out is None:
-        out = torch.empty_like(x)
+        out = _made(torch.empty_like(x))
     _check_tensors(x.dtype, x=x, gamma=gamma, out=out)
     _check(lib().fl_rms_norm(_ptr(x), _ptr(gamma), _ptr(out), M, K, float(eps), _dtype_code(x), _stream(stream)))
     return out
@@ -385,8 +396,6 @@ class DecoderLayer:
             pass
 
 
-_captures = []  # of each Graph.capture at work: the workspaces that calls made for themselves, which replays use
-
 
 class Graph:
     """A CUDA graph of library calls (fl_capture_begin / fl_capture_end / fl_graph_launch)."""
@@ -397,7 +406,8 @@ class Graph:
     @classmethod
     def capture(cls, fn, stream=None):
         """Run fn() (which issues library calls on `stream`) under capture; returns the graph.
-        The stream must not be the legacy default stream (CUDA cannot capture it)."""
+        The stream must not be the legacy default stream (CUDA cannot capture it). The graph keeps what the calls make for
+        themselves (outputs and workspaces not given) until it is closed; tensors that fn is given or makes by other means are the caller's to keep."""
         s = _stream(stream)
         _check(lib().fl_capture_begin(s))
         kept = []
@@ -441,10 +451,10 @@ def swiglu_ffn(x, gamma, Wg, Wu, Wd, bias_down=None, out=None, eps=1e-6, workspa
     M, D = x.shape
     F = Wg.shape[0]
     if out is None:
-        out = torch.empty_like(x)
+        out = _made(torch.empty_like(x))
     need = swiglu_ffn_workspace_size(M, F, x.dtype)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _made(torch.empty(need, dtype=torch.uint8, device=x.device))
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     _check_tensors(x.dtype, x=x, gamma=gamma, Wg=Wg, Wu=Wu, Wd=Wd, bias_down=bias_down, out=out)
@@ -462,7 +472,7 @@ def swiglu_ffn_noalloc(x, gamma, Wg, Wu, Wd, bias_down=None, out=None, eps=1e-6,
     M, D = x.shape
     F = Wg.shape[0]
     if out is None:
-        out = torch.empty_like(x)
+        out = _made(torch.empty_like(x))
     _check_tensors(x.dtype, x=x, gamma=gamma, Wg=Wg, Wu=Wu, Wd=Wd, bias_down=bias_down, out=out)
     _check(lib().fl_swiglu_ffn_noalloc(_ptr(x), _ptr(gamma), _ptr(Wg), _ptr(Wu), _ptr(Wd), _ptr(bias_down),
                                        _ptr(out), M, D, F, float(eps), _dtype_code(x), _stream(stream)))
@@ -505,9 +515,8 @@ def _on(stream, name, args, makes=True):
 
 def _output(r):
     """The output of a call that returns it with the workspace it made, or None."""
-    if r[1] is not None:
-        for kept in _captures:
-            kept.append(r[1])
+    if _captures:
+        _made(r)
     return r[0]
 
 
@@ -515,8 +524,10 @@ def w4_quantize(W, group=128, q=None, scales=None, stream=None):
     """Symmetric round-to-nearest 4-bit quantisation of W [N, K]: returns (q, scales), codes [N, K / 2] uint8 (two
     along K to a byte, the even k in the low half, 8 standing for zero) and one scale of W's dtype per `group` k."""
     if stream is None:
-        return (_ops or ops()).w4_quantize(W, group, q, scales, None)
-    return _on(stream, "w4_quantize", (W, group, q, scales), q is None or scales is None)
+        r = (_ops or ops()).w4_quantize(W, group, q, scales, None)
+    else:
+        r = _on(stream, "w4_quantize", (W, group, q, scales), q is None or scales is None)
+    return _made(r) if _captures else r
 
 
 def w4_gemm_workspace_size(M: int, K: int, norm: bool) -> int:
@@ -558,9 +569,11 @@ def rope(q, k, positions, inv_freq, sections=None, interleaved=False, inverse=Fa
     the input. q, k and the outputs may be strided views with contiguous channels (column ranges of a stacked
     projection's output); an output may be its input itself."""
     if stream is None:
-        return (_ops or ops()).rope(q, k, positions, inv_freq, sections, interleaved, inverse, out_q, out_k, None)
-    return _on(stream, "rope", (q, k, positions, inv_freq, sections, interleaved, inverse, out_q, out_k),
-               out_q is None or (out_k is None and k is not None))
+        r = (_ops or ops()).rope(q, k, positions, inv_freq, sections, interleaved, inverse, out_q, out_k, None)
+    else:
+        r = _on(stream, "rope", (q, k, positions, inv_freq, sections, interleaved, inverse, out_q, out_k),
+                out_q is None or (out_k is None and k is not None))
+    return _made(r) if _captures else r
 
 
 def kv_write(k, v, k_cache, v_cache, k_scale, v_scale, page_table, start, cu_rows=None, stream=None):

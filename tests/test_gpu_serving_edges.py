@@ -158,3 +158,52 @@ def test_w4_swiglu_ffn_activation_of_negative_gates(dt, M):
     bound = u * np.abs(y) + (u + 2.0 ** -16 + small) * np.abs(h) * (1 + u) + 2 * least
     err = np.abs(got - y)
     assert (err <= bound).all(), (err / bound).max()
+
+
+# ---------------------------------------------------------------------------
+# graphs
+# ---------------------------------------------------------------------------
+def test_library_graph_keeps_what_its_calls_made():
+    """A captured chain whose calls make their own outputs and workspaces, dropped as soon as the next call has seen
+    them: tensors allocated after the capture, on either stream, are not written by replays, and each replay gives the
+    direct calls' bits."""
+    rng = gen(54)
+    M, D, F = 40, 512, 768
+    x = put(rng.standard_normal((M, D)), "bf16")
+    gamma = put(1 + 0.1 * rng.standard_normal(D), "bf16")
+    W16 = [put(rng.standard_normal(s) / np.sqrt(s[1]), "bf16") for s in ((F, D), (F, D), (D, F), (D, D))]
+    Q = [fl.w4_quantize(w, 64) for w in W16]
+    pos, f = put(np.arange(M, dtype=np.int32)), put((1e4 ** (-np.arange(32) / 32)).astype(np.float32))
+    y = torch.zeros_like(x)
+
+    def chain():
+        h = fl.swiglu_ffn(fl.norm_gemm(x, gamma, W16[3]), gamma, *W16[:3])
+        h = fl.w4_swiglu_ffn(fl.w4_gemm(h, *Q[3], gamma=gamma), gamma, *Q[:3])
+        q, _ = fl.rope(h.unflatten(1, (8, 64)), None, pos, f)
+        fl.w4_gemm(fl.rms_norm(q.flatten(1), gamma), *fl.w4_quantize(W16[3], 32), out=y)
+    chain()
+    torch.cuda.synchronize()
+    want = y.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        chain()                                     # (this stream's blocks exist before the capture)
+        side.synchronize()
+        graph = fl.Graph.capture(chain)
+
+    def guards():
+        return [torch.full((n,), 0xff, dtype=torch.uint8, device="cuda") for n in (64, 4096, 40960, M * D * 2, M * F * 2, D * D)
+                for _ in range(4)]
+    other = guards()
+    with torch.cuda.stream(side):
+        other += guards()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        y.zero_()
+        torch.cuda.synchronize()
+        graph.launch()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and all((t == 0xff).all() for t in other)
+    graph.close()
+    fl.device_status()
+    fl.device_status(side)

@@ -367,3 +367,89 @@ def test_codes_next_to_a_border():
                     r = r if takes_up else q
                 assert int(r) == nearest_even(Fraction(float(x)) / Fraction(float(s)))
     assert exact > 20
+
+
+# ---------------------------------------------------------------------------
+# what a graph keeps
+# ---------------------------------------------------------------------------
+class FakeLibrary:
+    """Every call succeeds; a capture ends with a graph handle."""
+    calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append(name)
+            if name == "fl_capture_end":
+                args[1]._obj.value = 1
+            return 64 if name.endswith("workspace_size") else 0
+        return call
+
+
+class FakeOperators:
+    """Stands in for the extension module: makes what is not given, and a workspace."""
+
+    @staticmethod
+    def _new():
+        return torch.zeros(8)
+
+    def w4_quantize(self, W, group, q, scales, stream):
+        return q if q is not None else self._new(), scales if scales is not None else self._new()
+
+    def w4_gemm(self, *a):
+        return a[7] if a[7] is not None else self._new(), None if a[10] is not None else self._new()
+
+    def w4_swiglu_ffn(self, *a):
+        return a[6] if a[6] is not None else self._new(), None if a[8] is not None else self._new()
+
+    def rope(self, q, k, pos, f, sections, inter, inverse, oq, ok, stream):
+        return oq if oq is not None else self._new(), ok if ok is not None else self._new()
+
+
+def test_graph_keeps_all_that_its_calls_made(monkeypatch):
+    """Outputs and workspaces that calls under Graph.capture make for themselves live as long as the graph, the 16-bit
+    functions' too, also those that only the next call saw. They are let go when the graph is closed, and calls outside a capture leave nothing behind."""
+    import gc
+    import weakref
+    fake = FakeLibrary()
+    monkeypatch.setattr(fl, "lib", lambda: fake)
+    monkeypatch.setattr(fl, "_ops", FakeOperators())
+    monkeypatch.setattr(fl, "_check_tensors", lambda *a, **k: None)
+    monkeypatch.setattr(fl, "_stream", lambda s: 1)
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True, raising=False)
+    made = []
+
+    def watched(f):
+        def call(*a, **k):
+            t = f(*a, **k)
+            made.append(weakref.ref(t))
+            return t
+        return call
+    x, W = torch.zeros((4, 8), dtype=torch.float16), torch.zeros((8, 8), dtype=torch.float16)
+    monkeypatch.setattr(torch, "empty", watched(torch.empty))
+    monkeypatch.setattr(torch, "empty_like", watched(torch.empty_like))
+    monkeypatch.setattr(FakeOperators, "_new", staticmethod(watched(FakeOperators._new)))
+
+    def calls():
+        fl.w4_gemm(fl.w4_gemm(x, None, None), None, None, out=x)
+        fl.w4_swiglu_ffn(x, None, None, None, None)
+        fl.w4_quantize(W)
+        fl.rope(x, x, None, None)
+        fl.gemm_epilogue(x, W)
+        fl.norm_gemm(x, None, W)
+        fl.norm_gemm_multi(x, None, [W, W])
+        fl.input_bias_gemm(x, None, W)
+        fl.rms_norm(x, None)
+        fl.swiglu_ffn(x, None, W, W, W)
+        fl.swiglu_ffn_noalloc(x, None, W, W, W)
+    calls()
+    count = len(made)
+    gc.collect()
+    assert count == 18 and not any(r() is not None for r in made)
+    del made[:]
+    graph = fl.Graph.capture(calls)
+    gc.collect()
+    assert len(made) == count and all(r() is not None for r in made)
+    graph.close()
+    gc.collect()
+    assert not any(r() is not None for r in made)
+    assert fl._captures == []
