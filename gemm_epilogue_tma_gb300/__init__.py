@@ -320,6 +320,7 @@ class DecoderLayer:
         h = ctypes.c_void_p()
         _check(lib().fl_layer_create(ctypes.byref(desc), ctypes.byref(h)))
         self._h = h
+        self.attached = ()
 
     def attach_cache(self, head_dim, positions=None, inv_freq=None, sections=None, interleaved=False, k_cache=None,
                      v_cache=None, k_scale=None, v_scale=None, page_table=None, start=None, cu_rows=None) -> None:
@@ -381,7 +382,8 @@ class DecoderLayer:
         self.attached = tuple(kept)  # kept alive as long as the layer uses them
 
     def issue(self, half: int, stream=None) -> None:
-        """Issue half 0 or 1 on the stream (capturable)."""
+        """Issue half 0 or 1 on the stream (capturable; the graph keeps the layer and what is attached to it now)."""
+        _made((self, self.attached))
         _check(lib().fl_layer_issue(self._h, int(half), _stream(stream)))
 
     def close(self) -> None:
@@ -407,7 +409,8 @@ class Graph:
     def capture(cls, fn, stream=None):
         """Run fn() (which issues library calls on `stream`) under capture; returns the graph.
         The stream must not be the legacy default stream (CUDA cannot capture it). The graph keeps what the calls make for
-        themselves (outputs and workspaces not given) until it is closed; tensors that fn is given or makes by other means are the caller's to keep."""
+        themselves (outputs and workspaces not given) and the layers issued, with what is attached to them, until it is
+        closed; tensors that fn is given or makes by other means are the caller's to keep."""
         s = _stream(stream)
         _check(lib().fl_capture_begin(s))
         kept = []

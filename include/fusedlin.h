@@ -584,8 +584,9 @@ fl_status fl_kv_read(const fl_kv_desc* desc, void* stream);
  * rotation) and fl_kv_desc (k_cache NULL: no cache; cu_rows NULL: one row per
  * sequence). The device pointers stay fixed and are read at each issue; axis_of
  * is copied. The description is checked as the two calls check theirs, without a
- * launch; a second call replaces the first, desc NULL detaches. Not to be called while
- * another thread issues the layer.
+ * launch; a second call replaces the first, desc NULL detaches. A graph captured
+ * before goes on reading and writing the tensors of its time. Not to be called
+ * while another thread issues the layer.
  */
 typedef struct {
     int head_dim;

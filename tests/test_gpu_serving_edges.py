@@ -207,3 +207,38 @@ def test_library_graph_keeps_what_its_calls_made():
     graph.close()
     fl.device_status()
     fl.device_status(side)
+
+
+def test_graph_of_a_layer_whose_attachment_was_replaced():
+    """A graph goes on with the positions that were attached when it was captured, although nobody else holds them."""
+    rng = gen(55)
+    M, D, Dkv, F, hd = 3, 256, 128, 256, 64
+    e = lambda *s: torch.zeros(s, dtype=torch.float16, device="cuda")  # noqa: E731
+    T = {n: put(rng.standard_normal(s) / np.sqrt(s[-1]), "f16") for n, s in
+         (("Wq", (D, D)), ("Wk", (Dkv, D)), ("Wv", (Dkv, D)), ("Wo", (D, D)), ("Wg", (F, D)), ("Wu", (F, D)), ("Wd", (D, F)))}
+    one = put(np.ones(D), "f16")
+    T.update(x=put(rng.standard_normal((M, D)), "f16"), gamma_attn=one, gamma_ffn=one, q=e(M, D), k=e(M, Dkv), v=e(M, Dkv),
+             attn=e(M, D), h=e(M, D), out=e(M, D))
+    layer = fl.DecoderLayer(**T)
+    f = put((1e4 ** (-np.arange(32) / 32)).astype(np.float32))
+
+    def i32(*v):
+        return put(np.array(v, dtype=np.int32))
+    layer.attach_cache(hd, positions=i32(5, 900, 70), inv_freq=f)
+    layer.issue(0)
+    torch.cuda.synchronize()
+    want = T["q"].clone()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        graph = fl.Graph.capture(lambda: layer.issue(0))
+    layer.attach_cache(hd, positions=i32(1, 2, 3), inv_freq=f)
+    guards = [torch.full((3,), 7, dtype=torch.int32, device="cuda") for _ in range(64)]
+    layer.issue(0)
+    torch.cuda.synchronize()
+    assert not torch.equal(T["q"], want)
+    graph.launch()
+    torch.cuda.synchronize()
+    assert torch.equal(T["q"], want) and all((g == 7).all() for g in guards)
+    graph.close()
+    layer.close()
+    fl.device_status()

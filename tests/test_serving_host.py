@@ -407,7 +407,8 @@ class FakeOperators:
 
 def test_graph_keeps_all_that_its_calls_made(monkeypatch):
     """Outputs and workspaces that calls under Graph.capture make for themselves live as long as the graph, the 16-bit
-    functions' too, also those that only the next call saw. They are let go when the graph is closed, and calls outside a capture leave nothing behind."""
+    functions' too, also those that only the next call saw; so do a layer and what was attached to it when it was issued.
+    They are let go when the graph is closed, and calls outside a capture leave nothing behind."""
     import gc
     import weakref
     fake = FakeLibrary()
@@ -425,6 +426,11 @@ def test_graph_keeps_all_that_its_calls_made(monkeypatch):
             return t
         return call
     x, W = torch.zeros((4, 8), dtype=torch.float16), torch.zeros((8, 8), dtype=torch.float16)
+    layer = fl.DecoderLayer(x=x, Wg=W, Wk=W)
+    attached = torch.zeros(3)
+    layer.attached = (attached,)
+    owned = [weakref.ref(attached), weakref.ref(layer)]
+    del attached
     monkeypatch.setattr(torch, "empty", watched(torch.empty))
     monkeypatch.setattr(torch, "empty_like", watched(torch.empty_like))
     monkeypatch.setattr(FakeOperators, "_new", staticmethod(watched(FakeOperators._new)))
@@ -446,10 +452,12 @@ def test_graph_keeps_all_that_its_calls_made(monkeypatch):
     gc.collect()
     assert count == 18 and not any(r() is not None for r in made)
     del made[:]
-    graph = fl.Graph.capture(calls)
+    graph = fl.Graph.capture(lambda: (calls(), layer.issue(0)))
+    layer.attached = ()
+    del layer
     gc.collect()
-    assert len(made) == count and all(r() is not None for r in made)
+    assert len(made) == count and all(r() is not None for r in made + owned)
     graph.close()
     gc.collect()
-    assert not any(r() is not None for r in made)
+    assert not any(r() is not None for r in made + owned)
     assert fl._captures == []
