@@ -84,7 +84,7 @@ struct DeviceInfo {
     // the library's own, so the process's default pool keeps its settings
     cudaMemPool_t pool = nullptr;
 };
-constexpr int kMaxDevices = 64;  // (allow_smem keeps one bit for each)
+using fl::host::kMaxDevices;
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_dev_mu;
 

@@ -14,6 +14,8 @@
 namespace fl {
 namespace host {
 
+constexpr int kMaxDevices = 64;  // (allow_smem keeps one bit for each)
+
 // Records the message for fl_last_error() and returns the status.
 fl_status fail(fl_status s, const char* fmt, ...);
 fl_status ok();

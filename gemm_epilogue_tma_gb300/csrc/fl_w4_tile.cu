@@ -59,6 +59,7 @@
 
 #include "fl_common.cuh"
 #include "fl_host.h"
+#include "fl_resident.h"
 #include "fl_w4.h"
 
 namespace fl {
@@ -694,17 +695,16 @@ struct Kern {
         return cudaLaunchKernelEx(&cfg, fl_w4_tile_kernel<DT, DUAL, NORM, RES>, p);
     }
     // clusters of `splits` CTAs that are resident at once
-    static int resident(int splits, int device) {
-        if (configure(device) != cudaSuccess) return 0;
-        cudaLaunchConfig_t cfg;
-        cudaLaunchAttribute a[2];
-        config(cfg, a, dim3((unsigned)splits), splits, 0, nullptr);
-        int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, fl_w4_tile_kernel<DT, DUAL, NORM, RES>, &cfg) != cudaSuccess) {
-            cudaGetLastError();
-            return 0;
+    static cudaError_t resident(int splits, int device, int* n) {
+        cudaError_t e = configure(device);
+        if (e == cudaSuccess) {
+            cudaLaunchConfig_t cfg;
+            cudaLaunchAttribute a[2];
+            config(cfg, a, dim3((unsigned)splits), splits, 0, nullptr);
+            e = cudaOccupancyMaxActiveClusters(n, fl_w4_tile_kernel<DT, DUAL, NORM, RES>, &cfg);
         }
-        return n;
+        if (e != cudaSuccess) cudaGetLastError();  // (reported here: not the next launch's)
+        return e;
     }
 };
 
@@ -739,24 +739,24 @@ fl_status w4_tile(int dt, bool dual, const W4Params& w, void* workspace, const h
     // whole waves may be split in a launch of their own (the tail), which fills
     // the multiprocessors as they fall idle. Ranges of a split are multiples of
     // 128 k, the largest group.
-    static std::atomic<int> resident[9];
+    static Resident<host::kMaxDevices, 8> resident;
     double least = 0;
     const int tt0 = (w.M + kTok - 1) / kTok;
-    int token_tiles = 0, tail_splits = 1, per_round = 0;
+    int token_tiles = 0, tail_splits = 1;
     auto split_steps = [&](int s) { return ((p.steps + 1) / 2 + s - 1) / s * 2; };
     auto can_split = [&](int s) {
         const int per = split_steps(s);
         return per >= 4 && (p.steps + per - 1) / per == s;
     };
-    auto clusters = [&](int s) {  // resident at once (0: none)
-        int n = resident[s].load();
-        if (n == 0) {
-            n = Kern<DT_BF16, false, false, false>::resident(s, ctx.device);
-            if (n <= 0) n = -1;
-            resident[s] = n;
-        }
-        return n > 0 ? n : 0;
+    auto clusters = [&](int s, int* n) {  // resident at once
+        return (cudaError_t)resident.get(
+            ctx.device, s, [&](int* got) { return (int)Kern<DT_BF16, false, false, false>::resident(s, ctx.device, got); }, n);
     };
+    int n1 = 0;
+    const cudaError_t asked = clusters(1, &n1);
+    if (asked != cudaSuccess)
+        return host::fail(FL_ERR_CUDA, "4-bit tile kernel: occupancy query: %s", cudaGetErrorString(asked));
+    if (n1 == 0) return host::fail(FL_ERR_CUDA, "4-bit tile kernel: no resident CTA");
     for (int tt = tt0; tt <= 3 * tt0 && tt <= tt0 + 64; ++tt) {
         const int bt = ((w.M + tt - 1) / tt + 15) / 16 * 16;
         if (tt > tt0 && bt < 64) break;
@@ -765,8 +765,6 @@ fl_status w4_tile(int dt, bool dual, const W4Params& w, void* workspace, const h
         const long long tiles = (long long)row_tiles * count;
         const double least_step = norm ? 690.0 : 570.0, step = 2.2 * bt > least_step ? 2.2 * bt : least_step;
         const double round = step * p.steps + 6000.0;
-        const int n1 = clusters(1);
-        if (n1 == 0) break;
         auto consider = [&](double cost, int splits, int tail) {
             if (token_tiles != 0 && cost >= least) return;
             least = cost;
@@ -777,20 +775,19 @@ fl_status w4_tile(int dt, bool dual, const W4Params& w, void* workspace, const h
         };
         consider(5000.0 + (double)((tiles + n1 - 1) / n1) * round, 1, 1);
         for (int s = 2; s <= 8; ++s) {
-            const int n = can_split(s) ? clusters(s) : 0;
-            if (n == 0) continue;
+            // (a size whose query fails is left out of this choice)
+            int n = 0;
+            if (!can_split(s) || clusters(s, &n) != cudaSuccess || n == 0) continue;
             const double one = step * split_steps(s) + 11000.0 + 12.0 * bt;
             consider((double)((tiles + n - 1) / n) * one, s, 1);
             if (tiles > n1 && tiles % n1 != 0)
                 consider(5000.0 + (double)(tiles / n1) * round + 3000.0 + (double)((tiles % n1 + n - 1) / n) * one, 1, s);
         }
-        per_round = n1;
     }
-    if (token_tiles == 0) return host::fail(FL_ERR_CUDA, "4-bit tile kernel: no resident CTA");
     const long long tiles = (long long)row_tiles * token_tiles;
     if (tiles * p.splits > 0x7fffffffll) return host::fail(FL_ERR_UNSUPPORTED, "4-bit tile kernel: too many tiles");
     p.row_tiles = row_tiles;
-    const int all = (int)tiles, plain = tail_splits > 1 ? all / per_round * per_round : all;
+    const int all = (int)tiles, plain = tail_splits > 1 ? all / n1 * n1 : all;
     // rings: as many stages of tokens as leave the codes two stages, eight at most; the rest to the codes
     p.b_bytes = p.bt * kStep * 2;
     p.stages = (kRing - 2 * kWBytes) / p.b_bytes;
@@ -812,7 +809,7 @@ fl_status w4_tile(int dt, bool dual, const W4Params& w, void* workspace, const h
         p.splits = splits, p.steps_per_split = split_steps(splits);
         const int n = t1 - t0;
         const bool res = w.residual != nullptr;
-        const dim3 grid((unsigned)(splits > 1 ? n * splits : n < per_round ? n : per_round));
+        const dim3 grid((unsigned)(splits > 1 ? n * splits : n < n1 ? n : n1));
         cudaError_t e;
 #define FL_LAUNCH(DT)                                                                                \
     e = dual ? Kern<DT, true, true, false>::launch(p, grid, ctx, stream)                             \

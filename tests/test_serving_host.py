@@ -461,3 +461,43 @@ def test_graph_keeps_all_that_its_calls_made(monkeypatch):
     gc.collect()
     assert not any(r() is not None for r in made + owned)
     assert fl._captures == []
+
+
+# ---------------------------------------------------------------------------
+# host code compiled by itself
+# ---------------------------------------------------------------------------
+RESIDENT = r"""
+#include "fl_resident.h"
+#include <cstdio>
+#define CHECK(X) if (!(X)) { std::printf("line %d: %s\n", __LINE__, #X); return 1; }
+int main() {
+    static fl::Resident<4, 8> r;
+    int asked = 0, n = -1;
+    auto says = [&](int value, int error) { return [&asked, value, error](int* out) { ++asked; *out = value; return error; }; };
+    // one device's answer is not another's
+    CHECK(r.get(0, 1, says(152, 0), &n) == 0 && n == 152 && asked == 1);
+    CHECK(r.get(1, 1, says(132, 0), &n) == 0 && n == 132 && asked == 2);
+    CHECK(r.get(0, 1, says(7, 0), &n) == 0 && n == 152 && asked == 2);
+    CHECK(r.get(1, 1, says(7, 0), &n) == 0 && n == 132 && asked == 2);
+    CHECK(r.get(3, 8, says(17, 0), &n) == 0 && n == 17 && asked == 3);
+    // a failed query is handed on, and asked again
+    CHECK(r.get(2, 4, says(9, 46), &n) == 46 && n == 0 && asked == 4);
+    CHECK(r.get(2, 4, says(9, 2), &n) == 2 && n == 0 && asked == 5);
+    CHECK(r.get(2, 4, says(30, 0), &n) == 0 && n == 30 && asked == 6);
+    CHECK(r.get(2, 4, says(1, 2), &n) == 0 && n == 30 && asked == 6);
+    // none resident is an answer
+    CHECK(r.get(0, 8, says(0, 0), &n) == 0 && n == 0 && asked == 7);
+    CHECK(r.get(0, 8, says(5, 0), &n) == 0 && n == 0 && asked == 7);
+    return 0;
+}
+"""
+
+
+def test_resident_counts_are_kept_by_device_and_only_when_known(tmp_path):
+    import subprocess
+    src = tmp_path / "resident.cpp"
+    src.write_text(RESIDENT)
+    exe = str(tmp_path / "resident")
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-I", _build.CSRC, str(src), "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
