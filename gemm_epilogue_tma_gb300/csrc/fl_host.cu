@@ -22,14 +22,14 @@
 using fl::GemmParams;
 using fl::GemmParamsMulti;
 
-// Device status words: a kernel records a bounded-wait expiry in the word of
-// the stream it was launched (or captured) on.
-__device__ int g_fl_status[fl::kStatusSlots];
-// Range words, one per stream like the status words: a kernel that reads
-// indexes from device memory (page tables, row offsets) skips an entry outside
-// its table and records it here. They are words of their own because a kernel
-// that finds its status word set gives up its slow waits.
-__device__ int g_fl_range[fl::kStatusSlots];
+// Words of each stream, read by fl_device_status in one copy.
+// [0] status: a kernel records a bounded-wait expiry in the word of the stream
+// it was launched (or captured) on.
+// [1] range: a kernel that reads indexes from device memory (page tables, row
+// offsets) skips an entry outside its table and records it here. They are words
+// of their own because a kernel that finds its status word set gives up its slow
+// waits.
+__device__ int g_fl_words[2][fl::kStatusSlots];
 
 namespace {
 
@@ -73,8 +73,8 @@ struct DeviceInfo {
     std::atomic<bool> ready{false};
     int sms = 0;
     int major = 0, minor = 0;
-    int* status = nullptr;  // device address of g_fl_status[0]
-    int* range = nullptr;   // device address of g_fl_range[0]
+    int* status = nullptr;  // device address of g_fl_words[0]
+    int* range = nullptr;   // and of g_fl_words[1]
     // stream handle of each status word (word 0: the legacy default stream
     // and overflow), filled in first-use order under slot_mu
     std::mutex slot_mu;
@@ -103,10 +103,9 @@ fl_status device_info(DeviceInfo** out) {
             d.sms = prop.multiProcessorCount;
             d.major = prop.major;
             d.minor = prop.minor;
-            e = cudaGetSymbolAddress(reinterpret_cast<void**>(&d.status), g_fl_status);
+            e = cudaGetSymbolAddress(reinterpret_cast<void**>(&d.status), g_fl_words);
             if (e != cudaSuccess) return fail(FL_ERR_CUDA, "cudaGetSymbolAddress: %s", cudaGetErrorString(e));
-            e = cudaGetSymbolAddress(reinterpret_cast<void**>(&d.range), g_fl_range);
-            if (e != cudaSuccess) return fail(FL_ERR_CUDA, "cudaGetSymbolAddress: %s", cudaGetErrorString(e));
+            d.range = d.status + fl::kStatusSlots;
             cudaMemPoolProps props = {};
             props.allocType = cudaMemAllocationTypePinned;
             props.location.type = cudaMemLocationTypeDevice;
@@ -1230,21 +1229,17 @@ fl_status fl_device_status(void* stream) {
     if (st != FL_OK) return st;
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(FL_ERR_CUDA, "stream synchronize: %s", cudaGetErrorString(e));
-    const size_t off = (size_t)status_slot(di, static_cast<cudaStream_t>(stream)) * sizeof(int);
-    int v = 0;
-    e = cudaMemcpyFromSymbol(&v, g_fl_status, sizeof(int), off);
+    const int slot = status_slot(di, static_cast<cudaStream_t>(stream));
+    int words[2][fl::kStatusSlots];
+    e = cudaMemcpyFromSymbol(words, g_fl_words, sizeof(words));
     if (e != cudaSuccess) return fail(FL_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
+    const int v = words[0][slot], row = words[1][slot];
+    if (v == 0 && row == 0) return ok();
     const int zero = 0;
-    if (v == 0) {
-        e = cudaMemcpyFromSymbol(&v, g_fl_range, sizeof(int), off);
-        if (e != cudaSuccess) return fail(FL_ERR_CUDA, "range word read: %s", cudaGetErrorString(e));
-        if (v == 0) return ok();
-        e = cudaMemcpyToSymbol(g_fl_range, &zero, sizeof(int), off);
-        if (e != cudaSuccess) return fail(FL_ERR_CUDA, "range word clear: %s", cudaGetErrorString(e));
-        return fail(FL_ERR_RANGE, "a row of the paged cache has no page or lies outside its table (row %d)", v - 1);
-    }
-    e = cudaMemcpyToSymbol(g_fl_status, &zero, sizeof(int), off);
+    e = cudaMemcpyToSymbol(g_fl_words, &zero, sizeof(int), (size_t)((v != 0 ? 0 : fl::kStatusSlots) + slot) * sizeof(int));
     if (e != cudaSuccess) return fail(FL_ERR_CUDA, "status clear: %s", cudaGetErrorString(e));
+    if (v == 0)
+        return fail(FL_ERR_RANGE, "a row of the paged cache has no page or lies outside its table (row %d)", row - 1);
     return fail(FL_ERR_TIMEOUT, "a device-side wait ran past its limit (code %d, wait site %d)", v & 0xff, v >> 8);
 }
 

@@ -242,3 +242,35 @@ def test_graph_of_a_layer_whose_attachment_was_replaced():
     graph.close()
     layer.close()
     fl.device_status()
+
+
+# ---------------------------------------------------------------------------
+# device status
+# ---------------------------------------------------------------------------
+def skipped_row(stream):
+    """A row without a page, written on `stream`."""
+    (kc, vc), (ks, vs) = cache(1, 16, 1, 64, "int8")
+    k = torch.ones((3, 1, 64), dtype=torch.float16, device="cuda")
+    table = put(np.zeros((3, 1), dtype=np.int32))
+    start = put(np.array([0, 1, 99], dtype=np.int32))
+    torch.cuda.synchronize()
+    fl.kv_write(k, k, kc, vc, ks, vs, table, start, stream=stream)
+    return kc, vc, ks, vs, k, table, start
+
+
+def test_a_timeout_and_a_skipped_row_are_told_one_after_the_other():
+    """Each stream has both words: the timeout is told first and the row by the next call, with its number; another
+    stream's stay its own."""
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    kept = skipped_row(a), skipped_row(b)
+    fl.debug_wait_timeout(1000, stream=a)
+    told = []
+    for stream in (a, a, a, b, b):
+        try:
+            fl.device_status(stream)
+            told.append(0)
+        except fl.FusedLinError as e:
+            told.append(e.status)
+            assert e.status != 7 or "row 2" in str(e)
+    assert told == [6, 7, 0, 7, 0]
+    del kept
