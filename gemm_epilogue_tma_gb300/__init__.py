@@ -358,8 +358,10 @@ class DecoderLayer:
                 raise ValueError(f"sections must give the {pairs} pairs to the {axes} axes (1..4)")
             d.rotary_dim, d.n_axes, d.interleaved = 2 * pairs, axes, int(bool(interleaved))
             d.axis_of = b"".join(bytes((a,)) * n for a, n in enumerate(sections))
-            d.positions = use("positions", positions, torch.int32, (axes, M) if positions.dim() == 2 else (M,))
-            d.positions_stride = M
+            if M > 1 and positions.stride(-1) != 1:
+                raise ValueError("positions must be contiguous along the rows")
+            d.positions = use("positions", positions, torch.int32, (axes, M) if positions.dim() == 2 else (M,), contiguous=False)
+            d.positions_stride = positions.stride(0) if positions.dim() == 2 else M
             d.inv_freq = use("inv_freq", inv_freq, torch.float32, (pairs,))
         if k_cache is not None:
             formats = {torch.int8: 0, torch.float8_e4m3fn: 1}
@@ -568,7 +570,7 @@ def rope(q, k, positions, inv_freq, sections=None, interleaved=False, inverse=Fa
 
     The pairs (i, i + R/2) of the first R = 2 * len(inv_freq) channels, or (2i, 2i + 1) if interleaved, are turned
     by positions * inv_freq[i]; the other channels are copied. positions: int32 [rows], or [axes, rows] with
-    `sections` saying how many consecutive pairs follow each axis. inverse turns back: the gradient with respect to
+    `sections` saying how many consecutive pairs follow each axis (rows contiguous; one row expanded to the axes will do). inverse turns back: the gradient with respect to
     the input. q, k and the outputs may be strided views with contiguous channels (column ranges of a stacked
     projection's output); an output may be its input itself."""
     if stream is None:

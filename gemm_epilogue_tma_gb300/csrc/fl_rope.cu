@@ -226,8 +226,8 @@ fl_status rope(const fl_rope_desc* d, bool check_only, cudaStream_t s) {
         return fail(FL_ERR_INVALID_ARG, "fl_rope: a required pointer is null");
     if ((reinterpret_cast<uintptr_t>(d->positions) | reinterpret_cast<uintptr_t>(d->inv_freq)) & 3u)
         return fail(FL_ERR_ALIGNMENT, "fl_rope: positions and inv_freq must be 4-byte aligned");
-    if (d->n_axes > 1 && d->positions_stride < d->rows)
-        return fail(FL_ERR_INVALID_ARG, "fl_rope: positions_stride below rows");
+    if (d->n_axes > 1 && d->positions_stride != 0 && d->positions_stride < d->rows)
+        return fail(FL_ERR_INVALID_ARG, "fl_rope: positions_stride below rows (and not 0)");
     const View in[2] = {{d->q, d->q_row, d->q_head, d->heads_q}, {d->k, d->k_row, d->k_head, d->heads_k}};
     const View out[2] = {{d->q_out, d->q_out_row, d->q_out_head, d->heads_q},
                          {d->k_out, d->k_out_row, d->k_out_head, d->heads_k}};

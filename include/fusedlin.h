@@ -492,7 +492,7 @@ fl_status fl_w4_swiglu_ffn(const void* x, const void* gamma, const fl_w4_weight*
  *   q_out, k_out: where to, with strides of their own; may be the inputs
  *   themselves (same pointer and strides). No other overlap is allowed.
  *   positions: device, [n_axes][rows] int32, axis a at positions + a *
- *   positions_stride. inv_freq: device, [rotary_dim / 2] fp32, finite.
+ *   positions_stride (rows at least, or 0: every axis reads the same row). inv_freq: device, [rotary_dim / 2] fp32, finite.
  *   axis_of: HOST, rotary_dim / 2 bytes below n_axes, read during the call;
  *   NULL: axis 0 for all.
  * Pointers are 2-byte aligned (inv_freq and positions 4); rows whose base and

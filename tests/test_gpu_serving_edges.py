@@ -274,3 +274,34 @@ def test_a_timeout_and_a_skipped_row_are_told_one_after_the_other():
             assert e.status != 7 or "row 2" in str(e)
     assert told == [6, 7, 0, 7, 0]
     del kept
+
+
+# ---------------------------------------------------------------------------
+# positions
+# ---------------------------------------------------------------------------
+def test_rope_of_expanded_positions():
+    """Text rows under several axes: one row of positions, expanded, gives what its copies give, also attached to a layer."""
+    rng = gen(56)
+    M, D, hd = 7, 256, 64
+    q, k = (put(rng.standard_normal((M, h, hd)), "bf16") for h in (4, 2))
+    row, f = put(rng.integers(0, 9000, M).astype(np.int32)), put((1e4 ** (-np.arange(32) / 32)).astype(np.float32))
+    want = fl.rope(q, k, row.repeat(3, 1), f, sections=(16, 8, 8))
+    got = fl.rope(q, k, row.expand(3, -1), f, sections=(16, 8, 8))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.equal(got[0], fl.rope(q, None, row, f)[0])
+    T = {n: put(rng.standard_normal(s) / 16, "bf16") for n, s in
+         (("Wq", (D, D)), ("Wk", (128, D)), ("Wv", (128, D)), ("Wo", (D, D)), ("Wg", (64, D)), ("Wu", (64, D)), ("Wd", (D, 64)),
+          ("x", (M, D)), ("q", (M, D)), ("k", (M, 128)), ("v", (M, 128)), ("attn", (M, D)), ("h", (M, D)), ("out", (M, D)))}
+    T["gamma_attn"] = T["gamma_ffn"] = put(np.ones(D), "bf16")
+    layer = fl.DecoderLayer(**T)
+    out = []
+    for pos in (row.repeat(3, 1), row.expand(3, -1)):
+        layer.attach_cache(hd, positions=pos, inv_freq=f, sections=(16, 8, 8))
+        layer.issue(0)
+        torch.cuda.synchronize()
+        out.append((T["q"].clone(), T["k"].clone()))
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+    with pytest.raises(ValueError):
+        layer.attach_cache(hd, positions=row.repeat(3, 2)[:, ::2], inv_freq=f, sections=(16, 8, 8))
+    layer.close()
+    fl.device_status()

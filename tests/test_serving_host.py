@@ -501,3 +501,12 @@ def test_resident_counts_are_kept_by_device_and_only_when_known(tmp_path):
     subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-I", _build.CSRC, str(src), "-o", exe], check=True)
     r = subprocess.run([exe], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout
+
+
+@no_gpu
+def test_rope_takes_one_row_of_positions_for_every_axis(L):
+    def call(**kw):
+        return L.fl_rope(ctypes.byref(rope_desc(n_axes=3, axis_of=bytes([0, 1, 2, 0] * 8), **kw)), None)
+    assert call(positions_stride=0) in PASSES                                  # expanded: a stride of 0
+    assert call(positions_stride=10) in PASSES and call(positions_stride=11) in PASSES
+    assert call(positions_stride=1) == INVALID and call(positions_stride=9) == INVALID and call(positions_stride=-10) == INVALID
