@@ -285,9 +285,9 @@ fl_status rope(const fl_rope_desc* d, bool check_only, cudaStream_t s) {
     p.per_inv = inverse(p.per), p.all_inv = inverse(p.all), p.pairs_inv = inverse((uint32_t)pairs);
     // one row per CTA until that fills the SMs several times over
     p.rows_per_cta = 1;
-    while (p.rows_per_cta < kRopeRows && (d->rows + p.rows_per_cta - 1) / p.rows_per_cta > 8 * ctx.sms)
-        p.rows_per_cta *= 2;
-    const dim3 grid((unsigned)((d->rows + p.rows_per_cta - 1) / p.rows_per_cta));
+    auto ctas = [&] { return ((long long)d->rows + p.rows_per_cta - 1) / p.rows_per_cta; };
+    while (p.rows_per_cta < kRopeRows && ctas() > 8 * ctx.sms) p.rows_per_cta *= 2;
+    const dim3 grid((unsigned)ctas());
     cudaError_t e;
     if (d->dtype == FL_F16)
         e = vec ? host::launch(fl_rope_kernel<DT_F16, 8>, grid, kRopeThreads, 0, ctx.pdl, s, p)

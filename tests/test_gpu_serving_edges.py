@@ -305,3 +305,22 @@ def test_rope_of_expanded_positions():
         layer.attach_cache(hd, positions=row.repeat(3, 2)[:, ::2], inv_freq=f, sections=(16, 8, 8))
     layer.close()
     fl.device_status()
+
+
+def test_rope_of_as_many_rows_as_an_int_holds():
+    """2^31 - 1 rows: places past 2^32 bytes, and a row count next to which no sum of ints may be formed."""
+    rows, hd = 2 ** 31 - 1, 8
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    x = put(gen(57).standard_normal((1, 1, hd)), "f16")
+    pos = torch.arange(rows, dtype=torch.int32, device="cuda")
+    f = put((1e4 ** (-np.arange(4) / 4)).astype(np.float32))
+    got = fl.rope(x.expand(rows, 1, hd), None, pos, f)[0]       # (every row the same x)
+    fl.device_status()
+    at = torch.tensor([0, 1, 5000, 2 ** 28 - 1, 2 ** 28, 2 ** 30 + 3, rows - 2, rows - 1], device="cuda")
+    want = oracle.rope(np.tile(f64(x), (len(at), 1, 1)), [at.cpu().numpy()], f.cpu().numpy(), [0] * 4)
+    pair = np.abs(f64(x)).reshape(2, 4).sum(0)
+    bound = U["f16"] * np.abs(want) + 2.0 ** -21 * np.tile(pair, 2) + 2.0 ** -25
+    assert (np.abs(f64(got[at]) - want) <= bound).all()
+    del got, pos
+    torch.cuda.empty_cache()
