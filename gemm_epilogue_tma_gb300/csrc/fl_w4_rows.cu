@@ -29,8 +29,9 @@
 // x * gamma is rounded to the dtype, the one rounding before the output's (in fp16 times
 // a power of two where a row's products leave the type's range: lift_rows). For up
 // to four rows half of the MMA's columns would be idle, and take what that rounding
-// cuts off: there is no rounding to speak of then (FFN of 3 rows 23.8 -> 24.1 us,
-// 3 x 4096 x 4096 5.3 -> 5.8).
+// cuts off, if both copies of the rows leave room for a second CTA (kSmemPair: four rows up to
+// K = 6592, one up to 26560): there is no rounding to speak of then (FFN of 3 rows
+// 23.8 -> 24.1 us, 3 x 4096 x 4096 5.3 -> 5.8).
 //
 // More than eight rows are slabs of at most eight, side by side in the grid:
 // they walk the weight at the same pace, so that it is read from HBM once and

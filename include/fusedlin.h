@@ -451,7 +451,8 @@ fl_status fl_w4_quantize(const void* W, void* q, void* scales, int N, int K, int
  *   gamma: [K], the RMSNorm prologue of fl_norm_gemm; NULL: x as it is. With
  *   gamma one product is formed in the dtype: x * gamma (few rows, of any size: in
  *   fp16 a row whose products would leave the type's range is carried times a power of
- *   two; up to four rows keep what the rounding cuts off) or w * gamma (many rows; in
+ *   two; up to four rows keep what the rounding cuts off, while M (K + 32) is at most
+ *   26624 with K rounded up to 64) or w * gamma (many rows; in
  *   fp16 64 * w * gamma, which has to stay within the type's range).
  *   bias [N] and residual [M,N] may be NULL; residual may be the same pointer
  *   as out. Epilogue order as in fl_gemm_epilogue.

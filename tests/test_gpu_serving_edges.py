@@ -9,7 +9,8 @@ import torch
 
 import gemm_epilogue_tma_gb300 as fl
 import oracle
-from test_gpu_serving import DT, U, cache, f64, gen, library, put, w4_ref, w4_tensors  # noqa: F401 (library: the fixture)
+from test_gpu_serving import (DT, U, cache, f64, gen, library, put, w4_check, w4_ref,  # noqa: F401 (library: the fixture)
+                              w4_tensors)
 
 pytestmark = pytest.mark.gpu
 
@@ -94,6 +95,72 @@ def test_w4_gemm_row_without_a_finite_sum_stays_alone():
         assert not torch.isfinite(got[1]).any() and torch.isnan(got[2]).all() and (got[3] == 0).all()
         keep = [m for m in range(M) if m not in (1, 2, 3)]
         assert torch.equal(got[keep], want[keep])
+
+
+# ---------------------------------------------------------------------------
+# long rows
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("M,N,K,group", [(1, 136, 28672, 128), (4, 264, 8192, 64), (7, 264, 14336, 128), (8, 264, 12736, 64),
+                                         (8, 264, 12800, 64), (8, 136, 28672, 128), (24, 264, 14336, 128), (40, 264, 14336, 32),
+                                         (300, 136, 28672, 128)])
+def test_w4_gemm_of_long_rows(dt, M, N, K, group):
+    """K past what eight rows take in shared memory (12736), on both sides of it and on both kernels."""
+    for k, (zeros, norm) in enumerate([(True, True), (False, False)]):
+        rng = gen(58, M, K, k)
+        x = put(rng.standard_normal((M, K)) * np.where(rng.random(K) < 0.01, 20.0, 1.0), dt)
+        w = w4_tensors(rng, N, K, group, zeros, dt)
+        gamma = put(1 + 0.1 * rng.standard_normal(K), dt) if norm else None
+        got = fl.w4_gemm(x, w[0], w[1], zeros=w[2], gamma=gamma)
+        fl.device_status()
+        y, mag, sq = w4_ref(x, w, gamma, 1e-6)
+        w4_check(got, y, mag, sq, K, dt, what=f"{dt} {M}x{N}x{K} {k}")
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("M,K,group", [(1, 26496, 128), (2, 13248, 32), (3, 8832, 64), (4, 6592, 32), (4, 6528, 128)])
+def test_w4_gemm_up_to_four_rows_of_the_longest_k(dt, M, K, group):
+    """Up to M (K + 32) = 26624 the rows' x * gamma is not rounded to speak of: u^2 of the terms, the output's u, and
+    the sums' K 2^-24 per term at most (fp32 sums of K terms, each addition off by 2^-24 of a partial sum that is
+    at most the terms' sum; a group's within the matrix unit, so K is far above their number)."""
+    rng = gen(59, M, K)
+    N = 136
+    assert M * ((K + 63) // 64 * 64 + 32) <= 26624
+    x = put(rng.standard_normal((M, K)), dt)
+    w = w4_tensors(rng, N, K, group, False, dt)
+    gamma = put(1 + 0.1 * rng.standard_normal(K), dt)
+    got = f64(fl.w4_gemm(x, w[0], w[1], gamma=gamma))
+    fl.device_status()
+    y, mag, _ = w4_ref(x, w, gamma, 1e-6)
+    u = U[dt]
+    err = np.abs(got - y)
+    assert (err <= u * np.abs(y) + (u * u + K * 2.0 ** -24) * mag + 2.0 ** -25).all()
+    # mean square: the output's rounding, and a tenth of it for all else
+    assert np.sqrt((err ** 2).mean()) <= 1.1 * u / np.sqrt(3) * np.sqrt((y ** 2).mean())
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("M", [1, 3, 8, 20, 200])
+def test_w4_swiglu_ffn_of_a_wide_block(dt, M):
+    """F = 14336: the down product's rows are past the decode kernel's room from eight rows on."""
+    rng = gen(60, M)
+    D, F, group = 512, 14336, 128
+    x, gamma = put(rng.standard_normal((M, D)), dt), put(1 + 0.1 * rng.standard_normal(D), dt)
+    Wg, Wu, Wd = (w4_tensors(rng, n, k, group, False, dt) for n, k in ((F, D), (F, D), (D, F)))
+    got = f64(fl.w4_swiglu_ffn(x, gamma, Wg[:2], Wu[:2], Wd[:2]))
+    fl.device_status()
+    g, gm, _ = w4_ref(x, Wg, gamma, 1e-6)
+    v, vm, _ = w4_ref(x, Wu, gamma, 1e-6)
+    h = oracle.silu(g) * v
+    W = oracle.w4_weight(Wd[0].cpu().numpy(), f64(Wd[1]))
+    y = h @ W.T + f64(x)
+    u = U[dt]
+    dg, dv = ((2.1 * u + D * 2.0 ** -22) * m for m in (gm, vm))
+    dh = (1.1 * dg + 2.0 ** -15 * np.abs(g)) * (np.abs(v) + dv) + np.abs(oracle.silu(g)) * dv + u * np.abs(h)
+    bound = u * np.abs(y) + dh @ np.abs(W).T + (1.05 * u + F * 2.0 ** -22) * (np.abs(h) @ np.abs(W).T)
+    err = np.abs(got - y)
+    assert (err <= bound).all(), (err / bound).max()
+    assert np.sqrt((err ** 2).mean()) <= 4 * u * np.sqrt((y ** 2).mean())
 
 
 # ---------------------------------------------------------------------------
