@@ -1,7 +1,8 @@
 """Edges of the serving operators on the GPU: ranges, long rows, small activations, what graphs keep (needs an sm_103a GPU).
 
 Bounds are those of tests/test_gpu_serving.py, u the largest relative error of one rounding to the dtype (2^-8 bf16,
-2^-11 fp16 with the type's smallest values next to it), each derived beside its test.
+2^-11 fp16 with the type's smallest values next to it), each derived beside its test. The cache's scales are amax times
+1 / top rounded to fp32, as the header has them, which may differ from fp32's quotient in the last bit.
 """
 import numpy as np
 import pytest
@@ -9,8 +10,8 @@ import torch
 
 import gemm_epilogue_tma_gb300 as fl
 import oracle
-from test_gpu_serving import (DT, U, cache, f64, gen, library, put, w4_check, w4_ref,  # noqa: F401 (library: the fixture)
-                              w4_tensors)
+from test_gpu_serving import (DT, U, cache, f64, gen, library, put, serving_calls, snapshot, w4_check,  # noqa: F401
+                              w4_ref, w4_tensors)  # (library: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -391,3 +392,93 @@ def test_rope_of_as_many_rows_as_an_int_holds():
     assert (np.abs(f64(got[at]) - want) <= bound).all()
     del got, pos
     torch.cuda.empty_cache()
+
+
+# ---------------------------------------------------------------------------
+# every way of issuing, from tensors that do not hold the answer
+# ---------------------------------------------------------------------------
+def put_back(tensors, held):
+    for t, h in zip(tensors, held):
+        t.view(h.dtype).copy_(h)
+
+
+@pytest.mark.parametrize("M", [2, 300])
+@pytest.mark.parametrize("pdl", [1, 0])
+def test_second_calls_write_the_result_again(M, pdl):
+    """The same call on the same tensors, which hold what they held before the first one: its whole result again, with and
+    without programmatic launches. (Of a tensor that the call fills, nothing of the old content is left.)"""
+    for call, made, launches in serving_calls(gen(61, M), M):
+        before = snapshot(made)
+        call()
+        torch.cuda.synchronize()
+        want = snapshot(made)
+        assert not all(torch.equal(w, b) for w, b in zip(want, before))
+        fl.set_option("pdl", pdl)
+        try:
+            for fill in (None, 0x5a):
+                put_back(made, before)
+                if fill is not None and made[0].dim() != 4:            # (all but the cache, of which a call writes places)
+                    for t in made:
+                        t.view(torch.uint8).fill_(fill)
+                torch.cuda.synchronize()
+                n = fl.kernel_launches()
+                call()
+                torch.cuda.synchronize()
+                assert fl.kernel_launches() - n == launches
+                assert all(torch.equal(t.view(torch.uint8), w.view(torch.uint8)) for t, w in zip(made, want))
+        finally:
+            fl.set_option("pdl", 1)
+    fl.device_status()
+
+
+def test_replayed_decode_step_writes_the_cache():
+    """A captured decode step (products, rotation, cache written and read back, FFN), replayed from the cache as it was
+    before the step and with every other tensor poisoned: the direct step's bits everywhere, twice."""
+    rng = gen(62)
+    D, hq, hk, hd, F, page, B = 512, 4, 2, 128, 1024, 16, 2
+    W = {n: fl.w4_quantize(put(rng.standard_normal(s) / np.sqrt(s[1]), "bf16"), 64) for n, s in
+         (("qkv", ((hq + 2 * hk) * hd, D)), ("o", (D, hq * hd)), ("g", (F, D)), ("u", (F, D)), ("d", (D, F)))}
+    gamma, x = put(1 + 0.1 * rng.standard_normal(D), "bf16"), put(rng.standard_normal((B, D)), "bf16")
+    f = put((1e4 ** (-np.arange(64) / 64)).astype(np.float32))
+
+    def i32(*v):
+        return put(np.array(v, dtype=np.int32))
+    table, at, ctx = put(np.array([[4, 1], [0, 3]], dtype=np.int32)), i32(15, 7), i32(0, 16, 24)
+    (kc, vc), (ks, vs) = cache(5, page, hk, hd, "int8")
+    held = [kc, vc, ks, vs]
+    for t in held[:2]:
+        t.copy_(put(rng.integers(-127, 128, t.shape).astype(np.int8)))
+    e = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    qkv, q1, ck, cv, h, y = e(B, (hq + 2 * hk) * hd), e(B, hq, hd), e(24, hk, hd), e(24, hk, hd), e(B, D), e(B, D)
+    ws = torch.empty(fl.w4_swiglu_ffn_workspace_size(B, D, F), dtype=torch.uint8, device="cuda")
+    out = [qkv, q1, ck, cv, h, y]
+
+    def step():
+        fl.w4_gemm(x, *W["qkv"], gamma=gamma, out=qkv)
+        q, k, v = (t.unflatten(1, (-1, hd)) for t in qkv.split((hq * hd, hk * hd, hk * hd), 1))
+        fl.rope(q, k, at, f, out_q=q1, out_k=k)
+        fl.kv_write(k, v, kc, vc, ks, vs, table, at)
+        fl.kv_read(kc, vc, ks, vs, table, ctx, out_k=ck, out_v=cv)
+        fl.w4_gemm(q1.flatten(1), *W["o"], residual=x, out=h)
+        fl.w4_swiglu_ffn(h, gamma, W["g"], W["u"], W["d"], out=y, workspace=ws)
+    before = snapshot(held)
+    step()
+    fl.device_status()
+    want = snapshot(held + out)
+    assert all(not torch.equal(a, b) for a, b in zip(want, before))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        graph = fl.Graph.capture(step)
+    torch.cuda.current_stream().wait_stream(side)
+    for _ in range(2):
+        put_back(held, before)
+        for t in out + [ws]:
+            t.view(torch.uint8).fill_(0xff)
+        torch.cuda.synchronize()
+        graph.launch()
+        torch.cuda.synchronize()
+        assert all(torch.equal(t.view(torch.uint8), w.view(torch.uint8)) for t, w in zip(held + out, want))
+    graph.close()
+    fl.device_status()
+    fl.device_status(side)
