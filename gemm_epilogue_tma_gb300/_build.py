@@ -5,7 +5,8 @@ objects link into gemm_epilogue_tma_gb300/libfusedlin.so (CUDA runtime linked
 statically, the driver reached through the runtime's entry-point query, so
 the library loads on a machine without a GPU). binding/fl_torch.cpp, the
 extension module that passes torch tensors to the serving operators, compiles
-beside them with the host compiler into _torch_binding.so.
+beside them with the host compiler into _torch_binding.so, against the torch
+that is installed; without one the library is built alone.
 
     python -m gemm_epilogue_tma_gb300._build [--force] [--verbose-ptxas]
 """
@@ -14,6 +15,7 @@ from __future__ import annotations
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -27,6 +29,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfusedlin.so")
 BINDING_SRC = os.path.join(PKG, "binding", "fl_torch.cpp")
 BINDING = os.path.join(PKG, "_torch_binding.so")
+STAMP = os.path.join(BUILD, "fl_torch.stamp")  # the torch that BINDING was built against
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -77,9 +80,26 @@ def _run(what: str, cmd) -> None:
         raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
 
 
-def _compile_binding() -> str:
+def _torch():
+    """The installed torch and Python, as text that changes with them; None without torch. (Not imported for it.)"""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or spec.origin is None:
+        return None
+    version = os.path.join(os.path.dirname(spec.origin), "version.py")
+    with open(version) as f:
+        return f"{spec.origin}\n{f.read()}\nPython {sys.version_info[0]}.{sys.version_info[1]}\n"
+
+
+def _stamped(torch_text) -> bool:
+    if not os.path.exists(STAMP):
+        return False
+    with open(STAMP) as f:
+        return f.read() == torch_text
+
+
+def _compile_binding(torch_text: str) -> str:
     obj = os.path.join(BUILD, "fl_torch.o")
-    if not _stale(obj, [BINDING_SRC] + _headers()):
+    if not _stale(obj, [BINDING_SRC] + _headers()) and _stamped(torch_text):
         return obj
     import sysconfig
 
@@ -105,22 +125,28 @@ def _link_binding(obj: str) -> None:
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = None) -> str:
-    """Compile csrc/*.cu and link libfusedlin.so; returns the library path."""
+    """Compile csrc/*.cu and link libfusedlin.so, and the binding if there is a torch; returns the library path."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
     if force:
         for o in glob.glob(os.path.join(BUILD, "*.o")):
             os.remove(o)
-    if not force and not _stale(LIB, srcs + _headers()) and not _stale(BINDING, [BINDING_SRC, LIB]):
+    torch_text = _torch()
+    bound = torch_text is None or (not _stale(BINDING, [BINDING_SRC, LIB] if os.path.exists(LIB) else [BINDING_SRC])
+                                   and _stamped(torch_text))
+    if not force and not _stale(LIB, srcs + _headers()) and bound:
         return LIB
     jobs = jobs or min(len(srcs) + 1, os.cpu_count() or 4)
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
-        binding = ex.submit(_compile_binding)
+        binding = None if torch_text is None else ex.submit(_compile_binding, torch_text)
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
         tmp = LIB + ".tmp"
         _run("link", [nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *objs])
         os.replace(tmp, LIB)
-        _link_binding(binding.result())
+        if binding is not None:
+            _link_binding(binding.result())
+            with open(STAMP, "w") as f:
+                f.write(torch_text)
     return LIB
 
 

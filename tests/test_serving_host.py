@@ -510,3 +510,65 @@ def test_rope_takes_one_row_of_positions_for_every_axis(L):
     assert call(positions_stride=0) in PASSES                                  # expanded: a stride of 0
     assert call(positions_stride=10) in PASSES and call(positions_stride=11) in PASSES
     assert call(positions_stride=1) == INVALID and call(positions_stride=9) == INVALID and call(positions_stride=-10) == INVALID
+
+
+# ---------------------------------------------------------------------------
+# the build
+# ---------------------------------------------------------------------------
+@pytest.fixture
+def toy_build(monkeypatch, tmp_path):
+    """_build on a folder of its own, with compilers that note what they are asked for and leave a file."""
+    csrc = tmp_path / "csrc"
+    csrc.mkdir()
+    (csrc / "one.cu").write_text("")
+    (tmp_path / "fl_torch.cpp").write_text("")
+    out = tmp_path / "_build"
+    for name, value in (("PKG", str(tmp_path)), ("CSRC", str(csrc)), ("BUILD", str(out)), ("INCLUDE", str(csrc)),
+                        ("LIB", str(tmp_path / "libfusedlin.so")), ("BINDING", str(tmp_path / "_torch_binding.so")),
+                        ("BINDING_SRC", str(tmp_path / "fl_torch.cpp")), ("STAMP", str(out / "fl_torch.stamp"))):
+        monkeypatch.setattr(_build, name, value, raising=False)
+    asked = []
+
+    def run(cmd, **kw):
+        made = cmd[cmd.index("-o") + 1]
+        asked.append(made.replace(str(tmp_path), "").removesuffix(".tmp"))
+        with open(made, "w") as f:
+            f.write("x")
+
+        class Result:
+            returncode, stdout, stderr = 0, "", ""
+        return Result
+    monkeypatch.setattr(_build.subprocess, "run", run)
+
+    def build():
+        del asked[:]
+        _build.build()
+        return sorted(asked)
+    return build
+
+
+EVERYTHING = ["/_build/fl_torch.o", "/_build/one.o", "/_torch_binding.so", "/libfusedlin.so"]
+
+
+def test_binding_is_rebuilt_when_torch_changes(toy_build, monkeypatch):
+    assert toy_build() == EVERYTHING
+    assert toy_build() == []
+    monkeypatch.setattr(_build, "_torch", lambda: "another torch", raising=False)
+    assert toy_build() == ["/_build/fl_torch.o", "/_torch_binding.so", "/libfusedlin.so"]
+    assert toy_build() == []
+
+
+def test_library_is_built_without_torch(toy_build, monkeypatch):
+    import builtins
+    import importlib.util
+    find, imports = importlib.util.find_spec, builtins.__import__
+
+    def no_torch(name, *a, **k):
+        if name == "torch" or name.startswith("torch."):
+            raise ImportError("no torch here")
+        return imports(name, *a, **k)
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: None if name == "torch" else find(name, *a))
+    monkeypatch.setattr(builtins, "__import__", no_torch)
+    assert toy_build() == ["/_build/one.o", "/libfusedlin.so"]
+    assert toy_build() == []
+    monkeypatch.undo()
