@@ -125,7 +125,9 @@ fl_status check_weight(const char* name, const fl_w4_weight* w, long long N, lon
     if (w->group != 32 && w->group != 64 && w->group != 128)
         return fail(FL_ERR_INVALID_ARG, "%s: group must be 32, 64 or 128 (%d)", name, w->group);
     if (N < 1 || K < 1) return fail(FL_ERR_INVALID_ARG, "%s: sizes must be positive (N=%lld K=%lld)", name, N, K);
+    // (tiles of rows and steps of k run past the ends before they are cut off: room for that below 2^31)
     if (N > 0x7fffff00ll) return fail(FL_ERR_UNSUPPORTED, "%s: too many rows (%lld)", name, N);
+    if (K > 0x7ffff000ll) return fail(FL_ERR_UNSUPPORTED, "%s: rows too long (%lld)", name, K);
     if (N % 8 != 0 || K % w->group != 0)
         return fail(FL_ERR_ALIGNMENT, "%s: N must be a multiple of 8 and K of the group (N=%lld K=%lld group %d)", name,
                     N, K, w->group);

@@ -56,7 +56,8 @@ constexpr int kSmemPair = 104 * 1024;  // two CTAs to an SM
 // Row stride of the activation rows in 16-byte vectors: 4 mod 8, so that the
 // 8 lanes of a quarter warp (two rows, four vectors each) hit different banks.
 __host__ __device__ __forceinline__ int row_vecs(int K) { return (K / 8 + 7) / 8 * 8 + 4; }
-__host__ __device__ __forceinline__ int smem_bytes(int M, int K) { return M * row_vecs(K) * 16; }
+// (64 bits: K may be any int)
+__host__ __device__ __forceinline__ long long smem_bytes(int M, int K) { return (long long)M * row_vecs(K) * 16; }
 
 template <int DT>
 struct Mma;
@@ -488,7 +489,7 @@ cudaError_t launch_rows(const W4Params& p, const host::LaunchContext& ctx, cudaS
     static std::atomic<unsigned long long> done{0};
     const cudaError_t attr = host::allow_smem(kern, kSmemMax, ctx.device, done);
     if (attr != cudaSuccess) return attr;
-    const int slabs = slabs_of(p.M), smem = smem_bytes(p.halves ? 2 * p.slab : p.slab, p.K), units = DUAL ? p.N / 8 : (p.N + 15) / 16;
+    const int slabs = slabs_of(p.M), smem = (int)smem_bytes(p.halves ? 2 * p.slab : p.slab, p.K), units = DUAL ? p.N / 8 : (p.N + 15) / 16;
     int most = ctx.sms * (smem <= kSmemPair ? 2 : 1) / slabs;  // resident CTAs of a slab
     if (most < 1) most = 1;
     return host::launch(kern, dim3((unsigned)(units < most ? units : most), (unsigned)slabs), kThreads, (size_t)smem, ctx.pdl,

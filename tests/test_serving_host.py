@@ -572,3 +572,33 @@ def test_library_is_built_without_torch(toy_build, monkeypatch):
     assert toy_build() == ["/_build/one.o", "/libfusedlin.so"]
     assert toy_build() == []
     monkeypatch.undo()
+
+
+# ---------------------------------------------------------------------------
+# sizes whose products pass 32 bits
+# ---------------------------------------------------------------------------
+def test_rows_of_any_length_are_measured_in_64_bits(L):
+    """Rows far too long for the decode kernel's shared memory go to the tile kernel, which wants its row scales, also
+    where the bytes they would take are a small number modulo 2^32."""
+    for M in (1, 2, 3, 8, 16, 24):
+        for K in (1 << 26, 1 << 27, 1 << 28, 1 << 29, 1 << 30, (1 << 28) + 128, 0x7fff0000):
+            assert fl.w4_gemm_workspace_size(M, K, True) >= 4 * M, (M, K)
+            assert fl.w4_swiglu_ffn_workspace_size(M, K, 64) >= 2 * 64 * M + 4 * M, (M, K)
+
+
+@no_gpu
+def test_rows_next_to_2_31_are_refused(L):
+    """Steps of 64 k and loads of 2048 run past a row's end before they are cut off: no sum of those may pass 2^31."""
+    def gemm(K):
+        return L.fl_w4_gemm(addr(0), addr(1), ctypes.byref(weight(group=32)), None, None, addr(4), 30, 8, K, 1e-6, 0, addr(5),
+                            1 << 30, 0, None)
+
+    def ffn(D, F):
+        w = [weight(i, group=32) for i in (20, 22, 24)]
+        return L.fl_w4_swiglu_ffn(addr(0), addr(1), *(ctypes.byref(v) for v in w), None, addr(4), 1, D, F, 1e-6, addr(6),
+                                  1 << 35, 0, None)
+    assert gemm(0x7fffffe0) == UNSUPPORTED and "too long" in fl.last_error()
+    assert gemm(0x7ffff020) == UNSUPPORTED and "too long" in fl.last_error()
+    assert gemm(0x7fff0000) in PASSES and "too long" not in fl.last_error()
+    assert ffn(0x7fffffe0, 32) == UNSUPPORTED and "too" in fl.last_error()
+    assert ffn(32, 0x7fffffe0) == UNSUPPORTED and "too" in fl.last_error()
