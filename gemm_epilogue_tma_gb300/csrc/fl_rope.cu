@@ -7,8 +7,8 @@
 // the row and the pair only, so a CTA computes the sines of its rows once into
 // shared memory and applies them to every head of q and k; a thread has four
 // tasks (8 pairs of a head each, two 16-byte vectors) in flight, the first of
-// them requested before the sines are computed. Measured: 4099 rows of 32 and 8
-// heads of 128 on three axes 15.0 us (5.6 TB/s); 7 rows 2.1 us, a launch and one
+// them requested before the sines are computed. Measured in graphs: 4099 rows of 32 and 8
+// heads of 128 on three axes 14.9 us (5.6 TB/s); 7 rows 2.2 us, a launch and one
 // round trip for the positions and one for the vectors.
 //
 // The angle is taken in turns, in fixed point: f = frac(inv_freq / 2 pi) as a

@@ -15,8 +15,8 @@
 // 128 or 1024, one subtraction leaves the integers); the activation rows are
 // stored in shared memory in the same order, one 16-byte vector per word.
 //
-// Measured: 1 x 4096 x 4096 4.9 us, 1 x 11008 x 4096 8.6 us (2.7 TB/s), SwiGLU FFN
-// 4096 x 11008 of 3 rows 24.1 us (2.9 TB/s). A CTA's start (rows of x to shared
+// Measured in graphs: 1 x 4096 x 4096 4.9 us, 1 x 11008 x 4096 8.5 us (2.7 TB/s), SwiGLU FFN
+// 4096 x 11008 of 3 rows 24.3 us (2.9 TB/s). A CTA's start (rows of x to shared
 // memory, their norm, the first codes: 2.3 us at 1 x 1024 x 1024) is what keeps one
 // product of a decode step from the rate of its stream. Loads land in L1 lines, so
 // shared memory taken for more than the rows costs loads in flight: with the
@@ -31,7 +31,7 @@
 // to four rows half of the MMA's columns would be idle, and take what that rounding
 // cuts off, if both copies of the rows leave room for a second CTA (kSmemPair: four rows up to
 // K = 6592, one up to 26560): there is no rounding to speak of then (FFN of 3 rows
-// 23.8 -> 24.1 us, 3 x 4096 x 4096 5.3 -> 5.8).
+// 23.8 -> 24.3 us, 3 x 4096 x 4096 5.3 -> 5.6).
 //
 // More than eight rows are slabs of at most eight, side by side in the grid:
 // they walk the weight at the same pace, so that it is read from HBM once and
@@ -497,12 +497,15 @@ cudaError_t launch_rows(const W4Params& p, const host::LaunchContext& ctx, cudaS
 }
 
 // The choice between this kernel and the tile kernel, by rows and weights,
-// measured side by side (us, this kernel / the tile kernel):
-//   1024 x 1024: 128 rows 6.2 / 9.1
-//   2048 x 2048: 64 rows 8.2 / 10.9; 4096 x 1024: 64 rows 9.2 / 9.4, 96 rows 12.8 / 9.9
-//   4096 x 4096: 24 rows 10.6 / 13.8, 32 rows 12.6 / 13.8, 64 rows 18.6 / 14.6
-//   11008 x 4096: 32 rows 24 / 33; 4096 x 11008: 16 rows 17 / 20, 24 rows 23 / 20, 32 rows 26 / 20
-//   FFN 4096 x 11008: 16 rows 44 / 66, 24 rows 58 / 66, 32 rows 71 / 66, 64 rows 130 / 68
+// measured side by side in graphs (us, this kernel / the tile kernel; with gamma but for
+// the 4096 x 11008):
+//   1024 x 1024: 64 rows 4.3 / 8.2, 128 rows 6.3 / 8.2
+//   2048 x 2048: 64 rows 8.3 / 9.7; 4096 x 1024: 64 rows 9.3 / 8.7, 96 rows 13.3 / 9.3
+//   4096 x 4096: 24 rows 10.5 / 15.6, 32 rows 12.5 / 15.6, 64 rows 18.7 / 16.4; without gamma
+//   32 rows 11.8 / 10.8
+//   11008 x 4096: 32 rows 24.5 / 33.4; 4096 x 11008: 16 rows 17.7 / 18.7, 24 rows 23.6 / 19.1,
+//   32 rows 26.8 / 19.1
+//   FFN 4096 x 11008: 16 rows 45 / 62, 24 rows 60 / 63, 32 rows 72 / 63, 64 rows 132 / 64
 //   (with its gate and up product here and the other there: 70 with 24 rows, so
 //   that long rows, for which 24 is late, keep to the limit of large weights)
 int rows_limit(long long weights, int K) {

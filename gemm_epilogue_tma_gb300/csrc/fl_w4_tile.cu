@@ -13,14 +13,16 @@
 // multiplied as they are: with the output's two roundings, the error 1.4 times
 // that of an fp32 product rounded once (rounding x * gamma as well would be a
 // third: 1.6 times). The row scale 1 / rms, from a kernel of its own
-// that reads x once (2 us at 333 x 4096, 5 at 2048 x 4096), is applied to the fp32 sums.
+// that reads x once, is applied to the fp32 sums. (That kernel and the products with
+// gamma: 64 x 4096 x 4096 16.4 us instead of 11.3, 333 rows 24.1 instead of 17.3, 2048
+// rows 58.5 instead of 45.5.)
 //
 // What bounds it, per K step: with 256 tokens the MMA (514 cycles; 512 by the
 // tensor rate), with fewer the expansion of the codes, which sets a step's
 // least time whatever the tile's width: some 540 cycles, a tenth more where gamma
-// is multiplied in. Measured: 4096^3 86 to 92 us by box (1490 to 1600 TFLOP/s),
-// 2048 rows of the SwiGLU FFN 4096 x 11008 366 to 403 us (1375 to 1510 TFLOP/s),
-// 333 x 6144 x 4096 30 us, 64 x 4096 x 4096 14.0 us. The warps fetch instructions
+// is multiplied in. Measured in graphs: 4096^3 86 to 92 us by box (1490 to 1600 TFLOP/s),
+// 2048 rows of the SwiGLU FFN 4096 x 11008 368 to 403 us (1375 to 1505 TFLOP/s),
+// 333 x 6144 x 4096 30 to 32 us, 64 x 4096 x 4096 14.0 to 16.4 us. The warps fetch instructions
 // as hard as they compute: a step's two halves as one loop of half the code took
 // 6 % off every size, four quarters gave it back. A tile of two blocks of 128
 // rows by 128 tokens moved fewer bytes per MMA but expanded every code for half
@@ -722,7 +724,8 @@ fl_status w4_tile(int dt, bool dual, const W4Params& w, void* workspace, const h
         const dim3 grid((unsigned)((w.M + 7) / 8));
         // Its CTAs begin only when the kernel before it is done if they have much to read: let in
         // early they crowd into the few multiprocessors that are idle in its last wave
-        // (us of a product, early / not: 64 x 4096^2 13.8 / 14.0, 333 22.0 / 22.0, 2048 67.3 / 61.5).
+        // (us of a product, early / not: 64 x 4096^2 16.6 / 16.9, 333 24.1 / 24.8, 1024 33.7 / 34.0,
+        // 2048 65.7 / 59.1; 333 x 6144 x 4096 33.8 / 31.8, 333 x 11008 x 4096 44.9 / 45.3).
         const int early = (long long)w.M * w.K < (1ll << 21) ? ctx.pdl : 0;
         auto kern = dt == FL_F16 ? fl_w4_row_scale_kernel<DT_F16> : fl_w4_row_scale_kernel<DT_BF16>;
         const fl_status st = host::launched(host::launch(kern, grid, 256, 0, early, stream, w.x, scale, w.M, w.K, w.eps),
