@@ -352,6 +352,8 @@ class DecoderLayer:
 
         M = T["x"].shape[0]
         if inv_freq is not None:
+            if positions is None or positions.dim() not in (1, 2) or inv_freq.dim() != 1:
+                raise ValueError("positions [rows] or [axes, rows] and inv_freq [pairs] must be given")
             pairs, axes = inv_freq.shape[0], positions.shape[0] if positions.dim() == 2 else 1
             sections = (pairs,) if sections is None and axes == 1 else sections
             if sections is None or len(sections) != axes or sum(sections) != pairs or min(sections) < 0 or axes > 4:
@@ -367,8 +369,10 @@ class DecoderLayer:
             formats = {torch.int8: 0, torch.float8_e4m3fn: 1}
             if k_cache.dtype not in formats:
                 raise ValueError(f"k_cache has dtype {k_cache.dtype}, expected int8 or float8_e4m3fn")
-            if start is None or page_table is None:
-                raise ValueError("page_table and start must be given")
+            if start is None or page_table is None or v_cache is None or k_scale is None or v_scale is None:
+                raise ValueError("v_cache, k_scale, v_scale, page_table and start must be given")
+            if k_cache.dim() != 4 or page_table.dim() != 2:
+                raise ValueError("k_cache must have four axes and page_table two")
             pages, size = k_cache.shape[:2]
             seqs, per = page_table.shape
             shape = (pages, size, T["k"].shape[1] // head_dim, head_dim)

@@ -602,3 +602,24 @@ def test_rows_next_to_2_31_are_refused(L):
     assert gemm(0x7fff0000) in PASSES and "too long" not in fl.last_error()
     assert ffn(0x7fffffe0, 32) == UNSUPPORTED and "too" in fl.last_error()
     assert ffn(32, 0x7fffffe0) == UNSUPPORTED and "too" in fl.last_error()
+
+
+def test_attach_cache_names_what_is_missing(monkeypatch):
+    """Parts of a description that are left out or have other axes are a ValueError, before the library is called."""
+    fake = FakeLibrary()
+    monkeypatch.setattr(fl, "lib", lambda: fake)
+    monkeypatch.setattr(fl, "_check_tensors", lambda *a, **k: None)
+    x, W = torch.zeros((4, 64), dtype=torch.float16), torch.zeros((64, 64), dtype=torch.float16)
+    layer = fl.DecoderLayer(x=x, Wg=W, Wk=W, q=x, k=x)
+    f, pos, table, start = torch.ones(16), torch.zeros(4, dtype=torch.int32), torch.zeros((4, 2), dtype=torch.int32), torch.zeros(4, dtype=torch.int32)
+    kc, ks = torch.zeros((8, 16, 2, 32), dtype=torch.int8), torch.zeros((8, 16, 2))
+    full = dict(k_cache=kc, v_cache=kc, k_scale=ks, v_scale=ks, page_table=table, start=start)
+    del fake.calls[:]
+    layer.attach_cache(32, positions=pos, inv_freq=f, **full)
+    assert fake.calls == ["fl_layer_attach_cache"]
+    for bad in (dict(inv_freq=f), dict(inv_freq=f, positions=pos[0]), dict(inv_freq=f[None], positions=pos),
+                *({**full, n: None} for n in ("v_cache", "k_scale", "v_scale", "page_table", "start")),
+                {**full, "k_cache": kc[0]}, {**full, "page_table": table[0]}):
+        with pytest.raises(ValueError):
+            layer.attach_cache(32, **bad)
+    assert fake.calls == ["fl_layer_attach_cache"]
