@@ -404,7 +404,6 @@ class DecoderLayer:
             pass
 
 
-
 class Graph:
     """A CUDA graph of library calls (fl_capture_begin / fl_capture_end / fl_graph_launch)."""
 
@@ -574,9 +573,9 @@ def rope(q, k, positions, inv_freq, sections=None, interleaved=False, inverse=Fa
 
     The pairs (i, i + R/2) of the first R = 2 * len(inv_freq) channels, or (2i, 2i + 1) if interleaved, are turned
     by positions * inv_freq[i]; the other channels are copied. positions: int32 [rows], or [axes, rows] with
-    `sections` saying how many consecutive pairs follow each axis (rows contiguous; one row expanded to the axes will do). inverse turns back: the gradient with respect to
-    the input. q, k and the outputs may be strided views with contiguous channels (column ranges of a stacked
-    projection's output); an output may be its input itself."""
+    `sections` saying how many consecutive pairs follow each axis (rows contiguous; one row expanded to the axes will
+    do). inverse turns back: the gradient with respect to the input. q, k and the outputs may be strided views with
+    contiguous channels (column ranges of a stacked projection's output); an output may be its input itself."""
     if stream is None:
         r = (_ops or ops()).rope(q, k, positions, inv_freq, sections, interleaved, inverse, out_q, out_k, None)
     else:
