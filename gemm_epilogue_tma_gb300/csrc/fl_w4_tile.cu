@@ -20,7 +20,7 @@
 // What bounds it, per K step: with 256 tokens the MMA (514 cycles; 512 by the
 // tensor rate), with fewer the expansion of the codes, which sets a step's
 // least time whatever the tile's width: some 540 cycles, a tenth more where gamma
-// is multiplied in. Measured in graphs: 4096^3 86 to 92 us by box (1490 to 1600 TFLOP/s),
+// is multiplied in. Measured in graphs: 4096^3 86 to 92 us from run to run (1490 to 1600 TFLOP/s),
 // 2048 rows of the SwiGLU FFN 4096 x 11008 368 to 403 us (1375 to 1505 TFLOP/s),
 // 333 x 6144 x 4096 30 to 32 us, 64 x 4096 x 4096 14.0 to 16.4 us. The warps fetch instructions
 // as hard as they compute: a step's two halves as one loop of half the code took
