@@ -16,7 +16,10 @@ Entry points mirror the C ABI declared in include/fusedlin.h:
     w4_gemm(x, q, scales, zeros, gamma, bias, residual, out, eps, act)    dense layer on a 4-bit weight
     w4_swiglu_ffn(x, gamma, Wg, Wu, Wd, bias_down, out, eps, workspace)   the SwiGLU block on 4-bit weights
     rope(q, k, positions, inv_freq, sections)                             rotary positions, one to four axes
+    attention(q, k, v, cu_q, cu_k, causal, scale, out)                    attention of a prompt's rows
     kv_write / kv_read                                                    paged 8-bit key/value cache
+    kv_attend(q, k_cache, ..., start, cu_rows, tree, scale, out)          attention of new rows over that cache
+    kv_resize / kv_fork / kv_compact                                      the cache's pages and accepted drafts
 """
 from __future__ import annotations
 
@@ -72,6 +75,34 @@ class KvDesc(ctypes.Structure):
                 + [(n, ctypes.c_void_p) for n in ("k_cache", "v_cache", "k_scale", "v_scale")])
 
 
+class AttentionDesc(ctypes.Structure):
+    """fl_attention_desc."""
+    _fields_ = ([(n, ctypes.c_int) for n in ("dtype", "rows_q", "rows_k", "heads_q", "heads_k", "head_dim", "n_seqs",
+                                             "causal")]
+                + [("scale", ctypes.c_float)]
+                + [(n, ctypes.c_void_p) for n in ("cu_q", "cu_k", "q", "k", "v", "out")]
+                + [(n, ctypes.c_longlong) for n in ("q_row", "q_head", "k_row", "k_head", "v_row", "v_head", "out_row",
+                                                    "out_head")])
+
+
+class KvAttendDesc(ctypes.Structure):
+    """fl_kv_attend_desc."""
+    _fields_ = ([(n, ctypes.c_int) for n in ("dtype", "format", "rows", "heads_q", "heads_k", "head_dim", "page_size",
+                                             "n_pages", "n_seqs", "table_pages", "tree_cols")]
+                + [("scale", ctypes.c_float)]
+                + [(n, ctypes.c_longlong) for n in ("table_stride", "tree_stride")]
+                + [(n, ctypes.c_void_p) for n in ("page_table", "cu_rows", "start", "tree", "q", "out")]
+                + [(n, ctypes.c_longlong) for n in ("q_row", "q_head", "out_row", "out_head")]
+                + [(n, ctypes.c_void_p) for n in ("k_cache", "v_cache", "k_scale", "v_scale")])
+
+
+class KvPages(ctypes.Structure):
+    """fl_kv_pages."""
+    _fields_ = ([(n, ctypes.c_int) for n in ("heads", "head_dim", "page_size", "n_pages", "n_seqs", "table_pages")]
+                + [("table_stride", ctypes.c_longlong)]
+                + [(n, ctypes.c_void_p) for n in ("page_table", "k_cache", "v_cache", "k_scale", "v_scale")])
+
+
 class LayerCacheDesc(ctypes.Structure):
     """fl_layer_cache_desc."""
     _fields_ = ([(n, ctypes.c_int) for n in ("head_dim", "rotary_dim", "n_axes", "interleaved")]
@@ -103,6 +134,13 @@ SIGNATURES = {
     "fl_rope": (_i, [ctypes.POINTER(RopeDesc), _vp]),
     "fl_kv_write": (_i, [ctypes.POINTER(KvDesc), _vp]),
     "fl_kv_read": (_i, [ctypes.POINTER(KvDesc), _vp]),
+    "fl_attention": (_i, [ctypes.POINTER(AttentionDesc), _vp]),
+    "fl_kv_attend_workspace_size": (_sz, [ctypes.POINTER(KvAttendDesc)]),
+    "fl_kv_attend": (_i, [ctypes.POINTER(KvAttendDesc), _vp, _sz, _vp]),
+    "fl_kv_pages_workspace_size": (_sz, [_i]),
+    "fl_kv_resize": (_i, [ctypes.POINTER(KvPages), _vp, _vp, _vp, _sz, _vp]),
+    "fl_kv_fork": (_i, [ctypes.POINTER(KvPages), _vp, _vp, _vp, _vp, _i, _vp, _sz, _vp]),
+    "fl_kv_compact": (_i, [ctypes.POINTER(KvPages), _vp, _vp, _i, _vp]),
     "fl_layer_create": (_i, [ctypes.POINTER(LayerDesc), ctypes.POINTER(_vp)]),
     "fl_layer_attach_cache": (_i, [_vp, ctypes.POINTER(LayerCacheDesc)]),
     "fl_layer_issue": (_i, [_vp, _i, _vp]),
@@ -608,6 +646,82 @@ def kv_read(k_cache, v_cache, k_scale, v_scale, page_table, cu_rows, start=None,
     (_ops or ops()).kv_read(out_k, out_v, k_cache, v_cache, k_scale, v_scale, page_table, cu_rows, start,
                             None if stream is None else stream.cuda_stream)
     return out_k, out_v
+
+
+def attention(q, k, v, cu_q=None, cu_k=None, causal=True, scale=None, out=None, stream=None):
+    """softmax(scale q k^T) v of a prompt: q [rows_q, heads_q, D], k and v [rows_k, heads_k, D]; returns out like q.
+
+    Query head h reads key head h / (heads_q / heads_k). cu_q, cu_k: int32 [sequences + 1], the rows of packed sequences
+    (cu_k None: as cu_q; both None: one sequence of all rows). Causal: the last rows of a sequence's q and k stand at the
+    same position, row i sees keys 0 .. i + len_k - len_q. A row that sees no key gets zeros; rows of q that
+    belong to no sequence are left as they were in out. scale: 1 / sqrt(D) if None. q, k, v and out may be strided views
+    with contiguous channels. D is a multiple of 8, 128 at most."""
+    if stream is None:
+        r = (_ops or ops()).attention(q, k, v, cu_q, cu_k, causal, scale, out, None)
+    else:
+        r = _on(stream, "attention", (q, k, v, cu_q, cu_k, causal, scale, out), out is None)
+    return _made(r) if _captures else r
+
+
+def kv_attend(q, k_cache, v_cache, k_scale, v_scale, page_table, start, cu_rows=None, tree=None, scale=None, out=None,
+              workspace=None, stream=None):
+    """Attention of new rows q [rows, heads_q, D] over the paged cache that kv_write filled (their own k and v in it
+    too); returns out like q.
+
+    Row i of sequence b (cu_rows, start and page_table as in kv_write) sees every position in front of start[b] and the
+    sequence's new rows up to itself; with tree, bool [rows, drafts], the j-th new row where tree[i, j] is
+    True, itself only if marked: the drafted tokens of a tree see their ancestors. A row that sees nothing gets zeros,
+    rows that belong to no sequence are left as they were in out. scale: 1 / sqrt(D) if None. The workspace
+    (kv_attend_workspace_size bytes) must not be shared by calls or captured graphs that may overlap on the GPU."""
+    if stream is None:
+        return _output((_ops or ops()).kv_attend(q, k_cache, v_cache, k_scale, v_scale, page_table, start, cu_rows, tree,
+                                                 scale, out, workspace, None))
+    return _output(_on(stream, "kv_attend", (q, k_cache, v_cache, k_scale, v_scale, page_table, start, cu_rows, tree, scale,
+                                             out, workspace), out is None or workspace is None))
+
+
+def kv_attend_workspace_size(q, k_cache, page_table, cu_rows=None) -> int:
+    """Bytes of kv_attend's workspace for tensors of these shapes."""
+    pages, size, heads, dim = k_cache.shape
+    d = KvAttendDesc(rows=q.shape[0], heads_q=q.shape[1], heads_k=heads, head_dim=dim, page_size=size, n_pages=pages,
+                     n_seqs=page_table.shape[0], table_pages=page_table.shape[1],
+                     cu_rows=None if cu_rows is None else cu_rows.data_ptr())
+    return int(lib().fl_kv_attend_workspace_size(ctypes.byref(d)))
+
+
+def kv_compact(k_cache, v_cache, k_scale, v_scale, page_table, start, accepted, stream=None):
+    """Moves the rows of accepted drafts to the end of their contexts, codes and scales: the row at position
+    start[b] + accepted[b, j] of sequence b to position start[b] + j. accepted: int32 [sequences, most], ascending,
+    each sequence's ending at its first negative one. The rows behind them stay as they are."""
+    (_ops or ops()).kv_compact(k_cache, v_cache, k_scale, v_scale, page_table, start, accepted,
+                               None if stream is None else stream.cuda_stream)
+
+
+def kv_pages_workspace_size(n_pages: int) -> int:
+    return int(lib().fl_kv_pages_workspace_size(n_pages))
+
+
+def kv_fork(k_cache, v_cache, k_scale, v_scale, page_table, refs, parents, children, lengths, workspace=None, stream=None):
+    """Sequence children[i] becomes a copy of the first lengths[i] positions of sequence parents[i] (all int32 [n]): it
+    releases what it held, shares the pages that lie in those positions as a whole, and gets a copy of a last, partly
+    filled one. refs: int32 [pages], the number of table entries that hold each page (0: free). No sequence may be a child
+    twice, or a child and a parent. Where no page is free the entry is -1 and device_status() raises FL_ERR_RANGE.
+    The workspace (kv_pages_workspace_size bytes) must not be shared by calls or graphs that may overlap."""
+    args = (k_cache, v_cache, k_scale, v_scale, page_table, refs, parents, children, lengths, workspace)
+    r = (_ops or ops()).kv_fork(*args, None) if stream is None else _on(stream, "kv_fork", args, workspace is None)
+    if _captures:
+        _made(r)
+
+
+def kv_resize(page_table, refs, lengths, page_size, workspace=None, stream=None):
+    """Brings every sequence's row of page_table to the pages of its first lengths[b] positions (int32 [sequences]):
+    entries past them are released (-1), missing ones get the lowest free pages, those just released among them; 0 frees
+    a sequence. refs: int32 [pages], the number of table entries that hold each page (0: free), kept up to date.
+    Where no page is free the entry is -1 and device_status() raises FL_ERR_RANGE. Workspace as for kv_fork."""
+    args = (page_table, refs, lengths, page_size, workspace)
+    r = (_ops or ops()).kv_resize(*args, None) if stream is None else _on(stream, "kv_resize", args, workspace is None)
+    if _captures:
+        _made(r)
 
 
 def launch_cache_stats():

@@ -17,6 +17,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <exception>
 
@@ -413,6 +414,199 @@ PyObject* kv(PyObject* const* a, bool write) {
 PyObject* kv_write(PyObject* const* a) { return kv(a, true); }
 PyObject* kv_read(PyObject* const* a) { return kv(a, false); }
 
+// ---------------------------------------------------------------------------
+// attention and the cache's pages
+// ---------------------------------------------------------------------------
+// attention(q, k, v, cu_q, cu_k, causal, scale, out, stream) -> out
+PyObject* attention(PyObject* const* a) {
+    const Call c(a[8]);
+    const at::Tensor *q = tensor(a[0], "q"), *k = tensor(a[1], "k"), *v = tensor(a[2], "v"), *cu_q = tensor(a[3], "cu_q", true),
+                     *cu_k = tensor(a[4], "cu_k", true);
+    const at::ScalarType t = q->scalar_type();
+    fl_attention_desc d = {};
+    d.dtype = dtype_of(*q);
+    const Heads hq(c, *q, "q", t), hk(c, *k, "k", t), hv(c, *v, "v", t);
+    shaped(k, "k", {hk.rows, hk.heads, hq.dim});
+    shaped(v, "v", k->sizes());
+    c.fits(cu_q, "cu_q", at::kInt);
+    c.fits(cu_k, "cu_k", at::kInt);
+    if (cu_k != nullptr && cu_q == nullptr) raise(PyExc_ValueError, "cu_k without cu_q");
+    if (cu_q != nullptr && cu_k == nullptr) {
+        if (hk.rows != hq.rows) raise(PyExc_ValueError, "cu_k must be given: k has %lld rows, q %lld", (long long)hk.rows, (long long)hq.rows);
+        cu_k = cu_q;
+    }
+    d.n_seqs = 1;
+    if (cu_q != nullptr) {
+        if (cu_q->dim() != 1 || cu_q->size(0) < 2)
+            raise(PyExc_ValueError, "cu_q has shape %s, expected [sequences + 1]", shape_of(cu_q->sizes()).c_str());
+        shaped(cu_k, "cu_k", cu_q->sizes());
+        d.n_seqs = size32(cu_q->size(0) - 1, "sequences");
+        d.cu_q = cu_q->data_ptr<int>(), d.cu_k = cu_k->data_ptr<int>();
+    }
+    d.causal = PyObject_IsTrue(a[5]);
+    if (d.causal < 0) throw Raised{};
+    d.scale = a[6] == Py_None ? 1.f / std::sqrt((float)hq.dim) : real(a[6]);
+    at::Tensor own;
+    if (a[7] == Py_None) {
+        own = c.empty(q->sizes(), t);
+        d.out = own.data_ptr(), d.out_row = hq.heads * hq.dim, d.out_head = hq.dim;
+    } else {
+        const at::Tensor* out = tensor(a[7], "out");
+        const Heads h(c, *out, "out", t);
+        shaped(out, "out", q->sizes());
+        d.out = out->data_ptr(), d.out_row = h.row, d.out_head = h.head;
+    }
+    d.rows_q = size32(hq.rows, "rows"), d.rows_k = size32(hk.rows, "rows"), d.heads_q = size32(hq.heads, "heads");
+    d.heads_k = size32(hk.heads, "heads"), d.head_dim = size32(hq.dim, "head_dim");
+    d.q = q->data_ptr(), d.k = k->data_ptr(), d.v = v->data_ptr();
+    d.q_row = hq.row, d.q_head = hq.head, d.k_row = hk.row, d.k_head = hk.head, d.v_row = hv.row, d.v_head = hv.head;
+    check(fl_attention(&d, c.stream));
+    return as_result(a[7], own);
+}
+
+// The codes, scales and page table of a cache.
+struct Cache {
+    const at::Tensor *kc, *vc, *ks, *vs, *table;
+    fl_kv_format format;
+    int64_t seqs, per;
+    Cache(const Call& c, PyObject* const* a)
+        : kc(tensor(a[0], "k_cache")), vc(tensor(a[1], "v_cache")), ks(tensor(a[2], "k_scale")), vs(tensor(a[3], "v_scale")),
+          table(tensor(a[4], "page_table")) {
+        const at::ScalarType kind = kc->scalar_type();
+        if (kind != at::kChar && kind != at::kFloat8_e4m3fn)
+            raise(PyExc_TypeError, "k_cache has dtype %s, expected int8 or float8_e4m3fn", c10::toString(kind));
+        if (kc->dim() != 4)
+            raise(PyExc_ValueError, "k_cache has shape %s, expected [pages, page_size, heads, head_dim]", shape_of(kc->sizes()).c_str());
+        format = kind == at::kChar ? FL_KV_INT8 : FL_KV_E4M3;
+        c.fits(kc, "k_cache", kind);
+        c.fits(vc, "v_cache", kind);
+        c.fits(ks, "k_scale", at::kFloat);
+        c.fits(vs, "v_scale", at::kFloat);
+        shaped(vc, "v_cache", kc->sizes());
+        const auto places = kc->sizes().slice(0, 3);
+        shaped(ks, "k_scale", places);
+        shaped(vs, "v_scale", places);
+        pages(c, table, seqs, per);
+    }
+    static void pages(const Call& c, const at::Tensor* table, int64_t& seqs, int64_t& per) {
+        c.fits(table, "page_table", at::kInt, false);
+        if (table->dim() != 2)
+            raise(PyExc_ValueError, "page_table has shape %s, expected [sequences, pages]", shape_of(table->sizes()).c_str());
+        seqs = table->size(0), per = table->size(1);
+        if (table->stride(1) != 1 && per > 1) raise(PyExc_ValueError, "page_table must be contiguous along a sequence's pages");
+    }
+    fl_kv_pages desc() const {
+        fl_kv_pages d = {};
+        d.heads = size32(kc->size(2), "heads"), d.head_dim = size32(kc->size(3), "head_dim");
+        d.page_size = size32(kc->size(1), "page_size"), d.n_pages = size32(kc->size(0), "pages");
+        d.n_seqs = size32(seqs, "sequences"), d.table_pages = size32(per, "pages of a sequence");
+        d.table_stride = seqs > 1 ? table->stride(0) : per;
+        d.page_table = table->data_ptr<int>();
+        d.k_cache = kc->data_ptr(), d.v_cache = vc->data_ptr();
+        d.k_scale = ks->data_ptr<float>(), d.v_scale = vs->data_ptr<float>();
+        return d;
+    }
+};
+// An int32 tensor of one axis, of n elements.
+int* ints(const Call& c, PyObject* o, const char* name, int64_t n) {
+    const at::Tensor* t = tensor(o, name);
+    c.fits(t, name, at::kInt);
+    shaped(t, name, {n});
+    return t->data_ptr<int>();
+}
+
+// kv_attend(q, k_cache, v_cache, k_scale, v_scale, page_table, start, cu_rows, tree, scale, out, workspace, stream)
+// -> out, workspace made here or None
+PyObject* kv_attend(PyObject* const* a) {
+    const Call c(a[12]);
+    const at::Tensor *q = tensor(a[0], "q"), *cu = tensor(a[7], "cu_rows", true), *tree = tensor(a[8], "tree", true);
+    const Cache cache(c, a + 1);
+    const fl_kv_pages k = cache.desc();
+    const at::ScalarType t = q->scalar_type();
+    fl_kv_attend_desc d = {};
+    d.dtype = dtype_of(*q);
+    const Heads hq(c, *q, "q", t);
+    if (hq.dim != k.head_dim) raise(PyExc_ValueError, "q has heads of %lld channels, the cache of %d", (long long)hq.dim, k.head_dim);
+    d.format = cache.format;
+    d.rows = size32(hq.rows, "rows"), d.heads_q = size32(hq.heads, "heads"), d.heads_k = k.heads, d.head_dim = k.head_dim;
+    d.page_size = k.page_size, d.n_pages = k.n_pages, d.n_seqs = k.n_seqs, d.table_pages = k.table_pages;
+    d.table_stride = k.table_stride, d.page_table = k.page_table;
+    d.start = ints(c, a[6], "start", cache.seqs);
+    if (cu != nullptr) d.cu_rows = ints(c, a[7], "cu_rows", cache.seqs + 1);
+    if (tree != nullptr) {
+        c.fits(tree, "tree", at::kBool, false);
+        if (tree->dim() != 2 || tree->size(0) != hq.rows)
+            raise(PyExc_ValueError, "tree has shape %s, expected [%lld, drafts]", shape_of(tree->sizes()).c_str(), (long long)hq.rows);
+        if (tree->stride(1) != 1 && tree->size(1) > 1) raise(PyExc_ValueError, "tree must be contiguous along a row");
+        d.tree = static_cast<const unsigned char*>(tree->data_ptr());
+        d.tree_cols = size32(tree->size(1), "drafts");
+        d.tree_stride = hq.rows > 1 ? tree->stride(0) : tree->size(1);
+        if (tree->size(1) == 0 && hq.rows > 0)  // (a tensor without elements has no address: no row sees a draft)
+            d.tree = reinterpret_cast<const unsigned char*>(d.start);
+    }
+    d.scale = a[9] == Py_None ? 1.f / std::sqrt((float)hq.dim) : real(a[9]);
+    at::Tensor own;
+    if (a[10] == Py_None) {
+        own = c.empty(q->sizes(), t);
+        d.out = own.data_ptr(), d.out_row = hq.heads * hq.dim, d.out_head = hq.dim;
+    } else {
+        const at::Tensor* out = tensor(a[10], "out");
+        const Heads h(c, *out, "out", t);
+        shaped(out, "out", q->sizes());
+        d.out = out->data_ptr(), d.out_row = h.row, d.out_head = h.head;
+    }
+    d.q = q->data_ptr(), d.q_row = hq.row, d.q_head = hq.head;
+    d.k_cache = k.k_cache, d.v_cache = k.v_cache, d.k_scale = k.k_scale, d.v_scale = k.v_scale;
+    const Workspace ws(c, a[11], fl_kv_attend_workspace_size(&d));
+    check(fl_kv_attend(&d, ws.p, ws.bytes, c.stream));
+    return pair_of(as_result(a[10], own), as_result(Py_None, ws.own));
+}
+
+// kv_compact(k_cache, v_cache, k_scale, v_scale, page_table, start, accepted, stream)
+PyObject* kv_compact(PyObject* const* a) {
+    const Call c(a[7]);
+    const Cache cache(c, a);
+    const at::Tensor* acc = tensor(a[6], "accepted");
+    c.fits(acc, "accepted", at::kInt);
+    if (acc->dim() != 2 || acc->size(0) != cache.seqs)
+        raise(PyExc_ValueError, "accepted has shape %s, expected [%lld, most]", shape_of(acc->sizes()).c_str(), (long long)cache.seqs);
+    const fl_kv_pages d = cache.desc();
+    check(fl_kv_compact(&d, ints(c, a[5], "start", cache.seqs), acc->data_ptr<int>(), size32(acc->size(1), "accepted"), c.stream));
+    Py_RETURN_NONE;
+}
+
+// kv_fork(k_cache, v_cache, k_scale, v_scale, page_table, refs, parents, children, lengths, workspace, stream)
+// -> workspace made here or None
+PyObject* kv_fork(PyObject* const* a) {
+    const Call c(a[10]);
+    const Cache cache(c, a);
+    const fl_kv_pages d = cache.desc();
+    const int64_t n = tensor(a[7], "children")->numel();
+    int* refs = ints(c, a[5], "refs", d.n_pages);
+    const int *parents = ints(c, a[6], "parents", n), *children = ints(c, a[7], "children", n), *lengths = ints(c, a[8], "lengths", n);
+    const Workspace ws(c, a[9], n == 0 ? 0 : fl_kv_pages_workspace_size(d.n_pages));
+    check(fl_kv_fork(&d, refs, parents, children, lengths, size32(n, "children"), ws.p, ws.bytes, c.stream));
+    return as_result(Py_None, ws.own);
+}
+
+// kv_resize(page_table, refs, lengths, page_size, workspace, stream) -> workspace made here or None
+PyObject* kv_resize(PyObject* const* a) {
+    const Call c(a[5]);
+    const at::Tensor *table = tensor(a[0], "page_table"), *refs = tensor(a[1], "refs");
+    int64_t seqs, per;
+    Cache::pages(c, table, seqs, per);
+    fl_kv_pages d = {};
+    c.fits(refs, "refs", at::kInt);
+    if (refs->dim() != 1) raise(PyExc_ValueError, "refs has shape %s, expected [pages]", shape_of(refs->sizes()).c_str());
+    d.n_pages = size32(refs->size(0), "pages"), d.page_size = integer(a[3], "page_size");
+    d.n_seqs = size32(seqs, "sequences"), d.table_pages = size32(per, "pages of a sequence");
+    d.table_stride = seqs > 1 ? table->stride(0) : per;
+    d.page_table = table->data_ptr<int>();
+    const Workspace ws(c, a[4], fl_kv_pages_workspace_size(d.n_pages));
+    check(fl_kv_resize(&d, refs->data_ptr<int>(), ints(c, a[2], "lengths", seqs), ws.p, ws.bytes, c.stream));
+    return as_result(Py_None, ws.own);
+}
+
 // FusedLinError, told once by the package
 PyObject* set_error(PyObject* const* a) {
     Py_INCREF(a[0]);
@@ -440,7 +634,9 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 #define FL_METHOD(NAME, N) {#NAME, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<NAME, N>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FL_METHOD(set_error, 1),      FL_METHOD(w4_quantize, 5), FL_METHOD(w4_gemm, 12),
                          FL_METHOD(w4_swiglu_ffn, 10), FL_METHOD(rope, 10),       FL_METHOD(kv_write, 10),
-                         FL_METHOD(kv_read, 10),       {nullptr, nullptr, 0, nullptr}};
+                         FL_METHOD(kv_read, 10),       FL_METHOD(attention, 9),   FL_METHOD(kv_attend, 13),
+                         FL_METHOD(kv_compact, 8),     FL_METHOD(kv_fork, 11),    FL_METHOD(kv_resize, 6),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,607 @@
+// Attention of a prompt's rows over 16-bit keys and values (fl_attention).
+//
+//   out[i, h] = sum_j p_j v[j] / sum_j p_j,  p_j = 2^(c s_j - m),  s_j = q[i, h] . k[j],  c = scale log2(e)
+//
+// over the keys j that row i of its sequence sees, all of them or, causal, those up
+// to i + len_k - len_q. One pass over the keys with a running maximum m and sum;
+// scores and p never leave the multiprocessor.
+//
+// A CTA takes 256 rows of one sequence and head, as two tiles of 128 rows, over all
+// keys in blocks of 128. Both products are tcgen05 MMAs: S = Q K^T from shared
+// memory into tensor memory; p replaces S there, in 16 bits, and is the A
+// operand of O += P V, whose B operand is the value block as it lies in memory
+// (keys along its rows: an MN-major operand, so nothing is transposed). Tensor memory
+// holds S and O of both tiles, all 512 columns. Two softmax warpgroups, one per tile and one
+// thread per row, work while the tensor core has the other tile's products.
+//
+// The maximum is moved only when a score passes it by 2^8, since only then is O
+// multiplied, in tensor memory, by the softmax warps themselves: p is at most
+// 2^8 otherwise, which fp32 sums and 16-bit p do not mind. Rounded are p (to the dtype)
+// and the output.
+//
+// Blocks that some row does not see as a whole are masked score by score. A value
+// that no row may see must not reach a row times zero (0 inf, 0 NaN): two warps
+// zero the rows behind the last key in such blocks, take what is not finite out
+// of the others and note the first key of each channel where it stood, and the
+// epilogue adds it to the rows that see that key.
+//
+// Every mbarrier wait is bounded as in the other kernels.
+#include <climits>
+
+#include <type_traits>
+
+#include "fl_common.cuh"
+#include "fl_host.h"
+
+namespace fl {
+
+namespace {
+
+constexpr int kRows = 128;               // rows of a tile, keys of a block
+constexpr int kThreads = 384;            // 8 softmax warps, MMA, TMA, 2 for values
+constexpr int kWarpMma = 8, kWarpTma = 9, kWarpFix = 10;
+constexpr float kLazy = 8.f;
+constexpr int kOCol = 256;               // tensor-memory columns: S of tile i at 128 i, O at 256 + 128 i
+
+struct AttnParams {
+    CUtensorMap tm_q, tm_k, tm_v;
+    uint16_t* out;
+    long long o_row, o_head;
+    const int* cu_q;
+    const int* cu_k;
+    int rows_q, rows_k, heads_q, group, head_dim, n_seqs, causal;
+    float c;  // scale * log2(e)
+    int* status;
+    unsigned long long timeout_ns;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// The bounded waits of fl_common.cuh without a call: a function call in a kernel
+// that moves registers between its warps (setmaxnreg) cannot be compiled.
+__device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, int* status, unsigned long long timeout_ns, int where) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 63) == 0) {
+            if (*reinterpret_cast<volatile int*>(status) != 0) return false;
+            if (globaltimer_ns() - t0 > timeout_ns) {
+                atomicCAS(status, 0, kStatusTimeout | (where << 8));
+                return false;
+            }
+        }
+    }
+}
+__device__ __forceinline__ void drain_here(uint32_t bar, uint32_t parity) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < 20000000ull) {}
+}
+
+// Four MMAs of 16 k each by an elected lane of a converged warp, A and B 32 bytes
+// further along their swizzled rows from one to the next.
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 r, x1, x2, x3, l1, l2, l3;\n\t.reg .b64 a0, a1, a2, a3, b0, b1, b2, b3;\n\t"
+        "elect.sync r|p, 0xffffffff;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "add.u32 x1, %1, 2;\n\tadd.u32 x2, %1, 4;\n\tadd.u32 x3, %1, 6;\n\t"
+        "add.u32 l1, %2, 2;\n\tadd.u32 l2, %2, 4;\n\tadd.u32 l3, %2, 6;\n\t"
+        "mov.b64 a0, {%1, %3};\n\tmov.b64 a1, {x1, %3};\n\tmov.b64 a2, {x2, %3};\n\tmov.b64 a3, {x3, %3};\n\t"
+        "mov.b64 b0, {%2, %3};\n\tmov.b64 b1, {l1, %3};\n\tmov.b64 b2, {l2, %3};\n\tmov.b64 b3, {l3, %3};\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a0, b0, %4, q;\n\t"
+        "setp.eq.u32 q, 0, 0;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %4, q;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %4, q;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %4, q;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// The same with A in tensor memory (8 columns of 16 k) and B of 16 keys, 2048 bytes, from one to the next.
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 r, x1, x2, x3, l1, l2, l3;\n\t.reg .b64 b0, b1, b2, b3;\n\t"
+        "elect.sync r|p, 0xffffffff;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "add.u32 x1, %1, 8;\n\tadd.u32 x2, %1, 16;\n\tadd.u32 x3, %1, 24;\n\t"
+        "add.u32 l1, %2, 128;\n\tadd.u32 l2, %2, 256;\n\tadd.u32 l3, %2, 384;\n\t"
+        "mov.b64 b0, {%2, %3};\n\tmov.b64 b1, {l1, %3};\n\tmov.b64 b2, {l2, %3};\n\tmov.b64 b3, {l3, %3};\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b0, %4, q;\n\t"
+        "setp.eq.u32 q, 0, 0;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [x1], b1, %4, q;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [x2], b2, %4, q;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [x3], b3, %4, q;\n\t}" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void commit_elected(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b32 r;\n\telect.sync r|p, 0xffffffff;\n\t"
+        "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
+}
+
+// High half of the descriptor of an MN-major operand with the 128-byte swizzle:
+// rows of 64 elements (128 bytes) along N, one per k; 1024 bytes from eight
+// k to the next, `chunk` bytes from 64 elements of N to the next.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint32_t chunk) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(chunk >> 4) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+constexpr uint32_t kBMajorN = 1u << 16;  // instruction descriptor: B is MN-major
+
+template <int DP>
+struct Layout {
+    static constexpr int kBlock = kRows * DP * 2;   // a tile of q, a block of k or v
+    static constexpr int kSlots = DP == 128 ? 4 : 8;  // blocks of k and v in turn
+    static constexpr int kOffRing = 2 * kBlock;
+    static constexpr int kOffNote = kOffRing + kSlots * kBlock;  // [3][DP] first keys of NaN, inf, -inf; [1] whether any
+    static constexpr int kOffBar = kOffNote + (3 * DP + 4) * 4;
+    static constexpr int kBars = 2 + 4 * kSlots + 2 + 2 + 2 + 2;
+    static constexpr int kOffSlot = kOffBar + kBars * 8;
+    static constexpr int kSmem = kOffSlot + 16 + 1024;
+};
+
+template <int DT>
+__device__ __forceinline__ bool not_finite2(uint32_t w) {
+    constexpr uint32_t kInf = DT == DT_F16 ? 0x7c00u : 0x7f80u;
+    return (w & kInf) == kInf || ((w >> 16) & kInf) == kInf;
+}
+
+// DP: head_dim rounded up to 64 or 128.
+template <int DT, int DP>
+__global__ void __launch_bounds__(kThreads, 1) fl_attention_kernel(const __grid_constant__ AttnParams p) {
+    using Ops = DTypeOps<DT>;
+    using Lay = Layout<DP>;
+    constexpr int NS = Lay::kSlots, CH = DP / 64;  // CH: 64-channel chunks of a block
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw), sbase = (raw + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (sbase - raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t bar0 = sbase + Lay::kOffBar;
+    auto q_full = [&](int i) { return bar0 + 8u * i; };
+    auto full = [&](int s) { return bar0 + 8u * (2 + s); };
+    auto empty = [&](int s) { return bar0 + 8u * (2 + NS + s); };
+    auto s_full = [&](int i) { return bar0 + 8u * (2 + 2 * NS + i); };
+    auto p_full = [&](int i) { return bar0 + 8u * (4 + 2 * NS + i); };
+    auto o_full = [&](int i) { return bar0 + 8u * (6 + 2 * NS + i); };
+    auto v_ready = [&](int s) { return bar0 + 8u * (8 + 2 * NS + s); };
+    auto v_raw = [&](int s) { return bar0 + 8u * (8 + 3 * NS + s); };
+    const uint32_t fixed = bar0 + 8u * (8 + 4 * NS), drain = fixed + 8u;
+    int* const note = reinterpret_cast<int*>(smem + Lay::kOffNote);
+
+    griddep_wait();
+    griddep_launch_dependents();
+
+    // ------------------------------------------------------------ the CTA's rows
+    // (tiles counted from the last: causal rows that see the most keys come first)
+    const int head = blockIdx.x % p.heads_q, index = blockIdx.x / p.heads_q;
+    int q0 = 0, lq = p.rows_q, k0 = 0, lk = p.rows_k, row0;  // the sequence; this CTA's first row in it
+    if (p.cu_q == nullptr) {
+        row0 = ((lq + 2 * kRows - 1) / (2 * kRows) - 1 - index) * (2 * kRows);
+        if (row0 < 0) return;
+    } else {
+        // every warp finds it for itself, 32 sequences at a time from the last
+        int left = index, found = -1, n = 0, first = 0;
+        for (int e = p.n_seqs; e > 0 && found < 0; e -= 32) {
+            const int b = e - 1 - lane;
+            int a = 0, z = 0;
+            if (b >= 0) {
+                a = max(0, min(__ldg(p.cu_q + b), p.rows_q));
+                z = max(a, min(__ldg(p.cu_q + b + 1), p.rows_q));
+            }
+            const int tiles = (z - a + 2 * kRows - 1) / (2 * kRows);
+            int up = tiles;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, up, o);
+                if (lane >= o) up += x;
+            }
+            const uint32_t m = __ballot_sync(0xffffffffu, left < up);
+            if (m != 0) {
+                const int l = __ffs(m) - 1;
+                found = e - 1 - l;
+                q0 = __shfl_sync(0xffffffffu, a, l);
+                lq = __shfl_sync(0xffffffffu, z, l) - q0;
+                n = __shfl_sync(0xffffffffu, tiles, l);
+                first = __shfl_sync(0xffffffffu, up, l) - n;
+            } else {
+                left -= __shfl_sync(0xffffffffu, up, 31);
+            }
+        }
+        if (found < 0) return;
+        row0 = (n - 1 - (left - first)) * (2 * kRows);
+        k0 = max(0, min(__ldg(p.cu_k + found), p.rows_k));
+        lk = max(0, min(__ldg(p.cu_k + found + 1), p.rows_k) - k0);
+    }
+    // row r of the sequence sees keys 0 .. r + shift, and lk - 1 at most
+    const int shift = p.causal ? lk - lq : lk;
+    auto blocks_of = [&](int i) {
+        const int first = row0 + i * kRows, last = min(lq, first + kRows) - 1;
+        if (first >= lq) return 0;
+        const long long end = min((long long)lk, (long long)last + shift + 1);
+        return end <= 0 ? 0 : (int)((end + kRows - 1) / kRows);
+    };
+    const int n0 = blocks_of(0), n1 = blocks_of(1), nb = max(n0, n1);
+    // from this block on some row does not see every key of it, or it is not whole
+    const int edge = (int)(max(0ll, min((long long)lk, (long long)row0 + shift + 1)) / kRows);
+    const int kv_head = head / p.group;
+    // Load number `load` of k and v in turn (k of block j is 2 j, v 2 j + 1) is full
+    // on full(slot), or for values of blocks from `edge` on, which are mended before
+    // they are used, on v_raw(slot) and then v_ready(slot); those barriers see nothing
+    // before. (Values use every other slot.)
+    auto mended = [&](int load) { return (load & 1) != 0 && load >= 2 * edge; };
+    auto parity = [&](int load) { return (uint32_t)((mended(load) ? (load / 2 - edge) / (NS / 2) : load / NS) & 1); };
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full(i), 1);
+            mbar_init(s_full(i), 1);
+            mbar_init(p_full(i), 4);
+            mbar_init(o_full(i), 1);
+        }
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+            mbar_init(v_ready(s), 2);
+            mbar_init(v_raw(s), 1);
+        }
+        mbar_init(fixed, 2);
+        mbar_init(drain, 1);
+        fence_mbar_init();
+    }
+    for (int i = threadIdx.x; i < 3 * DP + 1; i += kThreads) note[i] = i < 3 * DP ? INT_MAX : 0;
+    if (warp == kWarpMma) {
+        tmem_alloc(sbase + Lay::kOffSlot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // (all 512 columns: the base is 0)
+    // 384 threads are launched with 168 registers: the softmax warps take 216, the others 72 (256 * 216 + 128 * 72 = 384 * 168)
+    if (warp >= kWarpMma) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == kWarpTma) {
+        if (lane == 0) {
+            auto load = [&](const CUtensorMap* m, uint32_t dst, uint32_t bar, int h, int row) {
+                mbar_arrive_expect_tx(bar, Lay::kBlock);
+                for (int c = 0; c < CH; ++c) tma_load_3d(dst + c * (kRows * 128), m, bar, 64 * c, h, row);
+            };
+            bool ok = true;
+            int issued = 0;
+            auto next = [&](const CUtensorMap* m, int block) {
+                const int s = issued % NS;
+                if (!(ok = wait_here(empty(s), (uint32_t)((issued / NS) & 1) ^ 1u, p.status, p.timeout_ns, 40))) return;
+                load(m, sbase + Lay::kOffRing + s * Lay::kBlock, mended(issued) ? v_raw(s) : full(s), kv_head, k0 + block * kRows);
+                ++issued;
+            };
+            if (nb > 0) {
+                if (n0 > 0) load(&p.tm_q, sbase, q_full(0), head, q0 + row0);
+                next(&p.tm_k, 0);
+                if (n1 > 0) load(&p.tm_q, sbase + Lay::kBlock, q_full(1), head, q0 + row0 + kRows);
+                for (int j = 0; ok && j < nb; ++j) {
+                    next(&p.tm_v, j);
+                    if (ok && j + 1 < nb) next(&p.tm_k, j + 1);
+                }
+                // every load this thread issued lands before the CTA may exit
+                if (n0 > 0) drain_here(q_full(0), 0);
+                if (n1 > 0) drain_here(q_full(1), 0);
+                for (int i = issued - 1; i >= 0 && i >= issued - NS; --i)
+                    drain_here(mended(i) ? v_raw(i % NS) : full(i % NS), parity(i));
+            }
+        }
+    } else if (warp == kWarpMma) {
+        const uint32_t qk = umma_idesc_f16(Ops::kFormat, kRows, kRows), pv = umma_idesc_f16(Ops::kFormat, kRows, DP) | kBMajorN;
+        const uint64_t kd = sw128_kmajor_desc(sbase), vd = sw128_mnmajor_desc(sbase, kRows * 128);
+        const uint32_t k_hi = (uint32_t)(kd >> 32), v_hi = (uint32_t)(vd >> 32);
+        auto wait = [&](uint32_t bar, uint32_t parity, int where) {
+            const bool ok = __all_sync(0xffffffffu, wait_here(bar, parity, p.status, p.timeout_ns, where));
+            tc_fence_after();
+            return ok;
+        };
+        auto slot_lo = [&](uint64_t d, int load) { return (uint32_t)d + (uint32_t)((Lay::kOffRing + load % NS * Lay::kBlock) >> 4); };
+        auto scores = [&](int i, int load) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+                mma4_ss(128u * i, (uint32_t)kd + (uint32_t)((i * Lay::kBlock + c * kRows * 128) >> 4),
+                        slot_lo(kd, load) + (uint32_t)(c * kRows * 128 >> 4), k_hi, qk, c);
+            commit_elected(s_full(i));
+        };
+        bool ok = true;
+        if (nb > 0) {
+            ok = wait(full(0), 0, 41);
+            for (int i = 0; ok && i < 2; ++i)
+                if (0 < (i ? n1 : n0) && (ok = wait(q_full(i), 0, 42))) scores(i, 0);
+            if (ok) commit_elected(empty(0));
+        }
+        for (int j = 0; ok && j < nb; ++j) {
+            const int lv = 2 * j + 1, lkey = 2 * j + 2;
+            if (!(ok = wait(mended(lv) ? v_ready(lv % NS) : full(lv % NS), parity(lv), 43))) break;
+            if (j + 1 < nb && !(ok = wait(full(lkey % NS), parity(lkey), 45))) break;
+            for (int i = 0; ok && i < 2; ++i) {
+                const int n = i ? n1 : n0;
+                if (j >= n) continue;
+                if (!(ok = wait(p_full(i), (uint32_t)(j & 1), 46))) break;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    mma4_ts(kOCol + 128u * i, 128u * i + 32u * h, slot_lo(vd, lv) + (uint32_t)(h * 64 * 128 >> 4), v_hi, pv,
+                            (uint32_t)(j + h));
+                if (j + 1 < n) scores(i, lkey);
+                else commit_elected(o_full(i));
+            }
+            if (ok) {
+                commit_elected(empty(lv % NS));
+                if (j + 1 < nb) commit_elected(empty(lkey % NS));
+            }
+        }
+        // all MMAs issued by this warp complete before tensor memory is released
+        commit_elected(drain);
+        drain_here(drain, 0);
+    } else {
+        // values of blocks that are not seen whole
+        for (int j = edge; j < nb; ++j) {
+            const int lv = 2 * j + 1, s = lv % NS;
+            if (!__all_sync(0xffffffffu, wait_here(v_raw(s), parity(lv), p.status, p.timeout_ns, 47))) break;
+            const int valid = min(kRows, lk - j * kRows);
+            const uint32_t base = sbase + Lay::kOffRing + s * Lay::kBlock;
+            for (int e = threadIdx.x - kWarpFix * 32; e < kRows * CH * 8; e += 64) {
+                const int r = e / 8 % kRows, c = e / 8 / kRows, at = e & 7;  // row, 64-channel chunk, 16-byte place in its row
+                const uint32_t addr = base + c * (kRows * 128) + r * 128 + at * 16;
+                if (r >= valid) {
+                    st_shared_v4(addr, 0u, 0u, 0u, 0u);
+                    continue;
+                }
+                const uint4 x = ld_shared_v4(addr);
+                uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                if (!(not_finite2<DT>(w[0]) || not_finite2<DT>(w[1]) || not_finite2<DT>(w[2]) || not_finite2<DT>(w[3]))) continue;
+                constexpr uint32_t kInf = DT == DT_F16 ? 0x7c00u : 0x7f80u;
+                const int ch = c * 64 + ((at ^ (r & 7)) << 3);  // (the swizzle: place at holds chunk at ^ (row mod 8))
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t v = (w[i / 2] >> (16 * (i & 1))) & 0xffffu;
+                    if ((v & kInf) != kInf) continue;
+                    const int kind = (v & 0x7fffu) != kInf ? 0 : v >> 15 ? 2 : 1;
+                    atomicMin(&note[kind * DP + ch + i], j * kRows + r);
+                    w[i / 2] &= i & 1 ? 0x0000ffffu : 0xffff0000u;
+                }
+                note[3 * DP] = 1;
+                st_shared_v4(addr, w[0], w[1], w[2], w[3]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(v_ready(s));
+        }
+        if (lane == 0) mbar_arrive(fixed);
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        // ------------------------------------------------------------ softmax: a row per thread
+        const int i = warp >> 2, n = i ? n1 : n0, r = row0 + (int)threadIdx.x;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, s_col = lanes + 128u * i, o_col = lanes + kOCol + 128u * i;
+        const int last = (int)min((long long)lk - 1, (long long)r + shift);  // the last key that the row sees
+        const int warp_last = (int)min((long long)lk - 1, (long long)(r - lane) + shift);
+        const float kNone = __int_as_float(0xff800000);
+        float m = kNone, neg = 0.f;  // the maximum, and minus it (0 where there is none yet)
+        float2 l = make_float2(0.f, 0.f);
+        bool ok = true;
+        for (int j = 0; j < n; ++j) {
+            if (!(ok = __all_sync(0xffffffffu, wait_here(s_full(i), (uint32_t)(j & 1), p.status, p.timeout_ns, 48)))) break;
+            tc_fence_after();
+            float s[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_col + 32u * c, reinterpret_cast<uint32_t(&)[32]>(s[c]));
+            tmem_ld_wait();
+            if (j * kRows + kRows - 1 > warp_last) {
+                const int seen = last - j * kRows;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * c + e > seen) s[c][e] = kNone;
+            }
+            float top = kNone, top1 = kNone;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    top = fmaxf(top, fmaxf(s[c][e], s[c][e + 1]));
+                    top1 = fmaxf(top1, fmaxf(s[c][e + 2], s[c][e + 3]));
+                }
+            top = fmaxf(top, top1) * p.c;
+            const bool over = top > m + kLazy;
+            if (__any_sync(0xffffffffu, over)) {
+                float f = 1.f;
+                if (over) {
+                    f = ex2(m - top);
+                    m = top, neg = -top;
+                }
+                if (j > 0) {
+                    l.x *= f, l.y *= f;
+#pragma unroll
+                    for (int c = 0; c < DP / 32; ++c) {
+                        float o[32];
+                        tmem_ld_32x32b_x32(o_col + 32u * c, reinterpret_cast<uint32_t(&)[32]>(o));
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= f;
+                        tmem_st_32x32b_x32(o_col + 32u * c, reinterpret_cast<uint32_t(&)[32]>(o));
+                    }
+                }
+            }
+            const float2 cc = make_float2(p.c, p.c), nn = make_float2(neg, neg);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t w[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const float* x = &s[2 * h + e / 16][2 * (e % 16)];
+                    const float2 y = ffma2(make_float2(x[0], x[1]), cc, nn);
+                    const float2 v = make_float2(ex2(y.x), ex2(y.y));
+                    l = add2(l, v);
+                    w[e] = Ops::pack(v.x, v.y);
+                }
+                tmem_st_32x32b_x32(s_col + 32u * h, w);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full(i));
+        }
+        if (ok && n > 0) {
+            ok = __all_sync(0xffffffffu, wait_here(o_full(i), 0, p.status, p.timeout_ns, 49));
+            tc_fence_after();
+            if (ok) ok = __all_sync(0xffffffffu, wait_here(fixed, 0, p.status, p.timeout_ns, 50));
+        }
+        if (ok && row0 + i * kRows < lq) {
+            const bool any = n > 0 && *reinterpret_cast<volatile int*>(note + 3 * DP) != 0;
+            const float f = last >= 0 ? 1.f / (l.x + l.y) : 0.f;
+            uint16_t* out = p.out + (long long)(q0 + r) * p.o_row + (long long)head * p.o_head;
+#pragma unroll
+            for (int c = 0; c < DP / 32; ++c) {
+                float o[32];
+                if (n > 0) {
+                    tmem_ld_32x32b_x32(o_col + 32u * c, reinterpret_cast<uint32_t(&)[32]>(o));
+                    tmem_ld_wait();
+                }
+                if (any)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        // what the two warps took out, to the rows that see it
+                        const int ch = 32 * c + e;
+                        if (note[ch] <= last) o[e] += __int_as_float(0x7fffffff);
+                        if (note[DP + ch] <= last) o[e] -= kNone;
+                        if (note[2 * DP + ch] <= last) o[e] += kNone;
+                    }
+                if (r < lq)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        if (32 * c + e >= p.head_dim) continue;
+                        uint4 v = make_uint4(Ops::pack(o[e] * f, o[e + 1] * f), Ops::pack(o[e + 2] * f, o[e + 3] * f),
+                                             Ops::pack(o[e + 4] * f, o[e + 5] * f), Ops::pack(o[e + 6] * f, o[e + 7] * f));
+                        if (last < 0) v = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4*>(out + 32 * c + e) = v;
+                    }
+            }
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == kWarpMma) {
+        tc_fence_after();
+        tmem_dealloc(0u, 512);
+    }
+}
+
+}  // namespace
+
+}  // namespace fl
+
+extern "C" fl_status fl_attention(const fl_attention_desc* d, void* stream) {
+    using namespace fl;
+    using host::fail;
+    const char* what = "fl_attention";
+    if (d == nullptr) return fail(FL_ERR_INVALID_ARG, "%s: null description", what);
+    if (!host::valid_dtype(d->dtype)) return fail(FL_ERR_INVALID_ARG, "%s: bad dtype %d", what, (int)d->dtype);
+    if (d->rows_q < 0 || d->rows_k < 0 || d->heads_q < 1 || d->heads_k < 1 || d->head_dim < 1 || d->n_seqs < 1)
+        return fail(FL_ERR_INVALID_ARG, "%s: sizes must be positive (rows may be 0)", what);
+    if (d->heads_q % d->heads_k != 0)
+        return fail(FL_ERR_INVALID_ARG, "%s: heads_q (%d) must be a multiple of heads_k (%d)", what, d->heads_q, d->heads_k);
+    if (d->head_dim % 8 != 0) return fail(FL_ERR_ALIGNMENT, "%s: head_dim must be a multiple of 8 (%d)", what, d->head_dim);
+    if (d->head_dim > 128) return fail(FL_ERR_UNSUPPORTED, "%s: head_dim above 128 (%d)", what, d->head_dim);
+    if (!(d->scale > 0.f) || d->scale > 1e30f) return fail(FL_ERR_INVALID_ARG, "%s: scale must be positive and finite", what);
+    if ((d->cu_q == nullptr) != (d->cu_k == nullptr))
+        return fail(FL_ERR_INVALID_ARG, "%s: cu_q and cu_k must be given both or neither", what);
+    if (d->cu_q == nullptr && d->n_seqs != 1) return fail(FL_ERR_INVALID_ARG, "%s: cu_q must be given for several sequences", what);
+    if (d->n_seqs > 1 << 30) return fail(FL_ERR_UNSUPPORTED, "%s: more than 2^30 sequences", what);
+    // 256-row tiles at most: every sequence with rows has one that may be short
+    const long long seqs = d->rows_q < d->n_seqs ? d->rows_q : d->n_seqs;
+    const long long tiles = d->cu_q == nullptr ? (d->rows_q + 2ll * kRows - 1) / (2 * kRows) : d->rows_q / (2 * kRows) + seqs;
+    if (tiles * d->heads_q >= (1ll << 31) || d->rows_q > INT_MAX - 4 * kRows || d->rows_k > INT_MAX - 4 * kRows)
+        return fail(FL_ERR_UNSUPPORTED, "%s: too many rows", what);
+    if (d->rows_q == 0) return host::ok();
+    fl_status st;
+    if ((st = host::check_ptr("q", d->q, true)) != FL_OK) return st;
+    if ((st = host::check_ptr("k", d->k, d->rows_k > 0)) != FL_OK) return st;
+    if ((st = host::check_ptr("v", d->v, d->rows_k > 0)) != FL_OK) return st;
+    if ((st = host::check_ptr("out", d->out, true)) != FL_OK) return st;
+    if ((reinterpret_cast<uintptr_t>(d->cu_q) | reinterpret_cast<uintptr_t>(d->cu_k)) & 3u)
+        return fail(FL_ERR_ALIGNMENT, "%s: cu_q and cu_k must be 4-byte aligned", what);
+    struct Side {
+        const char* name;
+        const void* p;
+        int rows, heads;
+        long long row, head;
+    };
+    const Side sides[4] = {{"out", d->out, d->rows_q, d->heads_q, d->out_row, d->out_head},
+                           {"q", d->q, d->rows_q, d->heads_q, d->q_row, d->q_head},
+                           {"k", d->k, d->rows_k, d->heads_k, d->k_row, d->k_head},
+                           {"v", d->v, d->rows_k, d->heads_k, d->v_row, d->v_head}};
+    for (int i = 0; i < 4; ++i) {
+        const Side& s = sides[i];
+        if (s.rows == 0) continue;
+        if ((st = host::check_heads(what, s.name, s.rows, s.heads, d->head_dim, s.row, s.head, i == 0)) != FL_OK) return st;
+        // (a tensor map's strides are below 2^40 bytes)
+        if (s.row >= 1ll << 39 || s.head >= 1ll << 39)
+            return fail(FL_ERR_UNSUPPORTED, "%s: strides of %s above 2^39 elements", what, s.name);
+        if ((s.rows > 1 && s.row == 0) || (s.heads > 1 && s.head == 0))
+            return fail(FL_ERR_UNSUPPORTED, "%s: %s is expanded (a stride of 0)", what, s.name);
+        if (i == 0) continue;
+        if (host::apart(d->out, d->out_row, (d->heads_q - 1) * d->out_head + d->head_dim, s.p, s.row,
+                        (s.heads - 1) * s.head + d->head_dim, 2))
+            continue;
+        if (host::overlap(d->out, host::span_heads(d->rows_q, d->heads_q, d->head_dim, d->out_row, d->out_head), s.p,
+                          host::span_heads(s.rows, s.heads, d->head_dim, s.row, s.head)))
+            return fail(FL_ERR_INVALID_ARG, "%s: out overlaps %s", what, s.name);
+    }
+    for (const int* cu : {d->cu_q, d->cu_k})
+        if (cu != nullptr && host::overlap(d->out, host::span_heads(d->rows_q, d->heads_q, d->head_dim, d->out_row, d->out_head),
+                                           cu, ((size_t)d->n_seqs + 1) * 4))
+            return fail(FL_ERR_INVALID_ARG, "%s: out overlaps cu_q or cu_k", what);
+    host::LaunchContext ctx;
+    if ((st = host::launch_context(static_cast<cudaStream_t>(stream), &ctx)) != FL_OK) return st;
+    AttnParams p = {};
+    CUtensorMap* maps[3] = {&p.tm_q, &p.tm_k, &p.tm_v};
+    for (int i = 0; i < 3; ++i) {
+        Side s = sides[i + 1];
+        if (s.rows == 0) s = sides[1];  // (no keys: never read)
+        if ((st = host::encode_heads(maps[i], d->dtype, s.p, d->head_dim, s.heads, s.rows,
+                                     s.heads > 1 ? s.head : d->head_dim, s.rows > 1 ? s.row : d->head_dim, kRows)) != FL_OK)
+            return st;
+    }
+    p.out = static_cast<uint16_t*>(d->out), p.o_row = d->out_row, p.o_head = d->out_head;
+    p.cu_q = d->cu_q, p.cu_k = d->cu_k, p.rows_q = d->rows_q, p.rows_k = d->rows_k, p.heads_q = d->heads_q;
+    p.group = d->heads_q / d->heads_k, p.head_dim = d->head_dim, p.n_seqs = d->n_seqs, p.causal = d->causal != 0;
+    p.c = d->scale * 1.44269504088896341f;
+    p.status = ctx.status, p.timeout_ns = ctx.timeout_ns;
+    auto go = [&](auto dt, auto dp) -> fl_status {
+        constexpr int DT = decltype(dt)::value, DP = decltype(dp)::value;
+        static std::atomic<unsigned long long> done{0};
+        constexpr int bytes = Layout<DP>::kSmem;
+        static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
+        const cudaError_t e = host::allow_smem(fl_attention_kernel<DT, DP>, bytes, ctx.device, done);
+        if (e != cudaSuccess) return host::fail(FL_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+        return host::launched(host::launch(fl_attention_kernel<DT, DP>, dim3((unsigned)(tiles * d->heads_q)), kThreads, bytes,
+                                           ctx.pdl, static_cast<cudaStream_t>(stream), p),
+                              what);
+    };
+    using std::integral_constant;
+    if (d->dtype == FL_F16)
+        return d->head_dim <= 64 ? go(integral_constant<int, DT_F16>(), integral_constant<int, 64>())
+                                 : go(integral_constant<int, DT_F16>(), integral_constant<int, 128>());
+    return d->head_dim <= 64 ? go(integral_constant<int, DT_BF16>(), integral_constant<int, 64>())
+                             : go(integral_constant<int, DT_BF16>(), integral_constant<int, 128>());
+}

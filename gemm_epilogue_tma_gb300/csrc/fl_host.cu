@@ -962,9 +962,40 @@ fl_status check_ptr(const char* name, const void* p, bool required) { return ::c
 
 bool overlap(const void* a, size_t na, const void* b, size_t nb) { return ::overlap(a, na, b, nb); }
 
+fl_status check_heads(const char* what, const char* name, int rows, int heads, int head_dim, long long row, long long head,
+                      bool output) {
+    if (row % 8 != 0 || head % 8 != 0)
+        return fail(FL_ERR_ALIGNMENT, "%s: strides of %s must be multiples of 8 elements", what, name);
+    if (row < 0 || head < 0) return fail(FL_ERR_INVALID_ARG, "%s: negative stride of %s", what, name);
+    if (!output) return FL_OK;
+    if ((heads > 1 && head < head_dim) || (rows > 1 && row < head_dim))
+        return fail(FL_ERR_INVALID_ARG, "%s: a stride of %s below head_dim", what, name);
+    const long long by_row = (heads - 1) * head + head_dim, by_head = (rows - 1) * row + head_dim;
+    if (rows > 1 && heads > 1 && row < by_row && head < by_head)
+        return fail(FL_ERR_INVALID_ARG, "%s: strides make rows of %s overlap", what, name);
+    return FL_OK;
+}
+
 fl_status encode_matrix(CUtensorMap* m, int dt, int elem_bytes, const void* ptr, uint64_t inner, uint64_t outer,
                         uint32_t box_inner, uint32_t box_outer) {
     return encode_2d(m, dt, ptr, inner, outer, box_inner, box_outer, true, elem_bytes);
+}
+
+fl_status encode_heads(CUtensorMap* m, int dt, const void* ptr, uint64_t dim, uint64_t heads, uint64_t rows,
+                       uint64_t head_stride, uint64_t row_stride, uint32_t box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr) return ::fail(FL_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    cuuint64_t dims[3] = {dim, heads, rows};
+    cuuint64_t strides[2] = {head_stride * 2, row_stride * 2};
+    cuuint32_t box[3] = {64, 1, box_rows};
+    cuuint32_t estr[3] = {1, 1, 1};
+    const CUtensorMapDataType type = dt == FL_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const CUresult r = fn(m, type, 3, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return ::fail(FL_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for a [%llu, %llu, %llu] tensor", (int)r,
+                      (unsigned long long)rows, (unsigned long long)heads, (unsigned long long)dim);
+    return FL_OK;
 }
 
 }  // namespace host

@@ -52,11 +52,28 @@ inline bool apart(const void* a, long long a_row, long long a_width, const void*
 }
 inline bool valid_dtype(int dt) { return dt == FL_F16 || dt == FL_BF16; }
 
+// Strides (elements) of a [rows, heads, head_dim] tensor of 16-bit elements that is
+// read or written in 16-byte vectors: multiples of 8, not negative, and for an
+// output no two elements at one place (a row's heads lie inside its stride, or the
+// rows inside a head's).
+fl_status check_heads(const char* what, const char* name, int rows, int heads, int head_dim, long long row, long long head,
+                      bool output);
+// Its extent in bytes.
+inline size_t span_heads(int rows, int heads, int head_dim, long long row, long long head) {
+    return ((size_t)(rows - 1) * (size_t)row + (size_t)(heads - 1) * (size_t)head + (size_t)head_dim) * 2;
+}
+
 // Tensor map of a row-major [outer, inner] matrix of 16-bit elements (fp16 or
 // bf16 by dt) or of bytes, box {box_inner, box_outer}, 128-byte swizzle, zero
 // fill out of range.
 fl_status encode_matrix(CUtensorMap* m, int dt, int elem_bytes, const void* ptr, uint64_t inner, uint64_t outer,
                         uint32_t box_inner, uint32_t box_outer);
+
+// Tensor map of a [rows, heads, dim] tensor of 16-bit elements with contiguous
+// channels: coordinates (channel, head, row), boxes of 64 channels of box_rows rows
+// of one head, 128-byte swizzle, zero fill out of range.
+fl_status encode_heads(CUtensorMap* m, int dt, const void* ptr, uint64_t dim, uint64_t heads, uint64_t rows,
+                       uint64_t head_stride, uint64_t row_stride, uint32_t box_rows);
 
 // Lets `kern` use `bytes` of dynamic shared memory on `device`; asked of the
 // runtime once per device (`done`: its bit is set).

@@ -518,6 +518,39 @@ typedef struct {
 fl_status fl_rope(const fl_rope_desc* desc, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Attention
+ * ------------------------------------------------------------------------
+ * out = softmax(scale q k^T) v of a prompt's rows over 16-bit keys and values.
+ *   q, out: [rows_q, heads_q, head_dim], k, v: [rows_k, heads_k, head_dim] at the row
+ *   and head strides given (elements, multiples of 8; channels are contiguous), 16-byte
+ *   aligned; query head h reads key head h / (heads_q / heads_k). out overlaps no
+ *   other tensor (the columns of one matrix beside theirs do not).
+ *   cu_q, cu_k: device, [n_seqs + 1] int32, not decreasing: sequence b is rows
+ *   cu_q[b] .. cu_q[b + 1] - 1 of q and out, cu_k likewise of k and v; both NULL: one
+ *   sequence of all rows. Rows of q that belong to no sequence are left as
+ *   they were in out; entries past the row counts are taken as those.
+ *   causal: the last rows of a sequence's q and k stand at the same position: row i
+ *   sees keys 0 .. i + len_k - len_q. Otherwise all of its sequence.
+ * A row that sees no key gets zeros. Keys and values that a row does not see do not
+ * reach it, whatever they hold. Scores, maxima and sums are fp32; rounded to the
+ * dtype are the weights and the output. head_dim is a multiple of 8, 8 .. 128;
+ * scale is positive. rows_q 0 does nothing.
+ */
+typedef struct {
+    fl_dtype dtype;
+    int rows_q, rows_k, heads_q, heads_k, head_dim, n_seqs, causal;
+    float scale;
+    const int* cu_q;
+    const int* cu_k;
+    const void* q;
+    const void* k;
+    const void* v;
+    void* out;
+    long long q_row, q_head, k_row, k_head, v_row, v_head, out_row, out_head;
+} fl_attention_desc;
+fl_status fl_attention(const fl_attention_desc* desc, void* stream);
+
+/* ------------------------------------------------------------------------
  * Paged 8-bit key/value cache
  * ------------------------------------------------------------------------
  * k_cache, v_cache: [n_pages, page_size, heads, head_dim] codes, one byte each;
@@ -574,6 +607,98 @@ typedef struct {
 } fl_kv_desc;
 fl_status fl_kv_write(const fl_kv_desc* desc, void* stream);
 fl_status fl_kv_read(const fl_kv_desc* desc, void* stream);
+
+/*
+ * Attention of new rows over the cache: out = softmax(scale q k^T) v, where row i of
+ * sequence b (cu_rows, start and page_table as above; start is required) stands at
+ * position start[b] + i - cu_rows[b], and its k and v are in the cache already. It
+ * sees every position of its sequence from 0 to start[b] - 1, and of the
+ * sequence's new rows those up to itself, or with `tree` the j-th new row where
+ * tree[i * tree_stride + j] is not 0, j < tree_cols (device, one byte each; itself
+ * only if marked): the drafted tokens of a tree see their ancestors. A row that
+ * sees nothing gets zeros. Positions without a page are not seen, and
+ * reported as above; rows that belong to no sequence are left as they were.
+ *   q, out: [rows, heads_q, head_dim] at the strides given, as k and v above; query
+ *   head h reads key head h / (heads_q / heads_k). out overlaps no other tensor.
+ * Scores, maxima and sums are fp32; the codes are multiplied as they are. Rounded
+ * are the weights, to 11 bits, and the output. scale is positive.
+ * workspace: fl_kv_attend_workspace_size(desc) bytes (sizes, cu_rows NULL or not; up
+ * to 11 MB, 0 for short tables, and then NULL is accepted), 16-byte aligned, the
+ * call's own until its kernels are done.
+ */
+typedef struct {
+    fl_dtype dtype;
+    fl_kv_format format;
+    int rows, heads_q, heads_k, head_dim, page_size, n_pages, n_seqs, table_pages, tree_cols;
+    float scale;
+    long long table_stride, tree_stride;
+    const int* page_table;
+    const int* cu_rows;
+    const int* start;
+    const unsigned char* tree; /* or NULL */
+    const void* q;
+    void* out;
+    long long q_row, q_head, out_row, out_head;
+    const void* k_cache;
+    const void* v_cache;
+    const float* k_scale;
+    const float* v_scale;
+} fl_kv_attend_desc;
+size_t fl_kv_attend_workspace_size(const fl_kv_attend_desc* desc);
+fl_status fl_kv_attend(const fl_kv_attend_desc* desc, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The pages of a cache. Tables and counts are on the GPU and change there, in stream
+ * order, so that a step that takes pages, writes, attends, keeps what was accepted and
+ * gives pages back can be one graph.
+ *   page_table: as above, but written: entry j of sequence b holds the page with
+ *   positions j * page_size on, or none (negative, or n_pages and above).
+ *   refs: device, [n_pages] int32: how many table entries hold each page; 0: free.
+ *   Tables and counts agree when a call begins.
+ * Free pages are given out in ascending order, to entries in ascending order
+ * (sequence or child, then place in its table). Entries left without a page because
+ * none is free hold -1, and so does what a length past table_pages * page_size would
+ * have needed: fl_device_status() then reports FL_ERR_RANGE.
+ *
+ * fl_kv_resize: each sequence then holds the pages of its first lengths[b] positions
+ * (device, [n_seqs] int32; below 0: as 0) and no others: pages it has stay where
+ * they are, entries past them release theirs (refs - 1) and become -1, missing ones
+ * get free pages, those just released among them. 0 frees a sequence.
+ *
+ * fl_kv_fork: for i < n (children, parents, lengths: device, [n] int32) sequence
+ * children[i] becomes a copy of the first lengths[i] positions of sequence
+ * parents[i]: what it held is released; pages that lie in those positions as a whole
+ * are shared (refs + 1); the rows of a last, partly filled one are copied to a free page. No
+ * sequence is a child twice, or a child and a parent, in one call; what one then
+ * holds is not defined. A shared page must not be written: rows that are appended
+ * behind the length go to pages of the sequence's own.
+ *
+ * fl_kv_compact: of the rows drafted at positions start[b] + 0, 1, .. of each
+ * sequence those in accepted (device, [n_seqs][most] int32: ascending, none twice, ending at the
+ * first negative one) move to positions start[b] + 0, 1, .., codes and scales. The
+ * rows behind them stay as they are. A row whose position has no page is left out and
+ * reported as above.
+ * The places that a call moves rows to or from belong to one sequence each.
+ *
+ * fl_kv_resize takes page_table and the sizes of it alone; heads, head_dim and the
+ * caches may be 0 and NULL there. workspace: fl_kv_pages_workspace_size(n_pages) bytes,
+ * 16-byte aligned, the call's own until its kernels are done.
+ */
+typedef struct {
+    int heads, head_dim, page_size, n_pages, n_seqs, table_pages;
+    long long table_stride;
+    int* page_table;
+    void* k_cache;
+    void* v_cache;
+    float* k_scale;
+    float* v_scale;
+} fl_kv_pages;
+size_t fl_kv_pages_workspace_size(int n_pages);
+fl_status fl_kv_resize(const fl_kv_pages* cache, int* refs, const int* lengths, void* workspace, size_t workspace_bytes,
+                       void* stream);
+fl_status fl_kv_fork(const fl_kv_pages* cache, int* refs, const int* parents, const int* children, const int* lengths,
+                     int n, void* workspace, size_t workspace_bytes, void* stream);
+fl_status fl_kv_compact(const fl_kv_pages* cache, const int* start, const int* accepted, int most, void* stream);
 
 /*
  * Rotary positions and the cache as part of a prepared layer: half 0 of

@@ -10,3 +10,6 @@ from .fusedlin_oracle import (  # noqa: F401
 from .serving_oracle import (  # noqa: F401
     e4m3_round, kv_places, kv_quantize, rope, w4_pack, w4_quantize, w4_weight,
 )
+from .attention_oracle import (  # noqa: F401
+    attention, causal, kv_attend, kv_compact, kv_fork, kv_resize, softmax_rows,
+)
