@@ -998,6 +998,24 @@ fl_status encode_heads(CUtensorMap* m, int dt, const void* ptr, uint64_t dim, ui
     return FL_OK;
 }
 
+fl_status encode_pages(CUtensorMap* m, const void* ptr, uint64_t dim, uint64_t heads, uint64_t page_size, uint64_t pages,
+                       uint32_t box_channels, uint32_t box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr) return ::fail(FL_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    cuuint64_t dims[4] = {dim, heads, page_size, pages};
+    cuuint64_t strides[3] = {dim, dim * heads, dim * heads * page_size};
+    cuuint32_t box[4] = {box_channels, 1, box_rows, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          box_channels == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return ::fail(FL_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for a cache of %llu pages of [%llu, %llu, %llu]", (int)r,
+                      (unsigned long long)pages, (unsigned long long)page_size, (unsigned long long)heads, (unsigned long long)dim);
+    return FL_OK;
+}
+
 }  // namespace host
 }  // namespace fl
 

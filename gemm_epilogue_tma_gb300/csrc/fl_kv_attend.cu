@@ -14,20 +14,23 @@
 //
 // The cache is read once and nothing is written but the output, so HBM bounds it:
 // 2 head_dim + 8 bytes per position and key head, for all rows of a sequence
-// and all query heads of the group, which are the 16 or 32 rows of one MMA tile.
-// A warp takes 16 positions a step through a ring of its own in shared memory
-// (cp.async, no barriers), converts the codes to MMA fragments in registers (channels
-// and positions permuted so that 16-byte loads give whole fragments), and keeps
-// its own maxima, sums and outputs; the warps of a CTA are joined in shared
-// memory at the end.
+// and all query heads of the group. Keys are the rows of the first MMA, 16 positions,
+// and channels those of the second, O^T = V^T P^T; the rows of q are its columns, in
+// tiles of eight, so that a decode step of a group of four or eight heads pads
+// little, and P^T, 16 positions by 8, is the first product's result turned by
+// movmatrix. A warp takes 16 positions a step through a ring of its own in shared memory
+// (TMA boxes of the rows that lie in one page, no CTA barriers), converts the codes
+// to MMA fragments in registers (channels permuted so that 16-byte loads give
+// whole fragments), and keeps its own maxima, sums and outputs; the warps of a CTA
+// are joined in shared memory at the end.
 //
-// Long contexts are split: with T the number of 128-position tiles of all
-// sequences and heads, pieces of L = max(kLeast, T / kPieces) tiles at most, each to
-// a CTA, so that sequences of any lengths fill the GPU evenly. Every CTA finds
-// its piece from the lengths, which only the GPU knows. Pieces of a split
-// sequence are joined by a second launch, in order.
+// Long contexts are split into pieces of L tiles of 128 positions at most. The CTAs
+// are persistent and take every gridDim-th piece. L is the one of sixteen that makes the
+// rounds of CTAs shortest; every CTA finds it, and its pieces, from the lengths, which
+// only the GPU knows. Pieces of a split sequence are joined by a second launch, in order.
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "fl_common.cuh"
@@ -41,12 +44,15 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 16;               // positions of a warp's step
 constexpr int kTile = kStep * kWarps;   // positions of a tile
-constexpr int kPieces = 304;            // pieces aimed at: two CTAs on each of 152 multiprocessors
+constexpr int kResident = 304;          // CTAs at work at once: two on each of 152 multiprocessors
 constexpr int kLeast = 2;               // tiles of a piece at least
-constexpr int kSlots = 2 * kPieces;     // pieces of split sequences at most (each has more than L / 2 tiles)
+constexpr int kSlots = 2 * kResident;   // pieces of split sequences at most: L is T / kResident at least, and each has more than L / 2 tiles
+constexpr int kUnits = kSlots / 2;      // row blocks and heads of split sequences at most
+constexpr int kStart = 3, kJoin = 3;    // tiles that a piece's start and end, and the second launch, take as long as
 constexpr float kLazy = 8.f;            // a maximum is moved once it is exceeded by 2^8
 
 struct AttendParams {
+    CUtensorMap tm[2];  // k_cache, v_cache: boxes of 64 or 128 channels of box_rows positions of one head and page
     const uint16_t* q;
     uint16_t* out;
     long long q_row, q_head, o_row, o_head;
@@ -59,11 +65,26 @@ struct AttendParams {
     long long table_stride, tree_stride;
     int tree_cols;
     int rows, heads, group, head_dim, page_size, page_shift, n_pages, n_seqs, table_pages;
-    int vec8;          // 8-byte copies (head_dim not a multiple of 16)
+    int box_log;       // log2 of box_rows
     float log2_scale;  // scale * log2(e)
-    float* part;       // [kSlots][M][HD] sums, then [kSlots][M][4]: both maxima and the sum of weights
+    float* part;       // [kSlots][M][HD] sums, [kSlots][M][4] maxima, sum of weights, whether a position was seen; Units
     int* range;
+    int* status;
+    unsigned long long timeout_ns;
 };
+
+// What the second launch joins.
+struct Unit {
+    int row0, n, first, head, pieces, slot, step, unused;  // the sequence's rows; the block's first row; slots from one piece to the next
+};
+struct Units {
+    int count, unused[7];
+    Unit unit[kUnits];
+};
+template <int HD, int QT>
+__device__ __forceinline__ Units* units_of(const AttendParams& p) {
+    return reinterpret_cast<Units*>(p.part + (long long)kSlots * 8 * QT * (HD + 4));
+}
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -83,49 +104,51 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two codes as fp16. int8: in bytes 0 and 2 of x (the others are ignored):
-// 1024 + 128 + code in the mantissa, less 1152. e4m3: in bytes 1 and 3, the value
-// times 2^-8: exponent and mantissa moved to their places.
+// Two codes as fp16. int8: in bytes 0 and 2 of x (the others are ignored): 1024 + 128 +
+// code in the mantissa, less 1152. e4m3: in the low 16 bits, by the conversion
+// instruction (moving the bits takes three logical operations, which are issued at half rate:
+// 16 contexts of 3750 positions 44 -> 38 us).
 template <int FMT>
 __device__ __forceinline__ uint32_t widen(uint32_t x) {
+    uint32_t r;
     if constexpr (FMT == FL_KV_INT8) {
         const uint32_t m = (x & 0x00ff00ffu) ^ 0x64806480u;
-        uint32_t r;
         asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(0x64806480u));
-        return r;
     } else {
-        return (x & 0x80008000u) | ((x >> 1) & 0x3f803f80u);
+        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(x));
     }
+    return r;
 }
-// Codes 0 and 2, and 1 and 3, of a word.
+// The four codes of a word in two pairs, the first product's order of channels: int8 0 and 2, 1
+// and 3; e4m3 0 and 1, 2 and 3. (q is laid out to match: kPair.)
 template <int FMT>
-__device__ __forceinline__ void widen_word(uint32_t w, uint32_t& even, uint32_t& odd) {
-    even = widen<FMT>(FMT == FL_KV_INT8 ? w : w << 8);
-    odd = widen<FMT>(FMT == FL_KV_INT8 ? w >> 8 : w);
+__device__ __forceinline__ void widen_word(uint32_t w, uint32_t& first, uint32_t& second) {
+    first = widen<FMT>(w);
+    second = widen<FMT>(FMT == FL_KV_INT8 ? w >> 8 : w >> 16);
 }
+template <int FMT>
+constexpr int kPair = FMT == FL_KV_INT8 ? 2 : 1;  // distance of a pair's channels
 // Code b of word lo and of word hi.
 template <int FMT>
 __device__ __forceinline__ uint32_t widen_pair(uint32_t lo, uint32_t hi, int b) {
-    const uint32_t sel = FMT == FL_KV_INT8 ? (uint32_t)(b | (4 + b) << 8) : (uint32_t)(b << 4 | (4 + b) << 12);
-    return widen<FMT>(__byte_perm(lo, hi, FMT == FL_KV_INT8 ? (uint32_t)(b | b << 4 | (4 + b) << 8 | (4 + b) << 12) : sel));
+    return widen<FMT>(__byte_perm(lo, hi, (uint32_t)(FMT == FL_KV_INT8 ? b | b << 4 | (4 + b) << 8 | (4 + b) << 12 : b | (4 + b) << 4)));
 }
-// the value of an e4m3 code times 2^-8 stands in the fragments
-template <int FMT>
-constexpr float kCodeUnit = FMT == FL_KV_INT8 ? 1.f : 256.f;
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+// Arrives on the barrier when this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z, int w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
 }
 
 // A sequence's share of the work.
@@ -154,550 +177,679 @@ __device__ __forceinline__ Seq seq_of(const AttendParams& p, int b, int M) {
 
 struct Piece {
     int seq, block, head, k, pieces, slot;  // piece k of `pieces`; its place among the pieces of split sequences
+    int units;                              // row blocks and heads of split sequences in front of this one's
 };
 
-// The index-th piece (SPLIT: the index-th row block and head of a split
-// sequence, with its first piece's slot); seq -1 if there are fewer. All threads
-// of the CTA, which holds THREADS of them. Order: sequence, piece, row block, head.
-template <bool SPLIT, int THREADS>
-__device__ __forceinline__ Piece find_piece(const AttendParams& p, int index, int M) {
-    __shared__ unsigned long long warp_sum[THREADS / 32];
-    __shared__ Piece found;
-    const int per = (p.n_seqs + THREADS - 1) / THREADS;
-    const int b0 = min(p.n_seqs, (int)threadIdx.x * per), b1 = min(p.n_seqs, b0 + per);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    unsigned long long t = 0;
-    for (int b = b0; b < b1; ++b) {
-        const Seq s = seq_of(p, b, M);
-        t += (unsigned long long)s.tiles * s.blocks * p.heads;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    if (lane == 0) warp_sum[warp] = t;
-    if (threadIdx.x == 0) found.seq = -1;
-    __syncthreads();
-    t = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) t += warp_sum[w];
-    const int L = (int)max((unsigned long long)kLeast, (t + kPieces - 1) / kPieces);
-    __syncthreads();
-    // pieces in the low half, slots in the high one, of this thread's sequences; then those in front of them
-    auto count = [&](const Seq& s) {
-        const unsigned long long n = (unsigned long long)s.blocks * p.heads * max(1, (s.tiles + L - 1) / L);
-        return s.tiles > L ? n << 32 | n : n;
-    };
-    unsigned long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += count(seq_of(p, b, M));
-    unsigned long long before = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long up = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += up;
-    }
-    if (lane == 31) warp_sum[warp] = before;
-    before -= mine;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) before += warp_sum[w];
-    if (!SPLIT) {
-        if ((uint32_t)before <= (uint32_t)index && (uint32_t)index < (uint32_t)(before + mine))
-            for (int b = b0; b < b1; ++b) {
-                const Seq s = seq_of(p, b, M);
-                const unsigned long long c = count(s);
-                if ((uint32_t)index < (uint32_t)(before + c)) {
-                    const uint32_t rem = index - (uint32_t)before, units = (uint32_t)s.blocks * p.heads;
-                    const uint32_t u = rem % units;
-                    found = Piece{b, (int)(u / p.heads), (int)(u % p.heads), (int)(rem / units), max(1, (s.tiles + L - 1) / L),
-                                  (int)(before >> 32) + (int)rem};
-                    break;
-                }
-                before += c;
-            }
-    } else {
-        // (rows of a split sequence are joined unit by unit: its first piece's slots)
-        unsigned long long units = 0;
+// Candidates of L: T / kResident times these, / 8, and no split at all. (More than 8
+// makes room for the pieces that lengths which are no multiples of L leave over.)
+constexpr int kCandidates = 5;
+__device__ constexpr int kTimes[kCandidates + 1] = {8, 9, 11, 14, 20, 0};
+constexpr uint32_t kWhole = 1u << 30;
+
+// The pieces of all sequences, counted by all threads of a CTA. Order: sequence,
+// piece, row block, head, so that CTAs next to one another read the heads of the same positions.
+struct Pieces {
+    const AttendParams& p;
+    int M, per, b0, b1;      // this thread's sequences
+    Seq only;                // with one sequence to a thread it is read once
+    uint32_t L;
+    int W;                   // warps to a piece: 8, or less where no sequence is split
+    uint32_t fn, fs, fu, n;  // pieces, slots and units in front of this thread's sequences; its pieces
+    uint32_t units;          // of all split sequences
+    Piece (*found)[kWarps];  // [2], in shared memory: the pieces of this round and the next, and their sequences
+    Seq (*of)[kWarps];
+
+    __device__ __forceinline__ Seq seq(int b) const { return per == 1 ? only : seq_of(p, b, M); }
+    __device__ __forceinline__ uint32_t pieces(const Seq& s) const { return max(1u, ((uint32_t)s.tiles + L - 1) / L); }
+
+    // few: whether pieces may be given to fewer warps than a CTA has
+    __device__ __forceinline__ Pieces(const AttendParams& params, int rows, bool few) : p(params), M(rows) {
+        __shared__ Piece pieces_at[2][kWarps];
+        __shared__ Seq seqs_at[2][kWarps];
+        found = pieces_at, of = seqs_at;
+        if (threadIdx.x < kWarps) found[0][threadIdx.x].seq = -1;
+        __shared__ unsigned long long sum_t[kWarps];
+        __shared__ uint32_t top_t[kWarps], pieces_of[kWarps][kCandidates + 1];
+        __shared__ uint32_t sum_n[kWarps], sum_s[kWarps], sum_u[kWarps];
+        per = (p.n_seqs + kThreads - 1) / kThreads;
+        b0 = min(p.n_seqs, (int)threadIdx.x * per), b1 = min(p.n_seqs, b0 + per);
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        unsigned long long t = 0;
+        uint32_t top = 0;
+        only.blocks = only.tiles = 0;
         for (int b = b0; b < b1; ++b) {
-            const Seq s = seq_of(p, b, M);
-            if (s.tiles > L) units += (unsigned long long)s.blocks * p.heads;
+            only = seq_of(p, b, M);
+            t += (unsigned long long)only.tiles * only.blocks * p.heads;
+            if (only.blocks > 0) top = max(top, (uint32_t)only.tiles);
         }
-        unsigned long long first = units;
+        t = __reduce_add_sync(0xffffffffu, (uint32_t)t & 0xffffffu) +
+            ((unsigned long long)__reduce_add_sync(0xffffffffu, (uint32_t)(t >> 24)) << 24);
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (lane == 0) sum_t[warp] = t, top_t[warp] = top;
+        __syncthreads();
+        t = 0, top = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) t += sum_t[w], top = max(top, top_t[w]);
+        L = kWhole;
+        if (top > kLeast) {
+            // what each candidate costs: the rounds, times their longest piece and a start
+            uint32_t at[kCandidates + 1], k[kCandidates + 1];
+#pragma unroll
+            for (int c = 0; c <= kCandidates; ++c) {
+                const unsigned long long want = (t * kTimes[c] + 8 * kResident - 1) / (8 * kResident);
+                at[c] = c == kCandidates ? kWhole : (uint32_t)max((unsigned long long)kLeast, min(want, (unsigned long long)kWhole));
+                k[c] = 0;
+                const float inv = 1.f / (float)at[c];
+                for (int b = b0; b < b1; ++b) {
+                    const Seq s = seq(b);
+                    // (an estimate: the quotient is not exact next to a whole number)
+                    k[c] += (uint32_t)s.blocks * p.heads * (uint32_t)fmaxf(1.f, ceilf((float)s.tiles * inv));
+                }
+            }
+#pragma unroll
+            for (int c = 0; c <= kCandidates; ++c) k[c] = __reduce_add_sync(0xffffffffu, k[c]);
+            if (lane == 0) {
+#pragma unroll
+                for (int c = 0; c <= kCandidates; ++c) pieces_of[warp][c] = k[c];
+            }
+            __syncthreads();
+            uint32_t best = 0xffffffffu;
+#pragma unroll
+            for (int c = 0; c <= kCandidates; ++c) {
+                uint32_t all = 0;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) all += pieces_of[w][c];
+                const uint32_t cost = (all + kResident - 1) / kResident * (min(at[c], top) + kStart) + (at[c] < top ? kJoin : 0);
+                if (cost < best) best = cost, L = at[c];
+            }
+            if (L >= top) L = kWhole;
+        }
+        uint32_t sl = 0, un = 0;
+        n = 0;
+        for (int b = b0; b < b1; ++b) {
+            const Seq s = seq(b);
+            const uint32_t u = (uint32_t)s.blocks * p.heads, k = pieces(s);
+            n += u * k;
+            if (k > 1) sl += u * k, un += u;
+        }
+        fn = n, fs = sl, fu = un;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const unsigned long long up = __shfl_up_sync(0xffffffffu, first, o);
-            if (lane >= o) first += up;
+            const uint32_t a = __shfl_up_sync(0xffffffffu, fn, o), c = __shfl_up_sync(0xffffffffu, fs, o), d = __shfl_up_sync(0xffffffffu, fu, o);
+            if (lane >= o) fn += a, fs += c, fu += d;
         }
+        if (lane == 31) sum_n[warp] = fn, sum_s[warp] = fs, sum_u[warp] = fu;
+        fn -= n, fs -= sl, fu -= un;
         __syncthreads();
-        if (lane == 31) warp_sum[warp] = first;
-        first -= units;
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) first += warp_sum[w];
-        if ((unsigned long long)index >= first && (unsigned long long)index < first + units)
-            for (int b = b0; b < b1; ++b) {
-                const Seq s = seq_of(p, b, M);
-                const unsigned long long c = count(s);
-                if (s.tiles > L) {
-                    const unsigned long long n = (unsigned long long)s.blocks * p.heads;
-                    if ((unsigned long long)index < first + n) {
-                        const int u = (int)(index - first);
-                        found = Piece{b, u / p.heads, u % p.heads, 0, (s.tiles + L - 1) / L, (int)(before >> 32) + u};
-                        break;
-                    }
-                    first += n;
-                }
-                before += c;
-            }
+        units = 0;
+        uint32_t all = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) fn += sum_n[w], fs += sum_s[w], fu += sum_u[w];
+            units += sum_u[w], all += sum_n[w];
+        }
+        W = kWarps;
+        if (few && L == kWhole) {
+            // of 8, 4, 2 and 1 warps to a piece, the least rounds * (steps, a start and the joining)
+            const uint32_t w = kWarps >> (lane & 3), at_once = kResident * (kWarps / w);
+            const uint32_t c = (all + at_once - 1) / at_once * (top * (kWarps / w) + kStart + (3 - (lane & 3)));
+            const int who = __ffs(__ballot_sync(0xffffffffu, c == __reduce_min_sync(0xffffffffu, c))) - 1;
+            W = kWarps >> (who & 3);
+        }
     }
-    __syncthreads();
-    return found;
-}
+
+    // This warp's piece of the CTA's turn-th round, and its sequence: seq -1 if there is
+    // none; false if the CTA has none at all. (One barrier: the next round's writes
+    // come after the barrier of this one's readers, two rounds apart.)
+    __device__ __forceinline__ bool find(uint32_t turn, Piece& piece, Seq& s) const {
+        const int per_cta = kWarps / W;
+        const uint32_t first = (turn * gridDim.x + blockIdx.x) * per_cta;
+        bool any = false;
+        // (cleared a round ahead, so that this round's writers find it so)
+        if (threadIdx.x < kWarps) found[(turn + 1) & 1][threadIdx.x].seq = -1;
+        if (fn < first + per_cta && first < fn + n) {
+            uint32_t f = fn, fslots = fs, funits = fu;
+            for (int b = b0; b < b1 && f < first + per_cta; ++b) {
+                const Seq sq = seq(b);
+                const uint32_t u = (uint32_t)sq.blocks * p.heads, k = pieces(sq);
+                for (uint32_t index = max(f, first); index < min(f + u * k, first + per_cta); ++index) {
+                    const uint32_t rem = index - f, w = rem % u;
+                    found[turn & 1][index - first] = Piece{b, (int)(w / p.heads), (int)(w % p.heads), (int)(rem / u), (int)k, (int)(fslots + rem), (int)(funits + w)};
+                    of[turn & 1][index - first] = sq;
+                    any = true;
+                }
+                f += u * k;
+                if (k > 1) fslots += u * k, funits += u;
+            }
+        }
+        if (!__syncthreads_or(any)) return false;
+        const int at = (threadIdx.x >> 5) / W;
+        piece = found[turn & 1][at];
+        s = of[turn & 1][at];
+        return true;
+    }
+};
 
 // What the sums of a row are multiplied by, 0 (and .y) for one that sees nothing.
 // (a = -inf where all scores are: 0 / 0)
 template <int FMT>
 __device__ __forceinline__ float2 finish(float a, float b, float sum, float any) {
-    return any == 0.f ? make_float2(0.f, 1.f) : make_float2(exp2f(b - a) * kCodeUnit<FMT> / sum, 0.f);
+    return any == 0.f ? make_float2(0.f, 1.f) : make_float2(exp2f(b - a) / sum, 0.f);
 }
-// Channels ch .. ch + 7 of row r (of q, and head of the group) of a sequence.
-template <typename Ops>
-__device__ __forceinline__ void store_row(const AttendParams& p, const Seq& s, int head, int r, int ch, const float (&v)[8], float2 f) {
+// Row r (of q, and head of the group) of a sequence in the output.
+__device__ __forceinline__ uint16_t* row_at(const AttendParams& p, int row0, int head, int r) {
     const int i = r / p.group, h = r - i * p.group;
-    uint16_t* d = p.out + (long long)(s.row0 + i) * p.o_row + (long long)(head * p.group + h) * p.o_head + ch;
-    uint4 y = make_uint4(Ops::pack(v[0] * f.x, v[1] * f.x), Ops::pack(v[2] * f.x, v[3] * f.x), Ops::pack(v[4] * f.x, v[5] * f.x),
-                         Ops::pack(v[6] * f.x, v[7] * f.x));
-    if (f.y != 0.f) y = make_uint4(0u, 0u, 0u, 0u);
-    *reinterpret_cast<uint4*>(d) = y;
+    return p.out + (long long)(row0 + i) * p.o_row + (long long)(head * p.group + h) * p.o_head;
 }
 
-// 16-byte chunk c of row r of a ring stage: the places that the lanes of one
-// load touch lie in different banks.
+// 16-byte chunk c of row r of a stage's k or v, as TMA lays it out: rows of 64 or
+// 128 bytes with the swizzle of that width, 256 channels as two such blocks.
 template <int HD>
-__device__ __forceinline__ uint32_t place_k(int r, int c) {
-    return (uint32_t)(r * HD + ((HD == 64 ? c : c ^ (r & 4)) << 4));
-}
-template <int HD>
-__device__ __forceinline__ uint32_t place_v(int r, int c) {
-    const int f = HD == 64 ? (r & 2) : HD == 128 ? (r & 3) << 1 : (r & 1) | (r & 2) << 1;
-    return (uint32_t)(r * HD + ((c ^ f) << 4));
+__device__ __forceinline__ uint32_t place(int r, int c) {
+    if constexpr (HD == 64) return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+    return (uint32_t)((c >> 3) * (kStep * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-template <int HD>
-constexpr int kStageBytes = 2 * kStep * HD + 2 * kStep * 4 + 16;  // codes of k and v, their scales, which positions are there
-template <int HD>
-constexpr int kStages = HD == 64 ? 4 : HD == 128 ? 3 : 3;
-// (the ring, or what the warps leave to be joined: sums [warp][M][HD + 2], maxima and sums of weights [warp][M][4])
-template <int HD, int MT>
-constexpr int kJoinBytes = kWarps * 16 * MT * (HD + 2 + 4) * 4;
-template <int HD, int MT>
-constexpr int kRingBytes = kWarps * kStages<HD> * kStageBytes<HD>;
-template <int HD, int MT>
-constexpr bool kQInRegs = HD * MT <= 128;
-template <int HD, int MT>
-constexpr int kQBytes = kQInRegs<HD, MT> ? 0 : MT * (HD / 16) * 32 * 16;
-template <int HD, int MT>
-constexpr int kSmem = (kRingBytes<HD, MT> > kJoinBytes<HD, MT> ? kRingBytes<HD, MT> : kJoinBytes<HD, MT>) + kQBytes<HD, MT>;
+// Shared memory: the warps' rings (k and v of a stage, 1024-byte aligned); what a
+// warp leaves to be joined (sums [M][HD + 2], then [M][4]: maxima, sum of weights, seen)
+// lies in its own ring where that holds it, so that the warps of other pieces may still
+// be at work; per warp and stage scales of k and v and which positions
+// are there; the barriers; the rows of q as MMA fragments, where registers do not hold them.
+template <int HD, int QT>
+struct Layout {
+    static constexpr int M = 8 * QT;
+    static constexpr int kCtas = HD <= 128 && QT <= 2 ? 2 : 1;  // on a multiprocessor, as registers and shared memory allow
+    static constexpr bool kQInRegs = HD * QT <= 128;
+    static constexpr int kStages = HD == 64 ? 4 : 3;
+    static constexpr int kStage = 2 * kStep * HD;
+    static constexpr int kRing = kWarps * kStages * kStage;
+    static constexpr int kSums = M * (HD + 2) * 4;
+    static constexpr int kArea = kQInRegs ? kStages * kStage : kSums + M * 16;  // from one warp's sums to the next's
+    static_assert(kSums + M * 16 <= kArea, "sums of a warp");
+    static constexpr int kFirst = kRing > kWarps * kArea ? kRing : kWarps * kArea;
+    static constexpr int kMeta = 2 * kStep * 4 + 16;
+    static constexpr int kOffMeta = kFirst;
+    static constexpr int kOffQ = kOffMeta + kWarps * kStages * kMeta;
+    static constexpr int kQ = kQInRegs ? 0 : QT * (HD / 16) * 32 * 8;
+    static constexpr int kOffC = kOffQ + kQ;
+    static constexpr int kOffBar = kOffC + M * 4;
+    static constexpr int kSmem = kOffBar + kWarps * kStages * 8 + 1024;
+};
 
-// HD: head_dim rounded up to 64, 128 or 256. MT: blocks of 16 rows.
-template <int DT, int FMT, int HD, int MT>
-__global__ void __launch_bounds__(kThreads, HD * MT <= 128 ? 2 : 1) fl_kv_attend_kernel(const __grid_constant__ AttendParams p) {
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// HD: head_dim rounded up to 64, 128 or 256. QT: tiles of eight rows of q (of a
+// sequence's rows and a group's heads). TMA: head_dim a multiple of 16; otherwise the
+// codes come in copies of 8 bytes.
+template <int DT, int FMT, int HD, int QT, bool TMA>
+__global__ void __launch_bounds__(kThreads, Layout<HD, QT>::kCtas) fl_kv_attend_kernel(const __grid_constant__ AttendParams p) {
     using Ops = DTypeOps<DT>;
-    constexpr int M = 16 * MT, KS = HD / 16, NT = HD / 8, NS = kStages<HD>, VW = HD / 32;  // VW: words of v per lane and position
-    extern __shared__ __align__(16) uint8_t smem[];
+    using Lay = Layout<HD, QT>;
+    constexpr int M = 8 * QT, KS = HD / 16, MT = HD / 16, NS = Lay::kStages, VW = HD / 32;  // VW: words of v per lane and position
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t* const smem = smem_raw + (sbase - smem_u32(smem_raw));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    auto full = [&](int s) { return sbase + Lay::kOffBar + (uint32_t)(warp * NS + s) * 8u; };
+    if (lane == 0) {
+        for (int s = 0; s < NS; ++s) mbar_init(full(s), 33);
+        fence_mbar_init();
+    }
     griddep_wait();
     griddep_launch_dependents();
-    const Piece piece = find_piece<false, kThreads>(p, blockIdx.x, M);
-    if (piece.seq < 0) return;
-    const Seq s = seq_of(p, piece.seq, M);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const Pieces pieces(p, M, Lay::kQInRegs);
+    if (blockIdx.x == 0 && threadIdx.x == 0 && p.part != nullptr) units_of<HD, QT>(p)->count = (int)pieces.units;
+    const uint32_t ring = sbase + warp * NS * Lay::kStage, meta = sbase + Lay::kOffMeta + warp * NS * Lay::kMeta;
+    const float kNone = __int_as_float(0xff800000), kNoMax = 1e30f;
+    int stage = 0;       // the ring runs on from piece to piece
+    uint32_t phase = 0;
+
+    const int W = pieces.W, group = warp / W, own = warp % W;  // the piece's warps
+    const int stride = W * kStep;                              // positions of a step of all of them
+    auto group_sync = [&] {
+        if (W == kWarps) __syncthreads();
+        else if (W > 1) named_bar_sync(1 + group, 32 * W);
+        else __syncwarp();
+    };
+
+    bool ok = true;
+    for (uint32_t turn = 0;; ++turn) {
+    Seq s;
+    Piece piece;
+    if (!pieces.find(turn, piece, s)) break;
+    if (piece.seq >= 0) {
     const int r0 = piece.block * M, rows = min(M, s.n * p.group - r0);  // rows of this block: (row of q, head of the group)
     const int t0 = (int)((long long)s.tiles * piece.k / piece.pieces), t1 = (int)((long long)s.tiles * (piece.k + 1) / piece.pieces);
     const int k0 = t0 * kTile, k1 = min(s.keys, t1 * kTile);
-    if (piece.k == 0 && threadIdx.x == 0 && s.from + s.n > (long long)p.table_pages * p.page_size)
-        atomicCAS(p.range, 0, s.row0 + 1);
+    if (piece.k == 0 && own == 0 && lane == 0) {
+        if (s.from + s.n > (long long)p.table_pages * p.page_size) atomicCAS(p.range, 0, s.row0 + 1);
+        if (piece.pieces > 1)
+            units_of<HD, QT>(p)->unit[piece.units] = Unit{s.row0, s.n, r0, piece.head, piece.pieces, piece.slot, s.blocks * p.heads, 0};
+    }
 
     // ------------------------------------------------------------ the warp's ring
-    const uint32_t sbase = smem_u32(smem);
-    const uint32_t ring = sbase + warp * NS * kStageBytes<HD>;
-    if (p.head_dim < HD) {
+    if (!TMA) {
         // channels past head_dim stay zero
-        for (int i = threadIdx.x; i < kRingBytes<HD, MT> / 16; i += kThreads)
-            reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
-        __syncthreads();
+        for (int i = lane; i < NS * Lay::kStage / 16; i += 32) st_shared_v4(ring + 16 * i, 0u, 0u, 0u, 0u);
+        __syncwarp();
     }
-    const int steps = k1 > k0 + warp * kStep ? (k1 - k0 - warp * kStep + kTile - 1) / kTile : 0;
+    const int steps = k1 > k0 + own * kStep ? (k1 - k0 - own * kStep + stride - 1) / stride : 0;
     const int* table = p.page_table + piece.seq * p.table_stride;
-    const long long row_bytes = (long long)p.heads * p.head_dim;
-    auto page_row = [&](int pos, int& in_page) {
-        const int j = p.page_shift >= 0 ? pos >> p.page_shift : (int)((uint32_t)pos / (uint32_t)p.page_size);
-        in_page = pos - j * p.page_size;
-        return j;
-    };
-    // the table's entry of this lane's position of a step, one step ahead
-    int entry = -1, in_page = 0;
+    // the table's entry of this lane's position of a step, one step ahead; -2: there is no such position
+    int entry = -2, in_page = 0;
     auto look_up = [&](int step) {
-        const int pos = k0 + warp * kStep + step * kTile + (lane & 15);
+        const int pos = k0 + own * kStep + step * stride + (lane & 15);
         entry = -2;
-        if (step < steps && pos < k1) entry = __ldg(table + page_row(pos, in_page));
-    };
-    auto request = [&](int step, int stage) {
-        const uint32_t dst = ring + stage * kStageBytes<HD>;
-        if (step < steps) {
-            const bool there = entry >= 0 && entry < p.n_pages;
-            if (entry != -2 && !there) atomicCAS(p.range, 0, s.row0 + 1);
-            const long long place = there ? (long long)entry * p.page_size + in_page : 0;
-            const uint32_t bits = __ballot_sync(0xffffffffu, there) & 0xffffu;
-            const long long head = place * p.heads + piece.head;
-            cp_async4(dst + 2 * kStep * HD + lane * 4, (lane < 16 ? p.scale[0] : p.scale[1]) + head, there ? 4 : 0);
-            if (lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + 2 * kStep * HD + 2 * kStep * 4), "r"(bits) : "memory");
-            constexpr int C = HD / 16;  // chunks of a row
-#pragma unroll
-            for (int i = 0; i < kStep * C / 32; ++i) {
-                const int r = (i * 32 + lane) / C, c = lane % C;
-                const long long at = __shfl_sync(0xffffffffu, place, r) * row_bytes + piece.head * p.head_dim + c * 16;
-                const bool full = bits >> r & 1;
-                if (!p.vec8) {
-                    if (c * 16 < p.head_dim) {
-                        cp_async16(dst + place_k<HD>(r, c), p.cache[0] + (full ? at : 0), full ? 16 : 0);
-                        cp_async16(dst + kStep * HD + place_v<HD>(r, c), p.cache[1] + (full ? at : 0), full ? 16 : 0);
-                    }
-                } else {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (c * 16 + 8 * h < p.head_dim) {
-                            cp_async8(dst + place_k<HD>(r, c) + 8 * h, p.cache[0] + (full ? at + 8 * h : 0), full ? 8 : 0);
-                            cp_async8(dst + kStep * HD + place_v<HD>(r, c) + 8 * h, p.cache[1] + (full ? at + 8 * h : 0), full ? 8 : 0);
-                        }
-                }
-            }
+        if (step < steps && pos < k1) {
+            const int j = p.page_shift >= 0 ? pos >> p.page_shift : (int)((uint32_t)pos / (uint32_t)p.page_size);
+            in_page = pos - j * p.page_size;
+            entry = __ldg(table + j);
         }
-        cp_commit();
     };
-    look_up(0);
+    // lanes 0-15 ask for k, the others for v
+    auto request = [&](int step, int at) {
+        if (step >= steps) return;
+        const uint32_t bar = full(at), dst = ring + at * Lay::kStage + (lane >> 4) * (kStep * HD), m = meta + at * Lay::kMeta;
+        const bool there = entry >= 0 && entry < p.n_pages;
+        if (entry != -2 && !there) atomicCAS(p.range, 0, s.row0 + 1);
+        const uint32_t bits = __ballot_sync(0xffffffffu, there) & 0xffffu;
+        if (lane == 0) {
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(m + 2 * kStep * 4), "r"(bits) : "memory");
+            mbar_arrive_expect_tx(bar, TMA ? Lay::kStage : 0);
+        }
+        if (TMA) {
+            __syncwarp();
+            const int r = lane & 15;
+            if ((r & ((1 << p.box_log) - 1)) == 0) {
+                // (a page that is not there: past the last, zeros)
+                const CUtensorMap* map = &p.tm[lane >> 4];
+                const int page = there ? entry : p.n_pages, row = there ? in_page : 0;
+                tma_load_4d(dst + r * (HD == 64 ? 64 : 128), map, bar, 0, piece.head, row, page);
+                if (HD == 256) tma_load_4d(dst + kStep * 128 + r * 128, map, bar, 128, piece.head, row, page);
+            }
+        } else {
+            const long long from = there ? (((long long)entry * p.page_size + in_page) * p.heads + piece.head) * p.head_dim : 0;
+            const uint8_t* src = (lane < 16 ? p.cache[0] : p.cache[1]) + from;
+            for (int c = 0; c < p.head_dim; c += 8) cp_async8(dst + place<HD>(lane & 15, c / 16) + (c & 8), src + c);
+        }
+        if (there) cp_async4(m + lane * 4, (lane < 16 ? p.scale[0] : p.scale[1]) + ((long long)entry * p.page_size + in_page) * p.heads + piece.head);
+        cp_async_arrive(bar);
+    };
+    // ------------------------------------------------------------ the first loads
+    // (what they depend on, the table's entries, and the rows of q are asked for at once)
+    constexpr int QX = Lay::kQInRegs ? QT : 1;
+    uint4 qx[QX][KS / 2];
+    auto load_q = [&](int qt, uint4* x) {
+        const int r = 8 * qt + g, i = (r0 + r) / p.group, h = (r0 + r) - i * p.group;
+        const uint16_t* q = p.q + (long long)(s.row0 + i) * p.q_row + (long long)(piece.head * p.group + h) * p.q_head + 16 * t;
+#pragma unroll
+        for (int j = 0; j < KS / 2; ++j) {
+            const int ch = j / 2 * 64 + j % 2 * 8;
+            x[j] = r < rows && ch + 16 * t < p.head_dim ? ldg_v4(q + ch) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    int first_entry[NS], first_row[NS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        look_up(i);
+        first_entry[i] = entry, first_row[i] = in_page;
+    }
+    if constexpr (Lay::kQInRegs) {
+#pragma unroll
+        for (int qt = 0; qt < QT; ++qt) load_q(qt, qx[qt]);
+    }
+    int ahead = stage;
 #pragma unroll
     for (int i = 0; i < NS - 1; ++i) {
-        request(i, i);
-        look_up(i + 1);
+        entry = first_entry[i], in_page = first_row[i];
+        request(i, ahead);
+        if (++ahead == NS) ahead = 0;
     }
+    entry = first_entry[NS - 1], in_page = first_row[NS - 1];
 
-    // ------------------------------------------------------------ q as MMA fragments
-    // Step ks = 4 h + w of the first product takes channels 64 h + 16 t + 4 w + {0, 2} and {1, 3} of lane t.
-    uint32_t qf[kQInRegs<HD, MT> ? MT : 1][kQInRegs<HD, MT> ? KS : 1][4];
-    uint8_t* const qs = smem + kSmem<HD, MT> - kQBytes<HD, MT>;
-    auto q_of = [&](int r) {  // row r of the block
-        const int i = (r0 + r) / p.group, h = (r0 + r) - i * p.group;
-        return p.q + (long long)(s.row0 + i) * p.q_row + (long long)(piece.head * p.group + h) * p.q_head;
-    };
-    // bf16: the power of two that brings the row's largest value to 2^14 .. 2^15
-    float up[MT][2];
+    // ------------------------------------------------------------ q as the first product's B fragments
+    // Step ks = 4 h + w takes channels 64 h + 16 t + 4 w + 0 .. 3 of lane t, in widen_word's order, row g of the tile.
+    // c: what q' . code is multiplied by, for rows 2 t and 2 t + 1 of a tile.
+    uint2 qf[QX][Lay::kQInRegs ? KS : 1];
+    uint2* const qs = reinterpret_cast<uint2*>(smem + Lay::kOffQ);
+    float* const cs = reinterpret_cast<float*>(smem + Lay::kOffC);
+    float c[QT][2];
+    auto q_tile = [&](const uint4* x, auto put) {  // returns the factor of row g
+        float up = 1.f;
+        if (DT == DT_BF16) {
+            // 2^(14 - e) for a largest value of 2^e to 2^(e + 1); rows without a finite, not tiny one stay as they are
+            uint32_t top = 0;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+            for (int j = 0; j < KS / 2; ++j) {
+                const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
 #pragma unroll
-        for (int e = 0; e < 2; ++e) up[mt][e] = 1.f;
-    auto each_q = [&](auto f) {
+                for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+            }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            const int ex = (int)(max(top, __shfl_xor_sync(0xffffffffu, top, 2)) >> 7);
+            if (ex > 0 && ex < 255) up = __uint_as_float((uint32_t)min(254, 127 + 14 + 127 - ex) << 23);
+        }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int j = 0; j < KS / 2; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int r = 16 * mt + 8 * e + g;
-                const uint16_t* q = r < rows ? q_of(r) : nullptr;
-#pragma unroll
-                for (int h = 0; h < KS / 4; ++h)
-#pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        const int c = 64 * h + 16 * t + 8 * v;
-                        const uint4 x = q != nullptr && c < p.head_dim ? ldg_v4(q + c) : make_uint4(0u, 0u, 0u, 0u);
-                        f(mt, e, 4 * h + 2 * v, x);
-                    }
+                const float2 lo = Ops::unpack(e ? x[j].z : x[j].x), hi = Ops::unpack(e ? x[j].w : x[j].y);
+                const float2 second = kPair<FMT> == 2 ? make_float2(lo.y, hi.y) : hi;
+                put(j / 2 * 4 + j % 2 * 2 + e, make_uint2(DTypeOps<DT_F16>::pack(lo.x * up, (kPair<FMT> == 2 ? hi.x : lo.y) * up),
+                                                          DTypeOps<DT_F16>::pack(second.x * up, second.y * up)));
             }
+        return fmaxf(p.log2_scale / up, 0x1p-126f);
     };
-    if constexpr (DT == DT_BF16) {
-        uint32_t top[MT][2] = {};
-        each_q([&](int mt, int e, int, const uint4& x) {
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    if constexpr (Lay::kQInRegs) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top[mt][e] = max(top[mt][e], max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-        });
+        for (int qt = 0; qt < QT; ++qt) {
+            const float f = q_tile(qx[qt], [&](int ks, uint2 v) { qf[qt][ks] = v; });
+            c[qt][0] = __shfl_sync(0xffffffffu, f, 8 * t), c[qt][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+        }
+    } else {
+        for (int qt = warp; qt < QT; qt += kWarps) {
+            load_q(qt, qx[0]);
+            const float f = q_tile(qx[0], [&](int ks, uint2 v) { qs[(qt * KS + ks) * 32 + lane] = v; });
+            if (t == 0) cs[8 * qt + g] = f;
+        }
+        __syncthreads();
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                uint32_t m = max(top[mt][e], __shfl_xor_sync(0xffffffffu, top[mt][e], 1));
-                m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                // 2^(14 - e) for a largest value of 2^e to 2^(e + 1); rows without a finite, not tiny one stay as they are
-                const int ex = (int)(m >> 7);
-                if (ex > 0 && ex < 255) up[mt][e] = __uint_as_float((uint32_t)min(254, 127 + 14 + 127 - ex) << 23);
-            }
+        for (int qt = 0; qt < QT; ++qt) c[qt][0] = cs[8 * qt + 2 * t], c[qt][1] = cs[8 * qt + 2 * t + 1];
     }
-    const bool writes_q = kQInRegs<HD, MT> || warp == 0;
-    if (writes_q)
-        each_q([&](int mt, int e, int ks, const uint4& x) {
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float2 lo = Ops::unpack(w[2 * i]), hi = Ops::unpack(w[2 * i + 1]);
-                const uint32_t even = DTypeOps<DT_F16>::pack(lo.x * up[mt][e], hi.x * up[mt][e]);
-                const uint32_t odd = DTypeOps<DT_F16>::pack(lo.y * up[mt][e], hi.y * up[mt][e]);
-                if constexpr (kQInRegs<HD, MT>) {
-                    qf[mt][ks + i][e] = even;
-                    qf[mt][ks + i][2 + e] = odd;
-                } else {
-                    uint32_t* d = reinterpret_cast<uint32_t*>(qs) + ((mt * KS + ks + i) * 32 + lane) * 4;
-                    d[e] = even;
-                    d[2 + e] = odd;
-                }
-            }
-        });
-    if (!kQInRegs<HD, MT>) __syncthreads();
-    float c[MT][2];  // onto q' . code
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) c[mt][e] = p.log2_scale * kCodeUnit<FMT> / up[mt][e];
 
     // ------------------------------------------------------------ the warp's positions
-    const float kNone = __int_as_float(0xff800000);
-    float mx[MT][2], mw[MT][2], nx[MT][2], nw[MT][2], l[MT][2], o[MT][NT][4];  // n*: minus the maxima, 0 where there is none yet
+    // nx, nw: minus the maxima of the exponents x and x + log2 vs; kNoMax where there is
+    // none yet, which any finite exponent exceeds by more than kLazy
+    float nx[QT][2], nw[QT][2], l[QT][2], o[QT][MT][4];
+    uint32_t seen = 0;  // bit 2 qt + f: the row saw a position (which tells it from one whose scores are all -inf)
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int qt = 0; qt < QT; ++qt) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) mx[mt][e] = mw[mt][e] = kNone, nx[mt][e] = nw[mt][e] = l[mt][e] = 0.f;
+        for (int f = 0; f < 2; ++f) nx[qt][f] = nw[qt][f] = kNoMax, l[qt][f] = 0.f;
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int j = 0; j < MT; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[mt][j][e] = 0.f;
+            for (int e = 0; e < 4; ++e) o[qt][j][e] = 0.f;
     }
-    bool seen[MT][2] = {};  // (which tells a row that sees nothing from one whose scores are all -inf)
-    // this lane's rows: the row of q among the sequence's
-    int qi[MT][2];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) qi[mt][e] = min(r0 + 16 * mt + 8 * e + g, s.n * p.group - 1) / p.group;
 
-    int stage = 0, ahead = NS - 1;
     for (int step = 0; step < steps; ++step) {
-        cp_wait<NS - 2>();
-        __syncwarp();
+        __syncwarp();  // (the stage that is asked for next has been read)
         request(step + NS - 1, ahead);
         look_up(step + NS);
         if (++ahead == NS) ahead = 0;
-        const uint32_t src = ring + stage * kStageBytes<HD>;
-        if (++stage == NS) stage = 0;
-        const int pos0 = k0 + warp * kStep + step * kTile;
+        ok = __all_sync(0xffffffffu, wait_bar(full(stage), phase, p.status, p.timeout_ns, 51));
+        if (!ok) break;
+        const uint32_t src = ring + stage * Lay::kStage, sc = meta + stage * Lay::kMeta;
+        if (++stage == NS) stage = 0, phase ^= 1u;
+        const int pos0 = k0 + own * kStep + step * stride;
 
-        // scores: positions t + 4 i, i = 2 nt + column
-        float x[MT][2][4];
+        // scores x[qt][2 i + f] of position g + 8 i and row 2 t + f of the tile
+        float x[QT][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[mt][nt][e] = 0.f;
-        const int krow = (g >> 1) + 4 * (g & 1);
+            for (int e = 0; e < 4; ++e) x[qt][e] = 0.f;
 #pragma unroll
         for (int h = 0; h < KS / 4; ++h) {
-            uint4 kv[2];
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt) kv[nt] = ld_shared_v4(src + place_k<HD>(krow + 8 * nt, 4 * h + t));
+            const uint4 ka = ld_shared_v4(src + place<HD>(g, 4 * h + t)), kb = ld_shared_v4(src + place<HD>(g + 8, 4 * h + t));
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                uint32_t a[MT][4];
+                uint32_t a[4];
+                widen_word<FMT>(w == 0 ? ka.x : w == 1 ? ka.y : w == 2 ? ka.z : ka.w, a[0], a[2]);
+                widen_word<FMT>(w == 0 ? kb.x : w == 1 ? kb.y : w == 2 ? kb.z : kb.w, a[1], a[3]);
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    if constexpr (kQInRegs<HD, MT>) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) a[mt][e] = qf[mt][4 * h + w][e];
-                    } else {
-                        const uint4 v = *reinterpret_cast<const uint4*>(qs + ((mt * KS + 4 * h + w) * 32 + lane) * 16);
-                        a[mt][0] = v.x, a[mt][1] = v.y, a[mt][2] = v.z, a[mt][3] = v.w;
-                    }
-                }
-#pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    uint32_t b0, b1;
-                    widen_word<FMT>(w == 0 ? kv[nt].x : w == 1 ? kv[nt].y : w == 2 ? kv[nt].z : kv[nt].w, b0, b1);
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) mma16816(x[mt][nt], a[mt], b0, b1);
+                for (int qt = 0; qt < QT; ++qt) {
+                    uint2 b;
+                    if constexpr (Lay::kQInRegs) b = qf[qt][4 * h + w];
+                    else b = qs[(qt * KS + 4 * h + w) * 32 + lane];
+                    mma16816(x[qt], a, b.x, b.y);
                 }
             }
         }
-        // scales of the lane's four positions
-        const uint32_t sc = src + 2 * kStep * HD;
-        float ks[4], lv[4];
+        // scales of the lane's two positions
+        float ks[2], lv[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            ks[i] = ld_shared_f32(sc + 4 * (t + 4 * i));
-            lv[i] = lg2(ld_shared_f32(sc + kStep * 4 + 4 * (t + 4 * i)));
-        }
+        for (int i = 0; i < 2; ++i) ks[i] = ld_shared_f32(sc + 4 * g + 32 * i), lv[i] = lg2(ld_shared_f32(sc + 64 + 4 * g + 32 * i));
         const uint32_t bits = __float_as_uint(ld_shared_f32(sc + 2 * kStep * 4));
-        const bool all = bits == 0xffffu && pos0 + kStep <= s.from;  // every row sees every position
-        float y[MT][2][4];
-        bool over = false;
+        uint32_t hidden = 0;  // bit 4 qt + e: the row does not see the position
+        if (bits != 0xffffu || pos0 + kStep > s.from) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+            for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
+                for (int f = 0; f < 2; ++f) {
+                    // the row of q among the sequence's (rows past the last: as the last)
+                    const int qi = min(r0 + 8 * qt + 2 * t + f, s.n * p.group - 1) / p.group;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const long long j = pos0 + g + 8 * i - s.from;
+                        bool sees = bits >> (g + 8 * i) & 1;
+                        if (sees && j >= 0) {
+                            if (p.tree == nullptr) sees = j <= qi;
+                            else sees = j < p.tree_cols && __ldg(p.tree + (s.row0 + qi) * p.tree_stride + j) != 0;
+                        }
+                        if (sees) seen |= 1u << (2 * qt + f);
+                        else hidden |= 1u << (4 * qt + 2 * i + f);
+                    }
+                }
+        } else {
+            seen = (1u << 2 * QT) - 1;
+        }
+        // exponents less the maxima, for the sum of weights and for the weights of the values
+        float a[QT][4], b[QT][4], most = kNone;
+        auto exponents = [&] {
+#pragma unroll
+            for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int i = 2 * nt + (e & 1);
-                    float v = x[mt][nt][e] * c[mt][e >> 1] * ks[i], u = v + lv[i];
-                    if (!all) {
-                        const long long j = pos0 + t + 4 * i - s.from;
-                        bool sees = bits >> (t + 4 * i) & 1;
-                        if (sees && j >= 0) {
-                            if (p.tree == nullptr) sees = j <= qi[mt][e >> 1];
-                            else sees = j < p.tree_cols && __ldg(p.tree + (s.row0 + qi[mt][e >> 1]) * p.tree_stride + j) != 0;
+                    a[qt][e] = fmaf(x[qt][e], c[qt][e & 1], nx[qt][e & 1]);
+                    b[qt][e] = fmaf(x[qt][e], c[qt][e & 1], lv[e >> 1] + nw[qt][e & 1]);
+                }
+            if (hidden != 0) {
+#pragma unroll
+                for (int qt = 0; qt < QT; ++qt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (hidden >> (4 * qt + e) & 1) a[qt][e] = b[qt][e] = kNone;
+            }
+        };
+#pragma unroll
+        for (int qt = 0; qt < QT; ++qt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[qt][e] *= ks[e >> 1];
+        exponents();
+#pragma unroll
+        for (int qt = 0; qt < QT; ++qt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) most = fmaxf(most, fmaxf(a[qt][e], b[qt][e]));
+        if (__any_sync(0xffffffffu, most > kLazy)) {
+#pragma unroll
+            for (int qt = 0; qt < QT; ++qt)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    float ma = kNone, mb = kNone;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (!(hidden >> (4 * qt + 2 * i + f) & 1)) {
+                            const float y = x[qt][2 * i + f] * c[qt][f];
+                            ma = fmaxf(ma, y), mb = fmaxf(mb, y + lv[i]);
                         }
-                        if (!sees) v = u = kNone;
-                        seen[mt][e >> 1] |= sees;
-                    } else {
-                        seen[mt][e >> 1] = true;
+#pragma unroll
+                    for (int w = 4; w < 32; w <<= 1) {
+                        ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, w));
+                        mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, w));
                     }
-                    x[mt][nt][e] = v;
-                    y[mt][nt][e] = u;
-                    over |= v > mx[mt][e >> 1] + kLazy || u > mw[mt][e >> 1] + kLazy;
-                }
-        if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float a = mx[mt][e], b = mw[mt][e];
-#pragma unroll
-                    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                        for (int f = 0; f < 2; ++f) a = fmaxf(a, x[mt][nt][2 * e + f]), b = fmaxf(b, y[mt][nt][2 * e + f]);
-#pragma unroll
-                    for (int w = 1; w < 4; w <<= 1) {
-                        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, w));
-                        b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, w));
+                    // (a maximum that is there already only grows)
+                    if (nx[qt][f] == kNoMax ? ma > kNone : ma > -nx[qt][f]) {
+                        l[qt][f] *= nx[qt][f] == kNoMax ? 0.f : ex2(-nx[qt][f] - ma);
+                        nx[qt][f] = -ma;
                     }
-                    const float na = a == kNone ? 0.f : -a, nb = b == kNone ? 0.f : -b;
-                    l[mt][e] *= ex2(mx[mt][e] + na);
-                    const float f = ex2(mw[mt][e] + nb);
+                    if (nw[qt][f] == kNoMax ? mb > kNone : mb > -nw[qt][f]) {
+                        const float y = nw[qt][f] == kNoMax ? 0.f : ex2(-nw[qt][f] - mb);
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) o[mt][j][2 * e] *= f, o[mt][j][2 * e + 1] *= f;
-                    mx[mt][e] = a, mw[mt][e] = b, nx[mt][e] = na, nw[mt][e] = nb;
+                        for (int j = 0; j < MT; ++j) o[qt][j][f] *= y, o[qt][j][2 + f] *= y;
+                        nw[qt][f] = -mb;
+                    }
                 }
+            exponents();
         }
-        uint32_t w[MT][4];
+        // P^T: 16 positions (k) by 8 rows
+        uint2 w[QT];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int qt = 0; qt < QT; ++qt) {
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    l[mt][e] += ex2(x[mt][nt][2 * e] + nx[mt][e]) + ex2(x[mt][nt][2 * e + 1] + nx[mt][e]);
-                    w[mt][2 * nt + e] = DTypeOps<DT_F16>::pack(ex2(y[mt][nt][2 * e] + nw[mt][e]), ex2(y[mt][nt][2 * e + 1] + nw[mt][e]));
-                }
-        // values: n tile j is channel j of the lane's 4 VW
+            for (int f = 0; f < 2; ++f) l[qt][f] += ex2(a[qt][f]) + ex2(a[qt][2 + f]);
+            w[qt].x = movmatrix(DTypeOps<DT_F16>::pack(ex2(b[qt][0]), ex2(b[qt][1])));
+            w[qt].y = movmatrix(DTypeOps<DT_F16>::pack(ex2(b[qt][2]), ex2(b[qt][3])));
+        }
+        // values: row block j is channels 2 j (rows 0-7) and 2 j + 1 (8-15) of the lane's 4 VW, k positions 2 t, 2 t + 1, + 8
         uint32_t v[4][VW];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int r = t + 4 * i;
+            const int r = 8 * (i >> 1) + 2 * t + (i & 1);
             if constexpr (VW == 2) {
-                const uint32_t at = src + kStep * HD + place_v<HD>(r, g >> 1) + 8 * (g & 1);
+                const uint32_t at = src + kStep * HD + place<HD>(r, g >> 1) + 8 * (g & 1);
                 asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[i][0]), "=r"(v[i][1]) : "r"(at) : "memory");
             } else {
 #pragma unroll
                 for (int q = 0; q < VW / 4; ++q) {
-                    const uint4 u = ld_shared_v4(src + kStep * HD + place_v<HD>(r, g * (VW / 4) + q));
+                    const uint4 u = ld_shared_v4(src + kStep * HD + place<HD>(r, g * (VW / 4) + q));
                     v[i][4 * q] = u.x, v[i][4 * q + 1] = u.y, v[i][4 * q + 2] = u.z, v[i][4 * q + 3] = u.w;
                 }
             }
         }
+        if (bits != 0xffffu) {
+            // (what lies behind the last position may hold codes that are not numbers)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const uint32_t b0 = widen_pair<FMT>(v[0][j / 4], v[1][j / 4], j % 4), b1 = widen_pair<FMT>(v[2][j / 4], v[3][j / 4], j % 4);
+            for (int i = 0; i < 4; ++i)
+                if (!(bits >> (8 * (i >> 1) + 2 * t + (i & 1)) & 1))
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) mma16816(o[mt][j], w[mt], b0, b1);
+                    for (int q = 0; q < VW; ++q) v[i][q] = 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            uint32_t va[4];
+            va[0] = widen_pair<FMT>(v[0][j / 2], v[1][j / 2], j % 2 * 2), va[1] = widen_pair<FMT>(v[0][j / 2], v[1][j / 2], j % 2 * 2 + 1);
+            va[2] = widen_pair<FMT>(v[2][j / 2], v[3][j / 2], j % 2 * 2), va[3] = widen_pair<FMT>(v[2][j / 2], v[3][j / 2], j % 2 * 2 + 1);
+#pragma unroll
+            for (int qt = 0; qt < QT; ++qt) mma16816(o[qt][j], va, w[qt].x, w[qt].y);
         }
     }
-    cp_wait<0>();
+    if (!ok)  // a wait ran out: every load that was asked for lands before the CTA exits
+        for (int i = 0; i < NS; ++i) wait_bar_drain(full(i), (uint32_t)(i >= stage ? phase : phase ^ 1u), 20000000ull);
+    if constexpr (!Lay::kQInRegs) __syncthreads();  // (the rings of all warps have been read)
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int f = 0; f < 2; ++f)
 #pragma unroll
-            for (int f = 1; f < 4; f <<= 1) {
-                l[mt][e] += __shfl_xor_sync(0xffffffffu, l[mt][e], f);
-                seen[mt][e] |= __shfl_xor_sync(0xffffffffu, (int)seen[mt][e], f) != 0;
-            }
-    __syncthreads();
+            for (int w = 4; w < 32; w <<= 1) l[qt][f] += __shfl_xor_sync(0xffffffffu, l[qt][f], w);
+    // (seen: the same rows in lanes of the same t)
+#pragma unroll
+    for (int w = 4; w < 32; w <<= 1) seen |= __shfl_xor_sync(0xffffffffu, seen, w);
 
     // ------------------------------------------------------------ the CTA's warps joined
     constexpr int P = HD + 2;  // pitch of a row of sums
-    float* const sums = reinterpret_cast<float*>(smem);
-    float* const stat = sums + kWarps * M * P;
+    auto sums = [&](int w, int r) { return reinterpret_cast<float*>(smem + w * Lay::kArea) + r * P; };
+    auto stat = [&](int w, int r) { return reinterpret_cast<float4*>(smem + w * Lay::kArea + Lay::kSums) + r; };
+    __syncwarp();
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int r = 16 * mt + 8 * e + g;
-            float* d = sums + (warp * M + r) * P;
+        for (int f = 0; f < 2; ++f) {
+            const int r = 8 * qt + 2 * t + f;
+            float* d = sums(warp, r) + g * (4 * VW);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                d[2 * t * (4 * VW) + j] = o[mt][j][2 * e];
-                d[(2 * t + 1) * (4 * VW) + j] = o[mt][j][2 * e + 1];
-            }
-            if (t == 0) *reinterpret_cast<float4*>(stat + (warp * M + r) * 4) = make_float4(mx[mt][e], mw[mt][e], l[mt][e], seen[mt][e] ? 1.f : 0.f);
+            for (int j = 0; j < MT; ++j) *reinterpret_cast<float2*>(d + 2 * j) = make_float2(o[qt][j][f], o[qt][j][2 + f]);
+            if (g == 0)  // (this warp's part)
+                *stat(warp, r) =
+                    make_float4(nx[qt][f] == kNoMax ? kNone : -nx[qt][f], nw[qt][f] == kNoMax ? kNone : -nw[qt][f], l[qt][f],
+                                seen >> (2 * qt + f) & 1 ? 1.f : 0.f);
         }
-    __syncthreads();
+    group_sync();
     const bool whole = piece.pieces == 1;
-    for (int i = threadIdx.x; i < rows * (HD / 8); i += kThreads) {
-        const int r = i / (HD / 8), ch = i % (HD / 8) * 8;
-        float a = kNone, b = kNone, any = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float4 st = *reinterpret_cast<const float4*>(stat + (w * M + r) * 4);
-            a = fmaxf(a, st.x), b = fmaxf(b, st.y), any = fmaxf(any, st.w);
+    for (int i = own * 32 + lane; i < rows * (HD / 2); i += 32 * W) {
+        const int r = i / (HD / 2), ch = i % (HD / 2) * 2;
+        float ma = kNone, mb = kNone, any = 0.f;
+#pragma unroll 4
+        for (int w = group * W; w < group * W + W; ++w) {
+            const float4 st = *stat(w, r);
+            ma = fmaxf(ma, st.x), mb = fmaxf(mb, st.y), any = fmaxf(any, st.w);
         }
-        const float na = a == kNone ? 0.f : -a, nb = b == kNone ? 0.f : -b;
-        float sum = 0.f, v[8] = {};
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float4 st = *reinterpret_cast<const float4*>(stat + (w * M + r) * 4);
+        const float na = ma == kNone ? 0.f : -ma, nb = mb == kNone ? 0.f : -mb;
+        float sum = 0.f;
+        float2 v = make_float2(0.f, 0.f);
+#pragma unroll 4
+        for (int w = group * W; w < group * W + W; ++w) {
+            const float4 st = *stat(w, r);
             sum += st.z * ex2(st.x + na);
             const float f = ex2(st.y + nb);
-            const float* d = sums + (w * M + r) * P + ch;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = fmaf(d[e], f, v[e]);
+            const float2 d = *reinterpret_cast<const float2*>(sums(w, r) + ch);
+            v.x = fmaf(d.x, f, v.x), v.y = fmaf(d.y, f, v.y);
         }
         if (whole) {
-            if (ch < p.head_dim) store_row<Ops>(p, s, piece.head, r0 + r, ch, v, finish<FMT>(a, b, sum, any));
+            if (ch < p.head_dim) {
+                const float2 f = finish<FMT>(ma, mb, sum, any);
+                *reinterpret_cast<uint32_t*>(row_at(p, s.row0, piece.head, r0 + r) + ch) = f.y != 0.f ? 0u : Ops::pack(v.x * f.x, v.y * f.x);
+            }
         } else {
-            float* d = p.part + ((long long)piece.slot * M + r) * HD + ch;
-            *reinterpret_cast<float4*>(d) = make_float4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<float4*>(d + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            *reinterpret_cast<float2*>(p.part + ((long long)piece.slot * M + r) * HD + ch) = v;
             if (ch == 0)
                 *reinterpret_cast<float4*>(p.part + (long long)kSlots * M * HD + ((long long)piece.slot * M + r) * 4) =
-                    make_float4(a, b, sum, any);
+                    make_float4(ma, mb, sum, any);
         }
+    }
+    }
+    // the sums have been read before the next round's loads overwrite them
+    fence_proxy_async_smem();
+    if (!__syncthreads_and(ok)) break;
     }
 }
 
-// The pieces of row blocks of split sequences joined: one CTA to four rows of a
-// block and head, four warps to a row, each of which adds every fourth piece; always in the same order.
-constexpr int kJoinThreads = 512;
+// The pieces of row blocks of split sequences joined: a CTA of four warps to a row,
+// each of which adds every fourth piece; always in the same order.
+constexpr int kJoinThreads = 128;
 
-template <int DT, int FMT, int HD, int MT>
+template <int DT, int FMT, int HD, int QT>
 __global__ void __launch_bounds__(kJoinThreads) fl_kv_attend_join_kernel(const __grid_constant__ AttendParams p) {
     using Ops = DTypeOps<DT>;
-    constexpr int M = 16 * MT, C = HD / 32;  // channels of a lane
-    __shared__ float part[16][HD];
-    // (the lengths are older than the kernel in front, which waited for them itself before it let this one in)
-    const Piece u = find_piece<true, kJoinThreads>(p, blockIdx.x, M);
+    constexpr int M = 8 * QT, C = HD / 32;  // channels of a lane
+    __shared__ float part[4][HD];
     griddep_wait();
     griddep_launch_dependents();
-    if (u.seq < 0) return;
-    const Seq s = seq_of(p, u.seq, M);
+    const Units* all = units_of<HD, QT>(p);
+    const int count = max(0, min(__ldcg(&all->count), kUnits)) * M;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int r = blockIdx.y * 4 + (warp >> 2), first = warp & 3, rows = min(M, s.n * p.group - u.block * M);
-    const long long step = (long long)s.blocks * p.heads;  // slots from one piece to the next
     const float kNone = __int_as_float(0xff800000);
-    float a = kNone, b = kNone, sum = 0.f, any = 0.f, v[C] = {};
-    if (r < rows) {
-        const float* stat = p.part + (long long)kSlots * M * HD + ((long long)u.slot * M + r) * 4;
-        for (int k = lane; k < u.pieces; k += 32) {
+    for (int at = blockIdx.x; at < count; at += gridDim.x) {
+        const int4 u0 = __ldcg(reinterpret_cast<const int4*>(&all->unit[at / M]));
+        const int4 u1 = __ldcg(reinterpret_cast<const int4*>(&all->unit[at / M]) + 1);
+        const int row0 = u0.x, n = u0.y, block0 = u0.z, head = u0.w, pieces = u1.x, slot = u1.y, r = at % M;
+        const long long step = u1.z;  // slots from one piece to the next
+        // (records of a workspace that another call is writing at the same time stay harmless)
+        const bool fits = row0 >= 0 && n >= 0 && row0 <= p.rows - n && block0 >= 0 && head >= 0 && head < p.heads && pieces > 0 &&
+                          slot >= 0 && step > 0 && slot + (pieces - 1) * step < kSlots;
+        if (!fits || r >= n * p.group - block0) continue;
+        float a = kNone, b = kNone, sum = 0.f, any = 0.f, v[C] = {};
+        const float* stat = p.part + (long long)kSlots * M * HD + ((long long)slot * M + r) * 4;
+        const float* src = p.part + ((long long)slot * M + r) * HD + lane * C;
+        // (the first pieces' sums are asked for together with the maxima that they will be weighed by)
+        constexpr int U = 4;
+        float2 x[U][C / 2];
+        auto load = [&](int k, float2 (&d)[C / 2]) {
+#pragma unroll
+            for (int e = 0; e < C / 2; ++e) d[e] = __ldcg(reinterpret_cast<const float2*>(src + k * step * M * HD) + e);
+        };
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (warp + 4 * u < pieces) load(warp + 4 * u, x[u]);
+        float4 mine = make_float4(kNone, kNone, 0.f, 0.f);
+        for (int k = lane; k < pieces; k += 32) {
             const float4 st = __ldcg(reinterpret_cast<const float4*>(stat + k * step * M * 4));
+            if (k < 32) mine = st;
             a = fmaxf(a, st.x), b = fmaxf(b, st.y), any = fmaxf(any, st.w);
         }
 #pragma unroll
@@ -707,40 +859,46 @@ __global__ void __launch_bounds__(kJoinThreads) fl_kv_attend_join_kernel(const _
             any = fmaxf(any, __shfl_xor_sync(0xffffffffu, any, o));
         }
         const float na = a == kNone ? 0.f : -a, nb = b == kNone ? 0.f : -b;
-        for (int k = lane; k < u.pieces; k += 32) {
+        sum = mine.z * ex2(mine.x + na);
+        for (int k = lane + 32; k < pieces; k += 32) {
             const float4 st = __ldcg(reinterpret_cast<const float4*>(stat + k * step * M * 4));
             sum += st.z * ex2(st.x + na);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float* src = p.part + ((long long)u.slot * M + r) * HD + lane * C;
-#pragma unroll 4
-        for (int k = first; k < u.pieces; k += 4) {
-            const float f = ex2(__ldcg(stat + k * step * M * 4 + 1) + nb);
-            const float* d = src + k * step * M * HD;
+        for (int k0 = warp; k0 < pieces; k0 += 4 * U) {
+            if (k0 != warp) {
 #pragma unroll
-            for (int e = 0; e < C; e += 2) {
-                const float2 x = __ldcg(reinterpret_cast<const float2*>(d + e));
-                v[e] = fmaf(x.x, f, v[e]);
-                v[e + 1] = fmaf(x.y, f, v[e + 1]);
+                for (int u = 0; u < U; ++u)
+                    if (k0 + 4 * u < pieces) load(k0 + 4 * u, x[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = k0 + 4 * u;
+                const float mb = k < 32 ? __shfl_sync(0xffffffffu, mine.y, k) : k < pieces ? __ldcg(stat + k * step * M * 4 + 1) : kNone;
+                if (k >= pieces) continue;
+                const float f = ex2(mb + nb);
+#pragma unroll
+                for (int e = 0; e < C / 2; ++e) v[2 * e] = fmaf(x[u][e].x, f, v[2 * e]), v[2 * e + 1] = fmaf(x[u][e].y, f, v[2 * e + 1]);
             }
         }
 #pragma unroll
         for (int e = 0; e < C; ++e) part[warp][lane * C + e] = v[e];
-    }
-    __syncthreads();
-    if (r >= rows || first != 0) return;
-    const float2 f = finish<FMT>(a, b, sum, any);
-    for (int ch = lane * 8; ch < p.head_dim; ch += 256) {
-        float x[8];
+        __syncthreads();
+        if (threadIdx.x * 2 < p.head_dim) {
+            const int ch = threadIdx.x * 2;
+            const float2 f = finish<FMT>(a, b, sum, any);
+            float y[2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = (part[warp][ch + e] + part[warp + 1][ch + e]) + (part[warp + 2][ch + e] + part[warp + 3][ch + e]);
-        store_row<Ops>(p, s, u.head, u.block * M + r, ch, x, f);
+            for (int e = 0; e < 2; ++e) y[e] = (part[0][ch + e] + part[1][ch + e]) + (part[2][ch + e] + part[3][ch + e]);
+            *reinterpret_cast<uint32_t*>(row_at(p, row0, head, block0 + r) + ch) = f.y != 0.f ? 0u : Ops::pack(y[0] * f.x, y[1] * f.x);
+        }
+        __syncthreads();
     }
 }
 
 struct Plan {
-    int hd, mt, group;
+    int hd, qt, group;
     long long units;  // row blocks and heads at most
     bool split;       // whether a sequence can be long enough to be split
 };
@@ -748,16 +906,17 @@ Plan plan_of(const fl_kv_attend_desc* d) {
     Plan p;
     p.group = d->heads_q / d->heads_k;
     p.hd = d->head_dim <= 64 ? 64 : d->head_dim <= 128 ? 128 : 256;
-    // rows of a sequence: more than 16 fill two blocks (no registers for that at 256 channels)
+    // tiles for the rows of a sequence, 1, 2 or 4 of them (at 256 channels registers hold two): what does
+    // not fit is another row block, which reads the codes again
     const long long each = d->cu_rows == nullptr ? p.group : ((long long)d->rows + d->n_seqs - 1) / d->n_seqs * p.group;
-    p.mt = each > 16 && p.hd <= 128 ? 2 : 1;
-    const long long seqs = d->rows < d->n_seqs ? d->rows : d->n_seqs, M = 16 * p.mt;
+    p.qt = each <= 8 ? 1 : each <= 16 || p.hd == 256 ? 2 : 4;
+    const long long seqs = d->rows < d->n_seqs ? d->rows : d->n_seqs, M = 8 * p.qt;
     p.units = d->cu_rows == nullptr ? seqs * ((p.group + M - 1) / M) * d->heads_k
                                     : ((long long)d->rows * p.group / M + seqs) * d->heads_k;
     p.split = (long long)d->table_pages * d->page_size > (long long)kLeast * kTile;
     return p;
 }
-size_t workspace_of(const Plan& p) { return p.split ? (size_t)kSlots * 16 * p.mt * (p.hd + 4) * 4 : 0; }
+size_t workspace_of(const Plan& p) { return p.split ? (size_t)kSlots * 8 * p.qt * (p.hd + 4) * 4 + sizeof(Units) : 0; }
 
 fl_status check_sizes(const fl_kv_attend_desc* d) {
     using host::fail;
@@ -774,7 +933,7 @@ fl_status check_sizes(const fl_kv_attend_desc* d) {
     if (d->head_dim % 8 != 0) return fail(FL_ERR_ALIGNMENT, "%s: head_dim must be a multiple of 8 (%d)", what, d->head_dim);
     if (d->head_dim > 256) return fail(FL_ERR_UNSUPPORTED, "%s: head_dim above 256 (%d)", what, d->head_dim);
     if (d->n_seqs > 1 << 30) return fail(FL_ERR_UNSUPPORTED, "%s: more than 2^30 sequences", what);
-    if ((long long)d->rows * (d->heads_q / d->heads_k) >= (1ll << 31) - 64 || plan_of(d).units + kPieces >= (1ll << 31))
+    if ((long long)d->rows * (d->heads_q / d->heads_k) >= (1ll << 31) - 64 || plan_of(d).units + kSlots >= (1ll << 31))
         return fail(FL_ERR_UNSUPPORTED, "%s: too many rows", what);
     return FL_OK;
 }
@@ -841,35 +1000,52 @@ fl_status attend(const fl_kv_attend_desc* d, void* workspace, size_t workspace_b
     p.rows = d->rows, p.heads = d->heads_k, p.group = plan.group, p.head_dim = d->head_dim, p.page_size = d->page_size;
     p.page_shift = (d->page_size & (d->page_size - 1)) == 0 ? __builtin_ctz((unsigned)d->page_size) : -1;
     p.n_pages = d->n_pages, p.n_seqs = d->n_seqs, p.table_pages = d->table_pages;
-    p.vec8 = d->head_dim % 16 != 0;
     p.log2_scale = d->scale * 1.44269504088896341f;
-    p.part = static_cast<float*>(workspace);
-    p.range = ctx.range;
-    const dim3 grid((unsigned)(plan.units + (plan.split ? kPieces : 0)));
-    const dim3 join_grid((unsigned)(plan.units < kPieces ? plan.units : kPieces), 4u * plan.mt);
-    cudaError_t e = cudaErrorInvalidValue;
-    auto both = [&](auto dt, auto fmt, auto hd, auto mt) -> fl_status {
-        constexpr int DT = decltype(dt)::value, FMT = decltype(fmt)::value, HD = decltype(hd)::value, MT = decltype(mt)::value;
+    p.part = plan.split ? static_cast<float*>(workspace) : nullptr;
+    p.range = ctx.range, p.status = ctx.status, p.timeout_ns = ctx.timeout_ns;
+    // boxes: as many positions as a page holds whole numbers of, 16 at most
+    p.box_log = 0;
+    while (p.box_log < 4 && d->page_size % (2 << p.box_log) == 0) ++p.box_log;
+    const bool tma = d->head_dim % 16 == 0;
+    if (tma)
+        for (int w = 0; w < 2; ++w)
+            if ((st = host::encode_pages(&p.tm[w], w == 0 ? d->k_cache : d->v_cache, d->head_dim, d->heads_k, d->page_size,
+                                         d->n_pages, plan.hd == 64 ? 64 : 128, 1u << p.box_log)) != FL_OK)
+                return st;
+    // (L is T / kResident at least: that many pieces more than units at most)
+    const long long most = plan.units + (plan.split ? kResident : 0);
+    const dim3 grid((unsigned)std::min<long long>(most, (long long)ctx.sms * (plan.hd <= 128 && plan.qt <= 2 ? 2 : 1)));
+    const dim3 join_grid((unsigned)std::min<long long>(ctx.sms * 4ll, plan.units * 8 * plan.qt));
+    auto both = [&](auto dt, auto fmt, auto hd, auto qt, auto by_tma) -> fl_status {
+        constexpr int DT = decltype(dt)::value, FMT = decltype(fmt)::value, HD = decltype(hd)::value, QT = decltype(qt)::value;
+        constexpr bool TMA = decltype(by_tma)::value;
         static std::atomic<unsigned long long> done{0};
-        constexpr int bytes = kSmem<HD, MT>;
-        static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
-        e = host::allow_smem(fl_kv_attend_kernel<DT, FMT, HD, MT>, bytes, ctx.device, done);
+        constexpr int bytes = Layout<HD, QT>::kSmem;
+        static_assert(bytes <= 227 * 1024 / Layout<HD, QT>::kCtas - 1024, "shared memory of the resident CTAs");
+        cudaError_t e = host::allow_smem(fl_kv_attend_kernel<DT, FMT, HD, QT, TMA>, bytes, ctx.device, done);
         if (e != cudaSuccess) return host::fail(FL_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-        e = host::launch(fl_kv_attend_kernel<DT, FMT, HD, MT>, grid, kThreads, bytes, ctx.pdl, stream, p);
+        e = host::launch(fl_kv_attend_kernel<DT, FMT, HD, QT, TMA>, grid, kThreads, bytes, ctx.pdl, stream, p);
         const fl_status s = host::launched(e, what);
         if (s != FL_OK || !plan.split) return s;
-        e = host::launch(fl_kv_attend_join_kernel<DT, FMT, HD, MT>, join_grid, kJoinThreads, 0, ctx.pdl, stream, p);
+        e = host::launch(fl_kv_attend_join_kernel<DT, FMT, HD, QT>, join_grid, kJoinThreads, 0, ctx.pdl, stream, p);
         return host::launched(e, what);
     };
-    auto by_size = [&](auto dt, auto fmt) {
-        using std::integral_constant;
-        if (plan.hd == 64) return plan.mt == 2 ? both(dt, fmt, integral_constant<int, 64>(), integral_constant<int, 2>())
-                                               : both(dt, fmt, integral_constant<int, 64>(), integral_constant<int, 1>());
-        if (plan.hd == 128) return plan.mt == 2 ? both(dt, fmt, integral_constant<int, 128>(), integral_constant<int, 2>())
-                                                : both(dt, fmt, integral_constant<int, 128>(), integral_constant<int, 1>());
-        return both(dt, fmt, integral_constant<int, 256>(), integral_constant<int, 1>());
-    };
     using std::integral_constant;
+    auto by_rows = [&](auto dt, auto fmt, auto hd, auto by_tma) {
+        if (plan.qt == 1) return both(dt, fmt, hd, integral_constant<int, 1>(), by_tma);
+        if constexpr (decltype(hd)::value <= 128) {
+            if (plan.qt == 4) return both(dt, fmt, hd, integral_constant<int, 4>(), by_tma);
+        }
+        return both(dt, fmt, hd, integral_constant<int, 2>(), by_tma);
+    };
+    auto by_copies = [&](auto dt, auto fmt, auto hd) {
+        return tma ? by_rows(dt, fmt, hd, std::true_type()) : by_rows(dt, fmt, hd, std::false_type());
+    };
+    auto by_size = [&](auto dt, auto fmt) {
+        return plan.hd == 64    ? by_copies(dt, fmt, integral_constant<int, 64>())
+               : plan.hd == 128 ? by_copies(dt, fmt, integral_constant<int, 128>())
+                                : by_copies(dt, fmt, integral_constant<int, 256>());
+    };
     if (d->dtype == FL_F16)
         return d->format == FL_KV_INT8 ? by_size(integral_constant<int, DT_F16>(), integral_constant<int, FL_KV_INT8>())
                                        : by_size(integral_constant<int, DT_F16>(), integral_constant<int, FL_KV_E4M3>());
