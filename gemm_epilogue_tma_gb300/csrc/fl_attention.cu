@@ -32,6 +32,7 @@
 
 #include "fl_common.cuh"
 #include "fl_host.h"
+#include "fl_quant.cuh"
 
 namespace fl {
 
@@ -156,10 +157,42 @@ struct Layout {
     static constexpr int kSmem = kOffSlot + 16 + 1024;
 };
 
-template <int DT>
-__device__ __forceinline__ bool not_finite2(uint32_t w) {
-    constexpr uint32_t kInf = DT == DT_F16 ? 0x7c00u : 0x7f80u;
-    return (w & kInf) == kInf || ((w >> 16) & kInf) == kInf;
+// Takes what is not finite out of eight values at addr, channels ch .. of a key, and
+// notes the first key of each channel: NaN, inf and -inf apart.
+template <int DT, int DP>
+__device__ __forceinline__ void take_out(uint32_t addr, int ch, int key, int* note) {
+    constexpr uint32_t kInf = Bits16<DT>::kInf;
+    const uint4 x = ld_shared_v4(addr);
+    if (absmax_halves<DT>(absmax8<DT>(x)) < kInf) return;
+    note[3 * DP] = 1;
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+        uint16_t v;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr + 2 * i) : "memory");
+        if ((v & kInf) != kInf) continue;
+        atomicMin(&note[((v & 0x7fffu) != kInf ? 0 : v >> 15 ? 2 : 1) * DP + ch + i], key);
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr + 2 * i), "h"((uint16_t)0) : "memory");
+    }
+}
+// What was taken out, back to a row that sees keys up to `last`: channels ch .. of its output.
+template <int DT, int DP>
+__device__ __forceinline__ uint4 put_back(const uint4& v, int ch, int last, const int* note) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const float inf = __int_as_float(0x7f800000);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float2 f = DTypeOps<DT>::unpack(w[i]);
+        float* const y[2] = {&f.x, &f.y};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int c = ch + 2 * i + e;
+            if (note[c] <= last) *y[e] += __int_as_float(0x7fffffff);
+            if (note[DP + c] <= last) *y[e] += inf;
+            if (note[2 * DP + c] <= last) *y[e] -= inf;
+        }
+        w[i] = DTypeOps<DT>::pack(f.x, f.y);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // DP: head_dim rounded up to 64 or 128.
@@ -184,8 +217,36 @@ __global__ void __launch_bounds__(kThreads, 1) fl_attention_kernel(const __grid_
     const uint32_t fixed = bar0 + 8u * (8 + 4 * NS), drain = fixed + 8u;
     int* const note = reinterpret_cast<int*>(smem + Lay::kOffNote);
 
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full(i), 1);
+            mbar_init(s_full(i), 1);
+            mbar_init(p_full(i), 4);
+            mbar_init(o_full(i), 1);
+        }
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+            mbar_init(v_ready(s), 2);
+            mbar_init(v_raw(s), 1);
+        }
+        mbar_init(fixed, 2);
+        mbar_init(drain, 1);
+        fence_mbar_init();
+    }
+    for (int i = threadIdx.x; i < 3 * DP + 1; i += kThreads) note[i] = i < 3 * DP ? INT_MAX : 0;
+    if (warp == kWarpMma) {
+        tmem_alloc(sbase + Lay::kOffSlot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
     griddep_wait();
     griddep_launch_dependents();
+    auto release = [&] {
+        if (warp == kWarpMma) tmem_dealloc(0u, 512);
+    };
 
     // ------------------------------------------------------------ the CTA's rows
     // (tiles counted from the last: causal rows that see the most keys come first)
@@ -193,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) fl_attention_kernel(const __grid_
     int q0 = 0, lq = p.rows_q, k0 = 0, lk = p.rows_k, row0;  // the sequence; this CTA's first row in it
     if (p.cu_q == nullptr) {
         row0 = ((lq + 2 * kRows - 1) / (2 * kRows) - 1 - index) * (2 * kRows);
-        if (row0 < 0) return;
+        if (row0 < 0) return release();
     } else {
         // every warp finds it for itself, 32 sequences at a time from the last
         int left = index, found = -1, n = 0, first = 0;
@@ -223,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) fl_attention_kernel(const __grid_
                 left -= __shfl_sync(0xffffffffu, up, 31);
             }
         }
-        if (found < 0) return;
+        if (found < 0) return release();
         row0 = (n - 1 - (left - first)) * (2 * kRows);
         k0 = max(0, min(__ldg(p.cu_k + found), p.rows_k));
         lk = max(0, min(__ldg(p.cu_k + found + 1), p.rows_k) - k0);
@@ -247,31 +308,6 @@ __global__ void __launch_bounds__(kThreads, 1) fl_attention_kernel(const __grid_
     auto mended = [&](int load) { return (load & 1) != 0 && load >= 2 * edge; };
     auto parity = [&](int load) { return (uint32_t)((mended(load) ? (load / 2 - edge) / (NS / 2) : load / NS) & 1); };
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(q_full(i), 1);
-            mbar_init(s_full(i), 1);
-            mbar_init(p_full(i), 4);
-            mbar_init(o_full(i), 1);
-        }
-        for (int s = 0; s < NS; ++s) {
-            mbar_init(full(s), 1);
-            mbar_init(empty(s), 1);
-            mbar_init(v_ready(s), 2);
-            mbar_init(v_raw(s), 1);
-        }
-        mbar_init(fixed, 2);
-        mbar_init(drain, 1);
-        fence_mbar_init();
-    }
-    for (int i = threadIdx.x; i < 3 * DP + 1; i += kThreads) note[i] = i < 3 * DP ? INT_MAX : 0;
-    if (warp == kWarpMma) {
-        tmem_alloc(sbase + Lay::kOffSlot, 512);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
     // (all 512 columns: the base is 0)
     // 384 threads are launched with 168 registers: the softmax warps take 216, the others 72 (256 * 216 + 128 * 72 = 384 * 168)
     if (warp >= kWarpMma) {
@@ -359,27 +395,24 @@ __global__ void __launch_bounds__(kThreads, 1) fl_attention_kernel(const __grid_
             if (!__all_sync(0xffffffffu, wait_here(v_raw(s), parity(lv), p.status, p.timeout_ns, 47))) break;
             const int valid = min(kRows, lk - j * kRows);
             const uint32_t base = sbase + Lay::kOffRing + s * Lay::kBlock;
-            for (int e = threadIdx.x - kWarpFix * 32; e < kRows * CH * 8; e += 64) {
-                const int r = e / 8 % kRows, c = e / 8 / kRows, at = e & 7;  // row, 64-channel chunk, 16-byte place in its row
-                const uint32_t addr = base + c * (kRows * 128) + r * 128 + at * 16;
-                if (r >= valid) {
-                    st_shared_v4(addr, 0u, 0u, 0u, 0u);
-                    continue;
+            constexpr int U = 8;  // vectors in flight (one at a time a block took 1.7 us longer than its products)
+#pragma unroll 1
+            for (int e0 = threadIdx.x - kWarpFix * 32; e0 < kRows * CH * 8; e0 += 64 * U) {
+                // vector e: 64-channel chunk e / 1024, row e / 8 % 128, 16-byte place e % 8 in its row
+                uint32_t m = 0;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const uint4 x = ld_shared_v4(base + 16 * (e0 + 64 * u));
+                    m = absmax2<DT>(m, absmax8<DT>(x));
                 }
-                const uint4 x = ld_shared_v4(addr);
-                uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                if (!(not_finite2<DT>(w[0]) || not_finite2<DT>(w[1]) || not_finite2<DT>(w[2]) || not_finite2<DT>(w[3]))) continue;
-                constexpr uint32_t kInf = DT == DT_F16 ? 0x7c00u : 0x7f80u;
-                const int ch = c * 64 + ((at ^ (r & 7)) << 3);  // (the swizzle: place at holds chunk at ^ (row mod 8))
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t v = (w[i / 2] >> (16 * (i & 1))) & 0xffffu;
-                    if ((v & kInf) != kInf) continue;
-                    const int kind = (v & 0x7fffu) != kInf ? 0 : v >> 15 ? 2 : 1;
-                    atomicMin(&note[kind * DP + ch + i], j * kRows + r);
-                    w[i / 2] &= i & 1 ? 0x0000ffffu : 0xffff0000u;
+                // (the rare cases in a loop of their own: the instructions of the common one are few and stay cached)
+                if (absmax_halves<DT>(m) < Bits16<DT>::kInf && valid == kRows) continue;
+#pragma unroll 1
+                for (int e = e0; e < e0 + 64 * U; e += 64) {
+                    const int r = e / 8 % kRows;
+                    if (r >= valid) st_shared_v4(base + 16 * e, 0u, 0u, 0u, 0u);
+                    else take_out<DT, DP>(base + 16 * e, e / (8 * kRows) * 64 + (((e & 7) ^ (r & 7)) << 3), j * kRows + r, note);
                 }
-                note[3 * DP] = 1;
-                st_shared_v4(addr, w[0], w[1], w[2], w[3]);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -469,41 +502,44 @@ __global__ void __launch_bounds__(kThreads, 1) fl_attention_kernel(const __grid_
         if (ok && row0 + i * kRows < lq) {
             const bool any = n > 0 && *reinterpret_cast<volatile int*>(note + 3 * DP) != 0;
             const float f = last >= 0 ? 1.f / (l.x + l.y) : 0.f;
-            uint16_t* out = p.out + (long long)(q0 + r) * p.o_row + (long long)head * p.o_head;
-#pragma unroll
+            // A warp's rows go through its part of its tile of q, which no product reads any more, so that
+            // neighbouring lanes store neighbouring 16 bytes (a row per lane: 5 us instead of 1).
+            const uint32_t stage = sbase + i * Lay::kBlock + (warp & 3) * 32 * (DP * 2);
+#pragma unroll 1
             for (int c = 0; c < DP / 32; ++c) {
                 float o[32];
                 if (n > 0) {
                     tmem_ld_32x32b_x32(o_col + 32u * c, reinterpret_cast<uint32_t(&)[32]>(o));
                     tmem_ld_wait();
                 }
-                if (any)
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        // what the two warps took out, to the rows that see it
-                        const int ch = 32 * c + e;
-                        if (note[ch] <= last) o[e] += __int_as_float(0x7fffffff);
-                        if (note[DP + ch] <= last) o[e] -= kNone;
-                        if (note[2 * DP + ch] <= last) o[e] += kNone;
-                    }
-                if (r < lq)
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        if (32 * c + e >= p.head_dim) continue;
-                        uint4 v = make_uint4(Ops::pack(o[e] * f, o[e + 1] * f), Ops::pack(o[e + 2] * f, o[e + 3] * f),
-                                             Ops::pack(o[e + 4] * f, o[e + 5] * f), Ops::pack(o[e + 6] * f, o[e + 7] * f));
-                        if (last < 0) v = make_uint4(0u, 0u, 0u, 0u);
-                        *reinterpret_cast<uint4*>(out + 32 * c + e) = v;
-                    }
+                for (int e = 0; e < 32; e += 8) {
+                    uint4 v = make_uint4(Ops::pack(o[e] * f, o[e + 1] * f), Ops::pack(o[e + 2] * f, o[e + 3] * f),
+                                         Ops::pack(o[e + 4] * f, o[e + 5] * f), Ops::pack(o[e + 6] * f, o[e + 7] * f));
+                    if (last < 0) v = make_uint4(0u, 0u, 0u, 0u);
+                    const int chunk = 4 * c + e / 8;
+                    st_shared_v4(stage + lane * (DP * 2) + ((chunk ^ (lane & 7)) << 4), v.x, v.y, v.z, v.w);
+                }
+            }
+            __syncwarp();
+            uint16_t* out = p.out + (long long)head * p.o_head;
+            constexpr int C = DP / 8, R = 32 / C;  // chunks of a row, rows of a store
+            const int chunk = lane % C, first = r - lane;
+#pragma unroll 4
+            for (int k = 0; k < 32; k += R) {
+                const int row = k + lane / C;
+                uint4 v = ld_shared_v4(stage + row * (DP * 2) + ((chunk ^ (row & 7)) << 4));
+                const int sees = __shfl_sync(0xffffffffu, last, row);
+                if (any) v = put_back<DT, DP>(v, chunk * 8, sees, note);
+                if (first + row < lq && chunk * 8 < p.head_dim)
+                    *reinterpret_cast<uint4*>(out + (long long)(q0 + first + row) * p.o_row + chunk * 8) = v;
             }
         }
         tc_fence_before();
     }
     __syncthreads();
-    if (warp == kWarpMma) {
-        tc_fence_after();
-        tmem_dealloc(0u, 512);
-    }
+    tc_fence_after();
+    release();
 }
 
 }  // namespace
