@@ -25,7 +25,12 @@
 // of the others and note the first key of each channel where it stood, and the
 // epilogue adds it to the rows that see that key.
 //
+// Few rows over many keys: a cluster of up to 8 CTAs takes the same rows, each a run of
+// the blocks, and adds the parts through distributed shared memory, in order, each CTA
+// for its share of the rows.
+//
 // Every mbarrier wait is bounded as in the other kernels.
+#include <algorithm>
 #include <climits>
 
 #include <type_traits>
@@ -51,6 +56,7 @@ struct AttnParams {
     const int* cu_q;
     const int* cu_k;
     int rows_q, rows_k, heads_q, group, head_dim, n_seqs, causal;
+    int splits;  // CTAs of a cluster
     float c;  // scale * log2(e)
     int* status;
     unsigned long long timeout_ns;
@@ -155,6 +161,10 @@ struct Layout {
     static constexpr int kBars = 2 + 4 * kSlots + 2 + 2 + 2 + 2;
     static constexpr int kOffSlot = kOffBar + kBars * 8;
     static constexpr int kSmem = kOffSlot + 16 + 1024;
+    // parts of a cluster, in place of q, k and v: [256][kPitch] sums, [256] maxima and sums of weights
+    static constexpr int kPitch = DP + 4;
+    static constexpr int kOffMl = 2 * kRows * kPitch * 4;
+    static_assert(kOffMl + 2 * kRows * 8 <= kOffNote, "parts");
 };
 
 // Takes what is not finite out of eight values at addr, channels ch .. of a key, and
@@ -250,7 +260,8 @@ __global__ void __launch_bounds__(kThreads, 1) fl_attention_kernel(const __grid_
 
     // ------------------------------------------------------------ the CTA's rows
     // (tiles counted from the last: causal rows that see the most keys come first)
-    const int head = blockIdx.x % p.heads_q, index = blockIdx.x / p.heads_q;
+    const int rank = p.splits > 1 ? (int)cluster_rank() : 0, work = blockIdx.x / p.splits;
+    const int head = work % p.heads_q, index = work / p.heads_q;
     int q0 = 0, lq = p.rows_q, k0 = 0, lk = p.rows_k, row0;  // the sequence; this CTA's first row in it
     if (p.cu_q == nullptr) {
         row0 = ((lq + 2 * kRows - 1) / (2 * kRows) - 1 - index) * (2 * kRows);
@@ -260,10 +271,12 @@ __global__ void __launch_bounds__(kThreads, 1) fl_attention_kernel(const __grid_
         int left = index, found = -1, n = 0, first = 0;
         for (int e = p.n_seqs; e > 0 && found < 0; e -= 32) {
             const int b = e - 1 - lane;
-            int a = 0, z = 0;
+            int a = 0, z = 0, ka = 0, kz = 0;
             if (b >= 0) {
                 a = max(0, min(__ldg(p.cu_q + b), p.rows_q));
                 z = max(a, min(__ldg(p.cu_q + b + 1), p.rows_q));
+                ka = max(0, min(__ldg(p.cu_k + b), p.rows_k));
+                kz = max(ka, min(__ldg(p.cu_k + b + 1), p.rows_k));
             }
             const int tiles = (z - a + 2 * kRows - 1) / (2 * kRows);
             int up = tiles;
@@ -278,6 +291,8 @@ __global__ void __launch_bounds__(kThreads, 1) fl_attention_kernel(const __grid_
                 found = e - 1 - l;
                 q0 = __shfl_sync(0xffffffffu, a, l);
                 lq = __shfl_sync(0xffffffffu, z, l) - q0;
+                k0 = __shfl_sync(0xffffffffu, ka, l);
+                lk = __shfl_sync(0xffffffffu, kz, l) - k0;
                 n = __shfl_sync(0xffffffffu, tiles, l);
                 first = __shfl_sync(0xffffffffu, up, l) - n;
             } else {
@@ -286,8 +301,6 @@ __global__ void __launch_bounds__(kThreads, 1) fl_attention_kernel(const __grid_
         }
         if (found < 0) return release();
         row0 = (n - 1 - (left - first)) * (2 * kRows);
-        k0 = max(0, min(__ldg(p.cu_k + found), p.rows_k));
-        lk = max(0, min(__ldg(p.cu_k + found + 1), p.rows_k) - k0);
     }
     // row r of the sequence sees keys 0 .. r + shift, and lk - 1 at most
     const int shift = p.causal ? lk - lq : lk;
@@ -297,9 +310,12 @@ __global__ void __launch_bounds__(kThreads, 1) fl_attention_kernel(const __grid_
         const long long end = min((long long)lk, (long long)last + shift + 1);
         return end <= 0 ? 0 : (int)((end + kRows - 1) / kRows);
     };
-    const int n0 = blocks_of(0), n1 = blocks_of(1), nb = max(n0, n1);
+    // this CTA's blocks, of all of them: from j0 on, n0 and n1 for the two tiles, counted from there
+    const int all = max(blocks_of(0), blocks_of(1));
+    const int j0 = (int)((long long)all * rank / p.splits), nb = (int)((long long)all * (rank + 1) / p.splits) - j0;
+    const int n0 = max(0, min(blocks_of(0) - j0, nb)), n1 = max(0, min(blocks_of(1) - j0, nb));
     // from this block on some row does not see every key of it, or it is not whole
-    const int edge = (int)(max(0ll, min((long long)lk, (long long)row0 + shift + 1)) / kRows);
+    const int edge = max(0, (int)(max(0ll, min((long long)lk, (long long)row0 + shift + 1)) / kRows) - j0);
     const int kv_head = head / p.group;
     // Load number `load` of k and v in turn (k of block j is 2 j, v 2 j + 1) is full
     // on full(slot), or for values of blocks from `edge` on, which are mended before
@@ -323,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) fl_attention_kernel(const __grid_
             auto next = [&](const CUtensorMap* m, int block) {
                 const int s = issued % NS;
                 if (!(ok = wait_here(empty(s), (uint32_t)((issued / NS) & 1) ^ 1u, p.status, p.timeout_ns, 40))) return;
-                load(m, sbase + Lay::kOffRing + s * Lay::kBlock, mended(issued) ? v_raw(s) : full(s), kv_head, k0 + block * kRows);
+                load(m, sbase + Lay::kOffRing + s * Lay::kBlock, mended(issued) ? v_raw(s) : full(s), kv_head, k0 + (j0 + block) * kRows);
                 ++issued;
             };
             if (nb > 0) {
@@ -393,9 +409,12 @@ __global__ void __launch_bounds__(kThreads, 1) fl_attention_kernel(const __grid_
         for (int j = edge; j < nb; ++j) {
             const int lv = 2 * j + 1, s = lv % NS;
             if (!__all_sync(0xffffffffu, wait_here(v_raw(s), parity(lv), p.status, p.timeout_ns, 47))) break;
-            const int valid = min(kRows, lk - j * kRows);
+            const int first_key = (j0 + j) * kRows, valid = min(kRows, lk - first_key);
             const uint32_t base = sbase + Lay::kOffRing + s * Lay::kBlock;
             constexpr int U = 8;  // vectors in flight (one at a time a block took 1.7 us longer than its products)
+            for (int c = 0; c < CH; ++c)
+                for (int e = valid * 8 + (int)threadIdx.x - kWarpFix * 32; e < kRows * 8; e += 64)
+                    st_shared_v4(base + c * (kRows * 128) + 16 * e, 0u, 0u, 0u, 0u);
 #pragma unroll 1
             for (int e0 = threadIdx.x - kWarpFix * 32; e0 < kRows * CH * 8; e0 += 64 * U) {
                 // vector e: 64-channel chunk e / 1024, row e / 8 % 128, 16-byte place e % 8 in its row
@@ -403,15 +422,15 @@ __global__ void __launch_bounds__(kThreads, 1) fl_attention_kernel(const __grid_
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const uint4 x = ld_shared_v4(base + 16 * (e0 + 64 * u));
-                    m = absmax2<DT>(m, absmax8<DT>(x));
+                    if ((e0 + 64 * u) / 8 % kRows < valid) m = absmax2<DT>(m, absmax8<DT>(x));
                 }
                 // (the rare cases in a loop of their own: the instructions of the common one are few and stay cached)
-                if (absmax_halves<DT>(m) < Bits16<DT>::kInf && valid == kRows) continue;
+                if (absmax_halves<DT>(m) < Bits16<DT>::kInf) continue;
 #pragma unroll 1
                 for (int e = e0; e < e0 + 64 * U; e += 64) {
                     const int r = e / 8 % kRows;
-                    if (r >= valid) st_shared_v4(base + 16 * e, 0u, 0u, 0u, 0u);
-                    else take_out<DT, DP>(base + 16 * e, e / (8 * kRows) * 64 + (((e & 7) ^ (r & 7)) << 3), j * kRows + r, note);
+                    if (r < valid)
+                        take_out<DT, DP>(base + 16 * e, e / (8 * kRows) * 64 + (((e & 7) ^ (r & 7)) << 3), first_key + r, note);
                 }
             }
             fence_proxy_async_smem();
@@ -438,8 +457,8 @@ __global__ void __launch_bounds__(kThreads, 1) fl_attention_kernel(const __grid_
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_col + 32u * c, reinterpret_cast<uint32_t(&)[32]>(s[c]));
             tmem_ld_wait();
-            if (j * kRows + kRows - 1 > warp_last) {
-                const int seen = last - j * kRows;
+            if ((j0 + j) * kRows + kRows - 1 > warp_last) {
+                const int seen = last - (j0 + j) * kRows;
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -499,7 +518,37 @@ __global__ void __launch_bounds__(kThreads, 1) fl_attention_kernel(const __grid_
             tc_fence_after();
             if (ok) ok = __all_sync(0xffffffffu, wait_here(fixed, 0, p.status, p.timeout_ns, 50));
         }
-        if (ok && row0 + i * kRows < lq) {
+        if (p.splits > 1) {
+            // this CTA's part: sums as they are, in fp32, once no product reads shared memory any more
+            named_bar_sync(1, 2 * kRows);
+            const uint32_t part = sbase + threadIdx.x * (Lay::kPitch * 4);
+#pragma unroll 1
+            for (int c = 0; c < DP / 32; ++c) {
+                float o[32];
+                if (n > 0) {
+                    tmem_ld_32x32b_x32(o_col + 32u * c, reinterpret_cast<uint32_t(&)[32]>(o));
+                    tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                    st_shared_v4(part + (32 * c + e) * 4, __float_as_uint(o[e]), __float_as_uint(o[e + 1]), __float_as_uint(o[e + 2]),
+                                 __float_as_uint(o[e + 3]));
+            }
+            if (n > 0 && *reinterpret_cast<volatile int*>(note + 3 * DP) != 0) {
+#pragma unroll 1
+                for (int ch = 0; ch < DP; ++ch) {
+                    float y = ld_shared_f32(part + 4 * ch);
+                    if (note[ch] <= last) y += __int_as_float(0x7fffffff);
+                    if (note[DP + ch] <= last) y -= kNone;
+                    if (note[2 * DP + ch] <= last) y += kNone;
+                    st_shared_f32(part + 4 * ch, y);
+                }
+            }
+            *reinterpret_cast<float2*>(smem + Lay::kOffMl + threadIdx.x * 8) = make_float2(m, l.x + l.y);
+        } else if (ok && row0 + i * kRows < lq) {
             const bool any = n > 0 && *reinterpret_cast<volatile int*>(note + 3 * DP) != 0;
             const float f = last >= 0 ? 1.f / (l.x + l.y) : 0.f;
             // A warp's rows go through its part of its tile of q, which no product reads any more, so that
@@ -540,6 +589,51 @@ __global__ void __launch_bounds__(kThreads, 1) fl_attention_kernel(const __grid_
     __syncthreads();
     tc_fence_after();
     release();
+    if (p.splits > 1) {
+        cluster_barrier_sync();
+        // each CTA finishes its share of the rows: a row to a warp, DP / 32 channels to a lane
+        constexpr int C = DP / 32, kMost = 8;
+        const int rows = min(2 * kRows, lq - row0);
+        const float kNone = __int_as_float(0xff800000);
+        for (int r = rows * rank / p.splits + warp; r < rows * (rank + 1) / p.splits; r += kThreads / 32) {
+            float ml[2] = {kNone, 0.f};
+            if (lane < p.splits)
+                asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(ml[0]), "=f"(ml[1]) : "r"(mapa_cluster(sbase + Lay::kOffMl + r * 8, lane)) : "memory");
+            float o[kMost][C];
+#pragma unroll
+            for (int c = 0; c < kMost; ++c) {
+                if (c >= p.splits) continue;
+                const uint32_t at = mapa_cluster(sbase + (r * Lay::kPitch + lane * C) * 4, c);
+                if constexpr (C == 4)
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(o[c][0]), "=f"(o[c][1]), "=f"(o[c][2]), "=f"(o[c][3]) : "r"(at) : "memory");
+                else
+                    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(o[c][0]), "=f"(o[c][1]) : "r"(at) : "memory");
+            }
+            float top = ml[0];
+#pragma unroll
+            for (int w = 4; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+            top = __shfl_sync(0xffffffffu, top, 0);
+            const float weight = ml[0] == kNone ? 0.f : ex2(ml[0] - top);
+            float sum = 0.f, y[C] = {};
+#pragma unroll
+            for (int c = 0; c < kMost; ++c) {
+                if (c >= p.splits) continue;
+                const float w = __shfl_sync(0xffffffffu, weight, c);
+                sum = fmaf(__shfl_sync(0xffffffffu, ml[1], c), w, sum);
+#pragma unroll
+                for (int e = 0; e < C; ++e) y[e] = fmaf(o[c][e], w, y[e]);
+            }
+            const bool sees = min((long long)lk - 1, (long long)row0 + r + shift) >= 0;
+            const float f = sees ? 1.f / sum : 0.f;
+            uint16_t* out = p.out + (long long)(q0 + row0 + r) * p.o_row + (long long)head * p.o_head + lane * C;
+            if (lane * C >= p.head_dim) continue;
+            if constexpr (C == 4)
+                *reinterpret_cast<uint2*>(out) = sees ? make_uint2(Ops::pack(y[0] * f, y[1] * f), Ops::pack(y[2] * f, y[3] * f)) : make_uint2(0u, 0u);
+            else
+                *reinterpret_cast<uint32_t*>(out) = sees ? Ops::pack(y[0] * f, y[1] * f) : 0u;
+        }
+        cluster_barrier_sync();  // (the others have read this CTA's part)
+    }
 }
 
 }  // namespace
@@ -565,7 +659,8 @@ extern "C" fl_status fl_attention(const fl_attention_desc* d, void* stream) {
     if (d->n_seqs > 1 << 30) return fail(FL_ERR_UNSUPPORTED, "%s: more than 2^30 sequences", what);
     // 256-row tiles at most: every sequence with rows has one that may be short
     const long long seqs = d->rows_q < d->n_seqs ? d->rows_q : d->n_seqs;
-    const long long tiles = d->cu_q == nullptr ? (d->rows_q + 2ll * kRows - 1) / (2 * kRows) : d->rows_q / (2 * kRows) + seqs;
+    const long long tiles = d->cu_q == nullptr ? (d->rows_q + 2ll * kRows - 1) / (2 * kRows)
+                                               : (d->rows_q + (2ll * kRows - 1) * seqs) / (2 * kRows);
     if (tiles * d->heads_q >= (1ll << 31) || d->rows_q > INT_MAX - 4 * kRows || d->rows_k > INT_MAX - 4 * kRows)
         return fail(FL_ERR_UNSUPPORTED, "%s: too many rows", what);
     if (d->rows_q == 0) return host::ok();
@@ -623,6 +718,11 @@ extern "C" fl_status fl_attention(const fl_attention_desc* d, void* stream) {
     p.group = d->heads_q / d->heads_k, p.head_dim = d->head_dim, p.n_seqs = d->n_seqs, p.causal = d->causal != 0;
     p.c = d->scale * 1.44269504088896341f;
     p.status = ctx.status, p.timeout_ns = ctx.timeout_ns;
+    // Fewer CTAs than half the multiprocessors: clusters, while each CTA keeps four blocks of keys
+    // (of a sequence of average length).
+    const long long blocks = (d->rows_k / d->n_seqs + kRows - 1) / kRows;
+    p.splits = 1;
+    while (p.splits < 8 && tiles * d->heads_q * p.splits * 2 <= ctx.sms && blocks >= 8 * p.splits) p.splits *= 2;
     auto go = [&](auto dt, auto dp) -> fl_status {
         constexpr int DT = decltype(dt)::value, DP = decltype(dp)::value;
         static std::atomic<unsigned long long> done{0};
@@ -630,8 +730,8 @@ extern "C" fl_status fl_attention(const fl_attention_desc* d, void* stream) {
         static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
         const cudaError_t e = host::allow_smem(fl_attention_kernel<DT, DP>, bytes, ctx.device, done);
         if (e != cudaSuccess) return host::fail(FL_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-        return host::launched(host::launch(fl_attention_kernel<DT, DP>, dim3((unsigned)(tiles * d->heads_q)), kThreads, bytes,
-                                           ctx.pdl, static_cast<cudaStream_t>(stream), p),
+        return host::launched(host::launch_cluster(fl_attention_kernel<DT, DP>, dim3((unsigned)(tiles * d->heads_q * p.splits)), kThreads,
+                                                   bytes, ctx.pdl, p.splits, static_cast<cudaStream_t>(stream), p),
                               what);
     };
     using std::integral_constant;

@@ -108,6 +108,25 @@ cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, int pdl, cuda
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// The same in clusters of `cluster` CTAs along x.
+template <typename Kern, typename... Args>
+cudaError_t launch_cluster(Kern kern, dim3 grid, int threads, size_t smem, int pdl, int cluster, cudaStream_t stream,
+                           const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute a[2];
+    a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a[0].val.programmaticStreamSerializationAllowed = pdl;
+    a[1].id = cudaLaunchAttributeClusterDimension;
+    a[1].val.clusterDim.x = (unsigned)cluster, a[1].val.clusterDim.y = 1, a[1].val.clusterDim.z = 1;
+    cfg.attrs = a;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 }  // namespace host
 
 // The argument checks of fl_rope and fl_kv_write alone (fl_layer_attach_cache).

@@ -427,18 +427,7 @@ fl_status check_cache(const char* what, const fl_kv_pages* c) {
 
 template <bool FORK>
 fl_status launch_pages(const char* what, const PagesParams& p, const host::LaunchContext& ctx, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kCluster);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute a[2];
-    a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    a[0].val.programmaticStreamSerializationAllowed = ctx.pdl;
-    a[1].id = cudaLaunchAttributeClusterDimension;
-    a[1].val.clusterDim.x = kCluster, a[1].val.clusterDim.y = 1, a[1].val.clusterDim.z = 1;
-    cfg.attrs = a;
-    cfg.numAttrs = 2;
-    return host::launched(cudaLaunchKernelEx(&cfg, fl_kv_pages_kernel<FORK>, p), what);
+    return host::launched(host::launch_cluster(fl_kv_pages_kernel<FORK>, dim3(kCluster), kThreads, 0, ctx.pdl, kCluster, stream, p), what);
 }
 
 PagesParams pages_params(const fl_kv_pages* c, int* refs, const int* lengths, void* workspace, int* range) {

@@ -113,6 +113,42 @@ def test_attention(dt, hq, hkv, D, lq, lk, is_causal):
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("hq,hkv,D,lq,lk", [
+    (2, 1, 64, [1], [4096]),
+    (1, 1, 128, [130], [2100]),
+    (2, 2, 96, [300], [5000]),
+    (3, 1, 128, [7, 0, 200], [3000, 9, 4100]),
+    (4, 4, 64, [257, 1], [2000, 3]),
+    (32, 8, 128, [9], [1030]),
+])
+@pytest.mark.parametrize("is_causal", [True, False])
+def test_attention_few_rows_over_many_keys(dt, hq, hkv, D, lq, lk, is_causal):
+    """The keys are split over clusters, of sequences that have many and of ones that have few."""
+    got, ref, (*_, floor) = attention_case(dt, hq, hkv, D, lq, lk, is_causal, sum(lk) + D)
+    check(got, ref, U[dt], U[dt], 2.0 ** -20, floor, f"{lq} {lk}")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_attention_split_keys_that_are_not_finite(D, bad):
+    rng = gen(66, D)
+    n, m = 200, 2500
+    q, k, v = (put(rng.standard_normal((x, 1, D)), "bf16") for x in (n, m, m))
+    clean = fl.attention(q, k, v)
+    at = m - 90                                    # seen by rows 110 and up
+    v[at, 0, 3] = bad
+    got = fl.attention(q, k, v)
+    fl.device_status()
+    hit = got[110:, 0, 3]
+    assert torch.equal(got[:110], clean[:110]) and torch.equal(got[..., 4:], clean[..., 4:])
+    assert (torch.isnan(hit) if bad != bad else hit == bad).all()
+    # rows without keys beside split ones
+    got = fl.attention(q, k, v, cu_q=ints([0, 150, 200]), cu_k=ints([0, 2400, 2400]))
+    assert (got[150:] == 0).all() and torch.isfinite(got[:150]).all()
+    fl.device_status()
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
 def test_attention_large_scores(dt):
     """Scores of some hundreds in both directions, the largest of a row coming late: the running maximum moves often."""
     rng = gen(41)
