@@ -999,7 +999,7 @@ fl_status encode_heads(CUtensorMap* m, int dt, const void* ptr, uint64_t dim, ui
 }
 
 fl_status encode_pages(CUtensorMap* m, const void* ptr, uint64_t dim, uint64_t heads, uint64_t page_size, uint64_t pages,
-                       uint32_t box_channels, uint32_t box_rows) {
+                       uint32_t box_channels, uint32_t box_rows, bool swizzle) {
     EncodeTiledFn fn = encode_fn();
     if (fn == nullptr) return ::fail(FL_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
     cuuint64_t dims[4] = {dim, heads, page_size, pages};
@@ -1008,7 +1008,8 @@ fl_status encode_pages(CUtensorMap* m, const void* ptr, uint64_t dim, uint64_t h
     cuuint32_t estr[4] = {1, 1, 1, 1};
     const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(ptr), dims, strides, box, estr,
                           CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          box_channels == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                          !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE
+                          : box_channels == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return ::fail(FL_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for a cache of %llu pages of [%llu, %llu, %llu]", (int)r,

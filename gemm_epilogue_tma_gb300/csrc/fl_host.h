@@ -77,10 +77,10 @@ fl_status encode_heads(CUtensorMap* m, int dt, const void* ptr, uint64_t dim, ui
 
 // Tensor map of the codes of a paged cache [pages, page_size, heads, dim] bytes, dim a
 // multiple of 16: coordinates (channel, head, row in the page, page), boxes of
-// `box_channels` (64 or 128) channels of box_rows rows of one head, with the swizzle
-// of that width, zero fill out of range.
+// `box_channels` (64 or 128) channels of box_rows rows of one head, as they are or with the
+// swizzle of that width, zero fill out of range.
 fl_status encode_pages(CUtensorMap* m, const void* ptr, uint64_t dim, uint64_t heads, uint64_t page_size, uint64_t pages,
-                       uint32_t box_channels, uint32_t box_rows);
+                       uint32_t box_channels, uint32_t box_rows, bool swizzle);
 
 // Lets `kern` use `bytes` of dynamic shared memory on `device`; asked of the
 // runtime once per device (`done`: its bit is set).

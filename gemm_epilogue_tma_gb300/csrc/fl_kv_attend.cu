@@ -28,74 +28,23 @@
 // are persistent and take every gridDim-th piece. L is the one of sixteen that makes the
 // rounds of CTAs shortest; every CTA finds it, and its pieces, from the lengths, which
 // only the GPU knows. Pieces of a split sequence are joined by a second launch, in order.
-#include <cuda_fp16.h>
-
 #include <algorithm>
 #include <type_traits>
 
-#include "fl_common.cuh"
-#include "fl_host.h"
+#include "fl_kv_attend.cuh"
 
 namespace fl {
 
 namespace {
 
+using namespace attend;
+
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStep = 16;               // positions of a warp's step
-constexpr int kTile = kStep * kWarps;   // positions of a tile
-constexpr int kResident = 304;          // CTAs at work at once: two on each of 152 multiprocessors
-constexpr int kLeast = 2;               // tiles of a piece at least
-constexpr int kSlots = 2 * kResident;   // pieces of split sequences at most: L is T / kResident at least, and each has more than L / 2 tiles
-constexpr int kUnits = kSlots / 2;      // row blocks and heads of split sequences at most
-constexpr int kStart = 3, kJoin = 3;    // tiles that a piece's start and end, and the second launch, take as long as
-constexpr float kLazy = 8.f;            // a maximum is moved once it is exceeded by 2^8
+constexpr int kResident = 304;  // CTAs at work at once: two on each of 152 multiprocessors
+static_assert(kTile == kStep * kWarps, "a tile is a step of all warps");
+constexpr int kRowsLimit = 32;  // rows of a sequence and key head (of average length) from which the kernel for many rows is taken
 
-struct AttendParams {
-    CUtensorMap tm[2];  // k_cache, v_cache: boxes of 64 or 128 channels of box_rows positions of one head and page
-    const uint16_t* q;
-    uint16_t* out;
-    long long q_row, q_head, o_row, o_head;
-    const uint8_t* cache[2];
-    const float* scale[2];
-    const int* page_table;
-    const int* cu_rows;
-    const int* start;
-    const uint8_t* tree;
-    long long table_stride, tree_stride;
-    int tree_cols;
-    int rows, heads, group, head_dim, page_size, page_shift, n_pages, n_seqs, table_pages;
-    int box_log;       // log2 of box_rows
-    float log2_scale;  // scale * log2(e)
-    float* part;       // [kSlots][M][HD] sums, [kSlots][M][4] maxima, sum of weights, whether a position was seen; Units
-    int* range;
-    int* status;
-    unsigned long long timeout_ns;
-};
-
-// What the second launch joins.
-struct Unit {
-    int row0, n, first, head, pieces, slot, step, unused;  // the sequence's rows; the block's first row; slots from one piece to the next
-};
-struct Units {
-    int count, unused[7];
-    Unit unit[kUnits];
-};
-template <int HD, int QT>
-__device__ __forceinline__ Units* units_of(const AttendParams& p) {
-    return reinterpret_cast<Units*>(p.part + (long long)kSlots * 8 * QT * (HD + 4));
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float lg2(float x) {
-    float y;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -104,21 +53,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two codes as fp16. int8: in bytes 0 and 2 of x (the others are ignored): 1024 + 128 +
-// code in the mantissa, less 1152. e4m3: in the low 16 bits, by the conversion
-// instruction (moving the bits takes three logical operations, which are issued at half rate:
-// 16 contexts of 3750 positions 44 -> 38 us).
-template <int FMT>
-__device__ __forceinline__ uint32_t widen(uint32_t x) {
-    uint32_t r;
-    if constexpr (FMT == FL_KV_INT8) {
-        const uint32_t m = (x & 0x00ff00ffu) ^ 0x64806480u;
-        asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(0x64806480u));
-    } else {
-        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(x));
-    }
-    return r;
-}
 // The four codes of a word in two pairs, the first product's order of channels: int8 0 and 2, 1
 // and 3; e4m3 0 and 1, 2 and 3. (q is laid out to match: kPair.)
 template <int FMT>
@@ -137,211 +71,6 @@ __device__ __forceinline__ uint32_t widen_pair(uint32_t lo, uint32_t hi, int b) 
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-// Arrives on the barrier when this thread's copies so far have landed.
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z, int w) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
-        : "memory");
-}
-
-// A sequence's share of the work.
-struct Seq {
-    int row0, n;         // its rows of q
-    long long from;      // start: the position of its first row
-    int keys;            // positions to be read: 0 .. keys - 1
-    int blocks, tiles;   // row blocks of M, tiles of its keys
-};
-__device__ __forceinline__ Seq seq_of(const AttendParams& p, int b, int M) {
-    Seq s;
-    if (p.cu_rows == nullptr) {
-        s.row0 = b;
-        s.n = b < p.rows ? 1 : 0;
-    } else {
-        s.row0 = max(0, min(__ldg(p.cu_rows + b), p.rows));
-        s.n = max(0, min(__ldg(p.cu_rows + b + 1), p.rows) - s.row0);
-    }
-    s.from = p.start != nullptr ? __ldg(p.start + b) : 0;
-    const long long end = min(s.from + s.n, (long long)p.table_pages * p.page_size);
-    s.keys = (int)max(0ll, min(end, 0x7fffff00ll));
-    s.blocks = (s.n * p.group + M - 1) / M;
-    s.tiles = (s.keys + kTile - 1) / kTile;
-    return s;
-}
-
-struct Piece {
-    int seq, block, head, k, pieces, slot;  // piece k of `pieces`; its place among the pieces of split sequences
-    int units;                              // row blocks and heads of split sequences in front of this one's
-};
-
-// Candidates of L: T / kResident times these, / 8, and no split at all. (More than 8
-// makes room for the pieces that lengths which are no multiples of L leave over.)
-constexpr int kCandidates = 5;
-__device__ constexpr int kTimes[kCandidates + 1] = {8, 9, 11, 14, 20, 0};
-constexpr uint32_t kWhole = 1u << 30;
-
-// The pieces of all sequences, counted by all threads of a CTA. Order: sequence,
-// piece, row block, head, so that CTAs next to one another read the heads of the same positions.
-struct Pieces {
-    const AttendParams& p;
-    int M, per, b0, b1;      // this thread's sequences
-    Seq only;                // with one sequence to a thread it is read once
-    uint32_t L;
-    int W;                   // warps to a piece: 8, or less where no sequence is split
-    uint32_t fn, fs, fu, n;  // pieces, slots and units in front of this thread's sequences; its pieces
-    uint32_t units;          // of all split sequences
-    Piece (*found)[kWarps];  // [2], in shared memory: the pieces of this round and the next, and their sequences
-    Seq (*of)[kWarps];
-
-    __device__ __forceinline__ Seq seq(int b) const { return per == 1 ? only : seq_of(p, b, M); }
-    __device__ __forceinline__ uint32_t pieces(const Seq& s) const { return max(1u, ((uint32_t)s.tiles + L - 1) / L); }
-
-    // few: whether pieces may be given to fewer warps than a CTA has
-    __device__ __forceinline__ Pieces(const AttendParams& params, int rows, bool few) : p(params), M(rows) {
-        __shared__ Piece pieces_at[2][kWarps];
-        __shared__ Seq seqs_at[2][kWarps];
-        found = pieces_at, of = seqs_at;
-        if (threadIdx.x < kWarps) found[0][threadIdx.x].seq = -1;
-        __shared__ unsigned long long sum_t[kWarps];
-        __shared__ uint32_t top_t[kWarps], pieces_of[kWarps][kCandidates + 1];
-        __shared__ uint32_t sum_n[kWarps], sum_s[kWarps], sum_u[kWarps];
-        per = (p.n_seqs + kThreads - 1) / kThreads;
-        b0 = min(p.n_seqs, (int)threadIdx.x * per), b1 = min(p.n_seqs, b0 + per);
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        unsigned long long t = 0;
-        uint32_t top = 0;
-        only.blocks = only.tiles = 0;
-        for (int b = b0; b < b1; ++b) {
-            only = seq_of(p, b, M);
-            t += (unsigned long long)only.tiles * only.blocks * p.heads;
-            if (only.blocks > 0) top = max(top, (uint32_t)only.tiles);
-        }
-        t = __reduce_add_sync(0xffffffffu, (uint32_t)t & 0xffffffu) +
-            ((unsigned long long)__reduce_add_sync(0xffffffffu, (uint32_t)(t >> 24)) << 24);
-        top = __reduce_max_sync(0xffffffffu, top);
-        if (lane == 0) sum_t[warp] = t, top_t[warp] = top;
-        __syncthreads();
-        t = 0, top = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) t += sum_t[w], top = max(top, top_t[w]);
-        L = kWhole;
-        if (top > kLeast) {
-            // what each candidate costs: the rounds, times their longest piece and a start
-            uint32_t at[kCandidates + 1], k[kCandidates + 1];
-#pragma unroll
-            for (int c = 0; c <= kCandidates; ++c) {
-                const unsigned long long want = (t * kTimes[c] + 8 * kResident - 1) / (8 * kResident);
-                at[c] = c == kCandidates ? kWhole : (uint32_t)max((unsigned long long)kLeast, min(want, (unsigned long long)kWhole));
-                k[c] = 0;
-                const float inv = 1.f / (float)at[c];
-                for (int b = b0; b < b1; ++b) {
-                    const Seq s = seq(b);
-                    // (an estimate: the quotient is not exact next to a whole number)
-                    k[c] += (uint32_t)s.blocks * p.heads * (uint32_t)fmaxf(1.f, ceilf((float)s.tiles * inv));
-                }
-            }
-#pragma unroll
-            for (int c = 0; c <= kCandidates; ++c) k[c] = __reduce_add_sync(0xffffffffu, k[c]);
-            if (lane == 0) {
-#pragma unroll
-                for (int c = 0; c <= kCandidates; ++c) pieces_of[warp][c] = k[c];
-            }
-            __syncthreads();
-            uint32_t best = 0xffffffffu;
-#pragma unroll
-            for (int c = 0; c <= kCandidates; ++c) {
-                uint32_t all = 0;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) all += pieces_of[w][c];
-                const uint32_t cost = (all + kResident - 1) / kResident * (min(at[c], top) + kStart) + (at[c] < top ? kJoin : 0);
-                if (cost < best) best = cost, L = at[c];
-            }
-            if (L >= top) L = kWhole;
-        }
-        uint32_t sl = 0, un = 0;
-        n = 0;
-        for (int b = b0; b < b1; ++b) {
-            const Seq s = seq(b);
-            const uint32_t u = (uint32_t)s.blocks * p.heads, k = pieces(s);
-            n += u * k;
-            if (k > 1) sl += u * k, un += u;
-        }
-        fn = n, fs = sl, fu = un;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t a = __shfl_up_sync(0xffffffffu, fn, o), c = __shfl_up_sync(0xffffffffu, fs, o), d = __shfl_up_sync(0xffffffffu, fu, o);
-            if (lane >= o) fn += a, fs += c, fu += d;
-        }
-        if (lane == 31) sum_n[warp] = fn, sum_s[warp] = fs, sum_u[warp] = fu;
-        fn -= n, fs -= sl, fu -= un;
-        __syncthreads();
-        units = 0;
-        uint32_t all = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) fn += sum_n[w], fs += sum_s[w], fu += sum_u[w];
-            units += sum_u[w], all += sum_n[w];
-        }
-        W = kWarps;
-        if (few && L == kWhole) {
-            // of 8, 4, 2 and 1 warps to a piece, the least rounds * (steps, a start and the joining)
-            const uint32_t w = kWarps >> (lane & 3), at_once = kResident * (kWarps / w);
-            const uint32_t c = (all + at_once - 1) / at_once * (top * (kWarps / w) + kStart + (3 - (lane & 3)));
-            const int who = __ffs(__ballot_sync(0xffffffffu, c == __reduce_min_sync(0xffffffffu, c))) - 1;
-            W = kWarps >> (who & 3);
-        }
-    }
-
-    // This warp's piece of the CTA's turn-th round, and its sequence: seq -1 if there is
-    // none; false if the CTA has none at all. (One barrier: the next round's writes
-    // come after the barrier of this one's readers, two rounds apart.)
-    __device__ __forceinline__ bool find(uint32_t turn, Piece& piece, Seq& s) const {
-        const int per_cta = kWarps / W;
-        const uint32_t first = (turn * gridDim.x + blockIdx.x) * per_cta;
-        bool any = false;
-        // (cleared a round ahead, so that this round's writers find it so)
-        if (threadIdx.x < kWarps) found[(turn + 1) & 1][threadIdx.x].seq = -1;
-        if (fn < first + per_cta && first < fn + n) {
-            uint32_t f = fn, fslots = fs, funits = fu;
-            for (int b = b0; b < b1 && f < first + per_cta; ++b) {
-                const Seq sq = seq(b);
-                const uint32_t u = (uint32_t)sq.blocks * p.heads, k = pieces(sq);
-                for (uint32_t index = max(f, first); index < min(f + u * k, first + per_cta); ++index) {
-                    const uint32_t rem = index - f, w = rem % u;
-                    found[turn & 1][index - first] = Piece{b, (int)(w / p.heads), (int)(w % p.heads), (int)(rem / u), (int)k, (int)(fslots + rem), (int)(funits + w)};
-                    of[turn & 1][index - first] = sq;
-                    any = true;
-                }
-                f += u * k;
-                if (k > 1) fslots += u * k, funits += u;
-            }
-        }
-        if (!__syncthreads_or(any)) return false;
-        const int at = (threadIdx.x >> 5) / W;
-        piece = found[turn & 1][at];
-        s = of[turn & 1][at];
-        return true;
-    }
-};
-
-// What the sums of a row are multiplied by, 0 (and .y) for one that sees nothing.
-// (a = -inf where all scores are: 0 / 0)
-template <int FMT>
-__device__ __forceinline__ float2 finish(float a, float b, float sum, float any) {
-    return any == 0.f ? make_float2(0.f, 1.f) : make_float2(exp2f(b - a) / sum, 0.f);
-}
-// Row r (of q, and head of the group) of a sequence in the output.
-__device__ __forceinline__ uint16_t* row_at(const AttendParams& p, int row0, int head, int r) {
-    const int i = r / p.group, h = r - i * p.group;
-    return p.out + (long long)(row0 + i) * p.o_row + (long long)(head * p.group + h) * p.o_head;
-}
-
 // 16-byte chunk c of row r of a stage's k or v, as TMA lays it out: rows of 64 or
 // 128 bytes with the swizzle of that width, 256 channels as two such blocks.
 template <int HD>
@@ -401,8 +130,8 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, QT>::kCtas) fl_kv_attend_
     }
     griddep_wait();
     griddep_launch_dependents();
-    const Pieces pieces(p, M, Lay::kQInRegs);
-    if (blockIdx.x == 0 && threadIdx.x == 0 && p.part != nullptr) units_of<HD, QT>(p)->count = (int)pieces.units;
+    const Pieces<kWarps, kResident> pieces(p, M, Lay::kQInRegs);
+    if (blockIdx.x == 0 && threadIdx.x == 0 && p.part != nullptr) units_of<kResident, M, HD>(p)->count = (int)pieces.units;
     const uint32_t ring = sbase + warp * NS * Lay::kStage, meta = sbase + Lay::kOffMeta + warp * NS * Lay::kMeta;
     const float kNone = __int_as_float(0xff800000), kNoMax = 1e30f;
     int stage = 0;       // the ring runs on from piece to piece
@@ -428,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, QT>::kCtas) fl_kv_attend_
     if (piece.k == 0 && own == 0 && lane == 0) {
         if (s.from + s.n > (long long)p.table_pages * p.page_size) atomicCAS(p.range, 0, s.row0 + 1);
         if (piece.pieces > 1)
-            units_of<HD, QT>(p)->unit[piece.units] = Unit{s.row0, s.n, r0, piece.head, piece.pieces, piece.slot, s.blocks * p.heads, 0};
+            units_of<kResident, M, HD>(p)->unit[piece.units] = Unit{s.row0, s.n, r0, piece.head, piece.pieces, piece.slot, s.blocks * p.heads, 0};
     }
 
     // ------------------------------------------------------------ the warp's ring
@@ -792,13 +521,13 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, QT>::kCtas) fl_kv_attend_
         }
         if (whole) {
             if (ch < p.head_dim) {
-                const float2 f = finish<FMT>(ma, mb, sum, any);
+                const float2 f = finish(ma, mb, sum, any);
                 *reinterpret_cast<uint32_t*>(row_at(p, s.row0, piece.head, r0 + r) + ch) = f.y != 0.f ? 0u : Ops::pack(v.x * f.x, v.y * f.x);
             }
         } else {
             *reinterpret_cast<float2*>(p.part + ((long long)piece.slot * M + r) * HD + ch) = v;
             if (ch == 0)
-                *reinterpret_cast<float4*>(p.part + (long long)kSlots * M * HD + ((long long)piece.slot * M + r) * 4) =
+                *reinterpret_cast<float4*>(p.part + (long long)slots(kResident) * M * HD + ((long long)piece.slot * M + r) * 4) =
                     make_float4(ma, mb, sum, any);
         }
     }
@@ -809,98 +538,13 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, QT>::kCtas) fl_kv_attend_
     }
 }
 
-// The pieces of row blocks of split sequences joined: a CTA of four warps to a row,
-// each of which adds every fourth piece; always in the same order.
-constexpr int kJoinThreads = 128;
-
-template <int DT, int FMT, int HD, int QT>
-__global__ void __launch_bounds__(kJoinThreads) fl_kv_attend_join_kernel(const __grid_constant__ AttendParams p) {
-    using Ops = DTypeOps<DT>;
-    constexpr int M = 8 * QT, C = HD / 32;  // channels of a lane
-    __shared__ float part[4][HD];
-    griddep_wait();
-    griddep_launch_dependents();
-    const Units* all = units_of<HD, QT>(p);
-    const int count = max(0, min(__ldcg(&all->count), kUnits)) * M;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const float kNone = __int_as_float(0xff800000);
-    for (int at = blockIdx.x; at < count; at += gridDim.x) {
-        const int4 u0 = __ldcg(reinterpret_cast<const int4*>(&all->unit[at / M]));
-        const int4 u1 = __ldcg(reinterpret_cast<const int4*>(&all->unit[at / M]) + 1);
-        const int row0 = u0.x, n = u0.y, block0 = u0.z, head = u0.w, pieces = u1.x, slot = u1.y, r = at % M;
-        const long long step = u1.z;  // slots from one piece to the next
-        // (records of a workspace that another call is writing at the same time stay harmless)
-        const bool fits = row0 >= 0 && n >= 0 && row0 <= p.rows - n && block0 >= 0 && head >= 0 && head < p.heads && pieces > 0 &&
-                          slot >= 0 && step > 0 && slot + (pieces - 1) * step < kSlots;
-        if (!fits || r >= n * p.group - block0) continue;
-        float a = kNone, b = kNone, sum = 0.f, any = 0.f, v[C] = {};
-        const float* stat = p.part + (long long)kSlots * M * HD + ((long long)slot * M + r) * 4;
-        const float* src = p.part + ((long long)slot * M + r) * HD + lane * C;
-        // (the first pieces' sums are asked for together with the maxima that they will be weighed by)
-        constexpr int U = 4;
-        float2 x[U][C / 2];
-        auto load = [&](int k, float2 (&d)[C / 2]) {
-#pragma unroll
-            for (int e = 0; e < C / 2; ++e) d[e] = __ldcg(reinterpret_cast<const float2*>(src + k * step * M * HD) + e);
-        };
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (warp + 4 * u < pieces) load(warp + 4 * u, x[u]);
-        float4 mine = make_float4(kNone, kNone, 0.f, 0.f);
-        for (int k = lane; k < pieces; k += 32) {
-            const float4 st = __ldcg(reinterpret_cast<const float4*>(stat + k * step * M * 4));
-            if (k < 32) mine = st;
-            a = fmaxf(a, st.x), b = fmaxf(b, st.y), any = fmaxf(any, st.w);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-            b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
-            any = fmaxf(any, __shfl_xor_sync(0xffffffffu, any, o));
-        }
-        const float na = a == kNone ? 0.f : -a, nb = b == kNone ? 0.f : -b;
-        sum = mine.z * ex2(mine.x + na);
-        for (int k = lane + 32; k < pieces; k += 32) {
-            const float4 st = __ldcg(reinterpret_cast<const float4*>(stat + k * step * M * 4));
-            sum += st.z * ex2(st.x + na);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        for (int k0 = warp; k0 < pieces; k0 += 4 * U) {
-            if (k0 != warp) {
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (k0 + 4 * u < pieces) load(k0 + 4 * u, x[u]);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int k = k0 + 4 * u;
-                const float mb = k < 32 ? __shfl_sync(0xffffffffu, mine.y, k) : k < pieces ? __ldcg(stat + k * step * M * 4 + 1) : kNone;
-                if (k >= pieces) continue;
-                const float f = ex2(mb + nb);
-#pragma unroll
-                for (int e = 0; e < C / 2; ++e) v[2 * e] = fmaf(x[u][e].x, f, v[2 * e]), v[2 * e + 1] = fmaf(x[u][e].y, f, v[2 * e + 1]);
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < C; ++e) part[warp][lane * C + e] = v[e];
-        __syncthreads();
-        if (threadIdx.x * 2 < p.head_dim) {
-            const int ch = threadIdx.x * 2;
-            const float2 f = finish<FMT>(a, b, sum, any);
-            float y[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) y[e] = (part[0][ch + e] + part[1][ch + e]) + (part[2][ch + e] + part[3][ch + e]);
-            *reinterpret_cast<uint32_t*>(row_at(p, row0, head, block0 + r) + ch) = f.y != 0.f ? 0u : Ops::pack(y[0] * f.x, y[1] * f.x);
-        }
-        __syncthreads();
-    }
-}
-
 struct Plan {
     int hd, qt, group;
+    int tile;         // rows of a row block of the kernel for many rows, or 0
     long long units;  // row blocks and heads at most
     bool split;       // whether a sequence can be long enough to be split
+    int rows() const { return tile ? tile : 8 * qt; }
+    int resident() const { return tile ? kTileResident : kResident; }
 };
 Plan plan_of(const fl_kv_attend_desc* d) {
     Plan p;
@@ -910,13 +554,16 @@ Plan plan_of(const fl_kv_attend_desc* d) {
     // not fit is another row block, which reads the codes again
     const long long each = d->cu_rows == nullptr ? p.group : ((long long)d->rows + d->n_seqs - 1) / d->n_seqs * p.group;
     p.qt = each <= 8 ? 1 : each <= 16 || p.hd == 256 ? 2 : 4;
-    const long long seqs = d->rows < d->n_seqs ? d->rows : d->n_seqs, M = 8 * p.qt;
+    p.tile = each > kRowsLimit && p.hd <= 128 && d->head_dim % 16 == 0 ? (each <= 128 ? 128 : 256) : 0;
+    const long long seqs = d->rows < d->n_seqs ? d->rows : d->n_seqs, M = p.rows();
     p.units = d->cu_rows == nullptr ? seqs * ((p.group + M - 1) / M) * d->heads_k
-                                    : ((long long)d->rows * p.group / M + seqs) * d->heads_k;
+                                    : (((long long)d->rows * p.group + (M - 1) * seqs) / M) * d->heads_k;
     p.split = (long long)d->table_pages * d->page_size > (long long)kLeast * kTile;
     return p;
 }
-size_t workspace_of(const Plan& p) { return p.split ? (size_t)kSlots * 8 * p.qt * (p.hd + 4) * 4 + sizeof(Units) : 0; }
+size_t workspace_of(const Plan& p) {
+    return p.split ? part_bytes(p.resident(), p.rows(), p.hd) + sizeof(Units) : 0;
+}
 
 fl_status check_sizes(const fl_kv_attend_desc* d) {
     using host::fail;
@@ -933,12 +580,12 @@ fl_status check_sizes(const fl_kv_attend_desc* d) {
     if (d->head_dim % 8 != 0) return fail(FL_ERR_ALIGNMENT, "%s: head_dim must be a multiple of 8 (%d)", what, d->head_dim);
     if (d->head_dim > 256) return fail(FL_ERR_UNSUPPORTED, "%s: head_dim above 256 (%d)", what, d->head_dim);
     if (d->n_seqs > 1 << 30) return fail(FL_ERR_UNSUPPORTED, "%s: more than 2^30 sequences", what);
-    if ((long long)d->rows * (d->heads_q / d->heads_k) >= (1ll << 31) - 64 || plan_of(d).units + kSlots >= (1ll << 31))
+    if ((long long)d->rows * (d->heads_q / d->heads_k) >= (1ll << 31) - 64 || plan_of(d).units + slots(kResident) >= (1ll << 31))
         return fail(FL_ERR_UNSUPPORTED, "%s: too many rows", what);
     return FL_OK;
 }
 
-fl_status attend(const fl_kv_attend_desc* d, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+fl_status run(const fl_kv_attend_desc* d, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
     using host::fail;
     const char* what = "fl_kv_attend";
     fl_status st = check_sizes(d);
@@ -1010,8 +657,15 @@ fl_status attend(const fl_kv_attend_desc* d, void* workspace, size_t workspace_b
     if (tma)
         for (int w = 0; w < 2; ++w)
             if ((st = host::encode_pages(&p.tm[w], w == 0 ? d->k_cache : d->v_cache, d->head_dim, d->heads_k, d->page_size,
-                                         d->n_pages, plan.hd == 64 ? 64 : 128, 1u << p.box_log)) != FL_OK)
+                                         d->n_pages, plan.hd == 64 ? 64 : 128, 1u << p.box_log, plan.tile == 0)) != FL_OK)
                 return st;
+    if (plan.tile) {
+        int launches = 0;
+        const cudaError_t e = launch_tile(p, d->dtype, d->format, plan.hd, plan.tile, plan.units, plan.split, ctx, stream, &launches);
+        st = host::launched(e, what);
+        if (st == FL_OK && launches > 1) st = host::launched(cudaSuccess, what);  // (counted)
+        return st;
+    }
     // (L is T / kResident at least: that many pieces more than units at most)
     const long long most = plan.units + (plan.split ? kResident : 0);
     const dim3 grid((unsigned)std::min<long long>(most, (long long)ctx.sms * (plan.hd <= 128 && plan.qt <= 2 ? 2 : 1)));
@@ -1027,7 +681,7 @@ fl_status attend(const fl_kv_attend_desc* d, void* workspace, size_t workspace_b
         e = host::launch(fl_kv_attend_kernel<DT, FMT, HD, QT, TMA>, grid, kThreads, bytes, ctx.pdl, stream, p);
         const fl_status s = host::launched(e, what);
         if (s != FL_OK || !plan.split) return s;
-        e = host::launch(fl_kv_attend_join_kernel<DT, FMT, HD, QT>, join_grid, kJoinThreads, 0, ctx.pdl, stream, p);
+        e = host::launch(fl_kv_attend_join_kernel<DT, HD, kResident, 8 * QT>, join_grid, kJoinThreads, 0, ctx.pdl, stream, p);
         return host::launched(e, what);
     };
     using std::integral_constant;
@@ -1062,5 +716,5 @@ extern "C" size_t fl_kv_attend_workspace_size(const fl_kv_attend_desc* desc) {
 }
 
 extern "C" fl_status fl_kv_attend(const fl_kv_attend_desc* desc, void* workspace, size_t workspace_bytes, void* stream) {
-    return fl::attend(desc, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+    return fl::run(desc, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }

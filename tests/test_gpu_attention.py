@@ -387,6 +387,115 @@ def test_kv_attend(dt, fmt, H, group, D, page, n_rows, start):
         attend_check(got, ref, dt, cache, n_rows, start, kind)
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("H,group,D,page,n_rows,start", [
+    (1, 4, 128, 16, [48], [0]),
+    (1, 4, 128, 16, [48, 33], [100, 5]),
+    (2, 4, 64, 16, [64, 64], [700, 129]),
+    (1, 1, 96, 7, [129, 40], [300, 3]),
+    (2, 2, 128, 48, [70, 0, 9, 130], [5000, 3, 1, 0]),
+    (1, 3, 80, 64, [100], [2000]),
+    (1, 1, 16, 16, [300], [64]),
+    (8, 4, 128, 16, [40, 40], [300, 2000]),
+])
+def test_kv_attend_many_rows(dt, fmt, H, group, D, page, n_rows, start):
+    rng = gen(67, H, group, D, page, sum(start))
+    cache = Paged(rng, [a + b for a, b in zip(n_rows, start)], H, D, page, fmt)
+    for kind in ("causal", "tree"):
+        tree = None
+        if kind == "tree":
+            tree = rng.random((sum(n_rows), max(n_rows) - 1)) < 0.3
+        got, ref, q = attend_case(rng, dt, cache, H * group, n_rows, start, tree)
+        fl.device_status()
+        attend_check(got, ref, dt, cache, n_rows, start, kind)
+        again = fl.kv_attend(q, *cache.tensors(), ints(cache.table), ints(start), cu_rows=ints(sums(n_rows)),
+                             tree=None if tree is None else put(tree))
+        assert torch.equal(again, got)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_kv_attend_many_rows_what_is_not_seen(fmt, D):
+    """Junk in unused places, drafts that hold no number, rows that see nothing, positions without a page, rows behind
+    the last sequence, one row of q that is not finite: each stays where it belongs."""
+    rng = gen(68, D)
+    n_rows, start = [40, 50], [137, 0]
+    cache = Paged(rng, [177, 50], 1, D, 16, fmt)
+    tree = rng.random((95, 50)) < 0.4
+    tree[:, 7] = False
+    tree[3, 7] = tree[60, 7] = True
+    tree[45] = False                                # sees nothing: its context is empty
+    q = put(rng.standard_normal((95, 4, D)), "f16")
+    out = torch.full_like(q, 7.0)
+    clean, ref, _ = attend_case(rng, "f16", cache, 4, n_rows, start, tree, q=q, out=out)
+    clean = clean.clone()
+    assert (clean[90:] == 7).all() and (clean[45] == 0).all() and torch.isfinite(clean[:90]).all()
+    attend_check(clean[:90], ref, "f16", cache, n_rows, start)
+    used = np.zeros((cache.pages, 16), dtype=bool)
+    for b, n in ((0, 177), (1, 50)):
+        for p in range(n):
+            used[cache.table[b, p // 16], p % 16] = True
+    junk = torch.from_numpy(~used).cuda()
+    for t in (cache.ks, cache.vs):
+        t[junk] = float("nan")
+    for t in (cache.k, cache.v):
+        t.view(torch.uint8)[junk] = 0x7f            # a NaN in e4m3
+    args = (ints(cache.table), ints(start))
+    got = fl.kv_attend(q, *cache.tensors(), *args, cu_rows=ints(sums(n_rows)), tree=put(tree), out=out)
+    fl.device_status()
+    assert torch.equal(got, clean)
+    # draft 7 of each sequence holds no number: rows 3 and 60 see it, no others
+    for b, pos in ((0, 144), (1, 7)):
+        page, at = int(cache.table[b, pos // 16]), pos % 16
+        for t in (cache.k, cache.v):
+            t.view(torch.uint8)[page, at] = 0
+        for t in (cache.ks, cache.vs):
+            t[page, at] = float("nan")
+    got = fl.kv_attend(q, *cache.tensors(), *args, cu_rows=ints(sums(n_rows)), tree=put(tree), out=out)
+    rest = torch.ones(95, dtype=torch.bool, device="cuda")
+    rest[3] = rest[60] = False
+    assert torch.isnan(got[3]).all() and torch.isnan(got[60]).all() and torch.equal(got[rest], clean[rest])
+    q[20, 2, 1] = float("inf")
+    got = fl.kv_attend(q, *cache.tensors(), *args, cu_rows=ints(sums(n_rows)), tree=put(tree), out=out)
+    assert torch.isnan(got[20, 2]).any() and torch.equal(got[20, 1], clean[20, 1])
+    rest[20] = False
+    assert torch.equal(got[rest], clean[rest])
+    fl.device_status()
+    # a page that is not there
+    cache = Paged(rng, [177, 50], 1, D, 16, fmt)
+    cache.table[0, 4] = -1
+    got, ref, _ = attend_case(rng, "bf16", cache, 4, n_rows, start)
+    with pytest.raises(fl.FusedLinError):
+        fl.device_status()
+    attend_check(got, ref, "bf16", cache, n_rows, start)
+
+
+def test_kv_attend_many_rows_of_any_scale():
+    """Rows of bf16 far outside fp16's range, values whose scales lie 2^18 apart, scores that grow towards the end."""
+    rng = gen(69)
+    n_rows, start = [60], [900]
+    cache = Paged(rng, [960], 1, 128, 16, "int8")
+    cache.scale[1] = np.where(rng.random(cache.scale[1].shape) < 0.5, 2.0 ** -6, 2.0 ** -24).astype(np.float32)
+    order = np.empty(cache.pages * 16)
+    for p in range(60 * 16):
+        order[cache.table[0, p // 16] * 16 + p % 16] = 0.001 * 1.005 ** p
+    cache.scale[0] = order.reshape(cache.pages, 16, 1).astype(np.float32)
+    cache.ks, cache.vs = put(cache.scale[0]), put(cache.scale[1])
+    for size in (2.0 ** -50, 2.0 ** 40):
+        q = put(rng.standard_normal((60, 1, 128)) * size * np.exp2(rng.integers(-6, 6, (60, 1, 1))), "bf16")
+        got, ref, _ = attend_case(rng, "bf16", cache, 1, n_rows, start, q=q, scale=0.08 / size)
+        fl.device_status()
+        vals = cache.values()[0]
+        floor = np.zeros((60, 1))
+        for i in range(60):
+            x = vals[0][:901 + i, 0] @ f64(q)[i, 0] * 0.08 / size
+            w = np.exp(x - x.max())
+            vs = cache.scale[1][cache.table[0][:60]].reshape(-1)[:len(w)]
+            floor[i, 0] = len(w) * 2.0 ** -25 * 127 * (w / w.sum() * vs).max()
+        check(got, ref, U["bf16"], 2.0 ** -11, 2.0 ** -18, floor, f"{size}")
+
+
 def test_kv_attend_decode_without_offsets():
     rng = gen(51)
     start = [5, 1000, 0, 64]
