@@ -177,36 +177,34 @@ struct Pieces {
         for (int w = 0; w < kWarps; ++w) t += sum_t[w], top = max(top, top_t[w]);
         L = kWhole;
         if (top > kLeast) {
-            // what each candidate costs: the rounds, times their longest piece and a start
-            uint32_t at[kCandidates + 1], k[kCandidates + 1];
-#pragma unroll
+            // Each lane's candidate, and what it costs: the rounds, times their longest piece and a start. (In
+            // a loop: a CTA's first instructions come from far, so the fewer of them the better.)
+            const int me = min(lane, kCandidates);
+            const unsigned long long want = (t * kTimes[me] + 8 * kResident - 1) / (8 * kResident);
+            const uint32_t mine = me == kCandidates ? kWhole : (uint32_t)max((unsigned long long)kLeast, min(want, (unsigned long long)kWhole));
+            const float inv = __frcp_rn((float)mine);
+#pragma unroll 1
             for (int c = 0; c <= kCandidates; ++c) {
-                const unsigned long long want = (t * kTimes[c] + 8 * kResident - 1) / (8 * kResident);
-                at[c] = c == kCandidates ? kWhole : (uint32_t)max((unsigned long long)kLeast, min(want, (unsigned long long)kWhole));
-                k[c] = 0;
-                const float inv = 1.f / (float)at[c];
+                const float by = __shfl_sync(0xffffffffu, inv, c);
+                uint32_t k = 0;
                 for (int b = b0; b < b1; ++b) {
                     const Seq s = seq(b);
                     // (an estimate: the quotient is not exact next to a whole number)
-                    k[c] += (uint32_t)s.blocks * p.heads * (uint32_t)fmaxf(1.f, ceilf((float)s.tiles * inv));
+                    k += (uint32_t)s.blocks * p.heads * (uint32_t)fmaxf(1.f, ceilf((float)s.tiles * by));
                 }
-            }
-#pragma unroll
-            for (int c = 0; c <= kCandidates; ++c) k[c] = __reduce_add_sync(0xffffffffu, k[c]);
-            if (lane == 0) {
-#pragma unroll
-                for (int c = 0; c <= kCandidates; ++c) pieces_of[warp][c] = k[c];
+                k = __reduce_add_sync(0xffffffffu, k);
+                if (lane == 0) pieces_of[warp][c] = k;
             }
             __syncthreads();
-            uint32_t best = 0xffffffffu;
-#pragma unroll
-            for (int c = 0; c <= kCandidates; ++c) {
+            uint32_t cost = 0xffffffffu;
+            if (lane <= kCandidates) {
                 uint32_t all = 0;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) all += pieces_of[w][c];
-                const uint32_t cost = (all + kResident - 1) / kResident * (min(at[c], top) + kStart) + (at[c] < top ? kJoin : 0);
-                if (cost < best) best = cost, L = at[c];
+                for (int w = 0; w < kWarps; ++w) all += pieces_of[w][me];
+                cost = (all + kResident - 1) / kResident * (min(mine, top) + kStart) + (mine < top ? kJoin : 0);
             }
+            const int who = __ffs(__ballot_sync(0xffffffffu, cost == __reduce_min_sync(0xffffffffu, cost))) - 1;
+            L = __shfl_sync(0xffffffffu, mine, who);
             if (L >= top) L = kWhole;
         }
         uint32_t sl = 0, un = 0;

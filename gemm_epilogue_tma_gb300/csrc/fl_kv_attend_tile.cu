@@ -44,7 +44,7 @@ struct Layout {
     static constexpr int kOffBits = kOffTab + kTabs * 3 * kRows * 4;  // [kTabs][4]: which positions are there
     static constexpr int kOffC = kOffBits + kTabs * 16;
     static constexpr int kOffBar = kOffC + TILES * kRows * 4;
-    static constexpr int kBars = 4 * kRing + 6 + kTabs + 1;
+    static constexpr int kBars = 4 * kRing + 6 + kTabs + 2;
     static constexpr int kOffSlot = kOffBar + kBars * 8;
     static constexpr int kSmem = kOffSlot + 16 + 1024;
     // what the rows' threads leave, in place of q, k and v: [rows][kPitch] sums
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
     auto p_full = [&](int i) { return bar0 + 8u * (4 * kRing + 2 + i); };
     auto o_full = [&](int i) { return bar0 + 8u * (4 * kRing + 4 + i); };
     auto tab_full = [&](int j) { return bar0 + 8u * (4 * kRing + 6 + j % kTabs); };
-    const uint32_t drain = bar0 + 8u * (4 * kRing + 6 + kTabs);
+    const uint32_t drain = bar0 + 8u * (4 * kRing + 6 + kTabs), q_full = drain + 8u;
     auto round = [&](int x) { return (uint32_t)(x / kRing & 1); };
     float* const tabs = reinterpret_cast<float*>(smem + Lay::kOffTab);
     float* const cs = reinterpret_cast<float*>(smem + Lay::kOffC);
@@ -109,6 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
         }
         for (int j = 0; j < kTabs; ++j) mbar_init(tab_full(j), kWiden);
         mbar_init(drain, 1);
+        mbar_init(q_full, 1);
         fence_mbar_init();
     }
     if (warp == kWarpMma) {
@@ -141,36 +142,6 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
             units_of<kTileResident, M, DP>(p)->unit[piece.units] = Unit{s.row0, s.n, r0, piece.head, piece.pieces, piece.slot, s.blocks * p.heads, 0};
     }
 
-    // ------------------------------------------------------------ q as fp16, a row to sixteen lanes
-    for (int r = warp * 2 + (lane >> 4); r < M; r += 2 * kWarps) {
-        const int c = lane & 15, i = (r0 + r) / p.group, h = (r0 + r) - i * p.group;
-        const bool in = r < rows && 8 * c < p.head_dim;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (in) x = ldg_v4(p.q + (long long)(s.row0 + i) * p.q_row + (long long)(piece.head * p.group + h) * p.q_head + 8 * c);
-        uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        float up = 1.f;
-        if (DT == DT_BF16) {
-            // 2^(14 - e) for a largest value of 2^e to 2^(e + 1); rows without a finite, not tiny one stay as they are
-            uint32_t top = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const int ex = (int)(top >> 7);
-            if (ex > 0 && ex < 255) up = __uint_as_float((uint32_t)min(254, 127 + 14 + 127 - ex) << 23);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 f = Ops::unpack(w[e]);
-                w[e] = DTypeOps<DT_F16>::pack(f.x * up, f.y * up);
-            }
-        }
-        if (8 * c < DP)
-            st_shared_v4(sbase + r / kRows * Lay::kBlock + (c >> 3) * (kRows * 128) + r % kRows * 128 + (((c & 7) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
-        if (c == 0) cs[r] = fmaxf(p.log2_scale / up, 0x1p-126f);
-    }
-    fence_proxy_async_smem();
-    __syncthreads();
-
     // (all 512 columns of tensor memory: the base is 0)
     // 512 threads are launched with 128 registers: the softmax warps take 176, the others 80 (256 * 176 + 256 * 80 = 512 * 128)
     if (warp >= kWarpMma) {
@@ -194,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
         };
         bool ok = true;
         if (nb > 0) {
-            ok = wait(full(0), 0, 61);
+            ok = wait(q_full, 0, 60) && wait(full(0), 0, 61);
             for (int i = 0; ok && i < TILES; ++i)
                 if (0 < (i ? n1 : n0)) scores(i, 0);
             if (ok) commit_elected(empty(0));
@@ -324,6 +295,45 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
     }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        // ------------------------------------------------------------ q as fp16, a row to sixteen lanes, eight at a time
+        for (int b = warp * 2 + (lane >> 4); b < M; b += 16 * 8) {
+            const int c = lane & 15;
+            uint4 x[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int r = b + 16 * u, i = (r0 + r) / p.group, h = (r0 + r) - i * p.group;
+                x[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (r < rows && 8 * c < p.head_dim)
+                    x[u] = ldg_v4(p.q + (long long)(s.row0 + i) * p.q_row + (long long)(piece.head * p.group + h) * p.q_head + 8 * c);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int r = b + 16 * u;
+                uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+                float up = 1.f;
+                if (DT == DT_BF16) {
+                    // 2^(14 - e) for a largest value of 2^e to 2^(e + 1); rows without a finite, not tiny one stay as they are
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const int ex = (int)(top >> 7);
+                    if (ex > 0 && ex < 255) up = __uint_as_float((uint32_t)min(254, 127 + 14 + 127 - ex) << 23);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = Ops::unpack(w[e]);
+                        w[e] = DTypeOps<DT_F16>::pack(f.x * up, f.y * up);
+                    }
+                }
+                if (8 * c < DP)
+                    st_shared_v4(sbase + r / kRows * Lay::kBlock + (c >> 3) * (kRows * 128) + r % kRows * 128 + (((c & 7) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
+                if (c == 0) cs[r] = fmaxf(p.log2_scale / up, 0x1p-126f);
+            }
+        }
+        fence_proxy_async_smem();
+        named_bar_sync(1, 2 * kRows);
+        if (threadIdx.x == 0) mbar_arrive(q_full);
         // ------------------------------------------------------------ softmax: a row per thread
         const int i = warp >> 2, n = i ? n1 : n0, r = (int)threadIdx.x;  // (one tile: warps 4-7 have nothing to do)
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, s_col = lanes + 128u * i, o_col = lanes + kOCol + 128u * i;
@@ -360,41 +370,58 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
                 }
             }
             seen |= (sees[0] | sees[1] | sees[2] | sees[3]) != 0;
-            // the maxima first, then the weights, from tensor memory twice
-            float ta = kNone, tb = kNone;
+            // Weights of the values: 2^(x + log2 vs - mw) = 2^(x - mx) vs 2^(mx - mw). Once there are maxima, and where every
+            // position is seen, they are formed in one pass with those: good unless a weight passes 2^8 (or the
+            // sum fp32's range), which is rare. Otherwise the maxima are found first.
+            uint32_t w[4][16];
+            bool done = false;
+            const float2 cc = make_float2(c, c);
+            if (__all_sync(0xffffffffu, all && mx > kNone && mw > kNone)) {
+                const float to = ex2(nw - nx);
+                const float2 nn = make_float2(nx, nx), tt = make_float2(to, to);
+                float2 sum = l;
+                uint32_t most = 0;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float x[32];
-                tmem_ld_32x32b_x32(s_col + 32u * q, reinterpret_cast<uint32_t(&)[32]>(x));
-                tmem_ld_wait();
-                if (!all) {
+                for (int q = 0; q < 4; ++q) {
+                    float x[32];
+                    tmem_ld_32x32b_x32(s_col + 32u * q, reinterpret_cast<uint32_t(&)[32]>(x));
+                    tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (!(sees[q] >> e & 1)) x[e] = kNone;
-                }
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const uint4 k4 = ld_shared_v4(tab + (32 * q + e) * 4), l4 = ld_shared_v4(tab + (2 * kRows + 32 * q + e) * 4);
-                    const float kk[4] = {__uint_as_float(k4.x), __uint_as_float(k4.y), __uint_as_float(k4.z), __uint_as_float(k4.w)};
-                    const float lv[4] = {__uint_as_float(l4.x), __uint_as_float(l4.y), __uint_as_float(l4.z), __uint_as_float(l4.w)};
-#pragma unroll
-                    for (int f = 0; f < 4; f += 2) {
-                        const float2 y = mul2(mul2(make_float2(x[e + f], x[e + f + 1]), make_float2(kk[f], kk[f + 1])), make_float2(c, c));
-                        const float2 z = add2(y, make_float2(lv[f], lv[f + 1]));
-                        if (all) {
-                            ta = fmaxf(ta, fmaxf(y.x, y.y)), tb = fmaxf(tb, fmaxf(z.x, z.y));
-                        } else {
-                            // (a scale that is not there may be anything)
-                            if (sees[q] >> (e + f) & 1) ta = fmaxf(ta, y.x), tb = fmaxf(tb, z.x);
-                            if (sees[q] >> (e + f + 1) & 1) ta = fmaxf(ta, y.y), tb = fmaxf(tb, z.y);
-                        }
+                    for (int e = 0; e < 32; e += 4) {
+                        const uint4 k4 = ld_shared_v4(tab + (32 * q + e) * 4), v4 = ld_shared_v4(tab + (kRows + 32 * q + e) * 4);
+                        const float2 y0 = ffma2(mul2(make_float2(x[e], x[e + 1]), make_float2(__uint_as_float(k4.x), __uint_as_float(k4.y))), cc, nn);
+                        const float2 y1 = ffma2(mul2(make_float2(x[e + 2], x[e + 3]), make_float2(__uint_as_float(k4.z), __uint_as_float(k4.w))), cc, nn);
+                        const float2 a0 = make_float2(ex2(y0.x), ex2(y0.y)), a1 = make_float2(ex2(y1.x), ex2(y1.y));
+                        const float2 b0 = mul2(mul2(a0, make_float2(__uint_as_float(v4.x), __uint_as_float(v4.y))), tt);
+                        const float2 b1 = mul2(mul2(a1, make_float2(__uint_as_float(v4.z), __uint_as_float(v4.w))), tt);
+                        sum = add2(sum, add2(a0, a1));
+                        w[q][e / 2] = DTypeOps<DT_F16>::pack(b0.x, b0.y), w[q][e / 2 + 1] = DTypeOps<DT_F16>::pack(b1.x, b1.y);
+                        asm("max.f16x2 %0, %0, %1;" : "+r"(most) : "r"(w[q][e / 2]));
+                        asm("max.f16x2 %0, %0, %1;" : "+r"(most) : "r"(w[q][e / 2 + 1]));
                     }
                 }
+                // (weights are not negative: as 16-bit patterns they compare as numbers; 0x5c00 is 2^8)
+                done = __all_sync(0xffffffffu, max(most & 0xffffu, most >> 16) <= 0x5c00u && sum.x + sum.y < 0x1p100f);
+                if (done) l = sum;
             }
-            const bool over = ta > mx + kLazy || tb > mw + kLazy;
-            if (__any_sync(0xffffffffu, over)) {
-                float f = 1.f;
-                if (over) {
+            if (!done) {
+                float ta = kNone, tb = kNone;
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t m = q < 2 ? (q == 0 ? sees[0] : sees[1]) : (q == 2 ? sees[2] : sees[3]);
+                    float x[32];
+                    tmem_ld_32x32b_x32(s_col + 32u * q, reinterpret_cast<uint32_t(&)[32]>(x));
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        // (a scale that is not there may be anything)
+                        const float y = x[e] * ld_shared_f32(tab + (32 * q + e) * 4) * c;
+                        if (m >> e & 1) ta = fmaxf(ta, y), tb = fmaxf(tb, y + ld_shared_f32(tab + (2 * kRows + 32 * q + e) * 4));
+                    }
+                }
+                const bool over = ta > mx || tb > mw;
+                if (__any_sync(0xffffffffu, over)) {
+                    float f = 1.f;
                     if (ta > mx) {
                         const float g = ex2(mx - ta);
                         l.x *= g, l.y *= g;
@@ -404,47 +431,44 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
                         f = ex2(mw - tb);
                         mw = tb, nw = -tb;
                     }
-                }
-                if (j > 0) {
+                    if (j > 0) {
 #pragma unroll 1
-                    for (int q = 0; q < DP / 32; ++q) {
-                        float o[32];
-                        tmem_ld_32x32b_x32(o_col + 32u * q, reinterpret_cast<uint32_t(&)[32]>(o));
-                        tmem_ld_wait();
+                        for (int q = 0; q < DP / 32; ++q) {
+                            float o[32];
+                            tmem_ld_32x32b_x32(o_col + 32u * q, reinterpret_cast<uint32_t(&)[32]>(o));
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] *= f;
-                        tmem_st_32x32b_x32(o_col + 32u * q, reinterpret_cast<uint32_t(&)[32]>(o));
-                    }
-                }
-            }
-            // weights of the values: 2^(x + log2 vs - mw) = 2^(x - mx) vs 2^(mx - mw)
-            const float to = mw == kNone ? 0.f : ex2(nw - nx);
-            const float2 cc = make_float2(c, c), nn = make_float2(nx, nx), tt = make_float2(to, to);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float x[32];
-                tmem_ld_32x32b_x32(s_col + 32u * q, reinterpret_cast<uint32_t(&)[32]>(x));
-                tmem_ld_wait();
-                uint32_t w[16];
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const uint4 k4 = ld_shared_v4(tab + (32 * q + e) * 4), v4 = ld_shared_v4(tab + (kRows + 32 * q + e) * 4);
-                    const float kk[4] = {__uint_as_float(k4.x), __uint_as_float(k4.y), __uint_as_float(k4.z), __uint_as_float(k4.w)};
-                    const float vv[4] = {__uint_as_float(v4.x), __uint_as_float(v4.y), __uint_as_float(v4.z), __uint_as_float(v4.w)};
-#pragma unroll
-                    for (int f = 0; f < 4; f += 2) {
-                        const float2 y = ffma2(mul2(make_float2(x[e + f], x[e + f + 1]), make_float2(kk[f], kk[f + 1])), cc, nn);
-                        float2 a = make_float2(ex2(y.x), ex2(y.y));
-                        float2 b = mul2(mul2(a, make_float2(vv[f], vv[f + 1])), tt);
-                        if (!all) {
-                            if (!(sees[q] >> (e + f) & 1)) a.x = b.x = 0.f;
-                            if (!(sees[q] >> (e + f + 1) & 1)) a.y = b.y = 0.f;
+                            for (int e = 0; e < 32; ++e) o[e] *= f;
+                            tmem_st_32x32b_x32(o_col + 32u * q, reinterpret_cast<uint32_t(&)[32]>(o));
                         }
-                        l = add2(l, a);
-                        w[(e + f) / 2] = DTypeOps<DT_F16>::pack(b.x, b.y);
                     }
                 }
-                tmem_st_32x32b_x16(s_col + 16u * q, w);
+                const float to = mw == kNone ? 0.f : ex2(nw - nx);
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t m = q < 2 ? (q == 0 ? sees[0] : sees[1]) : (q == 2 ? sees[2] : sees[3]);
+                    float x[32];
+                    tmem_ld_32x32b_x32(s_col + 32u * q, reinterpret_cast<uint32_t(&)[32]>(x));
+                    tmem_ld_wait();
+                    uint32_t h[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float a[2], b[2];
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) {
+                            const int at = 32 * q + e + f;
+                            a[f] = ex2(fmaf(x[e + f] * ld_shared_f32(tab + at * 4), c, nx));
+                            b[f] = a[f] * ld_shared_f32(tab + (kRows + at) * 4) * to;
+                            if (!(m >> (e + f) & 1)) a[f] = b[f] = 0.f;
+                        }
+                        l = add2(l, make_float2(a[0], a[1]));
+                        h[e / 2] = DTypeOps<DT_F16>::pack(b[0], b[1]);
+                    }
+                    tmem_st_32x32b_x16(s_col + 16u * q, h);
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tmem_st_32x32b_x16(s_col + 16u * q, w[q]);
             }
             tmem_st_wait();
             tc_fence_before();
