@@ -43,7 +43,11 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kResident = 304;  // CTAs at work at once: two on each of 152 multiprocessors
 static_assert(kTile == kStep * kWarps, "a tile is a step of all warps");
-constexpr int kRowsLimit = 32;  // rows of a sequence and key head (of average length) from which the kernel for many rows is taken
+// The kernel for many rows is taken for more than kRowsLimit rows of a sequence and key head (on average) and tables
+// of kLongTable positions at least; the lengths themselves are not known here. Both sides, us, eight key heads: four contexts
+// of 5700 with 32 rows each 42 here, 49 there; with 36 64 and 50, with 96 83 and 51; 32 contexts of 1000 with 48 rows 91 and 76;
+// one of 500 with 192 rows 23 and 37, four of 300 with 48 rows 18 and 31.
+constexpr int kRowsLimit = 32, kLongTable = 1024;
 
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -554,7 +558,7 @@ Plan plan_of(const fl_kv_attend_desc* d) {
     // not fit is another row block, which reads the codes again
     const long long each = d->cu_rows == nullptr ? p.group : ((long long)d->rows + d->n_seqs - 1) / d->n_seqs * p.group;
     p.qt = each <= 8 ? 1 : each <= 16 || p.hd == 256 ? 2 : 4;
-    p.tile = each > kRowsLimit && p.hd <= 128 && d->head_dim % 16 == 0 ? (each <= 128 ? 128 : 256) : 0;
+    p.tile = each > kRowsLimit && (long long)d->table_pages * d->page_size >= kLongTable && p.hd <= 128 && d->head_dim % 16 == 0 ? (each <= 128 ? 128 : 256) : 0;
     const long long seqs = d->rows < d->n_seqs ? d->rows : d->n_seqs, M = p.rows();
     p.units = d->cu_rows == nullptr ? seqs * ((p.group + M - 1) / M) * d->heads_k
                                     : (((long long)d->rows * p.group + (M - 1) * seqs) / M) * d->heads_k;

@@ -82,6 +82,9 @@ __device__ __forceinline__ uint32_t widen(uint32_t x) {
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 // Arrives on the barrier when this thread's copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
@@ -125,7 +128,7 @@ struct Piece {
 // Candidates of L: T / RESIDENT times these, / 8, and no split at all. (More than 8
 // makes room for the pieces that lengths which are no multiples of L leave over.)
 constexpr int kCandidates = 5;
-__device__ constexpr int kTimes[kCandidates + 1] = {8, 9, 11, 14, 20, 0};
+constexpr unsigned long long kTimes = 0x140e0b0908ull;  // 8, 9, 11, 14, 20 (as a number: a table would be loaded from memory)
 constexpr uint32_t kWhole = 1u << 30;
 
 // The pieces of all sequences, counted by all threads of a CTA of WARPS warps, for
@@ -180,7 +183,7 @@ struct Pieces {
             // Each lane's candidate, and what it costs: the rounds, times their longest piece and a start. (In
             // a loop: a CTA's first instructions come from far, so the fewer of them the better.)
             const int me = min(lane, kCandidates);
-            const unsigned long long want = (t * kTimes[me] + 8 * kResident - 1) / (8 * kResident);
+            const unsigned long long want = (t * (kTimes >> 8 * me & 0xff) + 8 * kResident - 1) / (8 * kResident);
             const uint32_t mine = me == kCandidates ? kWhole : (uint32_t)max((unsigned long long)kLeast, min(want, (unsigned long long)kWhole));
             const float inv = __frcp_rn((float)mine);
 #pragma unroll 1

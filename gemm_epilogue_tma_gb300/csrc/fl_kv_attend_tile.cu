@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
         }
         for (int j = 0; j < kTabs; ++j) mbar_init(tab_full(j), kWiden);
         mbar_init(drain, 1);
-        mbar_init(q_full, 1);
+        mbar_init(q_full, kWarps - 1);
         fence_mbar_init();
     }
     if (warp == kWarpMma) {
@@ -140,6 +140,51 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
         if (s.from + s.n > (long long)p.table_pages * p.page_size) atomicCAS(p.range, 0, s.row0 + 1);
         if (piece.pieces > 1)
             units_of<kTileResident, M, DP>(p)->unit[piece.units] = Unit{s.row0, s.n, r0, piece.head, piece.pieces, piece.slot, s.blocks * p.heads, 0};
+    }
+
+    // ------------------------------------------------------------ q as fp16, a row to sixteen lanes
+    // (by all warps but the one that loads)
+    if (warp != kWarpTma) {
+        const int c = lane & 15, first = 2 * (warp < kWarpTma ? warp : warp - 1) + (lane >> 4);
+        constexpr int kStride = 2 * (kWarps - 1);
+        auto place = [&](int r) {
+            return sbase + r / kRows * Lay::kBlock + (c >> 3) * (kRows * 128) + r % kRows * 128 + (((c & 7) ^ (r & 7)) << 4);
+        };
+#pragma unroll 1
+        for (int r = first; r < M; r += kStride) {
+            const int i = (r0 + r) / p.group, h = (r0 + r) - i * p.group;
+            if (r < rows && 8 * c < p.head_dim)
+                cp_async16(place(r), p.q + (long long)(s.row0 + i) * p.q_row + (long long)(piece.head * p.group + h) * p.q_head + 8 * c);
+            else if (8 * c < DP)
+                st_shared_v4(place(r), 0u, 0u, 0u, 0u);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 2
+        for (int r = first; r < M; r += kStride) {  // (its own copies)
+            float up = 1.f;
+            if (DT == DT_BF16) {
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                if (8 * c < DP) x = ld_shared_v4(place(r));
+                // 2^(14 - e) for a largest value of 2^e to 2^(e + 1); rows without a finite, not tiny one stay as they are
+                uint32_t w[4] = {x.x, x.y, x.z, x.w}, top = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const int ex = (int)(top >> 7);
+                if (ex > 0 && ex < 255) up = __uint_as_float((uint32_t)min(254, 127 + 14 + 127 - ex) << 23);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = Ops::unpack(w[e]);
+                    w[e] = DTypeOps<DT_F16>::pack(f.x * up, f.y * up);
+                }
+                if (8 * c < DP) st_shared_v4(place(r), w[0], w[1], w[2], w[3]);
+            }
+            if (c == 0) cs[r] = fmaxf(p.log2_scale / up, 0x1p-126f);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
     }
 
     // (all 512 columns of tensor memory: the base is 0)
@@ -258,7 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
             float* const tab = tabs + j % kTabs * (3 * kRows);
             if ((x & 1) == 0 && tid < kRows) tab[2 * kRows + tid] = lg2(tab[kRows + tid]);
             const uint4 bits = ld_shared_v4(sbase + Lay::kOffBits + j % kTabs * 16);
-            constexpr int V = kRows * DP / 16, U = 3;  // vectors of 16 codes, in flight
+            const bool gaps = (bits.x & bits.y & bits.z & bits.w) != 0xffffffffu;
+            constexpr int V = kRows * DP / 16, U = (V + 32 * kWiden - 1) / (32 * kWiden);  // vectors of 16 codes, in flight
 #pragma unroll 1
             for (int e0 = tid; e0 < V; e0 += 32 * kWiden * U) {
                 uint4 v[U];
@@ -271,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
                 for (int u = 0; u < U; ++u) {
                     const int e = e0 + 32 * kWiden * u, r = e / (DP / 16), c = e % (DP / 16);
                     if (e >= V) continue;
-                    if (x & 1) {
+                    if ((x & 1) && gaps) {
                         // (a value that is not there may be none, and would not vanish times zero)
                         const uint32_t word = r < 64 ? (r < 32 ? bits.x : bits.y) : (r < 96 ? bits.z : bits.w);
                         if (!(word >> (r & 31) & 1)) v[u] = make_uint4(0u, 0u, 0u, 0u);
@@ -295,49 +341,11 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
     }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
-        // ------------------------------------------------------------ q as fp16, a row to sixteen lanes, eight at a time
-        for (int b = warp * 2 + (lane >> 4); b < M; b += 16 * 8) {
-            const int c = lane & 15;
-            uint4 x[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int r = b + 16 * u, i = (r0 + r) / p.group, h = (r0 + r) - i * p.group;
-                x[u] = make_uint4(0u, 0u, 0u, 0u);
-                if (r < rows && 8 * c < p.head_dim)
-                    x[u] = ldg_v4(p.q + (long long)(s.row0 + i) * p.q_row + (long long)(piece.head * p.group + h) * p.q_head + 8 * c);
-            }
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int r = b + 16 * u;
-                uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-                float up = 1.f;
-                if (DT == DT_BF16) {
-                    // 2^(14 - e) for a largest value of 2^e to 2^(e + 1); rows without a finite, not tiny one stay as they are
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-#pragma unroll
-                    for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    const int ex = (int)(top >> 7);
-                    if (ex > 0 && ex < 255) up = __uint_as_float((uint32_t)min(254, 127 + 14 + 127 - ex) << 23);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 f = Ops::unpack(w[e]);
-                        w[e] = DTypeOps<DT_F16>::pack(f.x * up, f.y * up);
-                    }
-                }
-                if (8 * c < DP)
-                    st_shared_v4(sbase + r / kRows * Lay::kBlock + (c >> 3) * (kRows * 128) + r % kRows * 128 + (((c & 7) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
-                if (c == 0) cs[r] = fmaxf(p.log2_scale / up, 0x1p-126f);
-            }
-        }
-        fence_proxy_async_smem();
-        named_bar_sync(1, 2 * kRows);
-        if (threadIdx.x == 0) mbar_arrive(q_full);
         // ------------------------------------------------------------ softmax: a row per thread
         const int i = warp >> 2, n = i ? n1 : n0, r = (int)threadIdx.x;  // (one tile: warps 4-7 have nothing to do)
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, s_col = lanes + 128u * i, o_col = lanes + kOCol + 128u * i;
         const float kNone = __int_as_float(0xff800000);
+        wait_here(q_full, 0, p.status, p.timeout_ns, 59);
         const float c = r < M ? cs[r] : 0.f;
         const int qi = min(r0 + r, s.n * p.group - 1) / p.group;  // the row of q among the sequence's
         const uint8_t* tree = p.tree == nullptr ? nullptr : p.tree + (s.row0 + qi) * p.tree_stride;

@@ -8,16 +8,16 @@
 // order to the entries that want one in ascending order (sequence, then place in
 // its table): the answer depends on the arguments alone.
 //
-// Resize and fork are one kernel of one cluster of eight CTAs, 256 warps. Each
-// warp takes a run of neighbouring table segments of 256 entries and a run of
-// neighbouring pages:
+// Resize and fork are one kernel of one CTA for small tables, where a barrier costs
+// little, or of one cluster of eight or sixteen. Each warp takes a run of
+// neighbouring table segments of 256 entries and a run of neighbouring pages:
 //   1. entries past the new length are released (refs - 1), wanting ones counted
 //   2. free pages counted; both counts go to every CTA through distributed
 //      shared memory, so that each warp knows how many stand in front of its own
 //   3. the k-th free page is written to place k of a list, k below the wanted number
 //   4. the k-th wanting entry takes page k of the list
-// with a cluster barrier after each. Nothing but latency bounds it: tables of 256 x
-// 1024 entries are 1 MB, read by eight multiprocessors.
+// with a barrier after each. Nothing but latency bounds it: the barriers, and the rounds of
+// loads of a warp's run, eight loads to a round.
 #include <algorithm>
 
 #include "fl_common.cuh"
@@ -27,7 +27,6 @@ namespace fl {
 
 namespace {
 
-constexpr int kCluster = 8;
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSegment = 256;  // table entries of a warp at a time
@@ -62,13 +61,21 @@ __device__ __forceinline__ void publish(Share& s, int count) {
         if (lane == 0) s.total = v;
     }
 }
+template <int CTAS>
+__device__ __forceinline__ void all_sync() {
+    if constexpr (CTAS == 1) __syncthreads();
+    else cluster_barrier_sync();
+}
+template <int CTAS>
 __device__ __forceinline__ void collect(Share& s, int& before, int& all) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
+    const uint32_t rank = CTAS == 1 ? 0u : cluster_rank();
     int v = 0, w = lane < warp ? s.mine[lane] : 0;
-    if (lane < kCluster)
+    if constexpr (CTAS == 1) {
+        if (lane == 0) v = s.total;
+    } else if (lane < CTAS)
         asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(mapa_cluster(smem_u32(&s.total), lane)) : "memory");
-    if ((uint32_t)lane < rank) w += v;
+    if (CTAS > 1 && (uint32_t)lane < rank) w += v;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -77,14 +84,14 @@ __device__ __forceinline__ void collect(Share& s, int& before, int& all) {
     before = w, all = v;
 }
 
-template <bool FORK>
+template <bool FORK, int CTAS>
 __global__ void __launch_bounds__(kThreads, 1) fl_kv_pages_kernel(const __grid_constant__ PagesParams p) {
     __shared__ Share wanting, freed;
     griddep_wait();
     griddep_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int me = (int)cluster_rank() * kWarps + warp;
-    constexpr int kAll = kCluster * kWarps;
+    const int me = (CTAS == 1 ? 0 : (int)cluster_rank()) * kWarps + warp;
+    constexpr int kAll = CTAS * kWarps;
     const int per_row = (p.table_pages + kSegment - 1) / kSegment;
     const long long segments = (long long)p.n * per_row;
     const long long s0 = segments * me / kAll, s1 = segments * (me + 1) / kAll;
@@ -115,11 +122,12 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_pages_kernel(const __grid_c
                 if (held(e)) atomicAdd(p.refs + e, -1);
             }
         }
-        cluster_barrier_sync();
+        all_sync<CTAS>();
     }
     // Entries of this warp's segments: want(u, j) for those that want a page.
     // Phase 0 releases or shares and counts, phase 1 gives pages.
     int count = 0;
+    uint32_t wants_of = 0;  // resize: which of a lane's entries want a page, of the first 32 / kPer segments
     for (long long s = s0; s < s1; ++s) {
         const int i = (int)(s / per_row), j0 = (int)(s % per_row) * kSegment;
         int part;
@@ -140,7 +148,9 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_pages_kernel(const __grid_c
                     atomicAdd(p.refs + e[u], -1);
                     row[j] = -1;
                 }
-                count += j < need && !held(e[u]);
+                const bool wants = j < need && !held(e[u]);
+                count += wants;
+                if (s - s0 < 32 / kPer) wants_of |= (uint32_t)wants << ((int)(s - s0) * kPer + u);
             }
         } else {
             const int c = __ldg(p.children + i), from = __ldg(p.parents + i);
@@ -172,41 +182,43 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_pages_kernel(const __grid_c
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) count += __shfl_xor_sync(0xffffffffu, count, o);
     publish(wanting, count);
-    cluster_barrier_sync();
+    all_sync<CTAS>();
     int rank, wanted, at, available;
-    collect(wanting, rank, wanted);
+    collect<CTAS>(wanting, rank, wanted);
 
     const int f0 = (int)((long long)p.n_pages * me / kAll), f1 = (int)((long long)p.n_pages * (me + 1) / kAll);
     if (wanted > 0) {  // (the same in the whole cluster)
+        // (which of its pages are free: 32 rounds of a page to a lane are kept, more are read again)
+        uint32_t flags = 0;
+        auto free_at = [&](int q) { return q < f1 && __ldcg(p.refs + q) == 0; };
         count = 0;
-        for (int b = f0; b < f1; b += 32 * kPer) {
+        for (int i0 = 0; f0 + 32 * i0 < f1; i0 += kPer) {
+            bool is[kPer];
+#pragma unroll
+            for (int u = 0; u < kPer; ++u) is[u] = free_at(f0 + 32 * (i0 + u) + lane);
 #pragma unroll
             for (int u = 0; u < kPer; ++u) {
-                const int q = b + 32 * u + lane;
-                count += q < f1 && __ldcg(p.refs + q) == 0;
+                count += is[u];
+                if (i0 + u < 32) flags |= (uint32_t)is[u] << ((i0 + u) & 31);
             }
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) count += __shfl_xor_sync(0xffffffffu, count, o);
         publish(freed, count);
-        cluster_barrier_sync();
-        collect(freed, at, available);
-        for (int b = f0; b < f1 && at < wanted; b += 32 * kPer) {
-            bool is[kPer];
-#pragma unroll
-            for (int u = 0; u < kPer; ++u) is[u] = b + 32 * u + lane < f1 && __ldcg(p.refs + b + 32 * u + lane) == 0;
-#pragma unroll
-            for (int u = 0; u < kPer; ++u) {
-                const uint32_t m = __ballot_sync(0xffffffffu, is[u]);
-                const int q = b + 32 * u + lane, k = at + __popc(m & ((1u << lane) - 1));
-                if (is[u] && k < wanted) {
-                    p.list[k] = q;
-                    p.refs[q] = 1;
-                }
-                at += __popc(m);
+        all_sync<CTAS>();
+        collect<CTAS>(freed, at, available);
+        for (int i = 0; f0 + 32 * i < f1 && at < wanted; ++i) {
+            const int q = f0 + 32 * i + lane;
+            const bool is = i < 32 ? flags >> i & 1 : free_at(q);
+            const uint32_t m = __ballot_sync(0xffffffffu, is);
+            const int k = at + __popc(m & ((1u << lane) - 1));
+            if (is && k < wanted) {
+                p.list[k] = q;
+                p.refs[q] = 1;
             }
+            at += __popc(m);
         }
-        cluster_barrier_sync();
+        all_sync<CTAS>();
         for (long long s = s0; s < s1; ++s) {
             const int i = (int)(s / per_row), j0 = (int)(s % per_row) * kSegment;
             int part, limit, first, c = i;
@@ -225,22 +237,29 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_pages_kernel(const __grid_c
             }
             if (!ok) continue;
             int* row = p.page_table + c * p.table_stride;
+            // (all places in the list first, then all loads from it)
+            int k[kPer], page[kPer];
 #pragma unroll
             for (int u = 0; u < kPer; ++u) {
                 const int j = j0 + 32 * u + lane;
-                const bool wants = j >= first && j < limit && j < p.table_pages && (FORK || !held(__ldcg(row + j)));
+                bool wants = j >= first && j < limit && j < p.table_pages;
+                if (!FORK) wants = s - s0 < 32 / kPer ? wants_of >> ((int)(s - s0) * kPer + u) & 1 : wants && !held(__ldcg(row + j));
                 const uint32_t m = __ballot_sync(0xffffffffu, wants);
-                const int k = rank + __popc(m & ((1u << lane) - 1));
-                if (wants) {
-                    row[j] = k < available ? __ldcg(p.list + k) : -1;
-                    if (k >= available) atomicCAS(p.range, 0, i + 1);
-                }
+                k[u] = wants ? rank + __popc(m & ((1u << lane) - 1)) : -1;
                 rank += __popc(m);
             }
+#pragma unroll
+            for (int u = 0; u < kPer; ++u) page[u] = k[u] >= 0 && k[u] < available ? __ldcg(p.list + k[u]) : -1;
+#pragma unroll
+            for (int u = 0; u < kPer; ++u)
+                if (k[u] >= 0) {
+                    row[j0 + 32 * u + lane] = page[u];
+                    if (k[u] >= available) atomicCAS(p.range, 0, i + 1);
+                }
         }
     }
-    // (the counts of this CTA may still be read by another)
-    cluster_barrier_sync();
+    // (the counts of this CTA may still be read by another; with pages given out there was a barrier since)
+    if (CTAS > 1 && wanted == 0) all_sync<CTAS>();
 }
 
 // The rows of a parent's last, partly filled page into the child's: one
@@ -427,7 +446,21 @@ fl_status check_cache(const char* what, const fl_kv_pages* c) {
 
 template <bool FORK>
 fl_status launch_pages(const char* what, const PagesParams& p, const host::LaunchContext& ctx, cudaStream_t stream) {
-    return host::launched(host::launch_cluster(fl_kv_pages_kernel<FORK>, dim3(kCluster), kThreads, 0, ctx.pdl, kCluster, stream, p), what);
+    // A segment to a warp decides: one CTA, eight or sixteen. Two resize calls, us, with 1 / 8 / 16 CTAs: seven
+    // sequences of 16 entries and 79 pages 6.9 / 9.1 / 13.3; 61 of 256 and 10863 pages 14.0 / 11.1 / 14.2; 256 of
+    // 1024 and 121048 pages 178 / 26.1 / 20.9; a fork of 8 to 56 children 15.6 / 11.9 / 15.2.
+    const long long segments = (long long)p.n * ((p.table_pages + kSegment - 1) / kSegment);
+    if (segments <= 32 && p.n_pages <= 2048)
+        return host::launched(host::launch(fl_kv_pages_kernel<FORK, 1>, dim3(1), kThreads, 0, ctx.pdl, stream, p), what);
+    if (segments <= 512 && p.n_pages <= 65536)
+        return host::launched(host::launch_cluster(fl_kv_pages_kernel<FORK, 8>, dim3(8), kThreads, 0, ctx.pdl, 8, stream, p), what);
+    static std::atomic<unsigned long long> done{0};
+    if (!(done.load(std::memory_order_relaxed) >> ctx.device & 1)) {
+        const cudaError_t e = cudaFuncSetAttribute(fl_kv_pages_kernel<FORK, 16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return fail(FL_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+        done.fetch_or(1ull << ctx.device, std::memory_order_relaxed);
+    }
+    return host::launched(host::launch_cluster(fl_kv_pages_kernel<FORK, 16>, dim3(16), kThreads, 0, ctx.pdl, 16, stream, p), what);
 }
 
 PagesParams pages_params(const fl_kv_pages* c, int* refs, const int* lengths, void* workspace, int* range) {

@@ -732,7 +732,8 @@ def random_tables(rng, B, per, pages, share=0.2):
 
 
 @pytest.mark.parametrize("B,per,pages,page", [(1, 1, 1, 16), (1, 9, 30, 16), (3, 300, 700, 1), (7, 16, 130, 16), (61, 40, 900, 7),
-                                              (256, 65, 9000, 64), (300, 3, 2000, 16), (2, 5000, 12000, 4), (40, 7, 60, 16)])
+                                              (256, 65, 9000, 64), (300, 3, 2000, 16), (2, 5000, 12000, 4), (40, 7, 60, 16),
+                                              (20, 20, 2049, 16), (600, 9, 700, 16), (9, 600, 70000, 16), (3, 40, 600000, 16)])
 def test_kv_resize(B, per, pages, page):
     rng = gen(60, B, per)
     table, refs = random_tables(rng, B, per, pages)
