@@ -116,8 +116,8 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
 }
 
 // HD: head_dim rounded up to 64, 128 or 256. QT: tiles of eight rows of q (of a
-// sequence's rows and a group's heads). TMA: head_dim a multiple of 16; otherwise the
-// codes come in copies of 8 bytes.
+// sequence's rows and a group's heads). TMA: head_dim a multiple of 16, and boxes that
+// can start where they have to; otherwise the codes come in copies of 8 bytes.
 template <int DT, int FMT, int HD, int QT, bool TMA>
 __global__ void __launch_bounds__(kThreads, Layout<HD, QT>::kCtas) fl_kv_attend_kernel(const __grid_constant__ AttendParams p) {
     using Ops = DTypeOps<DT>;
@@ -545,6 +545,8 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, QT>::kCtas) fl_kv_attend_
 struct Plan {
     int hd, qt, group;
     int tile;         // rows of a row block of the kernel for many rows, or 0
+    int box_log;      // log2 of the positions of a TMA box: as many as a page holds whole numbers of, 16 at most
+    bool tma;
     long long units;  // row blocks and heads at most
     bool split;       // whether a sequence can be long enough to be split
     int rows() const { return tile ? tile : 8 * qt; }
@@ -558,7 +560,11 @@ Plan plan_of(const fl_kv_attend_desc* d) {
     // not fit is another row block, which reads the codes again
     const long long each = d->cu_rows == nullptr ? p.group : ((long long)d->rows + d->n_seqs - 1) / d->n_seqs * p.group;
     p.qt = each <= 8 ? 1 : each <= 16 || p.hd == 256 ? 2 : 4;
-    p.tile = each > kRowsLimit && (long long)d->table_pages * d->page_size >= kLongTable && p.hd <= 128 && d->head_dim % 16 == 0 ? (each <= 128 ? 128 : 256) : 0;
+    p.box_log = 0;
+    while (p.box_log < 4 && d->page_size % (2 << p.box_log) == 0) ++p.box_log;
+    // (a box starts on 128 bytes of shared memory: two positions of 64 channels)
+    p.tma = d->head_dim % 16 == 0 && (p.hd > 64 || p.box_log > 0);
+    p.tile = each > kRowsLimit && (long long)d->table_pages * d->page_size >= kLongTable && p.hd <= 128 && p.tma ? (each <= 128 ? 128 : 256) : 0;
     const long long seqs = d->rows < d->n_seqs ? d->rows : d->n_seqs, M = p.rows();
     p.units = d->cu_rows == nullptr ? seqs * ((p.group + M - 1) / M) * d->heads_k
                                     : (((long long)d->rows * p.group + (M - 1) * seqs) / M) * d->heads_k;
@@ -654,11 +660,8 @@ fl_status run(const fl_kv_attend_desc* d, void* workspace, size_t workspace_byte
     p.log2_scale = d->scale * 1.44269504088896341f;
     p.part = plan.split ? static_cast<float*>(workspace) : nullptr;
     p.range = ctx.range, p.status = ctx.status, p.timeout_ns = ctx.timeout_ns;
-    // boxes: as many positions as a page holds whole numbers of, 16 at most
-    p.box_log = 0;
-    while (p.box_log < 4 && d->page_size % (2 << p.box_log) == 0) ++p.box_log;
-    const bool tma = d->head_dim % 16 == 0;
-    if (tma)
+    p.box_log = plan.box_log;
+    if (plan.tma)
         for (int w = 0; w < 2; ++w)
             if ((st = host::encode_pages(&p.tm[w], w == 0 ? d->k_cache : d->v_cache, d->head_dim, d->heads_k, d->page_size,
                                          d->n_pages, plan.hd == 64 ? 64 : 128, 1u << p.box_log, plan.tile == 0)) != FL_OK)
@@ -697,7 +700,7 @@ fl_status run(const fl_kv_attend_desc* d, void* workspace, size_t workspace_byte
         return both(dt, fmt, hd, integral_constant<int, 2>(), by_tma);
     };
     auto by_copies = [&](auto dt, auto fmt, auto hd) {
-        return tma ? by_rows(dt, fmt, hd, std::true_type()) : by_rows(dt, fmt, hd, std::false_type());
+        return plan.tma ? by_rows(dt, fmt, hd, std::true_type()) : by_rows(dt, fmt, hd, std::false_type());
     };
     auto by_size = [&](auto dt, auto fmt) {
         return plan.hd == 64    ? by_copies(dt, fmt, integral_constant<int, 64>())

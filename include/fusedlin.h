@@ -621,10 +621,11 @@ fl_status fl_kv_read(const fl_kv_desc* desc, void* stream);
  *   q, out: [rows, heads_q, head_dim] at the strides given, as k and v above; query
  *   head h reads key head h / (heads_q / heads_k). out overlaps no other tensor.
  * Scores, maxima and sums are fp32; the codes are multiplied as they are. Rounded
- * are the weights, to 11 bits, and the output. scale is positive.
+ * are the weights, to 11 bits, and the output. scale is positive. (The positions that
+ * are read hold what fl_kv_write wrote: no e4m3 code of a NaN.)
  * workspace: fl_kv_attend_workspace_size(desc) bytes (sizes, cu_rows NULL or not; up
- * to 11 MB, 0 for short tables, and then NULL is accepted), 16-byte aligned, the
- * call's own until its kernels are done.
+ * to 11 MB, or 42 for many rows to a sequence; 0 for short tables, and then NULL is
+ * accepted), 16-byte aligned, the call's own until its kernels are done.
  */
 typedef struct {
     fl_dtype dtype;

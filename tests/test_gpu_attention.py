@@ -374,6 +374,10 @@ def attend_check(got, ref, dt, cache, n_rows, start, what=""):
     (3, 1, 128, 64, [1], [4000]),
     (1, 8, 64, 16, [9], [2100]),
     (1, 20, 128, 16, [3], [1000]),
+    (2, 2, 64, 7, [1, 3], [200, 61]),
+    (1, 4, 48, 1, [2], [40]),
+    (2, 4, 64, 6, [5], [600]),
+    (1, 2, 256, 3, [2], [100]),
 ])
 def test_kv_attend(dt, fmt, H, group, D, page, n_rows, start):
     rng = gen(50, H, group, D, page, sum(start))
@@ -398,6 +402,9 @@ def test_kv_attend(dt, fmt, H, group, D, page, n_rows, start):
     (1, 3, 80, 64, [100], [2000]),
     (1, 1, 16, 16, [300], [64]),
     (8, 4, 128, 16, [40, 40], [300, 2000]),
+    (1, 4, 64, 9, [50], [1500]),
+    (1, 4, 64, 6, [50], [1500]),
+    (1, 4, 128, 1, [40], [1100]),
 ])
 def test_kv_attend_many_rows(dt, fmt, H, group, D, page, n_rows, start):
     rng = gen(67, H, group, D, page, sum(start))
