@@ -874,6 +874,112 @@ def test_kv_compact_rows_without_a_page():
     fl.device_status()
 
 
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("B,H,hq,D,page,rows,spread", [(300, 2, 4, 64, 16, 1, 3), (700, 1, 3, 128, 16, 3, 2), (1100, 1, 4, 64, 64, 9, 1)])
+def test_kv_attend_many_sequences(fmt, B, H, hq, D, page, rows, spread):
+    """More sequences than a CTA has threads, a few of them long, so that some are split; some without rows."""
+    rng = gen(71, B, H, hq)
+    n_rows = rng.integers(max(0, rows - spread), rows + spread + 1, B).tolist()
+    start = rng.integers(0, 40, B)
+    start[::97] = rng.integers(1000, 1500, len(start[::97]))
+    start = start.tolist()
+    cache = Paged(rng, [a + b for a, b in zip(n_rows, start)], H, D, page, fmt)
+    got, ref, q = attend_case(rng, "bf16", cache, hq, n_rows, start)
+    fl.device_status()
+    attend_check(got, ref, "bf16", cache, n_rows, start)
+    again = fl.kv_attend(q, *cache.tensors(), ints(cache.table), ints(start), cu_rows=ints(sums(n_rows)))
+    assert torch.equal(again, got)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("group,n", [(1, 1), (4, 12)])
+def test_cache_of_more_bytes_than_32_bits_count(fmt, group, n):
+    """The last pages of a cache of more than 2^32 bytes of k, and of v, answer as the first ones of a small cache do: rows
+    written, attended, forked and moved."""
+    rng = gen(72, group, n)
+    H, D, page, per, B = 8, 128, 64, 20, 3
+    pages = (1 << 32) // (page * H * D) + 200
+    start = [1150, 64, 100]
+    answers = []
+    for n_pages, first in ((100, 0), (pages, pages - 100)):
+        code = FMT[fmt][0]
+        cache = [torch.zeros((n_pages, page, H, D), dtype=torch.int8, device="cuda").view(code) for _ in "kv"]
+        cache += [torch.ones((n_pages, page, H), device="cuda") for _ in "kv"]
+        assert n_pages == 100 or cache[0].numel() > 1 << 32
+        r = gen(73, group, n)
+        refs = torch.ones(n_pages, dtype=torch.int32, device="cuda")
+        refs[first:first + 100] = 0
+        table = torch.full((B, per), -1, dtype=torch.int32, device="cuda")
+        total = [s + n for s in start]
+        fl.kv_resize(table, refs, ints(total[:2] + [0]), page)
+        k, v = (put(r.standard_normal((sum(total[:2]), H, D)), "bf16") for _ in "kv")
+        fl.kv_write(k, v, *cache, table, ints([0, 0, 0]), cu_rows=ints(sums(total[:2] + [0])))
+        fl.kv_fork(*cache, table, refs, ints([0]), ints([2]), ints([start[2]]))
+        fl.kv_resize(table, refs, ints(total), page)
+        k, v = (put(r.standard_normal((n, H, D)), "bf16") for _ in "kv")
+        fl.kv_write(k, v, *cache, table, ints([0, 0, start[2]]), cu_rows=ints([0, 0, 0, n]))
+        q = put(r.standard_normal((B * n, H * group, D)), "bf16")
+        cu = ints([0, n, 2 * n, 3 * n])
+        out = [fl.kv_attend(q, *cache, table, ints(start), cu_rows=cu)]
+        if n > 1:
+            fl.kv_compact(*cache, table, ints(start), ints([[1, 3, 7], [0, 11, -1], [-1, 0, 0]]))
+            out.append(fl.kv_attend(q, *cache, table, ints(start), cu_rows=cu))
+        back = [torch.empty((sum(total), H, D), dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+        fl.kv_read(*cache, table, ints(sums(total)), out_k=back[0], out_v=back[1])
+        fl.device_status()
+        answers.append((table - first * (table >= 0), refs[first:first + 100].clone(), *out, *back))
+        del cache
+    for a, b in zip(*answers):
+        assert torch.equal(a, b)
+    assert not torch.equal(answers[0][2], torch.zeros_like(answers[0][2]))
+
+
+def test_attention_strides_past_32_bits():
+    """Rows and heads whose places lie more than 2^32 bytes apart."""
+    rng = gen(74)
+    big = torch.empty((300, 1 << 23), dtype=torch.bfloat16, device="cuda")
+    assert big.numel() * 2 > 1 << 32
+    views = [big[:, i * 1024:i * 1024 + 256].unflatten(1, (2, 128)) for i in range(4)]
+    q, k, v = (put(rng.standard_normal((300, 2, 128)), "bf16") for _ in "qkv")
+    for x, y in zip(views, (q, k, v)):
+        x.copy_(y)
+    for cu in (None, ints([0, 17, 290])):
+        want, out = torch.full_like(q, 7.0), views[3]
+        out.fill_(7.0)
+        fl.attention(q, k, v, cu_q=cu, out=want)
+        fl.attention(*views[:3], cu_q=cu, out=out)
+        fl.device_status()
+        assert torch.equal(out, want)
+
+
+def test_calls_without_overlapped_launches():
+    """The same answers when a kernel starts only once the one before it has ended."""
+    rng = gen(75)
+    q = put(rng.standard_normal((40, 4, 64)), "f16")
+    kv = put(rng.standard_normal((5000, 1, 64)), "f16")
+    start = [5000, 30]
+    cache = Paged(rng, [5020, 50], 2, 64, 16, "int8")
+    x = put(rng.standard_normal((40, 4, 64)), "f16")
+
+    def calls():
+        refs = ints(np.bincount(cache.table[cache.table >= 0], minlength=cache.pages))
+        table = ints(cache.table)
+        a = fl.attention(q, kv, kv)
+        b = fl.kv_attend(x, *cache.tensors(), table, ints(start), cu_rows=ints([0, 20, 40]))
+        fl.kv_resize(table, refs, ints([100, 70]), 16)
+        return a, b, table, refs
+
+    want = calls()
+    fl.set_option("pdl", 0)
+    try:
+        got = calls()
+    finally:
+        fl.set_option("pdl", 1)
+    fl.device_status()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 # ---------------------------------------------------------------------------
 # a step as it is used
 # ---------------------------------------------------------------------------
