@@ -84,7 +84,7 @@ __device__ __forceinline__ uint32_t place(int r, int c) {
 }
 
 // Shared memory: the warps' rings (k and v of a stage, 1024-byte aligned); what a
-// warp leaves to be joined (sums [M][HD + 2], then [M][4]: maxima, sum of weights, seen)
+// warp leaves to be joined (sums [M][HD + 4], then [M][4]: maxima, sum of weights, seen)
 // lies in its own ring where that holds it, so that the warps of other pieces may still
 // be at work; per warp and stage scales of k and v and which positions
 // are there; the barriers; the rows of q as MMA fragments, where registers do not hold them.
@@ -96,7 +96,7 @@ struct Layout {
     static constexpr int kStages = HD == 64 ? 4 : 3;
     static constexpr int kStage = 2 * kStep * HD;
     static constexpr int kRing = kWarps * kStages * kStage;
-    static constexpr int kSums = M * (HD + 2) * 4;
+    static constexpr int kSums = M * (HD + 4) * 4;
     static constexpr int kArea = kQInRegs ? kStages * kStage : kSums + M * 16;  // from one warp's sums to the next's
     static_assert(kSums + M * 16 <= kArea, "sums of a warp");
     static constexpr int kFirst = kRing > kWarps * kArea ? kRing : kWarps * kArea;
@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, QT>::kCtas) fl_kv_attend_
     if (lane == 0) {
         for (int s = 0; s < NS; ++s) mbar_init(full(s), 33);
         fence_mbar_init();
+        if (TMA && warp < 2) tma_prefetch_desc(&p.tm[warp]);
     }
     griddep_wait();
     griddep_launch_dependents();
@@ -173,10 +174,10 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, QT>::kCtas) fl_kv_attend_
     const int steps = k1 > k0 + own * kStep ? (k1 - k0 - own * kStep + stride - 1) / stride : 0;
     const int* table = p.page_table + piece.seq * p.table_stride;
     // the table's entry of this lane's position of a step, one step ahead; -2: there is no such position
-    int entry = -2, in_page = 0;
-    auto look_up = [&](int step) {
+    int entry, in_page;
+    auto look_up = [&](int step, int& entry, int& in_page) {
         const int pos = k0 + own * kStep + step * stride + (lane & 15);
-        entry = -2;
+        entry = -2, in_page = 0;
         if (step < steps && pos < k1) {
             const int j = p.page_shift >= 0 ? pos >> p.page_shift : (int)((uint32_t)pos / (uint32_t)p.page_size);
             in_page = pos - j * p.page_size;
@@ -225,24 +226,28 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, QT>::kCtas) fl_kv_attend_
             x[j] = r < rows && ch + 16 * t < p.head_dim ? ldg_v4(q + ch) : make_uint4(0u, 0u, 0u, 0u);
         }
     };
-    int first_entry[NS], first_row[NS];
+    // (a lane's entries of steps lane / 16 and 2 + lane / 16)
+    int first_entry[2], first_row[2];
+    static_assert(NS == 3 || NS == 4, "two look-ups of two steps");
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-        look_up(i);
-        first_entry[i] = entry, first_row[i] = in_page;
-    }
+    for (int i = 0; i < 2; ++i) look_up(2 * i + (lane >> 4), first_entry[i], first_row[i]);
     if constexpr (Lay::kQInRegs) {
 #pragma unroll
         for (int qt = 0; qt < QT; ++qt) load_q(qt, qx[qt]);
     }
     int ahead = stage;
-#pragma unroll
+    auto first = [&](int i) {
+        const int from = 16 * (i & 1) + (lane & 15);
+        entry = __shfl_sync(0xffffffffu, i < 2 ? first_entry[0] : first_entry[1], from);
+        in_page = __shfl_sync(0xffffffffu, i < 2 ? first_row[0] : first_row[1], from);
+    };
+#pragma unroll 1
     for (int i = 0; i < NS - 1; ++i) {
-        entry = first_entry[i], in_page = first_row[i];
+        first(i);
         request(i, ahead);
         if (++ahead == NS) ahead = 0;
     }
-    entry = first_entry[NS - 1], in_page = first_row[NS - 1];
+    first(NS - 1);
 
     // ------------------------------------------------------------ q as the first product's B fragments
     // Step ks = 4 h + w takes channels 64 h + 16 t + 4 w + 0 .. 3 of lane t, in widen_word's order, row g of the tile.
@@ -312,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, QT>::kCtas) fl_kv_attend_
     for (int step = 0; step < steps; ++step) {
         __syncwarp();  // (the stage that is asked for next has been read)
         request(step + NS - 1, ahead);
-        look_up(step + NS);
+        look_up(step + NS, entry, in_page);
         if (++ahead == NS) ahead = 0;
         ok = __all_sync(0xffffffffu, wait_bar(full(stage), phase, p.status, p.timeout_ns, 51));
         if (!ok) break;
@@ -354,14 +359,14 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, QT>::kCtas) fl_kv_attend_
             for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
                 for (int f = 0; f < 2; ++f) {
-                    // the row of q among the sequence's (rows past the last: as the last)
-                    const int qi = min(r0 + 8 * qt + 2 * t + f, s.n * p.group - 1) / p.group;
+                    const int r = min(r0 + 8 * qt + 2 * t + f, s.n * p.group - 1);  // (rows past the last: as the last)
+                    const int qi = p.tree == nullptr ? 0 : r / p.group;             // the row of q among the sequence's
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const long long j = pos0 + g + 8 * i - s.from;
                         bool sees = bits >> (g + 8 * i) & 1;
                         if (sees && j >= 0) {
-                            if (p.tree == nullptr) sees = j <= qi;
+                            if (p.tree == nullptr) sees = j * p.group <= r;
                             else sees = j < p.tree_cols && __ldg(p.tree + (s.row0 + qi) * p.tree_stride + j) != 0;
                         }
                         if (sees) seen |= 1u << (2 * qt + f);
@@ -485,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, QT>::kCtas) fl_kv_attend_
     for (int w = 4; w < 32; w <<= 1) seen |= __shfl_xor_sync(0xffffffffu, seen, w);
 
     // ------------------------------------------------------------ the CTA's warps joined
-    constexpr int P = HD + 2;  // pitch of a row of sums
+    constexpr int P = HD + 4;  // pitch of a row of sums
     auto sums = [&](int w, int r) { return reinterpret_cast<float*>(smem + w * Lay::kArea) + r * P; };
     auto stat = [&](int w, int r) { return reinterpret_cast<float4*>(smem + w * Lay::kArea + Lay::kSums) + r; };
     __syncwarp();
@@ -504,8 +509,8 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, QT>::kCtas) fl_kv_attend_
         }
     group_sync();
     const bool whole = piece.pieces == 1;
-    for (int i = own * 32 + lane; i < rows * (HD / 2); i += 32 * W) {
-        const int r = i / (HD / 2), ch = i % (HD / 2) * 2;
+    for (int i = own * 32 + lane; i < rows * (HD / 4); i += 32 * W) {
+        const int r = i / (HD / 4), ch = i % (HD / 4) * 4;
         float ma = kNone, mb = kNone, any = 0.f;
 #pragma unroll 4
         for (int w = group * W; w < group * W + W; ++w) {
@@ -514,22 +519,24 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, QT>::kCtas) fl_kv_attend_
         }
         const float na = ma == kNone ? 0.f : -ma, nb = mb == kNone ? 0.f : -mb;
         float sum = 0.f;
-        float2 v = make_float2(0.f, 0.f);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int w = group * W; w < group * W + W; ++w) {
             const float4 st = *stat(w, r);
             sum += st.z * ex2(st.x + na);
             const float f = ex2(st.y + nb);
-            const float2 d = *reinterpret_cast<const float2*>(sums(w, r) + ch);
-            v.x = fmaf(d.x, f, v.x), v.y = fmaf(d.y, f, v.y);
+            const float4 d = *reinterpret_cast<const float4*>(sums(w, r) + ch);
+            v.x = fmaf(d.x, f, v.x), v.y = fmaf(d.y, f, v.y), v.z = fmaf(d.z, f, v.z), v.w = fmaf(d.w, f, v.w);
         }
         if (whole) {
             if (ch < p.head_dim) {
                 const float2 f = finish(ma, mb, sum, any);
-                *reinterpret_cast<uint32_t*>(row_at(p, s.row0, piece.head, r0 + r) + ch) = f.y != 0.f ? 0u : Ops::pack(v.x * f.x, v.y * f.x);
+                uint2 y = make_uint2(0u, 0u);
+                if (f.y == 0.f) y = make_uint2(Ops::pack(v.x * f.x, v.y * f.x), Ops::pack(v.z * f.x, v.w * f.x));
+                *reinterpret_cast<uint2*>(row_at(p, s.row0, piece.head, r0 + r) + ch) = y;
             }
         } else {
-            *reinterpret_cast<float2*>(p.part + ((long long)piece.slot * M + r) * HD + ch) = v;
+            *reinterpret_cast<float4*>(p.part + ((long long)piece.slot * M + r) * HD + ch) = v;
             if (ch == 0)
                 *reinterpret_cast<float4*>(p.part + (long long)slots(kResident) * M * HD + ((long long)piece.slot * M + r) * 4) =
                     make_float4(ma, mb, sum, any);
@@ -568,7 +575,7 @@ Plan plan_of(const fl_kv_attend_desc* d) {
     const long long seqs = d->rows < d->n_seqs ? d->rows : d->n_seqs, M = p.rows();
     p.units = d->cu_rows == nullptr ? seqs * ((p.group + M - 1) / M) * d->heads_k
                                     : (((long long)d->rows * p.group + (M - 1) * seqs) / M) * d->heads_k;
-    p.split = (long long)d->table_pages * d->page_size > (long long)kLeast * kTile;
+    p.split = (long long)d->table_pages * d->page_size > (long long)kWorth * kTile;
     return p;
 }
 size_t workspace_of(const Plan& p) {

@@ -14,6 +14,7 @@ constexpr int kStep = 16;     // positions of a warp's step in the kernel for fe
 constexpr int kTile = 128;    // positions of a tile
 constexpr int kLeast = 2;     // tiles of a piece at least
 constexpr int kStart = 3, kJoin = 3;  // tiles that a piece's start and end, and the second launch, take as long as
+constexpr int kWorth = kLeast + kJoin;  // tiles of a sequence up to which a split cannot pay for the second launch
 constexpr float kLazy = 8.f;  // a maximum is moved once it is exceeded by 2^8
 
 // Pieces of split sequences at most, with `resident` CTAs at work at once: L is T /
@@ -179,7 +180,7 @@ struct Pieces {
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) t += sum_t[w], top = max(top, top_t[w]);
         L = kWhole;
-        if (top > kLeast) {
+        if (top > kWorth) {
             // Each lane's candidate, and what it costs: the rounds, times their longest piece and a start. (In
             // a loop: a CTA's first instructions come from far, so the fewer of them the better.)
             const int me = min(lane, kCandidates);
@@ -221,8 +222,15 @@ struct Pieces {
         fn = n, fs = sl, fu = un;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t a = __shfl_up_sync(0xffffffffu, fn, o), c = __shfl_up_sync(0xffffffffu, fs, o), d = __shfl_up_sync(0xffffffffu, fu, o);
-            if (lane >= o) fn += a, fs += c, fu += d;
+            const uint32_t a = __shfl_up_sync(0xffffffffu, fn, o);
+            if (lane >= o) fn += a;
+        }
+        if (L != kWhole) {
+#pragma unroll 1
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t c = __shfl_up_sync(0xffffffffu, fs, o), d = __shfl_up_sync(0xffffffffu, fu, o);
+                if (lane >= o) fs += c, fu += d;
+            }
         }
         if (lane == 31) sum_n[warp] = fn, sum_s[warp] = fs, sum_u[warp] = fu;
         fn -= n, fs -= sl, fu -= un;
