@@ -14,7 +14,7 @@ constexpr int kStep = 16;     // positions of a warp's step in the kernel for fe
 constexpr int kTile = 128;    // positions of a tile
 constexpr int kLeast = 2;     // tiles of a piece at least
 constexpr int kStart = 3, kJoin = 3;  // tiles that a piece's start and end, and the second launch, take as long as
-constexpr int kWorth = kLeast + kJoin;  // tiles of a sequence up to which a split cannot pay for the second launch
+constexpr int kWorth = kLeast + kJoin - 1;  // tiles of a sequence up to which a split gains less than the second launch costs
 constexpr float kLazy = 8.f;  // a maximum is moved once it is exceeded by 2^8
 
 // Pieces of split sequences at most, with `resident` CTAs at work at once: L is T /
