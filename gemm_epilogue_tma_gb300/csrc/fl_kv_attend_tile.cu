@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
         mbar_init(q_full, kWarps - 1);
         fence_mbar_init();
     }
+    if (warp == kWarpTma && lane < 2) tma_prefetch_desc(&p.tm[lane]);
     if (warp == kWarpMma) {
         tmem_alloc(sbase + Lay::kOffSlot, 512);
         tmem_relinquish();
@@ -150,23 +151,23 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
         auto place = [&](int r) {
             return sbase + r / kRows * Lay::kBlock + (c >> 3) * (kRows * 128) + r % kRows * 128 + (((c & 7) ^ (r & 7)) << 4);
         };
-#pragma unroll 1
-        for (int r = first; r < M; r += kStride) {
-            const int i = (r0 + r) / p.group, h = (r0 + r) - i * p.group;
+        constexpr int Q = (M + kStride - 1) / kStride;
+        uint4 q[Q];
+#pragma unroll
+        for (int u = 0; u < Q; ++u) {
+            const int r = first + u * kStride, i = (r0 + r) / p.group, h = (r0 + r) - i * p.group;
+            q[u] = make_uint4(0u, 0u, 0u, 0u);
             if (r < rows && 8 * c < p.head_dim)
-                cp_async16(place(r), p.q + (long long)(s.row0 + i) * p.q_row + (long long)(piece.head * p.group + h) * p.q_head + 8 * c);
-            else if (8 * c < DP)
-                st_shared_v4(place(r), 0u, 0u, 0u, 0u);
+                q[u] = ldg_v4(p.q + (long long)(s.row0 + i) * p.q_row + (long long)(piece.head * p.group + h) * p.q_head + 8 * c);
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll 2
-        for (int r = first; r < M; r += kStride) {  // (its own copies)
+#pragma unroll
+        for (int u = 0; u < Q; ++u) {
+            const int r = first + u * kStride;
+            uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
             float up = 1.f;
             if (DT == DT_BF16) {
-                uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (8 * c < DP) x = ld_shared_v4(place(r));
                 // 2^(14 - e) for a largest value of 2^e to 2^(e + 1); rows without a finite, not tiny one stay as they are
-                uint32_t w[4] = {x.x, x.y, x.z, x.w}, top = 0;
+                uint32_t top = 0;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
 #pragma unroll
@@ -178,9 +179,9 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
                     const float2 f = Ops::unpack(w[e]);
                     w[e] = DTypeOps<DT_F16>::pack(f.x * up, f.y * up);
                 }
-                if (8 * c < DP) st_shared_v4(place(r), w[0], w[1], w[2], w[3]);
             }
-            if (c == 0) cs[r] = fmaxf(p.log2_scale / up, 0x1p-126f);
+            if (r < M && 8 * c < DP) st_shared_v4(place(r), w[0], w[1], w[2], w[3]);
+            if (r < M && c == 0) cs[r] = fmaxf(p.log2_scale / up, 0x1p-126f);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -348,35 +349,57 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
         wait_here(q_full, 0, p.status, p.timeout_ns, 59);
         const float c = r < M ? cs[r] : 0.f;
         const int qi = min(r0 + r, s.n * p.group - 1) / p.group;  // the row of q among the sequence's
-        const uint8_t* tree = p.tree == nullptr ? nullptr : p.tree + (s.row0 + qi) * p.tree_stride;
         float mx = kNone, mw = kNone, nx = 0.f, nw = 0.f;  // maxima of x and x + log2 vs; minus them (0 where there is none yet)
         float2 l = make_float2(0.f, 0.f);
         bool seen = false, ok = true;
+        const bool idle = r - lane >= rows;  // (a warp without rows: what its lines of the products hold is not read)
         for (int j = 0; j < n; ++j) {
-            ok = wait_here(tab_full(j), (uint32_t)(j / kTabs & 1), p.status, p.timeout_ns, 68) && wait_here(s_full(i), (uint32_t)(j & 1), p.status, p.timeout_ns, 69);
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            tc_fence_after();
-            const uint32_t tab = sbase + Lay::kOffTab + j % kTabs * (3 * kRows * 4);
-            const uint4 there = ld_shared_v4(sbase + Lay::kOffBits + j % kTabs * 16);
-            uint32_t sees[4] = {there.x, there.y, there.z, there.w};
+            // Drafts that the row sees, found while the scores are on their way. (A row of the tree per load and all rows'
+            // at once: a draft per load and thread, one after another, took 13 us in the last block of a tree of 48.)
             const int pos0 = k0 + j * kRows;
-            const bool all = (sees[0] & sees[1] & sees[2] & sees[3]) == 0xffffffffu && pos0 + kRows <= s.from;
-            if (!all) {
-                // drafts: those that the row sees
-#pragma unroll
+            uint32_t sees[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+            if (pos0 + kRows > s.from && !idle) {
+#pragma unroll 1
                 for (int w = 0; w < 4; ++w) {
                     const long long first = pos0 + 32 * w - s.from;  // the draft at the word's bit 0
                     if (first + 31 < 0) continue;
                     uint32_t m = 0;
-#pragma unroll 1
-                    for (int e = 0; e < 32; ++e) {
-                        const long long d = first + e;
-                        const bool is = d < 0 || (tree == nullptr ? d <= qi : d < p.tree_cols && __ldg(tree + d) != 0);
-                        m |= (uint32_t)is << e;
+                    if (p.tree == nullptr) {
+                        const long long d = qi - first;
+                        m = d >= 31 ? 0xffffffffu : d < 0 ? 0u : (2u << (int)d) - 1u;
+                    } else {
+                        const long long d = first + lane;
+                        uint32_t is[32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const long long row = s.row0 + __shfl_sync(0xffffffffu, qi, k);
+                            is[k] = d >= 0 && d < p.tree_cols ? __ldg(p.tree + row * p.tree_stride + d) : d < 0;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const uint32_t word = __ballot_sync(0xffffffffu, is[k] != 0);
+                            if (lane == k) m = word;
+                        }
                     }
-                    sees[w] &= m;
+                    if (w == 0) sees[0] = m;
+                    if (w == 1) sees[1] = m;
+                    if (w == 2) sees[2] = m;
+                    if (w == 3) sees[3] = m;
                 }
             }
+            ok = wait_here(tab_full(j), (uint32_t)(j / kTabs & 1), p.status, p.timeout_ns, 68) && wait_here(s_full(i), (uint32_t)(j & 1), p.status, p.timeout_ns, 69);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            tc_fence_after();
+            if (idle) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(i));
+                continue;
+            }
+            const uint32_t tab = sbase + Lay::kOffTab + j % kTabs * (3 * kRows * 4);
+            const uint4 there = ld_shared_v4(sbase + Lay::kOffBits + j % kTabs * 16);
+            sees[0] &= there.x, sees[1] &= there.y, sees[2] &= there.z, sees[3] &= there.w;
+            const bool all = (sees[0] & sees[1] & sees[2] & sees[3]) == 0xffffffffu;
             seen |= (sees[0] | sees[1] | sees[2] | sees[3]) != 0;
             // Weights of the values: 2^(x + log2 vs - mw) = 2^(x - mx) vs 2^(mx - mw). Once there are maxima, and where every
             // position is seen, they are formed in one pass with those: good unless a weight passes 2^8 (or the
@@ -384,6 +407,19 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
             uint32_t w[4][16];
             bool done = false;
             const float2 cc = make_float2(c, c);
+            if (__all_sync(0xffffffffu, all) && __any_sync(0xffffffffu, mx == kNone || mw == kNone)) {
+                // (the first maxima: those of a quarter, which mostly will do)
+                float x[32], ta = kNone, tb = kNone;
+                tmem_ld_32x32b_x32(s_col, reinterpret_cast<uint32_t(&)[32]>(x));
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const float y = x[e] * ld_shared_f32(tab + e * 4) * c;
+                    ta = fmaxf(ta, y), tb = fmaxf(tb, y + ld_shared_f32(tab + (2 * kRows + e) * 4));
+                }
+                if (mx == kNone && ta > kNone) mx = ta, nx = -ta;
+                if (mw == kNone && tb > kNone) mw = tb, nw = -tb;
+            }
             if (__all_sync(0xffffffffu, all && mx > kNone && mw > kNone)) {
                 const float to = ex2(nw - nx);
                 const float2 nn = make_float2(nx, nx), tt = make_float2(to, to);
@@ -515,6 +551,16 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
             if (piece.pieces > 1 && r < rows)
                 *reinterpret_cast<float4*>(p.part + (long long)slots(kTileResident) * M * DP + ((long long)piece.slot * M + r) * 4) =
                     make_float4(mx, mw, sum, seen ? 1.f : 0.f);
+            if (piece.pieces > 1) {
+                // (a row is 4 DP bytes in a run: one bulk copy; a row at a time by all lanes took 3 us)
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (r < rows) {
+                    float* d = p.part + ((long long)piece.slot * M + r) * DP;
+                    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(d), "r"(part), "r"(DP * 4) : "memory");
+                    asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+                }
+            } else
 #pragma unroll 4
             for (int k = 0; k < 32; ++k) {
                 const float fx = __shfl_sync(0xffffffffu, mine_f.x, k), fy = __shfl_sync(0xffffffffu, mine_f.y, k);
@@ -522,11 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
                 float o[C];
 #pragma unroll
                 for (int e = 0; e < C; ++e) o[e] = ld_shared_f32(sbase + ((first + k) * Lay::kPitch + lane * C + e) * 4);
-                if (piece.pieces > 1) {
-                    float* d = p.part + ((long long)piece.slot * M + first + k) * DP + lane * C;
-#pragma unroll
-                    for (int e = 0; e < C; e += 2) *reinterpret_cast<float2*>(d + e) = make_float2(o[e], o[e + 1]);
-                } else if (lane * C < p.head_dim) {
+                if (lane * C < p.head_dim) {
                     uint16_t* d = row_at(p, s.row0, piece.head, r0 + first + k) + lane * C;
 #pragma unroll
                     for (int e = 0; e < C; e += 2)
