@@ -349,13 +349,14 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
         wait_here(q_full, 0, p.status, p.timeout_ns, 59);
         const float c = r < M ? cs[r] : 0.f;
         const int qi = min(r0 + r, s.n * p.group - 1) / p.group;  // the row of q among the sequence's
+        const int q_first = __shfl_sync(0xffffffffu, qi, 0), q_last = __shfl_sync(0xffffffffu, qi, 31);  // of the warp
         float mx = kNone, mw = kNone, nx = 0.f, nw = 0.f;  // maxima of x and x + log2 vs; minus them (0 where there is none yet)
         float2 l = make_float2(0.f, 0.f);
         bool seen = false, ok = true;
         const bool idle = r - lane >= rows;  // (a warp without rows: what its lines of the products hold is not read)
         for (int j = 0; j < n; ++j) {
-            // Drafts that the row sees, found while the scores are on their way. (A row of the tree per load and all rows'
-            // at once: a draft per load and thread, one after another, took 13 us in the last block of a tree of 48.)
+            // Drafts that the row sees, found while the scores are on their way. (A row of the tree per load, eight at
+            // once: a draft per load and thread, one after another, took 13 us in the last block of a tree of 48.)
             const int pos0 = k0 + j * kRows;
             uint32_t sees[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
             if (pos0 + kRows > s.from && !idle) {
@@ -369,16 +370,22 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
                         m = d >= 31 ? 0xffffffffu : d < 0 ? 0u : (2u << (int)d) - 1u;
                     } else {
                         const long long d = first + lane;
-                        uint32_t is[32];
+                        const bool in = d >= 0 && d < p.tree_cols;
+                        constexpr int U = 8;
+#pragma unroll 1
+                        for (int q = q_first; q <= q_last; q += U) {
+                            const uint8_t* at = p.tree + (s.row0 + q) * p.tree_stride + d;
+                            uint32_t is[U];
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const long long row = s.row0 + __shfl_sync(0xffffffffu, qi, k);
-                            is[k] = d >= 0 && d < p.tree_cols ? __ldg(p.tree + row * p.tree_stride + d) : d < 0;
-                        }
+                            for (int u = 0; u < U; ++u) {
+                                is[u] = in && q + u <= q_last ? __ldg(at) : d < 0;
+                                at += p.tree_stride;
+                            }
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const uint32_t word = __ballot_sync(0xffffffffu, is[k] != 0);
-                            if (lane == k) m = word;
+                            for (int u = 0; u < U; ++u) {
+                                const uint32_t word = __ballot_sync(0xffffffffu, is[u] != 0);
+                                if (qi == q + u) m = word;
+                            }
                         }
                     }
                     if (w == 0) sees[0] = m;
@@ -425,11 +432,13 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
                 const float2 nn = make_float2(nx, nx), tt = make_float2(to, to);
                 float2 sum = l;
                 uint32_t most = 0;
+                float x2[2][32];  // (the next 32 scores on their way)
+                tmem_ld_32x32b_x32(s_col, reinterpret_cast<uint32_t(&)[32]>(x2[0]));
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    float x[32];
-                    tmem_ld_32x32b_x32(s_col + 32u * q, reinterpret_cast<uint32_t(&)[32]>(x));
                     tmem_ld_wait();
+                    if (q < 3) tmem_ld_32x32b_x32(s_col + 32u * (q + 1), reinterpret_cast<uint32_t(&)[32]>(x2[(q + 1) & 1]));
+                    const float (&x)[32] = x2[q & 1];
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
                         const uint4 k4 = ld_shared_v4(tab + (32 * q + e) * 4), v4 = ld_shared_v4(tab + (kRows + 32 * q + e) * 4);
@@ -457,10 +466,15 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
                     tmem_ld_32x32b_x32(s_col + 32u * q, reinterpret_cast<uint32_t(&)[32]>(x));
                     tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
+                    for (int e = 0; e < 32; e += 4) {
                         // (a scale that is not there may be anything)
-                        const float y = x[e] * ld_shared_f32(tab + (32 * q + e) * 4) * c;
-                        if (m >> e & 1) ta = fmaxf(ta, y), tb = fmaxf(tb, y + ld_shared_f32(tab + (2 * kRows + 32 * q + e) * 4));
+                        const uint4 k4 = ld_shared_v4(tab + (32 * q + e) * 4), l4 = ld_shared_v4(tab + (2 * kRows + 32 * q + e) * 4);
+                        const uint32_t ks[4] = {k4.x, k4.y, k4.z, k4.w}, lv[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) {
+                            const float y = x[e + f] * __uint_as_float(ks[f]) * c;
+                            if (m >> (e + f) & 1) ta = fmaxf(ta, y), tb = fmaxf(tb, y + __uint_as_float(lv[f]));
+                        }
                     }
                 }
                 const bool over = ta > mx || tb > mw;
@@ -496,17 +510,18 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
                     tmem_ld_wait();
                     uint32_t h[16];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        float a[2], b[2];
+                    for (int e = 0; e < 32; e += 4) {
+                        const uint4 k4 = ld_shared_v4(tab + (32 * q + e) * 4), v4 = ld_shared_v4(tab + (kRows + 32 * q + e) * 4);
+                        const uint32_t ks[4] = {k4.x, k4.y, k4.z, k4.w}, vs[4] = {v4.x, v4.y, v4.z, v4.w};
+                        float a[4], b[4];
 #pragma unroll
-                        for (int f = 0; f < 2; ++f) {
-                            const int at = 32 * q + e + f;
-                            a[f] = ex2(fmaf(x[e + f] * ld_shared_f32(tab + at * 4), c, nx));
-                            b[f] = a[f] * ld_shared_f32(tab + (kRows + at) * 4) * to;
+                        for (int f = 0; f < 4; ++f) {
+                            a[f] = ex2(fmaf(x[e + f] * __uint_as_float(ks[f]), c, nx));
+                            b[f] = a[f] * __uint_as_float(vs[f]) * to;
                             if (!(m >> (e + f) & 1)) a[f] = b[f] = 0.f;
                         }
-                        l = add2(l, make_float2(a[0], a[1]));
-                        h[e / 2] = DTypeOps<DT_F16>::pack(b[0], b[1]);
+                        l = add2(l, add2(make_float2(a[0], a[1]), make_float2(a[2], a[3])));
+                        h[e / 2] = DTypeOps<DT_F16>::pack(b[0], b[1]), h[e / 2 + 1] = DTypeOps<DT_F16>::pack(b[2], b[3]);
                     }
                     tmem_st_32x32b_x16(s_col + 16u * q, h);
                 }
@@ -543,7 +558,6 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
                                  __float_as_uint(o[e + 3]));
             }
             __syncwarp();
-            // a row at a time to the warp, so that neighbouring lanes store neighbouring channels
             const float sum = l.x + l.y;
             constexpr int C = DP / 32;
             const int first = r - lane;
@@ -560,19 +574,25 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
                     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(d), "r"(part), "r"(DP * 4) : "memory");
                     asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
                 }
-            } else
+            } else {
+                // a row at a time to the warp, so that neighbouring lanes store neighbouring channels
+                const unsigned long long mine_at = reinterpret_cast<unsigned long long>(row_at(p, s.row0, piece.head, r0 + min(r, rows - 1)));
 #pragma unroll 4
-            for (int k = 0; k < 32; ++k) {
-                const float fx = __shfl_sync(0xffffffffu, mine_f.x, k), fy = __shfl_sync(0xffffffffu, mine_f.y, k);
-                if (first + k >= rows) continue;
-                float o[C];
-#pragma unroll
-                for (int e = 0; e < C; ++e) o[e] = ld_shared_f32(sbase + ((first + k) * Lay::kPitch + lane * C + e) * 4);
-                if (lane * C < p.head_dim) {
-                    uint16_t* d = row_at(p, s.row0, piece.head, r0 + first + k) + lane * C;
-#pragma unroll
-                    for (int e = 0; e < C; e += 2)
-                        *reinterpret_cast<uint32_t*>(d + e) = fy != 0.f ? 0u : Ops::pack(o[e] * fx, o[e + 1] * fx);
+                for (int k = 0; k < 32; ++k) {
+                    const float fx = __shfl_sync(0xffffffffu, mine_f.x, k), fy = __shfl_sync(0xffffffffu, mine_f.y, k);
+                    uint16_t* d = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, mine_at, k)) + lane * C;
+                    if (first + k >= rows || lane * C >= p.head_dim) continue;
+                    const uint32_t at = sbase + ((first + k) * Lay::kPitch + lane * C) * 4;
+                    if constexpr (C == 4) {
+                        const uint4 o = ld_shared_v4(at);
+                        uint2 y = make_uint2(Ops::pack(__uint_as_float(o.x) * fx, __uint_as_float(o.y) * fx),
+                                             Ops::pack(__uint_as_float(o.z) * fx, __uint_as_float(o.w) * fx));
+                        if (fy != 0.f) y = make_uint2(0u, 0u);
+                        *reinterpret_cast<uint2*>(d) = y;
+                    } else {
+                        const uint32_t y = Ops::pack(ld_shared_f32(at) * fx, ld_shared_f32(at + 4) * fx);
+                        *reinterpret_cast<uint32_t*>(d) = fy != 0.f ? 0u : y;
+                    }
                 }
             }
         }
