@@ -153,9 +153,16 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
         };
         constexpr int Q = (M + kStride - 1) / kStride;
         uint4 q[Q];
+        // (row of q and head from step to step without a division)
+        const int i_step = kStride / p.group, h_step = kStride - i_step * p.group;
+        int i = (r0 + first) / p.group, h = (r0 + first) - i * p.group;
 #pragma unroll
         for (int u = 0; u < Q; ++u) {
-            const int r = first + u * kStride, i = (r0 + r) / p.group, h = (r0 + r) - i * p.group;
+            const int r = first + u * kStride;
+            if (u > 0) {
+                i += i_step, h += h_step;
+                if (h >= p.group) ++i, h -= p.group;
+            }
             q[u] = make_uint4(0u, 0u, 0u, 0u);
             if (r < rows && 8 * c < p.head_dim)
                 q[u] = ldg_v4(p.q + (long long)(s.row0 + i) * p.q_row + (long long)(piece.head * p.group + h) * p.q_head + 8 * c);
