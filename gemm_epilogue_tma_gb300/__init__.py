@@ -337,8 +337,8 @@ def rms_norm(x, gamma, out=None, eps=1e-6, stream=None):
 class DecoderLayer:
     """The dense part of a decoder layer as a prepared call sequence (fl_layer_*).
 
-    half 0: q, k, v = RMSNorm(x) [Wq; Wk; Wv]^T; the caller's attention then
-    writes attn; half 1: h = attn Wo^T (+ bias_o) + x, out = SwiGLU_FFN(h) + h.
+    half 0: q, k, v = RMSNorm(x) [Wq; Wk; Wv]^T; attention (attention, kv_attend or
+    the caller's) then writes attn; half 1: h = attn Wo^T (+ bias_o) + x, out = SwiGLU_FFN(h) + h.
     Every tensor is fixed for the life of the layer: write new inputs into x
     and attn in place. Capture whole steps with Graph.capture().
     """

@@ -25,9 +25,19 @@
 // of the others and note the first key of each channel where it stood, and the
 // epilogue adds it to the rows that see that key.
 //
+// What bounds it: softmax's 2^x and the two products take as long on a
+// multiprocessor, 1.3 us for a block of both tiles, where the products alone
+// would take 1.1. One causal sequence of 8192 rows, 32 and 8 heads of 128, bf16: 360 us,
+// 1530 TFLOP/s; 16384 rows of 16 heads 655 us, 1680; 4096 rows causal 108 us, 1270. A
+// CTA's start and end (tensor memory, the first loads, the edge blocks, the output)
+// are not hidden, since a multiprocessor holds one: 8 us, so that short
+// sequences fare worse (eight of 512 rows: 43 us, 400 TFLOP/s; five chunks of 330 to
+// 490 rows over 480 to 1930 keys: 55 us, 700). Two tiles to a CTA, not one,
+// so that each block of keys is read for 256 rows.
+//
 // Few rows over many keys: a cluster of up to 8 CTAs takes the same rows, each a run of
 // the blocks, and adds the parts through distributed shared memory, in order, each CTA
-// for its share of the rows.
+// for its share of the rows (one row over 4096 keys 44 -> 17 us, 16 over 30000 291 -> 80).
 //
 // Every mbarrier wait is bounded as in the other kernels.
 #include <algorithm>
@@ -238,118 +248,118 @@ __global__ void __launch_bounds__(kThreads, 1) fl_attention_kernel(const __grid_
     // (all 512 columns: the base is 0)
     // 384 threads are launched with 168 registers: the softmax warps take 216, the others 72 (256 * 216 + 128 * 72 = 384 * 168)
     if (warp >= kWarpMma) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == kWarpTma) {
-        if (lane == 0) {
-            auto load = [&](const CUtensorMap* m, uint32_t dst, uint32_t bar, int h, int row) {
-                mbar_arrive_expect_tx(bar, Lay::kBlock);
-                for (int c = 0; c < CH; ++c) tma_load_3d(dst + c * (kRows * 128), m, bar, 64 * c, h, row);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == kWarpTma) {
+            if (lane == 0) {
+                auto load = [&](const CUtensorMap* m, uint32_t dst, uint32_t bar, int h, int row) {
+                    mbar_arrive_expect_tx(bar, Lay::kBlock);
+                    for (int c = 0; c < CH; ++c) tma_load_3d(dst + c * (kRows * 128), m, bar, 64 * c, h, row);
+                };
+                bool ok = true;
+                int issued = 0;
+                auto next = [&](const CUtensorMap* m, int block) {
+                    const int s = issued % NS;
+                    if (!(ok = wait_here(empty(s), (uint32_t)((issued / NS) & 1) ^ 1u, p.status, p.timeout_ns, 40))) return;
+                    load(m, sbase + Lay::kOffRing + s * Lay::kBlock, mended(issued) ? v_raw(s) : full(s), kv_head, k0 + (j0 + block) * kRows);
+                    ++issued;
+                };
+                if (nb > 0) {
+                    if (n0 > 0) load(&p.tm_q, sbase, q_full(0), head, q0 + row0);
+                    next(&p.tm_k, 0);
+                    if (n1 > 0) load(&p.tm_q, sbase + Lay::kBlock, q_full(1), head, q0 + row0 + kRows);
+                    for (int j = 0; ok && j < nb; ++j) {
+                        next(&p.tm_v, j);
+                        if (ok && j + 1 < nb) next(&p.tm_k, j + 1);
+                    }
+                    // every load this thread issued lands before the CTA may exit
+                    if (n0 > 0) drain_here(q_full(0), 0);
+                    if (n1 > 0) drain_here(q_full(1), 0);
+                    for (int i = issued - 1; i >= 0 && i >= issued - NS; --i)
+                        drain_here(mended(i) ? v_raw(i % NS) : full(i % NS), parity(i));
+                }
+            }
+        } else if (warp == kWarpMma) {
+            const uint32_t qk = umma_idesc_f16(Ops::kFormat, kRows, kRows), pv = umma_idesc_f16(Ops::kFormat, kRows, DP) | kBMajorN;
+            const uint64_t kd = sw128_kmajor_desc(sbase), vd = sw128_mnmajor_desc(sbase, kRows * 128);
+            const uint32_t k_hi = (uint32_t)(kd >> 32), v_hi = (uint32_t)(vd >> 32);
+            auto wait = [&](uint32_t bar, uint32_t parity, int where) {
+                const bool ok = __all_sync(0xffffffffu, wait_here(bar, parity, p.status, p.timeout_ns, where));
+                tc_fence_after();
+                return ok;
+            };
+            auto slot_lo = [&](uint64_t d, int load) { return (uint32_t)d + (uint32_t)((Lay::kOffRing + load % NS * Lay::kBlock) >> 4); };
+            auto scores = [&](int i, int load) {
+#pragma unroll
+                for (int c = 0; c < CH; ++c)
+                    mma4_ss(128u * i, (uint32_t)kd + (uint32_t)((i * Lay::kBlock + c * kRows * 128) >> 4),
+                            slot_lo(kd, load) + (uint32_t)(c * kRows * 128 >> 4), k_hi, qk, c);
+                commit_elected(s_full(i));
             };
             bool ok = true;
-            int issued = 0;
-            auto next = [&](const CUtensorMap* m, int block) {
-                const int s = issued % NS;
-                if (!(ok = wait_here(empty(s), (uint32_t)((issued / NS) & 1) ^ 1u, p.status, p.timeout_ns, 40))) return;
-                load(m, sbase + Lay::kOffRing + s * Lay::kBlock, mended(issued) ? v_raw(s) : full(s), kv_head, k0 + (j0 + block) * kRows);
-                ++issued;
-            };
             if (nb > 0) {
-                if (n0 > 0) load(&p.tm_q, sbase, q_full(0), head, q0 + row0);
-                next(&p.tm_k, 0);
-                if (n1 > 0) load(&p.tm_q, sbase + Lay::kBlock, q_full(1), head, q0 + row0 + kRows);
-                for (int j = 0; ok && j < nb; ++j) {
-                    next(&p.tm_v, j);
-                    if (ok && j + 1 < nb) next(&p.tm_k, j + 1);
+                ok = wait(full(0), 0, 41);
+                for (int i = 0; ok && i < 2; ++i)
+                    if (0 < (i ? n1 : n0) && (ok = wait(q_full(i), 0, 42))) scores(i, 0);
+                if (ok) commit_elected(empty(0));
+            }
+            for (int j = 0; ok && j < nb; ++j) {
+                const int lv = 2 * j + 1, lkey = 2 * j + 2;
+                if (!(ok = wait(mended(lv) ? v_ready(lv % NS) : full(lv % NS), parity(lv), 43))) break;
+                if (j + 1 < nb && !(ok = wait(full(lkey % NS), parity(lkey), 45))) break;
+                for (int i = 0; ok && i < 2; ++i) {
+                    const int n = i ? n1 : n0;
+                    if (j >= n) continue;
+                    if (!(ok = wait(p_full(i), (uint32_t)(j & 1), 46))) break;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        mma4_ts(kOCol + 128u * i, 128u * i + 32u * h, slot_lo(vd, lv) + (uint32_t)(h * 64 * 128 >> 4), v_hi, pv,
+                                (uint32_t)(j + h));
+                    if (j + 1 < n) scores(i, lkey);
+                    else commit_elected(o_full(i));
                 }
-                // every load this thread issued lands before the CTA may exit
-                if (n0 > 0) drain_here(q_full(0), 0);
-                if (n1 > 0) drain_here(q_full(1), 0);
-                for (int i = issued - 1; i >= 0 && i >= issued - NS; --i)
-                    drain_here(mended(i) ? v_raw(i % NS) : full(i % NS), parity(i));
+                if (ok) {
+                    commit_elected(empty(lv % NS));
+                    if (j + 1 < nb) commit_elected(empty(lkey % NS));
+                }
             }
-        }
-    } else if (warp == kWarpMma) {
-        const uint32_t qk = umma_idesc_f16(Ops::kFormat, kRows, kRows), pv = umma_idesc_f16(Ops::kFormat, kRows, DP) | kBMajorN;
-        const uint64_t kd = sw128_kmajor_desc(sbase), vd = sw128_mnmajor_desc(sbase, kRows * 128);
-        const uint32_t k_hi = (uint32_t)(kd >> 32), v_hi = (uint32_t)(vd >> 32);
-        auto wait = [&](uint32_t bar, uint32_t parity, int where) {
-            const bool ok = __all_sync(0xffffffffu, wait_here(bar, parity, p.status, p.timeout_ns, where));
-            tc_fence_after();
-            return ok;
-        };
-        auto slot_lo = [&](uint64_t d, int load) { return (uint32_t)d + (uint32_t)((Lay::kOffRing + load % NS * Lay::kBlock) >> 4); };
-        auto scores = [&](int i, int load) {
-#pragma unroll
-            for (int c = 0; c < CH; ++c)
-                mma4_ss(128u * i, (uint32_t)kd + (uint32_t)((i * Lay::kBlock + c * kRows * 128) >> 4),
-                        slot_lo(kd, load) + (uint32_t)(c * kRows * 128 >> 4), k_hi, qk, c);
-            commit_elected(s_full(i));
-        };
-        bool ok = true;
-        if (nb > 0) {
-            ok = wait(full(0), 0, 41);
-            for (int i = 0; ok && i < 2; ++i)
-                if (0 < (i ? n1 : n0) && (ok = wait(q_full(i), 0, 42))) scores(i, 0);
-            if (ok) commit_elected(empty(0));
-        }
-        for (int j = 0; ok && j < nb; ++j) {
-            const int lv = 2 * j + 1, lkey = 2 * j + 2;
-            if (!(ok = wait(mended(lv) ? v_ready(lv % NS) : full(lv % NS), parity(lv), 43))) break;
-            if (j + 1 < nb && !(ok = wait(full(lkey % NS), parity(lkey), 45))) break;
-            for (int i = 0; ok && i < 2; ++i) {
-                const int n = i ? n1 : n0;
-                if (j >= n) continue;
-                if (!(ok = wait(p_full(i), (uint32_t)(j & 1), 46))) break;
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    mma4_ts(kOCol + 128u * i, 128u * i + 32u * h, slot_lo(vd, lv) + (uint32_t)(h * 64 * 128 >> 4), v_hi, pv,
-                            (uint32_t)(j + h));
-                if (j + 1 < n) scores(i, lkey);
-                else commit_elected(o_full(i));
-            }
-            if (ok) {
-                commit_elected(empty(lv % NS));
-                if (j + 1 < nb) commit_elected(empty(lkey % NS));
-            }
-        }
-        // all MMAs issued by this warp complete before tensor memory is released
-        commit_elected(drain);
-        drain_here(drain, 0);
-    } else {
-        // values of blocks that are not seen whole
-        for (int j = edge; j < nb; ++j) {
-            const int lv = 2 * j + 1, s = lv % NS;
-            if (!__all_sync(0xffffffffu, wait_here(v_raw(s), parity(lv), p.status, p.timeout_ns, 47))) break;
-            const int first_key = (j0 + j) * kRows, valid = min(kRows, lk - first_key);
-            const uint32_t base = sbase + Lay::kOffRing + s * Lay::kBlock;
-            constexpr int U = 8;  // vectors in flight (one at a time a block took 1.7 us longer than its products)
-            for (int c = 0; c < CH; ++c)
-                for (int e = valid * 8 + (int)threadIdx.x - kWarpFix * 32; e < kRows * 8; e += 64)
-                    st_shared_v4(base + c * (kRows * 128) + 16 * e, 0u, 0u, 0u, 0u);
+            // all MMAs issued by this warp complete before tensor memory is released
+            commit_elected(drain);
+            drain_here(drain, 0);
+        } else {
+            // values of blocks that are not seen whole
+            for (int j = edge; j < nb; ++j) {
+                const int lv = 2 * j + 1, s = lv % NS;
+                if (!__all_sync(0xffffffffu, wait_here(v_raw(s), parity(lv), p.status, p.timeout_ns, 47))) break;
+                const int first_key = (j0 + j) * kRows, valid = min(kRows, lk - first_key);
+                const uint32_t base = sbase + Lay::kOffRing + s * Lay::kBlock;
+                constexpr int U = 8;  // vectors in flight (one at a time a block took 1.7 us longer than its products)
+                for (int c = 0; c < CH; ++c)
+                    for (int e = valid * 8 + (int)threadIdx.x - kWarpFix * 32; e < kRows * 8; e += 64)
+                        st_shared_v4(base + c * (kRows * 128) + 16 * e, 0u, 0u, 0u, 0u);
 #pragma unroll 1
-            for (int e0 = threadIdx.x - kWarpFix * 32; e0 < kRows * CH * 8; e0 += 64 * U) {
-                // vector e: 64-channel chunk e / 1024, row e / 8 % 128, 16-byte place e % 8 in its row
-                uint32_t m = 0;
+                for (int e0 = threadIdx.x - kWarpFix * 32; e0 < kRows * CH * 8; e0 += 64 * U) {
+                    // vector e: 64-channel chunk e / 1024, row e / 8 % 128, 16-byte place e % 8 in its row
+                    uint32_t m = 0;
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const uint4 x = ld_shared_v4(base + 16 * (e0 + 64 * u));
-                    if ((e0 + 64 * u) / 8 % kRows < valid) m = absmax2<DT>(m, absmax8<DT>(x));
-                }
-                // (the rare cases in a loop of their own: the instructions of the common one are few and stay cached)
-                if (absmax_halves<DT>(m) < Bits16<DT>::kInf) continue;
+                    for (int u = 0; u < U; ++u) {
+                        const uint4 x = ld_shared_v4(base + 16 * (e0 + 64 * u));
+                        if ((e0 + 64 * u) / 8 % kRows < valid) m = absmax2<DT>(m, absmax8<DT>(x));
+                    }
+                    // (the rare cases in a loop of their own: the instructions of the common one are few and stay cached)
+                    if (absmax_halves<DT>(m) < Bits16<DT>::kInf) continue;
 #pragma unroll 1
-                for (int e = e0; e < e0 + 64 * U; e += 64) {
-                    const int r = e / 8 % kRows;
-                    if (r < valid)
-                        take_out<DT, DP>(base + 16 * e, e / (8 * kRows) * 64 + (((e & 7) ^ (r & 7)) << 3), first_key + r, note);
+                    for (int e = e0; e < e0 + 64 * U; e += 64) {
+                        const int r = e / 8 % kRows;
+                        if (r < valid)
+                            take_out<DT, DP>(base + 16 * e, e / (8 * kRows) * 64 + (((e & 7) ^ (r & 7)) << 3), first_key + r, note);
+                    }
                 }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(v_ready(s));
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(v_ready(s));
+            if (lane == 0) mbar_arrive(fixed);
         }
-        if (lane == 0) mbar_arrive(fixed);
-    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         // ------------------------------------------------------------ softmax: a row per thread

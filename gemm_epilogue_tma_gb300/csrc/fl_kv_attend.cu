@@ -25,9 +25,17 @@
 // are joined in shared memory at the end.
 //
 // Long contexts are split into pieces of L tiles of 128 positions at most. The CTAs
-// are persistent and take every gridDim-th piece. L is the one of sixteen that makes the
-// rounds of CTAs shortest; every CTA finds it, and its pieces, from the lengths, which
-// only the GPU knows. Pieces of a split sequence are joined by a second launch, in order.
+// are persistent and take every gridDim-th piece. L is the one of six that makes the
+// rounds of CTAs shortest (of sixteen: 4 us longer to find, no better); every CTA finds it,
+// and its pieces, from the lengths, which only the GPU knows. Pieces of a split sequence
+// are joined by a second launch, in order.
+//
+// What bounds it, by measurement with 32 and 8 heads of 128, bf16: 64 contexts of 8192
+// positions int8 225 us (4.9 TB/s), e4m3 193 (5.8); without the arithmetic 178, without
+// the loads 210 and 165: for int8 the conversion of codes, whose logical operations are issued at half
+// rate. 16 contexts of 500 to 9600, e4m3 fp16: 36.6 us, of which the longest piece takes 27 and
+// the start of a CTA (lengths, plan, table, first loads) 7 and the second launch 3. 61 of
+// 20 to 300 positions: 14.6 us, 7 of them that start, 5 the longest context, 2 the end.
 #include <algorithm>
 #include <type_traits>
 
@@ -152,400 +160,400 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, QT>::kCtas) fl_kv_attend_
 
     bool ok = true;
     for (uint32_t turn = 0;; ++turn) {
-    Seq s;
-    Piece piece;
-    if (!pieces.find(turn, piece, s)) break;
-    if (piece.seq >= 0) {
-    const int r0 = piece.block * M, rows = min(M, s.n * p.group - r0);  // rows of this block: (row of q, head of the group)
-    const int t0 = (int)((long long)s.tiles * piece.k / piece.pieces), t1 = (int)((long long)s.tiles * (piece.k + 1) / piece.pieces);
-    const int k0 = t0 * kTile, k1 = min(s.keys, t1 * kTile);
-    if (piece.k == 0 && own == 0 && lane == 0) {
-        if (s.from + s.n > (long long)p.table_pages * p.page_size) atomicCAS(p.range, 0, s.row0 + 1);
-        if (piece.pieces > 1)
-            units_of<kResident, M, HD>(p)->unit[piece.units] = Unit{s.row0, s.n, r0, piece.head, piece.pieces, piece.slot, s.blocks * p.heads, 0};
-    }
-
-    // ------------------------------------------------------------ the warp's ring
-    if (!TMA) {
-        // channels past head_dim stay zero
-        for (int i = lane; i < NS * Lay::kStage / 16; i += 32) st_shared_v4(ring + 16 * i, 0u, 0u, 0u, 0u);
-        __syncwarp();
-    }
-    const int steps = k1 > k0 + own * kStep ? (k1 - k0 - own * kStep + stride - 1) / stride : 0;
-    const int* table = p.page_table + piece.seq * p.table_stride;
-    // the table's entry of this lane's position of a step, one step ahead; -2: there is no such position
-    int entry, in_page;
-    auto look_up = [&](int step, int& entry, int& in_page) {
-        const int pos = k0 + own * kStep + step * stride + (lane & 15);
-        entry = -2, in_page = 0;
-        if (step < steps && pos < k1) {
-            const int j = p.page_shift >= 0 ? pos >> p.page_shift : (int)((uint32_t)pos / (uint32_t)p.page_size);
-            in_page = pos - j * p.page_size;
-            entry = __ldg(table + j);
-        }
-    };
-    // lanes 0-15 ask for k, the others for v
-    auto request = [&](int step, int at) {
-        if (step >= steps) return;
-        const uint32_t bar = full(at), dst = ring + at * Lay::kStage + (lane >> 4) * (kStep * HD), m = meta + at * Lay::kMeta;
-        const bool there = entry >= 0 && entry < p.n_pages;
-        if (entry != -2 && !there) atomicCAS(p.range, 0, s.row0 + 1);
-        const uint32_t bits = __ballot_sync(0xffffffffu, there) & 0xffffu;
-        if (lane == 0) {
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(m + 2 * kStep * 4), "r"(bits) : "memory");
-            mbar_arrive_expect_tx(bar, TMA ? Lay::kStage : 0);
-        }
-        if (TMA) {
-            __syncwarp();
-            const int r = lane & 15;
-            if ((r & ((1 << p.box_log) - 1)) == 0) {
-                // (a page that is not there: past the last, zeros)
-                const CUtensorMap* map = &p.tm[lane >> 4];
-                const int page = there ? entry : p.n_pages, row = there ? in_page : 0;
-                tma_load_4d(dst + r * (HD == 64 ? 64 : 128), map, bar, 0, piece.head, row, page);
-                if (HD == 256) tma_load_4d(dst + kStep * 128 + r * 128, map, bar, 128, piece.head, row, page);
+        Seq s;
+        Piece piece;
+        if (!pieces.find(turn, piece, s)) break;
+        if (piece.seq >= 0) {
+            const int r0 = piece.block * M, rows = min(M, s.n * p.group - r0);  // rows of this block: (row of q, head of the group)
+            const int t0 = (int)((long long)s.tiles * piece.k / piece.pieces), t1 = (int)((long long)s.tiles * (piece.k + 1) / piece.pieces);
+            const int k0 = t0 * kTile, k1 = min(s.keys, t1 * kTile);
+            if (piece.k == 0 && own == 0 && lane == 0) {
+                if (s.from + s.n > (long long)p.table_pages * p.page_size) atomicCAS(p.range, 0, s.row0 + 1);
+                if (piece.pieces > 1)
+                    units_of<kResident, M, HD>(p)->unit[piece.units] = Unit{s.row0, s.n, r0, piece.head, piece.pieces, piece.slot, s.blocks * p.heads, 0};
             }
-        } else {
-            const long long from = there ? (((long long)entry * p.page_size + in_page) * p.heads + piece.head) * p.head_dim : 0;
-            const uint8_t* src = (lane < 16 ? p.cache[0] : p.cache[1]) + from;
-            for (int c = 0; c < p.head_dim; c += 8) cp_async8(dst + place<HD>(lane & 15, c / 16) + (c & 8), src + c);
-        }
-        if (there) cp_async4(m + lane * 4, (lane < 16 ? p.scale[0] : p.scale[1]) + ((long long)entry * p.page_size + in_page) * p.heads + piece.head);
-        cp_async_arrive(bar);
-    };
-    // ------------------------------------------------------------ the first loads
-    // (what they depend on, the table's entries, and the rows of q are asked for at once)
-    constexpr int QX = Lay::kQInRegs ? QT : 1;
-    uint4 qx[QX][KS / 2];
-    auto load_q = [&](int qt, uint4* x) {
-        const int r = 8 * qt + g, i = (r0 + r) / p.group, h = (r0 + r) - i * p.group;
-        const uint16_t* q = p.q + (long long)(s.row0 + i) * p.q_row + (long long)(piece.head * p.group + h) * p.q_head + 16 * t;
+
+            // ------------------------------------------------------------ the warp's ring
+            if (!TMA) {
+                // channels past head_dim stay zero
+                for (int i = lane; i < NS * Lay::kStage / 16; i += 32) st_shared_v4(ring + 16 * i, 0u, 0u, 0u, 0u);
+                __syncwarp();
+            }
+            const int steps = k1 > k0 + own * kStep ? (k1 - k0 - own * kStep + stride - 1) / stride : 0;
+            const int* table = p.page_table + piece.seq * p.table_stride;
+            // the table's entry of this lane's position of a step, one step ahead; -2: there is no such position
+            int entry, in_page;
+            auto look_up = [&](int step, int& entry, int& in_page) {
+                const int pos = k0 + own * kStep + step * stride + (lane & 15);
+                entry = -2, in_page = 0;
+                if (step < steps && pos < k1) {
+                    const int j = p.page_shift >= 0 ? pos >> p.page_shift : (int)((uint32_t)pos / (uint32_t)p.page_size);
+                    in_page = pos - j * p.page_size;
+                    entry = __ldg(table + j);
+                }
+            };
+            // lanes 0-15 ask for k, the others for v
+            auto request = [&](int step, int at) {
+                if (step >= steps) return;
+                const uint32_t bar = full(at), dst = ring + at * Lay::kStage + (lane >> 4) * (kStep * HD), m = meta + at * Lay::kMeta;
+                const bool there = entry >= 0 && entry < p.n_pages;
+                if (entry != -2 && !there) atomicCAS(p.range, 0, s.row0 + 1);
+                const uint32_t bits = __ballot_sync(0xffffffffu, there) & 0xffffu;
+                if (lane == 0) {
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(m + 2 * kStep * 4), "r"(bits) : "memory");
+                    mbar_arrive_expect_tx(bar, TMA ? Lay::kStage : 0);
+                }
+                if (TMA) {
+                    __syncwarp();
+                    const int r = lane & 15;
+                    if ((r & ((1 << p.box_log) - 1)) == 0) {
+                        // (a page that is not there: past the last, zeros)
+                        const CUtensorMap* map = &p.tm[lane >> 4];
+                        const int page = there ? entry : p.n_pages, row = there ? in_page : 0;
+                        tma_load_4d(dst + r * (HD == 64 ? 64 : 128), map, bar, 0, piece.head, row, page);
+                        if (HD == 256) tma_load_4d(dst + kStep * 128 + r * 128, map, bar, 128, piece.head, row, page);
+                    }
+                } else {
+                    const long long from = there ? (((long long)entry * p.page_size + in_page) * p.heads + piece.head) * p.head_dim : 0;
+                    const uint8_t* src = (lane < 16 ? p.cache[0] : p.cache[1]) + from;
+                    for (int c = 0; c < p.head_dim; c += 8) cp_async8(dst + place<HD>(lane & 15, c / 16) + (c & 8), src + c);
+                }
+                if (there) cp_async4(m + lane * 4, (lane < 16 ? p.scale[0] : p.scale[1]) + ((long long)entry * p.page_size + in_page) * p.heads + piece.head);
+                cp_async_arrive(bar);
+            };
+            // ------------------------------------------------------------ the first loads
+            // (what they depend on, the table's entries, and the rows of q are asked for at once)
+            constexpr int QX = Lay::kQInRegs ? QT : 1;
+            uint4 qx[QX][KS / 2];
+            auto load_q = [&](int qt, uint4* x) {
+                const int r = 8 * qt + g, i = (r0 + r) / p.group, h = (r0 + r) - i * p.group;
+                const uint16_t* q = p.q + (long long)(s.row0 + i) * p.q_row + (long long)(piece.head * p.group + h) * p.q_head + 16 * t;
 #pragma unroll
-        for (int j = 0; j < KS / 2; ++j) {
-            const int ch = j / 2 * 64 + j % 2 * 8;
-            x[j] = r < rows && ch + 16 * t < p.head_dim ? ldg_v4(q + ch) : make_uint4(0u, 0u, 0u, 0u);
-        }
-    };
-    // (a lane's entries of steps lane / 16 and 2 + lane / 16)
-    int first_entry[2], first_row[2];
-    static_assert(NS == 3 || NS == 4, "two look-ups of two steps");
+                for (int j = 0; j < KS / 2; ++j) {
+                    const int ch = j / 2 * 64 + j % 2 * 8;
+                    x[j] = r < rows && ch + 16 * t < p.head_dim ? ldg_v4(q + ch) : make_uint4(0u, 0u, 0u, 0u);
+                }
+            };
+            // (a lane's entries of steps lane / 16 and 2 + lane / 16)
+            int first_entry[2], first_row[2];
+            static_assert(NS == 3 || NS == 4, "two look-ups of two steps");
 #pragma unroll
-    for (int i = 0; i < 2; ++i) look_up(2 * i + (lane >> 4), first_entry[i], first_row[i]);
-    if constexpr (Lay::kQInRegs) {
+            for (int i = 0; i < 2; ++i) look_up(2 * i + (lane >> 4), first_entry[i], first_row[i]);
+            if constexpr (Lay::kQInRegs) {
 #pragma unroll
-        for (int qt = 0; qt < QT; ++qt) load_q(qt, qx[qt]);
-    }
-    int ahead = stage;
-    auto first = [&](int i) {
-        const int from = 16 * (i & 1) + (lane & 15);
-        entry = __shfl_sync(0xffffffffu, i < 2 ? first_entry[0] : first_entry[1], from);
-        in_page = __shfl_sync(0xffffffffu, i < 2 ? first_row[0] : first_row[1], from);
-    };
+                for (int qt = 0; qt < QT; ++qt) load_q(qt, qx[qt]);
+            }
+            int ahead = stage;
+            auto first = [&](int i) {
+                const int from = 16 * (i & 1) + (lane & 15);
+                entry = __shfl_sync(0xffffffffu, i < 2 ? first_entry[0] : first_entry[1], from);
+                in_page = __shfl_sync(0xffffffffu, i < 2 ? first_row[0] : first_row[1], from);
+            };
 #pragma unroll 1
-    for (int i = 0; i < NS - 1; ++i) {
-        first(i);
-        request(i, ahead);
-        if (++ahead == NS) ahead = 0;
-    }
-    first(NS - 1);
-
-    // ------------------------------------------------------------ q as the first product's B fragments
-    // Step ks = 4 h + w takes channels 64 h + 16 t + 4 w + 0 .. 3 of lane t, in widen_word's order, row g of the tile.
-    // c: what q' . code is multiplied by, for rows 2 t and 2 t + 1 of a tile.
-    uint2 qf[QX][Lay::kQInRegs ? KS : 1];
-    uint2* const qs = reinterpret_cast<uint2*>(smem + Lay::kOffQ);
-    float* const cs = reinterpret_cast<float*>(smem + Lay::kOffC);
-    float c[QT][2];
-    auto q_tile = [&](const uint4* x, auto put) {  // returns the factor of row g
-        float up = 1.f;
-        if (DT == DT_BF16) {
-            // 2^(14 - e) for a largest value of 2^e to 2^(e + 1); rows without a finite, not tiny one stay as they are
-            uint32_t top = 0;
-#pragma unroll
-            for (int j = 0; j < KS / 2; ++j) {
-                const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+            for (int i = 0; i < NS - 1; ++i) {
+                first(i);
+                request(i, ahead);
+                if (++ahead == NS) ahead = 0;
             }
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            const int ex = (int)(max(top, __shfl_xor_sync(0xffffffffu, top, 2)) >> 7);
-            if (ex > 0 && ex < 255) up = __uint_as_float((uint32_t)min(254, 127 + 14 + 127 - ex) << 23);
-        }
-#pragma unroll
-        for (int j = 0; j < KS / 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float2 lo = Ops::unpack(e ? x[j].z : x[j].x), hi = Ops::unpack(e ? x[j].w : x[j].y);
-                const float2 second = kPair<FMT> == 2 ? make_float2(lo.y, hi.y) : hi;
-                put(j / 2 * 4 + j % 2 * 2 + e, make_uint2(DTypeOps<DT_F16>::pack(lo.x * up, (kPair<FMT> == 2 ? hi.x : lo.y) * up),
-                                                          DTypeOps<DT_F16>::pack(second.x * up, second.y * up)));
-            }
-        return fmaxf(p.log2_scale / up, 0x1p-126f);
-    };
-    if constexpr (Lay::kQInRegs) {
-#pragma unroll
-        for (int qt = 0; qt < QT; ++qt) {
-            const float f = q_tile(qx[qt], [&](int ks, uint2 v) { qf[qt][ks] = v; });
-            c[qt][0] = __shfl_sync(0xffffffffu, f, 8 * t), c[qt][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
-        }
-    } else {
-        for (int qt = warp; qt < QT; qt += kWarps) {
-            load_q(qt, qx[0]);
-            const float f = q_tile(qx[0], [&](int ks, uint2 v) { qs[(qt * KS + ks) * 32 + lane] = v; });
-            if (t == 0) cs[8 * qt + g] = f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int qt = 0; qt < QT; ++qt) c[qt][0] = cs[8 * qt + 2 * t], c[qt][1] = cs[8 * qt + 2 * t + 1];
-    }
+            first(NS - 1);
 
-    // ------------------------------------------------------------ the warp's positions
-    // nx, nw: minus the maxima of the exponents x and x + log2 vs; kNoMax where there is
-    // none yet, which any finite exponent exceeds by more than kLazy
-    float nx[QT][2], nw[QT][2], l[QT][2], o[QT][MT][4];
-    uint32_t seen = 0;  // bit 2 qt + f: the row saw a position (which tells it from one whose scores are all -inf)
+            // ------------------------------------------------------------ q as the first product's B fragments
+            // Step ks = 4 h + w takes channels 64 h + 16 t + 4 w + 0 .. 3 of lane t, in widen_word's order, row g of the tile.
+            // c: what q' . code is multiplied by, for rows 2 t and 2 t + 1 of a tile.
+            uint2 qf[QX][Lay::kQInRegs ? KS : 1];
+            uint2* const qs = reinterpret_cast<uint2*>(smem + Lay::kOffQ);
+            float* const cs = reinterpret_cast<float*>(smem + Lay::kOffC);
+            float c[QT][2];
+            auto q_tile = [&](const uint4* x, auto put) {  // returns the factor of row g
+                float up = 1.f;
+                if (DT == DT_BF16) {
+                    // 2^(14 - e) for a largest value of 2^e to 2^(e + 1); rows without a finite, not tiny one stay as they are
+                    uint32_t top = 0;
 #pragma unroll
-    for (int qt = 0; qt < QT; ++qt) {
+                    for (int j = 0; j < KS / 2; ++j) {
+                        const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
 #pragma unroll
-        for (int f = 0; f < 2; ++f) nx[qt][f] = nw[qt][f] = kNoMax, l[qt][f] = 0.f;
+                        for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+                    }
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    const int ex = (int)(max(top, __shfl_xor_sync(0xffffffffu, top, 2)) >> 7);
+                    if (ex > 0 && ex < 255) up = __uint_as_float((uint32_t)min(254, 127 + 14 + 127 - ex) << 23);
+                }
 #pragma unroll
-        for (int j = 0; j < MT; ++j)
+                for (int j = 0; j < KS / 2; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[qt][j][e] = 0.f;
-    }
-
-    for (int step = 0; step < steps; ++step) {
-        __syncwarp();  // (the stage that is asked for next has been read)
-        request(step + NS - 1, ahead);
-        look_up(step + NS, entry, in_page);
-        if (++ahead == NS) ahead = 0;
-        ok = __all_sync(0xffffffffu, wait_bar(full(stage), phase, p.status, p.timeout_ns, 51));
-        if (!ok) break;
-        const uint32_t src = ring + stage * Lay::kStage, sc = meta + stage * Lay::kMeta;
-        if (++stage == NS) stage = 0, phase ^= 1u;
-        const int pos0 = k0 + own * kStep + step * stride;
-
-        // scores x[qt][2 i + f] of position g + 8 i and row 2 t + f of the tile
-        float x[QT][4];
-#pragma unroll
-        for (int qt = 0; qt < QT; ++qt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[qt][e] = 0.f;
-#pragma unroll
-        for (int h = 0; h < KS / 4; ++h) {
-            const uint4 ka = ld_shared_v4(src + place<HD>(g, 4 * h + t)), kb = ld_shared_v4(src + place<HD>(g + 8, 4 * h + t));
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                uint32_t a[4];
-                widen_word<FMT>(w == 0 ? ka.x : w == 1 ? ka.y : w == 2 ? ka.z : ka.w, a[0], a[2]);
-                widen_word<FMT>(w == 0 ? kb.x : w == 1 ? kb.y : w == 2 ? kb.z : kb.w, a[1], a[3]);
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 lo = Ops::unpack(e ? x[j].z : x[j].x), hi = Ops::unpack(e ? x[j].w : x[j].y);
+                        const float2 second = kPair<FMT> == 2 ? make_float2(lo.y, hi.y) : hi;
+                        put(j / 2 * 4 + j % 2 * 2 + e, make_uint2(DTypeOps<DT_F16>::pack(lo.x * up, (kPair<FMT> == 2 ? hi.x : lo.y) * up),
+                                                                  DTypeOps<DT_F16>::pack(second.x * up, second.y * up)));
+                    }
+                return fmaxf(p.log2_scale / up, 0x1p-126f);
+            };
+            if constexpr (Lay::kQInRegs) {
 #pragma unroll
                 for (int qt = 0; qt < QT; ++qt) {
-                    uint2 b;
-                    if constexpr (Lay::kQInRegs) b = qf[qt][4 * h + w];
-                    else b = qs[(qt * KS + 4 * h + w) * 32 + lane];
-                    mma16816(x[qt], a, b.x, b.y);
+                    const float f = q_tile(qx[qt], [&](int ks, uint2 v) { qf[qt][ks] = v; });
+                    c[qt][0] = __shfl_sync(0xffffffffu, f, 8 * t), c[qt][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
                 }
+            } else {
+                for (int qt = warp; qt < QT; qt += kWarps) {
+                    load_q(qt, qx[0]);
+                    const float f = q_tile(qx[0], [&](int ks, uint2 v) { qs[(qt * KS + ks) * 32 + lane] = v; });
+                    if (t == 0) cs[8 * qt + g] = f;
+                }
+                __syncthreads();
+#pragma unroll
+                for (int qt = 0; qt < QT; ++qt) c[qt][0] = cs[8 * qt + 2 * t], c[qt][1] = cs[8 * qt + 2 * t + 1];
             }
-        }
-        // scales of the lane's two positions
-        float ks[2], lv[2];
+
+            // ------------------------------------------------------------ the warp's positions
+            // nx, nw: minus the maxima of the exponents x and x + log2 vs; kNoMax where there is
+            // none yet, which any finite exponent exceeds by more than kLazy
+            float nx[QT][2], nw[QT][2], l[QT][2], o[QT][MT][4];
+            uint32_t seen = 0;  // bit 2 qt + f: the row saw a position (which tells it from one whose scores are all -inf)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) ks[i] = ld_shared_f32(sc + 4 * g + 32 * i), lv[i] = lg2(ld_shared_f32(sc + 64 + 4 * g + 32 * i));
-        const uint32_t bits = __float_as_uint(ld_shared_f32(sc + 2 * kStep * 4));
-        uint32_t hidden = 0;  // bit 4 qt + e: the row does not see the position
-        if (bits != 0xffffu || pos0 + kStep > s.from) {
+            for (int qt = 0; qt < QT; ++qt) {
 #pragma unroll
-            for (int qt = 0; qt < QT; ++qt)
+                for (int f = 0; f < 2; ++f) nx[qt][f] = nw[qt][f] = kNoMax, l[qt][f] = 0.f;
 #pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                    const int r = min(r0 + 8 * qt + 2 * t + f, s.n * p.group - 1);  // (rows past the last: as the last)
-                    const int qi = p.tree == nullptr ? 0 : r / p.group;             // the row of q among the sequence's
+                for (int j = 0; j < MT; ++j)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const long long j = pos0 + g + 8 * i - s.from;
-                        bool sees = bits >> (g + 8 * i) & 1;
-                        if (sees && j >= 0) {
-                            if (p.tree == nullptr) sees = j * p.group <= r;
-                            else sees = j < p.tree_cols && __ldg(p.tree + (s.row0 + qi) * p.tree_stride + j) != 0;
-                        }
-                        if (sees) seen |= 1u << (2 * qt + f);
-                        else hidden |= 1u << (4 * qt + 2 * i + f);
-                    }
-                }
-        } else {
-            seen = (1u << 2 * QT) - 1;
-        }
-        // exponents less the maxima, for the sum of weights and for the weights of the values
-        float a[QT][4], b[QT][4], most = kNone;
-        auto exponents = [&] {
-#pragma unroll
-            for (int qt = 0; qt < QT; ++qt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    a[qt][e] = fmaf(x[qt][e], c[qt][e & 1], nx[qt][e & 1]);
-                    b[qt][e] = fmaf(x[qt][e], c[qt][e & 1], lv[e >> 1] + nw[qt][e & 1]);
-                }
-            if (hidden != 0) {
+                    for (int e = 0; e < 4; ++e) o[qt][j][e] = 0.f;
+            }
+
+            for (int step = 0; step < steps; ++step) {
+                __syncwarp();  // (the stage that is asked for next has been read)
+                request(step + NS - 1, ahead);
+                look_up(step + NS, entry, in_page);
+                if (++ahead == NS) ahead = 0;
+                ok = __all_sync(0xffffffffu, wait_bar(full(stage), phase, p.status, p.timeout_ns, 51));
+                if (!ok) break;
+                const uint32_t src = ring + stage * Lay::kStage, sc = meta + stage * Lay::kMeta;
+                if (++stage == NS) stage = 0, phase ^= 1u;
+                const int pos0 = k0 + own * kStep + step * stride;
+
+                // scores x[qt][2 i + f] of position g + 8 i and row 2 t + f of the tile
+                float x[QT][4];
 #pragma unroll
                 for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (hidden >> (4 * qt + e) & 1) a[qt][e] = b[qt][e] = kNone;
+                    for (int e = 0; e < 4; ++e) x[qt][e] = 0.f;
+#pragma unroll
+                for (int h = 0; h < KS / 4; ++h) {
+                    const uint4 ka = ld_shared_v4(src + place<HD>(g, 4 * h + t)), kb = ld_shared_v4(src + place<HD>(g + 8, 4 * h + t));
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        uint32_t a[4];
+                        widen_word<FMT>(w == 0 ? ka.x : w == 1 ? ka.y : w == 2 ? ka.z : ka.w, a[0], a[2]);
+                        widen_word<FMT>(w == 0 ? kb.x : w == 1 ? kb.y : w == 2 ? kb.z : kb.w, a[1], a[3]);
+#pragma unroll
+                        for (int qt = 0; qt < QT; ++qt) {
+                            uint2 b;
+                            if constexpr (Lay::kQInRegs) b = qf[qt][4 * h + w];
+                            else b = qs[(qt * KS + 4 * h + w) * 32 + lane];
+                            mma16816(x[qt], a, b.x, b.y);
+                        }
+                    }
+                }
+                // scales of the lane's two positions
+                float ks[2], lv[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) ks[i] = ld_shared_f32(sc + 4 * g + 32 * i), lv[i] = lg2(ld_shared_f32(sc + 64 + 4 * g + 32 * i));
+                const uint32_t bits = __float_as_uint(ld_shared_f32(sc + 2 * kStep * 4));
+                uint32_t hidden = 0;  // bit 4 qt + e: the row does not see the position
+                if (bits != 0xffffu || pos0 + kStep > s.from) {
+#pragma unroll
+                    for (int qt = 0; qt < QT; ++qt)
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) {
+                            const int r = min(r0 + 8 * qt + 2 * t + f, s.n * p.group - 1);  // (rows past the last: as the last)
+                            const int qi = p.tree == nullptr ? 0 : r / p.group;             // the row of q among the sequence's
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const long long j = pos0 + g + 8 * i - s.from;
+                                bool sees = bits >> (g + 8 * i) & 1;
+                                if (sees && j >= 0) {
+                                    if (p.tree == nullptr) sees = j * p.group <= r;
+                                    else sees = j < p.tree_cols && __ldg(p.tree + (s.row0 + qi) * p.tree_stride + j) != 0;
+                                }
+                                if (sees) seen |= 1u << (2 * qt + f);
+                                else hidden |= 1u << (4 * qt + 2 * i + f);
+                            }
+                        }
+                } else {
+                    seen = (1u << 2 * QT) - 1;
+                }
+                // exponents less the maxima, for the sum of weights and for the weights of the values
+                float a[QT][4], b[QT][4], most = kNone;
+                auto exponents = [&] {
+#pragma unroll
+                    for (int qt = 0; qt < QT; ++qt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            a[qt][e] = fmaf(x[qt][e], c[qt][e & 1], nx[qt][e & 1]);
+                            b[qt][e] = fmaf(x[qt][e], c[qt][e & 1], lv[e >> 1] + nw[qt][e & 1]);
+                        }
+                    if (hidden != 0) {
+#pragma unroll
+                        for (int qt = 0; qt < QT; ++qt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (hidden >> (4 * qt + e) & 1) a[qt][e] = b[qt][e] = kNone;
+                    }
+                };
+#pragma unroll
+                for (int qt = 0; qt < QT; ++qt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[qt][e] *= ks[e >> 1];
+                exponents();
+#pragma unroll
+                for (int qt = 0; qt < QT; ++qt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) most = fmaxf(most, fmaxf(a[qt][e], b[qt][e]));
+                if (__any_sync(0xffffffffu, most > kLazy)) {
+#pragma unroll
+                    for (int qt = 0; qt < QT; ++qt)
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) {
+                            float ma = kNone, mb = kNone;
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                if (!(hidden >> (4 * qt + 2 * i + f) & 1)) {
+                                    const float y = x[qt][2 * i + f] * c[qt][f];
+                                    ma = fmaxf(ma, y), mb = fmaxf(mb, y + lv[i]);
+                                }
+#pragma unroll
+                            for (int w = 4; w < 32; w <<= 1) {
+                                ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, w));
+                                mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, w));
+                            }
+                            // (a maximum that is there already only grows)
+                            if (nx[qt][f] == kNoMax ? ma > kNone : ma > -nx[qt][f]) {
+                                l[qt][f] *= nx[qt][f] == kNoMax ? 0.f : ex2(-nx[qt][f] - ma);
+                                nx[qt][f] = -ma;
+                            }
+                            if (nw[qt][f] == kNoMax ? mb > kNone : mb > -nw[qt][f]) {
+                                const float y = nw[qt][f] == kNoMax ? 0.f : ex2(-nw[qt][f] - mb);
+#pragma unroll
+                                for (int j = 0; j < MT; ++j) o[qt][j][f] *= y, o[qt][j][2 + f] *= y;
+                                nw[qt][f] = -mb;
+                            }
+                        }
+                    exponents();
+                }
+                // P^T: 16 positions (k) by 8 rows
+                uint2 w[QT];
+#pragma unroll
+                for (int qt = 0; qt < QT; ++qt) {
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) l[qt][f] += ex2(a[qt][f]) + ex2(a[qt][2 + f]);
+                    w[qt].x = movmatrix(DTypeOps<DT_F16>::pack(ex2(b[qt][0]), ex2(b[qt][1])));
+                    w[qt].y = movmatrix(DTypeOps<DT_F16>::pack(ex2(b[qt][2]), ex2(b[qt][3])));
+                }
+                // values: row block j is channels 2 j (rows 0-7) and 2 j + 1 (8-15) of the lane's 4 VW, k positions 2 t, 2 t + 1, + 8
+                uint32_t v[4][VW];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 8 * (i >> 1) + 2 * t + (i & 1);
+                    if constexpr (VW == 2) {
+                        const uint32_t at = src + kStep * HD + place<HD>(r, g >> 1) + 8 * (g & 1);
+                        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[i][0]), "=r"(v[i][1]) : "r"(at) : "memory");
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < VW / 4; ++q) {
+                            const uint4 u = ld_shared_v4(src + kStep * HD + place<HD>(r, g * (VW / 4) + q));
+                            v[i][4 * q] = u.x, v[i][4 * q + 1] = u.y, v[i][4 * q + 2] = u.z, v[i][4 * q + 3] = u.w;
+                        }
+                    }
+                }
+                if (bits != 0xffffu) {
+                    // (what lies behind the last position may hold codes that are not numbers)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (!(bits >> (8 * (i >> 1) + 2 * t + (i & 1)) & 1))
+#pragma unroll
+                            for (int q = 0; q < VW; ++q) v[i][q] = 0u;
+                }
+#pragma unroll
+                for (int j = 0; j < MT; ++j) {
+                    uint32_t va[4];
+                    va[0] = widen_pair<FMT>(v[0][j / 2], v[1][j / 2], j % 2 * 2), va[1] = widen_pair<FMT>(v[0][j / 2], v[1][j / 2], j % 2 * 2 + 1);
+                    va[2] = widen_pair<FMT>(v[2][j / 2], v[3][j / 2], j % 2 * 2), va[3] = widen_pair<FMT>(v[2][j / 2], v[3][j / 2], j % 2 * 2 + 1);
+#pragma unroll
+                    for (int qt = 0; qt < QT; ++qt) mma16816(o[qt][j], va, w[qt].x, w[qt].y);
+                }
             }
-        };
+            if (!ok)  // a wait ran out: every load that was asked for lands before the CTA exits
+                for (int i = 0; i < NS; ++i) wait_bar_drain(full(i), (uint32_t)(i >= stage ? phase : phase ^ 1u), 20000000ull);
+            if constexpr (!Lay::kQInRegs) __syncthreads();  // (the rings of all warps have been read)
 #pragma unroll
-        for (int qt = 0; qt < QT; ++qt)
+            for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[qt][e] *= ks[e >> 1];
-        exponents();
+                for (int f = 0; f < 2; ++f)
 #pragma unroll
-        for (int qt = 0; qt < QT; ++qt)
+                    for (int w = 4; w < 32; w <<= 1) l[qt][f] += __shfl_xor_sync(0xffffffffu, l[qt][f], w);
+            // (seen: the same rows in lanes of the same t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) most = fmaxf(most, fmaxf(a[qt][e], b[qt][e]));
-        if (__any_sync(0xffffffffu, most > kLazy)) {
+            for (int w = 4; w < 32; w <<= 1) seen |= __shfl_xor_sync(0xffffffffu, seen, w);
+
+            // ------------------------------------------------------------ the CTA's warps joined
+            constexpr int P = HD + 4;  // pitch of a row of sums
+            auto sums = [&](int w, int r) { return reinterpret_cast<float*>(smem + w * Lay::kArea) + r * P; };
+            auto stat = [&](int w, int r) { return reinterpret_cast<float4*>(smem + w * Lay::kArea + Lay::kSums) + r; };
+            __syncwarp();
 #pragma unroll
             for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
                 for (int f = 0; f < 2; ++f) {
-                    float ma = kNone, mb = kNone;
+                    const int r = 8 * qt + 2 * t + f;
+                    float* d = sums(warp, r) + g * (4 * VW);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (!(hidden >> (4 * qt + 2 * i + f) & 1)) {
-                            const float y = x[qt][2 * i + f] * c[qt][f];
-                            ma = fmaxf(ma, y), mb = fmaxf(mb, y + lv[i]);
-                        }
-#pragma unroll
-                    for (int w = 4; w < 32; w <<= 1) {
-                        ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, w));
-                        mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, w));
-                    }
-                    // (a maximum that is there already only grows)
-                    if (nx[qt][f] == kNoMax ? ma > kNone : ma > -nx[qt][f]) {
-                        l[qt][f] *= nx[qt][f] == kNoMax ? 0.f : ex2(-nx[qt][f] - ma);
-                        nx[qt][f] = -ma;
-                    }
-                    if (nw[qt][f] == kNoMax ? mb > kNone : mb > -nw[qt][f]) {
-                        const float y = nw[qt][f] == kNoMax ? 0.f : ex2(-nw[qt][f] - mb);
-#pragma unroll
-                        for (int j = 0; j < MT; ++j) o[qt][j][f] *= y, o[qt][j][2 + f] *= y;
-                        nw[qt][f] = -mb;
-                    }
+                    for (int j = 0; j < MT; ++j) *reinterpret_cast<float2*>(d + 2 * j) = make_float2(o[qt][j][f], o[qt][j][2 + f]);
+                    if (g == 0)  // (this warp's part)
+                        *stat(warp, r) =
+                            make_float4(nx[qt][f] == kNoMax ? kNone : -nx[qt][f], nw[qt][f] == kNoMax ? kNone : -nw[qt][f], l[qt][f],
+                                        seen >> (2 * qt + f) & 1 ? 1.f : 0.f);
                 }
-            exponents();
-        }
-        // P^T: 16 positions (k) by 8 rows
-        uint2 w[QT];
-#pragma unroll
-        for (int qt = 0; qt < QT; ++qt) {
-#pragma unroll
-            for (int f = 0; f < 2; ++f) l[qt][f] += ex2(a[qt][f]) + ex2(a[qt][2 + f]);
-            w[qt].x = movmatrix(DTypeOps<DT_F16>::pack(ex2(b[qt][0]), ex2(b[qt][1])));
-            w[qt].y = movmatrix(DTypeOps<DT_F16>::pack(ex2(b[qt][2]), ex2(b[qt][3])));
-        }
-        // values: row block j is channels 2 j (rows 0-7) and 2 j + 1 (8-15) of the lane's 4 VW, k positions 2 t, 2 t + 1, + 8
-        uint32_t v[4][VW];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 8 * (i >> 1) + 2 * t + (i & 1);
-            if constexpr (VW == 2) {
-                const uint32_t at = src + kStep * HD + place<HD>(r, g >> 1) + 8 * (g & 1);
-                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[i][0]), "=r"(v[i][1]) : "r"(at) : "memory");
-            } else {
-#pragma unroll
-                for (int q = 0; q < VW / 4; ++q) {
-                    const uint4 u = ld_shared_v4(src + kStep * HD + place<HD>(r, g * (VW / 4) + q));
-                    v[i][4 * q] = u.x, v[i][4 * q + 1] = u.y, v[i][4 * q + 2] = u.z, v[i][4 * q + 3] = u.w;
+            group_sync();
+            const bool whole = piece.pieces == 1;
+            for (int i = own * 32 + lane; i < rows * (HD / 4); i += 32 * W) {
+                const int r = i / (HD / 4), ch = i % (HD / 4) * 4;
+                float ma = kNone, mb = kNone, any = 0.f;
+#pragma unroll 4
+                for (int w = group * W; w < group * W + W; ++w) {
+                    const float4 st = *stat(w, r);
+                    ma = fmaxf(ma, st.x), mb = fmaxf(mb, st.y), any = fmaxf(any, st.w);
+                }
+                const float na = ma == kNone ? 0.f : -ma, nb = mb == kNone ? 0.f : -mb;
+                float sum = 0.f;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                for (int w = group * W; w < group * W + W; ++w) {
+                    const float4 st = *stat(w, r);
+                    sum += st.z * ex2(st.x + na);
+                    const float f = ex2(st.y + nb);
+                    const float4 d = *reinterpret_cast<const float4*>(sums(w, r) + ch);
+                    v.x = fmaf(d.x, f, v.x), v.y = fmaf(d.y, f, v.y), v.z = fmaf(d.z, f, v.z), v.w = fmaf(d.w, f, v.w);
+                }
+                if (whole) {
+                    if (ch < p.head_dim) {
+                        const float2 f = finish(ma, mb, sum, any);
+                        uint2 y = make_uint2(0u, 0u);
+                        if (f.y == 0.f) y = make_uint2(Ops::pack(v.x * f.x, v.y * f.x), Ops::pack(v.z * f.x, v.w * f.x));
+                        *reinterpret_cast<uint2*>(row_at(p, s.row0, piece.head, r0 + r) + ch) = y;
+                    }
+                } else {
+                    *reinterpret_cast<float4*>(p.part + ((long long)piece.slot * M + r) * HD + ch) = v;
+                    if (ch == 0)
+                        *reinterpret_cast<float4*>(p.part + (long long)slots(kResident) * M * HD + ((long long)piece.slot * M + r) * 4) =
+                            make_float4(ma, mb, sum, any);
                 }
             }
         }
-        if (bits != 0xffffu) {
-            // (what lies behind the last position may hold codes that are not numbers)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (!(bits >> (8 * (i >> 1) + 2 * t + (i & 1)) & 1))
-#pragma unroll
-                    for (int q = 0; q < VW; ++q) v[i][q] = 0u;
-        }
-#pragma unroll
-        for (int j = 0; j < MT; ++j) {
-            uint32_t va[4];
-            va[0] = widen_pair<FMT>(v[0][j / 2], v[1][j / 2], j % 2 * 2), va[1] = widen_pair<FMT>(v[0][j / 2], v[1][j / 2], j % 2 * 2 + 1);
-            va[2] = widen_pair<FMT>(v[2][j / 2], v[3][j / 2], j % 2 * 2), va[3] = widen_pair<FMT>(v[2][j / 2], v[3][j / 2], j % 2 * 2 + 1);
-#pragma unroll
-            for (int qt = 0; qt < QT; ++qt) mma16816(o[qt][j], va, w[qt].x, w[qt].y);
-        }
-    }
-    if (!ok)  // a wait ran out: every load that was asked for lands before the CTA exits
-        for (int i = 0; i < NS; ++i) wait_bar_drain(full(i), (uint32_t)(i >= stage ? phase : phase ^ 1u), 20000000ull);
-    if constexpr (!Lay::kQInRegs) __syncthreads();  // (the rings of all warps have been read)
-#pragma unroll
-    for (int qt = 0; qt < QT; ++qt)
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
-#pragma unroll
-            for (int w = 4; w < 32; w <<= 1) l[qt][f] += __shfl_xor_sync(0xffffffffu, l[qt][f], w);
-    // (seen: the same rows in lanes of the same t)
-#pragma unroll
-    for (int w = 4; w < 32; w <<= 1) seen |= __shfl_xor_sync(0xffffffffu, seen, w);
-
-    // ------------------------------------------------------------ the CTA's warps joined
-    constexpr int P = HD + 4;  // pitch of a row of sums
-    auto sums = [&](int w, int r) { return reinterpret_cast<float*>(smem + w * Lay::kArea) + r * P; };
-    auto stat = [&](int w, int r) { return reinterpret_cast<float4*>(smem + w * Lay::kArea + Lay::kSums) + r; };
-    __syncwarp();
-#pragma unroll
-    for (int qt = 0; qt < QT; ++qt)
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-            const int r = 8 * qt + 2 * t + f;
-            float* d = sums(warp, r) + g * (4 * VW);
-#pragma unroll
-            for (int j = 0; j < MT; ++j) *reinterpret_cast<float2*>(d + 2 * j) = make_float2(o[qt][j][f], o[qt][j][2 + f]);
-            if (g == 0)  // (this warp's part)
-                *stat(warp, r) =
-                    make_float4(nx[qt][f] == kNoMax ? kNone : -nx[qt][f], nw[qt][f] == kNoMax ? kNone : -nw[qt][f], l[qt][f],
-                                seen >> (2 * qt + f) & 1 ? 1.f : 0.f);
-        }
-    group_sync();
-    const bool whole = piece.pieces == 1;
-    for (int i = own * 32 + lane; i < rows * (HD / 4); i += 32 * W) {
-        const int r = i / (HD / 4), ch = i % (HD / 4) * 4;
-        float ma = kNone, mb = kNone, any = 0.f;
-#pragma unroll 4
-        for (int w = group * W; w < group * W + W; ++w) {
-            const float4 st = *stat(w, r);
-            ma = fmaxf(ma, st.x), mb = fmaxf(mb, st.y), any = fmaxf(any, st.w);
-        }
-        const float na = ma == kNone ? 0.f : -ma, nb = mb == kNone ? 0.f : -mb;
-        float sum = 0.f;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int w = group * W; w < group * W + W; ++w) {
-            const float4 st = *stat(w, r);
-            sum += st.z * ex2(st.x + na);
-            const float f = ex2(st.y + nb);
-            const float4 d = *reinterpret_cast<const float4*>(sums(w, r) + ch);
-            v.x = fmaf(d.x, f, v.x), v.y = fmaf(d.y, f, v.y), v.z = fmaf(d.z, f, v.z), v.w = fmaf(d.w, f, v.w);
-        }
-        if (whole) {
-            if (ch < p.head_dim) {
-                const float2 f = finish(ma, mb, sum, any);
-                uint2 y = make_uint2(0u, 0u);
-                if (f.y == 0.f) y = make_uint2(Ops::pack(v.x * f.x, v.y * f.x), Ops::pack(v.z * f.x, v.w * f.x));
-                *reinterpret_cast<uint2*>(row_at(p, s.row0, piece.head, r0 + r) + ch) = y;
-            }
-        } else {
-            *reinterpret_cast<float4*>(p.part + ((long long)piece.slot * M + r) * HD + ch) = v;
-            if (ch == 0)
-                *reinterpret_cast<float4*>(p.part + (long long)slots(kResident) * M * HD + ((long long)piece.slot * M + r) * 4) =
-                    make_float4(ma, mb, sum, any);
-        }
-    }
-    }
-    // the sums have been read before the next round's loads overwrite them
-    fence_proxy_async_smem();
-    if (!__syncthreads_and(ok)) break;
+        // the sums have been read before the next round's loads overwrite them
+        fence_proxy_async_smem();
+        if (!__syncthreads_and(ok)) break;
     }
 }
 

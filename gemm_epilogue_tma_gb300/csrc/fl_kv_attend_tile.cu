@@ -9,7 +9,11 @@
 // are, six warps write them out as the 16-bit operands' swizzled blocks, and the
 // scales go onto the scores and the weights as before, two per position. The
 // warp-level kernel widens them again for every 32 rows: trees of 48 rows for a group of four
-// heads, four contexts of 5700 positions, 146 us there.
+// heads over contexts of 1000 to 10600 positions, 23000 in all, 146 us there, 62 here.
+//
+// What bounds it: of those 62 us the start of a CTA (lengths and plan 4, rows of q 4)
+// takes 10, its 9 to 11 blocks 2.8 to 3 each (of which 1.8 are the softmax of a tile and 0.9 the
+// products and the barriers between, the other tile's the same), the end 3, the second launch 8.
 //
 // Roles: warps 0-7 softmax, one tile to four of them, a row to a thread; warp 8 the
 // MMAs, warp 9 the loads, 10-15 widen. Blocks of 128 positions of k and v take
@@ -198,155 +202,155 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
     // (all 512 columns of tensor memory: the base is 0)
     // 512 threads are launched with 128 registers: the softmax warps take 176, the others 80 (256 * 176 + 256 * 80 = 512 * 128)
     if (warp >= kWarpMma) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    if (warp == kWarpMma) {
-        const uint32_t qk = umma_idesc_f16(0, kRows, kRows), wv = umma_idesc_f16(0, kRows, DP) | kBMajorN;
-        const uint64_t kd = sw128_kmajor_desc(sbase), vd = sw128_mnmajor_desc(sbase, kRows * 128);
-        const uint32_t k_hi = (uint32_t)(kd >> 32), v_hi = (uint32_t)(vd >> 32);
-        auto wait = [&](uint32_t bar, uint32_t parity, int where) {
-            const bool ok = __all_sync(0xffffffffu, wait_here(bar, parity, p.status, p.timeout_ns, where));
-            tc_fence_after();
-            return ok;
-        };
-        auto slot_lo = [&](uint64_t d, int x) { return (uint32_t)d + (uint32_t)((Lay::kOffRing + x % kRing * Lay::kBlock) >> 4); };
-        auto scores = [&](int i, int x) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (warp == kWarpMma) {
+            const uint32_t qk = umma_idesc_f16(0, kRows, kRows), wv = umma_idesc_f16(0, kRows, DP) | kBMajorN;
+            const uint64_t kd = sw128_kmajor_desc(sbase), vd = sw128_mnmajor_desc(sbase, kRows * 128);
+            const uint32_t k_hi = (uint32_t)(kd >> 32), v_hi = (uint32_t)(vd >> 32);
+            auto wait = [&](uint32_t bar, uint32_t parity, int where) {
+                const bool ok = __all_sync(0xffffffffu, wait_here(bar, parity, p.status, p.timeout_ns, where));
+                tc_fence_after();
+                return ok;
+            };
+            auto slot_lo = [&](uint64_t d, int x) { return (uint32_t)d + (uint32_t)((Lay::kOffRing + x % kRing * Lay::kBlock) >> 4); };
+            auto scores = [&](int i, int x) {
 #pragma unroll
-            for (int c = 0; c < CH; ++c)
-                mma4_ss(128u * i, (uint32_t)kd + (uint32_t)((i * Lay::kBlock + c * kRows * 128) >> 4),
-                        slot_lo(kd, x) + (uint32_t)(c * kRows * 128 >> 4), k_hi, qk, c);
-            commit_elected(s_full(i));
-        };
-        bool ok = true;
-        if (nb > 0) {
-            ok = wait(q_full, 0, 60) && wait(full(0), 0, 61);
-            for (int i = 0; ok && i < TILES; ++i)
-                if (0 < (i ? n1 : n0)) scores(i, 0);
-            if (ok) commit_elected(empty(0));
-        }
-        for (int j = 0; ok && j < nb; ++j) {
-            const int xv = 2 * j + 1, xk = 2 * j + 2;
-            if (!(ok = wait(full(xv), round(xv), 62))) break;
-            if (j + 1 < nb && !(ok = wait(full(xk), round(xk), 63))) break;
-            for (int i = 0; ok && i < TILES; ++i) {
-                if (j >= (i ? n1 : n0)) continue;
-                if (!(ok = wait(p_full(i), (uint32_t)(j & 1), 64))) break;
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    mma4_ts(kOCol + 128u * i, 128u * i + 32u * h, slot_lo(vd, xv) + (uint32_t)(h * 64 * 128 >> 4), v_hi, wv, (uint32_t)(j + h));
-                if (j + 1 < nb) scores(i, xk);
-                else commit_elected(o_full(i));
+                for (int c = 0; c < CH; ++c)
+                    mma4_ss(128u * i, (uint32_t)kd + (uint32_t)((i * Lay::kBlock + c * kRows * 128) >> 4),
+                            slot_lo(kd, x) + (uint32_t)(c * kRows * 128 >> 4), k_hi, qk, c);
+                commit_elected(s_full(i));
+            };
+            bool ok = true;
+            if (nb > 0) {
+                ok = wait(q_full, 0, 60) && wait(full(0), 0, 61);
+                for (int i = 0; ok && i < TILES; ++i)
+                    if (0 < (i ? n1 : n0)) scores(i, 0);
+                if (ok) commit_elected(empty(0));
             }
-            if (ok) {
-                commit_elected(empty(xv));
-                if (j + 1 < nb) commit_elected(empty(xk));
-            }
-        }
-        // all MMAs issued by this warp complete before tensor memory is released
-        commit_elected(drain);
-        drain_here(drain, 0);
-    } else if (warp == kWarpTma) {
-        // positions lane + 32 u of a block: their table entries (one block ahead), boxes and scales
-        const int* table = p.page_table + piece.seq * p.table_stride;
-        int entry[4], row[4], next[4], next_row[4];
-        auto look_up = [&](int j, int* e, int* in_page) {
+            for (int j = 0; ok && j < nb; ++j) {
+                const int xv = 2 * j + 1, xk = 2 * j + 2;
+                if (!(ok = wait(full(xv), round(xv), 62))) break;
+                if (j + 1 < nb && !(ok = wait(full(xk), round(xk), 63))) break;
+                for (int i = 0; ok && i < TILES; ++i) {
+                    if (j >= (i ? n1 : n0)) continue;
+                    if (!(ok = wait(p_full(i), (uint32_t)(j & 1), 64))) break;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int pos = k0 + j * kRows + 32 * u + lane;
-                e[u] = -2, in_page[u] = 0;
-                if (j < nb && pos < k1) {
-                    const int page = p.page_shift >= 0 ? pos >> p.page_shift : (int)((uint32_t)pos / (uint32_t)p.page_size);
-                    in_page[u] = pos - page * p.page_size;
-                    e[u] = __ldg(table + page);
+                    for (int h = 0; h < 2; ++h)
+                        mma4_ts(kOCol + 128u * i, 128u * i + 32u * h, slot_lo(vd, xv) + (uint32_t)(h * 64 * 128 >> 4), v_hi, wv, (uint32_t)(j + h));
+                    if (j + 1 < nb) scores(i, xk);
+                    else commit_elected(o_full(i));
+                }
+                if (ok) {
+                    commit_elected(empty(xv));
+                    if (j + 1 < nb) commit_elected(empty(xk));
                 }
             }
-        };
-        look_up(0, next, next_row);
-        bool ok = true;
-        int issued = 0;
-        for (int x = 0; ok && x < 2 * nb; ++x) {
-            const int j = x >> 1;
-            if ((x & 1) == 0) {
+            // all MMAs issued by this warp complete before tensor memory is released
+            commit_elected(drain);
+            drain_here(drain, 0);
+        } else if (warp == kWarpTma) {
+            // positions lane + 32 u of a block: their table entries (one block ahead), boxes and scales
+            const int* table = p.page_table + piece.seq * p.table_stride;
+            int entry[4], row[4], next[4], next_row[4];
+            auto look_up = [&](int j, int* e, int* in_page) {
 #pragma unroll
-                for (int u = 0; u < 4; ++u) entry[u] = next[u], row[u] = next_row[u];
-                look_up(j + 1, next, next_row);
-            }
-            if (!(ok = __all_sync(0xffffffffu, wait_here(raw_empty(x), round(x) ^ 1u, p.status, p.timeout_ns, 65)))) break;
-            const uint32_t dst = sbase + Lay::kOffRaw + x % kRing * Lay::kCodes, tab = sbase + Lay::kOffTab + j % kTabs * (3 * kRows * 4);
-            if (lane == 0) mbar_arrive_expect_tx(raw_full(x), Lay::kCodes);
-            __syncwarp();
-            const CUtensorMap* map = &p.tm[x & 1];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const bool there = entry[u] >= 0 && entry[u] < p.n_pages;
-                const int at = 32 * u + lane;
-                // (a page that is not there: past the last, zeros)
-                if ((at & ((1 << p.box_log) - 1)) == 0)
-                    tma_load_4d(dst + at * DP, map, raw_full(x), 0, piece.head, there ? row[u] : 0, there ? entry[u] : p.n_pages);
+                for (int u = 0; u < 4; ++u) {
+                    const int pos = k0 + j * kRows + 32 * u + lane;
+                    e[u] = -2, in_page[u] = 0;
+                    if (j < nb && pos < k1) {
+                        const int page = p.page_shift >= 0 ? pos >> p.page_shift : (int)((uint32_t)pos / (uint32_t)p.page_size);
+                        in_page[u] = pos - page * p.page_size;
+                        e[u] = __ldg(table + page);
+                    }
+                }
+            };
+            look_up(0, next, next_row);
+            bool ok = true;
+            int issued = 0;
+            for (int x = 0; ok && x < 2 * nb; ++x) {
+                const int j = x >> 1;
                 if ((x & 1) == 0) {
-                    if (entry[u] != -2 && !there) atomicCAS(p.range, 0, s.row0 + 1);
-                    const uint32_t bits = __ballot_sync(0xffffffffu, there);
-                    if (lane == 0)
-                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(sbase + Lay::kOffBits + j % kTabs * 16 + 4 * u), "r"(bits) : "memory");
-                    if (there) {
-                        const long long from = ((long long)entry[u] * p.page_size + row[u]) * p.heads + piece.head;
-                        cp_async4(tab + at * 4, p.scale[0] + from);
-                        cp_async4(tab + (kRows + at) * 4, p.scale[1] + from);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) entry[u] = next[u], row[u] = next_row[u];
+                    look_up(j + 1, next, next_row);
+                }
+                if (!(ok = __all_sync(0xffffffffu, wait_here(raw_empty(x), round(x) ^ 1u, p.status, p.timeout_ns, 65)))) break;
+                const uint32_t dst = sbase + Lay::kOffRaw + x % kRing * Lay::kCodes, tab = sbase + Lay::kOffTab + j % kTabs * (3 * kRows * 4);
+                if (lane == 0) mbar_arrive_expect_tx(raw_full(x), Lay::kCodes);
+                __syncwarp();
+                const CUtensorMap* map = &p.tm[x & 1];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const bool there = entry[u] >= 0 && entry[u] < p.n_pages;
+                    const int at = 32 * u + lane;
+                    // (a page that is not there: past the last, zeros)
+                    if ((at & ((1 << p.box_log) - 1)) == 0)
+                        tma_load_4d(dst + at * DP, map, raw_full(x), 0, piece.head, there ? row[u] : 0, there ? entry[u] : p.n_pages);
+                    if ((x & 1) == 0) {
+                        if (entry[u] != -2 && !there) atomicCAS(p.range, 0, s.row0 + 1);
+                        const uint32_t bits = __ballot_sync(0xffffffffu, there);
+                        if (lane == 0)
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(sbase + Lay::kOffBits + j % kTabs * 16 + 4 * u), "r"(bits) : "memory");
+                        if (there) {
+                            const long long from = ((long long)entry[u] * p.page_size + row[u]) * p.heads + piece.head;
+                            cp_async4(tab + at * 4, p.scale[0] + from);
+                            cp_async4(tab + (kRows + at) * 4, p.scale[1] + from);
+                        }
                     }
                 }
+                __syncwarp();
+                cp_async_arrive(raw_full(x));
+                ++issued;
             }
-            __syncwarp();
-            cp_async_arrive(raw_full(x));
-            ++issued;
-        }
-        // every load of this warp lands before the CTA may exit
-        for (int x = issued - 1; x >= 0 && x >= issued - kRing; --x) drain_here(raw_full(x), round(x));
-    } else {
-        const int tid = (int)threadIdx.x - kWarpWiden * 32;
-        bool ok = true;
-        for (int x = 0; ok && x < 2 * nb; ++x) {
-            const int j = x >> 1;
-            ok = wait_here(raw_full(x), round(x), p.status, p.timeout_ns, 66) && wait_here(empty(x), round(x) ^ 1u, p.status, p.timeout_ns, 67);
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            const uint32_t src = sbase + Lay::kOffRaw + x % kRing * Lay::kCodes, dst = sbase + Lay::kOffRing + x % kRing * Lay::kBlock;
-            float* const tab = tabs + j % kTabs * (3 * kRows);
-            if ((x & 1) == 0 && tid < kRows) tab[2 * kRows + tid] = lg2(tab[kRows + tid]);
-            const uint4 bits = ld_shared_v4(sbase + Lay::kOffBits + j % kTabs * 16);
-            const bool gaps = (bits.x & bits.y & bits.z & bits.w) != 0xffffffffu;
-            constexpr int V = kRows * DP / 16, U = (V + 32 * kWiden - 1) / (32 * kWiden);  // vectors of 16 codes, in flight
+            // every load of this warp lands before the CTA may exit
+            for (int x = issued - 1; x >= 0 && x >= issued - kRing; --x) drain_here(raw_full(x), round(x));
+        } else {
+            const int tid = (int)threadIdx.x - kWarpWiden * 32;
+            bool ok = true;
+            for (int x = 0; ok && x < 2 * nb; ++x) {
+                const int j = x >> 1;
+                ok = wait_here(raw_full(x), round(x), p.status, p.timeout_ns, 66) && wait_here(empty(x), round(x) ^ 1u, p.status, p.timeout_ns, 67);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                const uint32_t src = sbase + Lay::kOffRaw + x % kRing * Lay::kCodes, dst = sbase + Lay::kOffRing + x % kRing * Lay::kBlock;
+                float* const tab = tabs + j % kTabs * (3 * kRows);
+                if ((x & 1) == 0 && tid < kRows) tab[2 * kRows + tid] = lg2(tab[kRows + tid]);
+                const uint4 bits = ld_shared_v4(sbase + Lay::kOffBits + j % kTabs * 16);
+                const bool gaps = (bits.x & bits.y & bits.z & bits.w) != 0xffffffffu;
+                constexpr int V = kRows * DP / 16, U = (V + 32 * kWiden - 1) / (32 * kWiden);  // vectors of 16 codes, in flight
 #pragma unroll 1
-            for (int e0 = tid; e0 < V; e0 += 32 * kWiden * U) {
-                uint4 v[U];
+                for (int e0 = tid; e0 < V; e0 += 32 * kWiden * U) {
+                    uint4 v[U];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int e = e0 + 32 * kWiden * u;
-                    if (e < V) v[u] = ld_shared_v4(src + 16 * e);
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int e = e0 + 32 * kWiden * u, r = e / (DP / 16), c = e % (DP / 16);
-                    if (e >= V) continue;
-                    if ((x & 1) && gaps) {
-                        // (a value that is not there may be none, and would not vanish times zero)
-                        const uint32_t word = r < 64 ? (r < 32 ? bits.x : bits.y) : (r < 96 ? bits.z : bits.w);
-                        if (!(word >> (r & 31) & 1)) v[u] = make_uint4(0u, 0u, 0u, 0u);
+                    for (int u = 0; u < U; ++u) {
+                        const int e = e0 + 32 * kWiden * u;
+                        if (e < V) v[u] = ld_shared_v4(src + 16 * e);
                     }
-                    uint32_t o[8];
-                    widen16<FMT>(v[u], o);
-                    const uint32_t at = dst + (c >> 2) * (kRows * 128) + r * 128;
-                    const uint32_t k = (uint32_t)(2 * (c & 3)) ^ (r & 7);
-                    st_shared_v4(at + (k << 4), o[0], o[1], o[2], o[3]);
-                    st_shared_v4(at + ((k ^ 1u) << 4), o[4], o[5], o[6], o[7]);
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int e = e0 + 32 * kWiden * u, r = e / (DP / 16), c = e % (DP / 16);
+                        if (e >= V) continue;
+                        if ((x & 1) && gaps) {
+                            // (a value that is not there may be none, and would not vanish times zero)
+                            const uint32_t word = r < 64 ? (r < 32 ? bits.x : bits.y) : (r < 96 ? bits.z : bits.w);
+                            if (!(word >> (r & 31) & 1)) v[u] = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        uint32_t o[8];
+                        widen16<FMT>(v[u], o);
+                        const uint32_t at = dst + (c >> 2) * (kRows * 128) + r * 128;
+                        const uint32_t k = (uint32_t)(2 * (c & 3)) ^ (r & 7);
+                        st_shared_v4(at + (k << 4), o[0], o[1], o[2], o[3]);
+                        st_shared_v4(at + ((k ^ 1u) << 4), o[4], o[5], o[6], o[7]);
+                    }
                 }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                if ((x & 1) == 0) mbar_arrive(tab_full(j));
-                mbar_arrive(full(x));
-                mbar_arrive(raw_empty(x));
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if ((x & 1) == 0) mbar_arrive(tab_full(j));
+                    mbar_arrive(full(x));
+                    mbar_arrive(raw_empty(x));
+                }
             }
         }
-    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         // ------------------------------------------------------------ softmax: a row per thread

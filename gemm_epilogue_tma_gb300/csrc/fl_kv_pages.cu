@@ -17,7 +17,9 @@
 //   3. the k-th free page is written to place k of a list, k below the wanted number
 //   4. the k-th wanting entry takes page k of the list
 // with a barrier after each. Nothing but latency bounds it: the barriers, and the rounds of
-// loads of a warp's run, eight loads to a round.
+// loads of a warp's run, eight loads to a round. Graph times: two calls for seven sequences
+// of 16 entries 6.9 us, for 256 of 1024 entries and 121000 pages 21; a fork of one
+// sequence into three 7.4 with its copy, of eight into 56 11.9; rows of one tree moved 2.9, of 61 3.8.
 #include <algorithm>
 
 #include "fl_common.cuh"

@@ -15,12 +15,12 @@
 // same calls issued directly: every graph launch boundary serialises the
 // stream, 371 against 308 us for four D = 4096 layers.)
 //
-// The layer is split where the attention core sits, which this library does
-// not compute:
+// The layer is split where the attention core sits, fl_attention or
+// fl_kv_attend on the layer's q, or a kernel of the caller's:
 //   half 0: q, k, v = RMSNorm(x; gamma_attn) [Wq; Wk; Wv]^T   (one fused launch);
 //           with fl_layer_attach_cache, q and k rotated in place and k and v
 //           quantised into the paged cache
-//   -- the caller's attention writes attn [M, D] --
+//   -- attention writes attn [M, D] --
 //   half 1: h   = attn Wo^T (+ bias_o) + x
 //           out = SwiGLU_FFN(h; gamma_ffn, Wg, Wu, Wd) + h      (RMSNorm fused)
 #include <cuda_runtime.h>

@@ -235,13 +235,13 @@ fl_status fl_swiglu_ffn_noalloc(const void* x, const void* gamma, const void* Wg
  * The dense part of a Llama-style decoder layer as a prepared call sequence.
  * At decode sizes every kernel of a layer takes a few microseconds, so host
  * launch costs weigh as much as the kernels; a decode step is meant to be
- * captured once, every layer with the caller's attention in between, into
+ * captured once, every layer with its attention in between, into
  * one CUDA graph (fl_capture_begin .. fl_capture_end) and replayed with one
  * launch (the "Fusion Compiler" glossary pairs fusion with CUDA Graph capture
  * as the coarse-grained launch optimisation). The layer is split where the
- * attention core sits, which this library does not compute:
+ * attention core sits (fl_attention, fl_kv_attend or a kernel of the caller's):
  *   half 0:  q, k, v = RMSNorm(x; gamma_attn) [Wq; Wk; Wv]^T       (fl_norm_gemm_multi)
- *   ... the caller's attention reads q, k, v and writes attn ...
+ *   ... attention reads q, k, v or the cache and writes attn ...
  *   half 1:  h   = attn Wo^T (+ bias_o) + x                        (fl_gemm_epilogue)
  *            out = silu(hn Wg^T) * (hn Wu^T) Wd^T + h, hn = RMSNorm(h; gamma_ffn)   (fl_swiglu_ffn)
  * Shapes: x, attn, h, out, q [M, D]; k, v [M, Dkv]; Wq, Wo [D, D];
@@ -534,7 +534,8 @@ fl_status fl_rope(const fl_rope_desc* desc, void* stream);
  * A row that sees no key gets zeros. Keys and values that a row does not see do not
  * reach it, whatever they hold. Scores, maxima and sums are fp32; rounded to the
  * dtype are the weights and the output. head_dim is a multiple of 8, 8 .. 128;
- * scale is positive. rows_q 0 does nothing.
+ * scale is positive. An expanded tensor (a stride of 0) is refused. rows_q 0 does
+ * nothing.
  */
 typedef struct {
     fl_dtype dtype;
@@ -616,7 +617,8 @@ fl_status fl_kv_read(const fl_kv_desc* desc, void* stream);
  * sequence's new rows those up to itself, or with `tree` the j-th new row where
  * tree[i * tree_stride + j] is not 0, j < tree_cols (device, one byte each; itself
  * only if marked): the drafted tokens of a tree see their ancestors. A row that
- * sees nothing gets zeros. Positions without a page are not seen, and
+ * sees nothing gets zeros, and a new row at a negative position is seen by
+ * none. Positions without a page are not seen, and
  * reported as above; rows that belong to no sequence are left as they were.
  *   q, out: [rows, heads_q, head_dim] at the strides given, as k and v above; query
  *   head h reads key head h / (heads_q / heads_k). out overlaps no other tensor.
