@@ -27,12 +27,13 @@
 //
 // What bounds it: softmax's 2^x and the two products take as long on a
 // multiprocessor, 1.3 us for a block of both tiles, where the products alone
-// would take 1.1. One causal sequence of 8192 rows, 32 and 8 heads of 128, bf16: 360 us,
-// 1530 TFLOP/s; 16384 rows of 16 heads 655 us, 1680; 4096 rows causal 108 us, 1270. A
-// CTA's start and end (tensor memory, the first loads, the edge blocks, the output)
-// are not hidden, since a multiprocessor holds one: 8 us, so that short
-// sequences fare worse (eight of 512 rows: 43 us, 400 TFLOP/s; five chunks of 330 to
-// 490 rows over 480 to 1930 keys: 55 us, 700). Two tiles to a CTA, not one,
+// would take 1.1. One causal sequence of 8192 rows, 32 and 8 heads of 128, bf16: 355 us,
+// 1547 TFLOP/s; 16384 rows of 16 heads 655 us, 1680; 4096 rows causal 106 us, 1300. A
+// CTA's start (its rows found, the first loads and scores: 2.9 us) and end (output: 2.5)
+// are not hidden, since a multiprocessor holds one, so that short
+// sequences fare worse (eight of 512 rows: 41.5 us, 415 TFLOP/s; five chunks of 330 to
+// 490 rows over 480 to 1930 keys: 54 us, 711). (CTAs that stay and take the next
+// rows while the last are finished were no faster: the softmax warps store the output.) Two tiles to a CTA, not one,
 // so that each block of keys is read for 256 rows.
 //
 // Few rows over many keys: a cluster of up to 8 CTAs takes the same rows, each a run of
