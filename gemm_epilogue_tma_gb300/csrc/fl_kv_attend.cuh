@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kJoinThreads) fl_kv_attend_join_kernel(const _
         const float* stat = p.part + (long long)slots(RESIDENT) * M * HD + ((long long)slot * M + r) * 4;
         const float* src = p.part + ((long long)slot * M + r) * HD + lane * C;
         // (the first pieces' sums are asked for together with the maxima that they will be weighed by)
-        constexpr int U = 4;
+        constexpr int U = M >= 128 ? 8 : 4;
         float2 x[U][C / 2];
         auto load = [&](int k, float2* d) {
 #pragma unroll

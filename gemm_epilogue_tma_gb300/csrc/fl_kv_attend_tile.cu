@@ -9,11 +9,11 @@
 // are, six warps write them out as the 16-bit operands' swizzled blocks, and the
 // scales go onto the scores and the weights as before, two per position. The
 // warp-level kernel widens them again for every 32 rows: trees of 48 rows for a group of four
-// heads over contexts of 1000 to 10600 positions, 23000 in all, 146 us there, 62 here.
+// heads over contexts of 1000 to 10600 positions, 23000 in all, 146 us there, 58 here.
 //
-// What bounds it: of those 62 us the start of a CTA (lengths and plan 4, rows of q 4)
+// What bounds it: of those 58 us the start of a CTA (lengths and plan 4, rows of q 4)
 // takes 10, its 9 to 11 blocks 2.8 to 3 each (of which 1.8 are the softmax of a tile and 0.9 the
-// products and the barriers between, the other tile's the same), the end 3, the second launch 8.
+// products and the barriers between, the other tile's the same), the end 3, the second launch 5.
 //
 // Roles: warps 0-7 softmax, one tile to four of them, a row to a thread; warp 8 the
 // MMAs, warp 9 the loads, 10-15 widen. Blocks of 128 positions of k and v take
@@ -630,7 +630,7 @@ cudaError_t launch_tile(const AttendParams& p, int dt, int fmt, int hd, int M, l
         if (e == cudaSuccess) e = host::launch(fl_kv_attend_tile_kernel<DT, FMT, HD, MR / kRows>, grid, kThreads, bytes, ctx.pdl, stream, p);
         *launches = 1;
         if (e != cudaSuccess || !split) return e;
-        const dim3 join((unsigned)std::min<long long>(ctx.sms * 8ll, units * (MR / 4)));
+        const dim3 join((unsigned)std::min<long long>(ctx.sms * 16ll, units * (MR / 4)));
         *launches = 2;
         return host::launch(fl_kv_attend_join_kernel<DT, HD, kTileResident, MR>, join, kJoinThreads, 0, ctx.pdl, stream, p);
     };
