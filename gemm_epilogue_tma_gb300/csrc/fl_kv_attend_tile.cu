@@ -276,6 +276,15 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
                 }
                 if (!(ok = __all_sync(0xffffffffu, wait_here(raw_empty(x), round(x) ^ 1u, p.status, p.timeout_ns, 65)))) break;
                 const uint32_t dst = sbase + Lay::kOffRaw + x % kRing * Lay::kCodes, tab = sbase + Lay::kOffTab + j % kTabs * (3 * kRows * 4);
+                // (which positions are there, in front of the arrival that hands it on: the one behind the copies orders them alone)
+                if ((x & 1) == 0) {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const uint32_t bits = __ballot_sync(0xffffffffu, entry[u] >= 0 && entry[u] < p.n_pages);
+                        if (lane == 0)
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(sbase + Lay::kOffBits + j % kTabs * 16 + 4 * u), "r"(bits) : "memory");
+                    }
+                }
                 if (lane == 0) mbar_arrive_expect_tx(raw_full(x), Lay::kCodes);
                 __syncwarp();
                 const CUtensorMap* map = &p.tm[x & 1];
@@ -288,9 +297,6 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
                         tma_load_4d(dst + at * DP, map, raw_full(x), 0, piece.head, there ? row[u] : 0, there ? entry[u] : p.n_pages);
                     if ((x & 1) == 0) {
                         if (entry[u] != -2 && !there) atomicCAS(p.range, 0, s.row0 + 1);
-                        const uint32_t bits = __ballot_sync(0xffffffffu, there);
-                        if (lane == 0)
-                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(sbase + Lay::kOffBits + j % kTabs * 16 + 4 * u), "r"(bits) : "memory");
                         if (there) {
                             const long long from = ((long long)entry[u] * p.page_size + row[u]) * p.heads + piece.head;
                             cp_async4(tab + at * 4, p.scale[0] + from);
