@@ -605,7 +605,8 @@ fl_status check_sizes(const fl_kv_attend_desc* d) {
     if (d->head_dim % 8 != 0) return fail(FL_ERR_ALIGNMENT, "%s: head_dim must be a multiple of 8 (%d)", what, d->head_dim);
     if (d->head_dim > 256) return fail(FL_ERR_UNSUPPORTED, "%s: head_dim above 256 (%d)", what, d->head_dim);
     if (d->n_seqs > 1 << 30) return fail(FL_ERR_UNSUPPORTED, "%s: more than 2^30 sequences", what);
-    if ((long long)d->rows * (d->heads_q / d->heads_k) >= (1ll << 31) - 64 || plan_of(d).units + slots(kResident) >= (1ll << 31))
+    // (512: the kernels count row blocks of up to 256 rows, the last of them filled up, in 32 bits)
+    if ((long long)d->rows * (d->heads_q / d->heads_k) > (1ll << 31) - 1 - 512 || plan_of(d).units + slots(kResident) >= (1ll << 31))
         return fail(FL_ERR_UNSUPPORTED, "%s: too many rows", what);
     return FL_OK;
 }

@@ -256,3 +256,19 @@ def test_oracle_mistakes_are_seen():
     assert not np.allclose(good, oracle.attention(q, k[:, ::-1], v[:, ::-1], [0, 6], [0, 9], True, 0.35)["out"])
     assert not np.allclose(good, oracle.attention(q, k, v, [0, 6], [0, 9], True, 0.36)["out"])
     assert not np.allclose(good, oracle.attention(q, k[:6], v[:6], [0, 6], [0, 6], True, 0.35)["out"])
+
+
+@no_gpu
+def test_kv_attend_sizes_next_to_32_bits(L):
+    """Row blocks of up to 256 rows are counted in 32 bits on the GPU: rows times heads of a group up to 2^31 - 513."""
+    def call(rows, **kw):
+        kw = {**dict(n_seqs=1, table_stride=40, tree=None, heads_q=1, heads_k=1, head_dim=16, q_row=16, q_head=16, out_row=16,
+                     out_head=16, q=1 << 40, out=1 << 41, page_size=64), **kw}
+        return L.fl_kv_attend(ctypes.byref(attend_desc(rows=rows, **kw)), addr(10), 1 << 30, None)
+    for kw in ({}, dict(page_size=8), dict(head_dim=256, q_row=256, q_head=256, out_row=256, out_head=256)):
+        assert passed(L, call((1 << 31) - 513, **kw))
+        for less in (512, 300, 255, 65, 64, 1):
+            assert call((1 << 31) - less, **kw) == UNSUPPORTED and "too many rows" in fl.last_error()
+    four = dict(heads_q=4, q_row=64, out_row=64)
+    assert passed(L, call((1 << 29) - 129, **four)) and call((1 << 29) - 128, **four) == UNSUPPORTED
+    assert "too many rows" in fl.last_error()
