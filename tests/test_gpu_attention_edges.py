@@ -62,3 +62,157 @@ def test_kv_attend_many_rows_gaps_that_differ_from_block_to_block(dt, fmt, H, gr
         with pytest.raises(fl.FusedLinError):
             fl.device_status()
         assert torch.equal(again, got)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("H,group,D,page,n_rows,start", [
+    (1, 4, 128, 16, [48], [0]),
+    (1, 4, 128, 16, [48, 33], [100, 5]),
+    (2, 4, 64, 16, [64, 64], [700, 129]),
+    (1, 1, 96, 7, [129, 40], [300, 3]),
+    (1, 1, 16, 16, [300], [64]),
+    (1, 4, 96, 9, [50], [1500]),
+    (1, 3, 128, 1000, [70, 1, 0], [130, 2000, 77]),
+    (1, 40, 64, 32, [1, 1], [90, 1029]),
+])
+def test_kv_attend_many_rows_in_wide_tables(dt, fmt, H, group, D, page, n_rows, start):
+    """Short and empty contexts, pages that do not divide a tile, blocks of one and of two tiles of rows: tables of 1024
+    positions at least, so that the many-row kernel has them. A wider table changes nothing, in no bit."""
+    rng = gen(81, H, group, D, page, sum(start))
+    cache = widened(Paged(rng, [a + b for a, b in zip(n_rows, start)], H, D, page, fmt), 1024)
+    for tree in (None, rng.random((sum(n_rows), max(max(n_rows) - 1, 1))) < 0.3):
+        got, ref, q = attend_case(rng, dt, cache, H * group, n_rows, start, tree)
+        fl.device_status()
+        assert row_blocks(q, cache, n_rows) == (128 if sum(n_rows) * group <= 128 * len(n_rows) else 256)
+        attend_check(got, ref, dt, cache, n_rows, start)
+        table = widened(cache, 6000).table
+        again = fl.kv_attend(q, *cache.tensors(), ints(table), ints(start), cu_rows=ints(sums(n_rows)),
+                             tree=None if tree is None else put(tree))
+        assert torch.equal(again, got)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("far", [0, 1100])
+def test_kv_attend_many_rows_junk_in_places_that_are_not_seen(dt, fmt, D, far):
+    """NaN codes and scales in unused places, drafts that hold no number, rows that see nothing, rows behind the last
+    sequence, one row of q that is not finite: each stays where it belongs. (The warps' rows choose together how the weights
+    are formed, so that beside rows that are not finite the others are compared with the oracle, not in each bit.)"""
+    rng = gen(82, D, far)
+    n_rows, start = [40, 50], [137 + far, 0]
+    cache = widened(Paged(rng, [177 + far, 50], 1, D, 16, fmt), 1024)
+    tree = rng.random((95, 50)) < 0.4
+    tree[:, 7] = False
+    tree[3, 7] = tree[60, 7] = True
+    tree[45] = False                                # sees nothing: its context is empty
+    q = put(rng.standard_normal((95, 4, D)), dt)
+    out = torch.full_like(q, 7.0)
+    clean, ref, _ = attend_case(rng, dt, cache, 4, n_rows, start, tree, q=q, out=out)
+    clean = clean.clone()
+    assert row_blocks(q, cache, n_rows) == 256
+    assert (clean[90:] == 7).all() and (clean[45] == 0).all()
+    attend_check(clean[:90], ref, dt, cache, n_rows, start)
+    used = np.zeros((cache.pages, 16), dtype=bool)
+    for b, n in ((0, 177 + far), (1, 50)):
+        for p in range(n):
+            used[cache.table[b, p // 16], p % 16] = True
+    junk = torch.from_numpy(~used).cuda()
+    for t in (cache.ks, cache.vs):
+        t[junk] = float("nan")
+    for t in (cache.k, cache.v):
+        t.view(torch.uint8)[junk] = 0x7f            # a NaN in e4m3
+
+    def call():
+        r = fl.kv_attend(q, *cache.tensors(), ints(cache.table), ints(start), cu_rows=ints(sums(n_rows)), tree=put(tree), out=out)
+        fl.device_status()
+        assert (r[90:] == 7).all()
+        return r
+    assert torch.equal(call(), clean)
+
+    def others(got, bad):
+        """All rows but `bad` as the oracle has them."""
+        keep = [i for i in range(90) if i not in bad]
+        attend_check(got[keep], {n: x[keep] for n, x in ref.items()}, dt, cache, n_rows, start)
+    # draft 7 of each sequence holds no number: rows 3 and 60 see it, no others
+    held = [x.clone() for x in cache.tensors()]
+    for b, pos in ((0, 144 + far), (1, 7)):
+        page, at = int(cache.table[b, pos // 16]), pos % 16
+        for t in (cache.k, cache.v):
+            t.view(torch.uint8)[page, at] = 0
+        for t in (cache.ks, cache.vs):
+            t[page, at] = float("nan")
+    got = call()
+    assert torch.isnan(got[3]).all() and torch.isnan(got[60]).all()
+    others(got, (3, 60))
+    for t, x in zip(cache.tensors(), held):
+        t.view(torch.uint8).copy_(x.view(torch.uint8))
+    # so does a row of q, of itself and one head
+    for bad in (float("inf"), float("nan")):
+        keep = q[20, 2, 1].clone()
+        q[20, 2, 1] = bad
+        got = call()
+        assert torch.isnan(got[20, 2]).any()
+        others(got, (20,))
+        heads = [0, 1, 3]
+        attend_check(got[20:21, heads], {n: x[20:21, heads] for n, x in ref.items()}, dt, cache, n_rows, start)
+        q[20, 2, 1] = keep
+    assert torch.equal(call(), clean)
+    # pages that are not there
+    cache = widened(Paged(rng, [177 + far, 50], 1, D, 16, fmt), 1024)
+    cache.table[0, 4] = -1
+    cache.table[0, (137 + far) // 16] = 1 << 30
+    got, ref, _ = attend_case(rng, dt, cache, 4, n_rows, start)
+    with pytest.raises(fl.FusedLinError) as e:
+        fl.device_status()
+    assert e.value.status == 7
+    attend_check(got, ref, dt, cache, n_rows, start)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_kv_attend_many_rows_scales_and_scores_far_apart(dt, D):
+    """Values whose scales lie 2^18 apart, scores that grow towards the end so that weights formed with the maxima so far do not
+    do, and rows of bf16 far outside fp16's range, over contexts that the many-row kernel has."""
+    rng = gen(83, D)
+    n, n_rows, start = 60, [60], [1300]
+    cache = Paged(rng, [1360], 1, D, 16, "int8")
+    assert cache.table.shape[1] * 16 >= 1024
+    cache.scale[1] = np.where(rng.random(cache.scale[1].shape) < 0.5, 2.0 ** -6, 2.0 ** -24).astype(np.float32)
+    pos = np.zeros((cache.pages, 16))
+    for p in range(1360):
+        pos[cache.table[0, p // 16], p % 16] = p
+    for grow in (1.003, 1.0):
+        cache.scale[0] = (0.002 * grow ** pos)[..., None].astype(np.float32)
+        cache.ks, cache.vs = put(cache.scale[0]), put(cache.scale[1])
+        for size in ((2.0 ** -50, 1.0, 2.0 ** 40) if dt == "bf16" else (2.0 ** -4, 2.0 ** 4)):
+            q = put(rng.standard_normal((n, 1, D)) * size * np.exp2(rng.integers(-6, 6, (n, 1, 1))), dt)
+            scale = 0.08 / size
+            got, ref, _ = attend_case(rng, dt, cache, 1, n_rows, start, q=q, scale=scale)
+            fl.device_status()
+            assert row_blocks(q, cache, n_rows) == 128
+            vals = cache.values()[0]
+            floor = np.zeros((n, 1))
+            for i in range(n):
+                x = vals[0][:1301 + i, 0] @ f64(q)[i, 0] * scale
+                w = np.exp(x - x.max())
+                vs = cache.scale[1][cache.table[0][:85]].reshape(-1)[:len(w)]
+                floor[i, 0] = len(w) * 2.0 ** -25 * 127 * (w / w.sum() * vs).max()
+            check(got, ref, U[dt], 2.0 ** -11, 2.0 ** -18, floor, f"{grow} {size}")
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("D,start", [(64, 9000), (128, 12100)])
+def test_kv_attend_many_rows_of_more_pieces_than_a_warp_has_lanes(dt, fmt, D, start):
+    """One row block over 71 and 95 tiles is split into pieces of two: 36 and 48 to be joined."""
+    rng = gen(84, D)
+    cache = Paged(rng, [start + 48], 1, D, 64, fmt)
+    got, ref, q = attend_case(rng, dt, cache, 4, [48], [start])
+    fl.device_status()
+    assert row_blocks(q, cache, [48]) == 256
+    attend_check(got, ref, dt, cache, [48], [start])
+    for _ in range(3):
+        again = fl.kv_attend(q, *cache.tensors(), ints(cache.table), ints([start]), cu_rows=ints([0, 48]))
+        assert torch.equal(again, got)
