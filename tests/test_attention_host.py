@@ -272,3 +272,12 @@ def test_kv_attend_sizes_next_to_32_bits(L):
     four = dict(heads_q=4, q_row=64, out_row=64)
     assert passed(L, call((1 << 29) - 129, **four)) and call((1 << 29) - 128, **four) == UNSUPPORTED
     assert "too many rows" in fl.last_error()
+
+
+def test_kv_attend_workspace_of_the_shortest_table_that_may_be_split(L):
+    """Up to 512 positions a sequence is never split (the GPU's plan goes by its lengths alone) and no workspace is needed."""
+    for size, pages in ((16, 32), (1, 512), (512, 1), (19, 26), (300, 1)):
+        for kw in ({}, dict(head_dim=256), dict(rows=300, n_seqs=1), dict(cu_rows=None), dict(head_dim=24)):
+            need = [L.fl_kv_attend_workspace_size(ctypes.byref(attend_desc(page_size=size, table_pages=n, table_stride=n, **kw)))
+                    for n in (pages, 512 // size + 1)]
+            assert need[0] == 0 and 0 < need[1] <= 42 << 20

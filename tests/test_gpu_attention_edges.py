@@ -216,3 +216,43 @@ def test_kv_attend_many_rows_of_more_pieces_than_a_warp_has_lanes(dt, fmt, D, st
     for _ in range(3):
         again = fl.kv_attend(q, *cache.tensors(), ints(cache.table), ints([start]), cu_rows=ints([0, 48]))
         assert torch.equal(again, got)
+
+
+# ---------------------------------------------------------------------------
+# few rows of a sequence over the cache
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("H,group,D,n_rows", [(1, 4, 128, [1, 1]), (8, 1, 64, [16, 5]), (2, 3, 256, [5, 1])])
+def test_kv_attend_tables_around_the_shortest_that_may_be_split(dt, fmt, H, group, D, n_rows):
+    """512 positions, filled to the last, need no workspace; one page more does."""
+    for pages in (32, 33):
+        rng = gen(85, H, D, pages)
+        start = [16 * pages - n_rows[0], 16 * pages - 20]
+        cache = Paged(rng, [a + b for a, b in zip(n_rows, start)], H, D, 16, fmt)
+        cache.table = cache.table[:, :pages]
+        got, ref, q = attend_case(rng, dt, cache, H * group, n_rows, start)
+        fl.device_status()
+        need = fl.kv_attend_workspace_size(q, cache.k, ints(cache.table), ints(sums(n_rows)))
+        assert (need == 0) == (pages == 32)
+        attend_check(got, ref, dt, cache, n_rows, start)
+        # the same pages in a wide table: the same plan of the same lengths, the same bits
+        wide = widened(cache, 4096).table
+        again = fl.kv_attend(q, *cache.tensors(), ints(wide), ints(start), cu_rows=ints(sums(n_rows)))
+        fl.device_status()
+        if sum(n_rows) * group <= 32 * len(n_rows):
+            assert torch.equal(again, got)
+        attend_check(again, ref, dt, cache, n_rows, start)
+
+
+# ---------------------------------------------------------------------------
+# attention over 16-bit keys and values
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lq,lk,is_causal", [([200, 150, 20], [60, 0, 3], True), ([5, 3], [0, 4], False), ([300, 1], [1, 700], True)])
+def test_attention_rows_with_keys_beside_rows_without(dt, D, lq, lk, is_causal):
+    got, ref, (*_, floor) = attention_case(dt, 2, 1, D, lq, lk, is_causal, 86)
+    check(got, ref, U[dt], U[dt], 2.0 ** -20, floor)
+    sees = ref["top"] > 0
+    assert (f64(got)[~sees] == 0).all() and not sees.all()
