@@ -57,6 +57,7 @@ constexpr int kRows = 128;               // rows of a tile, keys of a block
 constexpr int kThreads = 384;            // 8 softmax warps, MMA, TMA, 2 for values
 constexpr int kWarpMma = 8, kWarpTma = 9, kWarpFix = 10;
 constexpr float kLazy = 8.f;
+constexpr unsigned long long kBlockNs = 20000;  // that a block of keys takes at most where others use the GPU too
 constexpr int kOCol = 256;               // tensor-memory columns: S of tile i at 128 i, O at 256 + 128 i
 
 struct AttnParams {
@@ -327,9 +328,11 @@ __global__ void __launch_bounds__(kThreads, 1) fl_attention_kernel(const __grid_
             drain_here(drain, 0);
         } else {
             // values of blocks that are not seen whole
+            // (The first wait is for all blocks in front: 1.5 us each, over 2 s for some 1.4 million of them; every one adds to its limit.)
+            const unsigned long long in_front = (unsigned long long)min(edge, nb) * kBlockNs;
             for (int j = edge; j < nb; ++j) {
                 const int lv = 2 * j + 1, s = lv % NS;
-                if (!__all_sync(0xffffffffu, wait_here(v_raw(s), parity(lv), p.status, p.timeout_ns, 47))) break;
+                if (!__all_sync(0xffffffffu, wait_here(v_raw(s), parity(lv), p.status, p.timeout_ns + in_front, 47))) break;
                 const int first_key = (j0 + j) * kRows, valid = min(kRows, lk - first_key);
                 const uint32_t base = sbase + Lay::kOffRing + s * Lay::kBlock;
                 constexpr int U = 8;  // vectors in flight (one at a time a block took 1.7 us longer than its products)

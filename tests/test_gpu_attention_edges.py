@@ -256,3 +256,36 @@ def test_attention_rows_with_keys_beside_rows_without(dt, D, lq, lk, is_causal):
     check(got, ref, U[dt], U[dt], 2.0 ** -20, floor)
     sees = ref["top"] > 0
     assert (f64(got)[~sees] == 0).all() and not sees.all()
+
+
+def test_attention_keys_for_longer_than_a_wait_may_take():
+    """The values of the last block are mended once it is there, however long the blocks in front of it take."""
+    rng = gen(87)
+    n, hq, D, m = 256, 80, 64, 1000003
+    q = put(rng.standard_normal((n, hq, D)), "bf16")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(87)
+    k, v = (torch.randn(m, 1, D, generator=g, device="cuda").to(torch.bfloat16) for _ in "kv")
+    torch.cuda.synchronize()
+    a, b = (torch.cuda.Event(enable_timing=True) for _ in "ab")
+    fl.set_option("timeout_ms", 2)
+    try:
+        a.record()
+        got = fl.attention(q, k, v, causal=False)
+        b.record()
+        fl.device_status()
+    finally:
+        fl.set_option("timeout_ms", 2000)
+    assert a.elapsed_time(b) > 4
+    rows, heads = [0, 131, 255], [0, 41, 79]
+    ref = {x: np.zeros((3, 3, D)) for x in ("out", "mag", "sq")}
+    ref["size"] = np.zeros((3, 3))
+    kd, vd = k[:, 0].double(), v[:, 0].double()
+    for i, r in enumerate(rows):
+        for j, h in enumerate(heads):
+            x = q[r, h].double()
+            w = torch.softmax(kd @ x / 8, 0)
+            for name, val in (("out", w @ vd), ("mag", w @ vd.abs()), ("sq", w ** 2 @ vd ** 2)):
+                ref[name][i, j] = val.cpu().numpy()
+            ref["size"][i, j] = float((kd.abs() @ x.abs()).max()) / 8 / np.log(2.0)
+    check(got[rows][:, heads], ref, U["bf16"], U["bf16"], 2.0 ** -20, np.zeros((3, 3)))
