@@ -56,7 +56,7 @@ namespace {
 constexpr int kRows = 128;               // rows of a tile, keys of a block
 constexpr int kThreads = 384;            // 8 softmax warps, MMA, TMA, 2 for values
 constexpr int kWarpMma = 8, kWarpTma = 9, kWarpFix = 10;
-constexpr float kLazy = 8.f;
+constexpr float kLazy = 8.f, kLarge = 0x1p20f;
 constexpr unsigned long long kBlockNs = 20000;  // that a block of keys takes at most where others use the GPU too
 constexpr int kOCol = 256;               // tensor-memory columns: S of tile i at 128 i, O at 256 + 128 i
 
@@ -373,7 +373,33 @@ __global__ void __launch_bounds__(kThreads, 1) fl_attention_kernel(const __grid_
         const float kNone = __int_as_float(0xff800000);
         float m = kNone, neg = 0.f;  // the maximum, and minus it (0 where there is none yet)
         float2 l = make_float2(0.f, 0.f);
-        bool ok = true;
+        bool any_large = false, ok = true;
+        // c s - m is formed with one rounding. Once m is 2^20 in size its own rounding would show in that, as 2^4 and more from
+        // 2^28 on, which p cannot hold: such a row's scores are rounded, as m was, before the difference. (Warps without such a row pass by;
+        // the check and what stands behind it cost calls 0.1 to 1 us of a CTA's start, and 2 % at 64 channels.)
+        auto weights_of_large = [&](int j) {
+            const int seen = last - (j0 + j) * kRows;
+            const bool large = fabsf(neg) >= kLarge;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                float x[32];
+                uint32_t w[16];
+                tmem_ld_32x32b_x32(s_col + 32u * c, reinterpret_cast<uint32_t(&)[32]>(x));
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    float v[2];
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        const float y = large ? __fadd_rn(__fmul_rn(x[e + f], p.c), neg) : fmaf(x[e + f], p.c, neg);
+                        v[f] = 32 * c + e + f > seen ? 0.f : ex2(y);
+                    }
+                    l = add2(l, make_float2(v[0], v[1]));
+                    w[e / 2] = Ops::pack(v[0], v[1]);
+                }
+                tmem_st_32x32b_x16(s_col + 16u * c, w);
+            }
+        };
         for (int j = 0; j < n; ++j) {
             if (!(ok = __all_sync(0xffffffffu, wait_here(s_full(i), (uint32_t)(j & 1), p.status, p.timeout_ns, 48)))) break;
             tc_fence_after();
@@ -405,6 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) fl_attention_kernel(const __grid_
                     f = ex2(m - top);
                     m = top, neg = -top;
                 }
+                any_large = __any_sync(0xffffffffu, fabsf(neg) >= kLarge);
                 if (j > 0) {
                     l.x *= f, l.y *= f;
 #pragma unroll
@@ -418,19 +445,23 @@ __global__ void __launch_bounds__(kThreads, 1) fl_attention_kernel(const __grid_
                     }
                 }
             }
-            const float2 cc = make_float2(p.c, p.c), nn = make_float2(neg, neg);
+            if (__builtin_expect(any_large, 0)) {
+                weights_of_large(j);
+            } else {
+                const float2 cc = make_float2(p.c, p.c), nn = make_float2(neg, neg);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t w[32];
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t w[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const float* x = &s[2 * h + e / 16][2 * (e % 16)];
-                    const float2 y = ffma2(make_float2(x[0], x[1]), cc, nn);
-                    const float2 v = make_float2(ex2(y.x), ex2(y.y));
-                    l = add2(l, v);
-                    w[e] = Ops::pack(v.x, v.y);
+                    for (int e = 0; e < 32; ++e) {
+                        const float* x = &s[2 * h + e / 16][2 * (e % 16)];
+                        const float2 y = ffma2(make_float2(x[0], x[1]), cc, nn);
+                        const float2 v = make_float2(ex2(y.x), ex2(y.y));
+                        l = add2(l, v);
+                        w[e] = Ops::pack(v.x, v.y);
+                    }
+                    tmem_st_32x32b_x32(s_col + 32u * h, w);
                 }
-                tmem_st_32x32b_x32(s_col + 32u * h, w);
             }
             tmem_st_wait();
             tc_fence_before();

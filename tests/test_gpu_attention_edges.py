@@ -289,3 +289,40 @@ def test_attention_keys_for_longer_than_a_wait_may_take():
                 ref[name][i, j] = val.cpu().numpy()
             ref["size"][i, j] = float((kd.abs() @ x.abs()).max()) / 8 / np.log(2.0)
     check(got[rows][:, heads], ref, U["bf16"], U["bf16"], 2.0 ** -20, np.zeros((3, 3)))
+
+
+# ---------------------------------------------------------------------------
+# scores of any size
+# ---------------------------------------------------------------------------
+SIZES = [2.0 ** 12, 2.0 ** 20, 2.0 ** 24, 2.0 ** 27, 2.0 ** 31, 2.0 ** 62, 2.0 ** 99]
+
+
+def winners(q, k, sees, scale):
+    """The key with the largest score of each row of q [n, D] over k [m, D], and whether it is certain to have all the weight: in
+    front of the next by 2^60 in weight and by more than the scores are off by."""
+    x = np.where(sees, q @ k.T, -np.inf)
+    size = (np.abs(q) @ np.abs(k).T * sees).max(1)
+    two = np.sort(np.concatenate((np.full((len(x), 1), -np.inf), x), 1), 1)[:, -2:]
+    with np.errstate(invalid="ignore"):
+        gap = two[:, 1] - two[:, 0]
+    return x.argmax(1), sees.any(1) & (gap * scale > 42) & (gap > 2.0 ** -18 * size)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,m", [(300, 300), (5, 3000)])
+@pytest.mark.parametrize("scale", SIZES)
+def test_attention_scores_of_any_size(dt, D, n, m, scale):
+    """A row whose largest score stands alone gets its key's value. Its weight is 2^r, r the rounding of a score of 2^20 at most (larger
+    ones are differences of rounded products, r = 0); rounded to the dtype, divided by itself and multiplied, then rounded
+    once more: 2 u and some 2^-23 together."""
+    rng = gen(88, D, n)
+    q, k, v = (put(rng.standard_normal((x, h, D)), dt) for x, h in ((n, 2), (m, 1), (m, 1)))
+    got = f64(fl.attention(q, k, v, scale=scale))
+    fl.device_status()
+    assert np.isfinite(got).all()
+    for h in range(2):
+        best, sure = winners(f64(q)[:, h], f64(k)[:, 0], oracle.causal(n, m), scale)
+        assert sure.mean() > 0.9
+        y = f64(v)[best[sure], 0]
+        assert (np.abs(got[sure, h] - y) <= (2 * U[dt] + 2.0 ** -20) * np.abs(y) + 2.0 ** -25 * (dt == "f16")).all()
