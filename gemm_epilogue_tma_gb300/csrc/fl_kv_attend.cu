@@ -7,7 +7,7 @@
 // multiply: both formats fit fp16 exactly (e4m3 times 2^-8: its bits moved), so no
 // key or value is rounded; ks goes onto the fp32 scores, and vs into the weights
 // of the second product, w vs = 2^(x + log2 vs), which have a running maximum of
-// their own, so that they fill fp16's range whatever the scales are. Rounded are
+// their own, kept less that of x, so that they fill fp16's range whatever the scales are. Rounded are
 // those weights (fp16, 2^-12 of each) and the output. bf16 rows of q are
 // multiplied as fp16 times a power of two per row, which keeps their 8 bits down
 // to 2^-28 of the row's largest value.
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, QT>::kCtas) fl_kv_attend_
     const Pieces<kWarps, kResident> pieces(p, M, Lay::kQInRegs);
     if (blockIdx.x == 0 && threadIdx.x == 0 && p.part != nullptr) units_of<kResident, M, HD>(p)->count = (int)pieces.units;
     const uint32_t ring = sbase + warp * NS * Lay::kStage, meta = sbase + Lay::kOffMeta + warp * NS * Lay::kMeta;
-    const float kNone = __int_as_float(0xff800000), kNoMax = 1e30f;
+    const float kNone = __int_as_float(0xff800000), kNoMax = __int_as_float(0x7f7fffff);
     int stage = 0;       // the ring runs on from piece to piece
     uint32_t phase = 0;
 
@@ -308,14 +308,14 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, QT>::kCtas) fl_kv_attend_
             }
 
             // ------------------------------------------------------------ the warp's positions
-            // nx, nw: minus the maxima of the exponents x and x + log2 vs; kNoMax where there is
-            // none yet, which any finite exponent exceeds by more than kLazy
-            float nx[QT][2], nw[QT][2], l[QT][2], o[QT][MT][4];
+            // nx, nb: minus the maximum of the exponents x, and minus that of x + log2 vs less it; kNoMax, fp32's largest
+            // number, where there is none yet, which any exponent exceeds by more than kLazy
+            float nx[QT][2], nb[QT][2], l[QT][2], o[QT][MT][4];
             uint32_t seen = 0;  // bit 2 qt + f: the row saw a position (which tells it from one whose scores are all -inf)
 #pragma unroll
             for (int qt = 0; qt < QT; ++qt) {
 #pragma unroll
-                for (int f = 0; f < 2; ++f) nx[qt][f] = nw[qt][f] = kNoMax, l[qt][f] = 0.f;
+                for (int f = 0; f < 2; ++f) nx[qt][f] = nb[qt][f] = kNoMax, l[qt][f] = 0.f;
 #pragma unroll
                 for (int j = 0; j < MT; ++j)
 #pragma unroll
@@ -384,15 +384,17 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, QT>::kCtas) fl_kv_attend_
                 } else {
                     seen = (1u << 2 * QT) - 1;
                 }
-                // exponents less the maxima, for the sum of weights and for the weights of the values
+                // exponents less the maxima, for the sum of weights and for the weights of the values. (Each step is rounded: a fused
+                // one would show how the maximum was, by 2^4 and more for exponents of 2^28 on, which a weight cannot hold.)
                 float a[QT][4], b[QT][4], most = kNone;
                 auto exponents = [&] {
 #pragma unroll
                     for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            a[qt][e] = fmaf(x[qt][e], c[qt][e & 1], nx[qt][e & 1]);
-                            b[qt][e] = fmaf(x[qt][e], c[qt][e & 1], lv[e >> 1] + nw[qt][e & 1]);
+                        for (int i = 0; i < 2; ++i) {
+                            const float2 y = add2(make_float2(x[qt][2 * i], x[qt][2 * i + 1]), make_float2(nx[qt][0], nx[qt][1]));
+                            const float2 z = add2(y, add2(make_float2(lv[i], lv[i]), make_float2(nb[qt][0], nb[qt][1])));
+                            a[qt][2 * i] = y.x, a[qt][2 * i + 1] = y.y, b[qt][2 * i] = z.x, b[qt][2 * i + 1] = z.y;
                         }
                     if (hidden != 0) {
 #pragma unroll
@@ -405,7 +407,10 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, QT>::kCtas) fl_kv_attend_
 #pragma unroll
                 for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[qt][e] *= ks[e >> 1];
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 y = mul2(mul2(make_float2(x[qt][2 * i], x[qt][2 * i + 1]), make_float2(ks[i], ks[i])), make_float2(c[qt][0], c[qt][1]));
+                        x[qt][2 * i] = y.x, x[qt][2 * i + 1] = y.y;
+                    }
                 exponents();
 #pragma unroll
                 for (int qt = 0; qt < QT; ++qt)
@@ -419,25 +424,26 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, QT>::kCtas) fl_kv_attend_
                             float ma = kNone, mb = kNone;
 #pragma unroll
                             for (int i = 0; i < 2; ++i)
-                                if (!(hidden >> (4 * qt + 2 * i + f) & 1)) {
-                                    const float y = x[qt][2 * i + f] * c[qt][f];
-                                    ma = fmaxf(ma, y), mb = fmaxf(mb, y + lv[i]);
-                                }
+                                if (!(hidden >> (4 * qt + 2 * i + f) & 1)) ma = fmaxf(ma, x[qt][2 * i + f]);
 #pragma unroll
-                            for (int w = 4; w < 32; w <<= 1) {
-                                ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, w));
-                                mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, w));
-                            }
+                            for (int w = 4; w < 32; w <<= 1) ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, w));
                             // (a maximum that is there already only grows)
-                            if (nx[qt][f] == kNoMax ? ma > kNone : ma > -nx[qt][f]) {
-                                l[qt][f] *= nx[qt][f] == kNoMax ? 0.f : ex2(-nx[qt][f] - ma);
+                            const bool first = nx[qt][f] == kNoMax;
+                            if (first ? ma > kNone : ma > -nx[qt][f]) {
+                                l[qt][f] *= first ? 0.f : ex2(-nx[qt][f] - ma);
+                                if (nb[qt][f] != kNoMax) nb[qt][f] += ma + nx[qt][f];  // (that maximum itself stays)
                                 nx[qt][f] = -ma;
                             }
-                            if (nw[qt][f] == kNoMax ? mb > kNone : mb > -nw[qt][f]) {
-                                const float y = nw[qt][f] == kNoMax ? 0.f : ex2(-nw[qt][f] - mb);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                if (!(hidden >> (4 * qt + 2 * i + f) & 1)) mb = fmaxf(mb, x[qt][2 * i + f] + nx[qt][f] + lv[i]);
+#pragma unroll
+                            for (int w = 4; w < 32; w <<= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, w));
+                            if (nb[qt][f] == kNoMax ? mb > kNone : mb > -nb[qt][f]) {
+                                const float y = nb[qt][f] == kNoMax ? 0.f : ex2(-nb[qt][f] - mb);
 #pragma unroll
                                 for (int j = 0; j < MT; ++j) o[qt][j][f] *= y, o[qt][j][2 + f] *= y;
-                                nw[qt][f] = -mb;
+                                nb[qt][f] = -mb;
                             }
                         }
                     exponents();
@@ -512,42 +518,78 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, QT>::kCtas) fl_kv_attend_
                     for (int j = 0; j < MT; ++j) *reinterpret_cast<float2*>(d + 2 * j) = make_float2(o[qt][j][f], o[qt][j][2 + f]);
                     if (g == 0)  // (this warp's part)
                         *stat(warp, r) =
-                            make_float4(nx[qt][f] == kNoMax ? kNone : -nx[qt][f], nw[qt][f] == kNoMax ? kNone : -nw[qt][f], l[qt][f],
+                            make_float4(nx[qt][f] == kNoMax ? kNone : -nx[qt][f], nb[qt][f] == kNoMax ? kNone : -nb[qt][f], l[qt][f],
                                         seen >> (2 * qt + f) & 1 ? 1.f : 0.f);
                 }
             group_sync();
             const bool whole = piece.pieces == 1;
-            for (int i = own * 32 + lane; i < rows * (HD / 4); i += 32 * W) {
-                const int r = i / (HD / 4), ch = i % (HD / 4) * 4;
-                float ma = kNone, mb = kNone, any = 0.f;
+            // A row's maxima over the warps, and f(w) what warp w's sums are multiplied by: max a, max b less it, sum of weights, seen.
+            auto over_warps = [&](int r, auto factor) {
+                float4 m = make_float4(kNone, kNone, 0.f, 0.f);
 #pragma unroll 4
                 for (int w = group * W; w < group * W + W; ++w) {
                     const float4 st = *stat(w, r);
-                    ma = fmaxf(ma, st.x), mb = fmaxf(mb, st.y), any = fmaxf(any, st.w);
+                    m.x = fmaxf(m.x, st.x), m.w = fmaxf(m.w, st.w);
                 }
-                const float na = ma == kNone ? 0.f : -ma, nb = mb == kNone ? 0.f : -mb;
-                float sum = 0.f;
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
                 for (int w = group * W; w < group * W + W; ++w) {
                     const float4 st = *stat(w, r);
-                    sum += st.z * ex2(st.x + na);
-                    const float f = ex2(st.y + nb);
-                    const float4 d = *reinterpret_cast<const float4*>(sums(w, r) + ch);
-                    v.x = fmaf(d.x, f, v.x), v.y = fmaf(d.y, f, v.y), v.z = fmaf(d.z, f, v.z), v.w = fmaf(d.w, f, v.w);
+                    m.y = fmaxf(m.y, less(st.y, st.x, m.x));
                 }
-                if (whole) {
-                    if (ch < p.head_dim) {
-                        const float2 f = finish(ma, mb, sum, any);
-                        uint2 y = make_uint2(0u, 0u);
-                        if (f.y == 0.f) y = make_uint2(Ops::pack(v.x * f.x, v.y * f.x), Ops::pack(v.z * f.x, v.w * f.x));
-                        *reinterpret_cast<uint2*>(row_at(p, s.row0, piece.head, r0 + r) + ch) = y;
+                const float na = m.x == kNone ? 0.f : -m.x, nm = m.y == kNone ? 0.f : -m.y;
+#pragma unroll 4
+                for (int w = group * W; w < group * W + W; ++w) {
+                    const float4 st = *stat(w, r);
+                    m.z += st.z * ex2(st.x + na);
+                    factor(w, ex2(less(st.y, st.x, m.x) + nm));
+                }
+                return m;
+            };
+            auto add = [&](float4& v, int w, int r, int ch, float f) {
+                const float4 d = *reinterpret_cast<const float4*>(sums(w, r) + ch);
+                v.x = fmaf(d.x, f, v.x), v.y = fmaf(d.y, f, v.y), v.z = fmaf(d.z, f, v.z), v.w = fmaf(d.w, f, v.w);
+            };
+            auto put = [&](const float4& v, int r, int ch, const float2& f) {
+                if (ch >= p.head_dim) return;
+                uint2 y = make_uint2(0u, 0u);
+                if (f.y == 0.f) y = make_uint2(Ops::pack(v.x * f.x, v.y * f.x), Ops::pack(v.z * f.x, v.w * f.x));
+                *reinterpret_cast<uint2*>(row_at(p, s.row0, piece.head, r0 + r) + ch) = y;
+            };
+            auto part = [&](int r, int ch) { return reinterpret_cast<float4*>(p.part + ((long long)piece.slot * M + r) * HD + ch); };
+            auto part_stat = [&](int r) {
+                return reinterpret_cast<float4*>(p.part + (long long)slots(kResident) * M * HD + ((long long)piece.slot * M + r) * 4);
+            };
+            if constexpr (QT == 1) {
+                // (a thread has four channels of one row at 128 channels: it finds the row's maxima for itself)
+                for (int i = own * 32 + lane; i < rows * (HD / 4); i += 32 * W) {
+                    const int r = i / (HD / 4), ch = i % (HD / 4) * 4;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    const float4 m = over_warps(r, [&](int w, float f) { add(v, w, r, ch, f); });
+                    if (whole) {
+                        put(v, r, ch, finish(m.y, m.z, m.w));
+                    } else {
+                        *part(r, ch) = v;
+                        if (ch == 0) *part_stat(r) = m;
                     }
-                } else {
-                    *reinterpret_cast<float4*>(p.part + ((long long)piece.slot * M + r) * HD + ch) = v;
-                    if (ch == 0)
-                        *reinterpret_cast<float4*>(p.part + (long long)slots(kResident) * M * HD + ((long long)piece.slot * M + r) * 4) =
-                            make_float4(ma, mb, sum, any);
+                }
+            } else {
+                // (of more rows, once a row: the factors in place of the warps' maxima, what finishes the row behind the first. Both sides, us:
+                // four contexts of 5700 with 32 rows 43.0 and 42.2, with one row to a sequence 64 of 8192 225 and 235.)
+                for (int r = own * 32 + lane; r < rows; r += 32 * W) {
+                    const float4 m = over_warps(r, [&](int w, float f) { stat(w, r)->x = f; });
+                    const float2 f = finish(m.y, m.z, m.w);
+                    stat(group * W, r)->y = f.x, stat(group * W, r)->z = f.y;
+                    if (!whole) *part_stat(r) = m;
+                }
+                group_sync();
+                for (int i = own * 32 + lane; i < rows * (HD / 4); i += 32 * W) {
+                    const int r = i / (HD / 4), ch = i % (HD / 4) * 4;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                    for (int w = group * W; w < group * W + W; ++w) add(v, w, r, ch, stat(w, r)->x);
+                    const float4 f = *stat(group * W, r);
+                    if (whole) put(v, r, ch, make_float2(f.y, f.z));
+                    else *part(r, ch) = v;
                 }
             }
         }

@@ -16,6 +16,9 @@ constexpr int kLeast = 2;     // tiles of a piece at least
 constexpr int kStart = 3, kJoin = 3;  // tiles that a piece's start and end, and the second launch, take as long as
 constexpr int kWorth = kLeast + kJoin - 1;  // tiles of a sequence up to which a split gains less than the second launch costs
 constexpr float kLazy = 8.f;  // a maximum is moved once it is exceeded by 2^8
+// The kernel for many rows forms an exponent less its maximum with one rounding. Once the maximum is 2^20 in size its own rounding
+// would show in that, as 2^4 and more from 2^28 on, which a weight cannot hold: it then rounds the exponent, as the maximum was, first.
+constexpr float kLarge = 0x1p20f;
 
 // Pieces of split sequences at most, with `resident` CTAs at work at once: L is T /
 // resident at least, and each piece has more than L / 2 tiles.
@@ -38,7 +41,7 @@ struct AttendParams {
     int rows, heads, group, head_dim, page_size, page_shift, n_pages, n_seqs, table_pages;
     int box_log;       // log2 of box_rows
     float log2_scale;  // scale * log2(e)
-    float* part;       // [slots][M][HD] sums, [slots][M][4] maxima, sum of weights, whether a position was seen; Units
+    float* part;       // [slots][M][HD] sums, [slots][M][4] the two maxima, sum of weights, whether a position was seen; Units
     int* range;
     int* status;
     unsigned long long timeout_ns;
@@ -281,10 +284,14 @@ struct Pieces {
     }
 };
 
+// A row's state: the maximum a of the exponents x; the maximum b of x + log2 vs, the exponents of the values' weights, less a (so
+// that it keeps its digits whatever the size of a); both -inf where there is none.
+// b less another a, the largest of several parts.
+__device__ __forceinline__ float less(float b, float a, float top) { return a == top ? b : b + (a - top); }
 // What the sums of a row are multiplied by, 0 (and .y) for one that sees nothing.
-// (a = -inf where all scores are: 0 / 0)
-__device__ __forceinline__ float2 finish(float a, float b, float sum, float any) {
-    return any == 0.f ? make_float2(0.f, 1.f) : make_float2(exp2f(b - a) / sum, 0.f);
+// (0 / 0 where all scores are -inf)
+__device__ __forceinline__ float2 finish(float b, float sum, float any) {
+    return any == 0.f ? make_float2(0.f, 1.f) : make_float2(exp2f(b) / sum, 0.f);
 }
 // Row r (of q, and head of the group) of a sequence in the output.
 __device__ __forceinline__ uint16_t* row_at(const AttendParams& p, int row0, int head, int r) {
@@ -335,22 +342,27 @@ __global__ void __launch_bounds__(kJoinThreads) fl_kv_attend_join_kernel(const _
         for (int k = lane; k < pieces; k += 32) {
             const float4 st = __ldcg(reinterpret_cast<const float4*>(stat + k * step * M * 4));
             if (k < 32) mine = st;
-            a = fmaxf(a, st.x), b = fmaxf(b, st.y), any = fmaxf(any, st.w);
+            a = fmaxf(a, st.x), any = fmaxf(any, st.w);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-            b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
             any = fmaxf(any, __shfl_xor_sync(0xffffffffu, any, o));
         }
-        const float na = a == kNone ? 0.f : -a, nb = b == kNone ? 0.f : -b;
+        const float na = a == kNone ? 0.f : -a;
         sum = mine.z * ex2(mine.x + na);
+        b = mine.y = less(mine.y, mine.x, a);
         for (int k = lane + 32; k < pieces; k += 32) {
             const float4 st = __ldcg(reinterpret_cast<const float4*>(stat + k * step * M * 4));
             sum += st.z * ex2(st.x + na);
+            b = fmaxf(b, less(st.y, st.x, a));
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        for (int o = 16; o > 0; o >>= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
+        }
+        const float nb = b == kNone ? 0.f : -b;
         for (int k0 = part_of; k0 < pieces; k0 += WR * U) {
             if (k0 != part_of) {
 #pragma unroll
@@ -360,14 +372,18 @@ __global__ void __launch_bounds__(kJoinThreads) fl_kv_attend_join_kernel(const _
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int k = k0 + WR * u;
-                const float mb = k < 32 ? __shfl_sync(0xffffffffu, mine.y, k) : k < pieces ? __ldcg(stat + k * step * M * 4 + 1) : kNone;
+                float mb = k < 32 ? __shfl_sync(0xffffffffu, mine.y, k) : kNone;
                 if (k >= pieces) continue;
+                if (k >= 32) {
+                    const float2 st = __ldcg(reinterpret_cast<const float2*>(stat + k * step * M * 4));
+                    mb = less(st.y, st.x, a);
+                }
                 const float f = ex2(mb + nb);
 #pragma unroll
                 for (int e = 0; e < C / 2; ++e) v[2 * e] = fmaf(x[u][e].x, f, v[2 * e]), v[2 * e + 1] = fmaf(x[u][e].y, f, v[2 * e + 1]);
             }
         }
-        const float2 f = finish(a, b, sum, any);
+        const float2 f = finish(b, sum, any);
         uint16_t* out = row_at(p, row0, head, block0 + r);
         if constexpr (WR == 1) {
             if (lane * C < p.head_dim) {

@@ -362,12 +362,12 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
         // ------------------------------------------------------------ softmax: a row per thread
         const int i = warp >> 2, n = i ? n1 : n0, r = (int)threadIdx.x;  // (one tile: warps 4-7 have nothing to do)
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, s_col = lanes + 128u * i, o_col = lanes + kOCol + 128u * i;
-        const float kNone = __int_as_float(0xff800000);
+        const float kNone = __int_as_float(0xff800000), kNoMaxYet = __int_as_float(0x7f800000);
         wait_here(q_full, 0, p.status, p.timeout_ns, 59);
         const float c = r < M ? cs[r] : 0.f;
         const int qi = min(r0 + r, s.n * p.group - 1) / p.group;  // the row of q among the sequence's
         const int q_first = __shfl_sync(0xffffffffu, qi, 0), q_last = __shfl_sync(0xffffffffu, qi, 31);  // of the warp
-        float mx = kNone, mw = kNone, nx = 0.f, nw = 0.f;  // maxima of x and x + log2 vs; minus them (0 where there is none yet)
+        float mx = kNone, nx = 0.f, mb = kNone;  // the maximum of x, minus it (0 where there is none yet); that of x + log2 vs, less it
         float2 l = make_float2(0.f, 0.f);
         bool seen = false, ok = true;
         const bool idle = r - lane >= rows;  // (a warp without rows: what its lines of the products hold is not read)
@@ -425,13 +425,13 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
             sees[0] &= there.x, sees[1] &= there.y, sees[2] &= there.z, sees[3] &= there.w;
             const bool all = (sees[0] & sees[1] & sees[2] & sees[3]) == 0xffffffffu;
             seen |= (sees[0] | sees[1] | sees[2] | sees[3]) != 0;
-            // Weights of the values: 2^(x + log2 vs - mw) = 2^(x - mx) vs 2^(mx - mw). Once there are maxima, and where every
+            // Weights of the values: 2^(x + log2 vs - mx - mb) = 2^(x - mx) vs 2^-mb. Once there are maxima, and where every
             // position is seen, they are formed in one pass with those: good unless a weight passes 2^8 (or the
-            // sum fp32's range), which is rare. Otherwise the maxima are found first.
+            // sum fp32's range), which is rare. Otherwise, and for maxima of kLarge or more in size, the maxima are found first.
             uint32_t w[4][16];
             bool done = false;
             const float2 cc = make_float2(c, c);
-            if (__all_sync(0xffffffffu, all) && __any_sync(0xffffffffu, mx == kNone || mw == kNone)) {
+            if (__all_sync(0xffffffffu, all) && __any_sync(0xffffffffu, mx == kNone || mb == kNone)) {
                 // (the first maxima: those of a quarter, which mostly will do)
                 float x[32], ta = kNone, tb = kNone;
                 tmem_ld_32x32b_x32(s_col, reinterpret_cast<uint32_t(&)[32]>(x));
@@ -441,11 +441,11 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
                     const float y = x[e] * ld_shared_f32(tab + e * 4) * c;
                     ta = fmaxf(ta, y), tb = fmaxf(tb, y + ld_shared_f32(tab + (2 * kRows + e) * 4));
                 }
-                if (mx == kNone && ta > kNone) mx = ta, nx = -ta;
-                if (mw == kNone && tb > kNone) mw = tb, nw = -tb;
+                if (mx == kNone && ta > kNone && fabsf(ta) < kLarge) mx = ta, nx = -ta;
+                if (mb == kNone && tb > kNone && mx > kNone && fabsf(nx) < kLarge) mb = tb + nx;
             }
-            if (__all_sync(0xffffffffu, all && mx > kNone && mw > kNone)) {
-                const float to = ex2(nw - nx);
+            if (__all_sync(0xffffffffu, all && mx > kNone && mb > kNone && fabsf(nx) < kLarge)) {
+                const float to = ex2(-mb);
                 const float2 nn = make_float2(nx, nx), tt = make_float2(to, to);
                 float2 sum = l;
                 uint32_t most = 0;
@@ -489,22 +489,41 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
                         const uint32_t ks[4] = {k4.x, k4.y, k4.z, k4.w}, lv[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
                         for (int f = 0; f < 4; ++f) {
-                            const float y = x[e + f] * __uint_as_float(ks[f]) * c;
+                            const float y = __fmul_rn(x[e + f] * __uint_as_float(ks[f]), c);
                             if (m >> (e + f) & 1) ta = fmaxf(ta, y), tb = fmaxf(tb, y + __uint_as_float(lv[f]));
                         }
                     }
                 }
-                const bool over = ta > mx || tb > mw;
+                if (ta > mx) {
+                    const float by = mx - ta;  // (-inf for the first maximum)
+                    l.x *= ex2(by), l.y *= ex2(by);
+                    mb += by;
+                    mx = ta, nx = -ta;
+                }
+                tb = fabsf(nx) < kLarge ? tb + nx : kNoMaxYet;
+                if (__any_sync(0xffffffffu, tb == kNoMaxYet)) {
+                    // (the logarithm of vs is lost beside exponents of such a size: once more, less the maximum that is known now)
+                    float t = kNone;
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t m = q < 2 ? (q == 0 ? sees[0] : sees[1]) : (q == 2 ? sees[2] : sees[3]);
+                        float x[32];
+                        tmem_ld_32x32b_x32(s_col + 32u * q, reinterpret_cast<uint32_t(&)[32]>(x));
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float y = __fmul_rn(x[e] * ld_shared_f32(tab + (32 * q + e) * 4), c);
+                            if (m >> e & 1) t = fmaxf(t, __fadd_rn(y, nx) + ld_shared_f32(tab + (2 * kRows + 32 * q + e) * 4));
+                        }
+                    }
+                    if (tb == kNoMaxYet) tb = t;
+                }
+                const bool over = tb > mb;
                 if (__any_sync(0xffffffffu, over)) {
                     float f = 1.f;
-                    if (ta > mx) {
-                        const float g = ex2(mx - ta);
-                        l.x *= g, l.y *= g;
-                        mx = ta, nx = -ta;
-                    }
-                    if (tb > mw) {
-                        f = ex2(mw - tb);
-                        mw = tb, nw = -tb;
+                    if (over) {
+                        f = ex2(mb - tb);
+                        mb = tb;
                     }
                     if (j > 0) {
 #pragma unroll 1
@@ -518,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
                         }
                     }
                 }
-                const float to = mw == kNone ? 0.f : ex2(nw - nx);
+                const float to = mb == kNone ? 0.f : ex2(-mb);
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
                     const uint32_t m = q < 2 ? (q == 0 ? sees[0] : sees[1]) : (q == 2 ? sees[2] : sees[3]);
@@ -533,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
                         float a[4], b[4];
 #pragma unroll
                         for (int f = 0; f < 4; ++f) {
-                            a[f] = ex2(fmaf(x[e + f] * __uint_as_float(ks[f]), c, nx));
+                            a[f] = ex2(__fadd_rn(__fmul_rn(x[e + f] * __uint_as_float(ks[f]), c), nx));
                             b[f] = a[f] * __uint_as_float(vs[f]) * to;
                             if (!(m >> (e + f) & 1)) a[f] = b[f] = 0.f;
                         }
@@ -578,10 +597,10 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_attend_tile_kernel(const __
             const float sum = l.x + l.y;
             constexpr int C = DP / 32;
             const int first = r - lane;
-            const float2 mine_f = finish(mx, mw, sum, seen ? 1.f : 0.f);
+            const float2 mine_f = finish(mb, sum, seen ? 1.f : 0.f);
             if (piece.pieces > 1 && r < rows)
                 *reinterpret_cast<float4*>(p.part + (long long)slots(kTileResident) * M * DP + ((long long)piece.slot * M + r) * 4) =
-                    make_float4(mx, mw, sum, seen ? 1.f : 0.f);
+                    make_float4(mx, mb, sum, seen ? 1.f : 0.f);
             if (piece.pieces > 1) {
                 // (a row is 4 DP bytes in a run: one bulk copy; a row at a time by all lanes took 3 us)
                 fence_proxy_async_smem();

@@ -326,3 +326,36 @@ def test_attention_scores_of_any_size(dt, D, n, m, scale):
         assert sure.mean() > 0.9
         y = f64(v)[best[sure], 0]
         assert (np.abs(got[sure, h] - y) <= (2 * U[dt] + 2.0 ** -20) * np.abs(y) + 2.0 ** -25 * (dt == "f16")).all()
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("group,D,n_rows,start", [(4, 64, [1, 3], [700, 90]), (4, 128, [1, 3], [2900, 90]), (1, 256, [9], [300]),
+                                                  (4, 128, [6], [1000]), (4, 64, [48], [1200]), (2, 128, [48], [2700])])
+@pytest.mark.parametrize("far", [False, True])
+def test_kv_attend_scores_of_any_size(dt, fmt, group, D, n_rows, start, far):
+    """The same over the cache, with values of one size and of sizes that lie 2^44 apart: the weight times the value's scale and the output
+    are rounded (the scale's logarithm, 2^-19 of it, is one more term)."""
+    rng = gen(89, D, sum(start))
+    cache = Paged(rng, [a + b for a, b in zip(n_rows, start)], 1, D, 16, fmt)
+    if far:
+        cache.scale[1] = np.where(rng.random(cache.scale[1].shape) < 0.5, 2.0 ** -6, 2.0 ** -50).astype(np.float32)
+        cache.vs = put(cache.scale[1])
+    q = put(rng.standard_normal((sum(n_rows), group, D)), dt)
+    cu = sums(n_rows)
+    vals = cache.values()
+    certain = []
+    for scale in SIZES:
+        got = f64(fl.kv_attend(q, *cache.tensors(), ints(cache.table), ints(start), cu_rows=ints(cu), scale=scale))
+        fl.device_status()
+        assert np.isfinite(got).all()
+        for b, (n, at) in enumerate(zip(n_rows, start)):
+            for h in range(group):
+                best, sure = winners(f64(q)[cu[b]:cu[b + 1], h], vals[b][0][:at + n, 0], oracle.causal(n, at + n), scale)
+                certain.append(sure.mean())
+                y = vals[b][1][best[sure], 0]
+                err = np.abs(got[cu[b]:cu[b + 1], h][sure] - y)
+                # (the others' weights together are below (at + n) 2^-60)
+                rest = (at + n) * 2.0 ** -60 * np.abs(vals[b][1]).max() + 2.0 ** -25 * (dt == "f16")
+                assert (err <= (U[dt] + 2.0 ** -11 + 2.0 ** -16) * np.abs(y) + rest).all(), (scale, b, h)
+    assert np.mean(certain) > 0.5
