@@ -33,6 +33,7 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSegment = 256;  // table entries of a warp at a time
 constexpr int kPer = kSegment / 32;
+constexpr int kWants = -2;     // fork: an entry that wants a page, between the phases (none, like every negative one)
 
 struct PagesParams {
     int* page_table;
@@ -112,17 +113,22 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_pages_kernel(const __grid_c
     };
 
     if (FORK) {
-        // what the children held goes
+        // What the children held goes. (Exchanged, so that it goes once where a sequence is a child twice: that has no defined answer,
+        // but no page of another sequence may become free.)
         for (long long s = s0; s < s1; ++s) {
             const int i = (int)(s / per_row), j0 = (int)(s % per_row) * kSegment;
             const int c = __ldg(p.children + i);
             if (!valid(c) || !valid(__ldg(p.parents + i))) continue;
-            const int* row = p.page_table + c * p.table_stride;
+            int* row = p.page_table + c * p.table_stride;
+            int e[kPer];
 #pragma unroll
             for (int u = 0; u < kPer; ++u) {
-                const int j = j0 + 32 * u + lane, e = j < p.table_pages ? __ldcg(row + j) : -1;
-                if (held(e)) atomicAdd(p.refs + e, -1);
+                const int j = j0 + 32 * u + lane;
+                e[u] = j < p.table_pages ? atomicExch(row + j, -1) : -1;
             }
+#pragma unroll
+            for (int u = 0; u < kPer; ++u)
+                if (held(e[u])) atomicAdd(p.refs + e[u], -1);
         }
         all_sync<CTAS>();
     }
@@ -176,8 +182,9 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_pages_kernel(const __grid_c
                 const bool share = j < full && held(e[u]);
                 if (share) atomicAdd(p.refs + e[u], 1);
                 if (j < full + (part > 0) && !held(e[u])) atomicCAS(p.range, 0, i + 1);
-                row[j] = share ? e[u] : -1;
-                count += j == full && part > 0 && held(e[u]);
+                const bool wants = j == full && part > 0 && held(e[u]);
+                row[j] = share ? e[u] : wants ? kWants : -1;
+                count += wants;
             }
         }
     }
@@ -223,21 +230,15 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_pages_kernel(const __grid_c
         all_sync<CTAS>();
         for (long long s = s0; s < s1; ++s) {
             const int i = (int)(s / per_row), j0 = (int)(s % per_row) * kSegment;
-            int part, limit, first, c = i;
-            bool ok = true;
-            if (!FORK) {
-                limit = pages_of(__ldg(p.lengths + i), part);
-                limit += part > 0, first = 0;
-            } else {
+            int part = 0, limit, c = i;
+            if (FORK) {
                 c = __ldg(p.children + i);
-                const int from = __ldg(p.parents + i);
-                ok = valid(c) && valid(from);
-                first = ok ? pages_of(__ldg(p.lengths + i), part) : 0;
-                // (its parent's page was there)
-                ok = ok && part > 0 && held(__ldcg(p.page_table + from * p.table_stride + first));
-                limit = first + 1;
+                if (!valid(c) || !valid(__ldg(p.parents + i))) continue;
             }
-            if (!ok) continue;
+            limit = pages_of(__ldg(p.lengths + i), part);
+            const int first = FORK ? limit : 0;
+            if (FORK && part == 0) continue;
+            limit += part > 0;
             int* row = p.page_table + c * p.table_stride;
             // (all places in the list first, then all loads from it)
             int k[kPer], page[kPer];
@@ -245,7 +246,8 @@ __global__ void __launch_bounds__(kThreads, 1) fl_kv_pages_kernel(const __grid_c
             for (int u = 0; u < kPer; ++u) {
                 const int j = j0 + 32 * u + lane;
                 bool wants = j >= first && j < limit && j < p.table_pages;
-                if (!FORK) wants = s - s0 < 32 / kPer ? wants_of >> ((int)(s - s0) * kPer + u) & 1 : wants && !held(__ldcg(row + j));
+                if (FORK) wants = wants && __ldcg(row + j) == kWants;
+                else wants = s - s0 < 32 / kPer ? wants_of >> ((int)(s - s0) * kPer + u) & 1 : wants && !held(__ldcg(row + j));
                 const uint32_t m = __ballot_sync(0xffffffffu, wants);
                 k[u] = wants ? rank + __popc(m & ((1u << lane) - 1)) : -1;
                 rank += __popc(m);
@@ -270,6 +272,7 @@ struct CopyParams {
     uint8_t* cache[2];
     float* scale[2];
     const int* page_table;
+    const int* refs;
     const int* lengths;
     const int* parents;
     const int* children;
@@ -280,7 +283,7 @@ constexpr int kCopyThreads = 256;
 constexpr int kSlices = 8;
 
 template <typename T, int U>
-__device__ __forceinline__ void copy_run(T* dst, const T* src, long long n, int tid, int threads) {
+__device__ __forceinline__ void copy_run(T* dst, const T* src, long long n, int tid, int threads, bool own) {
     for (long long b = tid; b < n; b += (long long)threads * U) {
         T v[U];
 #pragma unroll
@@ -288,7 +291,7 @@ __device__ __forceinline__ void copy_run(T* dst, const T* src, long long n, int 
             if (b + u * threads < n) v[u] = __ldcg(src + b + u * threads);
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (b + u * threads < n) dst[b + u * threads] = v[u];
+            if (own && b + u * threads < n) dst[b + u * threads] = v[u];
     }
 }
 
@@ -301,6 +304,9 @@ __global__ void __launch_bounds__(kCopyThreads) fl_kv_fork_copy_kernel(const __g
     if (part == 0 || full >= p.table_pages) return;
     const int a = __ldcg(p.page_table + from * p.table_stride + full), b = __ldcg(p.page_table + c * p.table_stride + full);
     if (a < 0 || a >= p.n_pages || b < 0 || b >= p.n_pages || a == b) return;
+    // The child's own page is held once; another than that stands here only where a sequence is a child twice. (Asked for beside the
+    // rows, which are not stored otherwise.)
+    const bool own = __ldcg(p.refs + b) == 1;
     const long long src = (long long)a * p.page_size, dst = (long long)b * p.page_size;
     const int tid = blockIdx.y * kCopyThreads + threadIdx.x, threads = kSlices * kCopyThreads;
 #pragma unroll
@@ -308,10 +314,10 @@ __global__ void __launch_bounds__(kCopyThreads) fl_kv_fork_copy_kernel(const __g
         uint8_t* to = p.cache[w] + dst * p.row_bytes;
         const uint8_t* at = p.cache[w] + src * p.row_bytes;
         if (p.row_bytes % 16 == 0)
-            copy_run<uint4, 4>(reinterpret_cast<uint4*>(to), reinterpret_cast<const uint4*>(at), part * p.row_bytes / 16, tid, threads);
+            copy_run<uint4, 4>(reinterpret_cast<uint4*>(to), reinterpret_cast<const uint4*>(at), part * p.row_bytes / 16, tid, threads, own);
         else
-            copy_run<uint2, 4>(reinterpret_cast<uint2*>(to), reinterpret_cast<const uint2*>(at), part * p.row_bytes / 8, tid, threads);
-        copy_run<float, 2>(p.scale[w] + dst * p.heads, p.scale[w] + src * p.heads, (long long)part * p.heads, tid, threads);
+            copy_run<uint2, 4>(reinterpret_cast<uint2*>(to), reinterpret_cast<const uint2*>(at), part * p.row_bytes / 8, tid, threads, own);
+        copy_run<float, 2>(p.scale[w] + dst * p.heads, p.scale[w] + src * p.heads, (long long)part * p.heads, tid, threads, own);
     }
 }
 
@@ -541,7 +547,7 @@ extern "C" fl_status fl_kv_fork(const fl_kv_pages* cache, int* refs, const int* 
     CopyParams c = {};
     c.cache[0] = static_cast<uint8_t*>(cache->k_cache), c.cache[1] = static_cast<uint8_t*>(cache->v_cache);
     c.scale[0] = cache->k_scale, c.scale[1] = cache->v_scale;
-    c.page_table = cache->page_table, c.lengths = lengths, c.parents = parents, c.children = children;
+    c.page_table = cache->page_table, c.refs = refs, c.lengths = lengths, c.parents = parents, c.children = children;
     c.table_stride = cache->table_stride, c.row_bytes = (long long)cache->heads * cache->head_dim;
     c.heads = cache->heads, c.n_seqs = cache->n_seqs, c.table_pages = cache->table_pages;
     c.n_pages = cache->n_pages, c.page_size = cache->page_size;

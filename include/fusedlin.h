@@ -673,7 +673,8 @@ fl_status fl_kv_attend(const fl_kv_attend_desc* desc, void* workspace, size_t wo
  * parents[i]: what it held is released; pages that lie in those positions as a whole
  * are shared (refs + 1); the rows of a last, partly filled one are copied to a free page. No
  * sequence is a child twice, or a child and a parent, in one call; what one then
- * holds is not defined. A shared page must not be written: rows that are appended
+ * holds is not defined, nor how many pages stay counted for it, but the others keep
+ * theirs. A shared page must not be written: rows that are appended
  * behind the length go to pages of the sequence's own.
  *
  * fl_kv_compact: of the rows drafted at positions start[b] + 0, 1, .. of each

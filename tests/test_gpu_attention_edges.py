@@ -359,3 +359,52 @@ def test_kv_attend_scores_of_any_size(dt, fmt, group, D, n_rows, start, far):
                 rest = (at + n) * 2.0 ** -60 * np.abs(vals[b][1]).max() + 2.0 ** -25 * (dt == "f16")
                 assert (err <= (U[dt] + 2.0 ** -11 + 2.0 ** -16) * np.abs(y) + rest).all(), (scale, b, h)
     assert np.mean(certain) > 0.5
+
+
+# ---------------------------------------------------------------------------
+# pages
+# ---------------------------------------------------------------------------
+def forks_that_are_not_defined(rng, B, kind):
+    if kind == "child twice":
+        children = rng.integers(B // 2, B, 40)
+        parents = rng.integers(0, B // 2 - 2, 40)
+    else:                                              # some sequences are children and parents
+        children = rng.permutation(np.arange(2, B - 2))[:40]
+        parents = rng.integers(0, B - 2, 40)
+    return parents, children
+
+
+@pytest.mark.parametrize("kind", ["child twice", "child and parent"])
+@pytest.mark.parametrize("B,per", [(60, 9), (80, 300)])
+def test_kv_fork_of_one_sequence_twice_leaves_the_others_alone(kind, B, per):
+    """What such a child then holds is not defined. Every other sequence keeps its pages and what they hold, and no page is
+    counted less than it is held."""
+    for seed in range(4):
+        rng = gen(90, B, per, seed)
+        lens = rng.integers(0, 16 * per + 1, B).tolist()
+        cache = Paged(rng, lens, 1, 64, 16, "int8", spare=90)
+        cache.table = cache.table[:, :per]
+        shared = np.flatnonzero(np.asarray(lens) >= 32)[-1]
+        cache.table[B - 1] = -1
+        cache.table[B - 1, :2] = cache.table[shared, :2]  # pages that two sequences hold
+        refs = np.bincount(cache.table[cache.table >= 0], minlength=cache.pages).astype(np.int32)
+        parents, children = forks_that_are_not_defined(rng, B, kind)
+        lengths = [int(rng.integers(0, lens[p] + 1)) for p in parents]
+        t, r = ints(cache.table), ints(refs)
+        before = [x.clone() for x in cache.tensors()]
+        fl.kv_fork(*cache.tensors(), t, r, ints(parents), ints(children), ints(lengths))
+        try:
+            fl.device_status()
+        except fl.FusedLinError as e:
+            assert e.status == 7
+        table, counts = t.cpu().numpy(), r.cpu().numpy()
+        others = np.setdiff1d(np.arange(B), children)
+        assert np.array_equal(table[others], cache.table[others])
+        assert ((table >= -1) & (table < cache.pages)).all()
+        held = np.bincount(table[table >= 0], minlength=cache.pages)
+        assert (counts >= held).all()
+        pages = np.unique(cache.table[others])
+        pages = torch.from_numpy(pages[pages >= 0]).long().cuda()
+        for x, y in zip(cache.tensors(), before):
+            x, y = (z if z.dtype == torch.float32 else z.view(torch.uint8) for z in (x, y))
+            assert torch.equal(x[pages], y[pages])
