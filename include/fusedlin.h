@@ -532,10 +532,11 @@ fl_status fl_rope(const fl_rope_desc* desc, void* stream);
  *   causal: the last rows of a sequence's q and k stand at the same position: row i
  *   sees keys 0 .. i + len_k - len_q. Otherwise all of its sequence.
  * A row that sees no key gets zeros. Keys and values that a row does not see do not
- * reach it, whatever they hold. Scores, maxima and sums are fp32; rounded to the
- * dtype are the weights and the output. head_dim is a multiple of 8, 8 .. 128;
- * scale is positive. An expanded tensor (a stride of 0) is refused. rows_q 0 does
- * nothing.
+ * reach it, whatever they hold; a value that is not finite makes its channel of the
+ * rows that see it not finite (NaN in place of an infinity where the weight rounds
+ * to 0). Scores, maxima and sums are fp32; rounded to the dtype are the weights and
+ * the output. head_dim is a multiple of 8, 8 .. 128; scale is positive. An expanded
+ * tensor (a stride of 0) is refused. rows_q 0 does nothing.
  */
 typedef struct {
     fl_dtype dtype;
@@ -672,8 +673,8 @@ fl_status fl_kv_attend(const fl_kv_attend_desc* desc, void* workspace, size_t wo
  * children[i] becomes a copy of the first lengths[i] positions of sequence
  * parents[i]: what it held is released; pages that lie in those positions as a whole
  * are shared (refs + 1); the rows of a last, partly filled one are copied to a free page. No
- * sequence is a child twice, or a child and a parent, in one call; what one then
- * holds is not defined, nor how many pages stay counted for it, but the others keep
+ * sequence is a child twice, or a child and a parent, in one call: what one then
+ * holds is not defined, nor how many pages stay counted for it; the others keep
  * theirs. A shared page must not be written: rows that are appended
  * behind the length go to pages of the sequence's own.
  *

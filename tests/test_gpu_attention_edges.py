@@ -291,6 +291,32 @@ def test_attention_keys_for_longer_than_a_wait_may_take():
     check(got[rows][:, heads], ref, U["bf16"], U["bf16"], 2.0 ** -20, np.zeros((3, 3)))
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,m", [(700, 700), (40, 3000)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_attention_values_that_are_not_finite(dt, D, n, m, bad):
+    """A value that is not finite, early enough that blocks are seen as a whole: its channel is not finite in the rows that see it
+    (an infinity where their weight is not 0, else NaN), and nothing else changes."""
+    rng = gen(91, D, n)
+    q, k, v = (put(rng.standard_normal((x, h, D)), dt) for x, h in ((n, 2), (m, 1), (m, 1)))
+    clean = fl.attention(q, k, v)
+    at = m - n + 10
+    v[at, 0, 3] = bad
+    got = fl.attention(q, k, v)
+    fl.device_status()
+    rest = [c for c in range(D) if c != 3]
+    assert torch.equal(got[:10], clean[:10]) and torch.equal(got[..., rest], clean[..., rest])
+    hit = got[10:, :, 3]
+    assert (torch.isnan(hit) | (hit == bad)).all()
+    if bad != bad:
+        assert torch.isnan(hit).all()
+    k[at] = 40 * q[10, 0]                               # all the weight that fp32 has, in row 10
+    got = fl.attention(q, k, v)
+    fl.device_status()
+    assert torch.isnan(got[10, 0, 3]) if bad != bad else got[10, 0, 3] == bad
+
+
 # ---------------------------------------------------------------------------
 # scores of any size
 # ---------------------------------------------------------------------------
