@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, Layout<HD, QT>::kCtas) fl_kv_attend_
             const int steps = k1 > k0 + own * kStep ? (k1 - k0 - own * kStep + stride - 1) / stride : 0;
             const int* table = p.page_table + piece.seq * p.table_stride;
             // the table's entry of this lane's position of a step, one step ahead; -2: there is no such position
-            int entry, in_page;
+            int entry = -2, in_page = 0;
             auto look_up = [&](int step, int& entry, int& in_page) {
                 const int pos = k0 + own * kStep + step * stride + (lane & 15);
                 entry = -2, in_page = 0;
