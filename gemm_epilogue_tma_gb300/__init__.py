@@ -653,9 +653,9 @@ def attention(q, k, v, cu_q=None, cu_k=None, causal=True, scale=None, out=None, 
 
     Query head h reads key head h / (heads_q / heads_k). cu_q, cu_k: int32 [sequences + 1], the rows of packed sequences
     (cu_k None: as cu_q; both None: one sequence of all rows). Causal: the last rows of a sequence's q and k stand at the
-    same position, row i sees keys 0 .. i + len_k - len_q. A row that sees no key gets zeros; rows of q that
-    belong to no sequence are left as they were in out. scale: 1 / sqrt(D) if None. q, k, v and out may be strided views
-    with contiguous channels. D is a multiple of 8, 128 at most."""
+    same position, row i sees keys 0 .. i + len_k - len_q. A row that sees no key gets zeros; a value that is not
+    finite makes its channel of the rows that see it not finite, and of no others; rows of q that belong to no sequence are
+    left as they were in out. scale: 1 / sqrt(D) if None. q, k, v and out may be strided views with contiguous channels. D is a multiple of 8, 128 at most."""
     if stream is None:
         r = (_ops or ops()).attention(q, k, v, cu_q, cu_k, causal, scale, out, None)
     else:
@@ -705,7 +705,8 @@ def kv_fork(k_cache, v_cache, k_scale, v_scale, page_table, refs, parents, child
     """Sequence children[i] becomes a copy of the first lengths[i] positions of sequence parents[i] (all int32 [n]): it
     releases what it held, shares the pages that lie in those positions as a whole, and gets a copy of a last, partly
     filled one. refs: int32 [pages], the number of table entries that hold each page (0: free). No sequence may be a child
-    twice, or a child and a parent. Where no page is free the entry is -1 and device_status() raises FL_ERR_RANGE.
+    twice, or a child and a parent (what it then holds is not defined; the others keep theirs). Where no page is free the
+    entry is -1 and device_status() raises FL_ERR_RANGE.
     The workspace (kv_pages_workspace_size bytes) must not be shared by calls or graphs that may overlap."""
     args = (k_cache, v_cache, k_scale, v_scale, page_table, refs, parents, children, lengths, workspace)
     r = (_ops or ops()).kv_fork(*args, None) if stream is None else _on(stream, "kv_fork", args, workspace is None)

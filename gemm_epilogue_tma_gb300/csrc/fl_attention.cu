@@ -20,18 +20,21 @@
 // and the output.
 //
 // Blocks that some row does not see as a whole are masked score by score. A value
-// that no row may see must not reach a row times zero (0 inf, 0 NaN): two warps
+// that a row may not see must not reach it times zero (0 inf, 0 NaN): two warps
 // zero the rows behind the last key in such blocks, take what is not finite out
 // of the others and note the first key of each channel where it stood, and the
-// epilogue adds it to the rows that see that key.
+// epilogue adds it to the rows that see that key. (Blocks that every row sees are taken as they are: an infinity
+// times a weight that rounds to 0 is a NaN there.)
 //
 // What bounds it: the products. A block of both tiles takes 1.4 to 1.5 us, the products
-// alone 1.36 at the dense rate that was measured for a large library product. One causal sequence of 8192 rows, 32 and 8 heads of 128, bf16: 355 us,
-// 1547 TFLOP/s; 16384 rows of 16 heads 655 us, 1680; 4096 rows causal 106 us, 1300. A
+// alone 1.36 at the dense rate that was measured for a large library product. 32 and 8 heads of 128,
+// bf16, across boxes: one causal sequence of 8192 rows 353 to 376 us (1460 to 1557 TFLOP/s), 4096 106
+// (1290); 16384 rows of 16 heads 653 to 657 (1674 to 1685). Heads of 64 channels have half the
+// products for the same softmax: 8192 rows 290 us (949). A
 // CTA's start (its rows found, the first loads and scores: 2.9 us) and end (output: 2.5)
 // are not hidden, since a multiprocessor holds one, so that short
-// sequences fare worse (eight of 512 rows: 41.5 us, 415 TFLOP/s; five chunks of 330 to
-// 490 rows over 480 to 1930 keys: 54 us, 711). (CTAs that stay and take the next
+// sequences fare worse (eight of 512 rows: 41.9 us, 411 TFLOP/s; five chunks of 330 to
+// 490 rows over 480 to 1930 keys: 53 us, 724). (CTAs that stay and take the next
 // rows while the last are finished were no faster: the softmax warps store the output.) Two tiles to a CTA, not one,
 // so that each block of keys is read for 256 rows.
 //

@@ -4,7 +4,7 @@
 //   out[i, h] = sum_p w v[p] / sum_p w,  w = 2^x,  x = scale log2(e) ks[p] (q[i, h] . kc[p]),  v[p] = vs[p] vc[p]
 //
 // over the positions p that row i sees. The codes kc, vc are what the MMAs
-// multiply: both formats fit fp16 exactly (e4m3 times 2^-8: its bits moved), so no
+// multiply: both formats fit fp16 exactly (e4m3 by the conversion instruction), so no
 // key or value is rounded; ks goes onto the fp32 scores, and vs into the weights
 // of the second product, w vs = 2^(x + log2 vs), which have a running maximum of
 // their own, kept less that of x, so that they fill fp16's range whatever the scales are. Rounded are
@@ -12,9 +12,9 @@
 // multiplied as fp16 times a power of two per row, which keeps their 8 bits down
 // to 2^-28 of the row's largest value.
 //
-// The cache is read once and nothing is written but the output, so HBM bounds it:
-// 2 head_dim + 8 bytes per position and key head, for all rows of a sequence
-// and all query heads of the group. Keys are the rows of the first MMA, 16 positions,
+// The cache is read once for a row block (a sequence's rows and all query heads of the group, 8, 16
+// or 32 of them; more are further blocks, which read it again) and nothing is written but the
+// output, so HBM bounds it: 2 head_dim + 8 bytes per position and key head. Keys are the rows of the first MMA, 16 positions,
 // and channels those of the second, O^T = V^T P^T; the rows of q are its columns, in
 // tiles of eight, so that a decode step of a group of four or eight heads pads
 // little, and P^T, 16 positions by 8, is the first product's result turned by
@@ -31,11 +31,12 @@
 // are joined by a second launch, in order.
 //
 // What bounds it, by measurement with 32 and 8 heads of 128, bf16: 64 contexts of 8192
-// positions int8 225 us (4.9 TB/s), e4m3 193 (5.8); without the arithmetic 178, without
-// the loads 210 and 165: for int8 the conversion of codes, whose logical operations are issued at half
-// rate. 16 contexts of 500 to 9600, e4m3 fp16: 36.6 us, of which the longest piece takes 27 and
+// positions int8 225 us (4.9 TB/s), e4m3 186 (5.9); parts of an earlier form that took 236 and 195: without the arithmetic
+// 178, without the loads 210 and 165: for int8 the conversion of codes, whose logical operations are issued at half
+// rate. 16 contexts of 500 to 9600, e4m3 fp16: 37.1 us, of which the longest piece takes 27 and
 // the start of a CTA (lengths, plan, table, first loads) 7 and the second launch 3. 61 of
-// 20 to 300 positions: 14.6 us, 7 of them that start, 5 the longest context, 2 the end.
+// 20 to 300 positions: 14.6 to 14.9 us, 7 of them that start, 5 the longest context, 2 the end; 15.8 with a table of 4096
+// positions, which might be split, for a second launch that finds nothing to join.
 #include <algorithm>
 #include <type_traits>
 
@@ -53,8 +54,11 @@ constexpr int kResident = 304;  // CTAs at work at once: two on each of 152 mult
 static_assert(kTile == kStep * kWarps, "a tile is a step of all warps");
 // The kernel for many rows is taken for more than kRowsLimit rows of a sequence and key head (on average) and tables
 // of kLongTable positions at least; the lengths themselves are not known here. Both sides, us, eight key heads: four contexts
-// of 5700 with 32 rows each 42 here, 49 there; with 36 64 and 50, with 96 83 and 51; 32 contexts of 1000 with 48 rows 91 and 76;
-// one of 500 with 192 rows 23 and 37, four of 300 with 48 rows 18 and 31.
+// of 5700 with 16 rows each 29 here, 42 there; with 32 42 and 42, with 36 64 and 44, with 96 82 and 44; 32 contexts of 1000 with
+// 48 rows 88 and 65; one of 2000 with 36 rows 18 and 20. In short tables one of 500 with 192 rows 22.6 and 25.8, four of 300 with 48
+// rows 14 and 17. What the rule does not see: such short contexts in a wide table (16 and 20), and a short table with
+// very many rows, or many sequences, where the other side is the faster (four of 300 with 1024 rows 126 and 38, 32 of 300 with
+// 48 rows 50 and 35).
 constexpr int kRowsLimit = 32, kLongTable = 1024;
 
 

@@ -9,9 +9,9 @@
 // are, six warps write them out as the 16-bit operands' swizzled blocks, and the
 // scales go onto the scores and the weights as before, two per position. The
 // warp-level kernel widens them again for every 32 rows: trees of 48 rows for a group of four
-// heads over contexts of 1000 to 10600 positions, 23000 in all, 146 us there, 58 here.
+// heads over contexts of 1000 to 10600 positions, 23000 in all, 146 us there, 59 to 60 here.
 //
-// What bounds it: of those 58 us the start of a CTA (lengths and plan 4, rows of q 4)
+// What bounds it: of those the start of a CTA (lengths and plan 4, rows of q 4)
 // takes 10, its 9 to 11 blocks 2.8 to 3 each (of which 1.8 are the softmax of a tile and 0.9 the
 // products and the barriers between, the other tile's the same), the end 3, the second launch 5.
 //

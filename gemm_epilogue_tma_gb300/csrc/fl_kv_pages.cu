@@ -16,10 +16,11 @@
 //      shared memory, so that each warp knows how many stand in front of its own
 //   3. the k-th free page is written to place k of a list, k below the wanted number
 //   4. the k-th wanting entry takes page k of the list
+// (a fork releases what its children held in a phase of its own, in front, and marks the entries that want a page)
 // with a barrier after each. Nothing but latency bounds it: the barriers, and the rounds of
 // loads of a warp's run, eight loads to a round. Graph times: two calls for seven sequences
 // of 16 entries 6.9 us, for 256 of 1024 entries and 121000 pages 21; a fork of one
-// sequence into three 7.4 with its copy, of eight into 56 11.9; rows of one tree moved 2.9, of 61 3.8.
+// sequence into three 8.0 with its copy, of eight into 56 11.9; rows of one tree moved 2.9, of 61 3.8.
 #include <algorithm>
 
 #include "fl_common.cuh"
