@@ -655,7 +655,8 @@ def attention(q, k, v, cu_q=None, cu_k=None, causal=True, scale=None, out=None, 
     (cu_k None: as cu_q; both None: one sequence of all rows). Causal: the last rows of a sequence's q and k stand at the
     same position, row i sees keys 0 .. i + len_k - len_q. A row that sees no key gets zeros; a value that is not
     finite makes its channel of the rows that see it not finite, and of no others; rows of q that belong to no sequence are
-    left as they were in out. scale: 1 / sqrt(D) if None. q, k, v and out may be strided views with contiguous channels. D is a multiple of 8, 128 at most."""
+    left as they were in out. scale: 1 / sqrt(D) if None. q, k, v and out may be strided views with contiguous channels.
+    D is a multiple of 8, 128 at most."""
     if stream is None:
         r = (_ops or ops()).attention(q, k, v, cu_q, cu_k, causal, scale, out, None)
     else:
